@@ -290,6 +290,72 @@ q1_status q1_pack_from_dense(const void *dense, q1_dtype in_t, int64_t N, int64_
                                                 (cudaStream_t)stream));
 }
 
+namespace {
+q1_status check_delta(const q1_delta_args *a) {
+  if (!a) return Q1_ERR_NULL;
+  if (a->dtype != Q1_BF16 && a->dtype != Q1_F16 && a->dtype != Q1_F32) return Q1_ERR_DTYPE;
+  if ((a->DK != 64 && a->DK != 128) || (a->DV != 64 && a->DV != 128)) return Q1_ERR_SHAPE;
+  if (a->HK < 1 || a->HV < 1 || a->HV % a->HK != 0 || a->HV > 65535) return Q1_ERR_SHAPE;
+  if (a->T < 0 || a->T > ((int64_t)1 << 31) - 1 || a->B < 1 || a->B > (int64_t)1 << 24 || a->n_slots < 0 ||
+      a->max_len < 0)
+    return Q1_ERR_SHAPE;
+  if (!a->cu_seqlens && a->T % a->B != 0) return Q1_ERR_SHAPE;
+  if (!a->slots && a->n_slots < a->B) return Q1_ERR_SHAPE;
+  if (!a->state) return Q1_ERR_NULL;
+  if (!aligned(a->state, 16)) return Q1_ERR_ALIGN;
+  if ((a->cu_seqlens && !aligned(a->cu_seqlens, 4)) || (a->slots && !aligned(a->slots, 4)) ||
+      (a->fresh && !aligned(a->fresh, 4)))
+    return Q1_ERR_ALIGN;
+  if (a->T == 0) return Q1_OK;  // no rows to read: the states only
+  if (!a->q || !a->k || !a->v || !a->o || !a->g || !a->beta) return Q1_ERR_NULL;
+  const int64_t per16 = a->dtype == Q1_F32 ? 4 : 8;  // elements in 16 bytes
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->o, 16) || a->q_stride % per16 ||
+      a->k_stride % per16 || a->v_stride % per16 || a->o_stride % per16 || !aligned(a->g, 4) || !aligned(a->beta, 4))
+    return Q1_ERR_ALIGN;
+  const int64_t qk = (int64_t)a->HK * a->DK, vo = (int64_t)a->HV * a->DV;
+  if (a->T > 1 && (a->q_stride < qk || a->k_stride < qk || a->v_stride < vo || a->o_stride < vo ||
+                   a->g_stride < a->HV || a->beta_stride < a->HV))
+    return Q1_ERR_SHAPE;
+  return Q1_OK;
+}
+
+q1::DeltaView delta_view(const q1_delta_args *a) {
+  return q1::DeltaView{a->q, a->k, a->v, a->o, a->g, a->beta, a->state, a->cu_seqlens, a->slots, a->fresh,
+                       a->q_stride, a->k_stride, a->v_stride, a->o_stride, a->g_stride, a->beta_stride,
+                       a->T, a->B, a->n_slots, a->HK, a->HV, a->DK, a->DV, a->qk_l2norm != 0, a->scale};
+}
+}  // namespace
+
+size_t q1_gated_delta_workspace_size(const q1_delta_args *a) {
+  (void)a;
+  return 0;
+}
+
+q1_status q1_gated_delta(const q1_delta_args *a, void *workspace, size_t workspace_bytes, q1_stream stream) {
+  q1_status s = check_device();
+  if (s != Q1_OK) return s;
+  if ((s = check_delta(a)) != Q1_OK) return s;
+  (void)workspace;
+  (void)workspace_bytes;
+  return cuda_status(q1::launch_delta_step(delta_view(a), (q1_dtype)a->dtype, (cudaStream_t)stream));
+}
+
+q1_status q1_sample(const q1_sample_args *a, q1_stream stream) {
+  q1_status s = check_device();
+  if (s != Q1_OK) return s;
+  if (!a) return Q1_ERR_NULL;
+  if (a->dtype != Q1_BF16 && a->dtype != Q1_F16 && a->dtype != Q1_F32) return Q1_ERR_DTYPE;
+  if (a->B < 0 || a->B > (int64_t)1 << 24 || a->V < 1 || a->V > (int64_t)1 << 18 || (a->B > 1 && a->row_stride < a->V))
+    return Q1_ERR_SHAPE;
+  if (a->B == 0) return Q1_OK;
+  if (!a->logits || !a->u || !a->token) return Q1_ERR_NULL;
+  if (!aligned(a->logits, a->dtype == Q1_F32 ? 4 : 2) || !aligned(a->u, 4) || !aligned(a->token, 4) ||
+      !aligned(a->prob, 4) || !aligned(a->temperature, 4) || !aligned(a->top_p, 4) || !aligned(a->min_p, 4) ||
+      !aligned(a->top_k, 4))
+    return Q1_ERR_ALIGN;
+  return cuda_status(q1::launch_sample(*a, (cudaStream_t)stream));
+}
+
 q1_status q1_check_symmetric(const q1_weight *W, int32_t *d_is_symmetric, q1_stream stream) {
   q1_status s = check_device();
   if (s != Q1_OK) return s;

@@ -92,6 +92,40 @@ cudaError_t launch_wide(const WeightView &W, const void *x, int64_t M, void *y, 
 // fixed prefill tiling (token_tile, split), or the automatic choice when invalid
 void set_pair_plan(int token_tile, int split);
 
+// ---- gated delta rule (q1_delta.cu: token by token)
+constexpr float kDeltaEps = 1e-6f;  // added to a row's sum of squares before its root
+// The arguments of q1_gated_delta, as the kernels take them.
+struct DeltaView {
+  const void *q, *k, *v;
+  void *o;
+  const float *g, *beta;
+  float *state;
+  const int32_t *cu, *slots, *fresh;
+  int64_t q_stride, k_stride, v_stride, o_stride, g_stride, beta_stride;
+  int64_t T, B, n_slots;
+  int HK, HV, DK, DV;
+  int l2norm;
+  float scale;
+#ifdef __CUDACC__
+  // Tokens [t0, t1) of sequence b.  Offsets in cu that are out of range or
+  // decrease are cut to [0, T): no access leaves the arrays.
+  __device__ __forceinline__ void range(int64_t b, int64_t &t0, int64_t &t1) const {
+    if (cu) {
+      t0 = min(max((int64_t)cu[b], (int64_t)0), T);
+      t1 = min(max((int64_t)cu[b + 1], t0), T);
+    } else {
+      const int64_t L = T / B;
+      t0 = b * L;
+      t1 = t0 + L;
+    }
+  }
+#endif
+};
+cudaError_t launch_delta_step(const DeltaView &a, q1_dtype t, cudaStream_t st);
+
+// ---- sampling (q1_sample.cu)
+cudaError_t launch_sample(const q1_sample_args &a, cudaStream_t st);
+
 // ---- device error words (each translation unit with bounded waits owns one)
 // and the diagnostics of the bounded waits: their limit, and producers that
 // issue nothing (every wait for their data then runs out)

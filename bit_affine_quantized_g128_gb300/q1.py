@@ -27,6 +27,7 @@ EXPORTED = [
     "q1_device_errors", "q1_status_string", "q1_ffn_fused_noalloc",
     "q1_set_wait_limit_ns", "q1_set_stalled_producers",
     "q1_decode_chain_workspace_size", "q1_decode_chain", "q1_pack_from_dense",
+    "q1_gated_delta_workspace_size", "q1_gated_delta", "q1_sample",
 ]
 
 
@@ -48,6 +49,23 @@ _META = {torch.float16: 0, torch.bfloat16: 1}
 
 class _CLayer(ctypes.Structure):
     _fields_ = [("attn", _CWeight), ("gate", _CWeight), ("up", _CWeight), ("down", _CWeight)]
+
+
+class _CDelta(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "g", "beta", "state", "cu_seqlens", "slots",
+                                               "fresh")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "o_stride", "g_stride",
+                                              "beta_stride", "T", "B", "n_slots", "max_len")] + \
+               [(n, ctypes.c_int32) for n in ("HK", "HV", "DK", "DV", "dtype", "qk_l2norm")] + \
+               [("scale", ctypes.c_float)]
+
+
+class _CSample(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("logits", "u", "temperature", "top_p", "min_p", "top_k", "token",
+                                               "prob")] + \
+               [(n, ctypes.c_int64) for n in ("B", "V", "row_stride")] + \
+               [("dtype", ctypes.c_int32), ("top_k_value", ctypes.c_int32)] + \
+               [(n, ctypes.c_float) for n in ("temperature_value", "top_p_value", "min_p_value")]
 
 
 _lib = None
@@ -90,6 +108,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "q1_decode_chain_workspace_size": ([I64, I64, I64], SZ),
         "q1_pack_from_dense": ([P, I32, I64, I64, P, P, P, P, P], I32),
         "q1_decode_chain": ([ctypes.POINTER(_CLayer), I32, P, I64, I32, P, P, SZ, P], I32),
+        "q1_gated_delta_workspace_size": ([ctypes.POINTER(_CDelta)], SZ),
+        "q1_gated_delta": ([ctypes.POINTER(_CDelta), P, SZ, P], I32),
+        "q1_sample": ([ctypes.POINTER(_CSample), P], I32),
         "q1_device_errors": ([ctypes.POINTER(ctypes.c_uint), P], I32),
         "q1_status_string": ([I32], ctypes.c_char_p),
     }
@@ -442,6 +463,137 @@ def decode_chain(layers, x: torch.Tensor, workspace=None, out=None) -> torch.Ten
                                                     workspace.numel() * workspace.element_size(),
                                                     _stream()))
     return y.reshape(*lead, D)
+
+
+def _rows(x: torch.Tensor, name: str, heads: int, dim: int) -> torch.Tensor:
+    """x [T, heads, dim] as rows whose heads are contiguous and 16-byte aligned: x itself where it is (a
+    view of a projection's columns, say), else a contiguous copy."""
+    per16 = 4 if x.dtype == torch.float32 else 8
+    st = x.stride()
+    if (st[2] == 1 and (heads == 1 or st[1] == dim) and st[0] % per16 == 0 and x.data_ptr() % 16 == 0
+            and (x.shape[0] < 2 or st[0] >= heads * dim)):
+        return x
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
+def _vector(t, name: str, n: int, dtype, device) -> Optional[torch.Tensor]:
+    """An optional contiguous device vector of n elements of `dtype`."""
+    if t is None:
+        return None
+    _cuda(t, name, device, current=False)
+    if t.dtype != dtype or t.numel() != n:
+        raise ValueError(f"{name} must hold {n} elements of {dtype} (got {t.dtype}, {tuple(t.shape)})")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                state: torch.Tensor, *, cu_seqlens: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
+                slots: Optional[torch.Tensor] = None, fresh: Optional[torch.Tensor] = None,
+                scale: Optional[float] = None, qk_l2norm: bool = False, workspace: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gated delta rule over a batch of sequences; returns o and updates `state` in place.
+
+    q, k [T, HK, DK] and v [T, HV, DV] (one dtype: bf16, fp16 or fp32) hold the tokens of all sequences one
+    after another, g (log decay) and beta [T, HV] fp32.  Sequence b has tokens cu_seqlens[b] ..
+    cu_seqlens[b+1] (int32 [B+1] on the device; `max_len`, the longest, is then best given: without it T is
+    assumed).  Without cu_seqlens, q, k, v [B, L, H, D] and g, beta [B, L, HV] are B sequences of L tokens.
+    state fp32 [n_slots, HV, DK, DV]; slots int32 [B] names each sequence's entry (default: entry b; outside
+    the pool: none), fresh int32 [B] marks those that start from zero.  scale defaults to DK ** -0.5."""
+    _cuda(q, "q")
+    dev = q.device
+    for t, name in ((k, "k"), (v, "v"), (g, "g"), (beta, "beta"), (state, "state")):
+        _cuda(t, name, dev, current=False)
+    dt = _x_dtype(q, "q")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError(f"q, k and v must have one dtype (got {q.dtype}, {k.dtype}, {v.dtype})")
+    if g.dtype != torch.float32 or beta.dtype != torch.float32:
+        raise ValueError(f"g and beta must be float32 (got {g.dtype}, {beta.dtype})")
+    lead = v.shape[:-2]
+    if cu_seqlens is None:
+        if q.dim() != 4 or k.dim() != 4 or v.dim() != 4 or g.dim() != 3 or beta.dim() != 3:
+            raise ValueError("without cu_seqlens, q, k, v are [B, L, H, D] and g, beta [B, L, HV]")
+        B, L = int(q.shape[0]), int(q.shape[1])
+        q, k, v, g, beta = (t.flatten(0, 1) for t in (q, k, v, g, beta))
+        max_len = L
+    else:
+        if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or g.dim() != 2 or beta.dim() != 2:
+            raise ValueError("with cu_seqlens, q, k, v are [T, H, D] and g, beta [T, HV]")
+        B = cu_seqlens.numel() - 1
+        cu_seqlens = _vector(cu_seqlens, "cu_seqlens", B + 1, torch.int32, dev)
+    if B < 1:
+        raise ValueError("gated_delta needs at least one sequence")
+    T, HK, DK = q.shape
+    HV, DV = v.shape[1], v.shape[2]
+    if tuple(k.shape) != (T, HK, DK) or v.shape[0] != T or tuple(g.shape) != (T, HV) or tuple(beta.shape) != (T, HV):
+        raise ValueError(f"shapes do not agree: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, "
+                         f"g {tuple(g.shape)}, beta {tuple(beta.shape)}")
+    if DK not in (64, 128) or DV not in (64, 128) or HK < 1 or HV < 1 or HV % HK:
+        raise ValueError(f"need DK and DV of 64 or 128 and HV a multiple of HK (got DK {DK}, DV {DV}, HK {HK}, HV {HV})")
+    if (state.dtype != torch.float32 or state.dim() != 4 or tuple(state.shape[1:]) != (HV, DK, DV)
+            or not state.is_contiguous()):
+        raise ValueError(f"state must be a contiguous float32 [slots, {HV}, {DK}, {DV}] "
+                         f"(got {state.dtype}, {tuple(state.shape)}, contiguous={state.is_contiguous()})")
+    slots = _vector(slots, "slots", B, torch.int32, dev)
+    fresh = _vector(fresh, "fresh", B, torch.int32, dev)
+    if slots is None and state.shape[0] < B:
+        raise ValueError(f"state holds {state.shape[0]} entries for {B} sequences")
+    q, k, v = _rows(q, "q", HK, DK), _rows(k, "k", HK, DK), _rows(v, "v", HV, DV)
+    if g.stride(1) != 1:
+        g = g.contiguous()
+    if beta.stride(1) != 1:
+        beta = beta.contiguous()
+    o = _out(out, (T, HV, DV), q.dtype, dev)
+    a = _CDelta(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                state.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _ptr(fresh), q.stride(0), k.stride(0), v.stride(0),
+                HV * DV, g.stride(0), beta.stride(0), T, B, state.shape[0], T if max_len is None else int(max_len),
+                HK, HV, DK, DV, dt, 1 if qk_l2norm else 0, DK ** -0.5 if scale is None else float(scale))
+    L = lib()
+    need = L.q1_gated_delta_workspace_size(a)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _cuda(workspace, "workspace", dev)
+    wp, wn = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
+    _check("q1_gated_delta", L.q1_gated_delta(a, wp, wn, _stream()))
+    return o.reshape(*lead, HV, DV)
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None):
+    """One token per row of logits [B, V] from the uniform numbers u [B] (fp32, in [0, 1)).
+
+    Returns (token int32 [B], prob fp32 [B]).  temperature, top_k, top_p and min_p are off (None), a number
+    for every row (taken as fp32; top_k int32), or a device tensor of B such elements.  Tokens rank by descending logit,
+    equal logits by ascending index; temperature 0 takes the first.  See q1_sample in include/q1.h."""
+    _cuda(logits, "logits")
+    dev = logits.device
+    dt = _x_dtype(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be 2-D [B, V] (got {tuple(logits.shape)})")
+    B, V = logits.shape
+    if not 1 <= V <= 1 << 18:
+        raise ValueError(f"need 1 <= V <= {1 << 18} (got {V})")
+    if V > 1 and logits.stride(1) != 1 or B > 1 and logits.stride(0) < V:
+        logits = logits.contiguous()
+    u = _vector(u, "u", B, torch.float32, dev)
+    if u is None:
+        raise ValueError("u must be given")
+    ptrs, vals = [], []
+    for val, name, dtype, off in ((temperature, "temperature", torch.float32, 1.0), (top_p, "top_p", torch.float32, 1.0),
+                                  (min_p, "min_p", torch.float32, 0.0), (top_k, "top_k", torch.int32, 0)):
+        if isinstance(val, torch.Tensor):
+            ptrs.append(_vector(val, name, B, dtype, dev))
+            vals.append(off)
+        else:
+            ptrs.append(None)
+            vals.append(off if val is None else val)
+    token = torch.empty((B,), dtype=torch.int32, device=dev)
+    prob = torch.empty((B,), dtype=torch.float32, device=dev)
+    a = _CSample(logits.data_ptr(), u.data_ptr(), *[_ptr(p) for p in ptrs], token.data_ptr(), prob.data_ptr(),
+                 B, V, logits.stride(0), dt, max(0, min(int(vals[3]), V)), float(vals[0]), float(vals[1]),
+                 float(vals[2]))
+    _check("q1_sample", lib().q1_sample(a, _stream()))
+    return token, prob
 
 
 def check_symmetric(W: Q1Weight) -> torch.Tensor:

@@ -276,6 +276,88 @@ q1_status q1_decode_chain(const q1_decode_layer *layers, int32_t n_layers, const
                           int64_t M, q1_dtype dtype, void *y, void *workspace,
                           size_t workspace_bytes, q1_stream stream);
 
+/* ---- gated delta rule (serving form; the delta-net layers that the Q1 linears
+ * of a hybrid decoder surround: "Support Bonsai-27B affine Q1", higgs PR #212,
+ * "Measured impact", the recurrent layers' fused projections) ----------------
+ * Per sequence and value head h (key head h / (HV / HK)), token after token,
+ * with the state S [DK][DV] in fp32:
+ *   S~  = exp(g_t) S_{t-1}
+ *   d_t = beta_t (v_t - S~^T k_t)
+ *   S_t = S~ + k_t d_t^T          o_t = scale * S_t^T q_t
+ * qk_l2norm != 0: q_t and k_t are first divided by sqrt(sum of squares + 1e-6).
+ * Tokens of all sequences are packed: row t of q, k, v, o, g and beta is token
+ * t, rows *_stride elements apart (so q, k and v may be columns of one
+ * projection's rows); inside a row the heads are contiguous.
+ *   cu_seqlens  device int32 [B+1], ascending from 0 to T: sequence b has tokens
+ *               [cu[b], cu[b+1]), possibly none.  NULL: B sequences of T/B tokens
+ *               (T % B == 0).
+ *   state       fp32 [n_slots][HV][DK][DV], updated in place: sequence b reads
+ *               and writes entry slots[b] (slots NULL: entry b, n_slots >= B).
+ *               A slot outside [0, n_slots) means no entry: the sequence starts
+ *               from zero and leaves nothing.  Entries named twice in one call
+ *               are undefined.
+ *   fresh       device int32 [B] or NULL: where nonzero, the sequence starts
+ *               from zero (its entry is only written).
+ *   max_len     the longest sequence (a hint that picks the kernels; results
+ *               do not depend on it beyond rounding).
+ * dtype: of q, k, v and o.  g (log decay, at most 0 in use) and beta are fp32.
+ * DK and DV 64 or 128; HV a multiple of HK.  q, k, v, o and state 16-byte
+ * aligned, q/k/v/o strides multiples of 16 bytes.  o must not overlap the inputs.
+ * Offsets in cu_seqlens that leave [0, T] or decrease are cut to it: the
+ * results of such a batch are undefined, its accesses stay inside the arrays.
+ * Workspace: q1_gated_delta_workspace_size bytes (0 where none is needed). */
+typedef struct {
+  const void *q, *k, *v;     /* [T][HK][DK], [T][HK][DK], [T][HV][DV] */
+  void *o;                   /* [T][HV][DV] */
+  const float *g, *beta;     /* [T][HV] */
+  float *state;
+  const int32_t *cu_seqlens, *slots, *fresh;
+  int64_t q_stride, k_stride, v_stride, o_stride, g_stride, beta_stride;
+  int64_t T, B, n_slots, max_len;
+  int32_t HK, HV, DK, DV;
+  int32_t dtype;             /* q1_dtype */
+  int32_t qk_l2norm;
+  float scale;
+} q1_delta_args;
+size_t q1_gated_delta_workspace_size(const q1_delta_args *args);
+q1_status q1_gated_delta(const q1_delta_args *args, void *workspace, size_t workspace_bytes,
+                         q1_stream stream);
+
+/* ---- sampling from a given random number ------------------------------------
+ * (the step after the tied head, higgs PR #212, "What": one token per row of
+ * logits.)  Per row, with weights w_i = exp((l_i - max l) / temperature), and
+ * the tokens in the order of descending logits, equal ones by ascending index:
+ *   top_k  keeps the first top_k of the order (0 or less: all);
+ *   top_p  keeps of those the ones with less than top_p * (their total weight)
+ *          before them (1 or more: all; the first always stays);
+ *   min_p  keeps of those the ones with w_i >= min(min_p, 1) (0 or less: all);
+ *   token  is the lowest index i with sum_{kept j <= i} w_j > u * sum_{kept} w_j,
+ *   prob   its weight over the kept ones' sum.
+ * temperature 0 or less (or NaN): the first of the order, prob 1.
+ * u in [0, 1); values below count as 0 and values above take the last token.
+ * NaN and -inf logits are never kept; +inf logits, where there are some, share
+ * the whole weight.  A row with nothing to keep gives token -1 and prob 0.
+ * Weights are fixed-point integers (44 fractional bits, computed to about
+ * 2^-34): their sums do not depend on the order of the additions, results
+ * are the same on every run, and tokens below 2^-45 of the likeliest have
+ * weight 0.
+ * logits [B][V] in dtype (bf16, fp16 or fp32), rows row_stride elements apart,
+ * any alignment of the element size.  1 <= V <= 262144.
+ * Settings are per row where the pointer is given (device, [B]), else the value. */
+typedef struct {
+  const void *logits;
+  const float *u;                                   /* [B] */
+  const float *temperature, *top_p, *min_p;         /* [B] or NULL */
+  const int32_t *top_k;                             /* [B] or NULL */
+  int32_t *token;                                   /* [B] */
+  float *prob;                                      /* [B] or NULL */
+  int64_t B, V, row_stride;
+  int32_t dtype;                                    /* q1_dtype */
+  int32_t top_k_value;
+  float temperature_value, top_p_value, min_p_value;
+} q1_sample_args;
+q1_status q1_sample(const q1_sample_args *args, q1_stream stream);
+
 /* ---- symmetric check (higgs PR #212, walkthrough: symmetric bias
  * compaction and validation) -------------------------------------------------
  * Writes 1 to *d_is_symmetric (device int32) iff every stored bias equals

@@ -1,0 +1,306 @@
+"""q1.gated_delta against the token-by-token float64 oracle.
+
+Bounds, per element of o: half a unit in the last place of the output type
+(finfo.eps / 2 relative), plus the arithmetic's own error.  That is fp32
+(2^-24 per operation) wherever a state or a correction is formed; the operands
+of the chunked form's matrix products are fp16 pairs (22 bits), except that the
+weights of a chunk's own tokens in o are a single fp16 (2^-11 relative).  What
+an error in them is relative to is the size of the terms, at most
+scale |q| max_t |S_t[:, c]| times a small constant for the chunk's partial sums:
+4 is allowed.  The state: 2^-20 per chunk of products, and 2^-24 a few times per
+token, relative to the largest norm that the head's state had.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as O
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def _inputs(lengths, HK, HV, DK, DV, dtype, seed, pool=None, strided=True, keys="random", decay="mixed"):
+    g = torch.Generator().manual_seed(seed)
+    T = sum(lengths)
+    row = torch.randn(T, 2 * HK * DK + HV * DV, generator=g)
+    if keys == "same":       # every key of a head alike: the worst conditioned chunk
+        row[:, HK * DK:2 * HK * DK] = row[:1, HK * DK:2 * HK * DK]
+    if keys == "tiny":
+        row *= 1e-4
+    if keys == "large":
+        row *= 300.0
+    row = row.to(DT[dtype])
+    if not strided:
+        q, k, v = (x.contiguous() for x in row.split([HK * DK, HK * DK, HV * DV], 1))
+    else:
+        q, k, v = row.split([HK * DK, HK * DK, HV * DV], 1)
+    q, k, v = q.unflatten(1, (HK, DK)), k.unflatten(1, (HK, DK)), v.unflatten(1, (HV, DV))
+    step = torch.exp(torch.rand(T, HV, generator=g) * 6.0 - 7.0)
+    gate = {"mixed": -(1 + 8 * torch.rand(HV, generator=g)) * step, "none": torch.zeros(T, HV),
+            "strong": -40.0 * torch.rand(T, HV, generator=g),
+            "reset": torch.where(torch.rand(T, HV, generator=g) < 0.1, -float("inf"), -step)}[decay]
+    beta = torch.sigmoid(torch.randn(T, HV, generator=g))
+    state = 0.3 * torch.randn(pool or len(lengths), HV, DK, DV, generator=g)
+    starts = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    return q, k, v, gate, beta, state, starts
+
+
+def _np(x):
+    return x.double().numpy()
+
+
+def _check(o, state, want_o, want_state, colmax, q, dtype, starts, scale, l2norm, slots, fresh=None):
+    assert torch.isfinite(o.float()).all() and torch.isfinite(state).all()
+    qn = np.ones(q.shape[:2]) if l2norm else np.linalg.norm(_np(q), axis=-1)
+    qn = np.repeat(qn, want_o.shape[1] // q.shape[1], 1)
+    eps = torch.finfo(DT[dtype]).eps / 2
+    arith = 2.0 ** -19 if dtype == "fp32" else 2.0 ** -11
+    for b in range(len(starts) - 1):
+        s = slice(starts[b], starts[b + 1])
+        L = starts[b + 1] - starts[b]
+        size = abs(scale) * qn[s][:, :, None] * colmax[b][None]
+        bound = eps * np.abs(want_o[s]) + 4 * arith * size + (6e-8 if dtype == "fp16" else 1e-37)
+        err = np.abs(_np(o.cpu())[s] - want_o[s])
+        assert (err <= bound).all(), f"sequence {b} (L = {L}): o off by {(err / bound).max():.2f} bounds"
+        if slots[b] is None:
+            continue
+        fro = np.linalg.norm(colmax[b], axis=-1)
+        e = np.linalg.norm((_np(state.cpu())[slots[b]] - want_state[slots[b]]).reshape(len(fro), -1), axis=-1)
+        assert (e <= 2.0 ** -20 * (4 + L / 16) * fro + 1e-37).all(), \
+            f"sequence {b} (L = {L}): state off by {(e / fro).max():.2e}"
+
+
+def _run(q1, lengths, HK, HV, DK, DV, dtype, seed, l2norm=True, scale=None, slots=None, fresh=None, pool=None, **kw):
+    q, k, v, g, beta, state, starts = _inputs(lengths, HK, HV, DK, DV, dtype, seed, pool, **kw)
+    scale = DK ** -0.5 if scale is None else scale
+    want_o, want_s, colmax = O.gated_delta(_np(q), _np(k), _np(v), _np(g), _np(beta), _np(state), starts, scale, l2norm,
+                                           slots, fresh)
+    d = "cuda"
+    row = torch.cat([x.flatten(1) for x in (q, k, v)], 1).to(d)   # columns of one row, as a projection gives
+    n = [q.shape[1] * DK, k.shape[1] * DK, v.shape[1] * DV]
+    qd, kd, vd = (x.unflatten(1, (-1, D)) for x, D in zip(row.split(n, 1), (DK, DK, DV)))
+    if not kw.get("strided", True):
+        qd, kd, vd = qd.contiguous(), kd.contiguous(), vd.contiguous()
+    sd = state.to(d)
+    i32 = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32, device=d)  # noqa: E731
+    o = q1.gated_delta(qd, kd, vd, g.to(d), beta.to(d), sd, cu_seqlens=i32(starts.tolist()), max_len=max(lengths + [1]),
+                       slots=i32(slots), fresh=i32(fresh), scale=scale, qk_l2norm=l2norm)
+    entries = list(range(len(lengths))) if slots is None else [s if 0 <= s < state.shape[0] else None for s in slots]
+    _check(o, sd, want_o, want_s, colmax, q, dtype, starts, scale, l2norm, entries)
+    untouched = [i for i in range(state.shape[0]) if i not in entries]
+    assert torch.equal(sd.cpu()[untouched], state[untouched])
+    return o, sd
+
+
+@pytest.fixture(scope="module")
+def q1():
+    from bit_affine_quantized_g128_gb300 import q1 as mod
+    mod.load_library()
+    return mod
+
+
+SHAPES = [(2, 4, 128, 128), (3, 3, 64, 64), (1, 3, 128, 64), (2, 2, 64, 128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("HK,HV,DK,DV", SHAPES)
+@pytest.mark.parametrize("lengths", [[1], [1, 1, 1], [2, 5, 0, 1], [8, 7], [17, 33]], ids=str)
+def test_short_sequences(q1, lengths, HK, HV, DK, DV, dtype):
+    _run(q1, lengths, HK, HV, DK, DV, dtype, seed=11 + len(lengths))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("HK,HV,DK,DV", SHAPES)
+@pytest.mark.parametrize("lengths", [[64], [63, 65], [128, 1, 0, 191], [257], [3, 200, 64]], ids=str)
+def test_long_sequences(q1, lengths, HK, HV, DK, DV, dtype):
+    _run(q1, lengths, HK, HV, DK, DV, dtype, seed=23 + len(lengths))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("decay", ["none", "strong", "reset"])
+@pytest.mark.parametrize("lengths", [[5], [150, 70]], ids=str)
+def test_decays(q1, lengths, decay, dtype):
+    _run(q1, lengths, 2, 4, 128, 128, dtype, seed=5, decay=decay)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,keys", [("bf16", "same"), ("fp16", "same"), ("bf16", "tiny"), ("bf16", "large"),
+                                        ("fp16", "large")])
+@pytest.mark.parametrize("lengths", [[6], [130]], ids=str)
+def test_keys(q1, lengths, dtype, keys):
+    _run(q1, lengths, 2, 4, 128, 128, dtype, seed=7, keys=keys)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths", [[3, 1, 4], [100, 65, 90]], ids=str)
+def test_without_norm_and_with_a_scale(q1, lengths):
+    # keys of length about 1, as a caller that normalises itself passes them
+    q, k, v, g, beta, state, starts = _inputs(lengths, 2, 4, 128, 128, "bf16", 3)
+    k = (k.float() / k.float().norm(dim=-1, keepdim=True)).bfloat16()
+    want_o, want_s, colmax = O.gated_delta(_np(q), _np(k), _np(v), _np(g), _np(beta), _np(state), starts, 0.25, False)
+    sd = state.cuda()
+    o = q1.gated_delta(q.cuda(), k.cuda(), v.cuda(), g.cuda(), beta.cuda(), sd,
+                       cu_seqlens=torch.from_numpy(starts).cuda(), max_len=max(lengths), scale=0.25)
+    _check(o, sd, want_o, want_s, colmax, q, "bf16", starts, 0.25, False, [0, 1, 2])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths", [[1, 1, 1, 1], [70, 1, 130, 5]], ids=str)
+def test_slots_fresh_and_missing_entries(q1, lengths):
+    _run(q1, lengths, 2, 4, 128, 128, "bf16", seed=9, slots=[5, -1, 2, 0], fresh=[0, 0, 1, 0], pool=7)
+    _run(q1, lengths, 2, 4, 128, 128, "bf16", seed=9, slots=[5, 7, 2, 0], fresh=[1, 1, 1, 1], pool=7)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L", [1, 3, 96])
+def test_equal_lengths_without_offsets(q1, L):
+    q, k, v, g, beta, state, starts = _inputs([L] * 3, 2, 4, 128, 128, "bf16", 31)
+    b4 = lambda x: x.unflatten(0, (3, L)).cuda()  # noqa: E731
+    sd, se = state.cuda(), state.cuda()
+    o = q1.gated_delta(b4(q), b4(k), b4(v), b4(g), b4(beta), sd, qk_l2norm=True)
+    e = q1.gated_delta(q.cuda(), k.cuda(), v.cuda(), g.cuda(), beta.cuda(), se, max_len=L,
+                       cu_seqlens=torch.from_numpy(starts).cuda(), qk_l2norm=True)
+    assert o.shape == (3, L, 4, 128)
+    assert torch.equal(o.flatten(0, 1), e) and torch.equal(sd, se)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths", [[9, 4], [140, 77]], ids=str)
+def test_in_pieces_equals_whole(q1, lengths):
+    # the state carries a sequence over a cut
+    q, k, v, g, beta, state, starts = _inputs(lengths, 2, 4, 128, 128, "bf16", 41)
+    cut = [n // 2 for n in lengths]
+    ids = [torch.cat([torch.arange(starts[b], starts[b] + cut[b]) for b in range(2)]),
+           torch.cat([torch.arange(starts[b] + cut[b], starts[b + 1]) for b in range(2)])]
+    want_o, want_s, colmax = O.gated_delta(_np(q), _np(k), _np(v), _np(g), _np(beta), _np(state), starts, 128 ** -0.5, True)
+    sd = state.cuda()
+    o = torch.empty(v.shape, dtype=v.dtype)
+    for part, ns in zip(ids, (cut, [n - c for n, c in zip(lengths, cut)])):
+        cu = torch.tensor([0, ns[0], ns[0] + ns[1]], dtype=torch.int32, device="cuda")
+        o[part] = q1.gated_delta(q[part].cuda(), k[part].cuda(), v[part].cuda(), g[part].cuda(), beta[part].cuda(), sd,
+                                 cu_seqlens=cu, max_len=max(ns), qk_l2norm=True).cpu()
+    _check(o, sd, want_o, want_s, colmax, q, "bf16", starts, 128 ** -0.5, True, [0, 1])
+
+
+@pytest.mark.gpu
+def test_neighbours_do_not_leak(q1):
+    # a sequence full of infinities and NaN next to a clean one changes nothing in it
+    lengths = [70, 90, 3]
+    q, k, v, g, beta, state, starts = _inputs(lengths, 2, 4, 128, 128, "bf16", 43)
+    args = [x.cuda() for x in (q.contiguous(), k.contiguous(), v.contiguous(), g, beta)]
+    cu = torch.from_numpy(starts).cuda()
+    s0 = state.cuda()
+    o0 = q1.gated_delta(*args, s0, cu_seqlens=cu, max_len=90, qk_l2norm=True)
+    for x, bad in zip(args, (float("inf"), float("nan"), float("inf"), float("nan"), float("nan"))):
+        x[starts[1]:starts[2]] = bad
+    s1 = state.cuda()
+    o1 = q1.gated_delta(*args, s1, cu_seqlens=cu, max_len=90, qk_l2norm=True)
+    for b in (0, 2):
+        assert torch.equal(o0[starts[b]:starts[b + 1]], o1[starts[b]:starts[b + 1]])
+        assert torch.equal(s0[b], s1[b])
+
+
+@pytest.mark.gpu
+def test_offsets_out_of_range_stay_inside(q1):
+    # results are undefined; the call returns, and nothing outside the arrays is touched
+    q, k, v, g, beta, state, starts = _inputs([80, 50], 2, 4, 128, 128, "bf16", 47)
+    args = [x.cuda() for x in (q, k, v, g, beta)]
+    for bad in ([0, 500, 130], [-5, 80, 130], [90, 20, 1 << 30], [130, 0, 130]):
+        for ml in (1, 130):
+            q1.gated_delta(*args, state.cuda(), cu_seqlens=torch.tensor(bad, dtype=torch.int32, device="cuda"), max_len=ml)
+    torch.cuda.synchronize()
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L", [1, 100])
+def test_other_stream_and_graph(q1, L):
+    q, k, v, g, beta, state, starts = _inputs([L, L], 2, 4, 128, 128, "bf16", 51)
+    args = [x.cuda() for x in (q.contiguous(), k.contiguous(), v.contiguous(), g, beta)]
+    cu = torch.from_numpy(starts).cuda()
+    s0 = state.cuda()
+    o0 = q1.gated_delta(*args, s0, cu_seqlens=cu, max_len=L, qk_l2norm=True)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        s1 = state.cuda()
+        o1 = q1.gated_delta(*args, s1, cu_seqlens=cu, max_len=L, qk_l2norm=True)
+    st.synchronize()
+    assert torch.equal(o0, o1) and torch.equal(s0, s1)
+    s2, graph = state.cuda(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2 = q1.gated_delta(*args, s2, cu_seqlens=cu, max_len=L, qk_l2norm=True)
+    s2.copy_(state.cuda())
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o0, o2) and torch.equal(s0, s2)
+
+
+# ---- refusals (no GPU needed: validation comes before the library)
+@pytest.fixture
+def fake(monkeypatch):
+    from bit_affine_quantized_g128_gb300 import q1 as mod
+
+    def _forbidden(*a, **k):
+        raise AssertionError("the library was reached with invalid arguments")
+    monkeypatch.setattr(mod, "lib", _forbidden)
+    monkeypatch.setattr(mod, "load_library", _forbidden)
+    monkeypatch.setattr(mod, "_is_cuda", lambda t: True)
+    monkeypatch.setattr(mod, "_current_device", lambda: torch.device("cpu"))
+    return mod
+
+
+def _host(T=6, HK=2, HV=4, DK=64, DV=64, dtype=torch.bfloat16, B=2):
+    return dict(q=torch.zeros(T, HK, DK, dtype=dtype), k=torch.zeros(T, HK, DK, dtype=dtype),
+                v=torch.zeros(T, HV, DV, dtype=dtype), g=torch.zeros(T, HV), beta=torch.zeros(T, HV),
+                state=torch.zeros(B, HV, DK, DV), cu_seqlens=torch.tensor([0, 3, 6], dtype=torch.int32))
+
+
+@pytest.mark.parametrize("change,match", [
+    (dict(q=torch.zeros(6, 2, 64, dtype=torch.float64)), "bfloat16"),
+    (dict(k=torch.zeros(6, 2, 64)), "one dtype"),
+    (dict(g=torch.zeros(6, 4, dtype=torch.bfloat16)), "float32"),
+    (dict(beta=torch.zeros(6, 3)), "agree"),
+    (dict(v=torch.zeros(5, 4, 64, dtype=torch.bfloat16)), "agree"),
+    (dict(v=torch.zeros(6, 3, 64, dtype=torch.bfloat16), g=torch.zeros(6, 3), beta=torch.zeros(6, 3)), "multiple of HK"),
+    (dict(v=torch.zeros(6, 4, 96, dtype=torch.bfloat16)), "64 or 128"),
+    (dict(state=torch.zeros(2, 4, 64, 64, dtype=torch.bfloat16)), "state"),
+    (dict(state=torch.zeros(2, 4, 64, 128)[..., ::2]), "contiguous"),
+    (dict(state=torch.zeros(1, 4, 64, 64)), "entries"),
+    (dict(cu_seqlens=torch.tensor([0, 6])), "cu_seqlens"),
+    (dict(cu_seqlens=torch.tensor([0], dtype=torch.int32)), "at least one"),
+    (dict(cu_seqlens=None), "without cu_seqlens"),
+    (dict(slots=torch.zeros(3, dtype=torch.int32)), "slots"),
+    (dict(fresh=torch.zeros(2)), "fresh"),
+    (dict(out=torch.zeros(6, 4, 64)), "out"),
+])
+def test_refuses(fake, change, match):
+    with pytest.raises(ValueError, match=match):
+        fake.gated_delta(**{**_host(), **change})
+
+
+def test_refuses_host_tensors():
+    from bit_affine_quantized_g128_gb300 import q1 as mod
+    with pytest.raises(ValueError, match="CUDA"):
+        mod.gated_delta(**_host())
+
+
+@pytest.mark.gpu
+def test_c_refusals(q1):
+    z = torch.zeros(1 << 16, device="cuda")
+    p = z.data_ptr()
+
+    def call(**kw):
+        a = dict(q=p, k=p, v=p, o=p, g=p, beta=p, state=p, cu_seqlens=None, slots=None, fresh=None, q_stride=128,
+                 k_stride=128, v_stride=256, o_stride=256, g_stride=4, beta_stride=4, T=2, B=2, n_slots=2, max_len=1,
+                 HK=2, HV=4, DK=64, DV=64, dtype=0, qk_l2norm=1, scale=1.0)
+        a.update(kw)
+        return q1.lib().q1_gated_delta(q1._CDelta(**a), None, 0, None)
+    for kw, status in [(dict(q=None), 1), (dict(state=None), 1), (dict(DK=96), 2), (dict(HV=3), 2), (dict(HK=0), 2),
+                       (dict(T=3), 2), (dict(B=0), 2), (dict(n_slots=1), 2), (dict(v_stride=128), 2),
+                       (dict(q=p + 2), 3), (dict(k_stride=132), 3), (dict(state=p + 8), 3), (dict(dtype=3), 4)]:
+        assert call(**kw) == status, kw
+    assert q1.lib().q1_gated_delta(None, None, 0, None) == 1
