@@ -326,18 +326,27 @@ q1::DeltaView delta_view(const q1_delta_args *a) {
 }
 }  // namespace
 
+namespace {
+// Sequences of up to kDeltaStepMax tokens go token by token, as do fp32
+// activations (the chunked form's operands hold 16-bit inputs exactly, not
+// fp32 ones).
+constexpr int64_t kDeltaStepMax = 32;
+bool delta_in_chunks(const q1_delta_args *a) { return a->max_len > kDeltaStepMax && a->dtype != Q1_F32 && a->T > 0; }
+}  // namespace
+
 size_t q1_gated_delta_workspace_size(const q1_delta_args *a) {
-  (void)a;
-  return 0;
+  if (check_delta(a) != Q1_OK || !delta_in_chunks(a)) return 0;
+  return q1::delta_chunk_workspace_bytes(delta_view(a));
 }
 
 q1_status q1_gated_delta(const q1_delta_args *a, void *workspace, size_t workspace_bytes, q1_stream stream) {
   q1_status s = check_device();
   if (s != Q1_OK) return s;
   if ((s = check_delta(a)) != Q1_OK) return s;
-  (void)workspace;
-  (void)workspace_bytes;
-  return cuda_status(q1::launch_delta_step(delta_view(a), (q1_dtype)a->dtype, (cudaStream_t)stream));
+  const q1::DeltaView v = delta_view(a);
+  if (!delta_in_chunks(a)) return cuda_status(q1::launch_delta_step(v, (q1_dtype)a->dtype, (cudaStream_t)stream));
+  if ((s = check_ws(workspace, workspace_bytes, q1::delta_chunk_workspace_bytes(v))) != Q1_OK) return s;
+  return cuda_status(q1::launch_delta_chunks(v, (q1_dtype)a->dtype, workspace, (cudaStream_t)stream));
 }
 
 q1_status q1_sample(const q1_sample_args *a, q1_stream stream) {
@@ -374,6 +383,7 @@ q1_status push_diagnostics() {
   const int stall = g_stall.load();
   cudaError_t e = q1::set_narrow_diagnostics(ns, stall);
   if (e == cudaSuccess) e = q1::set_wide_diagnostics(ns, stall);
+  if (e == cudaSuccess) e = q1::set_delta_diagnostics(ns, stall);
   return cuda_status(e);
 }
 }  // namespace
@@ -395,11 +405,12 @@ q1_status q1_set_stalled_producers(int stall) {
 q1_status q1_device_errors(unsigned int *flags, q1_stream stream) {
   q1_status s = check_device();
   if (s != Q1_OK) return s;
-  cudaError_t e1 = cudaSuccess, e2 = cudaSuccess;
+  cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess;
   unsigned int v = q1::read_and_clear_wide_errors((cudaStream_t)stream, &e1);
   v |= q1::read_and_clear_narrow_errors((cudaStream_t)stream, &e2) << 1;
+  v |= q1::read_and_clear_delta_errors((cudaStream_t)stream, &e3) << 2;
   if (flags) *flags = v;
-  if (e1 != cudaSuccess || e2 != cudaSuccess) return Q1_ERR_CUDA;
+  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess) return Q1_ERR_CUDA;
   return v ? Q1_ERR_TIMEOUT : Q1_OK;
 }
 

@@ -1,0 +1,996 @@
+// Gated delta rule in chunks of 64 tokens (prefill).
+//
+// With G the inclusive sum of g inside a chunk, gamma = exp(G), the tokens of a
+// chunk that starts from the state S satisfy, all at once,
+//   A_ij = beta_i exp(G_i - G_j) (k_i . k_j)  (i > j),  T = (I + A)^-1 diag(beta)
+//   R    = V - diag(gamma) K S                          [64][DV]
+//   U    = T R
+//   O    = scale (diag(gamma) Q S + P U),   P_ij = exp(G_i - G_j) (q_i . k_j)  (i >= j)
+//   S   <- gamma_C S + K^T diag(exp(G_C - G)) U
+// and P U = (P T) R.  T and P' = scale P T depend on the keys, queries and
+// gates only: a first kernel computes them for all chunks at once, and a second
+// one, a CTA per sequence and head, walks the chunks with matrix products only.
+//
+// Operand precision.  The state is fp32 and goes through one product per
+// chunk, so operands rounded to 16 bits once would leave it 2^-9 or 2^-12 off.
+// Every fp32 operand (S, R, the scaled U, T) is a sum of two fp16 values
+// instead, high and low, 22 bits together, scaled by a power of two (per row
+// of the operand, or per tile) so that its largest value lies in
+// [2^14, 2^15): the products with both halves are exact in fp32 up to its own
+// rounding.  Keys and queries enter as single fp16 values, scaled per row:
+// bf16 and fp16 inputs are exact in them down to 2^-28 of the row's largest
+// value.  P' is a single fp16 (2^-11 relative): its product is an output that
+// is rounded to 16 bits, not a state.
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "q1_internal.h"
+
+namespace q1 {
+
+__device__ unsigned int g_delta_err = 0;
+__constant__ unsigned long long c_delta_wait_ns = 2000000000ull;
+__constant__ int c_delta_stall = 0;
+
+namespace {
+
+constexpr int kC = 64;                       // tokens of a chunk
+constexpr int kTile = kC * kC * 2;           // bytes of a 64 x 64 fp16 tile
+constexpr int kScalars = 3 * kC + 16;        // floats: a, c, b, then gamma_C and P's scale
+constexpr int kScalarBytes = kScalars * 4;
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// A chunk's place in the workspace: sequence b's chunks start at
+// cu[b] / 64 + b.  That leaves room for each sequence's last partial chunk
+// without a sum over the sequences before it, and stays below T / 64 + B + 1.
+__device__ __forceinline__ int64_t chunk_base(int64_t t0, int64_t b) { return t0 / kC + b; }
+
+struct ChunkPlaces {
+  unsigned char *kq;  // [chunks][HK] K tile, Q tile: 64 x DK fp16 each
+  unsigned char *tp;  // [chunks][HV] T high, P', T low: 64 x 64 fp16 each
+  float *sc;          // [chunks][HV][kScalars]
+};
+__host__ __device__ inline int64_t chunk_places(int64_t T, int64_t B) { return T / kC + B + 1; }
+
+// Tiles are stored as the products read them from shared memory: rows of 128
+// bytes (64 values), the 16-byte pieces of row r exchanged by XOR with r mod 8;
+// wider tiles are 64-column boxes one after another.
+__device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
+
+// 2^e as a float, and the e that brings a value of size mx into [2^14, 2^15).
+// Zero, infinite and NaN sizes take e = 0.
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ int scale_exp(float mx) {
+  const int e = (int)((__float_as_uint(mx) >> 23) & 0xFF);
+  if (e == 0 || e == 255) return 0;
+  const int s = 14 - (e - 127);
+  return s > 100 ? 100 : s < -100 ? -100 : s;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// (a, b) as fp16 high parts, and what they leave as fp16 low parts
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  lo = half2_bits(a - f.x, b - f.y);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ======================================================================
+// Per chunk and key head: the fp16 K and Q tiles, and for each of its value
+// heads T, P' and the per-token factors.  Four warps; warp w owns rows
+// 16w .. 16w+15 of the 64 x 64 products K K^T and Q K^T, which stay in its
+// registers while the value heads are gone through.
+constexpr int kPrepT = 128;
+constexpr int kLd = 68;  // row length of the fp32 matrices (keeps 16-byte rows)
+
+struct PrepShared {
+  float A[kC * kLd];   // A, unit lower triangle left out
+  float Ti[kC * kLd];  // (I + A)^-1
+  float W[16 * 52];    // a block row of A (I + A)^-1
+  float rk[kC], rq[kC];        // factors of the fp16 rows: norm, scale and 2^-e
+  float Gh[kC], Gl[kC];        // log2(e) G = Gh + Gl
+  float beta[kC];
+  float g[kC];
+  float red[8];
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    } else {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+template <typename T, int DK>
+__global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  constexpr int kKq = kC * DK * 2;                          // bytes of a K or Q tile
+  constexpr int kArea = 2 * kKq > 3 * kTile ? 2 * kKq : 3 * kTile;
+  unsigned char *kt = base, *qt = base + kKq;               // K, Q tiles; later T high, P', T low
+  PrepShared &sh = *reinterpret_cast<PrepShared *>(base + kArea);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t place = blockIdx.x;
+  const int hk = blockIdx.y;
+  // the sequence whose places include this one
+  int64_t lo = 0, hi = a.B - 1, t0, t1;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) / 2;
+    a.range(mid, t0, t1);
+    if (chunk_base(t0, mid) <= place) lo = mid;
+    else hi = mid - 1;
+  }
+  a.range(lo, t0, t1);
+  const int64_t nth = place - chunk_base(t0, lo);
+  t0 += nth * kC;
+  if (nth < 0 || t0 >= t1) return;
+  const int len = (int)min((int64_t)kC, t1 - t0);
+
+  // ---- K and Q rows -> fp16 tiles, scaled to the row's size; DK/8 lanes per row
+  constexpr int LPR = DK / 8, RPI = kPrepT / LPR, NI = kC / RPI;
+  const int piece = tid % LPR;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const T *src = static_cast<const T *>(which ? a.q : a.k) + t0 * (which ? a.q_stride : a.k_stride) + (int64_t)hk * DK + piece * 8;
+    const int64_t stride = which ? a.q_stride : a.k_stride;
+    uint4 v[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = tid / LPR + i * RPI;
+      v[i] = r < len ? __ldg(reinterpret_cast<const uint4 *>(src + r * stride)) : make_uint4(0, 0, 0, 0);
+    }
+    unsigned char *tile = which ? qt : kt;
+    unsigned char *out = ws.kq + ((place * a.HK + hk) * 2 + which) * (int64_t)kKq;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = tid / LPR + i * RPI;
+      float f[8], ss = 0.f, mx = 0.f;
+      unpack8<T>(v[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ss = fmaf(f[e], f[e], ss);
+        mx = fmaxf(mx, fabsf(f[e]));
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      }
+      const int e = scale_exp(mx);
+      const float s = pow2f(e);
+      uint4 h;
+      h.x = half2_bits(f[0] * s, f[1] * s);
+      h.y = half2_bits(f[2] * s, f[3] * s);
+      h.z = half2_bits(f[4] * s, f[5] * s);
+      h.w = half2_bits(f[6] * s, f[7] * s);
+      const uint32_t at = (uint32_t)(piece >> 3) * (kC * 128) + swz(r, piece & 7);
+      *reinterpret_cast<uint4 *>(tile + at) = h;
+      *reinterpret_cast<uint4 *>(out + at) = h;
+      if (piece == 0) {
+        const float n = (a.l2norm ? 1.f / sqrtf(ss + kDeltaEps) : 1.f) * pow2f(-e);
+        if (which) sh.rq[r] = n * a.scale;
+        else sh.rk[r] = n;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- K K^T and Q K^T, columns up to this warp's rows
+  float kk[4][2][4] = {}, qk[4][2][4] = {};
+#pragma unroll
+  for (int s = 0; s < DK / 16; ++s) {
+    const uint32_t box = (uint32_t)(s >> 2) * (kC * 128);
+    const int p0 = (s & 3) * 2;
+    uint32_t ak[4], aq[4];
+    const int ar = 16 * warp + (lane & 15);
+    ldsm4(smem_u32(kt + box) + swz(ar, p0 + (lane >> 4)), ak);
+    ldsm4(smem_u32(qt + box) + swz(ar, p0 + (lane >> 4)), aq);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j <= warp) {
+        uint32_t b[4];
+        ldsm4(smem_u32(kt + box) + swz(16 * j + (lane & 7) + ((lane >> 4) << 3), p0 + ((lane >> 3) & 1)), b);
+        mma16(kk[j][0], ak, b[0], b[1]);
+        mma16(kk[j][1], ak, b[2], b[3]);
+        mma16(qk[j][0], aq, b[0], b[1]);
+        mma16(qk[j][1], aq, b[2], b[3]);
+      }
+  }
+  __syncthreads();  // the tiles' area is free
+  unsigned char *th = base, *pt = base + kTile, *tl = base + 2 * kTile;
+
+  const int group = a.HV / a.HK;
+  const int r0 = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);  // fragment rows r0, r0 + 8; columns 8n + c0, + 1
+  for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
+    // ---- gates
+    if (tid < kC) {
+      float g = 0.f, be = 0.f;
+      if (tid < len) {
+        g = a.g[(t0 + tid) * a.g_stride + hv];
+        be = a.beta[(t0 + tid) * a.beta_stride + hv];
+        // exp(-200) is 0 in fp32 already; the limit keeps sums of g finite
+        g = g < -200.f ? -200.f : g;
+      }
+      sh.g[tid] = g;
+      sh.beta[tid] = be;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // G in float64: differences of sums that may be large are taken later
+      const double x = sh.g[2 * lane], y = sh.g[2 * lane + 1];
+      double s = x + y;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double z = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += z;
+      }
+      const double l2e = 1.4426950408889634;
+      const double g1 = s * l2e, g0 = (s - y) * l2e;
+      sh.Gh[2 * lane] = (float)g0;
+      sh.Gl[2 * lane] = (float)(g0 - (double)(float)g0);
+      sh.Gh[2 * lane + 1] = (float)g1;
+      sh.Gl[2 * lane + 1] = (float)(g1 - (double)(float)g1);
+    }
+    __syncthreads();
+    // ---- A into shared memory; P into registers (kept as the next product's operand)
+    float p[4][2][4];
+    float pmax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = r0 + 8 * e;
+      const float gh = sh.Gh[i], gl = sh.Gl[i], ba = sh.beta[i] * sh.rk[i], rq = sh.rq[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float av[2] = {0.f, 0.f}, pv[2] = {0.f, 0.f};
+          const int c = 16 * j + 8 * n + c0;
+          if (j <= warp) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (c + x <= i) {
+                const float w = exp2f((gh - sh.Gh[c + x]) + (gl - sh.Gl[c + x])) * sh.rk[c + x];
+                pv[x] = w * rq * qk[j][n][2 * e + x];
+                if (c + x < i) av[x] = w * ba * kk[j][n][2 * e + x];
+              }
+            *reinterpret_cast<float2 *>(&sh.A[i * kLd + c]) = make_float2(av[0], av[1]);
+          }
+          p[j][n][2 * e] = pv[0];
+          p[j][n][2 * e + 1] = pv[1];
+          pmax = fmaxf(pmax, fmaxf(fabsf(pv[0]), fabsf(pv[1])));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, o));
+    const int pe = scale_exp(pmax);
+    __syncthreads();
+    // ---- (I + A)^-1 by forward substitution: the four diagonal blocks of 16
+    // (a thread per column), then block row by block row
+    if (tid < kC) {
+      const int b16 = tid & ~15, j = tid & 15;
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float s = i == j ? 1.f : 0.f;
+        const float *row = &sh.A[(b16 + i) * kLd + b16];
+#pragma unroll
+        for (int m4 = 0; m4 < 16; m4 += 4)
+          if (m4 < i) {
+            const float4 av = *reinterpret_cast<const float4 *>(row + m4);
+            s = fmaf(-av.x, x[m4], s);
+            if (m4 + 1 < i) s = fmaf(-av.y, x[m4 + 1], s);
+            if (m4 + 2 < i) s = fmaf(-av.z, x[m4 + 2], s);
+            if (m4 + 3 < i) s = fmaf(-av.w, x[m4 + 3], s);
+          }
+        x[i] = s;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sh.Ti[(b16 + i) * kLd + b16 + j] = x[i];
+    } else {
+      // blocks above the diagonal
+      const int t = tid - kC;
+      for (int at = t; at < kC * 16; at += kC) {
+        const int row = at >> 4, col = (at & 15) * 4;
+        if ((col >> 4) > (row >> 4)) *reinterpret_cast<float4 *>(&sh.Ti[row * kLd + col]) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int I = 1; I < 4; ++I) {
+      const int r = tid >> 3, cc = tid & 7;
+      float acc[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int m = 0; m < 16 * I; m += 4) {
+        const float4 av = *reinterpret_cast<const float4 *>(&sh.A[(16 * I + r) * kLd + m]);
+        const float x[4] = {av.x, av.y, av.z, av.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int n = 0; n < 2 * I; ++n) acc[n] = fmaf(x[q], sh.Ti[(m + q) * kLd + cc + 8 * n], acc[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < 2 * I; ++n) sh.W[r * 52 + cc + 8 * n] = acc[n];
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < 6; ++n) acc[n] = 0.f;
+#pragma unroll
+      for (int m = 0; m < 16; m += 4) {
+        const float4 tv = *reinterpret_cast<const float4 *>(&sh.Ti[(16 * I + r) * kLd + 16 * I + m]);
+        const float x[4] = {tv.x, tv.y, tv.z, tv.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int n = 0; n < 2 * I; ++n) acc[n] = fmaf(-x[q], sh.W[(m + q) * 52 + cc + 8 * n], acc[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < 2 * I; ++n) sh.Ti[(16 * I + r) * kLd + cc + 8 * n] = acc[n];
+      __syncthreads();
+    }
+    // ---- T = (I + A)^-1 diag(beta) as fp16 pairs
+    float tv[32], tmax = 0.f;
+    const int tr = tid >> 1, tc = (tid & 1) * 32;  // half a row per thread
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(&sh.Ti[tr * kLd + tc + c]);
+      const float4 be = *reinterpret_cast<const float4 *>(&sh.beta[tc + c]);
+      tv[c] = x.x * be.x;
+      tv[c + 1] = x.y * be.y;
+      tv[c + 2] = x.z * be.z;
+      tv[c + 3] = x.w * be.w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tmax = fmaxf(tmax, fabsf(tv[c + e]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, o));
+    if (lane == 0) sh.red[warp] = tmax;
+    __syncthreads();
+    tmax = fmaxf(fmaxf(sh.red[0], sh.red[1]), fmaxf(sh.red[2], sh.red[3]));
+    const int te = scale_exp(tmax);
+    const float ts = pow2f(te);
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+      uint4 h, l;
+      split2(tv[c] * ts, tv[c + 1] * ts, h.x, l.x);
+      split2(tv[c + 2] * ts, tv[c + 3] * ts, h.y, l.y);
+      split2(tv[c + 4] * ts, tv[c + 5] * ts, h.z, l.z);
+      split2(tv[c + 6] * ts, tv[c + 7] * ts, h.w, l.w);
+      const uint32_t at = swz(tr, (tc + c) >> 3);
+      *reinterpret_cast<uint4 *>(th + at) = h;
+      *reinterpret_cast<uint4 *>(tl + at) = l;
+    }
+    __syncthreads();
+    // ---- P' = P T, both as fp16 pairs (three products)
+    float pp[4][2][4] = {};
+    const float ps = pow2f(pe);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (s <= warp) {
+        uint32_t ph[4], pl[4];
+        split2(p[s][0][0] * ps, p[s][0][1] * ps, ph[0], pl[0]);
+        split2(p[s][0][2] * ps, p[s][0][3] * ps, ph[1], pl[1]);
+        split2(p[s][1][0] * ps, p[s][1][1] * ps, ph[2], pl[2]);
+        split2(p[s][1][2] * ps, p[s][1][3] * ps, ph[3], pl[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j <= s) {
+            uint32_t bh[4], bl[4];
+            const uint32_t at = swz(16 * s + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * j + (lane >> 4));
+            ldsm4t(smem_u32(th) + at, bh);
+            ldsm4t(smem_u32(tl) + at, bl);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              mma16(pp[j][n], pl, bh[2 * n], bh[2 * n + 1]);
+              mma16(pp[j][n], ph, bl[2 * n], bl[2 * n + 1]);
+              mma16(pp[j][n], ph, bh[2 * n], bh[2 * n + 1]);
+            }
+          }
+      }
+    const float un = pow2f(-pe) * pow2f(-te);
+    float qmax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pp[j][n][e] *= un;
+          qmax = fmaxf(qmax, fabsf(pp[j][n][e]));
+        }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
+    if (lane == 0) sh.red[4 + warp] = qmax;
+    __syncthreads();
+    qmax = fmaxf(fmaxf(sh.red[4], sh.red[5]), fmaxf(sh.red[6], sh.red[7]));
+    const int qe = scale_exp(qmax);
+    const float qs = pow2f(qe);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint32_t *>(pt + swz(r0 + 8 * e, 2 * j + n) + c0 * 2) =
+              half2_bits(pp[j][n][2 * e] * qs, pp[j][n][2 * e + 1] * qs);
+    // ---- factors per token
+    float *sc = ws.sc + (place * a.HV + hv) * kScalars;
+    if (tid < kC) {
+      const float gam = exp2f(sh.Gh[tid] + sh.Gl[tid]);
+      const float tail = exp2f((sh.Gh[kC - 1] - sh.Gh[tid]) + (sh.Gl[kC - 1] - sh.Gl[tid]));
+      sc[tid] = gam * sh.rk[tid];
+      sc[kC + tid] = tail * sh.rk[tid] * pow2f(-te);
+      sc[2 * kC + tid] = gam * sh.rq[tid];
+      if (tid == kC - 1) {
+        sc[3 * kC] = gam;
+        sc[3 * kC + 1] = pow2f(-qe);
+      }
+    }
+    __syncthreads();
+    uint4 *dst = reinterpret_cast<uint4 *>(ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile));
+#pragma unroll
+    for (int i = tid; i < 3 * kTile / 16; i += kPrepT) dst[i] = reinterpret_cast<const uint4 *>(base)[i];
+    __syncthreads();
+  }
+}
+
+template <int DK>
+constexpr size_t prep_smem() {
+  return 1024 + (2 * kC * DK * 2 > 3 * kTile ? 2 * kC * DK * 2 : 3 * kTile) + sizeof(PrepShared);
+}
+
+// ======================================================================
+// The walk over a sequence's chunks, one CTA per sequence and value head.
+// All products are in the transposed form, a value column per lane of tensor
+// memory, so that the operand made from registers is the MMA's A operand in
+// tensor memory (M = 128 lanes) and K, Q, T and P' are its B operands as they
+// lie in shared memory:
+//   chain warps 0-7 (a lane = a column c of the state; warps w and w + 4 hold
+//   S[:DK/2, c] and S[DK/2:, c] in registers and take half of the tokens each):
+//     1  S -> high, low                     MMA: KS = S^T K^T, QS = S^T Q^T
+//     2  R = V - a KS -> high, low          MMA: [U | O2] = R^T [T ; P']^T
+//     3  c U -> high, low                   MMA: D = (c U)^T K
+//     4  S = gamma_C S + D
+//   output warps 8-11: o = b QS + O2
+//   warp 12: copies of the next chunk's tiles, factors and V rows (two stages)
+//   warp 13: tensor memory, and one thread that issues the MMAs
+// One chunk is a chain of three dependent products; the time is the latency of
+// that chain, not the rate of any unit.
+// Tensor memory (256 columns): S high [0, 64), low [64, 128); KS [128, 192);
+// QS [192, 256).  R and then c U: high [0, 32), low [32, 64).  U [64, 128) and
+// O2 [128, 192); D [64, 192).  Each reuse is behind the barrier of the MMA that
+// read, or the warps that loaded, what it overwrites.
+constexpr int kChainT = 448;
+constexpr uint32_t kColKS = 128, kColQS = 192, kColU = 64, kColO = 128, kColD = 64;
+
+struct ChainBars {
+  uint64_t full[2], empty[2];
+  uint64_t s_ready, ks_done, qs_done, r_ready, u_done, v_ready, o_read, d_done, drain, pair[4];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+};
+struct ChainShared {
+  ChainBars bar;
+  float inv_s[128], inv_r[128];  // 2^-e of the lane's S and R operands, for the output warps
+  float size[3][2][128];         // largest S, R, U of a lane in each half
+};
+constexpr int kChainHeader = 5120;
+static_assert(sizeof(ChainShared) <= kChainHeader, "header");
+
+template <int DK>
+struct ChainStage {
+  static constexpr int kKq = 2 * kC * DK * 2;
+  static constexpr int kV = kC * 128 * 2;
+  static constexpr int kBytes = kKq + 3 * kTile + kV + 1024;
+};
+template <int DK>
+constexpr size_t chain_smem() {
+  return 1024 + kChainHeader + 2 * (size_t)ChainStage<DK>::kBytes;
+}
+
+__device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t *b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long global_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// Bounded wait: gives up when the limit runs out or another role has.
+__device__ __noinline__ bool wait_slow(uint64_t *b, uint32_t parity, ChainBars *bars) {
+  const unsigned long long t0 = global_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try(b, parity)) return true;
+    if ((i & 15u) == 15u) {
+      if (bars->abort_flag) return false;
+      if (global_ns() - t0 > c_delta_wait_ns) {
+        bars->abort_flag = 1;
+        atomicOr(&g_delta_err, 1u);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait1(uint64_t *b, uint32_t parity, ChainBars *bars) {
+  return mbar_try(b, parity) || wait_slow(b, parity, bars);
+}
+// a whole warp; all lanes get one verdict
+__device__ __forceinline__ bool wait_warp(uint64_t *b, uint32_t parity, ChainBars *bars) {
+  if (__all_sync(0xffffffffu, mbar_try(b, parity))) return true;
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = wait_slow(b, parity, bars);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  if (ok) ok = mbar_try(b, parity);  // every lane observes the completed phase
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// 16 bytes, or zeros where !have
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+
+// K-major operand, rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// The same bytes read with the rows as the contraction index: 64 values of N
+// per row, 8-row groups 1024 bytes apart, 64-column boxes of 64 rows one after another.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(kC * 128 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp16 x fp16 -> fp32, M = 128; bit 16: B with its rows along the contraction
+__host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void umma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_ld32(uint32_t t, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// N values of the contraction index, scaled, as N / 2 columns of high and of
+// low halves (16 values at a time: few registers beside the state's)
+template <int N>
+__device__ __forceinline__ void split_store(const float *x, float s, uint32_t hi_col, uint32_t lo_col) {
+#pragma unroll
+  for (int k = 0; k < N; k += 16) {
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split2(x[k + 2 * i] * s, x[k + 2 * i + 1] * s, h[i], l[i]);
+    tm_st8(hi_col + k / 2, h);
+    tm_st8(lo_col + k / 2, l);
+  }
+}
+template <int N>
+__device__ __forceinline__ float absmax(const float *x) {
+  float m0 = 0.f, m1 = 0.f, m2 = 0.f, m3 = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    m0 = fmaxf(m0, fabsf(x[i]));
+    m1 = fmaxf(m1, fabsf(x[i + 1]));
+    m2 = fmaxf(m2, fabsf(x[i + 2]));
+    m3 = fmaxf(m3, fabsf(x[i + 3]));
+  }
+  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+}
+
+template <typename T>
+__device__ __forceinline__ float from16(T x);
+template <>
+__device__ __forceinline__ float from16<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float from16<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T to16(float x);
+template <>
+__device__ __forceinline__ __half to16<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 to16<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+template <typename T, int DK>
+__global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView a, const ChunkPlaces ws) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  using St = ChainStage<DK>;
+  ChainShared &sh = *reinterpret_cast<ChainShared *>(base);
+  ChainBars *bars = &sh.bar;
+  unsigned char *stages = base + kChainHeader;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t b = blockIdx.x / a.HV;
+  const int hv = (int)(blockIdx.x - b * a.HV), hk = hv / (a.HV / a.HK);
+  int64_t t0, t1;
+  a.range(b, t0, t1);
+  const int chunks = (int)((t1 - t0 + kC - 1) / kC);
+  const int64_t place0 = chunk_base(t0, b);
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->full[s], 1 + 32);  // bulk copies, and the producer's lanes for V
+      mbar_init(&bars->empty[s], 1 + 8 + 4);
+    }
+    mbar_init(&bars->s_ready, 8);
+    mbar_init(&bars->ks_done, 1);
+    mbar_init(&bars->qs_done, 1);
+    mbar_init(&bars->r_ready, 8);
+    mbar_init(&bars->u_done, 1);
+    mbar_init(&bars->v_ready, 8);
+    mbar_init(&bars->o_read, 4);
+    mbar_init(&bars->d_done, 1);
+    mbar_init(&bars->drain, 1);
+    for (int p = 0; p < 4; ++p) mbar_init(&bars->pair[p], 2);
+    bars->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 13) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(256)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp < 8) {
+    const int c = tid & 127, half = warp >> 2;  // state column = lane of tensor memory
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const bool mine = c < a.DV;
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    const bool have = slot >= 0 && slot < a.n_slots;
+    constexpr int H = DK / 2, J = kC / 2;  // rows of the state, tokens of a chunk in this half
+    float *state = a.state + ((have ? slot : 0) * a.HV + hv) * (int64_t)DK * a.DV + (int64_t)(half * H) * a.DV + c;
+    float S[H];
+    const bool load = have && mine && !(a.fresh && a.fresh[b]);
+#pragma unroll
+    for (int k = 0; k < H; ++k) S[k] = load ? state[(int64_t)k * a.DV] : 0.f;
+    // the exponent that scales both halves of the lane (a bounded wait, not a
+    // named barrier: the other warp may have given up)
+    uint32_t meet = 0;
+    auto common_exp = [&](float mx, int which, int &e) -> bool {
+      sh.size[which][half][c] = mx;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->pair[warp & 3]);
+      if (!wait_warp(&bars->pair[warp & 3], meet, bars)) return false;
+      meet ^= 1u;
+      e = scale_exp(fmaxf(mx, sh.size[which][half ^ 1][c]));
+      return true;
+    };
+    auto publish = [&](uint64_t *bar) {  // tensor-memory stores of this warp, to the MMAs
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    bool ok = true;
+    for (int n = 0; n < chunks; ++n) {
+      const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
+      const unsigned char *st = stages + s * St::kBytes;
+      const T *V = reinterpret_cast<const T *>(st + St::kKq + 3 * kTile) + (half * J) * a.DV + c;
+      const float *sc = reinterpret_cast<const float *>(st + St::kKq + 3 * kTile + St::kV) + half * J;
+      // 1: the state as the operand of K S and Q S
+      int es, er, eu;
+      if (!(ok = common_exp(absmax<H>(S), 0, es))) break;
+      split_store<H>(S, pow2f(es), tl + half * (H / 2), tl + 64 + half * (H / 2));
+      if (half == 0) sh.inv_s[c] = pow2f(-es);
+      publish(&bars->s_ready);
+      // 2: R
+      if (!(ok = wait_warp(&bars->full[s], sph, bars))) break;
+      if (!(ok = wait_warp(&bars->ks_done, ph, bars))) break;
+      fence_after();
+      float R[J];
+      tm_ld32(tl + kColKS + half * J, R);
+      wait_ld();
+      const float is = -pow2f(-es);
+#pragma unroll
+      for (int j = 0; j < J; j += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(sc + j);
+        const float fa[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) R[j + e] = fmaf(fa[e] * is, R[j + e], mine ? from16<T>(V[(j + e) * a.DV]) : 0.f);
+      }
+      if (!(ok = common_exp(absmax<J>(R), 1, er))) break;
+      if (!(ok = wait_warp(&bars->qs_done, ph, bars))) break;
+      fence_after();
+      split_store<J>(R, pow2f(er), tl + half * (J / 2), tl + 32 + half * (J / 2));
+      if (half == 0) sh.inv_r[c] = pow2f(-er);
+      publish(&bars->r_ready);
+      // 3: the scaled U
+      if (!(ok = wait_warp(&bars->u_done, ph, bars))) break;
+      fence_after();
+      tm_ld32(tl + kColU + half * J, R);
+      wait_ld();
+#pragma unroll
+      for (int j = 0; j < J; j += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(sc + kC + j);
+        R[j] *= f.x;
+        R[j + 1] *= f.y;
+        R[j + 2] *= f.z;
+        R[j + 3] *= f.w;
+      }
+      if (!(ok = common_exp(absmax<J>(R), 2, eu))) break;
+      split_store<J>(R, pow2f(eu), tl + half * (J / 2), tl + 32 + half * (J / 2));
+      publish(&bars->v_ready);
+      // 4: the state
+      const float gc = sc[3 * kC - half * J];
+      const float f = pow2f(-eu) * pow2f(-er);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->empty[s]);  // this warp is done with V and the factors
+      if (!(ok = wait_warp(&bars->d_done, ph, bars))) break;
+      fence_after();
+#pragma unroll
+      for (int k = 0; k < H; k += 32) {
+        float D[32];
+        tm_ld32(tl + kColD + half * H + k, D);
+        wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) S[k + e] = fmaf(gc, S[k + e], f * D[e]);
+      }
+    }
+    if (ok && have && mine) {
+#pragma unroll
+      for (int k = 0; k < H; ++k) state[(int64_t)k * a.DV] = S[k];
+    }
+  } else if (warp < 12) {
+    const int c = tid & 127;
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const bool mine = c < a.DV;
+    T *o = static_cast<T *>(a.o) + (int64_t)hv * a.DV + c;
+    for (int n = 0; n < chunks; ++n) {
+      const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
+      const float *sc = reinterpret_cast<const float *>(stages + s * St::kBytes + St::kKq + 3 * kTile + St::kV);
+      if (!wait_warp(&bars->full[s], sph, bars)) break;
+      if (!wait_warp(&bars->r_ready, ph, bars)) break;
+      if (!wait_warp(&bars->u_done, ph, bars)) break;
+      fence_after();
+      const float is = sh.inv_s[c], ir = sh.inv_r[c] * sc[3 * kC + 1];
+      float x[kC];
+#pragma unroll
+      for (int j = 0; j < kC; j += 32) {
+        float y[32];
+        tm_ld32(tl + kColQS + j, x + j);
+        tm_ld32(tl + kColO + j, y);
+        wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(sc + 2 * kC + j + e);
+          x[j + e] = fmaf(f.x * is, x[j + e], ir * y[e]);
+          x[j + e + 1] = fmaf(f.y * is, x[j + e + 1], ir * y[e + 1]);
+          x[j + e + 2] = fmaf(f.z * is, x[j + e + 2], ir * y[e + 2]);
+          x[j + e + 3] = fmaf(f.w * is, x[j + e + 3], ir * y[e + 3]);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars->o_read);
+        mbar_arrive(&bars->empty[s]);
+      }
+      const int64_t t = t0 + (int64_t)n * kC;
+      const int len = (int)min((int64_t)kC, t1 - t);
+      T *dst = o + t * a.o_stride;
+      if (mine) {
+#pragma unroll
+        for (int j = 0; j < kC; ++j)
+          if (j < len) dst[j * a.o_stride] = to16<T>(x[j]);
+      }
+    }
+  } else {
+    if (warp == 12 && !c_delta_stall) {
+      int n = 0;
+      for (; n < chunks; ++n) {
+        const uint32_t s = n & 1, sph = (n >> 1) & 1;
+        if (!wait_warp(&bars->empty[s], sph ^ 1u, bars)) break;
+        unsigned char *st = stages + s * St::kBytes;
+        const int64_t place = place0 + n;
+        if (lane == 0) {
+          mbar_expect(&bars->full[s], St::kKq + 3 * kTile + kScalarBytes);
+          bulk_load(st, ws.kq + (place * a.HK + hk) * (int64_t)St::kKq, St::kKq, &bars->full[s]);
+          bulk_load(st + St::kKq, ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile), 3 * kTile, &bars->full[s]);
+          bulk_load(st + St::kKq + 3 * kTile + St::kV, ws.sc + (place * a.HV + hv) * kScalars, kScalarBytes, &bars->full[s]);
+        }
+        const int64_t t = t0 + (int64_t)n * kC;
+        const int len = (int)min((int64_t)kC, t1 - t);
+        const T *v = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)hv * a.DV;
+        const uint32_t dst = smem_u32(st + St::kKq + 3 * kTile);
+        const int per = a.DV / 8;  // 16-byte pieces of a row
+        for (int i = lane; i < kC * per; i += 32) {
+          const int r = i / per, p = i - r * per;
+          copy16(dst + (uint32_t)i * 16, v + (r < len ? r : 0) * a.v_stride + p * 8, r < len);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars->full[s])) : "memory");
+      }
+      // no copy is in flight when the CTA ends
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      for (int m = n > 2 ? n - 2 : 0; m < n; ++m) {
+        const unsigned long long w0 = global_ns();
+        while (!mbar_try(&bars->full[m & 1], (m >> 1) & 1) && global_ns() - w0 < c_delta_wait_ns) {
+        }
+      }
+    } else if (warp == 13 && lane == 0) {
+      for (int n = 0; n < chunks; ++n) {
+        const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
+        const uint32_t kt = smem_u32(stages + s * St::kBytes), qt = kt + St::kKq / 2, tp = kt + St::kKq;
+        if (!wait1(&bars->full[s], sph, bars)) break;
+        if (!wait1(&bars->s_ready, ph, bars)) break;
+        fence_after();
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t bt = w ? qt : kt, d = tmem + (w ? kColQS : kColKS);
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k) {
+            const uint64_t bd = desc_k(bt + (k >> 2) * (kC * 128) + (k & 3) * 32);
+            umma(d, tmem + 64 + 8 * k, bd, idesc(64, false), k > 0);  // low
+            umma(d, tmem + 8 * k, bd, idesc(64, false), true);        // high
+          }
+          umma_commit(w ? &bars->qs_done : &bars->ks_done);
+        }
+        if (!wait1(&bars->r_ready, ph, bars)) break;
+        fence_after();
+#pragma unroll
+        for (int k = 0; k < kC / 16; ++k) {
+          const uint64_t bd = desc_k(tp + k * 32), bl = desc_k(tp + 2 * kTile + k * 32);
+          umma(tmem + kColU, tmem + 32 + 8 * k, bd, idesc(128, false), k > 0);  // R low  x [T high ; P']
+          umma(tmem + kColU, tmem + 8 * k, bd, idesc(128, false), true);        // R high x [T high ; P']
+          umma(tmem + kColU, tmem + 8 * k, bl, idesc(64, false), true);         // R high x T low
+        }
+        umma_commit(&bars->u_done);
+        if (!wait1(&bars->v_ready, ph, bars)) break;
+        if (!wait1(&bars->o_read, ph, bars)) break;
+        fence_after();
+#pragma unroll
+        for (int k = 0; k < kC / 16; ++k) {
+          const uint64_t bd = desc_mn(kt + k * 2048);
+          umma(tmem + kColD, tmem + 32 + 8 * k, bd, idesc(DK, true), k > 0);
+          umma(tmem + kColD, tmem + 8 * k, bd, idesc(DK, true), true);
+        }
+        umma_commit(&bars->d_done);
+        umma_commit(&bars->empty[s]);
+      }
+      // every MMA issued, complete before the memory it uses is released
+      umma_commit(&bars->drain);
+      const unsigned long long w0 = global_ns();
+      while (!mbar_try(&bars->drain, 0) && global_ns() - w0 < c_delta_wait_ns) {
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    __syncwarp();
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256));
+  }
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+ChunkPlaces places(const DeltaView &a, void *ws, size_t *total) {
+  const size_t n = (size_t)chunk_places(a.T, a.B);
+  const size_t kq = up256(n * a.HK * (size_t)(2 * kC * a.DK * 2)), tp = up256(n * a.HV * (size_t)(3 * kTile));
+  unsigned char *p = static_cast<unsigned char *>(ws);
+  if (total) *total = kq + tp + up256(n * a.HV * (size_t)kScalarBytes);
+  return ChunkPlaces{p, p + kq, reinterpret_cast<float *>(p + kq + tp)};
+}
+
+template <typename T, int DK>
+cudaError_t chunks_t(const DeltaView &a, void *workspace, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  const int dev = current_device();
+  if (not_done(ready, dev)) {
+    cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)prep_smem<DK>());
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(delta_chain_kernel<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)chain_smem<DK>());
+    if (e != cudaSuccess) return e;
+    mark_done(ready, dev);
+  }
+  const ChunkPlaces ws = places(a, workspace, nullptr);
+  const dim3 grid((unsigned)chunk_places(a.T, a.B), (unsigned)a.HK);
+  delta_prep_kernel<T, DK><<<grid, kPrepT, prep_smem<DK>(), st>>>(a, ws);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  delta_chain_kernel<T, DK><<<(unsigned)(a.B * a.HV), kChainT, chain_smem<DK>(), st>>>(a, ws);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t delta_chunk_workspace_bytes(const DeltaView &a) {
+  size_t n;
+  places(a, nullptr, &n);
+  return n;
+}
+
+cudaError_t launch_delta_chunks(const DeltaView &a, q1_dtype t, void *workspace, cudaStream_t st) {
+  if (t == Q1_BF16) return a.DK == 128 ? chunks_t<__nv_bfloat16, 128>(a, workspace, st) : chunks_t<__nv_bfloat16, 64>(a, workspace, st);
+  return a.DK == 128 ? chunks_t<__half, 128>(a, workspace, st) : chunks_t<__half, 64>(a, workspace, st);
+}
+
+cudaError_t set_delta_diagnostics(unsigned long long wait_ns, int stall) {
+  cudaError_t e = cudaMemcpyToSymbol(c_delta_wait_ns, &wait_ns, sizeof(wait_ns));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(c_delta_stall, &stall, sizeof(stall));
+  return e;
+}
+
+unsigned int read_and_clear_delta_errors(cudaStream_t st, cudaError_t *err) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_delta_err, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbolAsync(g_delta_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess && v) e = cudaStreamSynchronize(st);
+  *err = e;
+  return v;
+}
+
+}  // namespace q1

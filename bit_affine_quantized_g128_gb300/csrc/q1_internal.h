@@ -92,7 +92,8 @@ cudaError_t launch_wide(const WeightView &W, const void *x, int64_t M, void *y, 
 // fixed prefill tiling (token_tile, split), or the automatic choice when invalid
 void set_pair_plan(int token_tile, int split);
 
-// ---- gated delta rule (q1_delta.cu: token by token)
+// ---- gated delta rule (q1_delta.cu: token by token; q1_delta_chunk.cu: in
+// chunks of 64 tokens, bf16 and fp16 only)
 constexpr float kDeltaEps = 1e-6f;  // added to a row's sum of squares before its root
 // The arguments of q1_gated_delta, as the kernels take them.
 struct DeltaView {
@@ -122,6 +123,8 @@ struct DeltaView {
 #endif
 };
 cudaError_t launch_delta_step(const DeltaView &a, q1_dtype t, cudaStream_t st);
+size_t delta_chunk_workspace_bytes(const DeltaView &a);
+cudaError_t launch_delta_chunks(const DeltaView &a, q1_dtype t, void *workspace, cudaStream_t st);
 
 // ---- sampling (q1_sample.cu)
 cudaError_t launch_sample(const q1_sample_args &a, cudaStream_t st);
@@ -131,7 +134,9 @@ cudaError_t launch_sample(const q1_sample_args &a, cudaStream_t st);
 // issue nothing (every wait for their data then runs out)
 cudaError_t set_narrow_diagnostics(unsigned long long wait_ns, int stall);
 cudaError_t set_wide_diagnostics(unsigned long long wait_ns, int stall);
+cudaError_t set_delta_diagnostics(unsigned long long wait_ns, int stall);
 unsigned int read_and_clear_wide_errors(cudaStream_t st, cudaError_t *err);
 unsigned int read_and_clear_narrow_errors(cudaStream_t st, cudaError_t *err);
+unsigned int read_and_clear_delta_errors(cudaStream_t st, cudaError_t *err);
 
 }  // namespace q1

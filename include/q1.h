@@ -372,9 +372,10 @@ q1_status q1_check_symmetric(const q1_weight *W, int32_t *d_is_symmetric, q1_str
 q1_status q1_device_errors(unsigned int *flags, q1_stream stream);
 const char *q1_status_string(q1_status s);
 /* Controls of the bounded waits (no counterpart on the pages; for tests of
- * the timeout path).  Every wait of the narrow and prefill kernels on another
- * role's progress is bounded; one that runs out sets the device error word
- * (bit 0: prefill kernels, bit 1: narrow kernels).  Later waits of the
+ * the timeout path).  Every wait of the narrow, prefill and chunked delta-rule
+ * kernels on another role's progress is bounded; one that runs out sets the
+ * device error word (bit 0: prefill kernels, bit 1: narrow kernels, bit 2:
+ * delta-rule kernels, whose states it leaves unwritten).  Later waits of the
  * prefill kernels then give up at once until q1_device_errors reads the word;
  * those of the narrow kernels each run out on their own limit.
  * q1_set_wait_limit_ns: the bound, in ns of the GPU's global timer (default

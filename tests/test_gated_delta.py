@@ -239,6 +239,33 @@ def test_other_stream_and_graph(q1, L):
     assert torch.equal(o0, o2) and torch.equal(s0, s2)
 
 
+@pytest.mark.gpu
+def test_stalled_copies_time_out_and_recover(q1):
+    # nothing is copied for the chunked form: its waits run out, the call returns,
+    # bit 2 reports it, the states keep their values, and the next call is right
+    q, k, v, g, beta, state, starts = _inputs([100, 70], 2, 4, 128, 128, "bf16", 53)
+    args = [x.cuda() for x in (q, k, v, g, beta)]
+    cu = torch.from_numpy(starts).cuda()
+    want = state.cuda()
+    o = q1.gated_delta(*args, want, cu_seqlens=cu, max_len=100, qk_l2norm=True)
+    assert q1.device_errors() == 0
+    sd = state.cuda()
+    try:
+        q1.set_wait_limit_ns(1_000_000)
+        q1.set_stalled_producers(True)
+        q1.gated_delta(*args, sd, cu_seqlens=cu, max_len=100, qk_l2norm=True)
+        torch.cuda.synchronize()
+        assert q1.device_errors() == 4
+        assert torch.equal(sd.cpu(), state)
+    finally:
+        q1.set_stalled_producers(False)
+        q1.set_wait_limit_ns(0)
+    assert q1.device_errors() == 0
+    again = q1.gated_delta(*args, sd, cu_seqlens=cu, max_len=100, qk_l2norm=True)
+    assert torch.equal(o, again) and torch.equal(sd, want)
+    assert q1.device_errors() == 0
+
+
 # ---- refusals (no GPU needed: validation comes before the library)
 @pytest.fixture
 def fake(monkeypatch):
@@ -304,3 +331,5 @@ def test_c_refusals(q1):
                        (dict(q=p + 2), 3), (dict(k_stride=132), 3), (dict(state=p + 8), 3), (dict(dtype=3), 4)]:
         assert call(**kw) == status, kw
     assert q1.lib().q1_gated_delta(None, None, 0, None) == 1
+    # the chunked form without its workspace, or with too small a one
+    assert call(T=200, max_len=100) == 6
