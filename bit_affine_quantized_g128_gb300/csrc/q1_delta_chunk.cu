@@ -471,48 +471,49 @@ constexpr size_t prep_smem() {
 // All products are in the transposed form, a value column per lane of tensor
 // memory, so that the operand made from registers is the MMA's A operand in
 // tensor memory (M = 128 lanes) and K, Q, T and P' are its B operands as they
-// lie in shared memory:
-//   chain warps 0-7 (a lane = a column c of the state; warps w and w + 4 hold
-//   S[:DK/2, c] and S[DK/2:, c] in registers and take half of the tokens each):
+// lie in shared memory.  Chain warps 0-7 own 16 lanes (state columns) each, in
+// the fragment form of tensor memory loads (16x256b): a thread holds two rows
+// (columns lane/4 and lane/4 + 8 of the warp's 16) and pairs of neighbouring
+// tokens or key entries, which are also the pairs of an fp16 operand word and
+// of the two-wide fp32 instructions.  A row's size, for its scale, is then a
+// matter of four lanes.  Per chunk:
 //     1  S -> high, low                     MMA: KS = S^T K^T, QS = S^T Q^T
-//     2  R = V - a KS -> high, low          MMA: [U | O2] = R^T [T ; P']^T
+//     2  R = V - a KS -> high, low          MMA: U = R^T T^T, O2 = R^T P'^T
 //     3  c U -> high, low                   MMA: D = (c U)^T K
-//     4  S = gamma_C S + D
-//   output warps 8-11: o = b QS + O2
-//   warp 12: copies of the next chunk's tiles, factors and V rows (two stages)
-//   warp 13: tensor memory, and one thread that issues the MMAs
+//     o = b QS + O2 while D is computed; then S = gamma_C S + D
+//   warp 8: copies of the next chunk's tiles, factors and V rows (two stages)
+//   warp 9: tensor memory; issues the MMAs (the whole warp goes through the
+//     issue loop and elect.sync picks the thread: 17 clocks per MMA, against 44
+//     behind an `if (lane == 0)`, whose operands leave the uniform registers)
+//   warp 10: the chunk's rows of o, staged in shared memory, as bulk stores
 // One chunk is a chain of three dependent products; the time is the latency of
 // that chain, not the rate of any unit.
-// Tensor memory (256 columns): S high [0, 64), low [64, 128); KS [128, 192);
-// QS [192, 256).  R and then c U: high [0, 32), low [32, 64).  U [64, 128) and
-// O2 [128, 192); D [64, 192).  Each reuse is behind the barrier of the MMA that
-// read, or the warps that loaded, what it overwrites.
-constexpr int kChainT = 448;
-constexpr uint32_t kColKS = 128, kColQS = 192, kColU = 64, kColO = 128, kColD = 64;
+// Tensor memory columns: S high [0, 64), low [64, 128), and D over both;
+// KS [128, 192); QS [192, 256); R [256, 320); U [320, 384); O2 [384, 448);
+// c U [448, 512).
+constexpr int kChainWarps = 8;
+constexpr int kChainT = 32 * (kChainWarps + 3);
+constexpr uint32_t kColS = 0, kColD = 0, kColKS = 128, kColQS = 192, kColR = 256, kColU = 320, kColO = 384, kColW = 448;
+constexpr int kRow = 128 * 2 + 16;  // bytes of a staged row of V or o: 8 rows at one column fall into different banks
 
 struct ChainBars {
   uint64_t full[2], empty[2];
-  uint64_t s_ready, ks_done, qs_done, r_ready, u_done, v_ready, o_read, d_done, drain, pair[4];
+  uint64_t s_ready, ks_done, r_ready, u_done, o_done, w_ready, d_done, o_ready, o_free, drain;
   uint32_t tmem_base;
   volatile int abort_flag;
 };
-struct ChainShared {
-  ChainBars bar;
-  float inv_s[128], inv_r[128];  // 2^-e of the lane's S and R operands, for the output warps
-  float size[3][2][128];         // largest S, R, U of a lane in each half
-};
-constexpr int kChainHeader = 5120;
-static_assert(sizeof(ChainShared) <= kChainHeader, "header");
+constexpr int kChainHeader = 1024;
+static_assert(sizeof(ChainBars) <= kChainHeader, "header");
 
 template <int DK>
 struct ChainStage {
   static constexpr int kKq = 2 * kC * DK * 2;
-  static constexpr int kV = kC * 128 * 2;
-  static constexpr int kBytes = kKq + 3 * kTile + kV + 1024;
+  static constexpr int kTp = kKq, kV = kTp + 3 * kTile, kSc = kV + kC * kRow;
+  static constexpr int kBytes = (kSc + kScalarBytes + 1023) / 1024 * 1024;
 };
 template <int DK>
 constexpr size_t chain_smem() {
-  return 1024 + kChainHeader + 2 * (size_t)ChainStage<DK>::kBytes;
+  return 1024 + kChainHeader + 2 * (size_t)ChainStage<DK>::kBytes + kC * kRow;
 }
 
 __device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t count) {
@@ -536,42 +537,33 @@ __device__ __forceinline__ unsigned long long global_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
-// Bounded wait: gives up when the limit runs out or another role has.
-__device__ __noinline__ bool wait_slow(uint64_t *b, uint32_t parity, ChainBars *bars) {
-  const unsigned long long t0 = global_ns();
-  for (uint32_t i = 0;; ++i) {
-    if (mbar_try(b, parity)) return true;
-    if ((i & 15u) == 15u) {
-      if (bars->abort_flag) return false;
-      if (global_ns() - t0 > c_delta_wait_ns) {
-        bars->abort_flag = 1;
-        atomicOr(&g_delta_err, 1u);
-        return false;
-      }
-    }
+// Whether a wait gives up: its limit has run out, or another role has given up.
+__device__ __noinline__ bool give_up(ChainBars *bars, unsigned long long since) {
+  if (bars->abort_flag) return true;
+  if (global_ns() - since <= c_delta_wait_ns) return false;
+  bars->abort_flag = 1;
+  atomicOr(&g_delta_err, 1u);
+  return true;
+}
+// Bounded wait of a whole warp; one verdict for all its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *b, uint32_t parity, ChainBars *bars) {
+  bool ok = mbar_try(b, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  const unsigned long long since = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    ok = ok || mbar_try(b, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((i & 31u) == 0 && __any_sync(0xffffffffu, give_up(bars, since))) return false;
   }
 }
-__device__ __forceinline__ bool wait1(uint64_t *b, uint32_t parity, ChainBars *bars) {
-  return mbar_try(b, parity) || wait_slow(b, parity, bars);
-}
-// a whole warp; all lanes get one verdict
-__device__ __forceinline__ bool wait_warp(uint64_t *b, uint32_t parity, ChainBars *bars) {
-  if (__all_sync(0xffffffffu, mbar_try(b, parity))) return true;
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait_slow(b, parity, bars);
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  if (ok) ok = mbar_try(b, parity);  // every lane observes the completed phase
-  return __all_sync(0xffffffffu, ok);
-}
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-// 16 bytes, or zeros where !have
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
 // K-major operand, rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart
@@ -585,9 +577,16 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(kC * 128 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// fp16 x fp16 -> fp32, M = 128; bit 16: B with its rows along the contraction
-__host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+// fp16 x fp16 -> fp32, M = 128; bit 13: A negated (the low parts are stored as
+// their negatives); bit 16: B with its rows along the contraction
+__host__ __device__ constexpr uint32_t idesc(int N, bool neg, bool b_mn = false) {
+  return (1u << 4) | (neg ? 1u << 13 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void umma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
   asm volatile(
@@ -600,131 +599,191 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tm_ld32(uint32_t t, float *v) {
+
+// ---- pairs of fp32 values in one 64-bit register
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pk(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void upk(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of(f2 v) {
+  float a, b;
+  upk(v, a, b);
+  return half2_bits(a, b);
+}
+
+// 64 columns of this warp's 16 lanes: v[2g + h] = row lane/4 + 8h, columns 8g + 2 (lane % 4) and the next
+__device__ __forceinline__ void tm_ld(uint32_t t, f2 (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      "{\n .reg .b32 r<32>;\n"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {r0,r1,r2,r3,r4,r5,r6,r7,r8,r9,r10,r11,r12,r13,r14,r15,"
+      "r16,r17,r18,r19,r20,r21,r22,r23,r24,r25,r26,r27,r28,r29,r30,r31}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      "mov.b64 %0, {r0,r1};\n mov.b64 %1, {r2,r3};\n mov.b64 %2, {r4,r5};\n mov.b64 %3, {r6,r7};\n"
+      "mov.b64 %4, {r8,r9};\n mov.b64 %5, {r10,r11};\n mov.b64 %6, {r12,r13};\n mov.b64 %7, {r14,r15};\n"
+      "mov.b64 %8, {r16,r17};\n mov.b64 %9, {r18,r19};\n mov.b64 %10, {r20,r21};\n mov.b64 %11, {r22,r23};\n"
+      "mov.b64 %12, {r24,r25};\n mov.b64 %13, {r26,r27};\n mov.b64 %14, {r28,r29};\n mov.b64 %15, {r30,r31};\n}\n"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7]), "=l"(v[8]),
+        "=l"(v[9]), "=l"(v[10]), "=l"(v[11]), "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15])
       : "r"(t)
       : "memory");
 }
-__device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+// 16 columns of operand words: w[2g + h] = row lane/4 + 8h, column 4g + lane % 4
+__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&w)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-// N values of the contraction index, scaled, as N / 2 columns of high and of
-// low halves (16 values at a time: few registers beside the state's)
+
+// The larger of a row's absolute values in v[h], v[h + 2], ... over the four lanes that share the row
 template <int N>
-__device__ __forceinline__ void split_store(const float *x, float s, uint32_t hi_col, uint32_t lo_col) {
+__device__ __forceinline__ float row_size(const f2 *v, int h) {
+  float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < N; k += 16) {
+  for (int i = h; i < N; i += 2) {
+    float a, b;
+    upk(v[i], a, b);
+    m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+// v (N pairs of values, two rows) times its rows' scales, as high parts at
+// column hi and the negatives of the low parts at column lo.  Scaled values are
+// below 2^15, so adding and subtracting 1.5 * 2^27 rounds them to multiples of
+// 16: an fp16 high part, and a low part of at most 8.
+template <int N>
+__device__ __forceinline__ void split_store(const f2 *v, const float (&scale)[2], uint32_t hi, uint32_t lo) {
+  const f2 big = pk(201326592.f, 201326592.f), nbig = pk(-201326592.f, -201326592.f);
+  const f2 s[2] = {pk(scale[0], scale[0]), pk(scale[1], scale[1])};
+  const f2 ns[2] = {pk(-scale[0], -scale[0]), pk(-scale[1], -scale[1])};
+#pragma unroll
+  for (int k = 0; k < N; k += 8) {
     uint32_t h[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split2(x[k + 2 * i] * s, x[k + 2 * i + 1] * s, h[i], l[i]);
-    tm_st8(hi_col + k / 2, h);
-    tm_st8(lo_col + k / 2, l);
+    for (int i = 0; i < 8; ++i) {
+      const f2 x = v[k + i];
+      const f2 r = add2(fma2(x, s[i & 1], big), nbig);
+      h[i] = half2_of(r);
+      l[i] = half2_of(fma2(x, ns[i & 1], r));
+    }
+    tm_st(hi + 2 * k, h);
+    tm_st(lo + 2 * k, l);
   }
-}
-template <int N>
-__device__ __forceinline__ float absmax(const float *x) {
-  float m0 = 0.f, m1 = 0.f, m2 = 0.f, m3 = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    m0 = fmaxf(m0, fabsf(x[i]));
-    m1 = fmaxf(m1, fabsf(x[i + 1]));
-    m2 = fmaxf(m2, fabsf(x[i + 2]));
-    m3 = fmaxf(m3, fabsf(x[i + 3]));
-  }
-  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
 }
 
+// two 16-bit values (low half first) as a pair of fp32, and back
 template <typename T>
-__device__ __forceinline__ float from16(T x);
-template <>
-__device__ __forceinline__ float from16<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float from16<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ f2 pair_of(uint32_t w) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return pk(t.x, t.y);
+  } else {
+    return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+}
 template <typename T>
-__device__ __forceinline__ T to16(float x);
-template <>
-__device__ __forceinline__ __half to16<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 to16<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+__device__ __forceinline__ uint32_t word_of(f2 v) {
+  float a, b;
+  upk(v, a, b);
+  if constexpr (std::is_same<T, __half>::value) {
+    return half2_bits(a, b);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+}
+__device__ __forceinline__ f2 lds2(uint32_t addr) {
+  f2 v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView a, const ChunkPlaces ws) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   using St = ChainStage<DK>;
-  ChainShared &sh = *reinterpret_cast<ChainShared *>(base);
-  ChainBars *bars = &sh.bar;
-  unsigned char *stages = base + kChainHeader;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ChainBars *bars = reinterpret_cast<ChainBars *>(base);
+  const uint32_t stages = smem_u32(base) + kChainHeader, o_tile = stages + 2 * St::kBytes;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int64_t b = blockIdx.x / a.HV;
   const int hv = (int)(blockIdx.x - b * a.HV), hk = hv / (a.HV / a.HK);
   int64_t t0, t1;
   a.range(b, t0, t1);
   const int chunks = (int)((t1 - t0 + kC - 1) / kC);
   const int64_t place0 = chunk_base(t0, b);
+  // bf16 outputs keep 8 bits: the low parts of S and R are left out of their
+  // products with Q and P' (2^-12 relative), which they are needed in for fp16
+  constexpr bool kLowInO = std::is_same<T, __half>::value;
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars->full[s], 1 + 32);  // bulk copies, and the producer's lanes for V
-      mbar_init(&bars->empty[s], 1 + 8 + 4);
+      mbar_init(&bars->full[s], 1 + 32);  // bulk copies, and the producer's lanes (their zeros)
+      mbar_init(&bars->empty[s], 1 + kChainWarps);
     }
-    mbar_init(&bars->s_ready, 8);
+    mbar_init(&bars->s_ready, kChainWarps);
     mbar_init(&bars->ks_done, 1);
-    mbar_init(&bars->qs_done, 1);
-    mbar_init(&bars->r_ready, 8);
+    mbar_init(&bars->r_ready, kChainWarps);
     mbar_init(&bars->u_done, 1);
-    mbar_init(&bars->v_ready, 8);
-    mbar_init(&bars->o_read, 4);
+    mbar_init(&bars->o_done, 1);
+    mbar_init(&bars->w_ready, kChainWarps);
     mbar_init(&bars->d_done, 1);
+    mbar_init(&bars->o_ready, kChainWarps);
+    mbar_init(&bars->o_free, 1);
     mbar_init(&bars->drain, 1);
-    for (int p = 0; p < 4; ++p) mbar_init(&bars->pair[p], 2);
     bars->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 13) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(256)
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = bars->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
-  if (warp < 8) {
-    const int c = tid & 127, half = warp >> 2;  // state column = lane of tensor memory
-    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const bool mine = c < a.DV;
+  if (warp < kChainWarps) {
+    const int L0 = 32 * (warp & 3) + 16 * (warp >> 2);  // first of this warp's lanes = state columns
+    const int q = lane & 3, c = L0 + (lane >> 2);       // this thread's columns c and c + 8
+    const uint32_t tl = tmem + ((uint32_t)L0 << 16);
+    const bool mine = L0 < a.DV;
     const int64_t slot = a.slots ? a.slots[b] : b;
     const bool have = slot >= 0 && slot < a.n_slots;
-    constexpr int H = DK / 2, J = kC / 2;  // rows of the state, tokens of a chunk in this half
-    float *state = a.state + ((have ? slot : 0) * a.HV + hv) * (int64_t)DK * a.DV + (int64_t)(half * H) * a.DV + c;
-    float S[H];
+    float *state = a.state + ((have ? slot : 0) * a.HV + hv) * (int64_t)DK * a.DV + (int64_t)(2 * q) * a.DV + c;
+    constexpr int NS = DK / 4;  // pairs of state values per thread: S[2g + h] = key entries 8g + 2q, + 1 of column c + 8h
+    f2 S[NS];
     const bool load = have && mine && !(a.fresh && a.fresh[b]);
 #pragma unroll
-    for (int k = 0; k < H; ++k) S[k] = load ? state[(int64_t)k * a.DV] : 0.f;
-    // the exponent that scales both halves of the lane (a bounded wait, not a
-    // named barrier: the other warp may have given up)
-    uint32_t meet = 0;
-    auto common_exp = [&](float mx, int which, int &e) -> bool {
-      sh.size[which][half][c] = mx;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->pair[warp & 3]);
-      if (!wait_warp(&bars->pair[warp & 3], meet, bars)) return false;
-      meet ^= 1u;
-      e = scale_exp(fmaxf(mx, sh.size[which][half ^ 1][c]));
-      return true;
-    };
+    for (int i = 0; i < NS; ++i) {
+      const float *p = state + (int64_t)(8 * (i >> 1)) * a.DV + 8 * (i & 1);
+      S[i] = load ? pk(p[0], p[a.DV]) : pk(0.f, 0.f);
+    }
     auto publish = [&](uint64_t *bar) {  // tensor-memory stores of this warp, to the MMAs
       wait_st();
       fence_before();
@@ -734,201 +793,237 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
     bool ok = true;
     for (int n = 0; n < chunks; ++n) {
       const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
-      const unsigned char *st = stages + s * St::kBytes;
-      const T *V = reinterpret_cast<const T *>(st + St::kKq + 3 * kTile) + (half * J) * a.DV + c;
-      const float *sc = reinterpret_cast<const float *>(st + St::kKq + 3 * kTile + St::kV) + half * J;
+      const uint32_t st = stages + s * St::kBytes, sc = st + St::kSc + 8 * q;
       // 1: the state as the operand of K S and Q S
-      int es, er, eu;
-      if (!(ok = common_exp(absmax<H>(S), 0, es))) break;
-      split_store<H>(S, pow2f(es), tl + half * (H / 2), tl + 64 + half * (H / 2));
-      if (half == 0) sh.inv_s[c] = pow2f(-es);
+      const int es[2] = {scale_exp(row_size<NS>(S, 0)), scale_exp(row_size<NS>(S, 1))};
+      {
+        const float f[2] = {pow2f(es[0]), pow2f(es[1])};
+        split_store<NS>(S, f, tl + kColS, tl + kColS + 64);
+      }
       publish(&bars->s_ready);
-      // 2: R
+      // 2: R; V's pairs of tokens come transposed from its rows
       if (!(ok = wait_warp(&bars->full[s], sph, bars))) break;
+      uint32_t v[16];
+      f2 fac[8];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (mine)
+          ldsm4t(st + St::kV + (uint32_t)(16 * g + ((lane >> 4) << 3) + (lane & 7)) * kRow + (L0 + (((lane >> 3) & 1) << 3)) * 2, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * g + i] = w[i];
+      }
+#pragma unroll
+      for (int g = 0; g < 8; ++g) fac[g] = lds2(sc + 32 * g);
       if (!(ok = wait_warp(&bars->ks_done, ph, bars))) break;
       fence_after();
-      float R[J];
-      tm_ld32(tl + kColKS + half * J, R);
-      wait_ld();
-      const float is = -pow2f(-es);
+      f2 R[16];
+      tm_ld(tl + kColKS, R);
+      {
+        const f2 ni[2] = {pk(-pow2f(-es[0]), -pow2f(-es[0])), pk(-pow2f(-es[1]), -pow2f(-es[1]))};
 #pragma unroll
-      for (int j = 0; j < J; j += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(sc + j);
-        const float fa[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) R[j + e] = fmaf(fa[e] * is, R[j + e], mine ? from16<T>(V[(j + e) * a.DV]) : 0.f);
+        for (int i = 0; i < 16; ++i) R[i] = fma2(mul2(fac[i >> 1], ni[i & 1]), R[i], pair_of<T>(v[i]));
       }
-      if (!(ok = common_exp(absmax<J>(R), 1, er))) break;
-      if (!(ok = wait_warp(&bars->qs_done, ph, bars))) break;
-      fence_after();
-      split_store<J>(R, pow2f(er), tl + half * (J / 2), tl + 32 + half * (J / 2));
-      if (half == 0) sh.inv_r[c] = pow2f(-er);
+      const int er[2] = {scale_exp(row_size<16>(R, 0)), scale_exp(row_size<16>(R, 1))};
+      {
+        const float f[2] = {pow2f(er[0]), pow2f(er[1])};
+        split_store<16>(R, f, tl + kColR, tl + kColR + 32);
+      }
       publish(&bars->r_ready);
       // 3: the scaled U
+#pragma unroll
+      for (int g = 0; g < 8; ++g) fac[g] = lds2(sc + 4 * kC + 32 * g);
       if (!(ok = wait_warp(&bars->u_done, ph, bars))) break;
       fence_after();
-      tm_ld32(tl + kColU + half * J, R);
-      wait_ld();
+      tm_ld(tl + kColU, R);
 #pragma unroll
-      for (int j = 0; j < J; j += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(sc + kC + j);
-        R[j] *= f.x;
-        R[j + 1] *= f.y;
-        R[j + 2] *= f.z;
-        R[j + 3] *= f.w;
+      for (int i = 0; i < 16; ++i) R[i] = mul2(R[i], fac[i >> 1]);
+      const int eu[2] = {scale_exp(row_size<16>(R, 0)), scale_exp(row_size<16>(R, 1))};
+      {
+        const float f[2] = {pow2f(eu[0]), pow2f(eu[1])};
+        split_store<16>(R, f, tl + kColW, tl + kColW + 32);
       }
-      if (!(ok = common_exp(absmax<J>(R), 2, eu))) break;
-      split_store<J>(R, pow2f(eu), tl + half * (J / 2), tl + 32 + half * (J / 2));
-      publish(&bars->v_ready);
-      // 4: the state
-      const float gc = sc[3 * kC - half * J];
-      const float f = pow2f(-eu) * pow2f(-er);
+      // D overwrites S's operand, which the products with Q read
+      if (!(ok = wait_warp(&bars->o_done, ph, bars))) break;
+      fence_after();
+      publish(&bars->w_ready);
+      // o while D is computed
+      {
+        const float ps = lds1(st + St::kSc + (3 * kC + 1) * 4);
+        f2 O[16];
+        tm_ld(tl + kColQS, R);
+        tm_ld(tl + kColO, O);
+        const float is[2] = {pow2f(-es[0]), pow2f(-es[1])}, ir[2] = {pow2f(-er[0]) * ps, pow2f(-er[1]) * ps};
+        const f2 is2[2] = {pk(is[0], is[0]), pk(is[1], is[1])}, ir2[2] = {pk(ir[0], ir[0]), pk(ir[1], ir[1])};
+        if (n > 0 && !(ok = wait_warp(&bars->o_free, ph ^ 1u, bars))) break;
+#pragma unroll
+        for (int g = 0; g < 8; g += 2) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = 2 * g + i;
+            const f2 fb = lds2(sc + 8 * kC + 32 * (at >> 1));
+            w[i] = word_of<T>(fma2(mul2(fb, is2[i & 1]), R[at], mul2(O[at], ir2[i & 1])));
+          }
+          // four 8 x 8 blocks (tokens 8g and 8g + 8, columns L0 and L0 + 8), transposed into rows of tokens
+          const uint32_t at = o_tile + (uint32_t)(8 * g + ((lane >> 4) << 3) + (lane & 7)) * kRow + (L0 + (((lane >> 3) & 1) << 3)) * 2;
+          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                       "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      const float gc = lds1(st + St::kSc + 3 * kC * 4);
+      const float fd[2] = {pow2f(-eu[0]) * pow2f(-er[0]), pow2f(-eu[1]) * pow2f(-er[1])};
+      fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->empty[s]);  // this warp is done with V and the factors
+      if (lane == 0) {
+        mbar_arrive(&bars->o_ready);
+        mbar_arrive(&bars->empty[s]);  // this warp is done with V and the factors
+      }
+      // the state
       if (!(ok = wait_warp(&bars->d_done, ph, bars))) break;
       fence_after();
+      const f2 gc2 = pk(gc, gc), fd2[2] = {pk(fd[0], fd[0]), pk(fd[1], fd[1])};
 #pragma unroll
-      for (int k = 0; k < H; k += 32) {
-        float D[32];
-        tm_ld32(tl + kColD + half * H + k, D);
-        wait_ld();
+      for (int k = 0; k < NS; k += 16) {
+        f2 D[16];
+        tm_ld(tl + kColD + 4 * k, D);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[k + e] = fmaf(gc, S[k + e], f * D[e]);
+        for (int i = 0; i < 16; ++i) S[k + i] = fma2(gc2, S[k + i], mul2(D[i], fd2[i & 1]));
       }
     }
     if (ok && have && mine) {
 #pragma unroll
-      for (int k = 0; k < H; ++k) state[(int64_t)k * a.DV] = S[k];
-    }
-  } else if (warp < 12) {
-    const int c = tid & 127;
-    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const bool mine = c < a.DV;
-    T *o = static_cast<T *>(a.o) + (int64_t)hv * a.DV + c;
-    for (int n = 0; n < chunks; ++n) {
-      const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
-      const float *sc = reinterpret_cast<const float *>(stages + s * St::kBytes + St::kKq + 3 * kTile + St::kV);
-      if (!wait_warp(&bars->full[s], sph, bars)) break;
-      if (!wait_warp(&bars->r_ready, ph, bars)) break;
-      if (!wait_warp(&bars->u_done, ph, bars)) break;
-      fence_after();
-      const float is = sh.inv_s[c], ir = sh.inv_r[c] * sc[3 * kC + 1];
-      float x[kC];
-#pragma unroll
-      for (int j = 0; j < kC; j += 32) {
-        float y[32];
-        tm_ld32(tl + kColQS + j, x + j);
-        tm_ld32(tl + kColO + j, y);
-        wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(sc + 2 * kC + j + e);
-          x[j + e] = fmaf(f.x * is, x[j + e], ir * y[e]);
-          x[j + e + 1] = fmaf(f.y * is, x[j + e + 1], ir * y[e + 1]);
-          x[j + e + 2] = fmaf(f.z * is, x[j + e + 2], ir * y[e + 2]);
-          x[j + e + 3] = fmaf(f.w * is, x[j + e + 3], ir * y[e + 3]);
-        }
-      }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars->o_read);
-        mbar_arrive(&bars->empty[s]);
-      }
-      const int64_t t = t0 + (int64_t)n * kC;
-      const int len = (int)min((int64_t)kC, t1 - t);
-      T *dst = o + t * a.o_stride;
-      if (mine) {
-#pragma unroll
-        for (int j = 0; j < kC; ++j)
-          if (j < len) dst[j * a.o_stride] = to16<T>(x[j]);
+      for (int i = 0; i < NS; ++i) {
+        float *p = state + (int64_t)(8 * (i >> 1)) * a.DV + 8 * (i & 1);
+        upk(S[i], p[0], p[a.DV]);
       }
     }
-  } else {
-    if (warp == 12 && !c_delta_stall) {
+  } else if (warp == 8) {
+    if (!c_delta_stall) {
+      const uint32_t row_bytes = a.DV * 2;
       int n = 0;
       for (; n < chunks; ++n) {
         const uint32_t s = n & 1, sph = (n >> 1) & 1;
         if (!wait_warp(&bars->empty[s], sph ^ 1u, bars)) break;
-        unsigned char *st = stages + s * St::kBytes;
-        const int64_t place = place0 + n;
-        if (lane == 0) {
-          mbar_expect(&bars->full[s], St::kKq + 3 * kTile + kScalarBytes);
-          bulk_load(st, ws.kq + (place * a.HK + hk) * (int64_t)St::kKq, St::kKq, &bars->full[s]);
-          bulk_load(st + St::kKq, ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile), 3 * kTile, &bars->full[s]);
-          bulk_load(st + St::kKq + 3 * kTile + St::kV, ws.sc + (place * a.HV + hv) * kScalars, kScalarBytes, &bars->full[s]);
-        }
-        const int64_t t = t0 + (int64_t)n * kC;
+        const uint32_t st = stages + s * St::kBytes;
+        const int64_t place = place0 + n, t = t0 + (int64_t)n * kC;
         const int len = (int)min((int64_t)kC, t1 - t);
-        const T *v = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)hv * a.DV;
-        const uint32_t dst = smem_u32(st + St::kKq + 3 * kTile);
-        const int per = a.DV / 8;  // 16-byte pieces of a row
-        for (int i = lane; i < kC * per; i += 32) {
-          const int r = i / per, p = i - r * per;
-          copy16(dst + (uint32_t)i * 16, v + (r < len ? r : 0) * a.v_stride + p * 8, r < len);
+        if (lane == 0) {
+          mbar_expect(&bars->full[s], St::kKq + 3 * kTile + kScalarBytes + len * row_bytes);
+          bulk_load(st, ws.kq + (place * a.HK + hk) * (int64_t)St::kKq, St::kKq, &bars->full[s]);
+          bulk_load(st + St::kTp, ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile), 3 * kTile, &bars->full[s]);
+          bulk_load(st + St::kSc, ws.sc + (place * a.HV + hv) * kScalars, kScalarBytes, &bars->full[s]);
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars->full[s])) : "memory");
+        __syncwarp();
+        const T *v = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)hv * a.DV;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = lane + 32 * i;
+          const uint32_t dst = st + St::kV + r * kRow;
+          if (r < len) {
+            bulk_load(dst, v + r * a.v_stride, row_bytes, &bars->full[s]);
+          } else {  // rows past the sequence's end
+            for (uint32_t x = 0; x < row_bytes; x += 16)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + x), "r"(0) : "memory");
+          }
+        }
+        mbar_arrive(&bars->full[s]);
       }
       // no copy is in flight when the CTA ends
-      asm volatile("cp.async.wait_all;" ::: "memory");
       for (int m = n > 2 ? n - 2 : 0; m < n; ++m) {
-        const unsigned long long w0 = global_ns();
-        while (!mbar_try(&bars->full[m & 1], (m >> 1) & 1) && global_ns() - w0 < c_delta_wait_ns) {
+        const unsigned long long since = global_ns();
+        while (!mbar_try(&bars->full[m & 1], (m >> 1) & 1) && global_ns() - since < c_delta_wait_ns) {
         }
       }
-    } else if (warp == 13 && lane == 0) {
-      for (int n = 0; n < chunks; ++n) {
-        const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
-        const uint32_t kt = smem_u32(stages + s * St::kBytes), qt = kt + St::kKq / 2, tp = kt + St::kKq;
-        if (!wait1(&bars->full[s], sph, bars)) break;
-        if (!wait1(&bars->s_ready, ph, bars)) break;
-        fence_after();
+    }
+  } else if (warp == 9) {
+    for (int n = 0; n < chunks; ++n) {
+      const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
+      const uint32_t kt = stages + s * St::kBytes, qt = kt + St::kKq / 2, tp = kt + St::kTp;
+      if (!wait_warp(&bars->full[s], sph, bars)) break;
+      if (!wait_warp(&bars->s_ready, ph, bars)) break;
+      fence_after();
+      if (elect_one()) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t bt = w ? qt : kt, d = tmem + (w ? kColQS : kColKS);
-#pragma unroll
-          for (int k = 0; k < DK / 16; ++k) {
-            const uint64_t bd = desc_k(bt + (k >> 2) * (kC * 128) + (k & 3) * 32);
-            umma(d, tmem + 64 + 8 * k, bd, idesc(64, false), k > 0);  // low
-            umma(d, tmem + 8 * k, bd, idesc(64, false), true);        // high
-          }
-          umma_commit(w ? &bars->qs_done : &bars->ks_done);
+        for (int k = 0; k < DK / 16; ++k) {
+          const uint64_t bd = desc_k(kt + (k >> 2) * (kC * 128) + (k & 3) * 32);
+          umma(tmem + kColKS, tmem + kColS + 64 + 8 * k, bd, idesc(64, true), k > 0);
+          umma(tmem + kColKS, tmem + kColS + 8 * k, bd, idesc(64, false), true);
         }
-        if (!wait1(&bars->r_ready, ph, bars)) break;
-        fence_after();
+        umma_commit(&bars->ks_done);
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+          const uint64_t bd = desc_k(qt + (k >> 2) * (kC * 128) + (k & 3) * 32);
+          if (kLowInO) umma(tmem + kColQS, tmem + kColS + 64 + 8 * k, bd, idesc(64, true), k > 0);
+          umma(tmem + kColQS, tmem + kColS + 8 * k, bd, idesc(64, false), kLowInO || k > 0);
+        }
+      }
+      __syncwarp();
+      if (!wait_warp(&bars->r_ready, ph, bars)) break;
+      fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k) {
-          const uint64_t bd = desc_k(tp + k * 32), bl = desc_k(tp + 2 * kTile + k * 32);
-          umma(tmem + kColU, tmem + 32 + 8 * k, bd, idesc(128, false), k > 0);  // R low  x [T high ; P']
-          umma(tmem + kColU, tmem + 8 * k, bd, idesc(128, false), true);        // R high x [T high ; P']
-          umma(tmem + kColU, tmem + 8 * k, bl, idesc(64, false), true);         // R high x T low
+          const uint64_t th = desc_k(tp + k * 32), tl = desc_k(tp + 2 * kTile + k * 32);
+          umma(tmem + kColU, tmem + kColR + 32 + 8 * k, th, idesc(64, true), k > 0);
+          umma(tmem + kColU, tmem + kColR + 8 * k, tl, idesc(64, false), true);
+          umma(tmem + kColU, tmem + kColR + 8 * k, th, idesc(64, false), true);
         }
         umma_commit(&bars->u_done);
-        if (!wait1(&bars->v_ready, ph, bars)) break;
-        if (!wait1(&bars->o_read, ph, bars)) break;
-        fence_after();
+#pragma unroll
+        for (int k = 0; k < kC / 16; ++k) {
+          const uint64_t pd = desc_k(tp + kTile + k * 32);
+          if (kLowInO) umma(tmem + kColO, tmem + kColR + 32 + 8 * k, pd, idesc(64, true), k > 0);
+          umma(tmem + kColO, tmem + kColR + 8 * k, pd, idesc(64, false), kLowInO || k > 0);
+        }
+        umma_commit(&bars->o_done);
+      }
+      __syncwarp();
+      if (!wait_warp(&bars->w_ready, ph, bars)) break;
+      fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k) {
           const uint64_t bd = desc_mn(kt + k * 2048);
-          umma(tmem + kColD, tmem + 32 + 8 * k, bd, idesc(DK, true), k > 0);
-          umma(tmem + kColD, tmem + 8 * k, bd, idesc(DK, true), true);
+          umma(tmem + kColD, tmem + kColW + 32 + 8 * k, bd, idesc(DK, true, true), k > 0);
+          umma(tmem + kColD, tmem + kColW + 8 * k, bd, idesc(DK, false, true), true);
         }
         umma_commit(&bars->d_done);
         umma_commit(&bars->empty[s]);
       }
-      // every MMA issued, complete before the memory it uses is released
-      umma_commit(&bars->drain);
-      const unsigned long long w0 = global_ns();
-      while (!mbar_try(&bars->drain, 0) && global_ns() - w0 < c_delta_wait_ns) {
-      }
+      __syncwarp();
     }
+    // every MMA issued, complete before the memory it uses is released
+    if (elect_one()) umma_commit(&bars->drain);
+    __syncwarp();
+    const unsigned long long since = global_ns();
+    while (!mbar_try(&bars->drain, 0) && global_ns() - since < c_delta_wait_ns) {
+    }
+  } else {
+    const uint32_t row_bytes = a.DV * 2;
+    T *o = static_cast<T *>(a.o) + (int64_t)hv * a.DV;
+    for (int n = 0; n < chunks; ++n) {
+      if (!wait_warp(&bars->o_ready, n & 1, bars)) break;
+      const int64_t t = t0 + (int64_t)n * kC;
+      const int len = (int)min((int64_t)kC, t1 - t);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = lane + 32 * i;
+        if (r < len) bulk_store(o + (t + r) * a.o_stride, o_tile + r * kRow, row_bytes);
+      }
+      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->o_free);
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   fence_before();
   __syncthreads();
-  if (warp == 13) {
-    __syncwarp();
+  if (warp == 9) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
 }
 
