@@ -95,49 +95,113 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// ---- pairs of fp32 values in one 64-bit register
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pk(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void upk(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of(f2 v) {
+  float a, b;
+  upk(v, a, b);
+  return half2_bits(a, b);
+}
+
 // ======================================================================
 // Per chunk and key head: the fp16 K and Q tiles, and for each of its value
 // heads T, P' and the per-token factors.  Four warps; warp w owns rows
-// 16w .. 16w+15 of the 64 x 64 products K K^T and Q K^T, which stay in its
-// registers while the value heads are gone through.
+// 16w .. 16w+15 of all 64 x 64 matrices, in the fragment form of mma.sync:
+// K K^T and Q K^T stay in its registers while the value heads are gone
+// through, and A and P are made from them in place.  With D the 16 x 16 blocks
+// on the diagonal of (I + A)^-1 (forward substitution, a lane per column) and
+// Y = D A (all block rows at once),
+//   T_Ic = -sum_{c <= m < I} Y_Im T_mc          block row after block row,
+// which carries diag(beta) and the tile's scale along in T_cc.  All products
+// are mma.sync on fp16 pairs (three products each).
+//
+// Scales are powers of two from bounds, so that nothing is searched for: with
+// g <= 0, beta |k|^2 <= 2, the recurrence contracts and |(I + A)^-1| <= 1, hence
+// |T| <= max beta and |P'| <= max |q| max |k| max beta.  The bounds are put at
+// 2^9, which leaves 2^6 for what they do not cover; positive g raise them by
+// their sum.
 constexpr int kPrepT = 128;
-constexpr int kLd = 68;  // row length of the fp32 matrices (keeps 16-byte rows)
 
 struct PrepShared {
-  float A[kC * kLd];   // A, unit lower triangle left out
-  float Ti[kC * kLd];  // (I + A)^-1
-  float W[16 * 52];    // a block row of A (I + A)^-1
+  float D[4][16][20];          // per warp: the diagonal block of A, then its inverse
   float rk[kC], rq[kC];        // factors of the fp16 rows: norm, scale and 2^-e
   float Gh[kC], Gl[kC];        // log2(e) G = Gh + Gl
   float beta[kC];
-  float g[kC];
-  float red[8];
+  float size[2][4];            // largest key and query norms of each warp's rows
+  int te, bump;                // T's scale; what positive g add to the bounds' exponents
 };
 
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 &v, f2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
+    if constexpr (std::is_same<T, __half>::value) {
       const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
+      f[i] = pk(t.x, t.y);
     } else {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      f[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
   }
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// the 8 x 8 matrix of 16-bit values that the warp holds, transposed
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// d += (ah + al)(bh + bl) without the product of the low parts
+__device__ __forceinline__ void mma3(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], uint32_t bh0, uint32_t bh1,
+                                     uint32_t bl0, uint32_t bl1) {
+  mma16(d, al, bh0, bh1);
+  mma16(d, ah, bl0, bl1);
+  mma16(d, ah, bh0, bh1);
+}
+// a 16 x 16 block of fragments as the pair operand of the next product
+__device__ __forceinline__ void pair_operand(const f2 (&c)[2][2], uint32_t (&h)[4], uint32_t (&l)[4]) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x, y;
+      upk(c[n][e], x, y);
+      split2(x, y, h[2 * n + e], l[2 * n + e]);
+    }
 }
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  constexpr int kKq = kC * DK * 2;                          // bytes of a K or Q tile
+  constexpr int kKq = kC * DK * 2;  // bytes of a K or Q tile
   constexpr int kArea = 2 * kKq > 3 * kTile ? 2 * kKq : 3 * kTile;
-  unsigned char *kt = base, *qt = base + kKq;               // K, Q tiles; later T high, P', T low
-  PrepShared &sh = *reinterpret_cast<PrepShared *>(base + kArea);
+  __shared__ __align__(128) unsigned char area[kArea];  // K, Q tiles; later T high, P', T low
+  __shared__ PrepShared sh;
+  unsigned char *kt = area, *qt = area + kKq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t place = blockIdx.x;
   const int hk = blockIdx.y;
@@ -155,315 +219,316 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
   if (nth < 0 || t0 >= t1) return;
   const int len = (int)min((int64_t)kC, t1 - t0);
 
-  // ---- K and Q rows -> fp16 tiles, scaled to the row's size; DK/8 lanes per row
+  // ---- K and Q rows -> fp16 tiles; DK/8 lanes per row.  A row's scale brings
+  // its norm, and so every value, below 2^15
   constexpr int LPR = DK / 8, RPI = kPrepT / LPR, NI = kC / RPI;
   const int piece = tid % LPR;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    const T *src = static_cast<const T *>(which ? a.q : a.k) + t0 * (which ? a.q_stride : a.k_stride) + (int64_t)hk * DK + piece * 8;
     const int64_t stride = which ? a.q_stride : a.k_stride;
+    const T *src = static_cast<const T *>(which ? a.q : a.k) + (t0 + tid / LPR) * stride + (int64_t)hk * DK + piece * 8;
     uint4 v[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int r = tid / LPR + i * RPI;
-      v[i] = r < len ? __ldg(reinterpret_cast<const uint4 *>(src + r * stride)) : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < NI; ++i)
+      v[i] = tid / LPR + i * RPI < len ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(i * RPI) * stride)) : make_uint4(0, 0, 0, 0);
     unsigned char *tile = which ? qt : kt;
     unsigned char *out = ws.kq + ((place * a.HK + hk) * 2 + which) * (int64_t)kKq;
+    float big = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = tid / LPR + i * RPI;
-      float f[8], ss = 0.f, mx = 0.f;
+      f2 f[4], s2 = pk(0.f, 0.f);
       unpack8<T>(v[i], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(f[e], f[e], ss);
-        mx = fmaxf(mx, fabsf(f[e]));
-      }
+      for (int e = 0; e < 4; ++e) s2 = fma2(f[e], f[e], s2);
+      float ss, sy;
+      upk(s2, ss, sy);
+      ss += sy;
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      }
-      const int e = scale_exp(mx);
-      const float s = pow2f(e);
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float norm = sqrtf(ss);
+      const int e = scale_exp(norm);
+      const f2 sc = pk(pow2f(e), pow2f(e));
       uint4 h;
-      h.x = half2_bits(f[0] * s, f[1] * s);
-      h.y = half2_bits(f[2] * s, f[3] * s);
-      h.z = half2_bits(f[4] * s, f[5] * s);
-      h.w = half2_bits(f[6] * s, f[7] * s);
+      h.x = half2_of(mul2(f[0], sc));
+      h.y = half2_of(mul2(f[1], sc));
+      h.z = half2_of(mul2(f[2], sc));
+      h.w = half2_of(mul2(f[3], sc));
       const uint32_t at = (uint32_t)(piece >> 3) * (kC * 128) + swz(r, piece & 7);
       *reinterpret_cast<uint4 *>(tile + at) = h;
       *reinterpret_cast<uint4 *>(out + at) = h;
       if (piece == 0) {
-        const float n = (a.l2norm ? 1.f / sqrtf(ss + kDeltaEps) : 1.f) * pow2f(-e);
-        if (which) sh.rq[r] = n * a.scale;
-        else sh.rk[r] = n;
+        const float n = (a.l2norm ? 1.f / sqrtf(ss + kDeltaEps) : 1.f) * (which ? a.scale : 1.f);
+        (which ? sh.rq : sh.rk)[r] = n * pow2f(-e);
+        big = fmaxf(big, fabsf(n) * norm);
       }
     }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
+    if (LPR == 8) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
+    if (lane == 0) sh.size[which][warp] = big;
   }
   __syncthreads();
 
   // ---- K K^T and Q K^T, columns up to this warp's rows
   float kk[4][2][4] = {}, qk[4][2][4] = {};
+  const uint32_t kt32 = smem_u32(kt), qt32 = smem_u32(qt);
 #pragma unroll
   for (int s = 0; s < DK / 16; ++s) {
     const uint32_t box = (uint32_t)(s >> 2) * (kC * 128);
     const int p0 = (s & 3) * 2;
     uint32_t ak[4], aq[4];
     const int ar = 16 * warp + (lane & 15);
-    ldsm4(smem_u32(kt + box) + swz(ar, p0 + (lane >> 4)), ak);
-    ldsm4(smem_u32(qt + box) + swz(ar, p0 + (lane >> 4)), aq);
+    ldsm4(kt32 + box + swz(ar, p0 + (lane >> 4)), ak);
+    ldsm4(qt32 + box + swz(ar, p0 + (lane >> 4)), aq);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j <= warp) {
         uint32_t b[4];
-        ldsm4(smem_u32(kt + box) + swz(16 * j + (lane & 7) + ((lane >> 4) << 3), p0 + ((lane >> 3) & 1)), b);
+        ldsm4(kt32 + box + swz(16 * j + (lane & 7) + ((lane >> 4) << 3), p0 + ((lane >> 3) & 1)), b);
         mma16(kk[j][0], ak, b[0], b[1]);
         mma16(kk[j][1], ak, b[2], b[3]);
         mma16(qk[j][0], aq, b[0], b[1]);
         mma16(qk[j][1], aq, b[2], b[3]);
       }
   }
+  const float kn = fmaxf(fmaxf(sh.size[0][0], sh.size[0][1]), fmaxf(sh.size[0][2], sh.size[0][3]));
+  const float qn = fmaxf(fmaxf(sh.size[1][0], sh.size[1][1]), fmaxf(sh.size[1][2], sh.size[1][3]));
+  const int pe0 = scale_exp(kn * qn) - 6;  // 2^pe0 kn qn in [2^8, 2^9)
   __syncthreads();  // the tiles' area is free
-  unsigned char *th = base, *pt = base + kTile, *tl = base + 2 * kTile;
+  const uint32_t th = smem_u32(area), pt = th + kTile, tl = th + 2 * kTile;
+  // the blocks above the diagonal stay zero
+  for (int i = tid; i < 3 * kTile / 16; i += kPrepT) reinterpret_cast<uint4 *>(area)[i] = make_uint4(0, 0, 0, 0);
 
   const int group = a.HV / a.HK;
-  const int r0 = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);  // fragment rows r0, r0 + 8; columns 8n + c0, + 1
+  const int fr = lane >> 2, fc = 2 * (lane & 3);  // fragment rows fr, fr + 8 of the block; columns 8n + fc, + 1
+  // a fragment word (row, columns 8 piece + fc, + 1) of a tile
+  auto word_at = [&](uint32_t tile, int row, int pc) { return tile + swz(row, pc) + (uint32_t)fc * 2; };
+  auto put = [](uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); };
   for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
-    // ---- gates
-    if (tid < kC) {
-      float g = 0.f, be = 0.f;
-      if (tid < len) {
-        g = a.g[(t0 + tid) * a.g_stride + hv];
-        be = a.beta[(t0 + tid) * a.beta_stride + hv];
-        // exp(-200) is 0 in fp32 already; the limit keeps sums of g finite
-        g = g < -200.f ? -200.f : g;
-      }
-      sh.g[tid] = g;
-      sh.beta[tid] = be;
-    }
-    __syncthreads();
+    float *sc = ws.sc + (place * a.HV + hv) * kScalars;
+    // ---- gates: two tokens per lane of warp 0.  G in fixed point (2^-40):
+    // exact sums, whose differences are taken later
     if (warp == 0) {
-      // G in float64: differences of sums that may be large are taken later
-      const double x = sh.g[2 * lane], y = sh.g[2 * lane + 1];
-      double s = x + y;
+      float be[2], gv[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = 2 * lane + x;
+        gv[x] = t < len ? a.g[(t0 + t) * a.g_stride + hv] : 0.f;
+        be[x] = t < len ? a.beta[(t0 + t) * a.beta_stride + hv] : 0.f;
+      }
+      const uint32_t nan0 = __ballot_sync(0xffffffffu, gv[0] != gv[0]), nan1 = __ballot_sync(0xffffffffu, gv[1] != gv[1]);
+      float up = 0.f;
+      long long gi[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        // exp(-200) is 0 in fp32 already
+        const float l = fminf(fmaxf(gv[x], -200.f), 200.f) * 1.44269504f;
+        up += fmaxf(l, 0.f);
+        gi[x] = __float2ll_rn(l * 1099511627776.f);
+      }
+      long long sum = gi[0] + gi[1];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double z = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += z;
+        const long long z = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += z;
       }
-      const double l2e = 1.4426950408889634;
-      const double g1 = s * l2e, g0 = (s - y) * l2e;
-      sh.Gh[2 * lane] = (float)g0;
-      sh.Gl[2 * lane] = (float)(g0 - (double)(float)g0);
-      sh.Gh[2 * lane + 1] = (float)g1;
-      sh.Gl[2 * lane + 1] = (float)(g1 - (double)(float)g1);
+      float bmax = fmaxf(fabsf(be[0]), fabsf(be[1]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        up += __shfl_xor_sync(0xffffffffu, up, o);
+        bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, o));
+      }
+      const int bump = (int)ceilf(fminf(up, 20.f));
+      const int te = scale_exp(bmax) - 6 - bump;
+      const long long all = __shfl_sync(0xffffffffu, sum, 31);
+      const long long G[2] = {sum - gi[1], sum};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = 2 * lane + x;
+        // tokens from the first NaN on
+        const bool bad = (nan0 & ((2u << lane) - 1u)) || (nan1 & (x ? (2u << lane) - 1u : (1u << lane) - 1u));
+        float gh = (float)G[x];
+        const float gl = (float)(G[x] - (long long)gh) * 9.094947017729282e-13f;
+        gh *= 9.094947017729282e-13f;
+        if (bad) gh = __int_as_float(0x7fc00000);
+        sh.Gh[t] = gh;
+        sh.Gl[t] = gl;
+        sh.beta[t] = be[x];
+        const float gam = ex2(gh + gl);
+        const float tail = ex2((float)(all - G[x]) * 9.094947017729282e-13f);
+        sc[t] = gam * sh.rk[t];
+        sc[kC + t] = ((nan0 | nan1) ? __int_as_float(0x7fc00000) : tail) * sh.rk[t] * pow2f(-te);
+        sc[2 * kC + t] = gam * sh.rq[t];
+        if (t == kC - 1) {
+          sc[3 * kC] = gam;
+          sc[3 * kC + 1] = pow2f(-(pe0 - bump)) * pow2f(-te) * 512.f;
+        }
+      }
+      if (lane == 0) {
+        sh.te = te;
+        sh.bump = bump;
+      }
     }
     __syncthreads();
-    // ---- A into shared memory; P into registers (kept as the next product's operand)
-    float p[4][2][4];
-    float pmax = 0.f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = r0 + 8 * e;
-      const float gh = sh.Gh[i], gl = sh.Gl[i], ba = sh.beta[i] * sh.rk[i], rq = sh.rq[i];
+    const float ts = pow2f(sh.te), ps = pow2f(pe0 - sh.bump);
+    // ---- A and P in place of the products' fragments
+    f2 A[4][2][2], P[4][2][2];
+    {
+      const int i0 = 16 * warp + fr;
+      const f2 gh[2] = {pk(sh.Gh[i0], sh.Gh[i0]), pk(sh.Gh[i0 + 8], sh.Gh[i0 + 8])};
+      const f2 gl[2] = {pk(sh.Gl[i0], sh.Gl[i0]), pk(sh.Gl[i0 + 8], sh.Gl[i0 + 8])};
+      const float b0 = sh.beta[i0] * sh.rk[i0], b1 = sh.beta[i0 + 8] * sh.rk[i0 + 8];
+      const float q0 = sh.rq[i0] * ps, q1 = sh.rq[i0 + 8] * ps;
+      const f2 ba[2] = {pk(b0, b0), pk(b1, b1)}, rq[2] = {pk(q0, q0), pk(q1, q1)}, neg = pk(-1.f, -1.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
+        if (j <= warp) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float av[2] = {0.f, 0.f}, pv[2] = {0.f, 0.f};
-          const int c = 16 * j + 8 * n + c0;
-          if (j <= warp) {
+          for (int n = 0; n < 2; ++n) {
+            const int c = 16 * j + 8 * n + fc;
+            const f2 ch = *reinterpret_cast<const f2 *>(&sh.Gh[c]), cl = *reinterpret_cast<const f2 *>(&sh.Gl[c]);
+            const f2 rk = *reinterpret_cast<const f2 *>(&sh.rk[c]);
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-              if (c + x <= i) {
-                const float w = exp2f((gh - sh.Gh[c + x]) + (gl - sh.Gl[c + x])) * sh.rk[c + x];
-                pv[x] = w * rq * qk[j][n][2 * e + x];
-                if (c + x < i) av[x] = w * ba * kk[j][n][2 * e + x];
+            for (int e = 0; e < 2; ++e) {
+              float x, y;
+              upk(add2(fma2(ch, neg, gh[e]), fma2(cl, neg, gl[e])), x, y);
+              const f2 w = mul2(pk(ex2(x), ex2(y)), rk);
+              f2 av = mul2(mul2(w, ba[e]), pk(kk[j][n][2 * e], kk[j][n][2 * e + 1]));
+              f2 pv = mul2(mul2(w, rq[e]), pk(qk[j][n][2 * e], qk[j][n][2 * e + 1]));
+              if (j == warp) {  // the block on the diagonal
+                const int i = fr + 8 * e, cc = 8 * n + fc;
+                float u0, u1, v0, v1;
+                upk(av, u0, u1);
+                upk(pv, v0, v1);
+                av = pk(cc < i ? u0 : 0.f, cc + 1 < i ? u1 : 0.f);
+                pv = pk(cc <= i ? v0 : 0.f, cc + 1 <= i ? v1 : 0.f);
+                *reinterpret_cast<f2 *>(&sh.D[warp][i][cc]) = av;
               }
-            *reinterpret_cast<float2 *>(&sh.A[i * kLd + c]) = make_float2(av[0], av[1]);
-          }
-          p[j][n][2 * e] = pv[0];
-          p[j][n][2 * e + 1] = pv[1];
-          pmax = fmaxf(pmax, fmaxf(fabsf(pv[0]), fabsf(pv[1])));
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) pmax = fmaxf(pmax, __shfl_xor_sync(0xffffffffu, pmax, o));
-    const int pe = scale_exp(pmax);
-    __syncthreads();
-    // ---- (I + A)^-1 by forward substitution: the four diagonal blocks of 16
-    // (a thread per column), then block row by block row
-    if (tid < kC) {
-      const int b16 = tid & ~15, j = tid & 15;
-      float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float s = i == j ? 1.f : 0.f;
-        const float *row = &sh.A[(b16 + i) * kLd + b16];
-#pragma unroll
-        for (int m4 = 0; m4 < 16; m4 += 4)
-          if (m4 < i) {
-            const float4 av = *reinterpret_cast<const float4 *>(row + m4);
-            s = fmaf(-av.x, x[m4], s);
-            if (m4 + 1 < i) s = fmaf(-av.y, x[m4 + 1], s);
-            if (m4 + 2 < i) s = fmaf(-av.z, x[m4 + 2], s);
-            if (m4 + 3 < i) s = fmaf(-av.w, x[m4 + 3], s);
-          }
-        x[i] = s;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sh.Ti[(b16 + i) * kLd + b16 + j] = x[i];
-    } else {
-      // blocks above the diagonal
-      const int t = tid - kC;
-      for (int at = t; at < kC * 16; at += kC) {
-        const int row = at >> 4, col = (at & 15) * 4;
-        if ((col >> 4) > (row >> 4)) *reinterpret_cast<float4 *>(&sh.Ti[row * kLd + col]) = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int I = 1; I < 4; ++I) {
-      const int r = tid >> 3, cc = tid & 7;
-      float acc[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int m = 0; m < 16 * I; m += 4) {
-        const float4 av = *reinterpret_cast<const float4 *>(&sh.A[(16 * I + r) * kLd + m]);
-        const float x[4] = {av.x, av.y, av.z, av.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int n = 0; n < 2 * I; ++n) acc[n] = fmaf(x[q], sh.Ti[(m + q) * kLd + cc + 8 * n], acc[n]);
-      }
-#pragma unroll
-      for (int n = 0; n < 2 * I; ++n) sh.W[r * 52 + cc + 8 * n] = acc[n];
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < 6; ++n) acc[n] = 0.f;
-#pragma unroll
-      for (int m = 0; m < 16; m += 4) {
-        const float4 tv = *reinterpret_cast<const float4 *>(&sh.Ti[(16 * I + r) * kLd + 16 * I + m]);
-        const float x[4] = {tv.x, tv.y, tv.z, tv.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int n = 0; n < 2 * I; ++n) acc[n] = fmaf(-x[q], sh.W[(m + q) * 52 + cc + 8 * n], acc[n]);
-      }
-#pragma unroll
-      for (int n = 0; n < 2 * I; ++n) sh.Ti[(16 * I + r) * kLd + cc + 8 * n] = acc[n];
-      __syncthreads();
-    }
-    // ---- T = (I + A)^-1 diag(beta) as fp16 pairs
-    float tv[32], tmax = 0.f;
-    const int tr = tid >> 1, tc = (tid & 1) * 32;  // half a row per thread
-#pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(&sh.Ti[tr * kLd + tc + c]);
-      const float4 be = *reinterpret_cast<const float4 *>(&sh.beta[tc + c]);
-      tv[c] = x.x * be.x;
-      tv[c + 1] = x.y * be.y;
-      tv[c + 2] = x.z * be.z;
-      tv[c + 3] = x.w * be.w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tmax = fmaxf(tmax, fabsf(tv[c + e]));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, o));
-    if (lane == 0) sh.red[warp] = tmax;
-    __syncthreads();
-    tmax = fmaxf(fmaxf(sh.red[0], sh.red[1]), fmaxf(sh.red[2], sh.red[3]));
-    const int te = scale_exp(tmax);
-    const float ts = pow2f(te);
-#pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-      uint4 h, l;
-      split2(tv[c] * ts, tv[c + 1] * ts, h.x, l.x);
-      split2(tv[c + 2] * ts, tv[c + 3] * ts, h.y, l.y);
-      split2(tv[c + 4] * ts, tv[c + 5] * ts, h.z, l.z);
-      split2(tv[c + 6] * ts, tv[c + 7] * ts, h.w, l.w);
-      const uint32_t at = swz(tr, (tc + c) >> 3);
-      *reinterpret_cast<uint4 *>(th + at) = h;
-      *reinterpret_cast<uint4 *>(tl + at) = l;
-    }
-    __syncthreads();
-    // ---- P' = P T, both as fp16 pairs (three products)
-    float pp[4][2][4] = {};
-    const float ps = pow2f(pe);
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-      if (s <= warp) {
-        uint32_t ph[4], pl[4];
-        split2(p[s][0][0] * ps, p[s][0][1] * ps, ph[0], pl[0]);
-        split2(p[s][0][2] * ps, p[s][0][3] * ps, ph[1], pl[1]);
-        split2(p[s][1][0] * ps, p[s][1][1] * ps, ph[2], pl[2]);
-        split2(p[s][1][2] * ps, p[s][1][3] * ps, ph[3], pl[3]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j <= s) {
-            uint32_t bh[4], bl[4];
-            const uint32_t at = swz(16 * s + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * j + (lane >> 4));
-            ldsm4t(smem_u32(th) + at, bh);
-            ldsm4t(smem_u32(tl) + at, bl);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              mma16(pp[j][n], pl, bh[2 * n], bh[2 * n + 1]);
-              mma16(pp[j][n], ph, bl[2 * n], bl[2 * n + 1]);
-              mma16(pp[j][n], ph, bh[2 * n], bh[2 * n + 1]);
+              A[j][n][e] = av;
+              P[j][n][e] = pv;
             }
           }
-      }
-    const float un = pow2f(-pe) * pow2f(-te);
-    float qmax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pp[j][n][e] *= un;
-          qmax = fmaxf(qmax, fabsf(pp[j][n][e]));
         }
+    }
+    __syncwarp();
+    // ---- the diagonal block's inverse: lane c (and c + 16, the same) solves for column c
+    {
+      float x[16];
+      const int c = lane & 15;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, o));
-    if (lane == 0) sh.red[4 + warp] = qmax;
-    __syncthreads();
-    qmax = fmaxf(fmaxf(sh.red[4], sh.red[5]), fmaxf(sh.red[6], sh.red[7]));
-    const int qe = scale_exp(qmax);
-    const float qs = pow2f(qe);
+      for (int i = 0; i < 16; ++i) {
+        float s0 = i == c ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+        for (int m = 0; m < i; m += 4) {
+          const float4 av = *reinterpret_cast<const float4 *>(&sh.D[warp][i][m]);
+          s0 = fmaf(-av.x, x[m], s0);
+          if (m + 1 < i) s1 = fmaf(-av.y, x[m + 1], s1);
+          if (m + 2 < i) s0 = fmaf(-av.z, x[m + 2], s0);
+          if (m + 3 < i) s1 = fmaf(-av.w, x[m + 3], s1);
+        }
+        x[i] = s0 + s1;
+      }
+      __syncwarp();
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int i = 0; i < 16; ++i)
+        if ((i >> 3) == (lane >> 4)) sh.D[warp][i][c] = x[i];
+      __syncwarp();
+    }
+    // its fragments: T's block (with beta and the scale), and the operand of Y
+    uint32_t dh[4], dl[4];
+    {
+      f2 d[2][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<uint32_t *>(pt + swz(r0 + 8 * e, 2 * j + n) + c0 * 2) =
-              half2_bits(pp[j][n][2 * e] * qs, pp[j][n][2 * e + 1] * qs);
-    // ---- factors per token
-    float *sc = ws.sc + (place * a.HV + hv) * kScalars;
-    if (tid < kC) {
-      const float gam = exp2f(sh.Gh[tid] + sh.Gl[tid]);
-      const float tail = exp2f((sh.Gh[kC - 1] - sh.Gh[tid]) + (sh.Gl[kC - 1] - sh.Gl[tid]));
-      sc[tid] = gam * sh.rk[tid];
-      sc[kC + tid] = tail * sh.rk[tid] * pow2f(-te);
-      sc[2 * kC + tid] = gam * sh.rq[tid];
-      if (tid == kC - 1) {
-        sc[3 * kC] = gam;
-        sc[3 * kC + 1] = pow2f(-qe);
+      for (int n = 0; n < 2; ++n) {
+        const f2 be = mul2(*reinterpret_cast<const f2 *>(&sh.beta[16 * warp + 8 * n + fc]), pk(ts, ts));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          d[n][e] = *reinterpret_cast<const f2 *>(&sh.D[warp][fr + 8 * e][8 * n + fc]);
+          float x, y;
+          uint32_t h, l;
+          upk(mul2(d[n][e], be), x, y);
+          split2(x, y, h, l);
+          const int row = 16 * warp + fr + 8 * e, pc = 2 * warp + n;
+          put(word_at(th, row, pc), h);
+          put(word_at(tl, row, pc), l);
+        }
+      }
+      pair_operand(d, dh, dl);
+    }
+    // ---- Y = D A, the blocks left of the diagonal (kept as pairs)
+    uint32_t yh[3][4], yl[3][4];
+#pragma unroll
+    for (int m = 0; m < 3; ++m)
+      if (m < warp) {
+        uint32_t ah[4], al[4];
+        pair_operand(A[m], ah, al);
+        f2 y[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float d[4] = {};
+          mma3(d, dh, dl, movmatrix(ah[2 * n]), movmatrix(ah[2 * n + 1]), movmatrix(al[2 * n]), movmatrix(al[2 * n + 1]));
+          y[n][0] = pk(-d[0], -d[1]);
+          y[n][1] = pk(-d[2], -d[3]);
+        }
+        pair_operand(y, yh[m], yl[m]);
+      }
+    // the operand pair of block (m, c) of T, as rows along the contraction
+    auto t_block = [&](int m, int c, uint32_t (&bh)[4], uint32_t (&bl)[4]) {
+      const uint32_t at = swz(16 * m + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * c + (lane >> 4));
+      ldsm4t(th + at, bh);
+      ldsm4t(tl + at, bl);
+    };
+    // ---- T, block row after block row; P' gathers as the rows come
+    float tv[3][2][4] = {}, pp[4][2][4] = {};
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      __syncthreads();  // block row m is complete
+      uint32_t ph[4], pl[4];
+      if (m <= warp) pair_operand(P[m], ph, pl);
+#pragma unroll
+      for (int c = 0; c <= m; ++c)
+        if (m <= warp) {
+          uint32_t bh[4], bl[4];
+          t_block(m, c, bh, bl);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (m < 3 && m < warp) mma3(tv[c < 3 ? c : 0][n], yh[m < 3 ? m : 0], yl[m < 3 ? m : 0], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
+            mma3(pp[c][n], ph, pl, bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
+          }
+        }
+      if (m + 1 == warp) {  // this warp's block row is next
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          if (c <= m) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint32_t h, l;
+                split2(tv[c][n][2 * e], tv[c][n][2 * e + 1], h, l);
+                const int row = 16 * warp + fr + 8 * e, pc = 2 * c + n;
+                put(word_at(th, row, pc), h);
+                put(word_at(tl, row, pc), l);
+              }
+          }
       }
     }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c <= warp) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            put(word_at(pt, 16 * warp + fr + 8 * e, 2 * c + n),
+                half2_bits(pp[c][n][2 * e] * (1.f / 512.f), pp[c][n][2 * e + 1] * (1.f / 512.f)));
+      }
     __syncthreads();
     uint4 *dst = reinterpret_cast<uint4 *>(ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile));
 #pragma unroll
-    for (int i = tid; i < 3 * kTile / 16; i += kPrepT) dst[i] = reinterpret_cast<const uint4 *>(base)[i];
+    for (int i = 0; i < 3 * kTile / 16 / kPrepT; ++i) dst[tid + i * kPrepT] = reinterpret_cast<const uint4 *>(area)[tid + i * kPrepT];
     __syncthreads();
   }
-}
-
-template <int DK>
-constexpr size_t prep_smem() {
-  return 1024 + (2 * kC * DK * 2 > 3 * kTile ? 2 * kC * DK * 2 : 3 * kTile) + sizeof(PrepShared);
 }
 
 // ======================================================================
@@ -485,7 +550,7 @@ constexpr size_t prep_smem() {
 //   warp 9: tensor memory; issues the MMAs (the whole warp goes through the
 //     issue loop and elect.sync picks the thread: 17 clocks per MMA, against 44
 //     behind an `if (lane == 0)`, whose operands leave the uniform registers)
-//   warp 10: the chunk's rows of o, staged in shared memory, as bulk stores
+//   warp 10: the chunk's rows of o from shared memory, where the chain stages them
 // One chunk is a chain of three dependent products; the time is the latency of
 // that chain, not the rate of any unit.
 // Tensor memory columns: S high [0, 64), low [64, 128), and D over both;
@@ -498,7 +563,9 @@ constexpr int kRow = 128 * 2 + 16;  // bytes of a staged row of V or o: 8 rows a
 
 struct ChainBars {
   uint64_t full[2], empty[2];
-  uint64_t s_ready, ks_done, r_ready, u_done, o_done, w_ready, d_done, o_ready, o_free, drain;
+  // halves: of the key entries (S), of the tokens (R, c U)
+  uint64_t s_ready[2], r_ready[2], w_ready[2];
+  uint64_t ks_done, u_done, o_done, d_done, o_ready, o_free, drain;
   uint32_t tmem_base;
   volatile int abort_flag;
 };
@@ -562,8 +629,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+// 16 bytes, or zeros where !have
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
 }
 
 // K-major operand, rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart
@@ -601,35 +669,6 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ---- pairs of fp32 values in one 64-bit register
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pk(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void upk(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t half2_of(f2 v) {
-  float a, b;
-  upk(v, a, b);
-  return half2_bits(a, b);
-}
-
 // 64 columns of this warp's 16 lanes: v[2g + h] = row lane/4 + 8h, columns 8g + 2 (lane % 4) and the next
 __device__ __forceinline__ void tm_ld(uint32_t t, f2 (&v)[16]) {
   asm volatile(
@@ -653,18 +692,31 @@ __device__ __forceinline__ void tm_st(uint32_t t, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// The larger of a row's absolute values in v[h], v[h + 2], ... over the four lanes that share the row
+// The exponents that scale two rows: of the largest absolute values in v[0],
+// v[2], ... and v[1], v[3], ..., over the four lanes that share the rows
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 template <int N>
-__device__ __forceinline__ float row_size(const f2 *v, int h) {
-  float m = 0.f;
+__device__ __forceinline__ void row_exps(const f2 *v, int (&e)[2]) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = h; i < N; i += 2) {
+  for (int i = 0; i < N; ++i) {
     float a, b;
     upk(v[i], a, b);
-    m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+    m[i & 3] = max3(m[i & 3], a, b);
   }
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  float x = fmaxf(m[0], m[2]), y = fmaxf(m[1], m[3]);
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const float x2 = __shfl_xor_sync(0xffffffffu, x, o), y2 = __shfl_xor_sync(0xffffffffu, y, o);
+    x = fmaxf(x, x2);
+    y = fmaxf(y, y2);
+  }
+  e[0] = scale_exp(x);
+  e[1] = scale_exp(y);
 }
 // v (N pairs of values, two rows) times its rows' scales, as high parts at
 // column hi and the negatives of the low parts at column lo.  Scaled values are
@@ -744,13 +796,13 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->full[s], 1 + 32);  // bulk copies, and the producer's lanes (their zeros)
       mbar_init(&bars->empty[s], 1 + kChainWarps);
+      mbar_init(&bars->s_ready[s], kChainWarps);
+      mbar_init(&bars->r_ready[s], kChainWarps);
+      mbar_init(&bars->w_ready[s], kChainWarps);
     }
-    mbar_init(&bars->s_ready, kChainWarps);
     mbar_init(&bars->ks_done, 1);
-    mbar_init(&bars->r_ready, kChainWarps);
     mbar_init(&bars->u_done, 1);
     mbar_init(&bars->o_done, 1);
-    mbar_init(&bars->w_ready, kChainWarps);
     mbar_init(&bars->d_done, 1);
     mbar_init(&bars->o_ready, kChainWarps);
     mbar_init(&bars->o_free, 1);
@@ -795,12 +847,15 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
       const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
       const uint32_t st = stages + s * St::kBytes, sc = st + St::kSc + 8 * q;
       // 1: the state as the operand of K S and Q S
-      const int es[2] = {scale_exp(row_size<NS>(S, 0)), scale_exp(row_size<NS>(S, 1))};
+      int es[2], er[2], eu[2];
+      row_exps<NS>(S, es);
       {
         const float f[2] = {pow2f(es[0]), pow2f(es[1])};
-        split_store<NS>(S, f, tl + kColS, tl + kColS + 64);
+        split_store<NS / 2>(S, f, tl + kColS, tl + kColS + 64);
+        publish(&bars->s_ready[0]);
+        split_store<NS / 2>(S + NS / 2, f, tl + kColS + NS, tl + kColS + 64 + NS);
+        publish(&bars->s_ready[1]);
       }
-      publish(&bars->s_ready);
       // 2: R; V's pairs of tokens come transposed from its rows
       if (!(ok = wait_warp(&bars->full[s], sph, bars))) break;
       uint32_t v[16];
@@ -824,12 +879,14 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
 #pragma unroll
         for (int i = 0; i < 16; ++i) R[i] = fma2(mul2(fac[i >> 1], ni[i & 1]), R[i], pair_of<T>(v[i]));
       }
-      const int er[2] = {scale_exp(row_size<16>(R, 0)), scale_exp(row_size<16>(R, 1))};
+      row_exps<16>(R, er);
       {
         const float f[2] = {pow2f(er[0]), pow2f(er[1])};
-        split_store<16>(R, f, tl + kColR, tl + kColR + 32);
+        split_store<8>(R, f, tl + kColR, tl + kColR + 32);
+        publish(&bars->r_ready[0]);
+        split_store<8>(R + 8, f, tl + kColR + 16, tl + kColR + 48);
+        publish(&bars->r_ready[1]);
       }
-      publish(&bars->r_ready);
       // 3: the scaled U
 #pragma unroll
       for (int g = 0; g < 8; ++g) fac[g] = lds2(sc + 4 * kC + 32 * g);
@@ -838,15 +895,17 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
       tm_ld(tl + kColU, R);
 #pragma unroll
       for (int i = 0; i < 16; ++i) R[i] = mul2(R[i], fac[i >> 1]);
-      const int eu[2] = {scale_exp(row_size<16>(R, 0)), scale_exp(row_size<16>(R, 1))};
+      row_exps<16>(R, eu);
       {
         const float f[2] = {pow2f(eu[0]), pow2f(eu[1])};
-        split_store<16>(R, f, tl + kColW, tl + kColW + 32);
+        split_store<8>(R, f, tl + kColW, tl + kColW + 32);
+        // D overwrites S's operand, which the products with Q read
+        if (!(ok = wait_warp(&bars->o_done, ph, bars))) break;
+        fence_after();
+        publish(&bars->w_ready[0]);
+        split_store<8>(R + 8, f, tl + kColW + 16, tl + kColW + 48);
+        publish(&bars->w_ready[1]);
       }
-      // D overwrites S's operand, which the products with Q read
-      if (!(ok = wait_warp(&bars->o_done, ph, bars))) break;
-      fence_after();
-      publish(&bars->w_ready);
       // o while D is computed
       {
         const float ps = lds1(st + St::kSc + (3 * kC + 1) * 4);
@@ -871,7 +930,6 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
                        "r"(w[2]), "r"(w[3])
                        : "memory");
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       const float gc = lds1(st + St::kSc + 3 * kC * 4);
       const float fd[2] = {pow2f(-eu[0]) * pow2f(-er[0]), pow2f(-eu[1]) * pow2f(-er[1])};
@@ -902,7 +960,8 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
     }
   } else if (warp == 8) {
     if (!c_delta_stall) {
-      const uint32_t row_bytes = a.DV * 2;
+      const int pshift = a.DV == 128 ? 4 : 3, per = 1 << pshift;  // 16-byte pieces of a row of V
+      const T *v0 = static_cast<const T *>(a.v);
       int n = 0;
       for (; n < chunks; ++n) {
         const uint32_t s = n & 1, sph = (n >> 1) & 1;
@@ -911,27 +970,25 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
         const int64_t place = place0 + n, t = t0 + (int64_t)n * kC;
         const int len = (int)min((int64_t)kC, t1 - t);
         if (lane == 0) {
-          mbar_expect(&bars->full[s], St::kKq + 3 * kTile + kScalarBytes + len * row_bytes);
+          mbar_expect(&bars->full[s], St::kKq + 3 * kTile + kScalarBytes);
           bulk_load(st, ws.kq + (place * a.HK + hk) * (int64_t)St::kKq, St::kKq, &bars->full[s]);
           bulk_load(st + St::kTp, ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile), 3 * kTile, &bars->full[s]);
           bulk_load(st + St::kSc, ws.sc + (place * a.HV + hv) * kScalars, kScalarBytes, &bars->full[s]);
         }
-        __syncwarp();
-        const T *v = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)hv * a.DV;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = lane + 32 * i;
-          const uint32_t dst = st + St::kV + r * kRow;
-          if (r < len) {
-            bulk_load(dst, v + r * a.v_stride, row_bytes, &bars->full[s]);
-          } else {  // rows past the sequence's end
-            for (uint32_t x = 0; x < row_bytes; x += 16)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + x), "r"(0) : "memory");
-          }
+        // V's rows in pieces of 16 bytes, zeros past the sequence's end (a bulk
+        // copy per row took the warp about 50 clocks each)
+        const T *v = static_cast<const T *>(a.v) + (t + (lane >> pshift)) * a.v_stride + (int64_t)hv * a.DV + (lane & (per - 1)) * 8;
+        const uint32_t dst = st + St::kV + (uint32_t)(lane >> pshift) * kRow + (lane & (per - 1)) * 16;
+        const int rows = 32 >> pshift;
+#pragma unroll 8
+        for (int r = 0; r < kC; r += rows) {
+          const bool in = r + (lane >> pshift) < len;
+          copy16(dst + r * kRow, in ? v + (int64_t)r * a.v_stride : v0, in);
         }
-        mbar_arrive(&bars->full[s]);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars->full[s])) : "memory");
       }
       // no copy is in flight when the CTA ends
+      asm volatile("cp.async.wait_all;" ::: "memory");
       for (int m = n > 2 ? n - 2 : 0; m < n; ++m) {
         const unsigned long long since = global_ns();
         while (!mbar_try(&bars->full[m & 1], (m >> 1) & 1) && global_ns() - since < c_delta_wait_ns) {
@@ -943,57 +1000,75 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
       const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
       const uint32_t kt = stages + s * St::kBytes, qt = kt + St::kKq / 2, tp = kt + St::kTp;
       if (!wait_warp(&bars->full[s], sph, bars)) break;
-      if (!wait_warp(&bars->s_ready, ph, bars)) break;
-      fence_after();
-      if (elect_one()) {
+      bool ok = true;
 #pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
-          const uint64_t bd = desc_k(kt + (k >> 2) * (kC * 128) + (k & 3) * 32);
-          umma(tmem + kColKS, tmem + kColS + 64 + 8 * k, bd, idesc(64, true), k > 0);
-          umma(tmem + kColKS, tmem + kColS + 8 * k, bd, idesc(64, false), true);
-        }
-        umma_commit(&bars->ks_done);
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (!(ok = wait_warp(&bars->s_ready[h], ph, bars))) break;
+        fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
-          const uint64_t bd = desc_k(qt + (k >> 2) * (kC * 128) + (k & 3) * 32);
-          if (kLowInO) umma(tmem + kColQS, tmem + kColS + 64 + 8 * k, bd, idesc(64, true), k > 0);
-          umma(tmem + kColQS, tmem + kColS + 8 * k, bd, idesc(64, false), kLowInO || k > 0);
+          for (int i = 0; i < DK / 32; ++i) {
+            const int k = h * (DK / 32) + i;
+            const uint64_t bd = desc_k(kt + (k >> 2) * (kC * 128) + (k & 3) * 32);
+            umma(tmem + kColKS, tmem + kColS + 64 + 8 * k, bd, idesc(64, true), k > 0);
+            umma(tmem + kColKS, tmem + kColS + 8 * k, bd, idesc(64, false), true);
+          }
+          if (h == 1) {
+            umma_commit(&bars->ks_done);
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) {
+              const uint64_t bd = desc_k(qt + (k >> 2) * (kC * 128) + (k & 3) * 32);
+              if (kLowInO) umma(tmem + kColQS, tmem + kColS + 64 + 8 * k, bd, idesc(64, true), k > 0);
+              umma(tmem + kColQS, tmem + kColS + 8 * k, bd, idesc(64, false), kLowInO || k > 0);
+            }
+          }
         }
+        __syncwarp();
       }
-      __syncwarp();
-      if (!wait_warp(&bars->r_ready, ph, bars)) break;
-      fence_after();
-      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) {
-          const uint64_t th = desc_k(tp + k * 32), tl = desc_k(tp + 2 * kTile + k * 32);
-          umma(tmem + kColU, tmem + kColR + 32 + 8 * k, th, idesc(64, true), k > 0);
-          umma(tmem + kColU, tmem + kColR + 8 * k, tl, idesc(64, false), true);
-          umma(tmem + kColU, tmem + kColR + 8 * k, th, idesc(64, false), true);
-        }
-        umma_commit(&bars->u_done);
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (!(ok = wait_warp(&bars->r_ready[h], ph, bars))) break;
+        fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) {
-          const uint64_t pd = desc_k(tp + kTile + k * 32);
-          if (kLowInO) umma(tmem + kColO, tmem + kColR + 32 + 8 * k, pd, idesc(64, true), k > 0);
-          umma(tmem + kColO, tmem + kColR + 8 * k, pd, idesc(64, false), kLowInO || k > 0);
+          for (int k = 2 * h; k < 2 * h + 2; ++k) {
+            const uint64_t th = desc_k(tp + k * 32), tl = desc_k(tp + 2 * kTile + k * 32);
+            umma(tmem + kColU, tmem + kColR + 32 + 8 * k, th, idesc(64, true), k > 0);
+            umma(tmem + kColU, tmem + kColR + 8 * k, tl, idesc(64, false), true);
+            umma(tmem + kColU, tmem + kColR + 8 * k, th, idesc(64, false), true);
+          }
+          if (h == 1) {
+            umma_commit(&bars->u_done);
+#pragma unroll
+            for (int k = 0; k < kC / 16; ++k) {
+              const uint64_t pd = desc_k(tp + kTile + k * 32);
+              if (kLowInO) umma(tmem + kColO, tmem + kColR + 32 + 8 * k, pd, idesc(64, true), k > 0);
+              umma(tmem + kColO, tmem + kColR + 8 * k, pd, idesc(64, false), kLowInO || k > 0);
+            }
+            umma_commit(&bars->o_done);
+          }
         }
-        umma_commit(&bars->o_done);
+        __syncwarp();
       }
-      __syncwarp();
-      if (!wait_warp(&bars->w_ready, ph, bars)) break;
-      fence_after();
-      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) {
-          const uint64_t bd = desc_mn(kt + k * 2048);
-          umma(tmem + kColD, tmem + kColW + 32 + 8 * k, bd, idesc(DK, true, true), k > 0);
-          umma(tmem + kColD, tmem + kColW + 8 * k, bd, idesc(DK, false, true), true);
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (!(ok = wait_warp(&bars->w_ready[h], ph, bars))) break;
+        fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 2 * h; k < 2 * h + 2; ++k) {
+            const uint64_t bd = desc_mn(kt + k * 2048);
+            umma(tmem + kColD, tmem + kColW + 32 + 8 * k, bd, idesc(DK, true, true), k > 0);
+            umma(tmem + kColD, tmem + kColW + 8 * k, bd, idesc(DK, false, true), true);
+          }
+          if (h == 1) {
+            umma_commit(&bars->d_done);
+            umma_commit(&bars->empty[s]);
+          }
         }
-        umma_commit(&bars->d_done);
-        umma_commit(&bars->empty[s]);
+        __syncwarp();
       }
-      __syncwarp();
+      if (!ok) break;
     }
     // every MMA issued, complete before the memory it uses is released
     if (elect_one()) umma_commit(&bars->drain);
@@ -1002,22 +1077,23 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
     while (!mbar_try(&bars->drain, 0) && global_ns() - since < c_delta_wait_ns) {
     }
   } else {
-    const uint32_t row_bytes = a.DV * 2;
-    T *o = static_cast<T *>(a.o) + (int64_t)hv * a.DV;
+    const int pshift = a.DV == 128 ? 4 : 3, per = 1 << pshift, rows = 32 >> pshift;
+    const int r0 = lane >> pshift, at = (lane & (per - 1)) * 8;
+    T *o = static_cast<T *>(a.o) + (t0 + r0) * a.o_stride + (int64_t)hv * a.DV + at;
     for (int n = 0; n < chunks; ++n) {
       if (!wait_warp(&bars->o_ready, n & 1, bars)) break;
-      const int64_t t = t0 + (int64_t)n * kC;
-      const int len = (int)min((int64_t)kC, t1 - t);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = lane + 32 * i;
-        if (r < len) bulk_store(o + (t + r) * a.o_stride, o_tile + r * kRow, row_bytes);
+      const int len = (int)min((int64_t)kC, t1 - t0 - (int64_t)n * kC);
+#pragma unroll 8
+      for (int r = 0; r < kC; r += rows) {
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(o_tile + (r + r0) * kRow + at * 2) : "memory");
+        if (r + r0 < len) *reinterpret_cast<uint4 *>(o + (int64_t)r * a.o_stride) = w;
       }
-      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+      o += (int64_t)kC * a.o_stride;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->o_free);
     }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   fence_before();
   __syncthreads();
@@ -1042,17 +1118,14 @@ cudaError_t chunks_t(const DeltaView &a, void *workspace, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   const int dev = current_device();
   if (not_done(ready, dev)) {
-    cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)prep_smem<DK>());
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(delta_chain_kernel<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)chain_smem<DK>());
+    cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)chain_smem<DK>());
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
   }
   const ChunkPlaces ws = places(a, workspace, nullptr);
   const dim3 grid((unsigned)chunk_places(a.T, a.B), (unsigned)a.HK);
-  delta_prep_kernel<T, DK><<<grid, kPrepT, prep_smem<DK>(), st>>>(a, ws);
+  delta_prep_kernel<T, DK><<<grid, kPrepT, 0, st>>>(a, ws);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   delta_chain_kernel<T, DK><<<(unsigned)(a.B * a.HV), kChainT, chain_smem<DK>(), st>>>(a, ws);
