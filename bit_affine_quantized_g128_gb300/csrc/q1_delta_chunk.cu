@@ -95,29 +95,19 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// ---- pairs of fp32 values in one 64-bit register
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pk(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
+// ---- pairs of fp32 values: neighbouring columns of a fragment (plain fp32
+// instructions: the two-wide ones took 3.6 clocks a warp, a single one 1.2)
+struct f2 {
+  float a, b;
+};
+__device__ __forceinline__ f2 pk(float a, float b) { return f2{a, b}; }
+__device__ __forceinline__ void upk(f2 v, float &a, float &b) {
+  a = v.a;
+  b = v.b;
 }
-__device__ __forceinline__ void upk(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { return f2{fmaf(a.a, b.a, c.a), fmaf(a.b, b.b, c.b)}; }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { return f2{__fmul_rn(a.a, b.a), __fmul_rn(a.b, b.b)}; }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) { return f2{__fadd_rn(a.a, b.a), __fadd_rn(a.b, b.b)}; }
 __device__ __forceinline__ uint32_t half2_of(f2 v) {
   float a, b;
   upk(v, a, b);
@@ -175,6 +165,10 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+__device__ __forceinline__ f2 lds_pair(const float *p) {
+  const float2 v = *reinterpret_cast<const float2 *>(p);
+  return f2{v.x, v.y};
 }
 // d += (ah + al)(bh + bl) without the product of the low parts
 __device__ __forceinline__ void mma3(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], uint32_t bh0, uint32_t bh1,
@@ -386,8 +380,8 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const int c = 16 * j + 8 * n + fc;
-            const f2 ch = *reinterpret_cast<const f2 *>(&sh.Gh[c]), cl = *reinterpret_cast<const f2 *>(&sh.Gl[c]);
-            const f2 rk = *reinterpret_cast<const f2 *>(&sh.rk[c]);
+            const f2 ch = lds_pair(&sh.Gh[c]), cl = lds_pair(&sh.Gl[c]);
+            const f2 rk = lds_pair(&sh.rk[c]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float x, y;
@@ -402,7 +396,7 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
                 upk(pv, v0, v1);
                 av = pk(cc < i ? u0 : 0.f, cc + 1 < i ? u1 : 0.f);
                 pv = pk(cc <= i ? v0 : 0.f, cc + 1 <= i ? v1 : 0.f);
-                *reinterpret_cast<f2 *>(&sh.D[warp][i][cc]) = av;
+                *reinterpret_cast<float2 *>(&sh.D[warp][i][cc]) = make_float2(av.a, av.b);
               }
               A[j][n][e] = av;
               P[j][n][e] = pv;
@@ -440,10 +434,10 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
       f2 d[2][2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        const f2 be = mul2(*reinterpret_cast<const f2 *>(&sh.beta[16 * warp + 8 * n + fc]), pk(ts, ts));
+        const f2 be = mul2(lds_pair(&sh.beta[16 * warp + 8 * n + fc]), pk(ts, ts));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          d[n][e] = *reinterpret_cast<const f2 *>(&sh.D[warp][fr + 8 * e][8 * n + fc]);
+          d[n][e] = lds_pair(&sh.D[warp][fr + 8 * e][8 * n + fc]);
           float x, y;
           uint32_t h, l;
           upk(mul2(d[n][e], be), x, y);
@@ -536,7 +530,7 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
 // All products are in the transposed form, a value column per lane of tensor
 // memory, so that the operand made from registers is the MMA's A operand in
 // tensor memory (M = 128 lanes) and K, Q, T and P' are its B operands as they
-// lie in shared memory.  Chain warps 0-7 own 16 lanes (state columns) each, in
+// lie in shared memory.  The first 8 (or 4) warps, the chain, own 16 lanes (state columns) each, in
 // the fragment form of tensor memory loads (16x256b): a thread holds two rows
 // (columns lane/4 and lane/4 + 8 of the warp's 16) and pairs of neighbouring
 // tokens or key entries, which are also the pairs of an fp16 operand word and
@@ -546,41 +540,44 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
 //     2  R = V - a KS -> high, low          MMA: U = R^T T^T, O2 = R^T P'^T
 //     3  c U -> high, low                   MMA: D = (c U)^T K
 //     o = b QS + O2 while D is computed; then S = gamma_C S + D
-//   warp 8: copies of the next chunk's tiles, factors and V rows (two stages)
-//   warp 9: tensor memory; issues the MMAs (the whole warp goes through the
+//   next warp: copies of the next chunk's tiles, factors and V rows (two stages)
+//   next: tensor memory; issues the MMAs (the whole warp goes through the
 //     issue loop and elect.sync picks the thread: 17 clocks per MMA, against 44
 //     behind an `if (lane == 0)`, whose operands leave the uniform registers)
-//   warp 10: the chunk's rows of o from shared memory, where the chain stages them
+//   last: the chunk's rows of o from shared memory, where the chain stages them
 // One chunk is a chain of three dependent products; the time is the latency of
 // that chain, not the rate of any unit.
 // Tensor memory columns: S high [0, 64), low [64, 128), and D over both;
 // KS [128, 192); QS [192, 256); R [256, 320); U [320, 384); O2 [384, 448);
 // c U [448, 512).
-constexpr int kChainWarps = 8;
-constexpr int kChainT = 32 * (kChainWarps + 3);
 constexpr uint32_t kColS = 0, kColD = 0, kColKS = 128, kColQS = 192, kColR = 256, kColU = 320, kColO = 384, kColW = 448;
-constexpr int kRow = 128 * 2 + 16;  // bytes of a staged row of V or o: 8 rows at one column fall into different banks
 
 struct ChainBars {
   uint64_t full[2], empty[2];
-  // halves: of the key entries (S), of the tokens (R, c U)
-  uint64_t s_ready[2], r_ready[2], w_ready[2];
-  uint64_t ks_done, u_done, o_done, d_done, o_ready, o_free, drain;
+  // halves: of the key entries (S, D), of the tokens (R, c U)
+  uint64_t s_ready[2], r_ready[2], w_ready[2], d_done[2];
+  uint64_t ks_done, u_done, o_done, o_ready, o_free, drain;
   uint32_t tmem_base;
   volatile int abort_flag;
 };
-constexpr int kChainHeader = 1024;
-static_assert(sizeof(ChainBars) <= kChainHeader, "header");
+constexpr int kSortMax = 256;  // sequences that are taken longest first
+constexpr int kChainHeader = 2048;
+static_assert(sizeof(ChainBars) + kSortMax * 4 <= kChainHeader, "header");
 
-template <int DK>
+// M: the state columns of a CTA.  128 is one head; 64 gives half a head to a
+// CTA (tensor memory lanes 0-15 of each quarter), which halves the work per
+// chunk of the chain warps and so shortens the chain, on twice the SMs.
+template <int DK, int M>
 struct ChainStage {
+  static constexpr int kWarps = M / 16, kThreads = 32 * (kWarps + 3);
+  static constexpr int kRow = M * 2 + 16;  // bytes of a staged row of V or o: 8 rows at one column fall into different banks
   static constexpr int kKq = 2 * kC * DK * 2;
   static constexpr int kTp = kKq, kV = kTp + 3 * kTile, kSc = kV + kC * kRow;
   static constexpr int kBytes = (kSc + kScalarBytes + 1023) / 1024 * 1024;
 };
-template <int DK>
+template <int DK, int M>
 constexpr size_t chain_smem() {
-  return 1024 + kChainHeader + 2 * (size_t)ChainStage<DK>::kBytes + kC * kRow;
+  return 1024 + kChainHeader + 2 * (size_t)ChainStage<DK, M>::kBytes + kC * ChainStage<DK, M>::kRow;
 }
 
 __device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t count) {
@@ -645,11 +642,11 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(kC * 128 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// fp16 x fp16 -> fp32, M = 128; bit 13: A negated (the low parts are stored as
+// fp16 x fp16 -> fp32; bit 13: A negated (the low parts are stored as
 // their negatives); bit 16: B with its rows along the contraction
-__host__ __device__ constexpr uint32_t idesc(int N, bool neg, bool b_mn = false) {
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool neg, bool b_mn = false) {
   return (1u << 4) | (neg ? 1u << 13 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(128 >> 4) << 24);
+         ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
@@ -672,16 +669,9 @@ __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.
 // 64 columns of this warp's 16 lanes: v[2g + h] = row lane/4 + 8h, columns 8g + 2 (lane % 4) and the next
 __device__ __forceinline__ void tm_ld(uint32_t t, f2 (&v)[16]) {
   asm volatile(
-      "{\n .reg .b32 r<32>;\n"
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {r0,r1,r2,r3,r4,r5,r6,r7,r8,r9,r10,r11,r12,r13,r14,r15,"
-      "r16,r17,r18,r19,r20,r21,r22,r23,r24,r25,r26,r27,r28,r29,r30,r31}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      "mov.b64 %0, {r0,r1};\n mov.b64 %1, {r2,r3};\n mov.b64 %2, {r4,r5};\n mov.b64 %3, {r6,r7};\n"
-      "mov.b64 %4, {r8,r9};\n mov.b64 %5, {r10,r11};\n mov.b64 %6, {r12,r13};\n mov.b64 %7, {r14,r15};\n"
-      "mov.b64 %8, {r16,r17};\n mov.b64 %9, {r18,r19};\n mov.b64 %10, {r20,r21};\n mov.b64 %11, {r22,r23};\n"
-      "mov.b64 %12, {r24,r25};\n mov.b64 %13, {r26,r27};\n mov.b64 %14, {r28,r29};\n mov.b64 %15, {r30,r31};\n}\n"
-      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7]), "=l"(v[8]),
-        "=l"(v[9]), "=l"(v[10]), "=l"(v[11]), "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15])
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0].a), "=f"(v[0].b), "=f"(v[1].a), "=f"(v[1].b), "=f"(v[2].a), "=f"(v[2].b), "=f"(v[3].a), "=f"(v[3].b), "=f"(v[4].a), "=f"(v[4].b), "=f"(v[5].a), "=f"(v[5].b), "=f"(v[6].a), "=f"(v[6].b), "=f"(v[7].a), "=f"(v[7].b), "=f"(v[8].a), "=f"(v[8].b), "=f"(v[9].a), "=f"(v[9].b), "=f"(v[10].a), "=f"(v[10].b), "=f"(v[11].a), "=f"(v[11].b), "=f"(v[12].a), "=f"(v[12].b), "=f"(v[13].a), "=f"(v[13].b), "=f"(v[14].a), "=f"(v[14].b), "=f"(v[15].a), "=f"(v[15].b)
       : "r"(t)
       : "memory");
 }
@@ -700,14 +690,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 template <int N>
-__device__ __forceinline__ void row_exps(const f2 *v, int (&e)[2]) {
-  float m[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void row_max(const f2 *v, float (&m)[4]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float a, b;
-    upk(v[i], a, b);
-    m[i & 3] = max3(m[i & 3], a, b);
-  }
+  for (int i = 0; i < N; ++i) m[i & 3] = max3(m[i & 3], v[i].a, v[i].b);
+}
+__device__ __forceinline__ void row_exps(const float (&m)[4], int (&e)[2]) {
   float x = fmaxf(m[0], m[2]), y = fmaxf(m[1], m[3]);
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
@@ -765,7 +752,7 @@ __device__ __forceinline__ uint32_t word_of(f2 v) {
 }
 __device__ __forceinline__ f2 lds2(uint32_t addr) {
   f2 v;
-  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.a), "=f"(v.b) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ float lds1(uint32_t addr) {
@@ -774,16 +761,38 @@ __device__ __forceinline__ float lds1(uint32_t addr) {
   return v;
 }
 
-template <typename T, int DK>
-__global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView a, const ChunkPlaces ws) {
+template <typename T, int DK, int M>
+__global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_kernel(const DeltaView a, const ChunkPlaces ws, int sort) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  using St = ChainStage<DK>;
+  using St = ChainStage<DK, M>;
+  constexpr int NW = St::kWarps, kRow = St::kRow;  // chain warps; then the copies, the MMAs and the stores
   ChainBars *bars = reinterpret_cast<ChainBars *>(base);
   const uint32_t stages = smem_u32(base) + kChainHeader, o_tile = stages + 2 * St::kBytes;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int64_t b = blockIdx.x / a.HV;
-  const int hv = (int)(blockIdx.x - b * a.HV), hk = hv / (a.HV / a.HK);
+  const int parts = a.DV / M;
+  int64_t b = blockIdx.x / (a.HV * parts);
+  const int item = (int)(blockIdx.x - b * (a.HV * parts)), hv = item / parts, hk = hv / (a.HV / a.HK);
+  const int dv0 = (item - hv * parts) * M;  // this CTA's first state column
+  if (sort) {
+    // more CTAs than fit at once: the longest sequences first, so that the
+    // last CTAs to start are short
+    int *len = reinterpret_cast<int *>(base + kChainHeader - kSortMax * 4);
+    __shared__ int pick;
+    int64_t x0, x1;
+    for (int i = tid; i < (int)a.B; i += St::kThreads) {
+      a.range(i, x0, x1);
+      len[i] = (int)(x1 - x0);
+    }
+    __syncthreads();
+    for (int i = tid; i < (int)a.B; i += St::kThreads) {
+      int rank = 0;
+      for (int j = 0; j < (int)a.B; ++j) rank += len[j] > len[i] || (len[j] == len[i] && j < i);
+      if (rank == (int)b) pick = i;
+    }
+    __syncthreads();
+    b = pick;
+  }
   int64_t t0, t1;
   a.range(b, t0, t1);
   const int chunks = (int)((t1 - t0 + kC - 1) / kC);
@@ -795,22 +804,22 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->full[s], 1 + 32);  // bulk copies, and the producer's lanes (their zeros)
-      mbar_init(&bars->empty[s], 1 + kChainWarps);
-      mbar_init(&bars->s_ready[s], kChainWarps);
-      mbar_init(&bars->r_ready[s], kChainWarps);
-      mbar_init(&bars->w_ready[s], kChainWarps);
+      mbar_init(&bars->empty[s], 1 + NW);
+      mbar_init(&bars->s_ready[s], NW);
+      mbar_init(&bars->r_ready[s], NW);
+      mbar_init(&bars->w_ready[s], NW);
+      mbar_init(&bars->d_done[s], 1);
     }
     mbar_init(&bars->ks_done, 1);
     mbar_init(&bars->u_done, 1);
     mbar_init(&bars->o_done, 1);
-    mbar_init(&bars->d_done, 1);
-    mbar_init(&bars->o_ready, kChainWarps);
+    mbar_init(&bars->o_ready, NW);
     mbar_init(&bars->o_free, 1);
     mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == NW + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -820,22 +829,24 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
-  if (warp < kChainWarps) {
-    const int L0 = 32 * (warp & 3) + 16 * (warp >> 2);  // first of this warp's lanes = state columns
-    const int q = lane & 3, c = L0 + (lane >> 2);       // this thread's columns c and c + 8
-    const uint32_t tl = tmem + ((uint32_t)L0 << 16);
-    const bool mine = L0 < a.DV;
+  if (warp < NW) {
+    // first of this warp's 16 columns in the CTA's M, and of its lanes
+    const int L0 = M == 128 ? 32 * (warp & 3) + 16 * (warp >> 2) : 16 * warp;
+    const int q = lane & 3, c = dv0 + L0 + (lane >> 2);  // this thread's columns c and c + 8 of the state
+    const uint32_t tl = tmem + ((uint32_t)(M == 128 ? L0 : 32 * warp) << 16);
     const int64_t slot = a.slots ? a.slots[b] : b;
     const bool have = slot >= 0 && slot < a.n_slots;
     float *state = a.state + ((have ? slot : 0) * a.HV + hv) * (int64_t)DK * a.DV + (int64_t)(2 * q) * a.DV + c;
     constexpr int NS = DK / 4;  // pairs of state values per thread: S[2g + h] = key entries 8g + 2q, + 1 of column c + 8h
     f2 S[NS];
-    const bool load = have && mine && !(a.fresh && a.fresh[b]);
+    const bool load = have && !(a.fresh && a.fresh[b]);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const float *p = state + (int64_t)(8 * (i >> 1)) * a.DV + 8 * (i & 1);
       S[i] = load ? pk(p[0], p[a.DV]) : pk(0.f, 0.f);
     }
+    float big[4] = {};
+    row_max<NS>(S, big);
     auto publish = [&](uint64_t *bar) {  // tensor-memory stores of this warp, to the MMAs
       wait_st();
       fence_before();
@@ -848,7 +859,7 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
       const uint32_t st = stages + s * St::kBytes, sc = st + St::kSc + 8 * q;
       // 1: the state as the operand of K S and Q S
       int es[2], er[2], eu[2];
-      row_exps<NS>(S, es);
+      row_exps(big, es);
       {
         const float f[2] = {pow2f(es[0]), pow2f(es[1])};
         split_store<NS / 2>(S, f, tl + kColS, tl + kColS + 64);
@@ -862,9 +873,8 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
       f2 fac[8];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (mine)
-          ldsm4t(st + St::kV + (uint32_t)(16 * g + ((lane >> 4) << 3) + (lane & 7)) * kRow + (L0 + (((lane >> 3) & 1) << 3)) * 2, w);
+        uint32_t w[4];
+        ldsm4t(st + St::kV + (uint32_t)(16 * g + ((lane >> 4) << 3) + (lane & 7)) * kRow + (L0 + (((lane >> 3) & 1) << 3)) * 2, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[4 * g + i] = w[i];
       }
@@ -879,7 +889,11 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
 #pragma unroll
         for (int i = 0; i < 16; ++i) R[i] = fma2(mul2(fac[i >> 1], ni[i & 1]), R[i], pair_of<T>(v[i]));
       }
-      row_exps<16>(R, er);
+      {
+        float m[4] = {};
+        row_max<16>(R, m);
+        row_exps(m, er);
+      }
       {
         const float f[2] = {pow2f(er[0]), pow2f(er[1])};
         split_store<8>(R, f, tl + kColR, tl + kColR + 32);
@@ -895,7 +909,11 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
       tm_ld(tl + kColU, R);
 #pragma unroll
       for (int i = 0; i < 16; ++i) R[i] = mul2(R[i], fac[i >> 1]);
-      row_exps<16>(R, eu);
+      {
+        float m[4] = {};
+        row_max<16>(R, m);
+        row_exps(m, eu);
+      }
       {
         const float f[2] = {pow2f(eu[0]), pow2f(eu[1])};
         split_store<8>(R, f, tl + kColW, tl + kColW + 32);
@@ -939,28 +957,32 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
         mbar_arrive(&bars->o_ready);
         mbar_arrive(&bars->empty[s]);  // this warp is done with V and the factors
       }
-      // the state
-      if (!(ok = wait_warp(&bars->d_done, ph, bars))) break;
-      fence_after();
+      // the state, 64 key entries at a time
       const f2 gc2 = pk(gc, gc), fd2[2] = {pk(fd[0], fd[0]), pk(fd[1], fd[1])};
+      big[0] = big[1] = big[2] = big[3] = 0.f;
 #pragma unroll
-      for (int k = 0; k < NS; k += 16) {
+      for (int h = 0; h < DK / 64; ++h) {
+        if (!(ok = wait_warp(&bars->d_done[h], ph, bars))) break;
+        fence_after();
         f2 D[16];
-        tm_ld(tl + kColD + 4 * k, D);
+        tm_ld(tl + kColD + 64 * h, D);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[k + i] = fma2(gc2, S[k + i], mul2(D[i], fd2[i & 1]));
+        for (int i = 0; i < 16; ++i) S[16 * h + i] = fma2(gc2, S[16 * h + i], mul2(D[i], fd2[i & 1]));
+        row_max<16>(S + 16 * h, big);
       }
+      if (!ok) break;
     }
-    if (ok && have && mine) {
+    if (ok && have) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         float *p = state + (int64_t)(8 * (i >> 1)) * a.DV + 8 * (i & 1);
-        upk(S[i], p[0], p[a.DV]);
+        p[0] = S[i].a;
+        p[a.DV] = S[i].b;
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == NW) {
     if (!c_delta_stall) {
-      const int pshift = a.DV == 128 ? 4 : 3, per = 1 << pshift;  // 16-byte pieces of a row of V
+      constexpr int pshift = M == 128 ? 4 : 3, per = 1 << pshift;  // 16-byte pieces of a row of V
       const T *v0 = static_cast<const T *>(a.v);
       int n = 0;
       for (; n < chunks; ++n) {
@@ -977,9 +999,9 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
         }
         // V's rows in pieces of 16 bytes, zeros past the sequence's end (a bulk
         // copy per row took the warp about 50 clocks each)
-        const T *v = static_cast<const T *>(a.v) + (t + (lane >> pshift)) * a.v_stride + (int64_t)hv * a.DV + (lane & (per - 1)) * 8;
+        const T *v = static_cast<const T *>(a.v) + (t + (lane >> pshift)) * a.v_stride + (int64_t)hv * a.DV + dv0 + (lane & (per - 1)) * 8;
         const uint32_t dst = st + St::kV + (uint32_t)(lane >> pshift) * kRow + (lane & (per - 1)) * 16;
-        const int rows = 32 >> pshift;
+        constexpr int rows = 32 >> pshift;
 #pragma unroll 8
         for (int r = 0; r < kC; r += rows) {
           const bool in = r + (lane >> pshift) < len;
@@ -995,7 +1017,7 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
         }
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == NW + 1) {
     for (int n = 0; n < chunks; ++n) {
       const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
       const uint32_t kt = stages + s * St::kBytes, qt = kt + St::kKq / 2, tp = kt + St::kTp;
@@ -1010,16 +1032,16 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
           for (int i = 0; i < DK / 32; ++i) {
             const int k = h * (DK / 32) + i;
             const uint64_t bd = desc_k(kt + (k >> 2) * (kC * 128) + (k & 3) * 32);
-            umma(tmem + kColKS, tmem + kColS + 64 + 8 * k, bd, idesc(64, true), k > 0);
-            umma(tmem + kColKS, tmem + kColS + 8 * k, bd, idesc(64, false), true);
+            umma(tmem + kColKS, tmem + kColS + 64 + 8 * k, bd, idesc(M, 64, true), k > 0);
+            umma(tmem + kColKS, tmem + kColS + 8 * k, bd, idesc(M, 64, false), true);
           }
           if (h == 1) {
             umma_commit(&bars->ks_done);
 #pragma unroll
             for (int k = 0; k < DK / 16; ++k) {
               const uint64_t bd = desc_k(qt + (k >> 2) * (kC * 128) + (k & 3) * 32);
-              if (kLowInO) umma(tmem + kColQS, tmem + kColS + 64 + 8 * k, bd, idesc(64, true), k > 0);
-              umma(tmem + kColQS, tmem + kColS + 8 * k, bd, idesc(64, false), kLowInO || k > 0);
+              if (kLowInO) umma(tmem + kColQS, tmem + kColS + 64 + 8 * k, bd, idesc(M, 64, true), k > 0);
+              umma(tmem + kColQS, tmem + kColS + 8 * k, bd, idesc(M, 64, false), kLowInO || k > 0);
             }
           }
         }
@@ -1033,17 +1055,17 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
 #pragma unroll
           for (int k = 2 * h; k < 2 * h + 2; ++k) {
             const uint64_t th = desc_k(tp + k * 32), tl = desc_k(tp + 2 * kTile + k * 32);
-            umma(tmem + kColU, tmem + kColR + 32 + 8 * k, th, idesc(64, true), k > 0);
-            umma(tmem + kColU, tmem + kColR + 8 * k, tl, idesc(64, false), true);
-            umma(tmem + kColU, tmem + kColR + 8 * k, th, idesc(64, false), true);
+            umma(tmem + kColU, tmem + kColR + 32 + 8 * k, th, idesc(M, 64, true), k > 0);
+            umma(tmem + kColU, tmem + kColR + 8 * k, tl, idesc(M, 64, false), true);
+            umma(tmem + kColU, tmem + kColR + 8 * k, th, idesc(M, 64, false), true);
           }
           if (h == 1) {
             umma_commit(&bars->u_done);
 #pragma unroll
             for (int k = 0; k < kC / 16; ++k) {
               const uint64_t pd = desc_k(tp + kTile + k * 32);
-              if (kLowInO) umma(tmem + kColO, tmem + kColR + 32 + 8 * k, pd, idesc(64, true), k > 0);
-              umma(tmem + kColO, tmem + kColR + 8 * k, pd, idesc(64, false), kLowInO || k > 0);
+              if (kLowInO) umma(tmem + kColO, tmem + kColR + 32 + 8 * k, pd, idesc(M, 64, true), k > 0);
+              umma(tmem + kColO, tmem + kColR + 8 * k, pd, idesc(M, 64, false), kLowInO || k > 0);
             }
             umma_commit(&bars->o_done);
           }
@@ -1056,15 +1078,16 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
         fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int k = 2 * h; k < 2 * h + 2; ++k) {
-            const uint64_t bd = desc_mn(kt + k * 2048);
-            umma(tmem + kColD, tmem + kColW + 32 + 8 * k, bd, idesc(DK, true, true), k > 0);
-            umma(tmem + kColD, tmem + kColW + 8 * k, bd, idesc(DK, false, true), true);
+          for (int d = 0; d < DK / 64; ++d) {
+#pragma unroll
+            for (int k = 2 * h; k < 2 * h + 2; ++k) {
+              const uint64_t bd = desc_mn(kt + d * (kC * 128) + k * 2048);
+              umma(tmem + kColD + 64 * d, tmem + kColW + 32 + 8 * k, bd, idesc(M, 64, true, true), k > 0);
+              umma(tmem + kColD + 64 * d, tmem + kColW + 8 * k, bd, idesc(M, 64, false, true), true);
+            }
+            if (h == 1) umma_commit(&bars->d_done[d]);
           }
-          if (h == 1) {
-            umma_commit(&bars->d_done);
-            umma_commit(&bars->empty[s]);
-          }
+          if (h == 1) umma_commit(&bars->empty[s]);
         }
         __syncwarp();
       }
@@ -1077,9 +1100,9 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
     while (!mbar_try(&bars->drain, 0) && global_ns() - since < c_delta_wait_ns) {
     }
   } else {
-    const int pshift = a.DV == 128 ? 4 : 3, per = 1 << pshift, rows = 32 >> pshift;
+    constexpr int pshift = M == 128 ? 4 : 3, per = 1 << pshift, rows = 32 >> pshift;
     const int r0 = lane >> pshift, at = (lane & (per - 1)) * 8;
-    T *o = static_cast<T *>(a.o) + (t0 + r0) * a.o_stride + (int64_t)hv * a.DV + at;
+    T *o = static_cast<T *>(a.o) + (t0 + r0) * a.o_stride + (int64_t)hv * a.DV + dv0 + at;
     for (int n = 0; n < chunks; ++n) {
       if (!wait_warp(&bars->o_ready, n & 1, bars)) break;
       const int len = (int)min((int64_t)kC, t1 - t0 - (int64_t)n * kC);
@@ -1097,7 +1120,7 @@ __global__ void __launch_bounds__(kChainT, 1) delta_chain_kernel(const DeltaView
   }
   fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == NW + 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
@@ -1113,23 +1136,40 @@ ChunkPlaces places(const DeltaView &a, void *ws, size_t *total) {
   return ChunkPlaces{p, p + kq, reinterpret_cast<float *>(p + kq + tp)};
 }
 
-template <typename T, int DK>
-cudaError_t chunks_t(const DeltaView &a, void *workspace, cudaStream_t st) {
+template <typename T, int DK, int M>
+cudaError_t chain_t(const DeltaView &a, const ChunkPlaces &ws, int64_t sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   const int dev = current_device();
   if (not_done(ready, dev)) {
-    cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<T, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)chain_smem<DK>());
+    cudaError_t e = cudaFuncSetAttribute(delta_chain_kernel<T, DK, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)chain_smem<DK, M>());
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
+  }
+  const int64_t ctas = a.B * a.HV * (a.DV / M);
+  const int sort = a.cu && a.B > 1 && a.B <= kSortMax && ctas > sms;
+  delta_chain_kernel<T, DK, M><<<(unsigned)ctas, ChainStage<DK, M>::kThreads, chain_smem<DK, M>(), st>>>(a, ws, sort);
+  return cudaGetLastError();
+}
+
+template <typename T, int DK>
+cudaError_t chunks_t(const DeltaView &a, void *workspace, cudaStream_t st) {
+  static std::atomic<int> sm_count[kMaxDevices];
+  const int dev = current_device();
+  int sms = dev < kMaxDevices ? sm_count[dev].load(std::memory_order_relaxed) : 0;
+  if (!sms) {
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) sm_count[dev].store(sms, std::memory_order_relaxed);
   }
   const ChunkPlaces ws = places(a, workspace, nullptr);
   const dim3 grid((unsigned)chunk_places(a.T, a.B), (unsigned)a.HK);
   delta_prep_kernel<T, DK><<<grid, kPrepT, 0, st>>>(a, ws);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  delta_chain_kernel<T, DK><<<(unsigned)(a.B * a.HV), kChainT, chain_smem<DK>(), st>>>(a, ws);
-  return cudaGetLastError();
+  // half a head per CTA while all of them run at once
+  if (a.DV == 64 || 2 * a.B * a.HV <= sms) return chain_t<T, DK, 64>(a, ws, sms, st);
+  return chain_t<T, DK, 128>(a, ws, sms, st);
 }
 
 }  // namespace

@@ -120,6 +120,15 @@ def test_long_sequences(q1, lengths, HK, HV, DK, DV, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("HK,HV,DK,DV", [(4, 8, 128, 128), (8, 16, 128, 128), (8, 16, 64, 128), (16, 16, 128, 64)])
+def test_many_heads(q1, HK, HV, DK, DV, dtype):
+    # more heads than SMs hold at once, and between half as many and that
+    _run(q1, [70, 1, 130, 64, 0, 200, 33, 65, 128, 90], HK, HV, DK, DV, dtype, seed=61, slots=[9, 3, 4, 0, 1, 2, 8, -1, 6, 7],
+         fresh=[0, 0, 1, 0, 0, 1, 0, 0, 0, 0], pool=10)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("decay", ["none", "strong", "reset"])
 @pytest.mark.parametrize("lengths", [[5], [150, 70]], ids=str)
 def test_decays(q1, lengths, decay, dtype):
