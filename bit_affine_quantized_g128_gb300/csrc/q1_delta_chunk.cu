@@ -69,6 +69,13 @@ __device__ __forceinline__ int scale_exp(float mx) {
   return s > 100 ? 100 : s < -100 ? -100 : s;
 }
 
+// The e that brings the root of a sum of squares into [2^13, 2^15)
+__device__ __forceinline__ int root_exp(float ss) {
+  const int e = (int)((__float_as_uint(ss) >> 23) & 0xFF);
+  if (e == 0 || e == 255) return 0;
+  return 14 - ((e - 126) >> 1);
+}
+
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
@@ -133,12 +140,16 @@ __device__ __forceinline__ uint32_t half2_of(f2 v) {
 // their sum.
 constexpr int kPrepT = 128;
 
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
 struct PrepShared {
   float D[4][16][20];          // per warp: the diagonal block of A, then its inverse
   float rk[kC], rq[kC];        // factors of the fp16 rows: norm, scale and 2^-e
   float Gh[kC], Gl[kC];        // log2(e) G = Gh + Gl
   float beta[kC];
-  float size[2][4];            // largest key and query norms of each warp's rows
+  float size[4];               // largest key norms (warps 0, 1) and scaled query norms (2, 3)
   int te, bump;                // T's scale; what positive g add to the bounds' exponents
 };
 
@@ -190,10 +201,13 @@ __device__ __forceinline__ void pair_operand(const f2 (&c)[2][2], uint32_t (&h)[
 }
 
 template <typename T, int DK>
-__global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws) {
+__global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws) {
+  // bf16 outputs keep 8 bits: P and T enter P T as single fp16 values (2^-12
+  // relative each); for fp16 outputs as pairs
+  constexpr bool kPairP = std::is_same<T, __half>::value;
   constexpr int kKq = kC * DK * 2;  // bytes of a K or Q tile
   constexpr int kArea = 2 * kKq > 3 * kTile ? 2 * kKq : 3 * kTile;
-  __shared__ __align__(128) unsigned char area[kArea];  // K, Q tiles; later T high, P', T low
+  __shared__ __align__(128) unsigned char area[kArea];  // K, Q tiles; later T high, P', T low (as in the workspace)
   __shared__ PrepShared sh;
   unsigned char *kt = area, *qt = area + kKq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -226,8 +240,6 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
     for (int i = 0; i < NI; ++i)
       v[i] = tid / LPR + i * RPI < len ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(i * RPI) * stride)) : make_uint4(0, 0, 0, 0);
     unsigned char *tile = which ? qt : kt;
-    unsigned char *out = ws.kq + ((place * a.HK + hk) * 2 + which) * (int64_t)kKq;
-    float big = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = tid / LPR + i * RPI;
@@ -240,28 +252,34 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
       ss += sy;
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float norm = sqrtf(ss);
-      const int e = scale_exp(norm);
+      const int e = root_exp(ss);
       const f2 sc = pk(pow2f(e), pow2f(e));
       uint4 h;
       h.x = half2_of(mul2(f[0], sc));
       h.y = half2_of(mul2(f[1], sc));
       h.z = half2_of(mul2(f[2], sc));
       h.w = half2_of(mul2(f[3], sc));
-      const uint32_t at = (uint32_t)(piece >> 3) * (kC * 128) + swz(r, piece & 7);
-      *reinterpret_cast<uint4 *>(tile + at) = h;
-      *reinterpret_cast<uint4 *>(out + at) = h;
-      if (piece == 0) {
-        const float n = (a.l2norm ? 1.f / sqrtf(ss + kDeltaEps) : 1.f) * (which ? a.scale : 1.f);
-        (which ? sh.rq : sh.rk)[r] = n * pow2f(-e);
-        big = fmaxf(big, fabsf(n) * norm);
-      }
+      *reinterpret_cast<uint4 *>(tile + (uint32_t)(piece >> 3) * (kC * 128) + swz(r, piece & 7)) = h;
+      if (piece == 0) (which ? sh.rq : sh.rk)[r] = ss;
     }
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
-    if (LPR == 8) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
-    if (lane == 0) sh.size[which][warp] = big;
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
+  if (tid == 0) {
+    bulk_store(ws.kq + (place * a.HK + hk) * (int64_t)(2 * kKq), smem_u32(area), 2 * kKq);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+  {  // the rows' factors, a thread per row: keys by warps 0 and 1, queries by 2 and 3
+    const int which = tid >> 6;
+    float &slot = (which ? sh.rq : sh.rk)[tid & 63];
+    const float ss = slot;
+    const float n = (a.l2norm ? 1.f / sqrtf(ss + kDeltaEps) : 1.f) * (which ? a.scale : 1.f);
+    slot = n * pow2f(-root_exp(ss));
+    float size = fabsf(n) * sqrtf(ss);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
+    if (lane == 0) sh.size[warp] = size;
+  }
 
   // ---- K K^T and Q K^T, columns up to this warp's rows
   float kk[4][2][4] = {}, qk[4][2][4] = {};
@@ -285,10 +303,9 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
         mma16(qk[j][1], aq, b[2], b[3]);
       }
   }
-  const float kn = fmaxf(fmaxf(sh.size[0][0], sh.size[0][1]), fmaxf(sh.size[0][2], sh.size[0][3]));
-  const float qn = fmaxf(fmaxf(sh.size[1][0], sh.size[1][1]), fmaxf(sh.size[1][2], sh.size[1][3]));
-  const int pe0 = scale_exp(kn * qn) - 6;  // 2^pe0 kn qn in [2^8, 2^9)
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncthreads();  // the tiles' area is free
+  const int pe0 = scale_exp(fmaxf(sh.size[0], sh.size[1]) * fmaxf(sh.size[2], sh.size[3])) - 6;  // 2^pe0 |k| |q| below 2^9
   const uint32_t th = smem_u32(area), pt = th + kTile, tl = th + 2 * kTile;
   // the blocks above the diagonal stay zero
   for (int i = tid; i < 3 * kTile / 16; i += kPrepT) reinterpret_cast<uint4 *>(area)[i] = make_uint4(0, 0, 0, 0);
@@ -366,7 +383,8 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
     __syncthreads();
     const float ts = pow2f(sh.te), ps = pow2f(pe0 - sh.bump);
     // ---- A and P in place of the products' fragments
-    f2 A[4][2][2], P[4][2][2];
+    f2 A[4][2][2];
+    uint32_t Ph[4][4], Pl[kPairP ? 4 : 1][4];
     {
       const int i0 = 16 * warp + fr;
       const f2 gh[2] = {pk(sh.Gh[i0], sh.Gh[i0]), pk(sh.Gh[i0 + 8], sh.Gh[i0 + 8])};
@@ -399,7 +417,8 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
                 *reinterpret_cast<float2 *>(&sh.D[warp][i][cc]) = make_float2(av.a, av.b);
               }
               A[j][n][e] = av;
-              P[j][n][e] = pv;
+              if constexpr (kPairP) split2(pv.a, pv.b, Ph[j][2 * n + e], Pl[j][2 * n + e]);
+              else Ph[j][2 * n + e] = half2_of(pv);
             }
           }
         }
@@ -467,27 +486,26 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
         pair_operand(y, yh[m], yl[m]);
       }
     // the operand pair of block (m, c) of T, as rows along the contraction
-    auto t_block = [&](int m, int c, uint32_t (&bh)[4], uint32_t (&bl)[4]) {
+    auto t_block = [&](int m, int c, uint32_t (&bh)[4], uint32_t (&bl)[4], bool low) {
       const uint32_t at = swz(16 * m + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * c + (lane >> 4));
       ldsm4t(th + at, bh);
-      ldsm4t(tl + at, bl);
+      if (low) ldsm4t(tl + at, bl);
     };
     // ---- T, block row after block row; P' gathers as the rows come
     float tv[3][2][4] = {}, pp[4][2][4] = {};
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       __syncthreads();  // block row m is complete
-      uint32_t ph[4], pl[4];
-      if (m <= warp) pair_operand(P[m], ph, pl);
 #pragma unroll
       for (int c = 0; c <= m; ++c)
         if (m <= warp) {
           uint32_t bh[4], bl[4];
-          t_block(m, c, bh, bl);
+          t_block(m, c, bh, bl, kPairP || m < warp);
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             if (m < 3 && m < warp) mma3(tv[c < 3 ? c : 0][n], yh[m < 3 ? m : 0], yl[m < 3 ? m : 0], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
-            mma3(pp[c][n], ph, pl, bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
+            if constexpr (kPairP) mma3(pp[c][n], Ph[m], Pl[m], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
+            else mma16(pp[c][n], Ph[m], bh[2 * n], bh[2 * n + 1]);
           }
         }
       if (m + 1 == warp) {  // this warp's block row is next
@@ -517,12 +535,15 @@ __global__ void __launch_bounds__(kPrepT, 3) delta_prep_kernel(const DeltaView a
             put(word_at(pt, 16 * warp + fr + 8 * e, 2 * c + n),
                 half2_bits(pp[c][n][2 * e] * (1.f / 512.f), pp[c][n][2 * e + 1] * (1.f / 512.f)));
       }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    uint4 *dst = reinterpret_cast<uint4 *>(ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile));
-#pragma unroll
-    for (int i = 0; i < 3 * kTile / 16 / kPrepT; ++i) dst[tid + i * kPrepT] = reinterpret_cast<const uint4 *>(area)[tid + i * kPrepT];
-    __syncthreads();
+    if (tid == 0) {
+      bulk_store(ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile), th, 3 * kTile);
+      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    // the next head's first barrier (after its gates) holds back its stores into the tiles
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ======================================================================
