@@ -6,7 +6,7 @@
 //   S_t = S~ + k_t d_t^T,   o_t = scale S_t^T q_t
 // Both reductions over DK run on the state as it was before the token:
 //   S~^T k = alpha (S^T k),   S_t^T q = alpha (S^T q) + (k . q) d_t,
-// so one pass over the state, and one block reduction, serve a token.  The
+// so one pass over the state, and one reduction, serve a token.  The
 // norms of k and q are sums over DK too and join the same reduction: the raw
 // rows are used, and their scales multiply the reduced values.
 #include <cuda_bf16.h>
@@ -16,14 +16,17 @@
 namespace q1 {
 namespace {
 
-// One CTA: 32 columns (DV) of one head's state.  Thread (group, quad): rows
-// group*R .. group*R+R-1 of the state (16 groups over DK), columns
-// 4*quad .. 4*quad+3, held in registers over the tokens.  A warp's load of the
-// state covers 4 rows x 128 bytes.  The slice of 32 columns gives 4 CTAs per
-// 128-wide head, so that one sequence of 32 heads spreads over 128 SMs.
-constexpr int kStepThreads = 128;
+// A warp owns 16 columns (DV) of one head's state and keeps them in registers
+// over the tokens: lane (group, quad) holds rows group*R .. group*R+R-1 of 8
+// groups over DK and columns 4*quad .. 4*quad+3 (64 values at DK = 128), so the
+// reductions over DK are three shuffle levels and no warp waits for another.
+// The state is kept as S = Gamma St, with Gamma the product of the decays since
+// it was last folded in: a token then costs one multiply-add per state value
+// for the update, as for each of the two reductions.  CTAs are two warps (32
+// columns), so that one sequence of 32 heads spreads over 128 SMs.
+constexpr int kStepThreads = 64;
 constexpr int kStepCols = 32;
-constexpr int kStepGroups = kStepThreads / (kStepCols / 4);  // 16
+constexpr int kStepGroups = 8;
 
 template <typename T>
 __device__ __forceinline__ float widen(T x);
@@ -67,19 +70,13 @@ struct Raw {
   }
 };
 
-struct StepShared {
-  float kv[2][kStepThreads / 32][kStepCols];
-  float qv[2][kStepThreads / 32][kStepCols];
-  float dot[2][kStepThreads / 32][4];  // k.k, q.q, k.q
-};
-
 template <typename T, int DK>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaView a) {
   constexpr int R = DK / kStepGroups;  // state rows per thread
-  __shared__ StepShared sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quad = lane & 7, group = warp * 4 + (lane >> 3);
-  const int h = blockIdx.y, b = blockIdx.x, col = blockIdx.z * kStepCols + 4 * quad;
+  constexpr int P = R / 4;             // of them, the rows of this lane's share of the products of k and q
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = lane & 3, group = lane >> 2;
+  const int h = blockIdx.y, b = blockIdx.x, col = blockIdx.z * kStepCols + 16 * warp + 4 * quad;
   const int hk = h / (a.HV / a.HK);
   int64_t t0, t1;
   a.range(b, t0, t1);
@@ -97,6 +94,7 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaVie
 #pragma unroll
     for (int r = 0; r < R; ++r) S[r][0] = S[r][1] = S[r][2] = S[r][3] = 0.f;
   }
+  float gamma = 1.f;  // the state is gamma * S
   const T *qp = static_cast<const T *>(a.q) + (int64_t)hk * DK + group * R;
   const T *kp = static_cast<const T *>(a.k) + (int64_t)hk * DK + group * R;
   const T *vp = static_cast<const T *>(a.v) + (int64_t)h * a.DV + col;
@@ -113,81 +111,88 @@ __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(const DeltaVie
   };
   if (t0 < t1) fetch(t0);
   for (int64_t t = t0; t < t1; ++t) {
-    const int par = (int)(t - t0) & 1;  // two reduction buffers: one barrier per token
     float q[R], k[R], v[4];
     qr.get(q);
     kr.get(k);
     vr.get(v);
     const float alpha = expf(gr), beta = br;
     if (t + 1 < t1) fetch(t + 1);
-    float kv[4] = {0.f, 0.f, 0.f, 0.f}, qv[4] = {0.f, 0.f, 0.f, 0.f}, kk = 0.f, qq = 0.f, kq = 0.f;
+    float kv[4] = {0.f, 0.f, 0.f, 0.f}, qv[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         kv[c] = fmaf(k[r], S[r][c], kv[c]);
         qv[c] = fmaf(q[r], S[r][c], qv[c]);
       }
-      kk = fmaf(k[r], k[r], kk);
-      qq = fmaf(q[r], q[r], qq);
-      kq = fmaf(k[r], q[r], kq);
+    // k.k, q.q and k.q: the four lanes of a group take a quarter of its rows each
+    float kk = 0.f, qq = 0.f, kq = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      float x = k[j], y = q[j];
+#pragma unroll
+      for (int c = 1; c < 4; ++c) {
+        x = quad == c ? k[c * P + j] : x;
+        y = quad == c ? q[c * P + j] : y;
+      }
+      kk = fmaf(x, x, kk);
+      qq = fmaf(y, y, qq);
+      kq = fmaf(x, y, kq);
     }
 #pragma unroll
-    for (int o = 8; o <= 16; o <<= 1) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        kv[c] += __shfl_xor_sync(0xffffffffu, kv[c], o);
-        qv[c] += __shfl_xor_sync(0xffffffffu, qv[c], o);
-      }
+    for (int o = 1; o <= 16; o <<= 1) {
       kk += __shfl_xor_sync(0xffffffffu, kk, o);
       qq += __shfl_xor_sync(0xffffffffu, qq, o);
       kq += __shfl_xor_sync(0xffffffffu, kq, o);
-    }
-    if (lane < 8) {
-      *reinterpret_cast<float4 *>(&sh.kv[par][warp][4 * quad]) = make_float4(kv[0], kv[1], kv[2], kv[3]);
-      *reinterpret_cast<float4 *>(&sh.qv[par][warp][4 * quad]) = make_float4(qv[0], qv[1], qv[2], qv[3]);
-      if (lane == 0) *reinterpret_cast<float4 *>(&sh.dot[par][warp][0]) = make_float4(kk, qq, kq, 0.f);
-    }
-    __syncthreads();
-    kk = qq = kq = 0.f;
+      if (o >= 4) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) kv[c] = qv[c] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kStepThreads / 32; ++w) {
-      const float4 x = *reinterpret_cast<const float4 *>(&sh.kv[par][w][4 * quad]);
-      const float4 y = *reinterpret_cast<const float4 *>(&sh.qv[par][w][4 * quad]);
-      const float4 z = *reinterpret_cast<const float4 *>(&sh.dot[par][w][0]);
-      kv[0] += x.x, kv[1] += x.y, kv[2] += x.z, kv[3] += x.w;
-      qv[0] += y.x, qv[1] += y.y, qv[2] += y.z, qv[3] += y.w;
-      kk += z.x, qq += z.y, kq += z.z;
+        for (int c = 0; c < 4; ++c) {
+          kv[c] += __shfl_xor_sync(0xffffffffu, kv[c], o);
+          qv[c] += __shfl_xor_sync(0xffffffffu, qv[c], o);
+        }
+      }
     }
-    const float rk = a.l2norm ? 1.f / sqrtf(kk + kDeltaEps) : 1.f;
-    const float rq = a.l2norm ? 1.f / sqrtf(qq + kDeltaEps) : 1.f;
+    const float rk = a.l2norm ? rsqrtf(kk + kDeltaEps) : 1.f;
+    const float rq = a.l2norm ? rsqrtf(qq + kDeltaEps) : 1.f;
+    // S~^T k and S~^T q carry the decay of this token too
+    float next = gamma * alpha;
     float d[4], out[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      d[c] = beta * (v[c] - alpha * (rk * kv[c]));
-      out[c] = a.scale * rq * fmaf(alpha, qv[c], rk * kq * d[c]);
-      d[c] *= rk;
+      d[c] = beta * (v[c] - next * (rk * kv[c]));
+      out[c] = a.scale * rq * fmaf(next, qv[c], rk * kq * d[c]);
     }
+    // fold Gamma in before its reciprocal, or what it multiplies, can leave fp32
+    if (!(next >= 9.5367431640625e-7f && next <= 1048576.f)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[r][c] *= next;
+      next = 1.f;
+    }
+    const float w = rk / next;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) d[c] *= w;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) S[r][c] = fmaf(alpha, S[r][c], k[r] * d[c]);
+      for (int c = 0; c < 4; ++c) S[r][c] = fmaf(k[r], d[c], S[r][c]);
+    gamma = next;
     if (group == 0) {
       T *dst = op + t * a.o_stride;
-      Raw<T, 4> w;
-      T *e = reinterpret_cast<T *>(w.w);
+      Raw<T, 4> o4;
+      T *e = reinterpret_cast<T *>(o4.w);
 #pragma unroll
       for (int c = 0; c < 4; ++c) e[c] = narrow<T>(out[c]);
 #pragma unroll
-      for (int i = 0; i < Raw<T, 4>::kWords; ++i) reinterpret_cast<uint2 *>(dst)[i] = w.w[i];
+      for (int i = 0; i < Raw<T, 4>::kWords; ++i) reinterpret_cast<uint2 *>(dst)[i] = o4.w[i];
     }
   }
   if (have) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      *reinterpret_cast<float4 *>(state + (int64_t)r * a.DV) = make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
+      *reinterpret_cast<float4 *>(state + (int64_t)r * a.DV) =
+          make_float4(gamma * S[r][0], gamma * S[r][1], gamma * S[r][2], gamma * S[r][3]);
   }
 }
 

@@ -1,7 +1,7 @@
 // Sampling: one token per row of logits from a given uniform number, with
 // temperature, top-k, top-p and min-p.
 //
-// A cluster of 8 CTAs takes one row.  Each CTA reads its slice of the row
+// A cluster of 1 to 8 CTAs takes one row.  Each CTA reads its slice of the row
 // once, into shared memory; everything after that (maximum, weights, the
 // truncations' thresholds, the draw) runs on chip, and the CTAs exchange a few
 // words through distributed shared memory.
@@ -10,10 +10,16 @@
 // V weights, and with tens of thousands of small weights an fp32 sum is off by
 // more than one of them.  The weights are therefore fixed-point integers,
 // w = 2^44 exp((l - max) / temperature), relative error about 2^-34: integer
-// sums are exact and the same in any order (so shared-memory atomics and any
-// split over threads give one answer).  The tokens are ordered by the 64-bit
-// value (order-preserving bits of l, ~index), so "before" is one compare and
-// ties fall to the lowest index.
+// sums are exact and the same in any order (so atomics and any split over
+// threads give one answer).  The tokens are ordered by the 64-bit value
+// (order-preserving bits of l, ~index), so "before" is one compare and ties
+// fall to the lowest index.
+//
+// Truncations.  One pass counts the tokens by log2(weight) in bins 1.6 % wide;
+// counts alone (32-bit atomics, no weights) give the bin in which top-k ends
+// and, since a bin's weights lie between its edges, the few bins in which
+// top-p must end.  A second pass sums the exact weights above those bins in
+// registers and collects their tokens, which are sorted.
 #include <cuda_bf16.h>
 
 #include "q1_internal.h"
@@ -23,9 +29,10 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-constexpr int kBins = 2 * kThreads;  // histogram over log2(weight), two bins per thread when scanned
-constexpr int kList = 2048;          // a bin of at most this many tokens is sorted; a fuller one is bisected
+constexpr int kMaxCluster = 8;
+constexpr int kPer = 4;              // histogram bins per thread when scanned
+constexpr int kBins = kPer * kThreads;
+constexpr int kList = 2048;          // at most this many tokens are sorted; a fuller bin is bisected
 constexpr int kFrac = 44;            // fractional bits of a weight
 constexpr float kRange = 46.f;       // log2 range of the histogram: below it a weight rounds to zero
 
@@ -54,37 +61,34 @@ __device__ const Exp2Table g_exp2 = make_table();
 
 struct alignas(16) SampleShared {
   float2 exp2[1024];
-  u64 sum[kBins];
-  u64 list[kList];
+  union {                      // rank 0:
+    u64 list[kList];           // the collected tokens, or
+    u64 sum[kBins];            // weights of the bins in question, where they hold too many tokens to sort
+  };
   unsigned int cnt[kBins];
   // written by the CTAs of the cluster (index: their rank)
-  u64 part_sum[2][kCluster];
-  float part_max[kCluster];
-  int part_idx[kCluster];
-  // written by rank 0 into every CTA; [0] for top-k, [1] for top-p (a slot of
-  // its own each: a CTA may read the first after rank 0 has begun the second)
+  u64 part_sum[2][kMaxCluster];
+  float part_max[kMaxCluster];
+  int part_idx[kMaxCluster];
+  // written by rank 0 into every CTA, a slot per stage (a CTA may read one after
+  // rank 0 has begun the next): 0 top-k, 1 top-p's bins, 2 top-p's one bin
   struct Find {
-    u64 need;             // the count (top-k) or weight (top-p) wanted from the bin
-    int bin;              // the bin to resolve, -1: none
-    unsigned int in_bin;  // tokens in it
-  } find[2];
-  u64 threshold;          // tokens with a smaller order value are not kept
+    int lo, hi;                // the bins in question, lo > hi: none
+    int many;                  // they hold more than kList tokens
+    u64 need;                  // the count (top-k) or weight wanted
+  } find[3];
+  u64 threshold;               // tokens with a smaller order value are not kept
   // this CTA's own
   unsigned int list_n;
   u64 warp_sum[kWarps], warp_cnt[kWarps];
   float warp_max[kWarps];
   int warp_idx[kWarps];
   u64 found, found_sum;
-  float c_hi, c_lo;     // log2(e) / temperature
+  int pick[2];
+  float c_hi, c_lo;            // log2(e) / temperature
   u64 w_min;
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ uint32_t rank_in_cluster() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 // The generic address of p's counterpart in CTA `rank` of the cluster.
 template <typename P>
 __device__ __forceinline__ P *peer(P *p, uint32_t rank) {
@@ -92,11 +96,9 @@ __device__ __forceinline__ P *peer(P *p, uint32_t rank) {
   asm volatile("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"((u64)p), "r"(rank));
   return reinterpret_cast<P *>(out);
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
-  cluster_wait();
+__device__ __forceinline__ void cluster_sync(int cs) {
+  if (cs == 1) __syncthreads();
+  else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -122,6 +124,17 @@ __device__ __forceinline__ float order_logit(u64 v) {
   return __uint_as_float((key & 0x80000000u) ? (key ^ 0x80000000u) : ~key);
 }
 
+// A weight 2^44 w as hi 2^22 + lo: two 32-bit sums per thread instead of one of 64 bits
+struct Weight {
+  uint32_t hi;
+  int32_t lo;
+  __device__ __forceinline__ u64 whole() const { return ((u64)hi << 22) + (u64)(long long)lo; }
+  __device__ __forceinline__ void add(const Weight &w) {
+    hi += w.hi;
+    lo += w.lo;
+  }
+};
+
 struct RowScale {
   float m, c_hi, c_lo;
   const float2 *exp2;
@@ -131,28 +144,31 @@ struct RowScale {
     return (l - m) * c_hi;
   }
   __device__ __forceinline__ int bin(float y) const { return min(kBins - 1, (int)(-y * ((float)kBins / kRange))); }
-  // 2^44 exp((l - m) / temperature) as an integer; y = log2w(l)
-  __device__ __forceinline__ u64 weight(float l, float y) const {
-    if (!(y > -kRange)) return 0;
-    float lo = 0.f;
-    if (l != m) {
-      // l - m = s + e exactly (two-sum), times c_hi + c_lo
-      const float s = l - m, bb = s - l;
-      const float e = (l - (s - bb)) - (m + bb);
-      lo = fmaf(s, c_hi, -y) + fmaf(s, c_lo, e * c_hi);
-    }
-    const float t = rintf(y * 1024.f);
-    const float r = fmaf(t, -1.f / 1024.f, y) + lo;  // |r| <= 2^-11; the difference is exact
+  // 2^44 exp((l - m) / temperature) as an integer, for y = log2w(l) > -kRange.
+  // Adding 1.5 * 2^23 to a number below 2^22 leaves its nearest integer in the
+  // low bits of the sum.
+  __device__ __forceinline__ Weight weight(float l, float y) const {
+    if (y == 0.f) return Weight{1u << 22, 0};
+    constexpr float kMagic = 12582912.f;
+    constexpr int kMagicBits = 0x4B400000;
+    // l - m = s + e exactly (two-sum), times c_hi + c_lo = y + lo
+    const float s = l - m, bb = s - l;
+    const float e = (l - (s - bb)) - (m + bb);
+    const float lo = fmaf(s, c_hi, -y) + fmaf(s, c_lo, e * c_hi);
+    const float t = fmaf(y, 1024.f, kMagic);
+    const int tb = __float_as_int(t);                       // 2^y = 2^n 2^(i/1024) 2^r
+    const float r = fmaf(t - kMagic, -1.f / 1024.f, y) + lo;  // |r| <= 2^-11; the difference is exact
     const float p = r * 0.693147180559945f;
     const float x = fmaf(p * p, fmaf(p, 1.f / 6.f, 0.5f), p);  // e^p - 1
-    const int ti = (int)t, i = ti & 1023, n = ti >> 10;      // n <= 0
-    const float2 h = exp2[i];
-    // 2^(i/1024) e^p with 40 fractional bits: hi's 24-bit significand plus a small correction
-    const long long mant = (long long)((__float_as_uint(h.x) & 0x7FFFFFu) | 0x800000u) << 17;
-    const long long v = mant + (long long)__float2int_rn(fmaf(h.x, x, h.y) * 1099511627776.f);
-    const int sh = n + (kFrac - 40);
-    if (sh >= 0) return (u64)v << sh;
-    return ((u64)v + (1ull << (-sh - 1))) >> -sh;
+    const float2 h = exp2[tb & 1023];
+    const int n = (tb - kMagicBits) >> 10;                  // -46 .. 0
+    const float scale = __int_as_float((n + 127 + 22) << 23);
+    const float v = h.x * scale;                            // exact
+    const float c = fmaf(h.x, x, h.y);
+    const float t1 = fmaf(c, scale, v) + kMagic;
+    const float rem = fmaf(c, scale, v - (t1 - kMagic));    // at most 3/4; one rounding
+    const float t2 = fmaf(rem, 4194304.f, kMagic);
+    return Weight{(uint32_t)(__float_as_int(t1) - kMagicBits), __float_as_int(t2) - kMagicBits};
   }
 };
 
@@ -170,28 +186,34 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
   }
   return v;
 }
-// exclusive prefix sums of (c, s) over the block's threads, and the totals
-__device__ __forceinline__ void block_scan(SampleShared &sh, u64 &c, u64 &s, u64 &c_all, u64 &s_all) {
+// exclusive prefix sum over the block's threads, and the total
+__device__ __forceinline__ u64 block_scan(u64 *scratch, u64 v, u64 &all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const u64 ci = warp_scan(c, lane), si = warp_scan(s, lane);
+  const u64 incl = warp_scan(v, lane);
   __syncthreads();
-  if (lane == 31) {
-    sh.warp_cnt[warp] = ci;
-    sh.warp_sum[warp] = si;
-  }
+  if (lane == 31) scratch[warp] = incl;
   __syncthreads();
-  u64 cb = 0, sb = 0;
-  c_all = s_all = 0;
+  u64 before = 0;
+  all = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) {
-      cb += sh.warp_cnt[w];
-      sb += sh.warp_sum[w];
-    }
-    c_all += sh.warp_cnt[w];
-    s_all += sh.warp_sum[w];
+    const u64 x = scratch[w];
+    if (w < warp) before += x;
+    all += x;
   }
-  c = cb + ci - c;
-  s = sb + si - s;
+  return before + incl - v;
+}
+// This CTA's sum of v, written to slot `rank` of part_sum[par] in CTA `to`, or in all (to < 0)
+__device__ __forceinline__ void send_sum(SampleShared &sh, u64 v, int par, uint32_t rank, int cs, int to) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) sh.warp_sum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if ((int)threadIdx.x < cs && (to < 0 || to == (int)threadIdx.x)) {
+    u64 all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) all += sh.warp_sum[w];
+    *peer(&sh.part_sum[par][rank], threadIdx.x) = all;
+  }
 }
 
 // floor(x 2^64) for x in [0, 1)
@@ -221,134 +243,100 @@ struct Slice {
   }
 };
 
-// The last token kept in the bin sh.find[by_sum].bin, found by the whole
-// cluster: with the bin's tokens in order, the need-th one (by_sum = 0), or the
-// first at which the weights of the bin reach need (by_sum = 1).  In rank 0, sh.found is its order
-// value and sh.found_sum the weight of the bin's tokens up to it.
-template <typename T>
-__device__ void resolve_bin(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, uint32_t rank,
-                            int by_sum) {
+// Rank 0, all threads: sorts the collected tokens and finds the last one kept:
+// the need-th (by_sum = 0), or the first at which their weights reach need.
+// sh.found is its order value, sh.found_sum the weight of the tokens up to it.
+__device__ void sort_and_find(SampleShared &sh, const RowScale &rs, int by_sum, u64 need) {
   const int tid = threadIdx.x;
-  const int bin = sh.find[by_sum].bin;
-  const u64 need = sh.find[by_sum].need;
-  if (sh.find[by_sum].in_bin <= kList) {
-    SampleShared *lead = peer(&sh, 0);
-    slice.each([&](float l, uint32_t idx) {
-      const float y = rs.log2w(l);
-      if (y > -kRange && rs.bin(y) == bin && rs.weight(l, y) != 0) {
-        const unsigned int at = atomicAdd(&lead->list_n, 1u);
-        if (at < kList) lead->list[at] = order_value(l, idx);
-      }
-    });
-    cluster_sync();
-    if (rank == 0) {
-      const int n = (int)min(sh.list_n, (unsigned int)kList);
-      int n2 = 1;
-      while (n2 < n) n2 <<= 1;
-      for (int i = n + tid; i < n2; i += kThreads) sh.list[i] = 0;
-      __syncthreads();
-      for (int size = 2; size <= n2; size <<= 1)
-        for (int step = size >> 1; step > 0; step >>= 1) {  // bitonic sort, descending
-          for (int i = tid; i < n2 / 2; i += kThreads) {
-            const int x = 2 * i - (i & (step - 1)), z = x + step;
-            const u64 p = sh.list[x], q = sh.list[z];
-            if ((p < q) == ((x & size) == 0)) {
-              sh.list[x] = q;
-              sh.list[z] = p;
-            }
-          }
-          __syncthreads();
-        }
-      constexpr int P = kList / kThreads;
-      u64 w[P], c = 0, s = 0, ca, sa;
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int at = tid * P + i;
-        w[i] = 0;
-        if (at < n) {
-          const float l = order_logit(sh.list[at]);
-          w[i] = rs.weight(l, rs.log2w(l));
-        }
-        s += w[i];
-      }
-      block_scan(sh, c, s, ca, sa);
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int at = tid * P + i;
-        const bool last = by_sum ? (s < need && need <= s + w[i]) : (u64)(at + 1) == need;
-        s += w[i];
-        if (at < n && last) {
-          sh.found = sh.list[at];
-          sh.found_sum = s;
+  const int n = (int)min(sh.list_n, (unsigned int)kList);
+  int n2 = 1;
+  while (n2 < n) n2 <<= 1;
+  for (int i = n + tid; i < n2; i += kThreads) sh.list[i] = 0;
+  __syncthreads();
+  for (int size = 2; size <= n2; size <<= 1)
+    for (int step = size >> 1; step > 0; step >>= 1) {  // bitonic sort, descending
+      for (int i = tid; i < n2 / 2; i += kThreads) {
+        const int x = 2 * i - (i & (step - 1)), z = x + step;
+        const u64 p = sh.list[x], q = sh.list[z];
+        if ((p < q) == ((x & size) == 0)) {
+          sh.list[x] = q;
+          sh.list[z] = p;
         }
       }
-      __syncthreads();
+      // up to step 32 a warp's pairs lie in 64 places of its own
+      if (step > 32 || (step == 1 && size > 32)) __syncthreads();
+      else __syncwarp();
     }
-    return;
+  constexpr int P = kList / kThreads;
+  u64 w[P], s = 0, all;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int at = tid * P + i;
+    w[i] = 0;
+    if (at < n) {
+      const float l = order_logit(sh.list[at]);
+      w[i] = rs.weight(l, rs.log2w(l)).whole();
+    }
+    s += w[i];
   }
-  // Bit by bit, the largest order value with enough tokens (or weight) at or
-  // above it.  Bits 31..18 are set in every value (indices are below 2^18).
+  s = block_scan(sh.warp_cnt, s, all);
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int at = tid * P + i;
+    const bool last = by_sum ? (s < need && need <= s + w[i]) : (u64)(at + 1) == need;
+    s += w[i];
+    if (at < n && last) {
+      sh.found = sh.list[at];
+      sh.found_sum = s;
+    }
+  }
+  __syncthreads();
+}
+
+// The whole cluster: the last token kept of a bin that holds too many to sort,
+// bit by bit: the largest order value with enough tokens (or weight) of the bin
+// at or above it.  Bits 31..18 are set in every value (indices are below 2^18).
+// In rank 0, sh.found and sh.found_sum as above.
+template <typename T>
+__device__ void bisect(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, uint32_t rank, int cs, int bin, int by_sum,
+                       u64 need) {
   u64 t = 0xFFFC0000ull;
   int par = 0;
-  for (int bit = 63; bit >= 0; --bit) {
+  for (int bit = 63; bit >= -1; --bit) {
     if (bit >= 18 && bit < 32) continue;
-    const u64 cand = t | (1ull << bit);
+    const u64 cand = bit >= 0 ? t | (1ull << bit) : t;  // the last round: the weight at or above t
     u64 acc = 0;
     slice.each([&](float l, uint32_t idx) {
       const float y = rs.log2w(l);
-      if (y > -kRange && rs.bin(y) == bin && order_value(l, idx) >= cand) {
-        const u64 w = rs.weight(l, y);
-        acc += by_sum ? w : (u64)(w != 0);
-      }
+      if (y > -kRange && rs.bin(y) == bin && order_value(l, idx) >= cand) acc += by_sum || bit < 0 ? rs.weight(l, y).whole() : 1ull;
     });
-    acc = warp_sum(acc);
-    if ((tid & 31) == 0) sh.warp_sum[tid >> 5] = acc;
-    __syncthreads();
-    if (tid < kCluster) {
-      u64 v = 0;
-      for (int w = 0; w < kWarps; ++w) v += sh.warp_sum[w];
-      *peer(&sh.part_sum[par][rank], (uint32_t)tid) = v;
-    }
-    cluster_sync();
+    send_sum(sh, acc, par, rank, cs, -1);
+    cluster_sync(cs);
     u64 all = 0;
-    for (int r = 0; r < kCluster; ++r) all += sh.part_sum[par][r];
-    if (all >= need) t = cand;
+    for (int r = 0; r < cs; ++r) all += sh.part_sum[par][r];
+    if (bit < 0) {
+      if (threadIdx.x == 0) {
+        sh.found = t;
+        sh.found_sum = all;
+      }
+    } else if (all >= need) {
+      t = cand;
+    }
     par ^= 1;
-  }
-  // the weight at or above t
-  u64 acc = 0;
-  slice.each([&](float l, uint32_t idx) {
-    const float y = rs.log2w(l);
-    if (y > -kRange && rs.bin(y) == bin && order_value(l, idx) >= t) acc += rs.weight(l, y);
-  });
-  acc = warp_sum(acc);
-  if ((tid & 31) == 0) sh.warp_sum[tid >> 5] = acc;
-  __syncthreads();
-  if (tid == 0) {
-    u64 v = 0;
-    for (int w = 0; w < kWarps; ++w) v += sh.warp_sum[w];
-    *peer(&sh.part_sum[par][rank], 0) = v;
-  }
-  cluster_sync();
-  if (rank == 0 && tid == 0) {
-    u64 v = 0;
-    for (int r = 0; r < kCluster; ++r) v += sh.part_sum[par][r];
-    sh.found = t;
-    sh.found_sum = v;
   }
   __syncthreads();
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const q1_sample_args a, int per) {
+__global__ void __launch_bounds__(kThreads) sample_kernel(const q1_sample_args a, int per, int cs) {
   extern __shared__ __align__(16) unsigned char dyn[];
   SampleShared &sh = *reinterpret_cast<SampleShared *>(dyn);
   T *data = reinterpret_cast<T *>(dyn + sizeof(SampleShared));
   constexpr int E = Slice<T>::E;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = rank_in_cluster();
-  const int64_t b = blockIdx.x / kCluster;
-  cluster_arrive();  // peers' shared memory may be written once all have arrived
+  const int64_t b = blockIdx.x / (unsigned)cs;
+  const uint32_t rank = blockIdx.x - (uint32_t)b * cs;
+  if (cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // peers may write once all have arrived
   const float temp = a.temperature ? a.temperature[b] : a.temperature_value;
   const int top_k = a.top_k ? a.top_k[b] : a.top_k_value;
   const float top_p = a.top_p ? a.top_p[b] : a.top_p_value;
@@ -376,10 +364,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const q1_sample_args a
 #pragma unroll
     for (int i = 0; i < E; ++i) mx = fmaxf(mx, to_f32(e[i]));  // a NaN is passed over
   }
-  for (int i = tid; i < 1024; i += kThreads) sh.exp2[i] = g_exp2.v[i];
-  for (int i = tid; i < kBins; i += kThreads) {
-    sh.sum[i] = 0;
-    sh.cnt[i] = 0;
+  if (!greedy)
+    for (int i = tid; i < 1024; i += kThreads) sh.exp2[i] = g_exp2.v[i];
+  if (has_k || has_p) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sh.cnt[tid + i * kThreads] = 0;
   }
   if (tid == 0) {
     // log2(e) / temperature in two fp32 parts, small enough to stay finite
@@ -395,16 +384,16 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const q1_sample_args a
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) sh.warp_max[warp] = mx;
   __syncthreads();
-  cluster_wait();
-  if (tid < kCluster) {
+  if (cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (tid < cs) {
     float m = sh.warp_max[0];
+#pragma unroll
     for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.warp_max[w]);
     *peer(&sh.part_max[rank], (uint32_t)tid) = m;
   }
-  cluster_sync();
+  cluster_sync(cs);
   float m = sh.part_max[0];
-#pragma unroll
-  for (int r = 1; r < kCluster; ++r) m = fmaxf(m, sh.part_max[r]);
+  for (int r = 1; r < cs; ++r) m = fmaxf(m, sh.part_max[r]);
   if (!(m > __int_as_float(0xff800000))) {  // nothing to keep
     if (rank == 0 && tid == 0) {
       a.token[b] = -1;
@@ -424,9 +413,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const q1_sample_args a
       for (int w = 1; w < kWarps; ++w) best = min(best, sh.warp_idx[w]);
       *peer(&sh.part_idx[rank], 0) = best;
     }
-    cluster_sync();
+    cluster_sync(cs);
     if (rank == 0 && tid == 0) {
-      for (int r = 0; r < kCluster; ++r) best = min(best, sh.part_idx[r]);
+      for (int r = 0; r < cs; ++r) best = min(best, sh.part_idx[r]);
       a.token[b] = best;
       if (a.prob) a.prob[b] = 1.f;
     }
@@ -434,104 +423,211 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const q1_sample_args a
   }
   const RowScale rs{m, sh.c_hi, sh.c_lo, sh.exp2};
 
-  // ---- the truncations' threshold: a histogram over log2(weight) finds the bin
-  // in which top-k ends, and then the bin in which top-p ends
+  // ---- the truncations' threshold
   if (has_k || has_p) {
+    Weight acc{0, 0};  // all weights, which top-p needs where top-k leaves all
+    const bool all = !has_k;
     slice.each([&](float l, uint32_t) {
       const float y = rs.log2w(l);
-      const u64 w = rs.weight(l, y);
-      if (w) {
-        const int i = rs.bin(y);
-        atomicAdd(&sh.cnt[i], 1u);
-        atomicAdd(&sh.sum[i], w);
+      if (y > -kRange) {
+        atomicAdd(&sh.cnt[rs.bin(y)], 1u);
+        if (all) acc.add(rs.weight(l, y));
       }
     });
-    cluster_sync();
-    u64 c2[2] = {0, 0}, s2[2] = {0, 0}, c_before = 0, s_before = 0, c_all = 0, s_all = 0;
-    if (rank == 0) {  // the cluster's histogram: two bins per thread
-      for (int r = 0; r < kCluster; ++r) {
-        const uint2 c = *reinterpret_cast<const uint2 *>(peer(&sh.cnt[2 * tid], (uint32_t)r));
-        const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(peer(&sh.sum[2 * tid], (uint32_t)r));
-        c2[0] += c.x, c2[1] += c.y;
-        s2[0] += s.x, s2[1] += s.y;
+    send_sum(sh, acc.whole(), 0, rank, cs, 0);
+    cluster_sync(cs);
+    // rank 0 holds the cluster's counts, kPer bins per thread, and their prefix
+    unsigned int c4[kPer] = {};
+    u64 c_before = 0, c_all = 0, total = 0, thr = 0;
+    if (rank == 0) {
+      for (int r = 0; r < cs; ++r) {
+        const uint4 c = *reinterpret_cast<const uint4 *>(peer(&sh.cnt[kPer * tid], (uint32_t)r));
+        c4[0] += c.x, c4[1] += c.y, c4[2] += c.z, c4[3] += c.w;
+        total += sh.part_sum[0][r];
       }
-      c_before = c2[0] + c2[1];
-      s_before = s2[0] + s2[1];
-      block_scan(sh, c_before, s_before, c_all, s_all);
+      c_before = block_scan(sh.warp_cnt, (u64)c4[0] + c4[1] + c4[2] + c4[3], c_all);
     }
-    u64 total = s_all, thr = 0;  // rank 0: the weight that top-k leaves
-    for (int stage = has_k ? 0 : 1; stage < (has_p ? 2 : 1); ++stage) {
+    auto announce = [&](int stage) {  // rank 0: its find[stage] to the others
+      __syncthreads();
+      if (tid >= 1 && tid < cs) peer(&sh, (uint32_t)tid)->find[stage] = sh.find[stage];
+    };
+    // the tokens of bins lo..hi to rank 0's list (or, with `many`, their weights
+    // by bin), and the weight of the bins above to its part_sum[1]
+    auto collect = [&](int stage) {
+      const auto f = sh.find[stage];
+      SampleShared *lead = peer(&sh, 0);
+      Weight above{0, 0};
+      slice.each([&](float l, uint32_t idx) {
+        const float y = rs.log2w(l);
+        if (!(y > -kRange)) return;
+        const int i = rs.bin(y);
+        if (i < f.lo) {
+          above.add(rs.weight(l, y));
+        } else if (i <= f.hi) {
+          if (f.many) {
+            atomicAdd(&lead->sum[i], rs.weight(l, y).whole());
+          } else {
+            const unsigned int at = atomicAdd(&lead->list_n, 1u);
+            if (at < kList) lead->list[at] = order_value(l, idx);
+          }
+        }
+      });
+      send_sum(sh, above.whole(), 1, rank, cs, 0);
+      cluster_sync(cs);
+    };
+    auto above_all = [&]() {
+      u64 v = 0;
+      for (int r = 0; r < cs; ++r) v += sh.part_sum[1][r];
+      return v;
+    };
+    if (has_k) {
       if (rank == 0) {
         if (tid == 0) {
-          sh.find[stage].bin = -1;
+          sh.find[0] = {1, 0, 0, 0};
           sh.list_n = 0;
         }
-        u64 want = (u64)top_k;
-        if (stage == 1) {
-          // kept: less than ceil(top_p * total) before it; the first always is
-          const u64 p = fraction(top_p);
-          want = __umul64hi(p, total) + (p * total != 0 ? 1 : 0);
-          want = want ? want : 1;
-        }
         __syncthreads();
-        u64 c = c_before, s = s_before;
+        u64 c = c_before;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const u64 x = stage ? s : c, dx = stage ? s2[i] : c2[i];
-          if (x < want && want <= x + dx) {
-            sh.find[stage] = {want - x, 2 * tid + i, (unsigned int)c2[i]};
-            sh.found_sum = s;  // the weight before the bin
-          }
-          c += c2[i];
-          s += s2[i];
+        for (int i = 0; i < kPer; ++i) {
+          if (c < (u64)top_k && (u64)top_k <= c + c4[i])
+            sh.find[0] = {kPer * tid + i, kPer * tid + i, c4[i] > kList, (u64)top_k - c};
+          c += c4[i];
         }
-        __syncthreads();
-        if (tid >= 1 && tid < kCluster) peer(&sh, (uint32_t)tid)->find[stage] = sh.find[stage];
+        announce(0);
       }
-      cluster_sync();
-      if (sh.find[stage].bin >= 0) {
-        const u64 before = sh.found_sum;
-        __syncthreads();
-        resolve_bin(sh, slice, rs, rank, stage);
+      cluster_sync(cs);
+      // a top_k beyond the tokens that have a weight keeps them all
+      if (sh.find[0].lo > sh.find[0].hi) {
+        if (has_p) {  // their weight, which the first pass did not sum
+          Weight w{0, 0};
+          slice.each([&](float l, uint32_t) {
+            const float y = rs.log2w(l);
+            if (y > -kRange) w.add(rs.weight(l, y));
+          });
+          send_sum(sh, w.whole(), 1, rank, cs, 0);
+          cluster_sync(cs);
+          if (rank == 0) total = above_all();
+        }
+      } else {
+        collect(0);
+        const u64 above = rank == 0 ? above_all() : 0;
+        if (sh.find[0].many) bisect(sh, slice, rs, rank, cs, sh.find[0].lo, 0, sh.find[0].need);
+        else if (rank == 0) sort_and_find(sh, rs, 0, sh.find[0].need);
         if (rank == 0) {
-          total = before + sh.found_sum;
-          thr = thr > sh.found ? thr : sh.found;
+          thr = sh.found;
+          total = above + sh.found_sum;
         }
       }
-      __syncthreads();
     }
-    if (rank == 0 && tid < kCluster) peer(&sh, (uint32_t)tid)->threshold = thr;
-    cluster_sync();
+    if (has_p) {
+      u64 want = 0;
+      if (rank == 0) {
+        // kept: less than ceil(top_p * total) before it; the first always is
+        const u64 p = fraction(top_p);
+        want = __umul64hi(p, total) + (p * total != 0 ? 1 : 0);
+        want = want ? want : 1;
+        // between the sums that the bins' upper and lower edges give (with a
+        // margin for the rounding of bins and weights) lies the end of top-p
+        constexpr float kStep = kRange / kBins;
+        const int k_bin = has_k && thr ? sh.find[0].hi : kBins - 1;
+        u64 up[kPer], dn[kPer], us = 0, ds = 0, any;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const float e = exp2f(44.f - kStep * (float)(kPer * tid + i));
+          up[i] = (u64)c4[i] * ((u64)(e * 1.0001f) + 1);
+          dn[i] = (u64)c4[i] * (u64)(e * (exp2f(-kStep) * 0.9999f));
+          us += up[i];
+          ds += dn[i];
+        }
+        us = block_scan(sh.warp_cnt, us, any);
+        ds = block_scan(sh.warp_cnt, ds, any);
+        if (tid == 0) {
+          sh.pick[0] = k_bin;
+          sh.pick[1] = k_bin;
+          sh.list_n = 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (us < want && want <= us + up[i]) atomicMin(&sh.pick[0], kPer * tid + i);
+          if (ds < want && want <= ds + dn[i]) atomicMin(&sh.pick[1], kPer * tid + i);
+          us += up[i];
+          ds += dn[i];
+        }
+        __syncthreads();
+        const int lo = sh.pick[0], hi = max(sh.pick[1], lo);
+        u64 in = 0, c_in;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) in += kPer * tid + i >= lo && kPer * tid + i <= hi ? c4[i] : 0;
+        block_scan(sh.warp_cnt, in, c_in);
+        if (tid == 0) sh.find[1] = {lo, hi, c_in > kList, want};
+        if (c_in > kList) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) sh.sum[tid + i * kThreads] = 0;
+        }
+        announce(1);
+      }
+      cluster_sync(cs);
+      collect(1);
+      u64 above = 0;
+      if (rank == 0) above = above_all();
+      if (!sh.find[1].many) {
+        if (rank == 0) sort_and_find(sh, rs, 1, want - above);
+      } else {
+        // their weights by bin tell the bin; then its tokens
+        if (rank == 0) {
+          u64 w4[kPer], s = 0, any;
+          const int lo = sh.find[1].lo, hi = sh.find[1].hi;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            w4[i] = kPer * tid + i >= lo && kPer * tid + i <= hi ? sh.sum[kPer * tid + i] : 0;
+            s += w4[i];
+          }
+          s = above + block_scan(sh.warp_cnt, s, any);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            if (s < want && want <= s + w4[i]) sh.find[2] = {kPer * tid + i, kPer * tid + i, c4[i] > kList, want - s};
+            s += w4[i];
+          }
+          if (tid == 0) sh.list_n = 0;
+          announce(2);
+        }
+        cluster_sync(cs);
+        if (sh.find[2].many) {
+          bisect(sh, slice, rs, rank, cs, sh.find[2].lo, 1, sh.find[2].need);
+        } else {
+          collect(2);
+          if (rank == 0) sort_and_find(sh, rs, 1, sh.find[2].need);
+        }
+      }
+      if (rank == 0) thr = thr > sh.found ? thr : sh.found;
+    }
+    if (rank == 0 && tid < cs) peer(&sh, (uint32_t)tid)->threshold = thr;
+    cluster_sync(cs);
   }
 
   // ---- the kept weight: warp w of a CTA sums a contiguous run of vectors
   const u64 thr = sh.threshold, w_min = sh.w_min;
   const int vw = ((slice.nv + kWarps - 1) / kWarps + 31) & ~31;
   const int v0 = warp * vw, v1 = min(slice.nv, v0 + vw);
-  auto kept = [&](float l, uint32_t idx) -> u64 {
+  auto kept = [&](float l, uint32_t idx) -> Weight {
     const float y = rs.log2w(l);
-    if (!(y > -kRange) || (thr && order_value(l, idx) < thr)) return 0;
-    const u64 w = rs.weight(l, y);
-    return w >= w_min ? w : 0;
+    if (!(y > -kRange) || (thr && order_value(l, idx) < thr)) return Weight{0, 0};
+    const Weight w = rs.weight(l, y);
+    return w_min && w.whole() < w_min ? Weight{0, 0} : w;
   };
-  u64 acc = 0;
+  Weight acc{0, 0};
   for (int j = v0 + lane; j < v1; j += 32) {
     float f[E];
     slice.get(j, f);
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc += kept(f[i], (uint32_t)(slice.first + j * E + i));
+    for (int i = 0; i < E; ++i) acc.add(kept(f[i], (uint32_t)(slice.first + j * E + i)));
   }
-  acc = warp_sum(acc);
-  if (lane == 0) sh.warp_sum[warp] = acc;
-  __syncthreads();
-  if (tid < kCluster) {
-    u64 v = 0;
-    for (int w = 0; w < kWarps; ++w) v += sh.warp_sum[w];
-    *peer(&sh.part_sum[0][rank], (uint32_t)tid) = v;
-  }
-  cluster_sync();
+  send_sum(sh, acc.whole(), 0, rank, cs, -1);
+  cluster_sync(cs);
   u64 total = 0, before = 0;
-  for (int r = 0; r < kCluster; ++r) {
+  for (int r = 0; r < cs; ++r) {
     if (r < (int)rank) before += sh.part_sum[0][r];
     total += sh.part_sum[0][r];
   }
@@ -548,7 +644,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const q1_sample_args a
     if (j < v1) slice.get(j, f);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      w[i] = j < v1 ? kept(f[i], (uint32_t)(slice.first + j * E + i)) : 0;
+      w[i] = j < v1 ? kept(f[i], (uint32_t)(slice.first + j * E + i)).whole() : 0;
       s += w[i];
     }
     const u64 incl = warp_scan(s, lane);
@@ -576,26 +672,29 @@ cudaError_t sample_t(const q1_sample_args &a, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   constexpr int E = Slice<T>::E;
   const int dev = current_device();
-  const int per = (int)((a.V + kCluster - 1) / kCluster + 7) & ~7;
-  const size_t smem = sizeof(SampleShared) + ((size_t)per + 2 * E) * sizeof(T);
+  constexpr size_t kMost = 227 * 1024;  // shared memory of a CTA
+  constexpr int64_t kSliceMax = (int64_t)((kMost - sizeof(SampleShared)) / sizeof(T)) - 2 * E - 8;
   if (not_done(ready, dev)) {
-    const size_t most = sizeof(SampleShared) + ((size_t)(1 << 18) / kCluster + 2 * E) * sizeof(T);
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
   }
+  // as many CTAs per row as keep two per SM busy, and as the row needs
+  int cs = kMaxCluster;
+  while (cs > 1 && a.B * cs > 2 * 152 && (a.V + cs / 2 - 1) / (cs / 2) <= kSliceMax) cs /= 2;
+  const int per = (int)((a.V + cs - 1) / cs + 7) & ~7;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.B * kCluster));
+  cfg.gridDim = dim3((unsigned)(a.B * cs));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = sizeof(SampleShared) + ((size_t)per + 2 * E) * sizeof(T);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kCluster;
+  attr.val.clusterDim.x = (unsigned)cs;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, per);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, per, cs);
 }
 
 }  // namespace

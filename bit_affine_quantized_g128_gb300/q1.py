@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -51,6 +52,8 @@ class _CLayer(ctypes.Structure):
     _fields_ = [("attn", _CWeight), ("gate", _CWeight), ("up", _CWeight), ("down", _CWeight)]
 
 
+# The argument structs of q1_gated_delta and q1_sample; `pack` builds one from
+# its fields in order (a quarter of the time that setting them one by one takes).
 class _CDelta(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "g", "beta", "state", "cu_seqlens", "slots",
                                                "fresh")] + \
@@ -58,6 +61,7 @@ class _CDelta(ctypes.Structure):
                                               "beta_stride", "T", "B", "n_slots", "max_len")] + \
                [(n, ctypes.c_int32) for n in ("HK", "HV", "DK", "DV", "dtype", "qk_l2norm")] + \
                [("scale", ctypes.c_float)]
+    pack = struct.Struct("@10P10q6if0q").pack
 
 
 class _CSample(ctypes.Structure):
@@ -66,6 +70,7 @@ class _CSample(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("B", "V", "row_stride")] + \
                [("dtype", ctypes.c_int32), ("top_k_value", ctypes.c_int32)] + \
                [(n, ctypes.c_float) for n in ("temperature_value", "top_p_value", "min_p_value")]
+    pack = struct.Struct("@8P3q2i3f0q").pack
 
 
 _lib = None
@@ -133,6 +138,21 @@ def _check(fn: str, status: int):
 
 def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _on_current_device(*tensors) -> bool:
+    """Whether all are CUDA tensors on the current device: the checks of _cuda at once."""
+    d = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    if d < 0:
+        return False
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.get_device() != d:
+            return False
+    return True
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -481,7 +501,8 @@ def _vector(t, name: str, n: int, dtype, device) -> Optional[torch.Tensor]:
     """An optional contiguous device vector of n elements of `dtype`."""
     if t is None:
         return None
-    _cuda(t, name, device, current=False)
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        _cuda(t, name, device, current=False)
     if t.dtype != dtype or t.numel() != n:
         raise ValueError(f"{name} must hold {n} elements of {dtype} (got {t.dtype}, {tuple(t.shape)})")
     return t if t.is_contiguous() else t.contiguous()
@@ -500,10 +521,11 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     assumed).  Without cu_seqlens, q, k, v [B, L, H, D] and g, beta [B, L, HV] are B sequences of L tokens.
     state fp32 [n_slots, HV, DK, DV]; slots int32 [B] names each sequence's entry (default: entry b; outside
     the pool: none), fresh int32 [B] marks those that start from zero.  scale defaults to DK ** -0.5."""
-    _cuda(q, "q")
+    if not _on_current_device(q, k, v, g, beta, state):
+        _cuda(q, "q")
+        for t, name in ((k, "k"), (v, "v"), (g, "g"), (beta, "beta"), (state, "state")):
+            _cuda(t, name, q.device, current=False)
     dev = q.device
-    for t, name in ((k, "k"), (v, "v"), (g, "g"), (beta, "beta"), (state, "state")):
-        _cuda(t, name, dev, current=False)
     dt = _x_dtype(q, "q")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError(f"q, k and v must have one dtype (got {q.dtype}, {k.dtype}, {v.dtype})")
@@ -543,20 +565,25 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
         g = g.contiguous()
     if beta.stride(1) != 1:
         beta = beta.contiguous()
-    o = _out(out, (T, HV, DV), q.dtype, dev)
-    a = _CDelta(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                state.data_ptr(), _ptr(cu_seqlens), _ptr(slots), _ptr(fresh), q.stride(0), k.stride(0), v.stride(0),
-                HV * DV, g.stride(0), beta.stride(0), T, B, state.shape[0], T if max_len is None else int(max_len),
-                HK, HV, DK, DV, dt, 1 if qk_l2norm else 0, DK ** -0.5 if scale is None else float(scale))
-    L = lib()
-    need = L.q1_gated_delta_workspace_size(a)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    o = torch.empty((T, HV, DV), dtype=q.dtype, device=dev) if out is None else _out(out, (T, HV, DV), q.dtype, dev)
+    a = _CDelta.from_buffer_copy(_CDelta.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(),
+        _ptr(cu_seqlens) or 0, _ptr(slots) or 0, _ptr(fresh) or 0, q.stride(0), k.stride(0), v.stride(0), HV * DV,
+        g.stride(0), beta.stride(0), T, B, state.shape[0], T if max_len is None else int(max_len), HK, HV, DK, DV, dt,
+        1 if qk_l2norm else 0, DK ** -0.5 if scale is None else float(scale)))
+    L, stream = _lib or lib(), _raw_stream(dev.index)
     if workspace is not None:
         _cuda(workspace, "workspace", dev)
-    wp, wn = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) if workspace is not None else (None, 0)
-    _check("q1_gated_delta", L.q1_gated_delta(a, wp, wn, _stream()))
-    return o.reshape(*lead, HV, DV)
+        st = L.q1_gated_delta(a, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    else:
+        st = L.q1_gated_delta(a, None, 0, stream)
+        if st == 6:  # Q1_ERR_WORKSPACE: the chunked form
+            n = L.q1_gated_delta_workspace_size(a)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            st = L.q1_gated_delta(a, workspace.data_ptr(), n, stream)
+    if st:
+        _check("q1_gated_delta", st)
+    return o if o.shape[:-2] == lead else o.reshape(*lead, HV, DV)
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None):
@@ -565,7 +592,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     Returns (token int32 [B], prob fp32 [B]).  temperature, top_k, top_p and min_p are off (None), a number
     for every row (taken as fp32; top_k int32), or a device tensor of B such elements.  Tokens rank by descending logit,
     equal logits by ascending index; temperature 0 takes the first.  See q1_sample in include/q1.h."""
-    _cuda(logits, "logits")
+    if not _on_current_device(logits):
+        _cuda(logits, "logits")
     dev = logits.device
     dt = _x_dtype(logits, "logits")
     if logits.dim() != 2:
@@ -582,17 +610,21 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     for val, name, dtype, off in ((temperature, "temperature", torch.float32, 1.0), (top_p, "top_p", torch.float32, 1.0),
                                   (min_p, "min_p", torch.float32, 0.0), (top_k, "top_k", torch.int32, 0)):
         if isinstance(val, torch.Tensor):
-            ptrs.append(_vector(val, name, B, dtype, dev))
+            val = _vector(val, name, B, dtype, dev)
+            ptrs.append(val)
             vals.append(off)
         else:
             ptrs.append(None)
             vals.append(off if val is None else val)
     token = torch.empty((B,), dtype=torch.int32, device=dev)
     prob = torch.empty((B,), dtype=torch.float32, device=dev)
-    a = _CSample(logits.data_ptr(), u.data_ptr(), *[_ptr(p) for p in ptrs], token.data_ptr(), prob.data_ptr(),
-                 B, V, logits.stride(0), dt, max(0, min(int(vals[3]), V)), float(vals[0]), float(vals[1]),
-                 float(vals[2]))
-    _check("q1_sample", lib().q1_sample(a, _stream()))
+    a = _CSample.from_buffer_copy(_CSample.pack(
+        logits.data_ptr(), u.data_ptr(), *[0 if p is None else p.data_ptr() for p in ptrs], token.data_ptr(),
+        prob.data_ptr(), B, V, logits.stride(0), dt, max(0, min(int(vals[3]), V)), float(vals[0]), float(vals[1]),
+        float(vals[2])))
+    st = (_lib or lib()).q1_sample(a, _raw_stream(dev.index))
+    if st:
+        _check("q1_sample", st)
     return token, prob
 
 
