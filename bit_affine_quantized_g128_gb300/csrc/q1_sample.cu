@@ -1,7 +1,7 @@
 // Sampling: one token per row of logits from a given uniform number, with
 // temperature, top-k, top-p and min-p.
 //
-// A cluster of 1 to 8 CTAs takes one row.  Each CTA reads its slice of the row
+// A cluster of 1 to 16 CTAs takes one row.  Each CTA reads its slice of the row
 // once, into shared memory; everything after that (maximum, weights, the
 // truncations' thresholds, the draw) runs on chip, and the CTAs exchange a few
 // words through distributed shared memory.
@@ -15,14 +15,19 @@
 // (order-preserving bits of l, ~index), so "before" is one compare and ties
 // fall to the lowest index.
 //
-// Truncations.  One pass makes a histogram over log2(weight), in bins of 1/32:
-// counts for top-k (no weights computed), counts and exact weights for top-p.
-// It gives the bin in which the kept tokens end, exactly.  If few tokens lie
-// down to that bin, they go to one CTA, which sorts them and does the rest
-// with that list.  Otherwise the tokens of that one bin are sorted for the
-// order value of the last kept token, and a pass over the row sums the kept
-// weights by warp, which leads to the token.
+// Truncations.  The end of top-k is found in rounds of 8 buckets of log2(weight)
+// (a row of buckets per thread, no atomics): with small k the first round ends
+// it.  The end of top-p takes one pass that counts the tokens in bins of 1/32
+// octave, one shared atomic per token (17 clocks of the SM per warp: as much as
+// its exact weight costs): since a bin's weights lie between its edges, the counts
+// give the few bins in which top-p must end.  Should those hold too many tokens,
+// rounds with fp32 weights narrow them.  If all tokens that can be kept are few,
+// one CTA finishes the row from a list of them; otherwise a pass with exact
+// weights sums those above the bins in question and lists the tokens in them,
+// which are sorted for the last one kept.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "q1_internal.h"
 
@@ -31,12 +36,17 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kOctaves = 46;         // range of log2(weight) in use: below it a weight rounds to zero
-constexpr int kPer = 3;              // histogram bins per thread when scanned
+constexpr int kRange = 1024 * kOctaves + 1;  // in steps of 1/1024
+constexpr int kPer = 3;              // bins per thread when scanned
 constexpr int kBins = kPer * kThreads;
-static_assert(kBins >= 32 * kOctaves, "bins");
-constexpr int kList = 1024;          // at most this many tokens are sorted; a fuller bin is bisected
+static_assert(32 * kBins >= kRange, "bins");
+constexpr int kBuckets = 8;          // of a search round
+constexpr int kFirstShift = 12;      // the first round's buckets are 4 octaves wide (the last takes the rest)
+constexpr float kMargin = 1e-4f;     // above the relative errors of the rounds' fp32 weights (5e-6) and sums (2e-5)
+constexpr int kList = 1024;          // at most this many tokens are sorted; a fuller bucket is bisected
+constexpr int kRuns = 8;             // a warp's tokens are summed in this many runs
 constexpr float kMagic = 12582912.f; // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
 constexpr int kMagicBits = 0x4B400000;
 constexpr float kDead = kMagic - 1024.f * kOctaves;  // keys below have no weight
@@ -76,36 +86,34 @@ struct RowScale {
 struct alignas(16) SampleShared {
   float2 exp2[1024];
   union {
-    struct {
-      unsigned int cnt[kBins];      // tokens per bin
-      unsigned int sum[3][kBins];   // their weights in pieces of 15 bits
-    } hist;
-    struct {                        // rank 0, once the histograms are read:
+    unsigned int count[kBins];
+    struct {                        // a search round: a row of buckets per thread
+      float sum[kBuckets][kThreads];
+      unsigned char cnt[kBuckets][kThreads];
+    } own;
+    struct {                        // rank 0, after the rounds
       u64 list[kList];              // collected tokens
-      u64 weight[kList];            // theirs, in order
+      u64 weight[kList];            // theirs
     } few;
   };
   // written by the CTAs of the cluster (index: their rank)
   u64 part_sum[2][kMaxCluster];
+  u64 part_rest[kMaxCluster];
   float part_max[kMaxCluster];
   int part_idx[kMaxCluster];
-  // written by rank 0 into every CTA, a slot per search (a CTA may read one
-  // after rank 0 has begun the next)
-  struct Find {
-    int lo, hi;                     // bins whose tokens are collected; lo > hi: nothing to find
-    int few;                        // all tokens that can be kept are among them
-    int many;                       // more than kList tokens
-    u64 need;                       // the count or weight wanted from bin hi
-  } find[2];
-  u64 threshold;                    // tokens with a smaller order value are not kept
+  float bucket_sum[2][kMaxCluster][kBuckets];
+  unsigned int bucket_cnt[2][kMaxCluster][kBuckets];
+  // written by rank 0 into every CTA
+  u64 threshold[2];                 // tokens with a smaller order value are not kept: by top-k, by top-p
   unsigned int list_n;              // rank 0: collected tokens
   // this CTA's own
   RowScale rs;
-  double c;
   u64 warp_sum[kWarps];
+  u64 run_sum[kWarps][kRuns];       // kept weight of a warp's runs of tokens
   float warp_max[kWarps];
   int warp_idx[kWarps];
   u64 found;
+  int pick[4];
 };
 
 // The generic address of p's counterpart in CTA `rank` of the cluster.
@@ -156,18 +164,19 @@ struct Weight {
 
 // kMagic + rint(1024 log2 w), monotone in l; below kDead, or NaN, where the
 // weight is zero.  (Infinite m: the infinities share the weight.)
+template <bool WIDE>
 __device__ __forceinline__ float key_of(const RowScale &rs, float l) {
-  if (!rs.wide) return fmaf(l, 1024.f * rs.c_hi, rs.K);
+  if (!WIDE) return fmaf(l, 1024.f * rs.c_hi, rs.K);
   if (l == rs.m) return kMagic;
   return fmaf(fmaxf((l - rs.m) * rs.c_hi, -1e6f), 1024.f, kMagic) - (l != l ? __int_as_float(0x7fc00000) : 0.f);
 }
-__device__ __forceinline__ int bin_of(float t) { return (kMagicBits - __float_as_int(t)) >> 5; }
 // 2^44 2^((l - m) c) as an integer, for t = key_of(l) >= kDead: with i + 1024 n =
 // t's integer, 2^n 2^(i/1024) 2^r, |r| <= 2^-11 and a little.
+template <bool WIDE>
 __device__ __forceinline__ Weight weight_of(const RowScale &rs, const float2 *exp2, float l, float t) {
   const float ti = t - kMagic;
   float r;
-  if (!rs.wide) {
+  if (!WIDE) {
     // l c_hi - (A0 + ti/1024): the bracket is exact, the difference rounded once
     r = fmaf(l, rs.c_hi, -fmaf(ti, 1.f / 1024.f, rs.A0));
     r = fmaf(l, rs.c_lo, r - rs.a1);
@@ -189,6 +198,13 @@ __device__ __forceinline__ Weight weight_of(const RowScale &rs, const float2 *ex
   const float rem = fmaf(c, scale, v - (t1 - kMagic));  // at most 3/4; one rounding
   const float t2 = fmaf(rem, 4194304.f, kMagic);
   return Weight{(uint32_t)(__float_as_int(t1) - kMagicBits), __float_as_int(t2) - kMagicBits};
+}
+
+// the same where the row's case is not known at compile time
+__device__ __forceinline__ float key_any(const RowScale &rs, float l) { return rs.wide ? key_of<true>(rs, l) : key_of<false>(rs, l); }
+__device__ __forceinline__ u64 weight_any(const RowScale &rs, const float2 *exp2, float l) {
+  return rs.wide ? weight_of<true>(rs, exp2, l, key_of<true>(rs, l)).whole()
+                 : weight_of<false>(rs, exp2, l, key_of<false>(rs, l)).whole();
 }
 
 __device__ __forceinline__ u64 warp_total(u64 v) {
@@ -255,30 +271,8 @@ struct Slice {
   static constexpr int E = 16 / (int)sizeof(T);
   const T *data;   // shared memory, vectors of 16 bytes; places outside the slice hold -inf
   int nv, first;   // vectors, and the row index of the first element of vector 0
-  __device__ __forceinline__ void get(int j, float (&f)[E]) const {
-    const uint4 v = reinterpret_cast<const uint4 *>(data)[j];
-    const T *e = reinterpret_cast<const T *>(&v);
-#pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = to_f32(e[i]);
-  }
-  // fn(logit, key, index) for the tokens with a key of at least t_min
-  template <typename F>
-  __device__ __forceinline__ void each(const RowScale &rs, float t_min, F fn) const {
-    for (int j = threadIdx.x; j < nv; j += kThreads) {
-      float f[E], t[E], most = -1e30f;
-      get(j, f);
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        t[i] = key_of(rs, f[i]);
-        most = fmaxf(most, t[i]);  // a NaN is passed over
-      }
-      if (most >= t_min) {
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (t[i] >= t_min) fn(f[i], t[i], (uint32_t)(first + j * E + i));
-      }
-    }
-  }
+  __device__ __forceinline__ float at(int j) const { return to_f32(data[j]); }
+  __device__ __forceinline__ int size() const { return nv * E; }
 };
 
 // Ascending (or descending) bitonic sort of n2 (a power of two) values in
@@ -319,7 +313,7 @@ __device__ void find_in_list(SampleShared &sh, const RowScale &rs, int by_sum, u
     w[i] = 0;
     if (at < n) {
       const float l = order_logit(sh.few.list[at]);
-      w[i] = weight_of(rs, sh.exp2, l, key_of(rs, l)).whole();
+      w[i] = weight_any(rs, sh.exp2, l);
     }
     s += w[i];
   }
@@ -349,7 +343,7 @@ __device__ void draw_from_list(SampleShared &sh, const RowScale &rs, int top_k, 
     w[i] = 0;
     if (at < n && (top_k <= 0 || at < top_k)) {
       const float l = order_logit(sh.few.list[at]);
-      w[i] = weight_of(rs, sh.exp2, l, key_of(rs, l)).whole();
+      w[i] = weight_any(rs, sh.exp2, l);
     }
     s += w[i];
   }
@@ -400,11 +394,88 @@ __device__ void draw_from_list(SampleShared &sh, const RowScale &rs, int top_k, 
   }
 }
 
-// The whole cluster: the last token kept of a bin that holds too many to sort,
-// bit by bit: the largest order value with enough tokens (or weight) of the bin
-// at or above it.  Bits 31..18 are set in every value (indices are below 2^18).
+// The same for a list of at most kShort tokens, without sorting: four threads
+// per token go through the list, once for what lies before it in the order, once
+// for what lies before it by index.
+constexpr int kShort = kThreads / 2;
+__device__ void draw_from_short_list(SampleShared &sh, const RowScale &rs, int top_k, float top_p, u64 want, float u,
+                                     int32_t *token, float *prob) {
+  const int tid = threadIdx.x, n = (int)sh.list_n, part = tid & 3;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const float l = order_logit(sh.few.list[i]);
+    sh.few.weight[i] = weight_any(rs, sh.exp2, l);
+  }
+  __syncthreads();
+  constexpr int R = kShort / (kThreads / 4);  // tokens per thread
+  u64 mine[R], w[R], before[R], s = 0, total;
+  int ahead[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = (tid >> 2) + r * (kThreads / 4);
+    before[r] = 0;
+    ahead[r] = 0;
+    mine[r] = i < n ? sh.few.list[i] : 0;
+    w[r] = i < n ? sh.few.weight[i] : 0;
+    if (i < n) {
+      for (int j = part; j < n; j += 4)
+        if (sh.few.list[j] > mine[r]) {
+          ++ahead[r];
+          before[r] += sh.few.weight[j];
+        }
+    }
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+      ahead[r] += __shfl_xor_sync(0xffffffffu, ahead[r], o);
+      before[r] += __shfl_xor_sync(0xffffffffu, before[r], o);
+    }
+    if (top_k > 0 && ahead[r] >= top_k) w[r] = 0;
+    if (part == 0) s += w[r];
+  }
+  if (top_p < 1.f) {
+    if (!want) {
+      block_scan(sh, s, total);
+      want = part_up(top_p, total);
+      want = want ? want : 1;
+    }
+  } else {
+    want = ~0ull;
+  }
+  s = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = (tid >> 2) + r * (kThreads / 4);
+    if (before[r] >= want || w[r] < rs.least) w[r] = 0;
+    if (part == 0) {
+      s += w[r];
+      if (i < n) sh.few.weight[i] = w[r];
+    }
+  }
+  block_scan(sh, s, total);  // its barriers publish the weights
+  const u64 target = draw_target(u, total);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = (tid >> 2) + r * (kThreads / 4);
+    u64 c = 0;
+    if (i < n) {
+      for (int j = part; j < n; j += 4)
+        if ((uint32_t)sh.few.list[j] > (uint32_t)mine[r]) c += sh.few.weight[j];  // ~index: larger is earlier
+    }
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if (i < n && part == 0 && target >= c && target - c < w[r]) {
+      *token = (int32_t)~(uint32_t)mine[r];
+      if (prob) *prob = (float)((double)w[r] / (double)total);
+    }
+  }
+}
+
+// The whole cluster, where too many tokens are left for a list: bit by bit, the
+// largest order value with enough tokens (or weight) at or above it.  Bits
+// 31..18 are set in every value (indices are below 2^18).
 template <typename T>
-__device__ u64 bisect(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, uint32_t rank, int cs, int bin, int by_sum,
+__device__ u64 bisect(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, uint32_t rank, int cs, u64 from, bool by_sum,
                       u64 need) {
   u64 t = 0xFFFC0000ull;
   int par = 0;
@@ -412,9 +483,11 @@ __device__ u64 bisect(SampleShared &sh, const Slice<T> &slice, const RowScale &r
     if (bit >= 18 && bit < 32) continue;
     const u64 cand = t | (1ull << bit);
     u64 acc = 0;
-    slice.each(rs, kDead, [&](float l, float k, uint32_t idx) {
-      if (bin_of(k) == bin && order_value(l, idx) >= cand) acc += by_sum ? weight_of(rs, sh.exp2, l, k).whole() : 1ull;
-    });
+    for (int j = threadIdx.x; j < slice.size(); j += kThreads) {
+      const float l = slice.at(j);
+      const u64 value = order_value(l, (uint32_t)(slice.first + j));
+      if (key_any(rs, l) >= kDead && value >= cand && value >= from) acc += by_sum ? weight_any(rs, sh.exp2, l) : 1ull;
+    }
     send_sum(sh, acc, par, rank, cs);
     cluster_sync(cs);
     u64 all = 0;
@@ -423,6 +496,235 @@ __device__ u64 bisect(SampleShared &sh, const Slice<T> &slice, const RowScale &r
     par ^= 1;
   }
   return t;
+}
+
+// The window of a search: steps [d0, d1) of 1/1024 octave below the largest
+// logit, with what lies above it and in it.
+struct Window {
+  int d0, d1;
+  unsigned int above, in;  // tokens
+  float above_sum;
+};
+
+// The whole cluster: the bins in which the end of the share `share` of the weight
+// lies, from counts of the tokens of order value `from` on.
+template <typename T, bool WIDE>
+__device__ Window count_bins(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, uint32_t rank, int cs, u64 from, float share) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sh.count[tid + i * kThreads] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int j = tid; j < slice.size(); j += kThreads) {
+    const float l = slice.at(j), t = key_of<WIDE>(rs, l);
+    if (t >= kDead && (!from || order_value(l, (uint32_t)(slice.first + j)) >= from))
+      atomicAdd(&sh.count[(kMagicBits - __float_as_int(t)) >> 5], 1u);
+  }
+  cluster_sync(cs);
+  unsigned int c[kPer] = {};
+#pragma unroll 4
+  for (int r = 0; r < cs; ++r) {
+    const unsigned int *h = peer(&sh.count[kPer * tid], (uint32_t)r);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) c[i] += h[i];
+  }
+  // prefixes: tokens, and weights by the bins' upper and lower edges (the keys in
+  // them are rounded), in units of 2^-40 of the largest weight
+  u64 up[kPer], dn[kPer], cn = 0, un = 0, ln = 0, all, up_all, dn_all;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const float e = exp2f(40.f - (float)(kPer * tid + i) * (1.f / 32.f));
+    up[i] = (u64)c[i] * ((u64)(e * 1.0005f) + 1);
+    dn[i] = (u64)c[i] * (u64)(e * 0.9787f);  // 2^(-31.5/1024) = 0.97890
+    cn += c[i];
+    un += up[i];
+    ln += dn[i];
+  }
+  cn = block_scan(sh, cn, all);
+  un = block_scan(sh, un, up_all);
+  ln = block_scan(sh, ln, dn_all);
+  if (tid == 0) sh.pick[0] = sh.pick[1] = kBins - 1;
+  __syncthreads();
+  // The share of the weight down to the end of a bin is at most un / (un + the
+  // lower edges of the rest) and at least ln / (ln + the upper edges of the
+  // rest): the first bins at which these reach `share` enclose the end.
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    un += up[i];
+    ln += dn[i];
+    const double u = (double)un, l = (double)ln, p = (double)share;
+    if (c[i]) {
+      if (u >= p * (u + (double)(dn_all - ln)) * 0.99999999) atomicMin(&sh.pick[0], kPer * tid + i);
+      if (l >= p * (l + (double)(up_all - un)) * 1.00000001) atomicMin(&sh.pick[1], kPer * tid + i);
+    }
+  }
+  __syncthreads();
+  const int lo = sh.pick[0], hi = max(lo, sh.pick[1]);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int bin = kPer * tid + i;
+    if (bin == lo) sh.pick[2] = (int)cn;
+    cn += c[i];
+    if (bin == hi) sh.pick[3] = (int)cn;
+  }
+  cluster_sync(cs);  // the counts have been read, and the picks are there
+  const unsigned int above = (unsigned int)sh.pick[2];
+  return Window{32 * lo, min(kRange, 32 * (hi + 1)), above, (unsigned int)sh.pick[3] - above, 0.f};
+}
+
+// The whole cluster: rounds of kBuckets until the want-th token, or (SUMS) the end
+// of the share `share` of the weight, is among few tokens.  Only tokens from
+// order value `from` on count.  An empty window (d1 < 0): fewer than wanted.
+template <typename T, bool WIDE, bool SUMS>
+__device__ Window search(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, uint32_t rank, int cs, u64 from, unsigned int want,
+                         float share, int &par) {
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Window win{0, kRange, 0, 0, 0.f};
+  int shift = kFirstShift;
+  float goal = 0.f;
+  for (bool first = true;; first = false) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBuckets; ++i) {
+      if (SUMS) sh.own.sum[i][tid] = 0.f;
+      sh.own.cnt[i][tid] = 0;
+    }
+    const int d_span = win.d1 - win.d0;
+    const float mc = fmaf(rs.m, rs.c_hi, 0.f);
+#pragma unroll 4
+    for (int j = tid; j < slice.size(); j += kThreads) {
+      const float l = slice.at(j), t = key_of<WIDE>(rs, l);
+      const int d = kMagicBits - __float_as_int(t) - win.d0;
+      if (t >= kDead && (unsigned int)d < (unsigned int)d_span && (!from || order_value(l, (uint32_t)(slice.first + j)) >= from)) {
+        const int i = min(d >> shift, kBuckets - 1);
+        sh.own.cnt[i][tid] += 1;
+        if (SUMS) {
+          const float y = WIDE ? (l - rs.m) * rs.c_hi : fmaf(l, rs.c_hi, -mc);
+          float w;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(WIDE && l == rs.m ? 0.f : y));
+          sh.own.sum[i][tid] += w;
+        }
+      }
+    }
+    __syncthreads();
+    // two warps per bucket: its sums over the threads
+    {
+      const int i = warp >> 1;
+      unsigned int c = 0;
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < kThreads / 64; ++k) {
+        const int at = (warp & 1) * 32 + lane + 64 * k;
+        c += sh.own.cnt[i][at];
+        if (SUMS) x += sh.own.sum[i][at];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        c += __shfl_xor_sync(0xffffffffu, c, o);
+        if (SUMS) x += __shfl_xor_sync(0xffffffffu, x, o);
+      }
+      if (lane == 0) {
+        sh.warp_idx[warp] = (int)c;
+        sh.warp_max[warp] = x;
+      }
+    }
+    __syncthreads();
+    if (tid < kBuckets * cs) {
+      const int i = tid % kBuckets, to = tid / kBuckets;
+      SampleShared *d = peer(&sh, (uint32_t)to);
+      d->bucket_cnt[par][rank][i] = (unsigned int)(sh.warp_idx[2 * i] + sh.warp_idx[2 * i + 1]);
+      if (SUMS) d->bucket_sum[par][rank][i] = sh.warp_max[2 * i] + sh.warp_max[2 * i + 1];
+    }
+    cluster_sync(cs);
+    unsigned int c[kBuckets];
+    float x[kBuckets], all = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBuckets; ++i) {
+      c[i] = 0;
+      x[i] = 0.f;
+      for (int r = 0; r < cs; ++r) {
+        c[i] += sh.bucket_cnt[par][r][i];
+        if (SUMS) x[i] += sh.bucket_sum[par][r][i];
+      }
+      all += x[i];
+    }
+    par ^= 1;
+    if (SUMS && first) goal = share * all;
+    // the buckets in which the end lies: one, or (sums) those within the margin
+    int b0 = -1, b1 = -1;
+    unsigned int n = win.above, n0 = win.above, n1 = 0;
+    float s = win.above_sum, s0 = win.above_sum;
+#pragma unroll
+    for (int i = 0; i < kBuckets; ++i) {
+      const unsigned int n_in = n + c[i];
+      const float s_in = s + x[i];
+      if (b0 < 0 && (SUMS ? s_in >= goal * (1.f - kMargin) : n_in >= want)) {
+        b0 = i;
+        n0 = n;
+        s0 = s;
+      }
+      if (b1 < 0 && (SUMS ? s_in >= goal * (1.f + kMargin) : n_in >= want)) {
+        b1 = i;
+        n1 = n_in;
+      }
+      n = n_in;
+      s = s_in;
+    }
+    if (b0 < 0) {
+      if (!SUMS) return Window{0, -1, 0, 0, 0.f};
+      b0 = kBuckets - 1;
+      n0 = n - c[kBuckets - 1];
+      s0 = s - x[kBuckets - 1];
+    }
+    if (b1 < 0) {
+      b1 = kBuckets - 1;
+      n1 = n;
+    }
+    const int d1 = b1 == kBuckets - 1 ? win.d1 : win.d0 + ((b1 + 1) << shift);
+    win = Window{win.d0 + (b0 << shift), d1, n0, n1 - n0, s0};
+    if (win.in <= (unsigned int)kList || shift == 0) return win;
+    // the next round's buckets cover the window (the last one taking the rest of
+    // a wide one); where a round could not narrow it, no other would
+    const int last_shift = shift;
+    while (shift > 0 && (kBuckets << (shift - 1)) >= win.d1 - win.d0) --shift;
+    if (shift == last_shift && win.d1 - win.d0 >= d_span) return win;
+  }
+}
+
+// Exact weights over the slice, in runs of each warp: sh.run_sum gets those of
+// tokens above key t_hi, `rest` returns those at or below, and tokens with keys
+// in [t_lo, t_hi] go to rank 0's list.  TESTS: tokens before order value `from`
+// or with less weight than `least` do not count.
+template <typename T, bool WIDE, bool TESTS>
+__device__ u64 exact_pass(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, u64 from, u64 least, float t_lo, float t_hi) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_run = ((slice.size() + kWarps * kRuns - 1) / (kWarps * kRuns) + 31) & ~31;
+  SampleShared *lead = peer(&sh, 0);
+  Weight rest{0, 0};
+  for (int run = 0; run < kRuns; ++run) {
+    const int j0 = (warp * kRuns + run) * per_run, j1 = min(slice.size(), j0 + per_run);
+    Weight above{0, 0};
+#pragma unroll 4
+    for (int j = j0 + lane; j < j1; j += 32) {
+      const float l = slice.at(j), t = key_of<WIDE>(rs, l);
+      const Weight w = weight_of<WIDE>(rs, sh.exp2, l, t);
+      bool live = t >= kDead;
+      if (TESTS) live = live && w.whole() >= least && order_value(l, (uint32_t)(slice.first + j)) >= from;
+      if (live && t > t_hi) above.add(w);
+      if (live && !(t > t_hi)) {
+        rest.add(w);
+        if (t >= t_lo) {
+          const unsigned int at = atomicAdd(&lead->list_n, 1u);
+          if (at < kList) lead->few.list[at] = order_value(l, (uint32_t)(slice.first + j));
+        }
+      }
+    }
+    const u64 all = warp_total(above.whole());
+    if (lane == 0) sh.run_sum[warp][run] = all;
+  }
+  return rest.whole();
 }
 
 template <typename T>
@@ -464,23 +766,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const q1_sample_arg
 #pragma unroll
     for (int i = 0; i < E; ++i) mx = fmaxf(mx, to_f32(e[i]));  // a NaN is passed over
   }
-  auto clear_hist = [&]() {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      sh.hist.cnt[tid + i * kThreads] = 0;
-#pragma unroll
-      for (int x = 0; x < 3; ++x) sh.hist.sum[x][tid + i * kThreads] = 0;
-    }
-  };
   if (!greedy) {
 #pragma unroll
     for (int i = 0; i < 1024 / kThreads; ++i) sh.exp2[tid + i * kThreads] = g_exp2.v[tid + i * kThreads];
   }
-  if (has_k || has_p) clear_hist();
   if (tid == 0) {
     // small enough that its products stay finite
-    sh.c = fmin(1.4426950408889634 / (double)temp, 1.2676506002282294e30);
-    sh.threshold = 0;
+    const double c = fmin(1.4426950408889634 / (double)temp, 1.2676506002282294e30);
+    sh.rs.c_hi = (float)c;
+    sh.rs.c_lo = (float)(c - (double)sh.rs.c_hi);
+    sh.rs.top = 0;
+    sh.rs.least = 0;
+    sh.threshold[0] = sh.threshold[1] = 0;
     sh.list_n = 0;
   }
 #pragma unroll
@@ -506,13 +803,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const q1_sample_arg
   }
   if (greedy) {
     int best = 0x7fffffff;
-    for (int j = tid; j < slice.nv; j += kThreads) {
-      float f[E];
-      slice.get(j, f);
-#pragma unroll
-      for (int i = E - 1; i >= 0; --i)
-        if (f[i] == m) best = min(best, slice.first + j * E + i);
-    }
+    for (int j = tid; j < slice.size(); j += kThreads)
+      if (slice.at(j) == m) {
+        best = slice.first + j;
+        break;
+      }
     best = __reduce_min_sync(0xffffffffu, best);
     if (lane == 0) sh.warp_idx[warp] = best;
     __syncthreads();
@@ -529,190 +824,166 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const q1_sample_arg
     return;
   }
   if (tid == 0) {
-    RowScale rs;
+    RowScale rs = sh.rs;
     rs.m = m;
-    rs.c_hi = (float)sh.c;
-    rs.c_lo = (float)(sh.c - (double)rs.c_hi);
     const double mc = (double)m * (double)rs.c_hi;  // exact
     rs.wide = !(fabs(mc) < 4096.0);
     rs.K = rs.A0 = rs.a1 = 0.f;
     if (!rs.wide) {
-      const double grid = rint(mc * 1024.0);
-      rs.A0 = (float)(grid * (1.0 / 1024.0));
-      rs.K = (float)(12582912.0 - grid);
-      rs.a1 = (float)((mc - grid * (1.0 / 1024.0)) + (double)m * (double)rs.c_lo);
+      // rounded as key_of rounds (|m c_hi| 1024 is below 2^22), so that m's key is
+      // kMagic and no key exceeds it
+      const float grid = fmaf(m, 1024.f * rs.c_hi, kMagic) - kMagic;
+      rs.A0 = grid * (1.f / 1024.f);
+      rs.K = kMagic - grid;
+      rs.a1 = fmaf(m, rs.c_lo, fmaf(m, rs.c_hi, -rs.A0));
     }
-    rs.top = weight_of(rs, sh.exp2, m, key_of(rs, m)).whole();
     const float mp = a.min_p ? a.min_p[b] : a.min_p_value;
-    rs.least = mp > 0.f ? part_up(mp, rs.top) : 0;
+    if (mp > 0.f) {
+      rs.top = weight_any(rs, sh.exp2, m);
+      rs.least = part_up(mp, rs.top);
+    }
     sh.rs = rs;
   }
   __syncthreads();
   const RowScale rs = sh.rs;
 
   // ---- the truncations
-  if (has_k || has_p) {
-    // rank 0: the cluster's histogram, kPer bins per thread, with the prefixes
-    unsigned int c3[kPer];
-    u64 s3[kPer], c_before = 0, s_before = 0, c_all = 0, s_all = 0;
-    // counts (and weights) by bin of the tokens from order value `from` on
-    auto histogram = [&](bool sums, u64 from) {
-      slice.each(rs, kDead, [&](float l, float t, uint32_t idx) {
-        if (from && order_value(l, idx) < from) return;
-        const int i = bin_of(t);
-        atomicAdd(&sh.hist.cnt[i], 1u);
-        if (sums) {
-          const u64 w = weight_of(rs, sh.exp2, l, t).whole();
-          const uint32_t p0 = (uint32_t)w & 0x7FFFu, p1 = (uint32_t)(w >> 15) & 0x7FFFu, p2 = (uint32_t)(w >> 30);
-          atomicAdd(&sh.hist.sum[0][i], p0);
-          if (p1) atomicAdd(&sh.hist.sum[1][i], p1);
-          if (p2) atomicAdd(&sh.hist.sum[2][i], p2);
-        }
-      });
-      cluster_sync(cs);
-      if (rank == 0) {
-        u64 c = 0, s = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          c3[i] = 0;
-          s3[i] = 0;
-        }
-#pragma unroll 4
-        for (int r = 0; r < cs; ++r) {
-          const auto *h = &peer(&sh, (uint32_t)r)->hist;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int at = kPer * tid + i;
-            c3[i] += h->cnt[at];
-            if (sums) s3[i] += (u64)h->sum[0][at] + ((u64)h->sum[1][at] << 15) + ((u64)h->sum[2][at] << 30);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          c += c3[i];
-          s += s3[i];
-        }
-        c_before = block_scan(sh, c, c_all);
-        s_before = block_scan(sh, s, s_all);
-      }
-    };
-    // rank 0: the bin at which the count (by_sum = 0) or the weight reaches want, to everyone
-    auto locate = [&](int by_sum, u64 want) {
-      if (rank == 0) {
-        if (tid == 0) {
-          sh.find[by_sum] = {1, 0, 0, 0, 0};
-          sh.list_n = 0;
-        }
-        __syncthreads();
-        u64 c = c_before, s = s_before;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const u64 x = by_sum ? s : c, dx = by_sum ? s3[i] : c3[i];
-          if (x < want && want <= x + dx) {
-            const int bin = kPer * tid + i, few = c + c3[i] <= kList;
-            sh.find[by_sum] = {few ? 0 : bin, bin, few, !few && c3[i] > kList, want - x};
-          }
-          c += c3[i];
-          s += s3[i];
-        }
-        __syncthreads();
-        if (tid >= 1 && tid < cs) peer(&sh, (uint32_t)tid)->find[by_sum] = sh.find[by_sum];
-      }
-      cluster_sync(cs);
-    };
-    u64 thr = 0;
-    // the tokens of find[which]'s bins, from thr on, to rank 0's list
-    auto collect = [&](int which) {
-      const int lo = sh.find[which].lo, hi = sh.find[which].hi;
-      SampleShared *lead = peer(&sh, 0);
-      slice.each(rs, __int_as_float(kMagicBits - (32 * hi + 31)), [&](float l, float t, uint32_t idx) {
-        const u64 value = order_value(l, idx);
-        if (bin_of(t) < lo || value < thr) return;
-        const unsigned int at = atomicAdd(&lead->list_n, 1u);
-        if (at < kList) lead->few.list[at] = value;
-      });
-      cluster_sync(cs);
-    };
+  u64 thr = 0;            // tokens with a smaller order value are not kept
+  bool summed = false;    // sh.run_sum holds the kept weights
+  int par = 0;
+  auto run_search = [&](bool sums, unsigned int want, float share) -> Window {
+    if (!sums) return rs.wide ? search<T, true, false>(sh, slice, rs, rank, cs, thr, want, share, par)
+                              : search<T, false, false>(sh, slice, rs, rank, cs, thr, want, share, par);
+    const Window w = rs.wide ? count_bins<T, true>(sh, slice, rs, rank, cs, thr, share)
+                             : count_bins<T, false>(sh, slice, rs, rank, cs, thr, share);
+    if (w.in <= (unsigned int)kList) return w;
+    return rs.wide ? search<T, true, true>(sh, slice, rs, rank, cs, thr, want, share, par)
+                   : search<T, false, true>(sh, slice, rs, rank, cs, thr, want, share, par);
+  };
+  auto run_exact = [&](u64 from, u64 least, float t_lo, float t_hi) -> u64 {
+    if (rs.wide) return exact_pass<T, true, true>(sh, slice, rs, from, least, t_lo, t_hi);
+    if (from || least) return exact_pass<T, false, true>(sh, slice, rs, from, least, t_lo, t_hi);
+    return exact_pass<T, false, false>(sh, slice, rs, 0, 0, t_lo, t_hi);
+  };
+  auto key_at = [&](int d) { return __int_as_float(kMagicBits - d); };
+  auto draw = [&](int k, u64 want) {  // rank 0
+    float *prob = a.prob ? a.prob + b : nullptr;
+    if (sh.list_n <= kShort) draw_from_short_list(sh, rs, k, top_p, want, u, a.token + b, prob);
+    else draw_from_list(sh, rs, k, top_p, want, u, a.token + b, prob);
+  };
+  auto announce = [&](int which, u64 value) {  // rank 0's value to everyone
+    if (rank == 0 && tid < cs) peer(&sh, (uint32_t)tid)->threshold[which] = value;
+    cluster_sync(cs);
+    return sh.threshold[which];
+  };
+  if (has_k) {
+    const Window w = run_search(false, (unsigned int)top_k, 0.f);
+    has_k = w.d1 > 0;  // a top_k beyond the tokens that have a weight keeps them all
     if (has_k) {
-      histogram(false, 0);
-      locate(0, (u64)top_k);
-      const auto f = sh.find[0];
-      has_k = f.lo <= f.hi;  // a top_k beyond the tokens that have a weight keeps them all
-      if (has_k && f.few) {
-        collect(0);
-        if (rank == 0) draw_from_list(sh, rs, top_k, top_p, 0, u, a.token + b, a.prob ? a.prob + b : nullptr);
-        return;
-      }
-      if (has_k) {
-        if (f.many) {
-          thr = bisect(sh, slice, rs, rank, cs, f.hi, 0, f.need);
-        } else {
-          collect(0);
-          if (rank == 0) {
-            find_in_list(sh, rs, 0, f.need);
-            if (tid < cs) peer(&sh, (uint32_t)tid)->threshold = sh.found;
+      const bool few = w.above + w.in <= (unsigned int)kList;
+      if (few || w.in <= (unsigned int)kList) {
+        const float t_lo = key_at(w.d1 - 1), t_hi = few ? kMagic : key_at(w.d0);
+        SampleShared *lead = peer(&sh, 0);
+        auto collect = [&](auto wide) {
+#pragma unroll 4
+          for (int j = tid; j < slice.size(); j += kThreads) {
+            const float l = slice.at(j), t = key_of<decltype(wide)::value>(rs, l);
+            if (t >= t_lo && t <= t_hi) {
+              const unsigned int at = atomicAdd(&lead->list_n, 1u);
+              if (at < kList) lead->few.list[at] = order_value(l, (uint32_t)(slice.first + j));
+            }
           }
-          cluster_sync(cs);
-          thr = sh.threshold;
-        }
-      }
-      if (has_p) {  // the histogram again, with weights
-        clear_hist();
+        };
+        if (rs.wide) collect(std::true_type{});
+        else collect(std::false_type{});
         cluster_sync(cs);
-      }
-    }
-    if (has_p) {
-      histogram(true, thr);
-      u64 want = 0;
-      if (rank == 0) {
-        // kept: less than ceil(top_p * weight) before it; the first always is
-        want = part_up(top_p, s_all);
-        want = want ? want : 1;
-      }
-      locate(1, want);
-      const auto f = sh.find[1];
-      if (f.few) {
-        collect(1);
-        if (rank == 0) draw_from_list(sh, rs, has_k ? top_k : 0, top_p, want, u, a.token + b, a.prob ? a.prob + b : nullptr);
-        return;
-      }
-      if (f.many) {
-        thr = max(thr, bisect(sh, slice, rs, rank, cs, f.hi, 1, f.need));
-      } else {
-        collect(1);
+        if (few) {
+          if (rank == 0) draw(top_k, 0);
+          return;
+        }
         if (rank == 0) {
-          find_in_list(sh, rs, 1, f.need);
-          if (tid < cs) peer(&sh, (uint32_t)tid)->threshold = sh.found;
+          find_in_list(sh, rs, 0, (u64)top_k - w.above);
+          if (tid == 0) sh.list_n = 0;
         }
-        cluster_sync(cs);
-        thr = max(thr, sh.threshold);
+        thr = announce(0, sh.found);
+      } else {
+        thr = bisect(sh, slice, rs, rank, cs, 0, false, (u64)top_k);
       }
     }
-    if (tid == 0) sh.threshold = thr;
+  }
+  if (has_p) {
+    const Window w = run_search(true, 0, top_p);
+    const bool few = w.above + w.in <= (unsigned int)kList, many = !few && w.in > (unsigned int)kList;
+    const float t_lo = many ? 2.f * kMagic : key_at(w.d1 - 1), t_hi = few || many ? 2.f * kMagic : key_at(w.d0);
+    const u64 rest = run_exact(thr, 0, t_lo, t_hi);
+    // the weight above the window, and the rest
+    u64 mine = 0;
+    __syncwarp();
+    if (lane < kRuns) mine = sh.run_sum[warp][lane];
+    send_sum(sh, mine, 0, rank, cs);
     __syncthreads();
+    {
+      const u64 r = warp_total(rest);
+      if (lane == 0) sh.warp_sum[warp] = r;
+      __syncthreads();
+      if (tid < cs) {
+        u64 all = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) all += sh.warp_sum[i];
+        peer(&sh, (uint32_t)tid)->part_rest[rank] = all;
+      }
+    }
+    cluster_sync(cs);
+    u64 above = 0, total = 0;
+    for (int r = 0; r < cs; ++r) {
+      above += sh.part_sum[0][r];
+      total += sh.part_rest[r];
+    }
+    total += above;
+    // kept: less than ceil(top_p * weight) before it; the first always is
+    u64 want = part_up(top_p, total);
+    want = want ? want : 1;
+    if (few) {
+      if (rank == 0) draw(has_k ? top_k : 0, want);
+      return;
+    }
+    u64 last = 0;
+    if (!many) {
+      if (rank == 0) {
+        if (tid == 0) sh.found = 0;
+        if (want > above) find_in_list(sh, rs, 1, want - above);
+      }
+      __syncthreads();
+      last = announce(1, sh.found);
+      if (last && !rs.least) {
+        // the list's kept tokens join the sums of their runs
+        if (rank == 0) {
+          const int n_list = (int)min(sh.list_n, (unsigned int)kList);
+          for (int i = tid; i < n_list; i += kThreads) {
+            const u64 value = sh.few.list[i];
+            if (value >= last) {
+              const int index = (int)~(uint32_t)value, r = index / per;
+              // that CTA's slice: its first vector may begin before its first token
+              const int f0 = r * per, ph = (int)((reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) + b * a.row_stride + f0) & 15) / sizeof(T));
+              const int len = (int)(min((int64_t)f0 + per, a.V) - f0), size = (ph + len + E - 1) / E * E;
+              const int per_run = ((size + kWarps * kRuns - 1) / (kWarps * kRuns) + 31) & ~31;
+              const int run = (index - f0 + ph) / per_run;
+              atomicAdd(&peer(&sh, (uint32_t)r)->run_sum[run / kRuns][run % kRuns], weight_any(rs, sh.exp2, order_logit(value)));
+            }
+          }
+        }
+        cluster_sync(cs);
+        summed = true;
+      }
+    }
+    if (!last) last = bisect(sh, slice, rs, rank, cs, thr, true, want);
+    thr = max(thr, last);
   }
 
-  // ---- the kept weight: warp w of a CTA sums a contiguous run of vectors
-  const u64 thr = sh.threshold;
-  const float t_min = thr ? key_of(rs, order_logit(thr)) : kDead;
-  const int vw = ((slice.nv + kWarps - 1) / kWarps + 31) & ~31;
-  const int v0 = warp * vw, v1 = min(slice.nv, v0 + vw);
-  const bool tests = thr != 0 || rs.least != 0;
-  auto kept = [&](float l, uint32_t idx) -> Weight {
-    const float t = key_of(rs, l);
-    if (!(t >= t_min)) return Weight{0, 0};
-    const Weight w = weight_of(rs, sh.exp2, l, t);
-    if (tests && (order_value(l, idx) < thr || w.whole() < rs.least)) return Weight{0, 0};
-    return w;
-  };
-  Weight acc{0, 0};
-  for (int j = v0 + lane; j < v1; j += 32) {
-    float f[E];
-    slice.get(j, f);
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc.add(kept(f[i], (uint32_t)(slice.first + j * E + i)));
-  }
-  send_sum(sh, acc.whole(), 0, rank, cs);
+  // ---- the kept weight by warp and run, and the draw
+  if (!summed) run_exact(thr, rs.least, 2.f * kMagic, 0.f);
+  __syncwarp();
+  send_sum(sh, lane < kRuns ? sh.run_sum[warp][lane] : 0, 0, rank, cs);
   cluster_sync(cs);
   u64 total = 0, before = 0;
   for (int r = 0; r < cs; ++r) {
@@ -720,32 +991,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const q1_sample_arg
     total += sh.part_sum[0][r];
   }
   const u64 target = draw_target(u, total);
-  // ---- the draw: the warp whose run holds the target-th unit of weight
   for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
   if (target < before || target - before >= sh.warp_sum[warp]) return;
-  for (int j0 = v0; j0 < v1; j0 += 32) {
+  int run = 0;
+  while (target - before >= sh.run_sum[warp][run]) before += sh.run_sum[warp][run++];
+  const int per_run = ((slice.size() + kWarps * kRuns - 1) / (kWarps * kRuns) + 31) & ~31;
+  const int j1 = min(slice.size(), (warp * kRuns + run + 1) * per_run);
+  for (int j0 = (warp * kRuns + run) * per_run; j0 < j1; j0 += 32) {
     const int j = j0 + lane;
-    float f[E];
-    u64 w[E], s = 0;
-    if (j < v1) slice.get(j, f);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      w[i] = j < v1 ? kept(f[i], (uint32_t)(slice.first + j * E + i)).whole() : 0;
-      s += w[i];
+    u64 w = 0;
+    if (j < j1) {
+      const float l = slice.at(j);
+      if (key_any(rs, l) >= kDead && order_value(l, (uint32_t)(slice.first + j)) >= thr) w = weight_any(rs, sh.exp2, l);
+      if (w < rs.least) w = 0;
     }
-    const u64 incl = warp_scan(s, lane);
+    const u64 incl = warp_scan(w, lane);
     const u64 step = __shfl_sync(0xffffffffu, incl, 31);
     if (target - before < step) {
-      u64 c = before + incl - s;
-      if (target >= c && target < c + s) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          if (target >= c && target < c + w[i]) {
-            a.token[b] = slice.first + j * E + i;
-            if (a.prob) a.prob[b] = (float)((double)w[i] / (double)total);
-          }
-          c += w[i];
-        }
+      const u64 c = before + incl - w;
+      if (target >= c && target - c < w) {
+        a.token[b] = slice.first + j;
+        if (a.prob) a.prob[b] = (float)((double)w / (double)total);
       }
       return;
     }
@@ -762,6 +1028,7 @@ cudaError_t sample_t(const q1_sample_args &a, cudaStream_t st) {
   constexpr int64_t kSliceMax = (int64_t)((kMost - sizeof(SampleShared)) / sizeof(T)) - 2 * E - 8;
   if (not_done(ready, dev)) {
     cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
   }
