@@ -104,6 +104,7 @@ struct alignas(16) SampleShared {
   float bucket_sum[2][kMaxCluster][kBuckets];
   unsigned int bucket_cnt[2][kMaxCluster][kBuckets];
   // written by rank 0 into every CTA
+  int picked[4];                    // the bins in which top-p ends, the tokens before them and down to their end
   u64 threshold[2];                 // tokens with a smaller order value are not kept: by top-k, by top-p
   unsigned int list_n;              // rank 0: collected tokens
   // this CTA's own
@@ -252,7 +253,10 @@ __device__ __forceinline__ void send_sum(SampleShared &sh, u64 v, int par, uint3
 }
 // floor(x 2^64) for x in [0, 1)
 __device__ __forceinline__ u64 fraction(float x) {
-  return x > 0.f ? __double2ull_rd((double)x * 18446744073709551616.0) : 0ull;
+  if (!(x > 0.f)) return 0;
+  const int b = __float_as_int(x), e = (b >> 23) - 86;  // x 2^64 = significand 2^e
+  const u64 sig = (u64)((b & 0x7FFFFF) | (b >= 0x800000 ? 0x800000 : 0));
+  return e >= 0 ? sig << e : (e > -24 ? sig >> -e : 0);
 }
 // ceil(x w) for x in [0, 1]
 __device__ __forceinline__ u64 part_up(float x, u64 w) {
@@ -275,15 +279,19 @@ struct Slice {
   __device__ __forceinline__ int size() const { return nv * E; }
 };
 
-// Ascending (or descending) bitonic sort of n2 (a power of two) values in
-// shared memory by the block.  Up to step 32 a warp's pairs lie in 64 places of
-// its own.
+// Ascending (or descending) bitonic sort of n2 (a power of two, at most 1024)
+// values in shared memory by the block.  A warp holds 64 neighbouring places in
+// registers, two per lane, for the steps up to 32.
+__device__ __forceinline__ u64 shuffle_xor(u64 v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+__device__ __forceinline__ uint32_t shuffle_xor(uint32_t v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
 template <typename V>
 __device__ __forceinline__ void block_sort(V *v, int n2, bool descending) {
+  const int lane = threadIdx.x & 31, base = (threadIdx.x >> 5) * 64;
   __syncthreads();
-  for (int size = 2; size <= n2; size <<= 1)
-    for (int step = size >> 1; step > 0; step >>= 1) {
-      for (int i = threadIdx.x; i < n2 / 2; i += kThreads) {
+  for (int size = 2; size <= n2; size <<= 1) {
+    for (int step = size >> 1; step >= 64; step >>= 1) {
+      const int i = threadIdx.x;
+      if (i < n2 / 2) {
         const int x = 2 * i - (i & (step - 1)), z = x + step;
         const V p = v[x], q = v[z];
         if ((p < q) == (((x & size) == 0) == descending)) {
@@ -291,9 +299,35 @@ __device__ __forceinline__ void block_sort(V *v, int n2, bool descending) {
           v[z] = p;
         }
       }
-      if (step > 32 || (step == 1 && size > 32)) __syncthreads();
-      else __syncwarp();
+      __syncthreads();
     }
+    // all sizes up to 64 in one go
+    if (size < 64 && size < n2) continue;
+    if (base < n2) {
+      const int at0 = base + lane, at1 = at0 + 32;
+      V r0 = at0 < n2 ? v[at0] : V(0), r1 = at1 < n2 ? v[at1] : V(0);
+      for (int sz = size <= 64 ? 2 : size; sz <= size; sz <<= 1) {
+        if (sz >= 64 && n2 > 32) {
+          if ((r0 < r1) == (((at0 & sz) == 0) == descending)) {
+            const V t = r0;
+            r0 = r1;
+            r1 = t;
+          }
+        }
+        for (int step = min(sz >> 1, 16); step > 0; step >>= 1) {
+          const V p0 = shuffle_xor(r0, step), p1 = shuffle_xor(r1, step);
+          // the lower place of a pair keeps the larger value where its run descends
+          const bool low = (lane & step) == 0;
+          const bool big0 = low == (((at0 & sz) == 0) == descending), big1 = low == (((at1 & sz) == 0) == descending);
+          r0 = (r0 < p0) == big0 ? p0 : r0;
+          r1 = (r1 < p1) == big1 ? p1 : r1;
+        }
+      }
+      if (at0 < n2) v[at0] = r0;
+      if (at1 < n2) v[at1] = r1;
+    }
+    __syncthreads();
+  }
   __syncthreads();
 }
 __device__ __forceinline__ int power_of_two(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
@@ -522,55 +556,61 @@ __device__ Window count_bins(SampleShared &sh, const Slice<T> &slice, const RowS
       atomicAdd(&sh.count[(kMagicBits - __float_as_int(t)) >> 5], 1u);
   }
   cluster_sync(cs);
-  unsigned int c[kPer] = {};
+  if (rank == 0) {
+    unsigned int c[kPer] = {};
 #pragma unroll 4
-  for (int r = 0; r < cs; ++r) {
-    const unsigned int *h = peer(&sh.count[kPer * tid], (uint32_t)r);
+    for (int r = 0; r < cs; ++r) {
+      const unsigned int *h = peer(&sh.count[kPer * tid], (uint32_t)r);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) c[i] += h[i];
-  }
-  // prefixes: tokens, and weights by the bins' upper and lower edges (the keys in
-  // them are rounded), in units of 2^-40 of the largest weight
-  u64 up[kPer], dn[kPer], cn = 0, un = 0, ln = 0, all, up_all, dn_all;
+      for (int i = 0; i < kPer; ++i) c[i] += h[i];
+    }
+    // prefixes: tokens, and weights by the bins' upper and lower edges (the keys
+    // in them are rounded), in units of 2^-40 of the largest weight
+    u64 up[kPer], dn[kPer], cn = 0, un = 0, ln = 0, all, up_all, dn_all;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const float e = exp2f(40.f - (float)(kPer * tid + i) * (1.f / 32.f));
-    up[i] = (u64)c[i] * ((u64)(e * 1.0005f) + 1);
-    dn[i] = (u64)c[i] * (u64)(e * 0.9787f);  // 2^(-31.5/1024) = 0.97890
-    cn += c[i];
-    un += up[i];
-    ln += dn[i];
-  }
-  cn = block_scan(sh, cn, all);
-  un = block_scan(sh, un, up_all);
-  ln = block_scan(sh, ln, dn_all);
-  if (tid == 0) sh.pick[0] = sh.pick[1] = kBins - 1;
-  __syncthreads();
-  // The share of the weight down to the end of a bin is at most un / (un + the
-  // lower edges of the rest) and at least ln / (ln + the upper edges of the
-  // rest): the first bins at which these reach `share` enclose the end.
+    for (int i = 0; i < kPer; ++i) {
+      const float e = exp2f(40.f - (float)(kPer * tid + i) * (1.f / 32.f));
+      up[i] = (u64)c[i] * ((u64)(e * 1.0005f) + 1);
+      dn[i] = (u64)c[i] * (u64)(e * 0.9787f);  // 2^(-31.5/1024) = 0.97890
+      cn += c[i];
+      un += up[i];
+      ln += dn[i];
+    }
+    cn = block_scan(sh, cn, all);
+    un = block_scan(sh, un, up_all);
+    ln = block_scan(sh, ln, dn_all);
+    if (tid == 0) sh.pick[0] = sh.pick[1] = kBins - 1;
+    __syncthreads();
+    // The share of the weight down to the end of a bin is at most un / (un + the
+    // lower edges of the rest) and at least ln / (ln + the upper edges of the
+    // rest): the first bins at which these reach `share` enclose the end.
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    un += up[i];
-    ln += dn[i];
-    const double u = (double)un, l = (double)ln, p = (double)share;
-    if (c[i]) {
-      if (u >= p * (u + (double)(dn_all - ln)) * 0.99999999) atomicMin(&sh.pick[0], kPer * tid + i);
-      if (l >= p * (l + (double)(up_all - un)) * 1.00000001) atomicMin(&sh.pick[1], kPer * tid + i);
+    for (int i = 0; i < kPer; ++i) {
+      un += up[i];
+      ln += dn[i];
+      if (c[i]) {
+        if ((float)un * (1.f - share) * 1.00001f >= share * (float)(dn_all - ln)) atomicMin(&sh.pick[0], kPer * tid + i);
+        if ((float)ln * (1.f - share) >= share * (float)(up_all - un) * 1.00001f) atomicMin(&sh.pick[1], kPer * tid + i);
+      }
+    }
+    __syncthreads();
+    const int lo = sh.pick[0], hi = max(lo, sh.pick[1]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int bin = kPer * tid + i;
+      if (bin == lo) sh.pick[2] = (int)cn;
+      cn += c[i];
+      if (bin == hi) sh.pick[3] = (int)cn;
+    }
+    __syncthreads();
+    if (tid < cs * 4) {
+      SampleShared *d = peer(&sh, (uint32_t)(tid >> 2));
+      d->picked[tid & 3] = (tid & 3) == 1 ? max(lo, sh.pick[1]) : sh.pick[tid & 3];
     }
   }
-  __syncthreads();
-  const int lo = sh.pick[0], hi = max(lo, sh.pick[1]);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int bin = kPer * tid + i;
-    if (bin == lo) sh.pick[2] = (int)cn;
-    cn += c[i];
-    if (bin == hi) sh.pick[3] = (int)cn;
-  }
-  cluster_sync(cs);  // the counts have been read, and the picks are there
-  const unsigned int above = (unsigned int)sh.pick[2];
-  return Window{32 * lo, min(kRange, 32 * (hi + 1)), above, (unsigned int)sh.pick[3] - above, 0.f};
+  cluster_sync(cs);
+  const unsigned int above = (unsigned int)sh.picked[2];
+  return Window{32 * sh.picked[0], min(kRange, 32 * (sh.picked[1] + 1)), above, (unsigned int)sh.picked[3] - above, 0.f};
 }
 
 // The whole cluster: rounds of kBuckets until the want-th token, or (SUMS) the end

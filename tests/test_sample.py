@@ -72,6 +72,20 @@ def test_truncations(q1, V, dtype, std):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [32003, 262144])
+def test_wide_nuclei(q1, V, dtype):
+    # top-p that ends among tokens of tiny weight, flat rows, and large top-k before it
+    x, u, _ = _logits(6, V, dtype, V + 1)
+    p = torch.tensor([0.99, 0.9999, 0.99999, 0.999999, 1 - 2.0 ** -24, 0.5])
+    _compare(q1, x, u, top_p=p)
+    _compare(q1, x, u, top_p=p.flip(0), temperature=50.0)
+    _compare(q1, x, u, top_p=p, temperature=0.05)
+    _compare(q1, x, u, top_k=torch.tensor([1500, 3000, 9000, 20000, 31000, 32002], dtype=torch.int32), top_p=p.flip(0), temperature=3.0)
+    _compare(q1, x, u, top_k=torch.tensor([1025, 2048, 5000, 10000, 20000, 32000], dtype=torch.int32), min_p=1e-4)
+
+
+@pytest.mark.gpu
 def test_ties_go_to_the_lowest_index(q1):
     V = 20000   # more equal logits in one place than the sorted list holds
     x = torch.zeros(8, V)
