@@ -140,17 +140,15 @@ __device__ __forceinline__ uint32_t half2_of(f2 v) {
 // their sum.
 constexpr int kPrepT = 128;
 
-__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
 
 struct PrepShared {
   float D[4][16][20];          // per warp: the diagonal block of A, then its inverse
   float rk[kC], rq[kC];        // factors of the fp16 rows: norm, scale and 2^-e
-  float Gh[kC], Gl[kC];        // log2(e) G = Gh + Gl
-  float beta[kC];
+  // of up to four value heads, a warp each
+  float Gh[4][kC], Gl[4][kC];  // log2(e) G = Gh + Gl
+  float beta[4][kC];
+  int te[4], bump[4];          // T's scale; what positive g add to the bounds' exponents
   float size[4];               // largest key norms (warps 0, 1) and scaled query norms (2, 3)
-  int te, bump;                // T's scale; what positive g add to the bounds' exponents
 };
 
 template <typename T>
@@ -209,42 +207,64 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
   constexpr int kArea = 2 * kKq > 3 * kTile ? 2 * kKq : 3 * kTile;
   __shared__ __align__(128) unsigned char area[kArea];  // K, Q tiles; later T high, P', T low (as in the workspace)
   __shared__ PrepShared sh;
-  unsigned char *kt = area, *qt = area + kKq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t place = blockIdx.x;
   const int hk = blockIdx.y;
-  // the sequence whose places include this one
-  int64_t lo = 0, hi = a.B - 1, t0, t1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) / 2;
-    a.range(mid, t0, t1);
-    if (chunk_base(t0, mid) <= place) lo = mid;
-    else hi = mid - 1;
+  // the sequence whose places include this one: the last that begins at or before it
+  int64_t t0, t1;
+  int64_t seq = 0;
+  for (int64_t end = a.B, step; end - seq > 1; end = min(end, seq + step)) {  // 32 places at once
+    step = (end - seq + 31) / 32;
+    const int64_t b = seq + lane * step;
+    bool at_or_before = false;
+    if (b < end) {
+      a.range(b, t0, t1);
+      at_or_before = chunk_base(t0, b) <= place;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, at_or_before);
+    seq += m ? (31 - __clz(m)) * step : 0;
   }
-  a.range(lo, t0, t1);
-  const int64_t nth = place - chunk_base(t0, lo);
+  a.range(seq, t0, t1);
+  const int64_t nth = place - chunk_base(t0, seq);
   t0 += nth * kC;
   if (nth < 0 || t0 >= t1) return;
   const int len = (int)min((int64_t)kC, t1 - t0);
+  const int group = a.HV / a.HK;
+  // this warp's gates, two tokens per lane: of value head `warp` of the group
+  float gate_g[2], gate_b[2];
+  auto load_gates = [&](int of) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int t = 2 * lane + x;
+      const bool in = t < len && of < group;
+      gate_g[x] = in ? a.g[(t0 + t) * a.g_stride + hk * group + of] : 0.f;
+      gate_b[x] = in ? a.beta[(t0 + t) * a.beta_stride + hk * group + of] : 0.f;
+    }
+  };
+  load_gates(warp);
 
   // ---- K and Q rows -> fp16 tiles; DK/8 lanes per row.  A row's scale brings
   // its norm, and so every value, below 2^15
   constexpr int LPR = DK / 8, RPI = kPrepT / LPR, NI = kC / RPI;
   const int piece = tid % LPR;
+  uint4 raw[2][NI];
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     const int64_t stride = which ? a.q_stride : a.k_stride;
     const T *src = static_cast<const T *>(which ? a.q : a.k) + (t0 + tid / LPR) * stride + (int64_t)hk * DK + piece * 8;
-    uint4 v[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      v[i] = tid / LPR + i * RPI < len ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(i * RPI) * stride)) : make_uint4(0, 0, 0, 0);
-    unsigned char *tile = which ? qt : kt;
+      raw[which][i] =
+          tid / LPR + i * RPI < len ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(i * RPI) * stride)) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    unsigned char *out = ws.kq + ((place * a.HK + hk) * 2 + which) * (int64_t)kKq;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = tid / LPR + i * RPI;
       f2 f[4], s2 = pk(0.f, 0.f);
-      unpack8<T>(v[i], f);
+      unpack8<T>(raw[which][i], f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s2 = fma2(f[e], f[e], s2);
       float ss, sy;
@@ -259,21 +279,18 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       h.y = half2_of(mul2(f[1], sc));
       h.z = half2_of(mul2(f[2], sc));
       h.w = half2_of(mul2(f[3], sc));
-      *reinterpret_cast<uint4 *>(tile + (uint32_t)(piece >> 3) * (kC * 128) + swz(r, piece & 7)) = h;
+      const uint32_t at = (uint32_t)(piece >> 3) * (kC * 128) + swz(r, piece & 7);
+      *reinterpret_cast<uint4 *>(area + which * kKq + at) = h;
+      *reinterpret_cast<uint4 *>(out + at) = h;
       if (piece == 0) (which ? sh.rq : sh.rk)[r] = ss;
     }
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
-  if (tid == 0) {
-    bulk_store(ws.kq + (place * a.HK + hk) * (int64_t)(2 * kKq), smem_u32(area), 2 * kKq);
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  }
   {  // the rows' factors, a thread per row: keys by warps 0 and 1, queries by 2 and 3
     const int which = tid >> 6;
     float &slot = (which ? sh.rq : sh.rk)[tid & 63];
     const float ss = slot;
-    const float n = (a.l2norm ? 1.f / sqrtf(ss + kDeltaEps) : 1.f) * (which ? a.scale : 1.f);
+    const float n = (a.l2norm ? rsqrtf(ss + kDeltaEps) : 1.f) * (which ? a.scale : 1.f);
     slot = n * pow2f(-root_exp(ss));
     float size = fabsf(n) * sqrtf(ss);
 #pragma unroll
@@ -283,7 +300,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 
   // ---- K K^T and Q K^T, columns up to this warp's rows
   float kk[4][2][4] = {}, qk[4][2][4] = {};
-  const uint32_t kt32 = smem_u32(kt), qt32 = smem_u32(qt);
+  const uint32_t kt32 = smem_u32(area), qt32 = kt32 + kKq;
 #pragma unroll
   for (int s = 0; s < DK / 16; ++s) {
     const uint32_t box = (uint32_t)(s >> 2) * (kC * 128);
@@ -303,93 +320,90 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
         mma16(qk[j][1], aq, b[2], b[3]);
       }
   }
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncthreads();  // the tiles' area is free
   const int pe0 = scale_exp(fmaxf(sh.size[0], sh.size[1]) * fmaxf(sh.size[2], sh.size[3])) - 6;  // 2^pe0 |k| |q| below 2^9
   const uint32_t th = smem_u32(area), pt = th + kTile, tl = th + 2 * kTile;
   // the blocks above the diagonal stay zero
   for (int i = tid; i < 3 * kTile / 16; i += kPrepT) reinterpret_cast<uint4 *>(area)[i] = make_uint4(0, 0, 0, 0);
 
-  const int group = a.HV / a.HK;
   const int fr = lane >> 2, fc = 2 * (lane & 3);  // fragment rows fr, fr + 8 of the block; columns 8n + fc, + 1
   // a fragment word (row, columns 8 piece + fc, + 1) of a tile
   auto word_at = [&](uint32_t tile, int row, int pc) { return tile + swz(row, pc) + (uint32_t)fc * 2; };
   auto put = [](uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); };
-  for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
-    float *sc = ws.sc + (place * a.HV + hv) * kScalars;
-    // ---- gates: two tokens per lane of warp 0.  G in fixed point (2^-40):
-    // exact sums, whose differences are taken later
-    if (warp == 0) {
-      float be[2], gv[2];
+  // the gates of value head `of` (this warp's): G in fixed point (2^-40), exact
+  // sums whose differences are taken later; the factors of the chain go out
+  auto gates = [&](int of) {
+    float *sc = ws.sc + (place * a.HV + hk * group + of) * kScalars;
+    const uint32_t nan0 = __ballot_sync(0xffffffffu, gate_g[0] != gate_g[0]), nan1 = __ballot_sync(0xffffffffu, gate_g[1] != gate_g[1]);
+    float up = 0.f;
+    long long gi[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int t = 2 * lane + x;
-        gv[x] = t < len ? a.g[(t0 + t) * a.g_stride + hv] : 0.f;
-        be[x] = t < len ? a.beta[(t0 + t) * a.beta_stride + hv] : 0.f;
-      }
-      const uint32_t nan0 = __ballot_sync(0xffffffffu, gv[0] != gv[0]), nan1 = __ballot_sync(0xffffffffu, gv[1] != gv[1]);
-      float up = 0.f;
-      long long gi[2];
+    for (int x = 0; x < 2; ++x) {
+      // exp(-200) is 0 in fp32 already
+      const float l = fminf(fmaxf(gate_g[x], -200.f), 200.f) * 1.44269504f;
+      up += fmaxf(l, 0.f);
+      gi[x] = __float2ll_rn(l * 1099511627776.f);
+    }
+    long long sum = gi[0] + gi[1];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        // exp(-200) is 0 in fp32 already
-        const float l = fminf(fmaxf(gv[x], -200.f), 200.f) * 1.44269504f;
-        up += fmaxf(l, 0.f);
-        gi[x] = __float2ll_rn(l * 1099511627776.f);
-      }
-      long long sum = gi[0] + gi[1];
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long z = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += z;
+    }
+    float bmax = fmaxf(fabsf(gate_b[0]), fabsf(gate_b[1]));
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long z = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += z;
-      }
-      float bmax = fmaxf(fabsf(be[0]), fabsf(be[1]));
+    for (int o = 16; o > 0; o >>= 1) {
+      up += __shfl_xor_sync(0xffffffffu, up, o);
+      bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, o));
+    }
+    const int bump = (int)ceilf(fminf(up, 20.f));
+    const int te = scale_exp(bmax) - 6 - bump;
+    const long long all = __shfl_sync(0xffffffffu, sum, 31);
+    const long long G[2] = {sum - gi[1], sum};
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        up += __shfl_xor_sync(0xffffffffu, up, o);
-        bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, o));
-      }
-      const int bump = (int)ceilf(fminf(up, 20.f));
-      const int te = scale_exp(bmax) - 6 - bump;
-      const long long all = __shfl_sync(0xffffffffu, sum, 31);
-      const long long G[2] = {sum - gi[1], sum};
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int t = 2 * lane + x;
-        // tokens from the first NaN on
-        const bool bad = (nan0 & ((2u << lane) - 1u)) || (nan1 & (x ? (2u << lane) - 1u : (1u << lane) - 1u));
-        float gh = (float)G[x];
-        const float gl = (float)(G[x] - (long long)gh) * 9.094947017729282e-13f;
-        gh *= 9.094947017729282e-13f;
-        if (bad) gh = __int_as_float(0x7fc00000);
-        sh.Gh[t] = gh;
-        sh.Gl[t] = gl;
-        sh.beta[t] = be[x];
-        const float gam = ex2(gh + gl);
-        const float tail = ex2((float)(all - G[x]) * 9.094947017729282e-13f);
-        sc[t] = gam * sh.rk[t];
-        sc[kC + t] = ((nan0 | nan1) ? __int_as_float(0x7fc00000) : tail) * sh.rk[t] * pow2f(-te);
-        sc[2 * kC + t] = gam * sh.rq[t];
-        if (t == kC - 1) {
-          sc[3 * kC] = gam;
-          sc[3 * kC + 1] = pow2f(-(pe0 - bump)) * pow2f(-te) * 512.f;
-        }
-      }
-      if (lane == 0) {
-        sh.te = te;
-        sh.bump = bump;
+    for (int x = 0; x < 2; ++x) {
+      const int t = 2 * lane + x;
+      // tokens from the first NaN on
+      const bool bad = (nan0 & ((2u << lane) - 1u)) || (nan1 & (x ? (2u << lane) - 1u : (1u << lane) - 1u));
+      float gh = (float)G[x];
+      const float gl = (float)(G[x] - (long long)gh) * 9.094947017729282e-13f;
+      gh *= 9.094947017729282e-13f;
+      if (bad) gh = __int_as_float(0x7fc00000);
+      sh.Gh[warp][t] = gh;
+      sh.Gl[warp][t] = gl;
+      sh.beta[warp][t] = gate_b[x];
+      const float gam = ex2(gh + gl);
+      const float tail = ex2((float)(all - G[x]) * 9.094947017729282e-13f);
+      sc[t] = gam * sh.rk[t];
+      sc[kC + t] = ((nan0 | nan1) ? __int_as_float(0x7fc00000) : tail) * sh.rk[t] * pow2f(-te);
+      sc[2 * kC + t] = gam * sh.rq[t];
+      if (t == kC - 1) {
+        sc[3 * kC] = gam;
+        sc[3 * kC + 1] = pow2f(-(pe0 - bump)) * pow2f(-te) * 512.f;
       }
     }
-    __syncthreads();
-    const float ts = pow2f(sh.te), ps = pow2f(pe0 - sh.bump);
+    if (lane == 0) {
+      sh.te[warp] = te;
+      sh.bump[warp] = bump;
+    }
+  };
+  for (int of = 0; of < group; ++of) {
+    const int at = of & 3, hv = hk * group + of;
+    if (at == 0) {
+      if (of > 0) load_gates(of + warp);
+      if (of + warp < group) gates(of + warp);
+    }
+    __syncthreads();  // the gates are there; the last head's tiles have been copied out
+    const float *Gh = sh.Gh[at], *Gl = sh.Gl[at], *beta = sh.beta[at];
+    const float ts = pow2f(sh.te[at]), ps = pow2f(pe0 - sh.bump[at]);
     // ---- A and P in place of the products' fragments
     f2 A[4][2][2];
     uint32_t Ph[4][4], Pl[kPairP ? 4 : 1][4];
     {
       const int i0 = 16 * warp + fr;
-      const f2 gh[2] = {pk(sh.Gh[i0], sh.Gh[i0]), pk(sh.Gh[i0 + 8], sh.Gh[i0 + 8])};
-      const f2 gl[2] = {pk(sh.Gl[i0], sh.Gl[i0]), pk(sh.Gl[i0 + 8], sh.Gl[i0 + 8])};
-      const float b0 = sh.beta[i0] * sh.rk[i0], b1 = sh.beta[i0 + 8] * sh.rk[i0 + 8];
+      const f2 gh[2] = {pk(Gh[i0], Gh[i0]), pk(Gh[i0 + 8], Gh[i0 + 8])};
+      const f2 gl[2] = {pk(Gl[i0], Gl[i0]), pk(Gl[i0 + 8], Gl[i0 + 8])};
+      const float b0 = beta[i0] * sh.rk[i0], b1 = beta[i0 + 8] * sh.rk[i0 + 8];
       const float q0 = sh.rq[i0] * ps, q1 = sh.rq[i0 + 8] * ps;
       const f2 ba[2] = {pk(b0, b0), pk(b1, b1)}, rq[2] = {pk(q0, q0), pk(q1, q1)}, neg = pk(-1.f, -1.f);
 #pragma unroll
@@ -398,7 +412,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const int c = 16 * j + 8 * n + fc;
-            const f2 ch = lds_pair(&sh.Gh[c]), cl = lds_pair(&sh.Gl[c]);
+            const f2 ch = lds_pair(&Gh[c]), cl = lds_pair(&Gl[c]);
             const f2 rk = lds_pair(&sh.rk[c]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -453,7 +467,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       f2 d[2][2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        const f2 be = mul2(lds_pair(&sh.beta[16 * warp + 8 * n + fc]), pk(ts, ts));
+        const f2 be = mul2(lds_pair(&beta[16 * warp + 8 * n + fc]), pk(ts, ts));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           d[n][e] = lds_pair(&sh.D[warp][fr + 8 * e][8 * n + fc]);
@@ -491,27 +505,24 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       ldsm4t(th + at, bh);
       if (low) ldsm4t(tl + at, bl);
     };
-    // ---- T, block row after block row; P' gathers as the rows come
-    float tv[3][2][4] = {}, pp[4][2][4] = {};
+    // ---- T, block row after block row
+    {
+      float tv[3][2][4] = {};
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      __syncthreads();  // block row m is complete
+      for (int m = 0; m < 3; ++m) {
+        __syncthreads();  // block row m is complete
+        if (m < warp) {
 #pragma unroll
-      for (int c = 0; c <= m; ++c)
-        if (m <= warp) {
-          uint32_t bh[4], bl[4];
-          t_block(m, c, bh, bl, kPairP || m < warp);
+          for (int c = 0; c <= m; ++c) {
+            uint32_t bh[4], bl[4];
+            t_block(m, c, bh, bl, true);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            if (m < 3 && m < warp) mma3(tv[c < 3 ? c : 0][n], yh[m < 3 ? m : 0], yl[m < 3 ? m : 0], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
-            if constexpr (kPairP) mma3(pp[c][n], Ph[m], Pl[m], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
-            else mma16(pp[c][n], Ph[m], bh[2 * n], bh[2 * n + 1]);
+            for (int n = 0; n < 2; ++n) mma3(tv[c][n], yh[m], yl[m], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
           }
         }
-      if (m + 1 == warp) {  // this warp's block row is next
+        if (m + 1 == warp) {  // this warp's block row is next
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
-          if (c <= m) {
+          for (int c = 0; c <= m; ++c)
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -522,28 +533,37 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
                 put(word_at(th, row, pc), h);
                 put(word_at(tl, row, pc), l);
               }
-          }
+        }
       }
     }
+    __syncthreads();
+    // ---- P' = P T
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (c <= warp) {
+        float pp[2][4] = {};
+#pragma unroll
+        for (int m = c; m < 4; ++m)
+          if (m <= warp) {
+            uint32_t bh[4], bl[4];
+            t_block(m, c, bh, bl, kPairP);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              if constexpr (kPairP) mma3(pp[n], Ph[m], Pl[m], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
+              else mma16(pp[n], Ph[m], bh[2 * n], bh[2 * n + 1]);
+            }
+          }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            put(word_at(pt, 16 * warp + fr + 8 * e, 2 * c + n),
-                half2_bits(pp[c][n][2 * e] * (1.f / 512.f), pp[c][n][2 * e + 1] * (1.f / 512.f)));
+            put(word_at(pt, 16 * warp + fr + 8 * e, 2 * c + n), half2_bits(pp[n][2 * e] * (1.f / 512.f), pp[n][2 * e + 1] * (1.f / 512.f)));
       }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    if (tid == 0) {
-      bulk_store(ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile), th, 3 * kTile);
-      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
-    }
-    // the next head's first barrier (after its gates) holds back its stores into the tiles
+    uint4 *dst = reinterpret_cast<uint4 *>(ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile));
+#pragma unroll
+    for (int i = 0; i < 3 * kTile / 16 / kPrepT; ++i) dst[tid + i * kPrepT] = reinterpret_cast<const uint4 *>(area)[tid + i * kPrepT];
   }
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ======================================================================
