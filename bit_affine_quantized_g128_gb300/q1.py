@@ -46,6 +46,7 @@ class _CWeight(ctypes.Structure):
 
 # q1_meta_dtype of the scales/biases tensors
 _META = {torch.float16: 0, torch.bfloat16: 1}
+_F32, _I32 = torch.float32, torch.int32
 
 
 class _CLayer(ctypes.Structure):
@@ -485,16 +486,17 @@ def decode_chain(layers, x: torch.Tensor, workspace=None, out=None) -> torch.Ten
     return y.reshape(*lead, D)
 
 
-def _rows(x: torch.Tensor, name: str, heads: int, dim: int) -> torch.Tensor:
-    """x [T, heads, dim] as rows whose heads are contiguous and 16-byte aligned: x itself where it is (a
-    view of a projection's columns, say), else a contiguous copy."""
-    per16 = 4 if x.dtype == torch.float32 else 8
-    st = x.stride()
-    if (st[2] == 1 and (heads == 1 or st[1] == dim) and st[0] % per16 == 0 and x.data_ptr() % 16 == 0
-            and (x.shape[0] < 2 or st[0] >= heads * dim)):
-        return x
+def _rows(x: torch.Tensor, heads: int, dim: int, per16: int):
+    """x [T, heads, dim] as rows whose heads are contiguous and 16-byte aligned (x itself where it is, a view
+    of a projection's columns say, else a contiguous copy), its pointer and its row stride."""
+    s0, s1, s2 = x.stride()
+    p = x.data_ptr()
+    if s2 == 1 and (s1 == dim or heads == 1) and s0 % per16 == 0 and p % 16 == 0 and s0 >= heads * dim:
+        return x, p, s0
     x = x.contiguous()
-    return x if x.data_ptr() % 16 == 0 else x.clone()
+    if x.data_ptr() % 16:
+        x = x.clone()
+    return x, x.data_ptr(), heads * dim
 
 
 def _vector(t, name: str, n: int, dtype, device) -> Optional[torch.Tensor]:
@@ -525,52 +527,64 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
         _cuda(q, "q")
         for t, name in ((k, "k"), (v, "v"), (g, "g"), (beta, "beta"), (state, "state")):
             _cuda(t, name, q.device, current=False)
-    dev = q.device
-    dt = _x_dtype(q, "q")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    dev, dtype = q.device, q.dtype
+    dt = _DT.get(dtype)
+    if dt is None:
+        _x_dtype(q, "q")
+    if k.dtype != dtype or v.dtype != dtype:
         raise ValueError(f"q, k and v must have one dtype (got {q.dtype}, {k.dtype}, {v.dtype})")
-    if g.dtype != torch.float32 or beta.dtype != torch.float32:
+    if g.dtype != _F32 or beta.dtype != _F32:
         raise ValueError(f"g and beta must be float32 (got {g.dtype}, {beta.dtype})")
-    lead = v.shape[:-2]
+    lead = None
     if cu_seqlens is None:
         if q.dim() != 4 or k.dim() != 4 or v.dim() != 4 or g.dim() != 3 or beta.dim() != 3:
             raise ValueError("without cu_seqlens, q, k, v are [B, L, H, D] and g, beta [B, L, HV]")
-        B, L = int(q.shape[0]), int(q.shape[1])
+        lead = v.shape[:-2]
+        B, max_len = int(q.shape[0]), int(q.shape[1])
         q, k, v, g, beta = (t.flatten(0, 1) for t in (q, k, v, g, beta))
-        max_len = L
     else:
         if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or g.dim() != 2 or beta.dim() != 2:
             raise ValueError("with cu_seqlens, q, k, v are [T, H, D] and g, beta [T, HV]")
         B = cu_seqlens.numel() - 1
-        cu_seqlens = _vector(cu_seqlens, "cu_seqlens", B + 1, torch.int32, dev)
+        cu_seqlens = _vector(cu_seqlens, "cu_seqlens", B + 1, _I32, dev)
     if B < 1:
         raise ValueError("gated_delta needs at least one sequence")
-    T, HK, DK = q.shape
-    HV, DV = v.shape[1], v.shape[2]
-    if tuple(k.shape) != (T, HK, DK) or v.shape[0] != T or tuple(g.shape) != (T, HV) or tuple(beta.shape) != (T, HV):
+    T, HK, DK = qs = q.shape
+    T_v, HV, DV = v.shape
+    if k.shape != qs or T_v != T or g.shape != (T, HV) or beta.shape != (T, HV):
         raise ValueError(f"shapes do not agree: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, "
                          f"g {tuple(g.shape)}, beta {tuple(beta.shape)}")
     if DK not in (64, 128) or DV not in (64, 128) or HK < 1 or HV < 1 or HV % HK:
         raise ValueError(f"need DK and DV of 64 or 128 and HV a multiple of HK (got DK {DK}, DV {DV}, HK {HK}, HV {HV})")
-    if (state.dtype != torch.float32 or state.dim() != 4 or tuple(state.shape[1:]) != (HV, DK, DV)
-            or not state.is_contiguous()):
+    n_slots = len(state) if state.dim() == 4 else 0
+    if state.dtype != _F32 or state.shape != (n_slots, HV, DK, DV) or not state.is_contiguous():
         raise ValueError(f"state must be a contiguous float32 [slots, {HV}, {DK}, {DV}] "
                          f"(got {state.dtype}, {tuple(state.shape)}, contiguous={state.is_contiguous()})")
-    slots = _vector(slots, "slots", B, torch.int32, dev)
-    fresh = _vector(fresh, "fresh", B, torch.int32, dev)
-    if slots is None and state.shape[0] < B:
-        raise ValueError(f"state holds {state.shape[0]} entries for {B} sequences")
-    q, k, v = _rows(q, "q", HK, DK), _rows(k, "k", HK, DK), _rows(v, "v", HV, DV)
-    if g.stride(1) != 1:
+    if slots is not None:
+        slots = _vector(slots, "slots", B, _I32, dev)
+    elif n_slots < B:
+        raise ValueError(f"state holds {n_slots} entries for {B} sequences")
+    if fresh is not None:
+        fresh = _vector(fresh, "fresh", B, _I32, dev)
+    per16 = 4 if dtype == _F32 else 8
+    q, qp, qs0 = _rows(q, HK, DK, per16)
+    k, kp, ks0 = _rows(k, HK, DK, per16)
+    v, vp, vs0 = _rows(v, HV, DV, per16)
+    gs0, gs1 = g.stride()
+    bs0, bs1 = beta.stride()
+    if gs1 != 1 or gs0 < HV:
         g = g.contiguous()
-    if beta.stride(1) != 1:
+        gs0 = HV
+    if bs1 != 1 or bs0 < HV:
         beta = beta.contiguous()
-    o = torch.empty((T, HV, DV), dtype=q.dtype, device=dev) if out is None else _out(out, (T, HV, DV), q.dtype, dev)
+        bs0 = HV
+    o = torch.empty((T, HV, DV), dtype=dtype, device=dev) if out is None else _out(out, (T, HV, DV), dtype, dev)
     a = _CDelta.from_buffer_copy(_CDelta.pack(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(),
-        _ptr(cu_seqlens) or 0, _ptr(slots) or 0, _ptr(fresh) or 0, q.stride(0), k.stride(0), v.stride(0), HV * DV,
-        g.stride(0), beta.stride(0), T, B, state.shape[0], T if max_len is None else int(max_len), HK, HV, DK, DV, dt,
-        1 if qk_l2norm else 0, DK ** -0.5 if scale is None else float(scale)))
+        qp, kp, vp, o.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(),
+        0 if cu_seqlens is None else cu_seqlens.data_ptr(), 0 if slots is None else slots.data_ptr(),
+        0 if fresh is None else fresh.data_ptr(), qs0, ks0, vs0, HV * DV, gs0, bs0, T, B, n_slots,
+        T if max_len is None else max_len, HK, HV, DK, DV, dt, 1 if qk_l2norm else 0,
+        DK ** -0.5 if scale is None else scale))
     L, stream = _lib or lib(), _raw_stream(dev.index)
     if workspace is not None:
         _cuda(workspace, "workspace", dev)
@@ -583,7 +597,16 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
             st = L.q1_gated_delta(a, workspace.data_ptr(), n, stream)
     if st:
         _check("q1_gated_delta", st)
-    return o if o.shape[:-2] == lead else o.reshape(*lead, HV, DV)
+    return o if lead is None else o.reshape(*lead, HV, DV)
+
+
+def _setting(val, name: str, n: int, dtype, device, off):
+    """A sampling setting as (device vector or None, value)."""
+    if val is None:
+        return None, off
+    if isinstance(val, torch.Tensor):
+        return _vector(val, name, n, dtype, device), off
+    return None, val
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None):
@@ -606,22 +629,16 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     u = _vector(u, "u", B, torch.float32, dev)
     if u is None:
         raise ValueError("u must be given")
-    ptrs, vals = [], []
-    for val, name, dtype, off in ((temperature, "temperature", torch.float32, 1.0), (top_p, "top_p", torch.float32, 1.0),
-                                  (min_p, "min_p", torch.float32, 0.0), (top_k, "top_k", torch.int32, 0)):
-        if isinstance(val, torch.Tensor):
-            val = _vector(val, name, B, dtype, dev)
-            ptrs.append(val)
-            vals.append(off)
-        else:
-            ptrs.append(None)
-            vals.append(off if val is None else val)
-    token = torch.empty((B,), dtype=torch.int32, device=dev)
-    prob = torch.empty((B,), dtype=torch.float32, device=dev)
+    t, tv = _setting(temperature, "temperature", B, _F32, dev, 1.0)
+    k, kv = _setting(top_k, "top_k", B, _I32, dev, 0)
+    p, pv = _setting(top_p, "top_p", B, _F32, dev, 1.0)
+    m, mv = _setting(min_p, "min_p", B, _F32, dev, 0.0)
+    token = torch.empty((B,), dtype=_I32, device=dev)
+    prob = torch.empty((B,), dtype=_F32, device=dev)
     a = _CSample.from_buffer_copy(_CSample.pack(
-        logits.data_ptr(), u.data_ptr(), *[0 if p is None else p.data_ptr() for p in ptrs], token.data_ptr(),
-        prob.data_ptr(), B, V, logits.stride(0), dt, max(0, min(int(vals[3]), V)), float(vals[0]), float(vals[1]),
-        float(vals[2])))
+        logits.data_ptr(), u.data_ptr(), 0 if t is None else t.data_ptr(), 0 if p is None else p.data_ptr(),
+        0 if m is None else m.data_ptr(), 0 if k is None else k.data_ptr(), token.data_ptr(), prob.data_ptr(), B, V,
+        logits.stride(0), dt, max(0, min(int(kv), V)), tv, pv, mv))
     st = (_lib or lib()).q1_sample(a, _raw_stream(dev.index))
     if st:
         _check("q1_sample", st)
