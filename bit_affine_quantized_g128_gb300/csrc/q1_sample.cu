@@ -46,7 +46,7 @@ constexpr int kBuckets = 8;          // of a search round
 constexpr int kFirstShift = 12;      // the first round's buckets are 4 octaves wide (the last takes the rest)
 constexpr float kMargin = 1e-4f;     // above the relative errors of the rounds' fp32 weights (5e-6) and sums (2e-5)
 constexpr int kList = 1024;          // at most this many tokens are sorted; a fuller bucket is bisected
-constexpr int kRuns = 8;             // a warp's tokens are summed in this many runs
+constexpr int kRuns = 4;             // a warp's tokens are summed in this many runs
 constexpr float kMagic = 12582912.f; // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
 constexpr int kMagicBits = 0x4B400000;
 constexpr float kDead = kMagic - 1024.f * kOctaves;  // keys below have no weight
@@ -157,10 +157,6 @@ struct Weight {
   uint32_t hi;
   int32_t lo;
   __device__ __forceinline__ u64 whole() const { return ((u64)hi << 22) + (u64)(long long)lo; }
-  __device__ __forceinline__ void add(const Weight &w) {
-    hi += w.hi;
-    lo += w.lo;
-  }
 };
 
 // kMagic + rint(1024 log2 w), monotone in l; below kDead, or NaN, where the
@@ -733,11 +729,12 @@ __device__ Window search(SampleShared &sh, const Slice<T> &slice, const RowScale
   }
 }
 
-// Exact weights over the slice, in runs of each warp: sh.run_sum gets those of
-// tokens above key t_hi, `rest` returns those at or below, and tokens with keys
-// in [t_lo, t_hi] go to rank 0's list.  TESTS: tokens before order value `from`
-// or with less weight than `least` do not count.
-template <typename T, bool WIDE, bool TESTS>
+// Exact weights over the slice, in runs of each warp.  LIST: sh.run_sum gets those
+// of tokens above key t_hi, the result is this thread's weight at or below it, and
+// tokens with keys in [t_lo, t_hi] go to rank 0's list.  Otherwise sh.run_sum gets
+// all.  TESTS: tokens before order value `from` or with less weight than `least`
+// do not count.
+template <typename T, bool WIDE, bool TESTS, bool LIST>
 __device__ u64 exact_pass(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, u64 from, u64 least, float t_lo, float t_hi) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_run = ((slice.size() + kWarps * kRuns - 1) / (kWarps * kRuns) + 31) & ~31;
@@ -752,10 +749,14 @@ __device__ u64 exact_pass(SampleShared &sh, const Slice<T> &slice, const RowScal
       const Weight w = weight_of<WIDE>(rs, sh.exp2, l, t);
       bool live = t >= kDead;
       if (TESTS) live = live && w.whole() >= least && order_value(l, (uint32_t)(slice.first + j)) >= from;
-      if (live && t > t_hi) above.add(w);
-      if (live && !(t > t_hi)) {
-        rest.add(w);
-        if (t >= t_lo) {
+      const bool up = LIST ? live && t > t_hi : live;
+      above.hi += up ? w.hi : 0;
+      above.lo += up ? w.lo : 0;
+      if (LIST) {
+        const bool down = live && !up;
+        rest.hi += down ? w.hi : 0;
+        rest.lo += down ? w.lo : 0;
+        if (down && t >= t_lo) {
           const unsigned int at = atomicAdd(&lead->list_n, 1u);
           if (at < kList) lead->few.list[at] = order_value(l, (uint32_t)(slice.first + j));
         }
@@ -900,10 +901,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const q1_sample_arg
     return rs.wide ? search<T, true, true>(sh, slice, rs, rank, cs, thr, want, share, par)
                    : search<T, false, true>(sh, slice, rs, rank, cs, thr, want, share, par);
   };
-  auto run_exact = [&](u64 from, u64 least, float t_lo, float t_hi) -> u64 {
-    if (rs.wide) return exact_pass<T, true, true>(sh, slice, rs, from, least, t_lo, t_hi);
-    if (from || least) return exact_pass<T, false, true>(sh, slice, rs, from, least, t_lo, t_hi);
-    return exact_pass<T, false, false>(sh, slice, rs, 0, 0, t_lo, t_hi);
+  auto run_exact = [&](u64 from, float t_lo, float t_hi) -> u64 {  // top-p's: with a list
+    if (rs.wide) return exact_pass<T, true, true, true>(sh, slice, rs, from, 0, t_lo, t_hi);
+    if (from) return exact_pass<T, false, true, true>(sh, slice, rs, from, 0, t_lo, t_hi);
+    return exact_pass<T, false, false, true>(sh, slice, rs, 0, 0, t_lo, t_hi);
+  };
+  auto run_kept = [&](u64 from) {
+    if (rs.wide) exact_pass<T, true, true, false>(sh, slice, rs, from, rs.least, 0.f, 0.f);
+    else if (from || rs.least) exact_pass<T, false, true, false>(sh, slice, rs, from, rs.least, 0.f, 0.f);
+    else exact_pass<T, false, false, false>(sh, slice, rs, 0, 0, 0.f, 0.f);
   };
   auto key_at = [&](int d) { return __int_as_float(kMagicBits - d); };
   auto draw = [&](int k, u64 want) {  // rank 0
@@ -955,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const q1_sample_arg
     const Window w = run_search(true, 0, top_p);
     const bool few = w.above + w.in <= (unsigned int)kList, many = !few && w.in > (unsigned int)kList;
     const float t_lo = many ? 2.f * kMagic : key_at(w.d1 - 1), t_hi = few || many ? 2.f * kMagic : key_at(w.d0);
-    const u64 rest = run_exact(thr, 0, t_lo, t_hi);
+    const u64 rest = run_exact(thr, t_lo, t_hi);
     // the weight above the window, and the rest
     u64 mine = 0;
     __syncwarp();
@@ -1021,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const q1_sample_arg
   }
 
   // ---- the kept weight by warp and run, and the draw
-  if (!summed) run_exact(thr, rs.least, 2.f * kMagic, 0.f);
+  if (!summed) run_kept(thr);
   __syncwarp();
   send_sum(sh, lane < kRuns ? sh.run_sum[warp][lane] : 0, 0, rank, cs);
   cluster_sync(cs);
