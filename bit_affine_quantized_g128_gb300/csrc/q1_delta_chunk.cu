@@ -199,7 +199,7 @@ __device__ __forceinline__ void pair_operand(const f2 (&c)[2][2], uint32_t (&h)[
 }
 
 template <typename T, int DK>
-__global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws) {
+__global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws, int heads) {
   // bf16 outputs keep 8 bits: P and T enter P T as single fp16 values (2^-12
   // relative each); for fp16 outputs as pairs
   constexpr bool kPairP = std::is_same<T, __half>::value;
@@ -230,18 +230,19 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
   if (nth < 0 || t0 >= t1) return;
   const int len = (int)min((int64_t)kC, t1 - t0);
   const int group = a.HV / a.HK;
-  // this warp's gates, two tokens per lane: of value head `warp` of the group
+  const int of0 = blockIdx.z * heads, of1 = min(group, of0 + heads);  // this CTA's value heads of the group
+  // this warp's gates, two tokens per lane, of one of them
   float gate_g[2], gate_b[2];
   auto load_gates = [&](int of) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int t = 2 * lane + x;
-      const bool in = t < len && of < group;
+      const bool in = t < len && of < of1;
       gate_g[x] = in ? a.g[(t0 + t) * a.g_stride + hk * group + of] : 0.f;
       gate_b[x] = in ? a.beta[(t0 + t) * a.beta_stride + hk * group + of] : 0.f;
     }
   };
-  load_gates(warp);
+  load_gates(of0 + warp);
 
   // ---- K and Q rows -> fp16 tiles; DK/8 lanes per row.  A row's scale brings
   // its norm, and so every value, below 2^15
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       h.w = half2_of(mul2(f[3], sc));
       const uint32_t at = (uint32_t)(piece >> 3) * (kC * 128) + swz(r, piece & 7);
       *reinterpret_cast<uint4 *>(area + which * kKq + at) = h;
-      *reinterpret_cast<uint4 *>(out + at) = h;
+      if (of0 == 0) *reinterpret_cast<uint4 *>(out + at) = h;
       if (piece == 0) (which ? sh.rq : sh.rk)[r] = ss;
     }
   }
@@ -387,11 +388,11 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       sh.bump[warp] = bump;
     }
   };
-  for (int of = 0; of < group; ++of) {
-    const int at = of & 3, hv = hk * group + of;
+  for (int of = of0; of < of1; ++of) {
+    const int at = (of - of0) & 3, hv = hk * group + of;
     if (at == 0) {
-      if (of > 0) load_gates(of + warp);
-      if (of + warp < group) gates(of + warp);
+      if (of > of0) load_gates(of + warp);
+      if (of + warp < of1) gates(of + warp);
     }
     __syncthreads();  // the gates are there; the last head's tiles have been copied out
     const float *Gh = sh.Gh[at], *Gl = sh.Gl[at], *beta = sh.beta[at];
@@ -1204,8 +1205,12 @@ cudaError_t chunks_t(const DeltaView &a, void *workspace, cudaStream_t st) {
     if (dev < kMaxDevices) sm_count[dev].store(sms, std::memory_order_relaxed);
   }
   const ChunkPlaces ws = places(a, workspace, nullptr);
-  const dim3 grid((unsigned)chunk_places(a.T, a.B), (unsigned)a.HK);
-  delta_prep_kernel<T, DK><<<grid, kPrepT, 0, st>>>(a, ws);
+  // a CTA takes the value heads of a key head one after another, unless that
+  // leaves SMs idle: then a CTA per value head
+  const int64_t n = chunk_places(a.T, a.B);
+  const int group = a.HV / a.HK, heads = n * a.HK <= 2 * sms ? 1 : group;
+  const dim3 grid((unsigned)n, (unsigned)a.HK, (unsigned)((group + heads - 1) / heads));
+  delta_prep_kernel<T, DK><<<grid, kPrepT, 0, st>>>(a, ws, heads);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // half a head per CTA while all of them run at once
