@@ -299,7 +299,16 @@ q1_status q1_decode_chain(const q1_decode_layer *layers, int32_t n_layers, const
  *   fresh       device int32 [B] or NULL: where nonzero, the sequence starts
  *               from zero (its entry is only written).
  *   max_len     the longest sequence (a hint that picks the kernels; results
- *               do not depend on it beyond rounding).
+ *               do not depend on it beyond rounding).  bf16 and fp16 sequences of
+ *               more than 36 tokens (20 with more than 152 heads in the batch) go
+ *               in chunks of 64 tokens on the tensor cores, all others token by
+ *               token.
+ * The state and everything it is made from are computed to fp32 accuracy in both
+ * forms (in chunks: as pairs of fp16 values, relative error below 1e-6 where
+ * beta |k|^2 <= 2); o is rounded to its type once, in chunks of fp16 outputs after
+ * weights of 11 bits.  In the chunked form a NaN or infinity among a sequence's
+ * inputs also reaches the outputs of earlier tokens of its chunk; it never
+ * reaches another sequence.
  * dtype: of q, k, v and o.  g (log decay, at most 0 in use) and beta are fp32.
  * DK and DV 64 or 128; HV a multiple of HK.  q, k, v, o and state 16-byte
  * aligned, q/k/v/o strides multiples of 16 bytes.  o must not overlap the inputs.
