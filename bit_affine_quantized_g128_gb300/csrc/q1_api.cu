@@ -296,8 +296,8 @@ q1_status check_delta(const q1_delta_args *a) {
   if (a->dtype != Q1_BF16 && a->dtype != Q1_F16 && a->dtype != Q1_F32) return Q1_ERR_DTYPE;
   if ((a->DK != 64 && a->DK != 128) || (a->DV != 64 && a->DV != 128)) return Q1_ERR_SHAPE;
   if (a->HK < 1 || a->HV < 1 || a->HV % a->HK != 0 || a->HV > 65535) return Q1_ERR_SHAPE;
-  if (a->T < 0 || a->T > ((int64_t)1 << 31) - 1 || a->B < 1 || a->B > (int64_t)1 << 24 || a->n_slots < 0 ||
-      a->max_len < 0)
+  if (a->T < 0 || a->T > ((int64_t)1 << 31) - 1 || a->B < 1 || a->B > (int64_t)1 << 24 ||
+      a->B * a->HV > (int64_t)1 << 29 || a->n_slots < 0 || a->max_len < 0)
     return Q1_ERR_SHAPE;
   if (!a->cu_seqlens && a->T % a->B != 0) return Q1_ERR_SHAPE;
   if (!a->slots && a->n_slots < a->B) return Q1_ERR_SHAPE;

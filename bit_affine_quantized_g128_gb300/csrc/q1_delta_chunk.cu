@@ -736,16 +736,22 @@ __device__ __forceinline__ void row_max(const f2 *v, float (&m)[4]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) m[i & 3] = max3(m[i & 3], v[i].a, v[i].b);
 }
-__device__ __forceinline__ void row_exps(const float (&m)[4], int (&e)[2]) {
-  float x = fmaxf(m[0], m[2]), y = fmaxf(m[1], m[3]);
+// 2^e that brings the rows' sizes (m, over the four lanes that share them) into
+// [2^14, 2^15), and 2^-e: from the exponent bits.  Sizes below 2^-100 count as that.
+__device__ __forceinline__ void row_scales(const float (&m)[4], float (&up)[2], float (&dn)[2]) {
+  float x[2] = {fmaxf(m[0], m[2]), fmaxf(m[1], m[3])};
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
-    const float x2 = __shfl_xor_sync(0xffffffffu, x, o), y2 = __shfl_xor_sync(0xffffffffu, y, o);
-    x = fmaxf(x, x2);
-    y = fmaxf(y, y2);
+    const float x2 = __shfl_xor_sync(0xffffffffu, x[0], o), y2 = __shfl_xor_sync(0xffffffffu, x[1], o);
+    x[0] = fmaxf(x[0], x2);
+    x[1] = fmaxf(x[1], y2);
   }
-  e[0] = scale_exp(x);
-  e[1] = scale_exp(y);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t e = __float_as_uint(fmaxf(x[h], 7.8886090522101181e-31f)) & 0x7F800000u;
+    up[h] = __uint_as_float((268u << 23) - e);  // 127 + 14 - (e - 127)
+    dn[h] = __uint_as_float(e - (14u << 23));
+  }
 }
 // v (N pairs of values, two rows) times its rows' scales, as high parts at
 // column hi and the negatives of the low parts at column lo.  Scaled values are
@@ -900,10 +906,9 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
       const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
       const uint32_t st = stages + s * St::kBytes, sc = st + St::kSc + 8 * q;
       // 1: the state as the operand of K S and Q S
-      int es[2], er[2], eu[2];
-      row_exps(big, es);
+      float f[2], is[2], ir[2], iu[2];  // a scale of the rows; the reciprocals of S's, R's and c U's
+      row_scales(big, f, is);
       {
-        const float f[2] = {pow2f(es[0]), pow2f(es[1])};
         split_store<NS / 2>(S, f, tl + kColS, tl + kColS + 64);
         publish(&bars->s_ready[0]);
         split_store<NS / 2>(S + NS / 2, f, tl + kColS + NS, tl + kColS + 64 + NS);
@@ -927,17 +932,16 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
       f2 R[16];
       tm_ld(tl + kColKS, R);
       {
-        const f2 ni[2] = {pk(-pow2f(-es[0]), -pow2f(-es[0])), pk(-pow2f(-es[1]), -pow2f(-es[1]))};
+        const f2 ni[2] = {pk(-is[0], -is[0]), pk(-is[1], -is[1])};
 #pragma unroll
         for (int i = 0; i < 16; ++i) R[i] = fma2(mul2(fac[i >> 1], ni[i & 1]), R[i], pair_of<T>(v[i]));
       }
       {
         float m[4] = {};
         row_max<16>(R, m);
-        row_exps(m, er);
+        row_scales(m, f, ir);
       }
       {
-        const float f[2] = {pow2f(er[0]), pow2f(er[1])};
         split_store<8>(R, f, tl + kColR, tl + kColR + 32);
         publish(&bars->r_ready[0]);
         split_store<8>(R + 8, f, tl + kColR + 16, tl + kColR + 48);
@@ -954,10 +958,9 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
       {
         float m[4] = {};
         row_max<16>(R, m);
-        row_exps(m, eu);
+        row_scales(m, f, iu);
       }
       {
-        const float f[2] = {pow2f(eu[0]), pow2f(eu[1])};
         split_store<8>(R, f, tl + kColW, tl + kColW + 32);
         // D overwrites S's operand, which the products with Q read
         if (!(ok = wait_warp(&bars->o_done, ph, bars))) break;
@@ -972,8 +975,7 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
         f2 O[16];
         tm_ld(tl + kColQS, R);
         tm_ld(tl + kColO, O);
-        const float is[2] = {pow2f(-es[0]), pow2f(-es[1])}, ir[2] = {pow2f(-er[0]) * ps, pow2f(-er[1]) * ps};
-        const f2 is2[2] = {pk(is[0], is[0]), pk(is[1], is[1])}, ir2[2] = {pk(ir[0], ir[0]), pk(ir[1], ir[1])};
+        const f2 is2[2] = {pk(is[0], is[0]), pk(is[1], is[1])}, ir2[2] = {pk(ir[0] * ps, ir[0] * ps), pk(ir[1] * ps, ir[1] * ps)};
         if (n > 0 && !(ok = wait_warp(&bars->o_free, ph ^ 1u, bars))) break;
 #pragma unroll
         for (int g = 0; g < 8; g += 2) {
@@ -992,7 +994,7 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
         }
       }
       const float gc = lds1(st + St::kSc + 3 * kC * 4);
-      const float fd[2] = {pow2f(-eu[0]) * pow2f(-er[0]), pow2f(-eu[1]) * pow2f(-er[1])};
+      const float fd[2] = {iu[0] * ir[0], iu[1] * ir[1]};
       fence_before();
       __syncwarp();
       if (lane == 0) {

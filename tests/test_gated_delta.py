@@ -157,6 +157,20 @@ def test_without_norm_and_with_a_scale(q1, lengths):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("decay", ["none", "mixed"])
+def test_keys_that_nearly_stop_contracting(q1, dtype, decay):
+    # beta |k|^2 up to 1.9: a token's own correction overshoots, the state keeps its size
+    q, k, v, g, beta, state, starts = _inputs([200, 50], 2, 4, 128, 128, dtype, 57, decay=decay)
+    k = (k.float() / k.float().norm(dim=-1, keepdim=True) * 1.37).to(DT[dtype])
+    want_o, want_s, colmax = O.gated_delta(_np(q), _np(k), _np(v), _np(g), _np(beta), _np(state), starts, 0.1, False)
+    sd = state.cuda()
+    o = q1.gated_delta(q.cuda(), k.cuda(), v.cuda(), g.cuda(), beta.cuda(), sd, cu_seqlens=torch.from_numpy(starts).cuda(),
+                       max_len=200, scale=0.1)
+    _check(o, sd, want_o, want_s, colmax, q, dtype, starts, 0.1, False, [0, 1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("lengths", [[1, 1, 1, 1], [70, 1, 130, 5]], ids=str)
 def test_slots_fresh_and_missing_entries(q1, lengths):
     _run(q1, lengths, 2, 4, 128, 128, "bf16", seed=9, slots=[5, -1, 2, 0], fresh=[0, 0, 1, 0], pool=7)
