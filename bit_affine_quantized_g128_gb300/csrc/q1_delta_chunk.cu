@@ -583,9 +583,9 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 //     3  c U -> high, low                   MMA: D = (c U)^T K
 //     o = b QS + O2 while D is computed; then S = gamma_C S + D
 //   next warp: copies of the next chunk's tiles, factors and V rows (two stages)
-//   next: tensor memory; issues the MMAs (the whole warp goes through the
-//     issue loop and elect.sync picks the thread: 17 clocks per MMA, against 44
-//     behind an `if (lane == 0)`, whose operands leave the uniform registers)
+//   next: tensor memory; issues the MMAs from the thread that elect.sync picks
+//     (17 clocks per MMA, against 44 behind an `if (lane == 0)`, whose operands
+//     leave the uniform registers)
 //   last: the chunk's rows of o from shared memory, where the chain stages them
 // One chunk is a chain of three dependent products; the time is the latency of
 // that chain, not the rate of any unit.
@@ -660,6 +660,16 @@ __device__ __forceinline__ bool wait_warp(uint64_t *b, uint32_t parity, ChainBar
     ok = ok || mbar_try(b, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
     if ((i & 31u) == 0 && __any_sync(0xffffffffu, give_up(bars, since))) return false;
+  }
+}
+
+// the same for one thread
+__device__ __forceinline__ bool wait_one(uint64_t *b, uint32_t parity, ChainBars *bars) {
+  if (mbar_try(b, parity)) return true;
+  const unsigned long long since = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try(b, parity)) return true;
+    if ((i & 31u) == 0 && give_up(bars, since)) return false;
   }
 }
 
@@ -1062,16 +1072,15 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
       }
     }
   } else if (warp == NW + 1) {
-    for (int n = 0; n < chunks; ++n) {
-      const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
-      const uint32_t kt = stages + s * St::kBytes, qt = kt + St::kKq / 2, tp = kt + St::kTp;
-      if (!wait_warp(&bars->full[s], sph, bars)) break;
-      bool ok = true;
+    if (elect_one()) {
+      for (int n = 0; n < chunks; ++n) {
+        const uint32_t ph = n & 1, s = n & 1, sph = (n >> 1) & 1;
+        const uint32_t kt = stages + s * St::kBytes, qt = kt + St::kKq / 2, tp = kt + St::kTp;
+        bool ok = wait_one(&bars->full[s], sph, bars);
 #pragma unroll
-      for (int h = 0; h < 2 && ok; ++h) {
-        if (!(ok = wait_warp(&bars->s_ready[h], ph, bars))) break;
-        fence_after();
-        if (elect_one()) {
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || !(ok = wait_one(&bars->s_ready[h], ph, bars))) break;
+          fence_after();
 #pragma unroll
           for (int i = 0; i < DK / 32; ++i) {
             const int k = h * (DK / 32) + i;
@@ -1089,13 +1098,10 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
             }
           }
         }
-        __syncwarp();
-      }
 #pragma unroll
-      for (int h = 0; h < 2 && ok; ++h) {
-        if (!(ok = wait_warp(&bars->r_ready[h], ph, bars))) break;
-        fence_after();
-        if (elect_one()) {
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || !(ok = wait_one(&bars->r_ready[h], ph, bars))) break;
+          fence_after();
 #pragma unroll
           for (int k = 2 * h; k < 2 * h + 2; ++k) {
             const uint64_t th = desc_k(tp + k * 32), tl = desc_k(tp + 2 * kTile + k * 32);
@@ -1114,13 +1120,10 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
             umma_commit(&bars->o_done);
           }
         }
-        __syncwarp();
-      }
 #pragma unroll
-      for (int h = 0; h < 2 && ok; ++h) {
-        if (!(ok = wait_warp(&bars->w_ready[h], ph, bars))) break;
-        fence_after();
-        if (elect_one()) {
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || !(ok = wait_one(&bars->w_ready[h], ph, bars))) break;
+          fence_after();
 #pragma unroll
           for (int d = 0; d < DK / 64; ++d) {
 #pragma unroll
@@ -1133,12 +1136,11 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
           }
           if (h == 1) umma_commit(&bars->empty[s]);
         }
-        __syncwarp();
+        if (!ok) break;
       }
-      if (!ok) break;
+      // every MMA issued, complete before the memory it uses is released
+      umma_commit(&bars->drain);
     }
-    // every MMA issued, complete before the memory it uses is released
-    if (elect_one()) umma_commit(&bars->drain);
     __syncwarp();
     const unsigned long long since = global_ns();
     while (!mbar_try(&bars->drain, 0) && global_ns() - since < c_delta_wait_ns) {
