@@ -322,7 +322,7 @@ q1_status check_delta(const q1_delta_args *a) {
 q1::DeltaView delta_view(const q1_delta_args *a) {
   return q1::DeltaView{a->q, a->k, a->v, a->o, a->g, a->beta, a->state, a->cu_seqlens, a->slots, a->fresh,
                        a->q_stride, a->k_stride, a->v_stride, a->o_stride, a->g_stride, a->beta_stride,
-                       a->T, a->B, a->n_slots, a->HK, a->HV, a->DK, a->DV, a->qk_l2norm != 0, a->scale};
+                       a->T, a->B, a->n_slots, a->max_len, a->HK, a->HV, a->DK, a->DV, a->qk_l2norm != 0, a->scale};
 }
 }  // namespace
 

@@ -23,6 +23,8 @@
 // is rounded to 16 bits, not a state.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "q1_internal.h"
@@ -51,6 +53,17 @@ struct ChunkPlaces {
   unsigned char *kq;  // [chunks][HK] K tile, Q tile: 64 x DK fp16 each
   unsigned char *tp;  // [chunks][HV] T high, P', T low: 64 x 64 fp16 each
   float *sc;          // [chunks][HV][kScalars]
+  // between slabs, where there are any (batches that the chain does not sort):
+  // the states [B][HV][DK][DV], and per 16 state columns [B][HV][DV / 16]
+  // whether a wait for them ran out
+  float *carry;
+  int *failed;
+};
+// The chunks [first, end) of every sequence, which one launch of each kernel
+// does; more: another slab follows, whose chunk kernel may run beside this one's
+// chain.
+struct Slab {
+  int first, end, more;
 };
 __host__ __device__ inline int64_t chunk_places(int64_t T, int64_t B) { return T / kC + B + 1; }
 
@@ -199,7 +212,7 @@ __device__ __forceinline__ void pair_operand(const f2 (&c)[2][2], uint32_t (&h)[
 }
 
 template <typename T, int DK>
-__global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws, int heads) {
+__global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws, const Slab slab, int heads) {
   // bf16 outputs keep 8 bits: P and T enter P T as single fp16 values (2^-12
   // relative each); for fp16 outputs as pairs
   constexpr bool kPairP = std::is_same<T, __half>::value;
@@ -227,7 +240,17 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
   a.range(seq, t0, t1);
   const int64_t nth = place - chunk_base(t0, seq);
   t0 += nth * kC;
-  if (nth < 0 || t0 >= t1) return;
+  // A later slab's grid starts beside the chain of the slab before it and writes
+  // only what that chain does not touch; one of its CTAs ends after that chain,
+  // so that the next chain, which follows this grid, follows both.
+  auto leave = [&] {
+    if (slab.first > 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
+  if (nth < slab.first || nth >= slab.end || t0 >= t1) {
+    leave();
+    return;
+  }
   const int len = (int)min((int64_t)kC, t1 - t0);
   const int group = a.HV / a.HK;
   const int of0 = blockIdx.z * heads, of1 = min(group, of0 + heads);  // this CTA's value heads of the group
@@ -565,6 +588,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 #pragma unroll
     for (int i = 0; i < 3 * kTile / 16 / kPrepT; ++i) dst[tid + i * kPrepT] = reinterpret_cast<const uint4 *>(area)[tid + i * kPrepT];
   }
+  leave();
 }
 
 // ======================================================================
@@ -820,7 +844,8 @@ __device__ __forceinline__ float lds1(uint32_t addr) {
 }
 
 template <typename T, int DK, int M>
-__global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_kernel(const DeltaView a, const ChunkPlaces ws, int sort) {
+__global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_kernel(const DeltaView a, const ChunkPlaces ws, const Slab slab, int sort) {
+  if (slab.more) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ unsigned char smem_raw[];
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   using St = ChainStage<DK, M>;
@@ -853,8 +878,9 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
   }
   int64_t t0, t1;
   a.range(b, t0, t1);
-  const int chunks = (int)((t1 - t0 + kC - 1) / kC);
-  const int64_t place0 = chunk_base(t0, b);
+  const int64_t place0 = chunk_base(t0, b) + slab.first;
+  t0 = min(t0 + (int64_t)slab.first * kC, t1);
+  const int chunks = (int)min((t1 - t0 + kC - 1) / kC, (int64_t)slab.end - slab.first);
   // bf16 outputs keep 8 bits: the low parts of S and R are left out of their
   // products with Q and P' (2^-12 relative), which they are needed in for fp16
   constexpr bool kLowInO = std::is_same<T, __half>::value;
@@ -894,13 +920,15 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
     const uint32_t tl = tmem + ((uint32_t)(M == 128 ? L0 : 32 * warp) << 16);
     const int64_t slot = a.slots ? a.slots[b] : b;
     const bool have = slot >= 0 && slot < a.n_slots;
-    float *state = a.state + ((have ? slot : 0) * a.HV + hv) * (int64_t)DK * a.DV + (int64_t)(2 * q) * a.DV + c;
+    const int64_t mine = (int64_t)(2 * q) * a.DV + c;
+    float *state = a.state + ((have ? slot : 0) * a.HV + hv) * (int64_t)DK * a.DV + mine;
     constexpr int NS = DK / 4;  // pairs of state values per thread: S[2g + h] = key entries 8g + 2q, + 1 of column c + 8h
     f2 S[NS];
-    const bool load = have && !(a.fresh && a.fresh[b]);
+    const bool load = slab.first > 0 || (have && !(a.fresh && a.fresh[b]));
+    const float *from = slab.first > 0 ? ws.carry + (int64_t)(blockIdx.x / parts) * DK * a.DV + mine : state;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const float *p = state + (int64_t)(8 * (i >> 1)) * a.DV + 8 * (i & 1);
+      const float *p = from + (int64_t)(8 * (i >> 1)) * a.DV + 8 * (i & 1);
       S[i] = load ? pk(p[0], p[a.DV]) : pk(0.f, 0.f);
     }
     float big[4] = {};
@@ -1026,10 +1054,16 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
       }
       if (!ok) break;
     }
-    if (ok && have) {
+    int *failed = ws.failed + ((int64_t)(blockIdx.x / parts) * a.DV + dv0 + L0) / 16;
+    if (slab.first > 0 && *failed) ok = false;  // the state keeps its value
+    __syncwarp();
+    if (slab.more || (ok && have)) {
+      // (not kept over the walk: its registers are worth 1 %)
+      float *to = slab.more ? ws.carry + ((int64_t)(blockIdx.x / parts) * DK + 2 * q) * a.DV + c : state;
+      if (slab.more && lane == 0) *failed = !ok;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        float *p = state + (int64_t)(8 * (i >> 1)) * a.DV + 8 * (i & 1);
+        float *p = to + (int64_t)(8 * (i >> 1)) * a.DV + 8 * (i & 1);
         p[0] = S[i].a;
         p[a.DV] = S[i].b;
       }
@@ -1174,16 +1208,26 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+constexpr int64_t kSlabCtas = 76;  // half of the 152 SMs
+// Half a head per CTA: heads of 64 columns, or while all of them run at once.
+bool half_heads(const DeltaView &a, int64_t sms) { return a.DV == 64 || 2 * a.B * a.HV <= sms; }
+// Whether the chain leaves half of the SMs idle, on which the chunk kernel of a
+// later slab then runs.
+bool can_slab(const DeltaView &a) { return a.B * a.HV * (a.DV / 64) <= kSlabCtas; }
+
 ChunkPlaces places(const DeltaView &a, void *ws, size_t *total) {
   const size_t n = (size_t)chunk_places(a.T, a.B);
   const size_t kq = up256(n * a.HK * (size_t)(2 * kC * a.DK * 2)), tp = up256(n * a.HV * (size_t)(3 * kTile));
   unsigned char *p = static_cast<unsigned char *>(ws);
-  if (total) *total = kq + tp + up256(n * a.HV * (size_t)kScalarBytes);
-  return ChunkPlaces{p, p + kq, reinterpret_cast<float *>(p + kq + tp)};
+  const size_t sc = up256(n * a.HV * (size_t)kScalarBytes), st = (size_t)(a.B * a.HV) * a.DK * a.DV * 4;
+  if (total) *total = kq + tp + sc + (can_slab(a) ? st + (size_t)(a.B * a.HV) * (a.DV / 16) * 4 : 0);
+  unsigned char *carry = p + kq + tp + sc;
+  return ChunkPlaces{p, p + kq, reinterpret_cast<float *>(p + kq + tp), reinterpret_cast<float *>(carry),
+                     reinterpret_cast<int *>(carry + st)};
 }
 
 template <typename T, int DK, int M>
-cudaError_t chain_t(const DeltaView &a, const ChunkPlaces &ws, int64_t sms, cudaStream_t st) {
+cudaError_t chain_t(const DeltaView &a, const ChunkPlaces &ws, const Slab &slab, int64_t sms, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   const int dev = current_device();
   if (not_done(ready, dev)) {
@@ -1194,7 +1238,7 @@ cudaError_t chain_t(const DeltaView &a, const ChunkPlaces &ws, int64_t sms, cuda
   }
   const int64_t ctas = a.B * a.HV * (a.DV / M);
   const int sort = a.cu && a.B > 1 && a.B <= kSortMax && ctas > sms;
-  delta_chain_kernel<T, DK, M><<<(unsigned)ctas, ChainStage<DK, M>::kThreads, chain_smem<DK, M>(), st>>>(a, ws, sort);
+  delta_chain_kernel<T, DK, M><<<(unsigned)ctas, ChainStage<DK, M>::kThreads, chain_smem<DK, M>(), st>>>(a, ws, slab, sort);
   return cudaGetLastError();
 }
 
@@ -1213,13 +1257,41 @@ cudaError_t chunks_t(const DeltaView &a, void *workspace, cudaStream_t st) {
   // leaves SMs idle: then a CTA per value head
   const int64_t n = chunk_places(a.T, a.B);
   const int group = a.HV / a.HK, heads = n * a.HK <= 2 * sms ? 1 : group;
-  const dim3 grid((unsigned)n, (unsigned)a.HK, (unsigned)((group + heads - 1) / heads));
-  delta_prep_kernel<T, DK><<<grid, kPrepT, 0, st>>>(a, ws, heads);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // half a head per CTA while all of them run at once
-  if (a.DV == 64 || 2 * a.B * a.HV <= sms) return chain_t<T, DK, 64>(a, ws, sms, st);
-  return chain_t<T, DK, 128>(a, ws, sms, st);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)n, (unsigned)a.HK, (unsigned)((group + heads - 1) / heads));
+  cfg.blockDim = dim3(kPrepT);
+  cfg.stream = st;
+  cudaLaunchAttribute beside;
+  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  beside.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &beside;  // of the later slabs' launches
+  // Slabs of 1, 2, 4, ... parts: only the first one's chunk kernel is waited for,
+  // and the others', on the half of the SMs that the chain leaves, keep ahead of
+  // it.  A further slab costs 9 us (two launches, the state out and in), so their
+  // number goes by the chunk kernel's work, in chunks times heads.  Times in us
+  // with 1, 2, 3, 4 slabs (bf16, heads of 128 x 128):
+  //   16 heads,  4096 tokens (1024)    174   173   178   183
+  //   32 heads,  2048 tokens (1024)    106   107   116   128
+  //   32 heads,  4096 tokens (2048)    203   187   191   201
+  //   32 heads,  8192 tokens (4096)    396   356   346   351
+  //   32 heads, 32768 tokens (16384)  1539  1377  1330  1308
+  const int64_t chunks = (std::min(a.max_len, a.T) + kC - 1) / kC;
+  const int64_t work = std::min(chunks * a.B, n) * a.HV;
+  const int slabs = !can_slab(a) || 2 * kSlabCtas > sms || work <= 1024 ? 1 : work <= 2600 ? 2 : work <= 6400 ? 3 : 4;
+  const int parts = (1 << slabs) - 1;
+  Slab slab = {0, 0, 0};
+  for (int i = 0; i < slabs; ++i) {
+    slab.first = slab.end;
+    slab.more = i + 1 < slabs;
+    slab.end = slab.more ? (int)(chunks * ((2 << i) - 1) / parts) : INT_MAX;
+    cfg.numAttrs = i > 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, delta_prep_kernel<T, DK>, a, ws, slab, heads);
+    if (e != cudaSuccess) return e;
+    // half a head per CTA while all of them run at once
+    e = half_heads(a, sms) ? chain_t<T, DK, 64>(a, ws, slab, sms, st) : chain_t<T, DK, 128>(a, ws, slab, sms, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace

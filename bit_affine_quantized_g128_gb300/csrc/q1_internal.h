@@ -103,7 +103,7 @@ struct DeltaView {
   float *state;
   const int32_t *cu, *slots, *fresh;
   int64_t q_stride, k_stride, v_stride, o_stride, g_stride, beta_stride;
-  int64_t T, B, n_slots;
+  int64_t T, B, n_slots, max_len;
   int HK, HV, DK, DV;
   int l2norm;
   float scale;

@@ -289,6 +289,88 @@ def test_stalled_copies_time_out_and_recover(q1):
     assert q1.device_errors() == 0
 
 
+def _long(lengths, HK, HV, DK, DV, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    T = sum(lengths)
+    q, k = (torch.randn(T, HK, DK, generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    v = torch.randn(T, HV, DV, generator=g).to(DT[dtype]).cuda()
+    gate, beta = -0.2 * torch.rand(T, HV, generator=g).cuda(), torch.rand(T, HV, generator=g).cuda()
+    state = 0.3 * torch.randn(len(lengths) + 1, HV, DK, DV, generator=g).cuda()
+    cu = torch.tensor([0] + list(np.cumsum(lengths)), dtype=torch.int32, device="cuda")
+    return (q, k, v, gate, beta), state, cu
+
+
+# few heads and many chunks: done in two, three or four slabs, whose chunk
+# kernels run beside the chain; a hint of 64 tokens gives one slab
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths,HK,HV,DK,DV,dtype", [
+    ([2113], 16, 32, 128, 128, "bf16"), ([2113], 32, 32, 64, 64, "fp16"), ([5300], 8, 32, 128, 128, "fp16"),
+    ([13000], 8, 32, 128, 64, "bf16"), ([40, 8200, 0, 1500], 3, 9, 128, 128, "bf16"), ([17000], 2, 38, 64, 128, "bf16"),
+    ([3000, 64, 3000], 4, 24, 128, 64, "fp16")], ids=str)
+def test_slabs_equal_one_walk(q1, lengths, HK, HV, DK, DV, dtype):
+    args, state, cu = _long(lengths, HK, HV, DK, DV, dtype, seed=71)
+    B = len(lengths)
+    slots = torch.tensor([B, -1, 0, 1][:B], dtype=torch.int32, device="cuda")  # the second has none
+    for fresh in (None, torch.tensor([1, 1, 0, 0][:B], dtype=torch.int32, device="cuda")):
+        kw = dict(cu_seqlens=cu, slots=slots, fresh=fresh, qk_l2norm=True)
+        s0, s1, s2 = state.clone(), state.clone(), state.clone()
+        o0 = q1.gated_delta(*args, s0, max_len=64, **kw)
+        o1 = q1.gated_delta(*args, s1, max_len=max(lengths), **kw)
+        o2 = q1.gated_delta(*args, s2, **kw)
+        assert torch.isfinite(o0.float()).all()
+        assert torch.equal(o0, o1) and torch.equal(s0, s1)
+        assert torch.equal(o0, o2) and torch.equal(s0, s2)
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_slabs_against_the_oracle(q1):
+    _run(q1, [2100], 2, 38, 64, 64, "bf16", seed=73)
+
+
+@pytest.mark.gpu
+def test_slabs_one_call_after_another(q1):
+    # calls that share one workspace, without a wait between them, and in a graph
+    args, state, cu = _long([4500], 16, 32, 128, 128, "bf16", seed=79)
+    other, _, _ = _long([4500], 16, 32, 128, 128, "bf16", seed=83)
+    want, ws = state.clone(), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    outs = [q1.gated_delta(*x, want, cu_seqlens=cu, max_len=64, qk_l2norm=True) for x in (args, other, args, other)]
+    got = state.clone()
+    again = [q1.gated_delta(*x, got, cu_seqlens=cu, max_len=4500, qk_l2norm=True, workspace=ws)
+             for x in (args, other, args, other)]
+    assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(outs, again))
+    graph, got = torch.cuda.CUDAGraph(), state.clone()
+    with torch.cuda.graph(graph):
+        again = [q1.gated_delta(*x, got, cu_seqlens=cu, max_len=4500, qk_l2norm=True, workspace=ws)
+                 for x in (args, other, args, other)]
+    for _ in range(2):
+        got.copy_(state)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(outs, again))
+
+
+@pytest.mark.gpu
+def test_stalled_copies_in_slabs_keep_the_states(q1):
+    args, state, cu = _long([5300], 8, 32, 128, 128, "bf16", seed=89)
+    want, sd = state.clone(), state.clone()
+    o = q1.gated_delta(*args, want, cu_seqlens=cu, max_len=5300, qk_l2norm=True)
+    assert q1.device_errors() == 0
+    try:
+        q1.set_wait_limit_ns(1_000_000)
+        q1.set_stalled_producers(True)
+        q1.gated_delta(*args, sd, cu_seqlens=cu, max_len=5300, qk_l2norm=True)
+        torch.cuda.synchronize()
+        assert q1.device_errors() == 4
+        assert torch.equal(sd, state)
+    finally:
+        q1.set_stalled_producers(False)
+        q1.set_wait_limit_ns(0)
+    again = q1.gated_delta(*args, sd, cu_seqlens=cu, max_len=5300, qk_l2norm=True)
+    assert torch.equal(o, again) and torch.equal(sd, want)
+    assert q1.device_errors() == 0
+
+
 # ---- refusals (no GPU needed: validation comes before the library)
 @pytest.fixture
 def fake(monkeypatch):
