@@ -24,6 +24,11 @@ namespace {
 // it was last folded in: a token then costs one multiply-add per state value
 // for the update, as for each of the two reductions.  CTAs are two warps (32
 // columns), so that one sequence of 32 heads spreads over 128 SMs.
+//
+// Bound by the state's bytes for one token: 64 sequences of 32 heads (128 x 128)
+// move 270 MB in 44.4 us, 6.1 TB/s, 90 % of a plain copy; one sequence takes 2.8
+// us, the launch.  Over several tokens by instruction issue: 8 sequences of 48
+// heads and 8 tokens take 18.6 us (29 us with barriers between warps).
 constexpr int kStepThreads = 64;
 constexpr int kStepCols = 32;
 constexpr int kStepGroups = 8;

@@ -25,6 +25,11 @@
 // one CTA finishes the row from a list of them; otherwise a pass with exact
 // weights sums those above the bins in question and lists the tokens in them,
 // which are sorted for the last one kept.
+//
+// Bound by latency for few rows (one row of a large vocabulary: 15 us, ten
+// dependent steps over 16 CTAs; top-k near 1000 with top-p: 43 us) and by
+// instruction issue for many: 28 us for 64 rows (48 instructions per token, 31 of
+// them the exact weight), 51 us for 301 rows of 32003 tokens (108 per token).
 #include <cuda_bf16.h>
 
 #include <type_traits>
