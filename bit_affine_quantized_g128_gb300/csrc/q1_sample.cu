@@ -508,7 +508,9 @@ __device__ void draw_from_short_list(SampleShared &sh, const RowScale &rs, int t
 
 // The whole cluster, where too many tokens are left for a list: bit by bit, the
 // largest order value with enough tokens (or weight) at or above it.  Bits
-// 31..18 are set in every value (indices are below 2^18).
+// 31..18 are set in every value (indices are below 2^18).  It writes both slots of
+// part_sum: what the caller read of them has to lie behind a barrier of the
+// cluster.  Its last round reads slot 1, so slot 0 may be written after it.
 template <typename T>
 __device__ u64 bisect(SampleShared &sh, const Slice<T> &slice, const RowScale &rs, uint32_t rank, int cs, u64 from, bool by_sum,
                       u64 need) {
@@ -1027,7 +1029,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const q1_sample_arg
         summed = true;
       }
     }
-    if (!last) last = bisect(sh, slice, rs, rank, cs, thr, true, want);
+    if (!last) {
+      cluster_sync(cs);  // every CTA has read the sums above
+      last = bisect(sh, slice, rs, rank, cs, thr, true, want);
+    }
     thr = max(thr, last);
   }
 

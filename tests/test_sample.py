@@ -104,6 +104,33 @@ def test_ties_go_to_the_lowest_index(q1):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V", [1030, 2100, 20000])
+def test_nuclei_of_equal_logits_many_times(q1, V):
+    # top-p that ends among more equal logits than the sorted list holds: every CTA of
+    # a row forms the same sums before they go on to bisect for the end.  Short slices
+    # leave the least time between the two; enough rows run to fill the GPU.
+    for B in (1, 64, 400):
+        x = torch.zeros(B, V)
+        x[:, 0] = (torch.arange(B) % 3).float()          # rows differ
+        u = (0.137 + 0.7548776662 * torch.arange(B)) % 1.0
+        p = 0.2 + 0.6 * ((torch.arange(B) * 0.6180339887) % 1.0)
+        # one weight of exp(l_0) at index 0, then V - 1 ones: the kept ones are 0 .. n - 1
+        # (all rows' sums are far from a border between two tokens: checked here)
+        w0 = torch.exp(x[:, 0].double())
+        total = w0 + (V - 1)
+        over = p.float().double() * total - w0           # ones needed beyond index 0
+        assert ((over - over.round()).abs() > 2e-6).all()
+        kept = w0 + torch.ceil(over).clamp(min=0)
+        at = u.float().double() * kept - w0
+        assert ((at - at.round()).abs() > 2e-6).all()
+        want = torch.where(at < 0, 0.0, torch.floor(at) + 1).int()
+        xd, ud, pd = x.cuda(), u.cuda(), p.cuda()
+        for _ in range(20):
+            token, _ = q1.sample(xd, ud, top_p=pd)
+            assert torch.equal(token.cpu(), want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_masked_rows(q1, dtype):
     V, inf = 3000, float("inf")
