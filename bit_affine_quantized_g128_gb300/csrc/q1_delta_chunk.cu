@@ -13,14 +13,16 @@
 //
 // Operand precision.  The state is fp32 and goes through one product per
 // chunk, so operands rounded to 16 bits once would leave it 2^-9 or 2^-12 off.
-// Every fp32 operand (S, R, the scaled U, T) is a sum of two fp16 values
-// instead, high and low, 22 bits together, scaled by a power of two (per row
-// of the operand, or per tile) so that its largest value lies in
-// [2^14, 2^15): the products with both halves are exact in fp32 up to its own
-// rounding.  Keys and queries enter as single fp16 values, scaled per row:
-// bf16 and fp16 inputs are exact in them down to 2^-28 of the row's largest
-// value.  P' is a single fp16 (2^-11 relative): its product is an output that
-// is rounded to 16 bits, not a state.
+// Nor is o served by them, though it is rounded to 16 bits in the end: where a
+// token overwrites what the state held under its key, Q S and P' R cancel, and what
+// is left can be any number of times smaller than both.  So every fp32 operand
+// (S, R, the scaled U, T, P') is a sum of two fp16 values, high and low, 22
+// bits of each value together, scaled by a power of two (per row of the operand,
+// or per tile) so that the largest lies in [2^14, 2^15); what lies 2^-17 or
+// more below it keeps fewer bits, down to 2^-39 of it.  Products are exact in fp32
+// up to its own rounding; those of two low parts are left out (2^-21).  Keys and
+// queries enter as single fp16 values, scaled per row: bf16 and fp16 inputs are exact
+// in them down to 2^-28 of the row's largest value.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -41,6 +43,7 @@ constexpr int kC = 64;                       // tokens of a chunk
 constexpr int kTile = kC * kC * 2;           // bytes of a 64 x 64 fp16 tile
 constexpr int kScalars = 3 * kC + 16;        // floats: a, c, b, then gamma_C and P's scale
 constexpr int kScalarBytes = kScalars * 4;
+constexpr int kTiles = 4 * kTile;            // T high, T low, P' high, P' low
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -51,7 +54,7 @@ __device__ __forceinline__ int64_t chunk_base(int64_t t0, int64_t b) { return t0
 
 struct ChunkPlaces {
   unsigned char *kq;  // [chunks][HK] K tile, Q tile: 64 x DK fp16 each
-  unsigned char *tp;  // [chunks][HV] T high, P', T low: 64 x 64 fp16 each
+  unsigned char *tp;  // [chunks][HV] T high, T low, P' high, P' low: 64 x 64 fp16 each
   float *sc;          // [chunks][HV][kScalars]
   // between slabs, where there are any (batches that the chain does not sort):
   // the states [B][HV][DK][DV], and per 16 state columns [B][HV][DV / 16]
@@ -218,12 +221,9 @@ __device__ __forceinline__ void pair_operand(const f2 (&c)[2][2], uint32_t (&h)[
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a, const ChunkPlaces ws, const Slab slab, int heads) {
-  // bf16 outputs keep 8 bits: P and T enter P T as single fp16 values (2^-12
-  // relative each); for fp16 outputs as pairs
-  constexpr bool kPairP = std::is_same<T, __half>::value;
   constexpr int kKq = kC * DK * 2;  // bytes of a K or Q tile
-  constexpr int kArea = 2 * kKq > 3 * kTile ? 2 * kKq : 3 * kTile;
-  __shared__ __align__(128) unsigned char area[kArea];  // K, Q tiles; later T high, P', T low (as in the workspace)
+  constexpr int kArea = 2 * kKq > kTiles ? 2 * kKq : kTiles;
+  __shared__ __align__(128) unsigned char area[kArea];  // K, Q tiles; later T and P' (as in the workspace)
   __shared__ PrepShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t place = blockIdx.x;
@@ -351,9 +351,9 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
   }
   __syncthreads();  // the tiles' area is free
   const int pe0 = scale_exp(fmaxf(sh.size[0], sh.size[1]) * fmaxf(sh.size[2], sh.size[3])) - 6;  // 2^pe0 |k| |q| below 2^9
-  const uint32_t th = smem_u32(area), pt = th + kTile, tl = th + 2 * kTile;
+  const uint32_t th = smem_u32(area), tl = th + kTile, ph = th + 2 * kTile, pl = th + 3 * kTile;
   // the blocks above the diagonal stay zero
-  for (int i = tid; i < 3 * kTile / 16; i += kPrepT) reinterpret_cast<uint4 *>(area)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < kTiles / 16; i += kPrepT) reinterpret_cast<uint4 *>(area)[i] = make_uint4(0, 0, 0, 0);
 
   const int fr = lane >> 2, fc = 2 * (lane & 3);  // fragment rows fr, fr + 8 of the block; columns 8n + fc, + 1
   // a fragment word (row, columns 8 piece + fc, + 1) of a tile
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
     const float ts = pow2f(sh.te[at]), ps = pow2f(pe0 - sh.bump[at]);
     // ---- A and P in place of the products' fragments
     f2 A[4][2][2];
-    uint32_t Ph[4][4], Pl[kPairP ? 4 : 1][4];
+    uint32_t Ph[4][4], Pl[4][4];
     {
       const int i0 = 16 * warp + fr;
       const f2 gh[2] = {pk(Gh[i0], Gh[i0]), pk(Gh[i0 + 8], Gh[i0 + 8])};
@@ -460,8 +460,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
                 *reinterpret_cast<float2 *>(&sh.D[warp][i][cc]) = make_float2(av.a, av.b);
               }
               A[j][n][e] = av;
-              if constexpr (kPairP) split2(pv.a, pv.b, Ph[j][2 * n + e], Pl[j][2 * n + e]);
-              else Ph[j][2 * n + e] = half2_of(pv);
+              split2(pv.a, pv.b, Ph[j][2 * n + e], Pl[j][2 * n + e]);
             }
           }
         }
@@ -529,10 +528,10 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
         pair_operand(y, yh[m], yl[m]);
       }
     // the operand pair of block (m, c) of T, as rows along the contraction
-    auto t_block = [&](int m, int c, uint32_t (&bh)[4], uint32_t (&bl)[4], bool low) {
+    auto t_block = [&](int m, int c, uint32_t (&bh)[4], uint32_t (&bl)[4]) {
       const uint32_t at = swz(16 * m + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * c + (lane >> 4));
       ldsm4t(th + at, bh);
-      if (low) ldsm4t(tl + at, bl);
+      ldsm4t(tl + at, bl);
     };
     // ---- T, block row after block row
     {
@@ -544,7 +543,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 #pragma unroll
           for (int c = 0; c <= m; ++c) {
             uint32_t bh[4], bl[4];
-            t_block(m, c, bh, bl, true);
+            t_block(m, c, bh, bl);
 #pragma unroll
             for (int n = 0; n < 2; ++n) mma3(tv[c][n], yh[m], yl[m], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
           }
@@ -575,23 +574,24 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
         for (int m = c; m < 4; ++m)
           if (m <= warp) {
             uint32_t bh[4], bl[4];
-            t_block(m, c, bh, bl, kPairP);
+            t_block(m, c, bh, bl);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              if constexpr (kPairP) mma3(pp[n], Ph[m], Pl[m], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
-              else mma16(pp[n], Ph[m], bh[2 * n], bh[2 * n + 1]);
-            }
+            for (int n = 0; n < 2; ++n) mma3(pp[n], Ph[m], Pl[m], bh[2 * n], bh[2 * n + 1], bl[2 * n], bl[2 * n + 1]);
           }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            put(word_at(pt, 16 * warp + fr + 8 * e, 2 * c + n), half2_bits(pp[n][2 * e] * (1.f / 512.f), pp[n][2 * e + 1] * (1.f / 512.f)));
+          for (int e = 0; e < 2; ++e) {
+            uint32_t h, l;
+            split2(pp[n][2 * e] * (1.f / 512.f), pp[n][2 * e + 1] * (1.f / 512.f), h, l);
+            put(word_at(ph, 16 * warp + fr + 8 * e, 2 * c + n), h);
+            put(word_at(pl, 16 * warp + fr + 8 * e, 2 * c + n), l);
+          }
       }
     __syncthreads();
-    uint4 *dst = reinterpret_cast<uint4 *>(ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile));
+    uint4 *dst = reinterpret_cast<uint4 *>(ws.tp + (place * a.HV + hv) * (int64_t)kTiles);
 #pragma unroll
-    for (int i = 0; i < 3 * kTile / 16 / kPrepT; ++i) dst[tid + i * kPrepT] = reinterpret_cast<const uint4 *>(area)[tid + i * kPrepT];
+    for (int i = 0; i < kTiles / 16 / kPrepT; ++i) dst[tid + i * kPrepT] = reinterpret_cast<const uint4 *>(area)[tid + i * kPrepT];
   }
   leave();
 }
@@ -645,7 +645,7 @@ struct ChainStage {
   static constexpr int kWarps = M / 16, kThreads = 32 * (kWarps + 3);
   static constexpr int kRow = M * 2 + 16;  // bytes of a staged row of V or o: 8 rows at one column fall into different banks
   static constexpr int kKq = 2 * kC * DK * 2;
-  static constexpr int kTp = kKq, kV = kTp + 3 * kTile, kSc = kV + kC * kRow;
+  static constexpr int kTp = kKq, kV = kTp + kTiles, kSc = kV + kC * kRow;
   static constexpr int kBytes = (kSc + kScalarBytes + 1023) / 1024 * 1024;
 };
 template <int DK, int M>
@@ -725,11 +725,9 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(kC * 128 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-// fp16 x fp16 -> fp32; bit 13: A negated (the low parts are stored as
-// their negatives); bit 16: B with its rows along the contraction
-__host__ __device__ constexpr uint32_t idesc(int M, int N, bool neg, bool b_mn = false) {
-  return (1u << 4) | (neg ? 1u << 13 : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
+// fp16 x fp16 -> fp32; bit 16: B with its rows along the contraction
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn = false) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
@@ -794,24 +792,21 @@ __device__ __forceinline__ void row_scales(const float (&m)[4], float (&up)[2], 
     dn[h] = __uint_as_float(e - (14u << 23));
   }
 }
-// v (N pairs of values, two rows) times its rows' scales, as high parts at
-// column hi and the negatives of the low parts at column lo.  Scaled values are
-// below 2^15, so adding and subtracting 1.5 * 2^27 rounds them to multiples of
-// 16: an fp16 high part, and a low part of at most 8.
+// v (N pairs of values, two rows) times its rows' scales: the first 11 bits of
+// each as fp16 at column hi, the first 11 of what they leave at column lo.  Cut
+// off, not rounded: a mask, where a conversion to fp16 and back made a chunk 5 %
+// longer (8192 tokens of 32 heads: 354 and 373 us), for one bit of the 23.
 template <int N>
 __device__ __forceinline__ void split_store(const f2 *v, const float (&scale)[2], uint32_t hi, uint32_t lo) {
-  const f2 big = pk(201326592.f, 201326592.f), nbig = pk(-201326592.f, -201326592.f);
-  const f2 s[2] = {pk(scale[0], scale[0]), pk(scale[1], scale[1])};
-  const f2 ns[2] = {pk(-scale[0], -scale[0]), pk(-scale[1], -scale[1])};
 #pragma unroll
   for (int k = 0; k < N; k += 8) {
     uint32_t h[8], l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const f2 x = v[k + i];
-      const f2 r = add2(fma2(x, s[i & 1], big), nbig);
-      h[i] = half2_of(r);
-      l[i] = half2_of(fma2(x, ns[i & 1], r));
+      const float x = __fmul_rn(v[k + i].a, scale[i & 1]), y = __fmul_rn(v[k + i].b, scale[i & 1]);
+      const float xh = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u), yh = __uint_as_float(__float_as_uint(y) & 0xFFFFE000u);
+      h[i] = half2_bits(xh, yh);
+      l[i] = half2_bits(x - xh, y - yh);
     }
     tm_st(hi + 2 * k, h);
     tm_st(lo + 2 * k, l);
@@ -888,9 +883,6 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
   const int64_t place0 = chunk_base(t0, b) + slab.first;
   t0 = min(t0 + (int64_t)slab.first * kC, t1);
   const int chunks = (int)min((t1 - t0 + kC - 1) / kC, (int64_t)slab.end - slab.first);
-  // bf16 outputs keep 8 bits: the low parts of S and R are left out of their
-  // products with Q and P' (2^-12 relative), which they are needed in for fp16
-  constexpr bool kLowInO = std::is_same<T, __half>::value;
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -1087,9 +1079,9 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
         const int64_t place = place0 + n, t = t0 + (int64_t)n * kC;
         const int len = (int)min((int64_t)kC, t1 - t);
         if (lane == 0) {
-          mbar_expect(&bars->full[s], St::kKq + 3 * kTile + kScalarBytes);
+          mbar_expect(&bars->full[s], St::kKq + kTiles + kScalarBytes);
           bulk_load(st, ws.kq + (place * a.HK + hk) * (int64_t)St::kKq, St::kKq, &bars->full[s]);
-          bulk_load(st + St::kTp, ws.tp + (place * a.HV + hv) * (int64_t)(3 * kTile), 3 * kTile, &bars->full[s]);
+          bulk_load(st + St::kTp, ws.tp + (place * a.HV + hv) * (int64_t)kTiles, kTiles, &bars->full[s]);
           bulk_load(st + St::kSc, ws.sc + (place * a.HV + hv) * kScalars, kScalarBytes, &bars->full[s]);
         }
         // V's rows in pieces of 16 bytes, zeros past the sequence's end (a bulk
@@ -1126,16 +1118,16 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
           for (int i = 0; i < DK / 32; ++i) {
             const int k = h * (DK / 32) + i;
             const uint64_t bd = desc_k(kt + (k >> 2) * (kC * 128) + (k & 3) * 32);
-            umma(tmem + kColKS, tmem + kColS + 64 + 8 * k, bd, idesc(M, 64, true), k > 0);
-            umma(tmem + kColKS, tmem + kColS + 8 * k, bd, idesc(M, 64, false), true);
+            umma(tmem + kColKS, tmem + kColS + 64 + 8 * k, bd, idesc(M, 64), k > 0);
+            umma(tmem + kColKS, tmem + kColS + 8 * k, bd, idesc(M, 64), true);
           }
           if (h == 1) {
             umma_commit(&bars->ks_done);
 #pragma unroll
             for (int k = 0; k < DK / 16; ++k) {
               const uint64_t bd = desc_k(qt + (k >> 2) * (kC * 128) + (k & 3) * 32);
-              if (kLowInO) umma(tmem + kColQS, tmem + kColS + 64 + 8 * k, bd, idesc(M, 64, true), k > 0);
-              umma(tmem + kColQS, tmem + kColS + 8 * k, bd, idesc(M, 64, false), kLowInO || k > 0);
+              umma(tmem + kColQS, tmem + kColS + 64 + 8 * k, bd, idesc(M, 64), k > 0);
+              umma(tmem + kColQS, tmem + kColS + 8 * k, bd, idesc(M, 64), true);
             }
           }
         }
@@ -1145,18 +1137,19 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
           fence_after();
 #pragma unroll
           for (int k = 2 * h; k < 2 * h + 2; ++k) {
-            const uint64_t th = desc_k(tp + k * 32), tl = desc_k(tp + 2 * kTile + k * 32);
-            umma(tmem + kColU, tmem + kColR + 32 + 8 * k, th, idesc(M, 64, true), k > 0);
-            umma(tmem + kColU, tmem + kColR + 8 * k, tl, idesc(M, 64, false), true);
-            umma(tmem + kColU, tmem + kColR + 8 * k, th, idesc(M, 64, false), true);
+            const uint64_t th = desc_k(tp + k * 32), tl = desc_k(tp + kTile + k * 32);
+            umma(tmem + kColU, tmem + kColR + 32 + 8 * k, th, idesc(M, 64), k > 0);
+            umma(tmem + kColU, tmem + kColR + 8 * k, tl, idesc(M, 64), true);
+            umma(tmem + kColU, tmem + kColR + 8 * k, th, idesc(M, 64), true);
           }
           if (h == 1) {
             umma_commit(&bars->u_done);
 #pragma unroll
             for (int k = 0; k < kC / 16; ++k) {
-              const uint64_t pd = desc_k(tp + kTile + k * 32);
-              if (kLowInO) umma(tmem + kColO, tmem + kColR + 32 + 8 * k, pd, idesc(M, 64, true), k > 0);
-              umma(tmem + kColO, tmem + kColR + 8 * k, pd, idesc(M, 64, false), kLowInO || k > 0);
+              const uint64_t ph = desc_k(tp + 2 * kTile + k * 32), pl = desc_k(tp + 3 * kTile + k * 32);
+              umma(tmem + kColO, tmem + kColR + 32 + 8 * k, ph, idesc(M, 64), k > 0);
+              umma(tmem + kColO, tmem + kColR + 8 * k, pl, idesc(M, 64), true);
+              umma(tmem + kColO, tmem + kColR + 8 * k, ph, idesc(M, 64), true);
             }
             umma_commit(&bars->o_done);
           }
@@ -1170,8 +1163,8 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
 #pragma unroll
             for (int k = 2 * h; k < 2 * h + 2; ++k) {
               const uint64_t bd = desc_mn(kt + d * (kC * 128) + k * 2048);
-              umma(tmem + kColD + 64 * d, tmem + kColW + 32 + 8 * k, bd, idesc(M, 64, true, true), k > 0);
-              umma(tmem + kColD + 64 * d, tmem + kColW + 8 * k, bd, idesc(M, 64, false, true), true);
+              umma(tmem + kColD + 64 * d, tmem + kColW + 32 + 8 * k, bd, idesc(M, 64, true), k > 0);
+              umma(tmem + kColD + 64 * d, tmem + kColW + 8 * k, bd, idesc(M, 64, true), true);
             }
             if (h == 1) umma_commit(&bars->d_done[d]);
           }
@@ -1224,7 +1217,7 @@ bool can_slab(const DeltaView &a) { return a.B * a.HV * (a.DV / 64) <= kSlabCtas
 
 ChunkPlaces places(const DeltaView &a, void *ws, size_t *total) {
   const size_t n = (size_t)chunk_places(a.T, a.B);
-  const size_t kq = up256(n * a.HK * (size_t)(2 * kC * a.DK * 2)), tp = up256(n * a.HV * (size_t)(3 * kTile));
+  const size_t kq = up256(n * a.HK * (size_t)(2 * kC * a.DK * 2)), tp = up256(n * a.HV * (size_t)kTiles);
   unsigned char *p = static_cast<unsigned char *>(ws);
   const size_t sc = up256(n * a.HV * (size_t)kScalarBytes), st = (size_t)(a.B * a.HV) * a.DK * a.DV * 4;
   if (total) *total = kq + tp + sc + (can_slab(a) ? st + (size_t)(a.B * a.HV) * (a.DV / 16) * 4 : 0);

@@ -305,10 +305,9 @@ q1_status q1_decode_chain(const q1_decode_layer *layers, int32_t n_layers, const
  *               token.
  * The state and everything it is made from are computed to fp32 accuracy in both
  * forms (in chunks: as pairs of fp16 values, relative error below 1e-6 where
- * beta |k|^2 <= 2); o is rounded to its type once, in chunks of fp16 outputs after
- * weights of 11 bits.  In the chunked form a NaN or infinity among a sequence's
- * inputs also reaches the outputs of earlier tokens of its chunk; it never
- * reaches another sequence.
+ * beta |k|^2 <= 2); o is computed like it and rounded to its type once.  In the
+ * chunked form a NaN or infinity among a sequence's inputs also reaches the outputs
+ * of earlier tokens of its chunk; it never reaches another sequence.
  * dtype: of q, k, v and o.  g (log decay, at most 0 in use) and beta are fp32.
  * DK and DV 64 or 128; HV a multiple of HK.  q, k, v, o and state 16-byte
  * aligned, q/k/v/o strides multiples of 16 bytes.  o must not overlap the inputs.

@@ -36,6 +36,34 @@ def gated_delta(q, k, v, g, beta, state, starts, scale, l2norm, slots=None, fres
     return o, state, colmax
 
 
+def delta_sizes(k, v, g, beta, state, starts, l2norm, slots=None, fresh=None):
+    """What rounding at a token can be relative to, per value column: the largest norm
+    that the column's state or a token's write had, decayed by the gates since (a
+    correction that erases does not make it smaller).  [T, HV, DV], and what it
+    is after the last token, [B, HV, DV]."""
+    k, v, g, beta, state = (np.asarray(x, np.float64) for x in (k, v, g, beta, state))
+    T, HK, DK = k.shape
+    HV, DV = v.shape[1:]
+    if l2norm:
+        k = k / np.sqrt((k * k).sum(-1, keepdims=True) + 1e-6)
+    k = np.repeat(k, HV // HK, 1)
+    sizes, last = np.zeros((T, HV, DV)), np.zeros((len(starts) - 1, HV, DV))
+    for b in range(len(starts) - 1):
+        slot = b if slots is None else int(slots[b])
+        have = 0 <= slot < state.shape[0]
+        S = state[slot].copy() if have and not (fresh is not None and fresh[b]) else np.zeros((HV, DK, DV))
+        z = np.sqrt((S * S).sum(1))
+        for t in range(starts[b], starts[b + 1]):
+            a = np.exp(g[t])[:, None]
+            S = S * a[:, :, None]
+            S = S + k[t][:, :, None] * (beta[t][:, None] * (v[t] - np.einsum("hkv,hk->hv", S, k[t])))[:, None, :]
+            write = beta[t][:, None] * np.linalg.norm(k[t], axis=-1)[:, None] * np.abs(v[t])
+            z = np.maximum(np.maximum(a * z, write), np.sqrt((S * S).sum(1)))
+            sizes[t] = z
+        last[b] = z
+    return sizes, last
+
+
 def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     """(token, prob) of one row."""
     x = np.asarray(logits, np.float64).copy()
