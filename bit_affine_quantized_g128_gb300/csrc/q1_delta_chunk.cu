@@ -75,14 +75,13 @@ __host__ __device__ inline int64_t chunk_places(int64_t T, int64_t B) { return T
 // wider tiles are 64-column boxes one after another.
 __device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
 
-// 2^e as a float, and the e that brings a value of size mx into [2^14, 2^15).
-// Zero, infinite and NaN sizes take e = 0.
+// 2^e as a float, and the e that brings a value of size mx into [2^14, 2^15), at
+// most 60 either way (sums of two stay exponents of fp32 values).  Infinite and NaN
+// sizes take e = 0.
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 __device__ __forceinline__ int scale_exp(float mx) {
   const int e = (int)((__float_as_uint(mx) >> 23) & 0xFF);
-  if (e == 0 || e == 255) return 0;
-  const int s = 14 - (e - 127);
-  return s > 100 ? 100 : s < -100 ? -100 : s;
+  return e == 255 ? 0 : min(max(14 - (e - 127), -60), 60);
 }
 
 // The e that brings the root of a sum of squares into [2^13, 2^15)
@@ -149,18 +148,30 @@ __device__ __forceinline__ uint32_t half2_of(f2 v) {
 // which carries diag(beta) and the tile's scale along in T_cc.  All products
 // are mma.sync on fp16 pairs (three products each).
 //
-// 85 us for 8192 tokens of 32 heads, 175 us for 16384, of which the bytes are 35
-// and 69 us at a plain copy's rate: bound by the latency of the block rows' chain
-// and its barriers.  Four CTAs a SM: three take as long, five or six spill more
+// 199 us for 16384 tokens of 32 heads, of which the bytes are 80 us at a plain
+// copy's rate: bound by the latency of the block rows' chain and its barriers.  Four CTAs a SM: three take as long, five or six spill more
 // and take 3 to 12 % longer.
 //
-// Scales are powers of two from bounds, so that nothing is searched for: with
-// g <= 0, beta |k|^2 <= 2, the recurrence contracts and |(I + A)^-1| <= 1, hence
-// |T| <= max beta and |P'| <= max |q| max |k| max beta.  The bounds are put at
-// 2^9, which leaves 2^6 for what they do not cover; positive g raise them by
-// their sum.
+// Scales are powers of two from bounds, so that nothing is searched for on the
+// way (searches for the largest value of each block row made this kernel 20 %
+// slower).  With |k| the keys' norms after their factors, a token multiplies
+// what lies before it by at most e^g max(1, |1 - beta |k|^2|): at most 1 with
+// g <= 0 and beta |k|^2 <= 2, and otherwise grow, the product over the chunk of
+// those above 1.  Then, entry by entry,
+//   |A| <= X = max(beta |k|) max |k|          (times the growth of the gates)
+//   |(I + A)^-1| <= grow max(1, X), |Y| <= grow X, |T| <= grow max(1, X) max beta
+//   |P| <= max |q| max |k|                    (times the growth of the gates)
+//   |P'| <= grow max |q| max |k| max beta
+// and each is scaled so that its bound lies in [2^14, 2^15).  grow counts up to
+// 2^kGrow: one fp16 pair reaches over 39 octaves, and what the bound takes of them the
+// ordinary values lack.  A chunk that grows the state by more overflows.
+constexpr float kGrow = 16.f;
 constexpr int kPrepT = 128;
 
+// Exponents of the scales of a value head's operands: A, (I + A)^-1, Y, T, P and P'
+struct Scales {
+  int a, d, y, t, p, x;
+};
 
 struct PrepShared {
   float D[4][16][20];          // per warp: the diagonal block of A, then its inverse
@@ -168,8 +179,9 @@ struct PrepShared {
   // of up to four value heads, a warp each
   float Gh[4][kC], Gl[4][kC];  // log2(e) G = Gh + Gl
   float beta[4][kC];
-  int te[4], bump[4];          // T's scale; what positive g add to the bounds' exponents
-  float size[4];               // largest key norms (warps 0, 1) and scaled query norms (2, 3)
+  Scales scales[4];
+  float kn[kC];                // the keys' norms, after their factors
+  float size[4];               // the largest of them (warps 0, 1), and of the scaled queries' (2, 3)
 };
 
 template <typename T>
@@ -207,15 +219,14 @@ __device__ __forceinline__ void mma3(float (&d)[4], const uint32_t (&ah)[4], con
   mma16(d, ah, bl0, bl1);
   mma16(d, ah, bh0, bh1);
 }
-// a 16 x 16 block of fragments as the pair operand of the next product
-__device__ __forceinline__ void pair_operand(const f2 (&c)[2][2], uint32_t (&h)[4], uint32_t (&l)[4]) {
+// a 16 x 16 block of fragments, times a power of two, as the pair operand of the next product
+__device__ __forceinline__ void pair_operand(const f2 (&c)[2][2], float scale, uint32_t (&h)[4], uint32_t (&l)[4]) {
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float x, y;
-      upk(c[n][e], x, y);
-      split2(x, y, h[2 * n + e], l[2 * n + e]);
+      const f2 v = mul2(c[n][e], pk(scale, scale));
+      split2(v.a, v.b, h[2 * n + e], l[2 * n + e]);
     }
 }
 
@@ -322,6 +333,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
     const float n = (a.l2norm ? rsqrtf(ss + kDeltaEps) : 1.f) * (which ? a.scale : 1.f);
     slot = n * pow2f(-root_exp(ss));
     float size = fabsf(n) * sqrtf(ss);
+    if (!which) sh.kn[tid & 63] = size;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
     if (lane == 0) sh.size[warp] = size;
@@ -350,7 +362,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       }
   }
   __syncthreads();  // the tiles' area is free
-  const int pe0 = scale_exp(fmaxf(sh.size[0], sh.size[1]) * fmaxf(sh.size[2], sh.size[3])) - 6;  // 2^pe0 |k| |q| below 2^9
+  const float kmax = fmaxf(sh.size[0], sh.size[1]), qmax = fmaxf(sh.size[2], sh.size[3]);
   const uint32_t th = smem_u32(area), tl = th + kTile, ph = th + 2 * kTile, pl = th + 3 * kTile;
   // the blocks above the diagonal stay zero
   for (int i = tid; i < kTiles / 16; i += kPrepT) reinterpret_cast<uint4 *>(area)[i] = make_uint4(0, 0, 0, 0);
@@ -364,7 +376,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
   auto gates = [&](int of) {
     float *sc = ws.sc + (place * a.HV + hk * group + of) * kScalars;
     const uint32_t nan0 = __ballot_sync(0xffffffffu, gate_g[0] != gate_g[0]), nan1 = __ballot_sync(0xffffffffu, gate_g[1] != gate_g[1]);
-    float up = 0.f;
+    float up = 0.f, over = 0.f, bmax = 0.f, bk = 0.f;  // log2 of what gates and corrections grow by; largest beta, beta |k|
     long long gi[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -372,6 +384,10 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       const float l = fminf(fmaxf(gate_g[x], -200.f), 200.f) * 1.44269504f;
       up += fmaxf(l, 0.f);
       gi[x] = __float2ll_rn(l * 1099511627776.f);
+      const float b = fabsf(gate_b[x]), kn = sh.kn[2 * lane + x];
+      bmax = fmaxf(bmax, b);
+      bk = fmaxf(bk, b * kn);
+      over += __log2f(fmaxf(1.f, fabsf(1.f - gate_b[x] * kn * kn)));
     }
     long long sum = gi[0] + gi[1];
 #pragma unroll
@@ -379,14 +395,16 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       const long long z = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += z;
     }
-    float bmax = fmaxf(fabsf(gate_b[0]), fabsf(gate_b[1]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       up += __shfl_xor_sync(0xffffffffu, up, o);
-      bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, o));
+      over += __shfl_xor_sync(0xffffffffu, over, o);
     }
-    const int bump = (int)ceilf(fminf(up, 20.f));
-    const int te = scale_exp(bmax) - 6 - bump;
+    bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
+    bk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bk)));
+    const float by_gates = exp2f(fminf(up, kGrow)), grow = exp2f(fminf(up + over, kGrow)), X = bk * kmax;
+    const Scales e = {scale_exp(X * by_gates), scale_exp(grow * fmaxf(1.f, X)), scale_exp(X * grow),
+                      scale_exp(grow * fmaxf(1.f, X) * bmax), scale_exp(qmax * kmax * by_gates), scale_exp(grow * qmax * kmax * bmax)};
     const long long all = __shfl_sync(0xffffffffu, sum, 31);
     const long long G[2] = {sum - gi[1], sum};
 #pragma unroll
@@ -404,17 +422,14 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       const float gam = ex2(gh + gl);
       const float tail = ex2((float)(all - G[x]) * 9.094947017729282e-13f);
       sc[t] = gam * sh.rk[t];
-      sc[kC + t] = ((nan0 | nan1) ? __int_as_float(0x7fc00000) : tail) * sh.rk[t] * pow2f(-te);
+      sc[kC + t] = ((nan0 | nan1) ? __int_as_float(0x7fc00000) : tail) * sh.rk[t] * pow2f(-e.t);
       sc[2 * kC + t] = gam * sh.rq[t];
       if (t == kC - 1) {
         sc[3 * kC] = gam;
-        sc[3 * kC + 1] = pow2f(-(pe0 - bump)) * pow2f(-te) * 512.f;
+        sc[3 * kC + 1] = pow2f(-e.x);
       }
     }
-    if (lane == 0) {
-      sh.te[warp] = te;
-      sh.bump[warp] = bump;
-    }
+    if (lane == 0) sh.scales[warp] = e;
   };
   for (int of = of0; of < of1; ++of) {
     const int at = (of - of0) & 3, hv = hk * group + of;
@@ -424,7 +439,8 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
     }
     __syncthreads();  // the gates are there; the last head's tiles have been copied out
     const float *Gh = sh.Gh[at], *Gl = sh.Gl[at], *beta = sh.beta[at];
-    const float ts = pow2f(sh.te[at]), ps = pow2f(pe0 - sh.bump[at]);
+    const Scales e = sh.scales[at];
+    const float ps = pow2f(e.p);
     // ---- A and P in place of the products' fragments
     f2 A[4][2][2];
     uint32_t Ph[4][4], Pl[4][4];
@@ -489,43 +505,44 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
         if ((i >> 3) == (lane >> 4)) sh.D[warp][i][c] = x[i];
       __syncwarp();
     }
-    // its fragments: T's block (with beta and the scale), and the operand of Y
+    // its fragments: T's block (with beta), and the operand of Y
     uint32_t dh[4], dl[4];
     {
       f2 d[2][2];
+      const float ts = pow2f(e.t);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const f2 be = mul2(lds_pair(&beta[16 * warp + 8 * n + fc]), pk(ts, ts));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          d[n][e] = lds_pair(&sh.D[warp][fr + 8 * e][8 * n + fc]);
-          float x, y;
+        for (int i = 0; i < 2; ++i) {
+          d[n][i] = lds_pair(&sh.D[warp][fr + 8 * i][8 * n + fc]);
+          const f2 x = mul2(d[n][i], be);
           uint32_t h, l;
-          upk(mul2(d[n][e], be), x, y);
-          split2(x, y, h, l);
-          const int row = 16 * warp + fr + 8 * e, pc = 2 * warp + n;
+          split2(x.a, x.b, h, l);
+          const int row = 16 * warp + fr + 8 * i, pc = 2 * warp + n;
           put(word_at(th, row, pc), h);
           put(word_at(tl, row, pc), l);
         }
       }
-      pair_operand(d, dh, dl);
+      pair_operand(d, pow2f(e.d), dh, dl);
     }
     // ---- Y = D A, the blocks left of the diagonal (kept as pairs)
     uint32_t yh[3][4], yl[3][4];
+    const float as = pow2f(e.a), ys = -pow2f(max(e.y - e.a - e.d, -126));
 #pragma unroll
     for (int m = 0; m < 3; ++m)
       if (m < warp) {
         uint32_t ah[4], al[4];
-        pair_operand(A[m], ah, al);
+        pair_operand(A[m], as, ah, al);
         f2 y[2][2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           float d[4] = {};
           mma3(d, dh, dl, movmatrix(ah[2 * n]), movmatrix(ah[2 * n + 1]), movmatrix(al[2 * n]), movmatrix(al[2 * n + 1]));
-          y[n][0] = pk(-d[0], -d[1]);
-          y[n][1] = pk(-d[2], -d[3]);
+          y[n][0] = pk(d[0], d[1]);
+          y[n][1] = pk(d[2], d[3]);
         }
-        pair_operand(y, yh[m], yl[m]);
+        pair_operand(y, ys, yh[m], yl[m]);
       }
     // the operand pair of block (m, c) of T, as rows along the contraction
     auto t_block = [&](int m, int c, uint32_t (&bh)[4], uint32_t (&bl)[4]) {
@@ -536,6 +553,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
     // ---- T, block row after block row
     {
       float tv[3][2][4] = {};
+      const float tvs = pow2f(-e.y);
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         __syncthreads();  // block row m is complete
@@ -554,10 +572,10 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
+              for (int i = 0; i < 2; ++i) {
                 uint32_t h, l;
-                split2(tv[c][n][2 * e], tv[c][n][2 * e + 1], h, l);
-                const int row = 16 * warp + fr + 8 * e, pc = 2 * c + n;
+                split2(tv[c][n][2 * i] * tvs, tv[c][n][2 * i + 1] * tvs, h, l);
+                const int row = 16 * warp + fr + 8 * i, pc = 2 * c + n;
                 put(word_at(th, row, pc), h);
                 put(word_at(tl, row, pc), l);
               }
@@ -566,6 +584,7 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
     }
     __syncthreads();
     // ---- P' = P T
+    const float xs = pow2f(max(e.x - e.p - e.t, -126));
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (c <= warp) {
@@ -581,11 +600,11 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int i = 0; i < 2; ++i) {
             uint32_t h, l;
-            split2(pp[n][2 * e] * (1.f / 512.f), pp[n][2 * e + 1] * (1.f / 512.f), h, l);
-            put(word_at(ph, 16 * warp + fr + 8 * e, 2 * c + n), h);
-            put(word_at(pl, 16 * warp + fr + 8 * e, 2 * c + n), l);
+            split2(pp[n][2 * i] * xs, pp[n][2 * i + 1] * xs, h, l);
+            put(word_at(ph, 16 * warp + fr + 8 * i, 2 * c + n), h);
+            put(word_at(pl, 16 * warp + fr + 8 * i, 2 * c + n), l);
           }
       }
     __syncthreads();

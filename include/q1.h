@@ -303,11 +303,15 @@ q1_status q1_decode_chain(const q1_decode_layer *layers, int32_t n_layers, const
  *               more than 36 tokens (20 with more than 152 heads in the batch) go
  *               in chunks of 64 tokens on the tensor cores, all others token by
  *               token.
- * The state and everything it is made from are computed to fp32 accuracy in both
- * forms (in chunks: as pairs of fp16 values, relative error below 1e-6 where
- * beta |k|^2 <= 2); o is computed like it and rounded to its type once.  In the
- * chunked form a NaN or infinity among a sequence's inputs also reaches the outputs
- * of earlier tokens of its chunk; it never reaches another sequence.
+ * The state and everything it is made from are computed to fp32 accuracy, and o
+ * like it, rounded to its type once.  In chunks operands are pairs of fp16
+ * values: 2^-22 of each value, and 2^-39 of the largest that it is summed with in
+ * its chunk, before that has decayed.  Where the tokens of a chunk together can
+ * grow the state (factors e^g above 1, and |1 - beta |k|^2| where beta |k|^2 exceeds
+ * 2) the second bound grows with them, and by more than 2^16 it overflows to NaN;
+ * token by token it does not.  In the chunked form a NaN or infinity among a
+ * sequence's inputs also reaches the outputs of earlier tokens of its chunk; it never
+ * reaches another sequence.
  * dtype: of q, k, v and o.  g (log decay, at most 0 in use) and beta are fp32.
  * DK and DV 64 or 128; HV a multiple of HK.  q, k, v, o and state 16-byte
  * aligned, q/k/v/o strides multiples of 16 bytes.  o must not overlap the inputs.

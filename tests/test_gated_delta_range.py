@@ -75,11 +75,39 @@ lengths = pytest.mark.parametrize("L", [20, 64, 130])   # token by token, one ch
 @pytest.mark.gpu
 @both
 @lengths
+@pytest.mark.parametrize("factor", [10.0, 100.0, 1000.0, 1e4])
+@pytest.mark.parametrize("HK,HV,DK,DV", [(2, 4, 128, 128), (1, 3, 64, 64)])
+def test_one_large_value_that_fades(q1, HK, HV, DK, DV, factor, L, dtype):
+    for at in (3, 13):
+        a, dt = _inputs(L, dtype, 5, HK, HV, DK, DV)
+        a["g"] -= 0.3
+        a["v"][at] *= factor
+        _run(q1, a, dt)
+
+
+@pytest.mark.gpu
+@both
+@lengths
 def test_one_large_value_late(q1, L, dtype):
     # what lies before it in its chunk does not see it
     a, dt = _inputs(L, dtype, 6)
     a["v"][L - 3] *= 1e4
     _run(q1, a, dt)
+
+
+@pytest.mark.gpu
+@both
+@lengths
+@pytest.mark.parametrize("before,after", [(1.0, 1.0), (1000.0, 1.0), (1000.0, 0.0)])
+def test_a_strong_decay_inside(q1, before, after, L, dtype):
+    # what was written before is left at 2^-14 of its size; without new values, all of it
+    for at in (9, L // 2, L // 2 + 3):
+        a, dt = _inputs(L, dtype, 7)
+        a["g"][at] = -10.0
+        a["v"][:at] *= before
+        a["state"] *= before
+        a["v"][at:] *= after
+        _run(q1, a, dt)
 
 
 @pytest.mark.gpu
@@ -114,3 +142,56 @@ def test_a_large_entry_that_is_not_asked_for(q1, L, dtype):
     a["k"][:, :, 5] = 0.0
     a["q"][:, :, 5] = 0.0
     _run(q1, a, dt)
+
+
+@pytest.mark.gpu
+@both
+@lengths
+@pytest.mark.parametrize("small", [1e-4, 1e-6])
+def test_small_beta_behind_large_ones(q1, small, L, dtype):
+    for at in (2, 6):
+        a, dt = _inputs(L, dtype, 11)
+        a["beta"][at:] = small * (0.5 + 0.5 * a["beta"][at:])
+        a["g"][at] = -14.0
+        a["state"] *= 0.0
+        _run(q1, a, dt)
+
+
+@pytest.mark.gpu
+@both
+@pytest.mark.parametrize("L", [18, 64, 100])
+@pytest.mark.parametrize("bk2", [2.05, 3.0])
+def test_keys_that_overshoot(q1, bk2, L, dtype):
+    # beta |k|^2 above 2: every token's correction grows what it corrects.  The sums
+    # over earlier tokens no longer shrink: 2^-15.
+    a, dt = _inputs(L, dtype, 12)
+    a["k"] *= bk2 ** 0.5 / a["k"].norm(dim=-1, keepdim=True)
+    a["beta"][:] = 1.0
+    _run(q1, a, dt, l2norm=False, scale=0.1, arith=2.0 ** -15)
+
+
+@pytest.mark.gpu
+@both
+@pytest.mark.parametrize("L", [18, 64, 100])
+def test_one_key_that_overshoots(q1, L, dtype):
+    # beta |k|^2 = r + 1 = 2.2 with one key throughout: what lies under it changes its sign
+    # and grows by r = 1.2 with every token, and so does every error.  Each of L tokens
+    # then adds 2^-19 of the terms that it sums, and of a series of alternating signs and
+    # ratio r the terms are (r + 1) / (r - 1) = 11 times their sum.  (The recurrence in fp32,
+    # 2^-24 per step, is 1e-4 off after 64 tokens.)
+    a, dt = _inputs(L, dtype, 12)
+    a["k"][:] = a["k"][:1]
+    a["k"] *= 2.2 ** 0.5 / a["k"].norm(dim=-1, keepdim=True)
+    a["beta"][:] = 1.0
+    # fp16 outputs end at 65504
+    _run(q1, a, dt, l2norm=False, scale=0.1 if dt == torch.bfloat16 else 1e-4, arith=11 * L * 2.0 ** -19)
+
+
+@pytest.mark.gpu
+@both
+@lengths
+def test_gates_that_grow(q1, L, dtype):
+    # positive log decays, e^6 over a chunk
+    a, dt = _inputs(L, dtype, 13)
+    a["g"] = a["g"].abs() + 0.08
+    _run(q1, a, dt, arith=2.0 ** -15)
