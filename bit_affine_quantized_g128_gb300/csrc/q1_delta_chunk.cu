@@ -202,6 +202,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// 2^(G 2^-40): the whole octaves go into the exponent, so that the rest is small
+// enough for fp32 whatever G is
+__device__ __forceinline__ float ex2_fixed(long long G) {
+  const int n = (int)(G >> 40);
+  const float f = (float)(G & ((1ll << 40) - 1)) * 9.094947017729282e-13f;
+  return n < -126 ? 0.f : n > 127 ? __int_as_float(0x7f800000) : ex2(f) * pow2f(n);
+}
 // the 8 x 8 matrix of 16-bit values that the warp holds, transposed
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   uint32_t r;
@@ -381,9 +388,11 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       // exp(-200) is 0 in fp32 already
-      const float l = fminf(fmaxf(gate_g[x], -200.f), 200.f) * 1.44269504f;
+      const float g = fminf(fmaxf(gate_g[x], -200.f), 200.f), l = g * 1.44269504f;
+      // the product's own rounding, and log2(e) beyond fp32, are part of the sum
+      const float rest = fmaf(g, 1.925963e-8f, fmaf(g, 1.44269504f, -l));
       up += fmaxf(l, 0.f);
-      gi[x] = __float2ll_rn(l * 1099511627776.f);
+      gi[x] = __float2ll_rn(l * 1099511627776.f) + __float2ll_rn(rest * 1099511627776.f);
       const float b = fabsf(gate_b[x]), kn = sh.kn[2 * lane + x];
       bmax = fmaxf(bmax, b);
       bk = fmaxf(bk, b * kn);
@@ -419,8 +428,8 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
       sh.Gh[warp][t] = gh;
       sh.Gl[warp][t] = gl;
       sh.beta[warp][t] = gate_b[x];
-      const float gam = ex2(gh + gl);
-      const float tail = ex2((float)(all - G[x]) * 9.094947017729282e-13f);
+      const float gam = bad ? gh : ex2_fixed(G[x]);
+      const float tail = ex2_fixed(all - G[x]);
       sc[t] = gam * sh.rk[t];
       sc[kC + t] = ((nan0 | nan1) ? __int_as_float(0x7fc00000) : tail) * sh.rk[t] * pow2f(-e.t);
       sc[2 * kC + t] = gam * sh.rq[t];

@@ -44,7 +44,7 @@ def _inputs(L, dtype, seed, HK=2, HV=4, DK=128, DV=128):
     return a, DT[dtype]
 
 
-def _run(q1, a, dt, l2norm=True, scale=None, arith=2.0 ** -17):
+def _run(q1, a, dt, l2norm=True, scale=None, arith=2.0 ** -17, least=2.0 ** -36):
     q, k, v = (a[n].to(dt) for n in "qkv")
     L, _, DK = q.shape
     scale = DK ** -0.5 if scale is None else scale
@@ -57,7 +57,7 @@ def _run(q1, a, dt, l2norm=True, scale=None, arith=2.0 ** -17):
     o, s = _np(o.cpu()), _np(sd.cpu())
     assert q1.device_errors() == 0
     assert np.isfinite(o).all() and np.isfinite(s).all()
-    floor = 2.0 ** -36 * np.maximum(sizes.max(0), np.linalg.norm(args[5][0], axis=1))
+    floor = least * np.maximum(sizes.max(0), np.linalg.norm(args[5][0], axis=1))
     e = np.linalg.norm(s[0] - want_s[0], axis=1) / (arith * last[0] + floor + 1e-37)
     assert (e <= 1).all(), f"state off by {e.max():.3g} bounds"
     qn = np.ones(q.shape[:2]) if l2norm else np.linalg.norm(args[0], axis=-1)
@@ -185,6 +185,21 @@ def test_one_key_that_overshoots(q1, L, dtype):
     a["beta"][:] = 1.0
     # fp16 outputs end at 65504
     _run(q1, a, dt, l2norm=False, scale=0.1 if dt == torch.bfloat16 else 1e-4, arith=11 * L * 2.0 ** -19)
+
+
+@pytest.mark.gpu
+@both
+@pytest.mark.parametrize("L", [64, 130])
+@pytest.mark.parametrize("total,steps", [(-5.0, 64), (-30.0, 64), (-30.0, 1), (-45.0, 3)])
+def test_a_state_that_only_decays(q1, total, steps, L, dtype):
+    # nothing is written: the state is e^G of what it was, however small, and o reads it.
+    # Chunk by chunk a factor of 2^-22 and a product's rounding, and an operand's 2^-22;
+    # nothing is summed that has not decayed as far.
+    a, dt = _inputs(L, dtype, 14)
+    a["beta"][:] = 0.0
+    a["g"][:] = 0.0
+    a["g"][5:5 + steps] = total / steps * (0.75 + 0.5 * torch.rand(steps, 4, generator=torch.Generator().manual_seed(15)))[:L - 5]
+    _run(q1, a, dt, arith=2.0 ** -20, least=0.0)
 
 
 @pytest.mark.gpu
