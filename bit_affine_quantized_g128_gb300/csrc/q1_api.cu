@@ -291,7 +291,8 @@ q1_status q1_pack_from_dense(const void *dense, q1_dtype in_t, int64_t N, int64_
 }
 
 namespace {
-q1_status check_delta(const q1_delta_args *a) {
+// types and sizes: all that the workspace's size goes by
+q1_status check_delta_sizes(const q1_delta_args *a) {
   if (!a) return Q1_ERR_NULL;
   if (a->dtype != Q1_BF16 && a->dtype != Q1_F16 && a->dtype != Q1_F32) return Q1_ERR_DTYPE;
   if ((a->DK != 64 && a->DK != 128) || (a->DV != 64 && a->DV != 128)) return Q1_ERR_SHAPE;
@@ -299,6 +300,12 @@ q1_status check_delta(const q1_delta_args *a) {
   if (a->T < 0 || a->T > ((int64_t)1 << 31) - 1 || a->B < 1 || a->B > (int64_t)1 << 24 ||
       a->B * a->HV > (int64_t)1 << 29 || a->n_slots < 0 || a->max_len < 0)
     return Q1_ERR_SHAPE;
+  return Q1_OK;
+}
+
+q1_status check_delta(const q1_delta_args *a) {
+  const q1_status s = check_delta_sizes(a);
+  if (s != Q1_OK) return s;
   if (!a->cu_seqlens && a->T % a->B != 0) return Q1_ERR_SHAPE;
   if (!a->slots && a->n_slots < a->B) return Q1_ERR_SHAPE;
   if (!a->state) return Q1_ERR_NULL;
@@ -338,7 +345,7 @@ bool delta_in_chunks(const q1_delta_args *a) {
 }  // namespace
 
 size_t q1_gated_delta_workspace_size(const q1_delta_args *a) {
-  if (check_delta(a) != Q1_OK || !delta_in_chunks(a)) return 0;
+  if (check_delta_sizes(a) != Q1_OK || !delta_in_chunks(a)) return 0;
   return q1::delta_chunk_workspace_bytes(delta_view(a));
 }
 

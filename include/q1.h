@@ -317,7 +317,9 @@ q1_status q1_decode_chain(const q1_decode_layer *layers, int32_t n_layers, const
  * aligned, q/k/v/o strides multiples of 16 bytes.  o must not overlap the inputs.
  * Offsets in cu_seqlens that leave [0, T] or decrease are cut to it: the
  * results of such a batch are undefined, its accesses stay inside the arrays.
- * Workspace: q1_gated_delta_workspace_size bytes (0 where none is needed). */
+ * Workspace: q1_gated_delta_workspace_size bytes, 256-byte aligned (0 where none is
+ * needed).  It goes by dtype, T, B, HK, HV, DK, DV and max_len alone: pointers and
+ * strides may still be unset. */
 typedef struct {
   const void *q, *k, *v;     /* [T][HK][DK], [T][HK][DK], [T][HV][DV] */
   void *o;                   /* [T][HV][DV] */

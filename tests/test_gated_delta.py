@@ -420,6 +420,20 @@ def test_refuses_host_tensors():
         mod.gated_delta(**_host())
 
 
+def test_workspace_size_before_the_tensors_exist():
+    # by sizes alone (no GPU needed): with and without pointers the same
+    from bit_affine_quantized_g128_gb300 import q1 as mod
+    size = mod.lib().q1_gated_delta_workspace_size
+    sizes = dict(T=300, B=2, HK=2, HV=4, DK=64, DV=64, max_len=200, dtype=0)
+    full = dict(q=4096, k=4096, v=4096, o=4096, g=4096, beta=4096, state=4096, cu_seqlens=4096, n_slots=2, q_stride=128,
+                k_stride=128, v_stride=256, o_stride=256, g_stride=4, beta_stride=4)
+    n = size(mod._CDelta(**sizes, **full))
+    assert n > 0 and size(mod._CDelta(**sizes)) == n
+    assert size(mod._CDelta(**{**sizes, "T": 301})) > 0        # two unequal sequences: the offsets come later
+    for none in (dict(max_len=1), dict(dtype=2), dict(T=0), dict(DK=96), dict(HV=3), dict(B=0)):
+        assert size(mod._CDelta(**{**sizes, **none})) == 0
+
+
 @pytest.mark.gpu
 def test_c_refusals(q1):
     z = torch.zeros(1 << 16, device="cuda")
