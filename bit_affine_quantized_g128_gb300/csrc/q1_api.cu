@@ -335,12 +335,19 @@ q1::DeltaView delta_view(const q1_delta_args *a) {
 
 namespace {
 // Short sequences go token by token, as do fp32 activations (the chunked form's
-// operands hold 16-bit inputs exactly, not fp32 ones).  Where the two meet (bf16,
-// heads of 128 x 128): one sequence of 32 heads takes 17 us in chunks up to 64
-// tokens, and 15.6 / 21.9 us token by token at 32 / 48; 8 sequences of 48 heads 45
-// us against 35 / 49 us at 16 / 24; 32 of 32 heads 85 us against 77 / 110 us.
+// operands hold 16-bit inputs exactly, not fp32 ones).  A token costs the first form
+// the state's size once the heads fill the GPU, the second one next to nothing up
+// to 64 tokens.  Where the two meet, bf16, in us token by token / in chunks:
+//   1 sequence of 32 heads     128 x 128  16.7 / 17.9 at 36, 18.4 / 18.1 at 40
+//                              64 x 64    14.2 / 16.0 at 36, 15.7 / 16.0 at 40
+//   8 sequences of 48 heads    128 x 128  41.5 / 43.1 at 20, 48.7 / 43.3 at 24
+//                              64 x 128   33.2 / 35.1 at 24, 38.1 / 35.2 at 28
+//                              128 x 64   33.8 / 36.0 at 32, 37.5 / 36.8 at 36
+//                              64 x 64    27.9 / 31.6 at 40, 32.9 / 32.3 at 48
+//   32 sequences of 32 heads   95 / 91 at 20, 74 / 74 at 24, 76 / 77 at 32, 61 / 66 at 40
 bool delta_in_chunks(const q1_delta_args *a) {
-  return a->max_len > (a->B * a->HV <= 152 ? 36 : 20) && a->dtype != Q1_F32 && a->T > 0;
+  const int filled = a->DV == 64 ? (a->DK == 64 ? 40 : 32) : (a->DK == 64 ? 24 : 20);
+  return a->max_len > (a->B * a->HV <= 152 ? 36 : filled) && a->dtype != Q1_F32 && a->T > 0;
 }
 }  // namespace
 

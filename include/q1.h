@@ -300,9 +300,9 @@ q1_status q1_decode_chain(const q1_decode_layer *layers, int32_t n_layers, const
  *               from zero (its entry is only written).
  *   max_len     the longest sequence (a hint that picks the kernels; results
  *               do not depend on it beyond rounding).  bf16 and fp16 sequences of
- *               more than 36 tokens (20 with more than 152 heads in the batch) go
- *               in chunks of 64 tokens on the tensor cores, all others token by
- *               token.
+ *               more than 36 tokens (with more than 152 heads in the batch: 20 to
+ *               40, the fewer the larger the heads) go in chunks of 64 tokens on
+ *               the tensor cores, all others token by token.
  * The state and everything it is made from are computed to fp32 accuracy, and o
  * like it, rounded to its type once.  In chunks operands are pairs of fp16
  * values: 2^-22 of each value, and 2^-39 of the largest that it is summed with in

@@ -434,6 +434,16 @@ def test_workspace_size_before_the_tensors_exist():
         assert size(mod._CDelta(**{**sizes, **none})) == 0
 
 
+@pytest.mark.parametrize("B,DK,DV,last", [(1, 128, 128, 36), (1, 64, 64, 36), (8, 128, 128, 20), (8, 64, 128, 24),
+                                          (8, 128, 64, 32), (8, 64, 64, 40)])
+def test_longest_sequences_that_go_token_by_token(B, DK, DV, last):
+    # those need no workspace: by the number of heads and, once they fill the GPU, their size
+    from bit_affine_quantized_g128_gb300 import q1 as mod
+    size = lambda L: mod.lib().q1_gated_delta_workspace_size(  # noqa: E731
+        mod._CDelta(T=B * L, B=B, HK=16, HV=48, DK=DK, DV=DV, max_len=L, dtype=0))
+    assert size(last) == 0 and size(last + 1) > 0
+
+
 @pytest.mark.gpu
 def test_c_refusals(q1):
     z = torch.zeros(1 << 16, device="cuda")
