@@ -1082,7 +1082,8 @@ __global__ void __launch_bounds__((ChainStage<DK, M>::kThreads), 1) delta_chain_
       if (!ok) break;
     }
     int *failed = ws.failed + ((int64_t)(blockIdx.x / parts) * a.DV + dv0 + L0) / 16;
-    if (slab.first > 0 && *failed) ok = false;  // the state keeps its value
+    // these columns keep their value (others of the sequence may have advanced)
+    if (slab.first > 0 && *failed) ok = false;
     __syncwarp();
     if (slab.more || (ok && have)) {
       // (not kept over the walk: its registers are worth 1 %)

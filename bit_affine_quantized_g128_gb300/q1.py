@@ -522,7 +522,8 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     cu_seqlens[b+1] (int32 [B+1] on the device; `max_len`, the longest, is then best given: without it T is
     assumed).  Without cu_seqlens, q, k, v [B, L, H, D] and g, beta [B, L, HV] are B sequences of L tokens.
     state fp32 [n_slots, HV, DK, DV]; slots int32 [B] names each sequence's entry (default: entry b; outside
-    the pool: none), fresh int32 [B] marks those that start from zero.  scale defaults to DK ** -0.5."""
+    the pool: none), fresh int32 [B] marks those that start from zero.  scale defaults to DK ** -0.5.
+    Where device_errors reports bit 2 afterwards, o and the states of these sequences are undefined."""
     if not _on_current_device(q, k, v, g, beta, state):
         _cuda(q, "q")
         for t, name in ((k, "k"), (v, "v"), (g, "g"), (beta, "beta"), (state, "state")):

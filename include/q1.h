@@ -305,8 +305,8 @@ q1_status q1_decode_chain(const q1_decode_layer *layers, int32_t n_layers, const
  *               the tensor cores, all others token by token.
  * The state and everything it is made from are computed to fp32 accuracy, and o
  * like it, rounded to its type once.  In chunks operands are pairs of fp16
- * values: 2^-22 of each value, and 2^-39 of the largest that it is summed with in
- * its chunk, before that has decayed.  Where the tokens of a chunk together can
+ * values: 2^-22 of each value, and 2^-39 of the largest of its kind in the chunk,
+ * before that has decayed.  Where the tokens of a chunk together can
  * grow the state (factors e^g above 1, and |1 - beta |k|^2| where beta |k|^2 exceeds
  * 2) the second bound grows with them, and by more than 2^16 it overflows to NaN;
  * token by token it does not.  In the chunked form a NaN or infinity among a
@@ -389,7 +389,9 @@ const char *q1_status_string(q1_status s);
  * the timeout path).  Every wait of the narrow, prefill and chunked delta-rule
  * kernels on another role's progress is bounded; one that runs out sets the
  * device error word (bit 0: prefill kernels, bit 1: narrow kernels, bit 2:
- * delta-rule kernels, whose states it leaves unwritten).  Later waits of the
+ * delta-rule kernels).  The outputs of such a call are undefined, and so are the
+ * states of all its sequences: columns whose own waits did not run out may have
+ * advanced, so the caller restores them before it repeats the call.  Later waits of the
  * prefill kernels then give up at once until q1_device_errors reads the word;
  * those of the narrow kernels each run out on their own limit.
  * q1_set_wait_limit_ns: the bound, in ns of the GPU's global timer (default
