@@ -27,8 +27,13 @@ namespace {
 //
 // Bound by the state's bytes for one token: 64 sequences of 32 heads (128 x 128)
 // move 270 MB in 44.4 us, 6.1 TB/s, 90 % of a plain copy; one sequence takes 2.8
-// us, the launch.  Over several tokens by instruction issue: 8 sequences of 48
-// heads and 8 tokens take 18.6 us (29 us with barriers between warps).
+// us, the launch.  Windows of several tokens: 8 sequences of 48 heads and 8 tokens
+// take 18.6 us (29 us with barriers between warps).  Of these the state's bytes are
+// 7.7 us and the instructions 11 us of full issue (the multiply-adds 4 us; the rest
+// are the reductions, and the norms, which every warp of a head forms again), and
+// three warps per scheduler overlap little of it (0.58 issued per clock).  Few
+// sequences: latency, 0.35 us a token, in which the shuffles, roots, exponential and
+// division stand one behind another.
 constexpr int kStepThreads = 64;
 constexpr int kStepCols = 32;
 constexpr int kStepGroups = 8;

@@ -645,9 +645,10 @@ __global__ void __launch_bounds__(kPrepT, 4) delta_prep_kernel(const DeltaView a
 //     leave the uniform registers)
 //   last: the chunk's rows of o from shared memory, where the chain stages them
 // One chunk is a chain of three dependent products; the time is the latency of
-// that chain, not the rate of any unit: 2.6 us a chunk on half heads, 2.9 us on
+// that chain, not the rate of any unit: 2.6 us a chunk on half heads, 3.0 us on
 // whole ones (1024 tokens of 32 heads, both kernels: 62 us on half heads, 69 us
-// on whole ones; of 96 heads 126 and 86 us).
+// on whole ones; of 96 heads 131 and 101 us).  The low parts in o cost it 1 to 2 %:
+// their products run while the next operand is made.
 // Tensor memory columns: S high [0, 64), low [64, 128), and D over both;
 // KS [128, 192); QS [192, 256); R [256, 320); U [320, 384); O2 [384, 448);
 // c U [448, 512).
@@ -1299,11 +1300,13 @@ cudaError_t chunks_t(const DeltaView &a, void *workspace, cudaStream_t st) {
   // it.  A further slab costs 9 us (two launches, the state out and in), so their
   // number goes by the chunk kernel's work, in chunks times heads.  Times in us
   // with 1, 2, 3, 4 slabs (bf16, heads of 128 x 128):
-  //   16 heads,  4096 tokens (1024)    174   173   178   183
-  //   32 heads,  2048 tokens (1024)    106   107   116   128
-  //   32 heads,  4096 tokens (2048)    203   187   191   201
-  //   32 heads,  8192 tokens (4096)    396   356   346   351
-  //   32 heads, 32768 tokens (16384)  1539  1377  1330  1308
+  //   16 heads,  4096 tokens (1024)    177   177   182   191
+  //   32 heads,  2048 tokens (1024)    112   113   126   142
+  //   32 heads,  4096 tokens (2048)    216   196   201   218
+  //   32 heads,  8192 tokens (4096)    422   373   364   375
+  //   32 heads, 32768 tokens (16384)  1637  1437  1366  1361
+  // Heads of 64 columns or key entries gain in the same places (32 heads of 64 x 64,
+  // 4096 tokens: 176 in one, 159 by this rule; 8192 tokens: 343 and 292).
   const int64_t chunks = (std::min(a.max_len, a.T) + kC - 1) / kC;
   const int64_t work = std::min(chunks * a.B, n) * a.HV;
   const int slabs = !can_slab(a) || 2 * kSlabCtas > sms || work <= 1024 ? 1 : work <= 2600 ? 2 : work <= 6400 ? 3 : 4;

@@ -27,9 +27,12 @@
 // which are sorted for the last one kept.
 //
 // Bound by latency for few rows (one row of a large vocabulary: 15 us, ten
-// dependent steps over 16 CTAs; top-k near 1000 with top-p: 43 us) and by
-// instruction issue for many: 28 us for 64 rows (48 instructions per token, 31 of
-// them the exact weight), 51 us for 301 rows of 32003 tokens (108 per token).
+// dependent steps over 16 CTAs; top-k near 1000 with top-p: 43 us).  For many rows
+// by its steps in a row: 28 us for 64 rows (48 instructions per token, 31 of them
+// the exact weight: 13 us of full issue), 51 us for 301 rows of 32003 tokens (108
+// per token).  Load, maximum, count, weights and sort lie between barriers, all CTAs
+// of the single wave go through them together, and half of the issue slots stay
+// empty (0.52 and 0.58 per scheduler and clock).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -173,7 +176,8 @@ __device__ __forceinline__ float key_of(const RowScale &rs, float l) {
   return fmaf(fmaxf((l - rs.m) * rs.c_hi, -1e6f), 1024.f, kMagic) - (l != l ? __int_as_float(0x7fc00000) : 0.f);
 }
 // 2^44 2^((l - m) c) as an integer, for t = key_of(l) >= kDead: with i + 1024 n =
-// t's integer, 2^n 2^(i/1024) 2^r, |r| <= 2^-11 and a little.
+// t's integer, 2^n 2^(i/1024) 2^r, |r| <= 2^-10 and a little (2^-11 from the key's
+// rounding, as much from a1).
 template <bool WIDE>
 __device__ __forceinline__ Weight weight_of(const RowScale &rs, const float2 *exp2, float l, float t) {
   const float ti = t - kMagic;
