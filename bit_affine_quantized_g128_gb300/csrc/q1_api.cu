@@ -382,6 +382,108 @@ q1_status q1_sample(const q1_sample_args *a, q1_stream stream) {
   return cuda_status(q1::launch_sample(*a, (cudaStream_t)stream));
 }
 
+namespace {
+q1_status check_kv_sizes(const q1_kv_cache *c) {
+  if (!c) return Q1_ERR_NULL;
+  if (c->D != 64 && c->D != 128 && c->D != 256) return Q1_ERR_SHAPE;
+  if ((c->group_size != 64 && c->group_size != 128) || c->group_size > c->D) return Q1_ERR_GROUP;
+  if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1))) return Q1_ERR_SHAPE;
+  if (c->HK < 1 || c->HK > 65535 || c->T < 0 || c->T > ((int64_t)1 << 31) - 1 || c->B < 1 || c->B > (int64_t)1 << 24 ||
+      c->n_pages < 0 || c->n_pages > ((int64_t)1 << 31) - 1 || c->table_width < 0 ||
+      c->table_width > (int64_t)1 << 31 || c->table_width * c->page_size > ((int64_t)1 << 31) - 65536 || c->T * c->HK * c->D > (int64_t)1 << 40)
+    return Q1_ERR_SHAPE;
+  return Q1_OK;
+}
+
+q1_status check_kv(const q1_kv_cache *c) {
+  const q1_status s = check_kv_sizes(c);
+  if (s != Q1_OK) return s;
+  if (!c->cu_seqlens && c->T % c->B != 0) return Q1_ERR_SHAPE;
+  if (c->B > 1 && c->table_stride < c->table_width) return Q1_ERR_SHAPE;
+  if (c->T == 0) return Q1_OK;
+  if (!c->lengths || (c->n_pages > 0 && !c->data) || (c->table_width > 0 && !c->block_table)) return Q1_ERR_NULL;
+  if (!aligned(c->data, 16) || !aligned(c->block_table, 4) || !aligned(c->lengths, 4) || !aligned(c->cu_seqlens, 4))
+    return Q1_ERR_ALIGN;
+  return Q1_OK;
+}
+
+// rows of `heads` heads of c->D elements
+q1_status check_kv_rows(const q1_kv_cache *c, const void *p, int64_t stride, int64_t heads, q1_dtype t) {
+  if (!p) return Q1_ERR_NULL;
+  if (!aligned(p, 16) || stride % (t == Q1_F32 ? 4 : 8)) return Q1_ERR_ALIGN;
+  return c->T > 1 && stride < heads * c->D ? Q1_ERR_SHAPE : Q1_OK;
+}
+
+q1_status check_kv_attention_sizes(const q1_kv_cache *c, const q1_kv_attention_args *a) {
+  const q1_status s = check_kv_sizes(c);
+  if (s != Q1_OK) return s;
+  if (!a) return Q1_ERR_NULL;
+  if (a->dtype != Q1_BF16 && a->dtype != Q1_F16 && a->dtype != Q1_F32) return Q1_ERR_DTYPE;
+  if (a->HQ < 1 || a->HQ > 65535 || a->HQ % c->HK != 0 || a->max_q < 0 || a->max_len < 0 || a->window < 0 ||
+      (a->window > 0 && !a->causal) || c->T * a->HQ > ((int64_t)1 << 31) - 1 || c->B * c->HK > (int64_t)1 << 24)
+    return Q1_ERR_SHAPE;
+  return Q1_OK;
+}
+
+q1::KvView kv_view(const q1_kv_cache *c) {
+  int shift = 0;
+  while ((1 << shift) < c->page_size) ++shift;
+  return q1::KvView{static_cast<unsigned char *>(c->data), c->block_table, c->lengths, c->cu_seqlens, c->n_pages,
+                    c->table_width, c->table_stride, c->T, c->B, c->HK, c->D, c->group_size, shift};
+}
+
+q1::KvAttention kv_attention_view(const q1_kv_attention_args *a) {
+  return q1::KvAttention{a->q, a->o, a->lse, a->q_stride, a->o_stride, a->max_q, a->max_len, a->HQ, a->causal != 0, a->window,
+                         a->scale};
+}
+}  // namespace
+
+q1_status q1_kv_store(const q1_kv_cache *c, const void *k, int64_t k_stride, const void *v, int64_t v_stride, q1_dtype t,
+                      q1_stream stream) {
+  q1_status s = check_device();
+  if (s != Q1_OK) return s;
+  if ((s = check_kv(c)) != Q1_OK) return s;
+  if (t != Q1_BF16 && t != Q1_F16 && t != Q1_F32) return Q1_ERR_DTYPE;
+  if (c->T == 0) return Q1_OK;
+  if ((s = check_kv_rows(c, k, k_stride, c->HK, t)) != Q1_OK) return s;
+  if ((s = check_kv_rows(c, v, v_stride, c->HK, t)) != Q1_OK) return s;
+  return cuda_status(q1::launch_kv_store(kv_view(c), k, k_stride, v, v_stride, t, (cudaStream_t)stream));
+}
+
+q1_status q1_kv_load(const q1_kv_cache *c, void *k, int64_t k_stride, void *v, int64_t v_stride, q1_dtype t, q1_stream stream) {
+  q1_status s = check_device();
+  if (s != Q1_OK) return s;
+  if ((s = check_kv(c)) != Q1_OK) return s;
+  if (t != Q1_BF16 && t != Q1_F16 && t != Q1_F32) return Q1_ERR_DTYPE;
+  if (c->T == 0) return Q1_OK;
+  if ((s = check_kv_rows(c, k, k_stride, c->HK, t)) != Q1_OK) return s;
+  if ((s = check_kv_rows(c, v, v_stride, c->HK, t)) != Q1_OK) return s;
+  return cuda_status(q1::launch_kv_load(kv_view(c), k, k_stride, v, v_stride, t, (cudaStream_t)stream));
+}
+
+size_t q1_kv_attention_workspace_size(const q1_kv_cache *c, const q1_kv_attention_args *a) {
+  if (check_kv_attention_sizes(c, a) != Q1_OK || c->T == 0) return 0;
+  return q1::kv_decode_workspace_bytes(kv_view(c), kv_attention_view(a), (q1_dtype)a->dtype);
+}
+
+q1_status q1_kv_attention(const q1_kv_cache *c, const q1_kv_attention_args *a, void *workspace, size_t workspace_bytes,
+                          q1_stream stream) {
+  q1_status s = check_device();
+  if (s != Q1_OK) return s;
+  if ((s = check_kv_attention_sizes(c, a)) != Q1_OK) return s;
+  if ((s = check_kv(c)) != Q1_OK) return s;
+  if (c->T == 0) return Q1_OK;
+  const q1_dtype t = (q1_dtype)a->dtype;
+  if ((s = check_kv_rows(c, a->q, a->q_stride, a->HQ, t)) != Q1_OK) return s;
+  if ((s = check_kv_rows(c, a->o, a->o_stride, a->HQ, t)) != Q1_OK) return s;
+  if (!aligned(a->lse, 4)) return Q1_ERR_ALIGN;
+  const q1::KvView v = kv_view(c);
+  const q1::KvAttention at = kv_attention_view(a);
+  const size_t need = q1::kv_decode_workspace_bytes(v, at, t);
+  if (need && (s = check_ws(workspace, workspace_bytes, need)) != Q1_OK) return s;
+  return cuda_status(q1::launch_kv_decode(v, at, t, workspace, (cudaStream_t)stream));
+}
+
 q1_status q1_check_symmetric(const q1_weight *W, int32_t *d_is_symmetric, q1_stream stream) {
   q1_status s = check_device();
   if (s != Q1_OK) return s;

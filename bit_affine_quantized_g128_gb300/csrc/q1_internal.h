@@ -129,6 +129,56 @@ cudaError_t launch_delta_chunks(const DeltaView &a, q1_dtype t, void *workspace,
 // ---- sampling (q1_sample.cu)
 cudaError_t launch_sample(const q1_sample_args &a, cudaStream_t st);
 
+// ---- 4-bit cache (q1_kv.cu: store and load; q1_kv_decode.cu: attention of few rows)
+// The description of q1_kv_cache, as the kernels take it.
+struct KvView {
+  unsigned char *data;
+  const int32_t *table, *lengths, *cu;
+  int64_t n_pages, table_width, table_stride, T, B;
+  int HK, D, gs;
+  int page_shift;  // log2(page_size)
+#ifdef __CUDACC__
+  // Rows [t0, t1) of sequence b (cut to [0, T)).
+  __device__ __forceinline__ void range(int64_t b, int64_t &t0, int64_t &t1) const {
+    if (cu) {
+      t0 = min(max((int64_t)cu[b], (int64_t)0), T);
+      t1 = min(max((int64_t)cu[b + 1], t0), T);
+    } else {
+      const int64_t L = T / B;
+      t0 = b * L;
+      t1 = t0 + L;
+    }
+  }
+  __device__ __forceinline__ int block_bytes() const { return 16 * (D + 8 * (D / gs)); }
+  // The page of position p >= 0 of sequence b, or -1.
+  __device__ __forceinline__ int page(int64_t b, int p) const {
+    const int i = p >> page_shift;
+    if (i >= table_width) return -1;
+    const int pg = table[b * table_stride + i];
+    return pg >= 0 && pg < n_pages ? pg : -1;
+  }
+  // The block of head hk that holds position p, p in page pg.
+  __device__ __forceinline__ unsigned char *block(int pg, int hk, int p) const {
+    const int per = 1 << (page_shift - 4);
+    return data + (((int64_t)pg * HK + hk) * per + ((p >> 4) & (per - 1))) * block_bytes();
+  }
+#endif
+};
+// The arguments of q1_kv_attention.
+struct KvAttention {
+  const void *q;
+  void *o;
+  float *lse;
+  int64_t q_stride, o_stride, max_q, max_len;
+  int HQ, causal, window;
+  float scale;
+};
+cudaError_t launch_kv_store(const KvView &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride, q1_dtype t,
+                            cudaStream_t st);
+cudaError_t launch_kv_load(const KvView &c, void *k, int64_t k_stride, void *v, int64_t v_stride, q1_dtype t, cudaStream_t st);
+size_t kv_decode_workspace_bytes(const KvView &c, const KvAttention &a, q1_dtype t);
+cudaError_t launch_kv_decode(const KvView &c, const KvAttention &a, q1_dtype t, void *workspace, cudaStream_t st);
+
 // ---- device error words (each translation unit with bounded waits owns one)
 // and the diagnostics of the bounded waits: their limit, and producers that
 // issue nothing (every wait for their data then runs out)

@@ -29,6 +29,7 @@ EXPORTED = [
     "q1_set_wait_limit_ns", "q1_set_stalled_producers",
     "q1_decode_chain_workspace_size", "q1_decode_chain", "q1_pack_from_dense",
     "q1_gated_delta_workspace_size", "q1_gated_delta", "q1_sample",
+    "q1_kv_store", "q1_kv_load", "q1_kv_attention_workspace_size", "q1_kv_attention",
 ]
 
 
@@ -74,6 +75,21 @@ class _CSample(ctypes.Structure):
     pack = struct.Struct("@8P3q2i3f0q").pack
 
 
+class _CKvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("data", "block_table", "lengths", "cu_seqlens")] + \
+               [(n, ctypes.c_int64) for n in ("n_pages", "table_width", "table_stride", "T", "B")] + \
+               [(n, ctypes.c_int32) for n in ("HK", "D", "group_size", "page_size")]
+    pack = struct.Struct("@4P5q4i0q").pack
+
+
+class _CKvAttention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "o", "lse")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "o_stride", "max_q", "max_len")] + \
+               [(n, ctypes.c_int32) for n in ("HQ", "dtype", "causal", "window")] + \
+               [("scale", ctypes.c_float)]
+    pack = struct.Struct("@3P4q4if0q").pack
+
+
 _lib = None
 
 # K of the narrow kernel (q1_qmv / q1_qmm_narrow); q1_qmm runs larger K on the prefill path
@@ -117,6 +133,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "q1_gated_delta_workspace_size": ([ctypes.POINTER(_CDelta)], SZ),
         "q1_gated_delta": ([ctypes.POINTER(_CDelta), P, SZ, P], I32),
         "q1_sample": ([ctypes.POINTER(_CSample), P], I32),
+        "q1_kv_store": ([ctypes.POINTER(_CKvCache), P, I64, P, I64, I32, P], I32),
+        "q1_kv_load": ([ctypes.POINTER(_CKvCache), P, I64, P, I64, I32, P], I32),
+        "q1_kv_attention_workspace_size": ([ctypes.POINTER(_CKvCache), ctypes.POINTER(_CKvAttention)], SZ),
+        "q1_kv_attention": ([ctypes.POINTER(_CKvCache), ctypes.POINTER(_CKvAttention), P, SZ, P], I32),
         "q1_device_errors": ([ctypes.POINTER(ctypes.c_uint), P], I32),
         "q1_status_string": ([I32], ctypes.c_char_p),
     }
@@ -644,6 +664,166 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     if st:
         _check("q1_sample", st)
     return token, prob
+
+
+# bytes of a block of 16 tokens -> (D, group_size)
+_KV_BLOCKS = {16 * (d + 8 * d // gs): (d, gs) for d in (64, 128, 256) for gs in (64, 128) if gs <= d}
+
+
+def kv_cache(n_pages: int, heads: int, dim: int, page_size: int = 64, group_size: int = 64, device="cuda") -> torch.Tensor:
+    """An empty (zero) 4-bit cache: uint8 [n_pages, heads, page_size / 16, bytes of a block of 16 tokens].
+
+    dim 64, 128 or 256; group_size, the channels that share a scale and a bias, 64 or 128; page_size a power of
+    two of at least 16.  Its layout is in include/q1.h.  16-bit K and V take 3.6 (groups of 64) or 3.8 times as much."""
+    nbytes = 16 * (dim + 8 * dim // group_size) if group_size > 0 else 0
+    if _KV_BLOCKS.get(nbytes) != (dim, group_size):
+        raise ValueError(f"need dim 64, 128 or 256 and group_size 64 or 128, at most dim (got {dim}, {group_size})")
+    if n_pages < 0 or heads < 1 or not 16 <= page_size <= 65536 or page_size & (page_size - 1):
+        raise ValueError(f"need n_pages >= 0, heads >= 1 and page_size a power of two from 16 to 65536 (got {n_pages}, {heads}, {page_size})")
+    return torch.zeros((n_pages, heads, page_size // 16, nbytes), dtype=torch.uint8, device=device)
+
+
+def _kv(cache, block_table, lengths, cu_seqlens, T: int, dev):
+    """The checked description of a cache and the call's rows, the tensors it points into, and heads, dim and B."""
+    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] not in _KV_BLOCKS:
+        raise ValueError(f"cache must be a contiguous uint8 tensor as q1.kv_cache makes it (got {cache.dtype}, {tuple(cache.shape)})")
+    n_pages, heads, blocks, nbytes = cache.shape
+    dim, gs = _KV_BLOCKS[nbytes]
+    if blocks < 1 or blocks > 4096 or blocks & (blocks - 1):
+        raise ValueError(f"the pages of a cache hold a power of two of blocks, at most 4096 (got {blocks})")
+    if block_table.dtype != _I32 or block_table.dim() != 2:
+        raise ValueError(f"block_table must be int32 [B, pages] (got {block_table.dtype}, {tuple(block_table.shape)})")
+    B, width = block_table.shape
+    if B < 1:
+        raise ValueError("need at least one sequence")
+    if width > 1 and block_table.stride(1) != 1 or B > 1 and block_table.stride(0) < width:
+        block_table = block_table.contiguous()
+    lengths = _vector(lengths, "lengths", B, _I32, dev)
+    if lengths is None:
+        raise ValueError("lengths must be given")
+    if cu_seqlens is not None:
+        cu_seqlens = _vector(cu_seqlens, "cu_seqlens", B + 1, _I32, dev)
+    c = _CKvCache.from_buffer_copy(_CKvCache.pack(
+        cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), 0 if cu_seqlens is None else cu_seqlens.data_ptr(), n_pages,
+        width, block_table.stride(0), T, B, heads, dim, gs, 16 * blocks))
+    return c, (block_table, lengths, cu_seqlens), heads, dim, B
+
+
+def _kv_rows(x: torch.Tensor, name: str, B: int, packed: bool):
+    """x [T, H, D] (packed) or [B, L, H, D], as [T, H, D]."""
+    if x.dim() != (3 if packed else 4) or not packed and x.shape[0] != B:
+        raise ValueError(f"{name} must be {'[T, H, D] with' if packed else f'[{B}, L, H, D] without'} cu_seqlens (got {tuple(x.shape)})")
+    return x if packed else x.flatten(0, 1)
+
+
+def _kv_on_device(first, **tensors):
+    if _on_current_device(first[1], *tensors.values()):
+        return
+    _cuda(first[1], first[0])
+    for name, t in tensors.items():
+        _cuda(t, name, first[1].device, current=False)
+
+
+def kv_store(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor, *,
+             cu_seqlens: Optional[torch.Tensor] = None) -> None:
+    """Quantises K and V rows to 4 bits into the pages of their sequences (in place).
+
+    k, v [T, heads, dim] (one dtype: bf16, fp16 or fp32): sequence b has rows cu_seqlens[b] .. cu_seqlens[b+1] (int32
+    [B+1] on the device), its last tokens: the last row is token lengths[b] - 1 (lengths int32 [B], these rows
+    included).  Without cu_seqlens, k, v [B, L, heads, dim].  Token p of sequence b lies in page
+    block_table[b, p // page_size] (int32 [B, pages]); rows without a page in the cache are left out."""
+    _kv_on_device(("cache", cache), k=k, v=v, block_table=block_table)
+    dev, packed = cache.device, cu_seqlens is not None
+    dt = _x_dtype(k, "k")
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError(f"k and v must agree (got {k.dtype} {tuple(k.shape)}, {v.dtype} {tuple(v.shape)})")
+    B = block_table.shape[0] if block_table.dim() == 2 else 0
+    k, v = _kv_rows(k, "k", B, packed), _kv_rows(v, "v", B, packed)
+    c, keep, heads, dim, _ = _kv(cache, block_table, lengths, cu_seqlens, k.shape[0], dev)
+    if k.shape[1:] != (heads, dim):
+        raise ValueError(f"the cache holds {heads} heads of {dim} (k and v have {tuple(k.shape[1:])})")
+    per16 = 4 if k.dtype == _F32 else 8
+    k, kp, ks = _rows(k, heads, dim, per16)
+    v, vp, vs = _rows(v, heads, dim, per16)
+    st = (_lib or lib()).q1_kv_store(c, kp, ks, vp, vs, dt, _raw_stream(dev.index))
+    if st:
+        _check("q1_kv_store", st)
+
+
+def kv_load(cache: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor, rows: int, *,
+            cu_seqlens: Optional[torch.Tensor] = None, dtype=torch.bfloat16):
+    """The cached K and V of the last tokens of each sequence, as `dtype`.
+
+    With cu_seqlens, `rows` tokens in all, cu_seqlens[b+1] - cu_seqlens[b] of sequence b: two [rows, heads, dim].
+    Without it, `rows` tokens of each sequence: two [B, rows, heads, dim].  Tokens without a page are zeros."""
+    _kv_on_device(("cache", cache), block_table=block_table)
+    dev, packed = cache.device, cu_seqlens is not None
+    if dtype not in _DT:
+        raise ValueError(f"dtype must be bfloat16, float16 or float32 (got {dtype})")
+    B = block_table.shape[0] if block_table.dim() == 2 else 0
+    if rows < 0:
+        raise ValueError(f"rows must not be negative (got {rows})")
+    T = rows if packed else B * rows
+    c, keep, heads, dim, _ = _kv(cache, block_table, lengths, cu_seqlens, T, dev)
+    out = torch.empty((2, T, heads, dim), dtype=dtype, device=dev)
+    st = (_lib or lib()).q1_kv_load(c, out.data_ptr(), heads * dim, out.data_ptr() + T * heads * dim * out.element_size(), heads * dim,
+                                    _DT[dtype], _raw_stream(dev.index))
+    if st:
+        _check("q1_kv_load", st)
+    k, v = out.unbind(0)
+    return (k, v) if packed else (k.unflatten(0, (B, rows)), v.unflatten(0, (B, rows)))
+
+
+def kv_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor, *,
+                 cu_seqlens: Optional[torch.Tensor] = None, max_q: Optional[int] = None, max_len: Optional[int] = None,
+                 scale: Optional[float] = None, causal: bool = True, window: int = 0, return_lse: bool = False,
+                 workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """Attention of the sequences' last tokens over their 4-bit cache (their own K and V stored before).
+
+    q [T, HQ, dim] with cu_seqlens, else [B, L, HQ, dim]; rows as in kv_store; query head h reads head
+    h // (HQ / heads).  A row at position i sees tokens j <= i (causal; else all of its sequence), and with
+    window > 0 only j > i - window.  scale defaults to dim ** -0.5.  `max_q` (the longest sequence's rows) and
+    `max_len` (the largest of lengths) are best given: they pick the kernels and how the work is split; without them T
+    (or L) and the block table's width count.  Returns o like q, and with return_lse the fp32 logarithms of the sums
+    of exponentials, o without its last dimension; a row that sees nothing gets 0 and -inf."""
+    _kv_on_device(("q", q), cache=cache, block_table=block_table)
+    dev, dtype, packed = q.device, q.dtype, cu_seqlens is not None
+    dt = _x_dtype(q, "q")
+    B = block_table.shape[0] if block_table.dim() == 2 else 0
+    lead = q.shape[:-2]
+    q = _kv_rows(q, "q", B, packed)
+    T, HQ, D = q.shape
+    c, keep, heads, dim, B = _kv(cache, block_table, lengths, cu_seqlens, T, dev)
+    if D != dim or HQ < 1 or HQ % heads:
+        raise ValueError(f"the cache holds {heads} heads of {dim}; q must have a multiple of them (got {tuple(q.shape[1:])})")
+    if window < 0 or window and not causal:
+        raise ValueError("window must not be negative, and needs causal")
+    q, qp, qs = _rows(q, HQ, dim, 4 if dtype == _F32 else 8)
+    o = torch.empty((T, HQ, dim), dtype=dtype, device=dev) if out is None else _out(out, (T, HQ, dim), dtype, dev)
+    lse = torch.empty((T, HQ), dtype=_F32, device=dev) if return_lse else None
+    if max_q is None or not packed:
+        max_q = T if packed else lead[1]
+    if max_len is None:
+        max_len = c.table_width * c.page_size
+    a = _CKvAttention.from_buffer_copy(_CKvAttention.pack(
+        qp, o.data_ptr(), 0 if lse is None else lse.data_ptr(), qs, HQ * dim, max_q, max_len, HQ, dt, 1 if causal else 0,
+        min(window, 2 ** 31 - 1), dim ** -0.5 if scale is None else scale))
+    L, stream = _lib or lib(), _raw_stream(dev.index)
+    if workspace is not None:
+        _cuda(workspace, "workspace", dev)
+        st = L.q1_kv_attention(c, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    else:
+        st = L.q1_kv_attention(c, a, None, 0, stream)
+        if st == 6:  # Q1_ERR_WORKSPACE: the context is split
+            n = L.q1_kv_attention_workspace_size(c, a)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            st = L.q1_kv_attention(c, a, workspace.data_ptr(), n, stream)
+    if st:
+        _check("q1_kv_attention", st)
+    if not packed:
+        o = o.reshape(*lead, HQ, dim)
+        lse = None if lse is None else lse.reshape(*lead, HQ)
+    return (o, lse) if return_lse else o
 
 
 def check_symmetric(W: Q1Weight) -> torch.Tensor:

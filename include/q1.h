@@ -372,6 +372,82 @@ typedef struct {
 } q1_sample_args;
 q1_status q1_sample(const q1_sample_args *args, q1_stream stream);
 
+/* ---- 4-bit cache of keys and values ------------------------------------------
+ * (the cache of the softmax-attention layers that the Q1 linears of a decoder
+ * surround; "Support Bonsai-27B affine Q1", higgs PR #212, "What": the affine
+ * form w = scale * q + bias, here with 4 bits.)
+ * A channel's value is scale * q + bias in fp32, q in -8..7, with one bf16 scale
+ * and bias per token, head and group of group_size channels.
+ *   data        [n_pages][HK][page_size / 16][block], 16-byte aligned.  A block is 16
+ *               consecutive tokens of one head: K codes, K metadata, V codes, V
+ *               metadata, 32-bit words, 16 * (D + 8 D / group_size) bytes in all.
+ *               A code word holds channels 8w .. 8w+7 of one token, each q + 8, lowest
+ *               bits first; a metadata word the scale (low half) and the bias.
+ *                 K codes   [token][D / 8], word w at place 2 (w % 4) + w / 4 for D = 64,
+ *                           else 16 (w / 16) + 4 (w % 4) + w % 16 / 4
+ *                 V codes   [D / 8][token], token t at place 4 (t / 2 % 4) + t % 2 + 2 (t / 8)
+ *                 metadata  [token][D / group_size]
+ *   block_table device int32, row b at b * table_stride: the pages of sequence b;
+ *               position p is in page block_table[b][p / page_size].  A page outside
+ *               [0, n_pages), or a position beyond table_width pages, means not there:
+ *               such a token is not stored, loads as zeros and is not attended to.
+ *   lengths     device int32 [B]: the tokens of each sequence, those of this call
+ *               included.
+ *   cu_seqlens  device int32 [B+1], ascending from 0 to T: rows [cu[b], cu[b+1]) of the
+ *               call's T rows belong to sequence b and stand for its last positions,
+ *               the last of them for position lengths[b] - 1.  NULL: T / B rows each.
+ *               Offsets that leave [0, T] or decrease are cut to it.  Rows with a
+ *               negative position (more rows than tokens) are not stored, load as
+ *               zeros and attend to nothing.
+ * The three calls take the same description, so a step is: store the new K and V,
+ * then attend.  lengths, block_table and cu_seqlens are read on the device: a
+ * captured graph follows their contents.  D 64, 128 or 256; group_size 64 or 128, at most
+ * D; page_size a power of two from 16 to 65536.  Bytes of a page that no stored token owns are left as they
+ * are, and may hold anything. */
+typedef struct {
+  void *data;
+  const int32_t *block_table, *lengths, *cu_seqlens;
+  int64_t n_pages, table_width, table_stride, T, B;
+  int32_t HK, D, group_size, page_size;
+} q1_kv_cache;
+/* k, v [T][HK][D] in dtype, rows *_stride elements apart, heads contiguous; 16-byte
+ * aligned, strides multiples of 16 bytes (so they may be columns of one projection's rows).
+ * Per group, every operation in fp32 and rounded once:
+ *   x       clamped to [-32768, 32768];  lo, hi = least and largest x
+ *   bias  = bf16(lo + 8 (hi - lo) f(1/15))
+ *   scale = bf16(max((hi - bias) f(1/7), (bias - lo) / 8)), 0 where that is below 2^-100
+ *   q     = rint((x - bias) f(1 / scale)) cut to [-8, 7], 0 where scale is 0
+ * f() rounds to fp32.  A group with a NaN gets scale and bias NaN.  Two rows of one call for
+ * the same place leave it undefined. */
+q1_status q1_kv_store(const q1_kv_cache *cache, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                      q1_dtype dtype, q1_stream stream);
+/* The other way round: fp32 values scale * q + bias (one rounding), rounded once to dtype. */
+q1_status q1_kv_load(const q1_kv_cache *cache, void *k, int64_t k_stride, void *v, int64_t v_stride, q1_dtype dtype,
+                     q1_stream stream);
+/* Attention of T query rows over the cache.  Query head h reads head h / (HQ / HK).
+ *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  lse = log sum_j p_j
+ * over the positions j below lengths[b] that the row at position i sees: j <= i if causal,
+ * and j > i - window if window > 0 (causal only).  A row that sees nothing gets o = 0
+ * and lse = -inf.  What is not seen may hold anything.
+ *   q, o        [T][HQ][D] in dtype, rows *_stride elements apart, as above; o must not overlap q
+ *   lse         fp32 [T][HQ] or NULL
+ *   max_q       the longest sequence's rows, max_len the largest of lengths: hints that pick
+ *               the kernels and their split (results do not depend on them beyond rounding).
+ * Codes are multiplied as they are, so a cached value enters exactly; sums, maxima and
+ * the states of the softmax are fp32.  Workspace: q1_kv_attention_workspace_size bytes,
+ * 256-byte aligned (may be 0); it goes by sizes and hints, not by pointers. */
+typedef struct {
+  const void *q;
+  void *o;
+  float *lse;
+  int64_t q_stride, o_stride, max_q, max_len;
+  int32_t HQ, dtype, causal, window;
+  float scale;
+} q1_kv_attention_args;
+size_t q1_kv_attention_workspace_size(const q1_kv_cache *cache, const q1_kv_attention_args *args);
+q1_status q1_kv_attention(const q1_kv_cache *cache, const q1_kv_attention_args *args, void *workspace,
+                          size_t workspace_bytes, q1_stream stream);
+
 /* ---- symmetric check (higgs PR #212, walkthrough: symmetric bias
  * compaction and validation) -------------------------------------------------
  * Writes 1 to *d_is_symmetric (device int32) iff every stored bias equals

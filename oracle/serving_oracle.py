@@ -92,3 +92,87 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     c = np.cumsum(w[ids])
     at = 0 if not u > 0 else min(int((c <= u * c[-1]).sum()), len(ids) - 1)
     return int(ids[at]), float(w[ids[at]] / c[-1])
+
+
+# ---- the 4-bit cache
+def _bf16(x):
+    """fp32 rounded to the nearest bf16 (ties to even), as fp32."""
+    u = np.asarray(x, np.float32).view(np.uint32).astype(np.uint64)
+    return ((u + 0x7FFF + ((u >> 16) & 1)) & 0xFFFF0000).astype(np.uint32).view(np.float32)
+
+
+def kv_quantise(x, gs):
+    """q int [..., D], scale and bias fp32 [..., D/gs] of rows x fp32 [..., D]: one fp32 rounding per operation."""
+    f = np.float32
+    x = np.asarray(x, f)
+    g = np.clip(x, f(-32768), f(32768)).reshape(*x.shape[:-1], x.shape[-1] // gs, gs)
+    bad = np.isnan(g).any(-1)
+    g = np.where(bad[..., None], f(0), g)
+    lo, hi = g.min(-1), g.max(-1)
+    bias = _bf16(lo + f(8) * ((hi - lo) * f(1 / 15)))
+    scale = _bf16(np.maximum((hi - bias) * f(1 / 7), (bias - lo) * f(0.125)))
+    scale = np.where(scale < 2.0 ** -100, f(0), scale)
+    inv = np.where(scale > 0, f(1) / np.where(scale > 0, scale, f(1)), f(0)).astype(f)
+    q = np.clip(np.rint((g - bias[..., None]) * inv[..., None]), -8, 7).astype(np.int64).reshape(x.shape)
+    nan = np.array(0x7FC00000, np.uint32).view(f)
+    return q, np.where(bad, nan, scale).astype(f), np.where(bad, nan, bias).astype(f)
+
+
+def kv_values(q, scale, bias):
+    """The cached values in fp32: q scale + bias, rounded once."""
+    gs = q.shape[-1] // scale.shape[-1]
+    s, b = (np.repeat(np.asarray(a, np.float64), gs, -1) for a in (scale, bias))
+    return (q * s + b).astype(np.float32)
+
+
+def kv_block(kq, ks, kb, vq, vs, vb):
+    """The bytes of a block: codes int [16, D] and fp32 (bf16 values) metadata [16, G] of 16 tokens of one head."""
+    D = kq.shape[1]
+    out = []
+    for q, s, b, v in ((kq, ks, kb, False), (vq, vs, vb, True)):
+        words = np.zeros(2 * D, np.uint32)
+        for t in range(16):
+            for w in range(D // 8):
+                word = 0
+                for i in range(8):
+                    word |= (int(q[t, 8 * w + i]) + 8) << (4 * i)
+                if v:
+                    at = 16 * w + 4 * (t // 2 % 4) + t % 2 + 2 * (t // 8)
+                elif D == 64:
+                    at = t * 8 + 2 * (w % 4) + w // 4
+                else:
+                    at = t * (D // 8) + 16 * (w // 16) + 4 * (w % 4) + w % 16 // 4
+                words[at] = word
+        meta = (s.astype(np.float32).view(np.uint32) >> 16) | (b.astype(np.float32).view(np.uint32) & 0xFFFF0000)
+        out += [words, meta.astype(np.uint32).reshape(-1)]
+    return np.concatenate(out).view(np.uint8)
+
+
+def kv_attention(q, k, v, pos, scale, causal=True, window=0, there=None):
+    """o, lse, and what rounding errors of o are relative to, of rows q [n, HQ, D] at positions pos [n] over k, v [len,
+    HK, D] (float64).  `there` [len]: tokens that have a page.  Returns o, lse [n, HQ], sum p |v| [n, HQ, D] and the
+    largest scale sum_d |q_d k_d| of a row [n, HQ]."""
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    n, HQ, D = q.shape
+    L, HK = k.shape[:2]
+    o, size = np.zeros(q.shape), np.zeros(q.shape)
+    lse, big = np.full((n, HQ), -np.inf), np.zeros((n, HQ))
+    j = np.arange(L)
+    for i in range(n):
+        see = (j <= pos[i]) if causal else np.full(L, pos[i] >= 0)
+        if window:
+            see &= j > pos[i] - window
+        if there is not None:
+            see &= there
+        if not see.any():
+            continue
+        for h in range(HQ):
+            kk, vv = k[see, h // (HQ // HK)], v[see, h // (HQ // HK)]
+            x = scale * (kk @ q[i, h])
+            m = x.max()
+            p = np.exp(x - m)
+            s = p.sum()
+            o[i, h], size[i, h] = p @ vv / s, p @ np.abs(vv) / s
+            lse[i, h] = m + np.log(s)
+            big[i, h] = abs(scale) * (np.abs(kk) @ np.abs(q[i, h])).max()
+    return o, lse, size, big
