@@ -3,6 +3,7 @@
 // chaining.  No device memory is allocated here; scratch (the prefill path's
 // fp16 activation rows, the fused FFN's intermediate) comes from the caller's
 // workspace.
+#include <algorithm>
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
@@ -461,8 +462,16 @@ q1_status q1_kv_load(const q1_kv_cache *c, void *k, int64_t k_stride, void *v, i
   return cuda_status(q1::launch_kv_load(kv_view(c), k, k_stride, v, v_stride, t, (cudaStream_t)stream));
 }
 
+namespace {
+// Many rows per key head go to the tensor-memory kernel (fp32 ones do not: its
+// operands hold 16-bit inputs exactly, not fp32 ones).
+bool kv_by_tiles(const q1_kv_cache *c, const q1_kv_attention_args *a) {
+  return a->dtype != Q1_F32 && std::min(a->max_q, c->T) * (a->HQ / c->HK) > 64;
+}
+}  // namespace
+
 size_t q1_kv_attention_workspace_size(const q1_kv_cache *c, const q1_kv_attention_args *a) {
-  if (check_kv_attention_sizes(c, a) != Q1_OK || c->T == 0) return 0;
+  if (check_kv_attention_sizes(c, a) != Q1_OK || c->T == 0 || kv_by_tiles(c, a)) return 0;
   return q1::kv_decode_workspace_bytes(kv_view(c), kv_attention_view(a), (q1_dtype)a->dtype);
 }
 
@@ -479,6 +488,7 @@ q1_status q1_kv_attention(const q1_kv_cache *c, const q1_kv_attention_args *a, v
   if (!aligned(a->lse, 4)) return Q1_ERR_ALIGN;
   const q1::KvView v = kv_view(c);
   const q1::KvAttention at = kv_attention_view(a);
+  if (kv_by_tiles(c, a)) return cuda_status(q1::launch_kv_prefill(v, at, t, (cudaStream_t)stream));
   const size_t need = q1::kv_decode_workspace_bytes(v, at, t);
   if (need && (s = check_ws(workspace, workspace_bytes, need)) != Q1_OK) return s;
   return cuda_status(q1::launch_kv_decode(v, at, t, workspace, (cudaStream_t)stream));
@@ -503,6 +513,7 @@ q1_status push_diagnostics() {
   cudaError_t e = q1::set_narrow_diagnostics(ns, stall);
   if (e == cudaSuccess) e = q1::set_wide_diagnostics(ns, stall);
   if (e == cudaSuccess) e = q1::set_delta_diagnostics(ns, stall);
+  if (e == cudaSuccess) e = q1::set_kv_diagnostics(ns, stall);
   return cuda_status(e);
 }
 }  // namespace
@@ -524,12 +535,13 @@ q1_status q1_set_stalled_producers(int stall) {
 q1_status q1_device_errors(unsigned int *flags, q1_stream stream) {
   q1_status s = check_device();
   if (s != Q1_OK) return s;
-  cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess;
+  cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess, e4 = cudaSuccess;
   unsigned int v = q1::read_and_clear_wide_errors((cudaStream_t)stream, &e1);
   v |= q1::read_and_clear_narrow_errors((cudaStream_t)stream, &e2) << 1;
   v |= q1::read_and_clear_delta_errors((cudaStream_t)stream, &e3) << 2;
+  v |= q1::read_and_clear_kv_errors((cudaStream_t)stream, &e4) << 3;
   if (flags) *flags = v;
-  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess) return Q1_ERR_CUDA;
+  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess || e4 != cudaSuccess) return Q1_ERR_CUDA;
   return v ? Q1_ERR_TIMEOUT : Q1_OK;
 }
 

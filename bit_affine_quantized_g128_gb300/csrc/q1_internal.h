@@ -129,7 +129,8 @@ cudaError_t launch_delta_chunks(const DeltaView &a, q1_dtype t, void *workspace,
 // ---- sampling (q1_sample.cu)
 cudaError_t launch_sample(const q1_sample_args &a, cudaStream_t st);
 
-// ---- 4-bit cache (q1_kv.cu: store and load; q1_kv_decode.cu: attention of few rows)
+// ---- 4-bit cache (q1_kv.cu: store and load; q1_kv_decode.cu: attention of few rows;
+// q1_kv_prefill.cu: of many, bf16 and fp16 only)
 // The description of q1_kv_cache, as the kernels take it.
 struct KvView {
   unsigned char *data;
@@ -178,6 +179,7 @@ cudaError_t launch_kv_store(const KvView &c, const void *k, int64_t k_stride, co
 cudaError_t launch_kv_load(const KvView &c, void *k, int64_t k_stride, void *v, int64_t v_stride, q1_dtype t, cudaStream_t st);
 size_t kv_decode_workspace_bytes(const KvView &c, const KvAttention &a, q1_dtype t);
 cudaError_t launch_kv_decode(const KvView &c, const KvAttention &a, q1_dtype t, void *workspace, cudaStream_t st);
+cudaError_t launch_kv_prefill(const KvView &c, const KvAttention &a, q1_dtype t, cudaStream_t st);
 
 // ---- device error words (each translation unit with bounded waits owns one)
 // and the diagnostics of the bounded waits: their limit, and producers that
@@ -185,8 +187,10 @@ cudaError_t launch_kv_decode(const KvView &c, const KvAttention &a, q1_dtype t, 
 cudaError_t set_narrow_diagnostics(unsigned long long wait_ns, int stall);
 cudaError_t set_wide_diagnostics(unsigned long long wait_ns, int stall);
 cudaError_t set_delta_diagnostics(unsigned long long wait_ns, int stall);
+cudaError_t set_kv_diagnostics(unsigned long long wait_ns, int stall);
 unsigned int read_and_clear_wide_errors(cudaStream_t st, cudaError_t *err);
 unsigned int read_and_clear_narrow_errors(cudaStream_t st, cudaError_t *err);
 unsigned int read_and_clear_delta_errors(cudaStream_t st, cudaError_t *err);
+unsigned int read_and_clear_kv_errors(cudaStream_t st, cudaError_t *err);
 
 }  // namespace q1

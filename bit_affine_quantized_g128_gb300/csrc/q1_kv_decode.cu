@@ -152,7 +152,7 @@ struct Span {
     const int64_t there = c.table_width << c.page_shift;
     int end = a.causal ? pos0 + row1 / r + 1 : (pos0 + row1 / r < 0 ? 0 : len);  // positions below it are seen
     end = (int)min((int64_t)end, there);
-    const int begin = a.window ? max(pos0 + row0 / r - a.window + 1, 0) : 0;
+    const int begin = a.window ? (int)max((int64_t)pos0 + row0 / r - a.window + 1, (int64_t)0) : 0;
     first = begin >> 4;
     count = end > begin ? ((end + 15) >> 4) - first : 0;
     return true;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
         f[nt][k] = __shfl_sync(0xffffffffu, pow2f(-e), from) * (a.scale * kLog2e);
         const int pos = s.pos0 + min(tile * kRows + 8 * nt + 2 * t + k, s.rows - 1) / r;
         hi[nt][k] = pos < 0 ? -1 : a.causal ? pos : s.len - 1;
-        lo[nt][k] = a.window ? pos - a.window : -1;
+        lo[nt][k] = a.window ? max(pos, 0) - a.window : -1;
       }
     }
     if constexpr (C::kQShared) __syncthreads();

@@ -433,8 +433,12 @@ q1_status q1_kv_load(const q1_kv_cache *cache, void *k, int64_t k_stride, void *
  *   lse         fp32 [T][HQ] or NULL
  *   max_q       the longest sequence's rows, max_len the largest of lengths: hints that pick
  *               the kernels and their split (results do not depend on them beyond rounding).
- * Codes are multiplied as they are, so a cached value enters exactly; sums, maxima and
- * the states of the softmax are fp32.  Workspace: q1_kv_attention_workspace_size bytes,
+ * Sums, maxima and the states of the softmax are fp32.  Keys enter exactly.  Few rows per
+ * key head, and all fp32 ones, go through mma.sync with the codes as they are: values enter
+ * exactly, and the weights as fp16 (bf16 outputs) or with 22 bits.  Many bf16 or fp16 rows go
+ * through the tcgen05 kernel, whose values and weights are rounded to fp16; there, what a
+ * cache from elsewhere holds beyond fp16 in V reads as NaN.  Where a wait of that kernel runs
+ * out (q1_device_errors, bit 3) the outputs are undefined.  Workspace: q1_kv_attention_workspace_size bytes,
  * 256-byte aligned (may be 0); it goes by sizes and hints, not by pointers. */
 typedef struct {
   const void *q;
@@ -463,9 +467,9 @@ q1_status q1_device_errors(unsigned int *flags, q1_stream stream);
 const char *q1_status_string(q1_status s);
 /* Controls of the bounded waits (no counterpart on the pages; for tests of
  * the timeout path).  Every wait of the narrow, prefill and chunked delta-rule
- * kernels on another role's progress is bounded; one that runs out sets the
+ * kernels, and of the cache's attention for many rows, on another role's progress is bounded; one that runs out sets the
  * device error word (bit 0: prefill kernels, bit 1: narrow kernels, bit 2:
- * delta-rule kernels).  The outputs of such a call are undefined, and so are the
+ * delta-rule kernels, bit 3: attention).  The outputs of such a call are undefined, and so are the
  * states of all its sequences: columns whose own waits did not run out may have
  * advanced, so the caller restores them before it repeats the call.  Later waits of the
  * prefill kernels then give up at once until q1_device_errors reads the word;

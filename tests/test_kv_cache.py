@@ -253,13 +253,16 @@ def test_many_sequences(q1):
 
 
 # ---- attention
-def check(q1, c, cache, new, HQ, dtype="bf16", causal=True, window=0, seed=11, scale=None, qsize=1.0, table=None, exact_k=True, **kw):
+def check(q1, c, cache, new, HQ, dtype="bf16", causal=True, window=0, seed=11, scale=None, qsize=1.0, table=None, tiles=False, **kw):
     """One call against the oracle.  Per value, with p the softmax's weights (sum 1):
       the output's rounding          eps / 2 |o|, but no less than half a step of the type's subnormals, eps / 2 times its least
                                      normal value (2^-25 for fp16: below 2^-14 its steps stay 2^-24)
       P scale as fp16                2^-11 sum p |v - bias| <= 2^-11 (sum p |v| + |bias|): bf16 outputs; a sum of two, 2^-22, else
       a logit's fp32 rounding        (D / 8 + 16) 2^-24 scale sum |q k| of relative error of p, and 2^-21 from exp
-    an error of p by a factor 1 + d moves o by at most 2 d sum p |v|."""
+    an error of p by a factor 1 + d moves o by at most 2 d sum p |v|.
+    tiles: the form for many rows, whose V is rounded to fp16 as well: 2^-11 sum p |v| for P and for V, 2^-25 for values below
+    fp16's normal ones and len 2^-32 max |v| for weights below them (2^-25 against a largest weight of at least 2^7); logits'
+    code and bias parts are summed separately, both parts' sizes count, and sums of q enter with 2^-22."""
     rng = _rng(seed)
     D, HK, T = c.D, c.heads, sum(new)
     q, qv = _rounded(rng.standard_normal((T, HQ, D)) * qsize, dtype)
@@ -279,8 +282,15 @@ def check(q1, c, cache, new, HQ, dtype="bf16", causal=True, window=0, seed=11, s
         want, want_lse, size, big = O.kv_attention(qv[rows], c.kval[b], c.vval[b], pos, scale, causal, window, there)
         bias = np.repeat(np.abs(c.vq[b][2]).max(0).repeat(c.gs, -1), HQ // HK, 0) if c.lengths[b] else 0.0
         logit = (D / 8 + 16) * 2.0 ** -24 * big
+        floor = 0.0
+        if tiles and c.lengths[b]:
+            kb = np.abs(c.kq[b][2]).max(0).repeat(c.gs, -1).repeat(HQ // HK, 0)
+            sums = abs(scale) * (kb * np.abs(qv[rows])).sum(-1)
+            logit = logit + ((D / 8 + 16) * 2.0 ** -24 * 2 + 2.0 ** -22) * sums
+            part, bias = 2 * 2.0 ** -11, 0.0
+            floor = 2.0 ** -25 + c.lengths[b] * 2.0 ** -32 * np.abs(c.vval[b]).max()
         info = torch.finfo(DTYPES[dtype])
-        bound = info.eps / 2 * np.maximum(np.abs(want), info.tiny) + part * (size + bias) + 2 * (2.0 ** -21 + logit)[..., None] * (size + bias)
+        bound = info.eps / 2 * np.maximum(np.abs(want), info.tiny) + floor + part * (size + bias) + 2 * (2.0 ** -21 + logit)[..., None] * (size + bias)
         err = np.abs(got[rows] - want)
         assert (err <= bound).all(), (b, float((err / np.maximum(bound, 1e-300)).max()))
         empty = np.isneginf(want_lse)
@@ -311,6 +321,27 @@ FEW = [  # D, gs, HK, HQ / HK, page, dtype, lengths, new, window
 def test_attention_of_few_rows(q1, D, gs, HK, r, page, dtype, lengths, new, window):
     c = Cache(q1, lengths, HK, D, gs, page, seed=sum(lengths))
     check(q1, c, c.store(q1), new, HK * r, dtype, window=window)
+
+
+MANY = [  # D, gs, HK, HQ / HK, page, dtype, lengths, new, window
+    (128, 64, 1, 4, 64, "bf16", [130], [130], 0),
+    (128, 64, 2, 2, 32, "fp16", [300, 40], [300, 33], 0),
+    (128, 128, 1, 5, 16, "bf16", [257, 600, 70], [100, 1, 70], 0),
+    (64, 64, 2, 1, 16, "bf16", [520, 129], [300, 129], 0),
+    (64, 64, 1, 8, 128, "fp16", [400, 33, 900], [17, 33, 90], 200),
+    (256, 64, 1, 2, 64, "bf16", [200, 65], [200, 65], 0),
+    (256, 128, 1, 6, 32, "fp16", [700, 64], [50, 64], 0),
+    (256, 64, 2, 1, 16, "bf16", [333], [200], 64),
+    (128, 64, 1, 1, 64, "bf16", [700], [513], 1),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,gs,HK,r,page,dtype,lengths,new,window", MANY)
+def test_attention_of_many_rows(q1, D, gs, HK, r, page, dtype, lengths, new, window):
+    c = Cache(q1, lengths, HK, D, gs, page, seed=sum(lengths))
+    check(q1, c, c.store(q1), new, HK * r, dtype, window=window, tiles=True)
+    assert q1.device_errors() == 0
 
 
 @pytest.mark.gpu
@@ -410,6 +441,94 @@ def test_offsets_beyond_32_bits(q1):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 256])
+def test_many_rows_that_see_nothing_and_small_hints(q1, D):
+    # no tokens, fewer tokens than rows, missing pages (a whole tile's too), a short table; more row tiles than the hint foresees
+    c = Cache(q1, [0, 30, 200, 320, 90], 1, D, page=32, seed=21)
+    cache = c.store(q1)
+    table = c.table.copy()
+    table[2, [0, 2]] = [-1, c.n_pages]
+    table[3, 0:4] = -1
+    new = [40, 70, 130, 100, 5]
+    check(q1, c, cache, new, 4, table=table, tiles=True)
+    check(q1, c, cache, new, 4, table=np.ascontiguousarray(table[:, :3]), tiles=True)
+    check(q1, c, cache, new, 4, "fp16", table=table, tiles=True, causal=False)
+    check(q1, c, cache, new, 4, table=table, tiles=True, window=20)
+    check(q1, c, cache, [0, 0, 200, 0, 90], 6, table=table, tiles=True, max_q=20)
+    check(q1, c, cache, [0, 0, 200, 0, 90], 6, "fp16", tiles=True, max_q=13, max_len=1)
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_many_rows_beside_what_they_do_not_see(q1):
+    # NaN everywhere but in the sequences; NaN in K and V of one token: only rows that see it become NaN
+    c = Cache(q1, [300, 140], 1, 128, page=32, seed=22)
+    nan = torch.full((1, 1, 128), float("nan"), device="cuda")
+    for window, at, kv in ((0, 290, "v"), (0, 290, "k"), (50, 160, "v"), (50, 160, "k"), (50, 299, "v"), (0, 0, "v")):
+        cache = torch.full((c.n_pages, 1, 2, 16 * (128 + 16)), 255, dtype=torch.uint8, device="cuda")
+        rows = [torch.from_numpy(np.concatenate(x).astype(np.float32)).cuda() for x in (c.k, c.v)]
+        cu = torch.tensor([0, 300, 440], dtype=torch.int32).cuda()
+        q1.kv_store(cache, *rows, c.d_table(), c.d_lengths(), cu_seqlens=cu)
+        one = [r[at:at + 1].clone() for r in rows]
+        one[kv == "v"] = nan
+        q1.kv_store(cache, *one, c.d_table(), torch.tensor([at + 1, 0], dtype=torch.int32).cuda(),
+                    cu_seqlens=torch.tensor([0, 1, 1], dtype=torch.int32).cuda())
+        q, qv = _rounded(_rng(9).standard_normal((280, 2, 128)), "bf16")
+        o, lse = q1.kv_attention(q.cuda(), cache, c.d_table(), c.d_lengths(), cu_seqlens=torch.tensor([0, 140, 280], dtype=torch.int32).cuda(),
+                                 max_q=140, max_len=300, window=window, return_lse=True)
+        for s in range(2):
+            pos = np.arange(140) + c.lengths[s] - 140
+            hit = (pos >= at) & ((pos < at + window) if window else True) if s == 0 else np.zeros(140, bool)
+            want, _, size, _ = O.kv_attention(qv[140 * s:140 * s + 140], c.kval[s], c.vval[s], pos, 128 ** -0.5, True, window)
+            got = o[140 * s:140 * s + 140].double().cpu().numpy()
+            assert np.isnan(got[hit]).all()
+            # check()'s bound with its logits' part below 2^-14
+            assert (np.abs(got - want)[~hit] <= (2.0 ** -8 * np.abs(want) + 2.0 ** -9 * size)[~hit]).all(), (window, at, kv, s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_sizes_of_values_by_tiles(q1, dtype):
+    rng = _rng(23)
+    n = 500
+    up = np.exp(rng.standard_normal((n, 1, 1))) * np.logspace(-8, 3, n)[:, None, None]
+    for size in (up, up[::-1], np.full((n, 1, 1), 1e-3), np.where(np.arange(n) < 300, 0.0, 1.0)[:, None, None]):
+        c = Cache(q1, [n], 1, 128, seed=24, v=[rng.standard_normal((n, 1, 128)) * size])
+        check(q1, c, c.store(q1), [90], 2, dtype, tiles=True)
+    c = Cache(q1, [n], 1, 128, seed=25, k=[20 * rng.standard_normal((n, 1, 128))])
+    for kw in (dict(qsize=3.0), dict(scale=-0.05), dict(scale=0.0), dict(qsize=1e-4, scale=1e4), dict(qsize=1e4, scale=1e-6)):
+        check(q1, c, c.store(q1), [90], 2, dtype, tiles=True, **kw)
+
+
+@pytest.mark.gpu
+def test_tiles_beyond_32_bits(q1):
+    n_pages = (1 << 32) // (2 * 4 * 16 * 144) + 40
+    c = Cache(q1, [200, 70], 2, 128, seed=26, n_pages=n_pages)
+    check(q1, c, c.store(q1, noise=False), [200, 33], 2, tiles=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [128, 256])
+def test_stalled_expansion_times_out_and_recovers(q1, D):
+    # no tile is expanded: the waits run out, the call returns, bit 3 reports it, and the next call is right
+    c = Cache(q1, [300], 1, D, seed=27)
+    cache = c.store(q1)
+    assert q1.device_errors() == 0
+    try:
+        q1.set_wait_limit_ns(1_000_000)
+        q1.set_stalled_producers(True)
+        q1.kv_attention(torch.zeros(1, 300, 4, D, dtype=torch.bfloat16, device="cuda"), cache, c.d_table(), c.d_lengths())
+        torch.cuda.synchronize()
+        assert q1.device_errors() == 8
+    finally:
+        q1.set_stalled_producers(False)
+        q1.set_wait_limit_ns(0)
+    assert q1.device_errors() == 0
+    check(q1, c, cache, [300], 4, tiles=True)
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.gpu
 def test_offsets_out_of_range_stay_inside(q1):
     # (results are undefined; nothing outside the arrays is touched, and the others are right)
     c = Cache(q1, [50, 60], 1, 64, seed=15)
@@ -418,6 +537,8 @@ def test_offsets_out_of_range_stay_inside(q1):
     for cu in ([0, 9, 4], [-5, 2, 4], [3, 1, 1 << 30], [0, 0, 0], [4, 4, 4]):
         q1.kv_attention(q, cache, c.d_table(), c.d_lengths(), cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), max_q=2, max_len=60)
         q1.kv_load(cache, c.d_table(), c.d_lengths(), 4, cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+        q1.kv_attention(q.half().repeat(1, 64, 1), cache, c.d_table(), c.d_lengths(), cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(),
+                        max_q=2, max_len=60)
     for lengths in ([-3, 60], [1 << 30, 60], [-(1 << 31), (1 << 31) - 1]):
         d = torch.tensor(lengths, dtype=torch.int32).cuda()
         q1.kv_attention(q, cache, c.d_table(), d, cu_seqlens=torch.tensor([0, 2, 4], dtype=torch.int32).cuda(), max_q=2, max_len=60)
