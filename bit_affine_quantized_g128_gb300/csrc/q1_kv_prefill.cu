@@ -9,8 +9,10 @@
 //   P = 2^(f S - M + 7) as fp16    a thread per row, back into S's columns
 //   O += P V                       P from tensor memory, O stays in tensor memory
 //
-// Roles: warps 0-3 and 4-7 the softmax of a row tile each (heads of 256: 0-3, and 4-7
-// expand K); warps 8-11 expand K and V; warp 12 issues the MMAs.
+// Roles, in groups of four warps: the softmax of a row tile each; K's expansion; V's; the
+// MMAs (one thread).  Five roles share each scheduler and its instruction cache, so their loops
+// are kept short (a few KB each): with the same loops unrolled twice as far the kernel took
+// 1.5 times as long, though it issued fewer instructions.
 //
 // Exactness.  K enters as scale q, which fp16 holds exactly (8 bits of scale, 4 of
 // code), and the biases through one more k16 step: columns bias_g (twice per
@@ -19,8 +21,8 @@
 // largest value lies in [2^7, 2^8): bf16 and fp16 inputs are exact down to 2^-22 of
 // that.  A 17th column of K is -inf where a token's page is missing, against 1 in Q.
 // V is scale q + bias rounded to fp16 (2^-12), P is rounded to fp16 (2^-12); the sum
-// of P is fp32 of the unrounded values.  M is a reference that moves when a logit exceeds it
-// by more than 8 octaves; 2^7 keeps all of P that matters among fp16's normal values.
+// of P is fp32 of the unrounded values.  M is a reference that moves when a tile's P would
+// overflow fp16; 2^7 keeps all of P that matters among fp16's normal values.
 //
 // The channels of a group of 8 are stored in the order 0 4 1 5 2 6 3 7, as a code word
 // expands: in Q and K alike, where their order does not matter, and in O's columns, which
@@ -41,10 +43,8 @@ __constant__ int c_kv_stall = 0;
 namespace {
 
 constexpr float kNone = -3.0e38f;  // a maximum over nothing
-constexpr float kSlack = 8.f;      // octaves by which a logit may exceed the reference
 constexpr float kShift = 7.f;      // P is 2^kShift times the softmax's numerator
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 512;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t count) {
@@ -67,8 +67,8 @@ __device__ __forceinline__ unsigned long long global_ns() {
 }
 
 struct Bars {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_ready[2], o_done[2], q_full, drain;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[4], p_ready[4], o_done[2], q_full, drain;
   uint32_t tmem_base;
   volatile int abort_flag, bad_v;  // a wait ran out; V has values beyond fp16
 };
@@ -103,16 +103,11 @@ __device__ __forceinline__ bool wait_one(uint64_t *b, uint32_t parity, Bars *bar
 }
 
 // Operands of 128-byte rows, the 16-byte pieces of row r exchanged by XOR with r mod 8,
-// 8-row groups 1024 bytes apart: rows along M or N, contraction along the row
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
-// or rows along the contraction, 64 columns of N per row, 64-column boxes `box` bytes apart
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t box) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(box >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
+// 8-row groups 1024 bytes apart: the low word of a descriptor, with rows along M or N and the contraction
+// along the row, or with rows along the contraction and 64-column boxes `box` bytes apart
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t box) { return ((saddr >> 4) & 0x3FFFu) | (box >> 4) << 16; }
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;  // stride of the 8-row groups, version, 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
 // fp16 x fp16 -> fp32; bit 16: B with its rows along the contraction
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
@@ -123,16 +118,18 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(kDescHigh), "r"((uint32_t)acc)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(kDescHigh), "r"((uint32_t)acc)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
@@ -140,7 +137,16 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// waits for the loads of this warp, v's 32 values the last of them
+__device__ __forceinline__ void wait_ld32(float *v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]),
+                 "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of this warp's 32 lanes, a lane per thread
@@ -162,6 +168,23 @@ __device__ __forceinline__ void tm_st32(uint32_t t, const uint32_t *v) {
       "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
       "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
       "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t), "r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+      "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld16(uint32_t t, uint32_t *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(t)
       : "memory");
 }
 
@@ -196,6 +219,12 @@ __device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_
 __device__ __forceinline__ bool beyond_fp16(uint32_t meta) {
   return !(fmaf(8.f, fabsf(__uint_as_float(meta << 16)), fabsf(__uint_as_float(meta & 0xFFFF0000u))) <= 65504.f);
 }
+// scale and bias of a metadata word as fp16, twice each
+__device__ __forceinline__ void split_meta(uint32_t meta, __half2 &s, __half2 &o) {
+  const uint32_t h = half2_bits(__uint_as_float(meta << 16), __uint_as_float(meta & 0xFFFF0000u));
+  s = half2_of(__byte_perm(h, h, 0x1010));
+  o = half2_of(__byte_perm(h, h, 0x3232));
+}
 template <int N>
 __device__ __forceinline__ void ldg_words(const unsigned char *p, uint32_t (&w)[N]) {
   if constexpr (N == 1) {
@@ -216,15 +245,28 @@ template <int D, int GS>
 struct Prefill {
   static constexpr int G = D / GS, kBlock = 16 * (D + 8 * G);
   static constexpr int QT = D <= 128 ? 2 : 1, kRows = 128 * QT;  // row tiles of a CTA
-  static constexpr int BN = D <= 128 ? 128 : 64;                 // cached tokens of a tile
-  static constexpr int kQTile = (D / 64) * 128 * 128, kBox = BN * 128, kStage = (D / 64) * kBox;
-  static constexpr int kHeader = 1024;
-  static constexpr int kQ = kHeader, kK = kQ + QT * kQTile, kV = kK + 2 * kStage, kX = kV + 2 * kStage;
-  // kX: the extra k16 step, 32 bytes of each row: K's stages 0 and 1, then Q's tiles
+  static constexpr int BN = D == 64 ? 128 : 64;                  // cached tokens of a tile
+  static constexpr int NB = D == 128 ? 4 : 2;                    // buffers of S
+  static constexpr bool kQTmem = D == 256;                       // Q as the MMA's operand in tensor memory
+  static constexpr int kQTile = kQTmem ? 0 : (D / 64) * 128 * 128, kBox = BN * 128, kStage = (D / 64) * kBox;
+  static constexpr int NST = D == 64 ? 2 : D == 128 ? 4 : 3;     // stages of K, and of V
+  static constexpr int kHeader = 2048;  // barriers, and from byte 1024 on the rows' factors
+  static constexpr int kQ = kHeader, kK = kQ + QT * kQTile, kV = kK + NST * kStage, kX = kV + NST * kStage;
+  // kX: the extra k16 step, 32 bytes of each of 128 rows: K's stages in the first two columns, Q's tiles in the others
   static constexpr int kSmem = kX + 128 * 128 + 1024;
-  static constexpr int kMajorWarps = QT == 2 ? 8 : 4;            // of the softmax
-  // registers per thread after the split: softmax, expansion, MMAs (heads of 256 keep 128 each)
-  static constexpr int kRegS = 192, kRegD = 88, kRegM = 40;
+  static_assert(kSmem <= 227 * 1024 && NST * BN <= 256, "shared memory");
+  // 16-byte pieces and rows of a stage's extra columns
+  static constexpr int x_piece(int stage) { return BN == 128 ? 2 * stage : stage & 2; }
+  static constexpr int x_row(int stage) { return BN == 128 ? 0 : 64 * (stage & 1); }
+  static constexpr int kFirstK = 4 * QT, kFirstV = kFirstK + 4, kMma = kFirstV + 4;  // the roles' first warps
+  static constexpr int kThreads = 32 * (kMma + 4);
+  // registers per thread: what a block of kThreads gets, and after the split the
+  // softmax's, the expansions' and the MMAs' (they add up to the first one's)
+  static constexpr int kRegs = QT == 2 ? 96 : 128;
+  static constexpr int kRegS = QT == 2 ? 128 : 128, kRegX = QT == 2 ? 80 : 128, kRegM = QT == 2 ? 64 : 128;
+  static_assert(QT * kRegS + 2 * kRegX + kRegM <= (QT + 3) * kRegs, "registers");
+  // tensor memory: S (and P) in NB times kS columns, O in 256 + D q; Q of heads of 256 in 128
+  static constexpr int kS = BN;
 };
 static_assert(sizeof(Bars) <= 1024, "header");
 
@@ -252,131 +294,6 @@ struct Rows {
   }
 };
 
-// K and V of a tile for one warp of the four that expand it: BN / 64 blocks of 16 tokens.
-template <int D, int GS>
-struct Expander {
-  using C = Prefill<D, GS>;
-  static constexpr int G = C::G, W = C::BN / 64, KW = D / 32, VM = D / 64;
-  struct KRegs {
-    uint32_t code[W][2][KW], meta[W][2][G];
-    int page[W];
-  };
-  struct VRegs {
-    uint4 code[W][VM];
-    uint32_t meta[W][4][G];
-    int page[W];
-  };
-  const KvView &c;
-  int64_t b;
-  int hk, warp, lane;
-  __device__ __forceinline__ int pos(int n0, int i) const { return n0 + 16 * (W * warp + i); }
-  __device__ __forceinline__ int page_of(int n0, int i) const { return c.page(b, pos(n0, i)); }
-  __device__ __forceinline__ const unsigned char *block(int page, int p) const {
-    const int per = 1 << (c.page_shift - 4);
-    return c.data + (((int64_t)page * c.HK + hk) * per + ((p >> 4) & (per - 1))) * C::kBlock;
-  }
-  // token of a half block whose 8 lanes of a quarter warp fall into different banks
-  __device__ __forceinline__ int k_token(int half) const { return 8 * half + (lane >> 3) + (lane & 4); }
-  __device__ __forceinline__ void fetch_k(int n0, const int (&page)[W], KRegs &r) const {
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      r.page[i] = page[i];
-      if (page[i] < 0) continue;
-      const unsigned char *p = block(page[i], pos(n0, i));
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = k_token(h);
-        if constexpr (D == 64) {
-          ldg_words(p + t * 32 + 8 * (lane & 3), r.code[i][h]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < D / 128; ++k) {
-            uint32_t w[4];
-            ldg_words(p + t * (D / 2) + 64 * k + 16 * (lane & 3), w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r.code[i][h][4 * k + j] = w[j];
-          }
-        }
-        ldg_words(p + 8 * D + t * G * 4, r.meta[i][h]);
-      }
-    }
-  }
-  // scale q into the tile at `dst`, the biases (twice) into the extra columns
-  __device__ __forceinline__ void put_k(const KRegs &r, uint32_t dst, uint32_t extra, int stage) const {
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * (W * warp + i) + k_token(h);
-        const bool have = r.page[i] >= 0;
-        __half2 s[G];
-        uint32_t bias[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < G; ++k) {
-          const uint32_t m = have ? r.meta[i][h][k] : 0u;
-          s[k] = __float2half2_rn(__uint_as_float(m << 16));
-          bias[k] = bits(__float2half2_rn(__uint_as_float(m & 0xFFFF0000u)));
-        }
-#pragma unroll
-        for (int j = 0; j < KW; ++j) {
-          __half2 v[4];
-          expand(r.code[i][h][j], v);
-          const __half2 f = s[32 * j / GS];
-          sts4(dst + (j >> 1) * C::kBox + swz(row, 4 * (j & 1) + (lane & 3)), bits(__hmul2(v[0], f)), bits(__hmul2(v[1], f)),
-               bits(__hmul2(v[2], f)), bits(__hmul2(v[3], f)));
-        }
-        if ((lane & 3) == 0) sts4(extra + swz(row, 2 * stage), bias[0], bias[1], bias[2], bias[3]);
-        if ((lane & 3) == 1) sts4(extra + swz(row, 2 * stage + 1), have ? 0u : 0x0000FC00u, 0u, 0u, 0u);  // -inf
-      }
-  }
-  __device__ __forceinline__ void fetch_v(int n0, const int (&page)[W], VRegs &r) const {
-    const int w = lane & 7, t = lane >> 3;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      r.page[i] = page[i];
-      if (page[i] < 0) continue;
-      const unsigned char *p = block(page[i], pos(n0, i)) + 8 * D + 64 * G;
-#pragma unroll
-      for (int m = 0; m < VM; ++m) r.code[i][m] = __ldg(reinterpret_cast<const uint4 *>(p + (8 * m + w) * 64 + 16 * t));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) ldg_words(p + 8 * D + (2 * t + (k & 1) + 8 * (k >> 1)) * G * 4, r.meta[i][k]);
-    }
-  }
-  // scale q + bias; tokens with values beyond fp16 become 0, which no P of 0 turns into NaN, and are reported if they are
-  // among the first `left` of the tile, the sequence's own
-  __device__ __forceinline__ bool put_v(const VRegs &r, uint32_t dst, int left) const {
-    const int w = lane & 7, t = lane >> 3;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int row = 16 * (W * warp + i) + 2 * t + (k & 1) + 8 * (k >> 1);
-        bool here = false;
-#pragma unroll
-        for (int n = 0; n < G; ++n) here |= beyond_fp16(r.meta[i][k][n]);
-        const bool use = r.page[i] >= 0 && !here;
-        bad |= here && r.page[i] >= 0 && row < left;
-        __half2 s[G], o[G];
-#pragma unroll
-        for (int n = 0; n < G; ++n) {
-          const uint32_t m = use ? r.meta[i][k][n] : 0u;
-          s[n] = __float2half2_rn(__uint_as_float(m << 16));
-          o[n] = __float2half2_rn(__uint_as_float(m & 0xFFFF0000u));
-        }
-#pragma unroll
-        for (int m = 0; m < VM; ++m) {
-          __half2 v[4];
-          expand(k == 0 ? r.code[i][m].x : k == 1 ? r.code[i][m].y : k == 2 ? r.code[i][m].z : r.code[i][m].w, v);
-          const int n = 64 * m / GS;
-          sts4(dst + m * C::kBox + swz(row, w), bits(__hfma2(v[0], s[n], o[n])), bits(__hfma2(v[1], s[n], o[n])),
-               bits(__hfma2(v[2], s[n], o[n])), bits(__hfma2(v[3], s[n], o[n])));
-        }
-      }
-    return bad;
-  }
-};
-
 // shared-memory stores of this warp, to the MMAs
 __device__ __forceinline__ void publish_smem(uint64_t *bar, int lane) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -384,8 +301,301 @@ __device__ __forceinline__ void publish_smem(uint64_t *bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+// One warp's share of the expansion of K or V: of every tile, W blocks of 16 tokens, numbered m = 0, 1, ... through all
+// tiles.
+template <int D, int GS>
+struct Expander {
+  using C = Prefill<D, GS>;
+  static constexpr int G = C::G, W = C::BN / 64, KW = D / 32, VM = D / 64;
+  const KvView &c;
+  int64_t b;
+  int hk, warp, lane, first, blocks;
+  __device__ __forceinline__ int pos(int m) const { return first + m / W * C::BN + 16 * (W * warp + m % W); }
+  __device__ __forceinline__ int page_of(int m) const { return m < blocks ? c.page(b, pos(m)) : -1; }
+  __device__ __forceinline__ const unsigned char *block(int page, int m) const {
+    const int per = 1 << (c.page_shift - 4);
+    return c.data + (((int64_t)page * c.HK + hk) * per + ((pos(m) >> 4) & (per - 1))) * C::kBlock;
+  }
+
+  // ---- K: half a block at a time, a token for four lanes: lane t mod 4 has channels 32 j + 8 t .. + 7 of token
+  // lane / 8 + (lane & 4), so that 8 lanes store to 8 different banks
+  struct KHalf {
+    uint32_t code[KW], meta[G];
+    bool have;
+  };
+  __device__ __forceinline__ int token() const { return (lane >> 3) + (lane & 4); }
+  __device__ __forceinline__ void fetch_k(const unsigned char *p, bool have, int half, KHalf &r) const {
+    r.have = have;
+    if (!have) return;
+    const int t = token() + 8 * half;
+    if constexpr (D == 64) {
+      ldg_words(p + t * 32 + 8 * (lane & 3), r.code);
+    } else {
+#pragma unroll
+      for (int k = 0; k < D / 128; ++k) {
+        uint32_t w[4];
+        ldg_words(p + t * (D / 2) + 64 * k + 16 * (lane & 3), w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.code[4 * k + j] = w[j];
+      }
+    }
+    ldg_words(p + 8 * D + t * G * 4, r.meta);
+  }
+  // scale q into the tile at `dst`, the biases (twice) into the extra columns; both addresses are this lane's, of the
+  // first half block's row
+  __device__ __forceinline__ void put_k(const KHalf &r, int half, uint32_t dst, uint32_t extra) const {
+    __half2 s[G], o[G];
+    uint32_t e[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      split_meta(r.have ? r.meta[k] : 0u, s[k], o[k]);
+      e[k] = bits(o[k]);
+    }
+#pragma unroll
+    for (int j = 0; j < KW; ++j) {
+      __half2 v[4];
+      expand(r.code[j], v);
+      const __half2 f = s[32 * j / GS];
+      sts4((j & 1 ? dst ^ 64 : dst) + (j >> 1) * C::kBox + half * 1024, bits(__hmul2(v[0], f)), bits(__hmul2(v[1], f)),
+           bits(__hmul2(v[2], f)), bits(__hmul2(v[3], f)));
+    }
+    // lane 0 of a token the biases, lane 1 the 17th column: -inf for a token without a page
+    if (lane & 1) {
+      e[0] = r.have ? 0u : 0x0000FC00u;
+      e[1] = e[2] = e[3] = 0u;
+    }
+    if ((lane & 2) == 0) sts4(extra + half * 1024, e[0], e[1], e[2], e[3]);
+  }
+  __device__ __forceinline__ void run_k(Bars *bars, uint32_t sm) const {
+    KHalf r0, r1;
+    int page = page_of(0), ahead = page_of(1);
+    const unsigned char *p = block(max(page, 0), 0);
+    fetch_k(p, page >= 0, 0, r0);
+    fetch_k(p, page >= 0, 1, r1);
+    const uint32_t to = sm + C::kK + swz(16 * W * warp + token(), lane & 3);
+    uint32_t s = 0, ph = 1;
+#pragma unroll 1
+    for (int m = 0; m < blocks; ++m) {
+      if (m % W == 0 && !wait_warp(&bars->k_empty[s], ph, bars)) break;
+      const uint32_t dst = to + s * C::kStage + (m % W) * 2048,
+                     extra = sm + C::kX + swz(C::x_row(s) + 16 * (W * warp + m % W) + token(), C::x_piece(s) + (lane & 1));
+      page = ahead;
+      ahead = page_of(m + 2);
+      p = block(max(page, 0), m + 1);
+      put_k(r0, 0, dst, extra);
+      fetch_k(p, page >= 0, 0, r0);
+      put_k(r1, 1, dst, extra);
+      fetch_k(p, page >= 0, 1, r1);
+      if (m % W == W - 1) {
+        publish_smem(&bars->k_full[s], lane);
+        if (++s == C::NST) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+  }
+
+  // ---- V: 64 channels of a block for a half warp, parts numbered through all tiles (NP per tile).  Lane l mod 16 has
+  // words 2 (l mod 4) and the next, tokens 2t, 2t + 1, 2t + 8, 2t + 9 with t = l / 4; where t is odd the words change
+  // places, again for the banks.
+  static constexpr int NP = W * VM / 2;
+  struct VPart {
+    uint4 code[2];
+    uint32_t meta[4];
+    bool have;
+  };
+  __device__ __forceinline__ int v_time() const { return (lane >> 2) & 3; }
+  __device__ __forceinline__ int v_piece(int w) const { return 2 * (lane & 3) + (w ^ ((lane >> 2) & 1)); }
+  __device__ __forceinline__ int v_item(int v) const { return 2 * (v % NP) + (lane >> 4); }  // 64 channels v_item % VM of block v_item / VM
+  __device__ __forceinline__ int v_block(int v) const { return v / NP * W + v_item(v) / VM; }
+  __device__ __forceinline__ void fetch_v(int v, int page, VPart &r) const {
+    r.have = page >= 0;
+    if (!r.have) return;
+    const int g = v_item(v) % VM, t = v_time();
+    const unsigned char *p = block(page, v_block(v)) + 8 * D + 64 * G;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) r.code[w] = __ldg(reinterpret_cast<const uint4 *>(p + (8 * g + v_piece(w)) * 64 + 16 * t));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      r.meta[j] = __ldg(reinterpret_cast<const uint32_t *>(p + 8 * D) + (2 * t + (j & 1) + 8 * (j >> 1)) * G + 64 * g / GS);
+  }
+  // scale q + bias; tokens with values beyond fp16 become 0, which no P of 0 turns into NaN, and are reported if they are
+  // among the first `left` of the tile, the sequence's own
+  __device__ __forceinline__ bool put_v(int v, const VPart &r, uint32_t dst, int left) const {
+    const int row0 = 16 * (W * warp + v_item(v) / VM) + 2 * v_time();
+    dst += v_item(v) % VM * C::kBox;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = row0 + (j & 1) + 8 * (j >> 1);
+      const bool out = beyond_fp16(r.meta[j]);
+      bad |= r.have && out && row < left;
+      __half2 s, o;
+      split_meta(r.have && !out ? r.meta[j] : 0u, s, o);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint4 &u = r.code[w];
+        __half2 h[4];
+        expand(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, h);
+        sts4(dst + swz(row, v_piece(w)), bits(__hfma2(h[0], s, o)), bits(__hfma2(h[1], s, o)), bits(__hfma2(h[2], s, o)),
+             bits(__hfma2(h[3], s, o)));
+      }
+    }
+    return bad;
+  }
+  __device__ __forceinline__ void run_v(Bars *bars, uint32_t sm, int len) const {
+    VPart r0, r1;
+    const int parts = blocks / W * NP;
+    auto page_of_part = [&](int v) { return v < parts ? page_of(v_block(v)) : -1; };
+    fetch_v(0, page_of_part(0), r0);
+    fetch_v(1, page_of_part(1), r1);
+    int ahead = page_of_part(2);
+    uint32_t s = 0, ph = 1;
+    auto step = [&](int v, VPart &r) {
+      const int i = v / NP;
+      if (v % NP == 0 && !wait_warp(&bars->v_empty[s], ph, bars)) return false;
+      const int page = ahead;
+      ahead = page_of_part(v + 3);
+      if (put_v(v, r, sm + C::kV + s * C::kStage, len - first - i * C::BN)) bars->bad_v = 1;
+      fetch_v(v + 2, page, r);
+      if (v % NP == NP - 1) {
+        publish_smem(&bars->v_full[s], lane);
+        if (++s == C::NST) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      return true;
+    };
+#pragma unroll 1
+    for (int v = 0; v < parts; v += 2)
+      if (!step(v, r0) || (v + 1 < parts && !step(v + 1, r1))) break;
+  }
+};
+
+// The power of two that brings a row's largest value into [2^7, 2^8), as the factor of Q (a negative scale goes with
+// it), and what S is multiplied with to give logits in octaves.
+__device__ __forceinline__ float2 q_factors(float big, float scale) {
+  const int be = (int)(__float_as_uint(big) >> 23);
+  const int e = be == 0 || be == 255 ? 0 : min(max(7 - (be - 127), -100), 100);
+  return make_float2(scale < 0.f ? -pow2f(e) : pow2f(e), fmaxf(fabsf(scale) * kLog2e * pow2f(-e), 1e-30f));
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const uint4 &v, float (&x)[8]) {
+  constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = meta_f32(w[k], bf);
+    x[2 * k + 1] = meta_f32(w[k] >> 16, bf);
+  }
+}
+// the high and low fp16 half of x
+__device__ __forceinline__ uint32_t high_low(float x) { return half2_bits(x, x - __half2float(__float2half_rn(x))); }
+
+// A warp's 32 rows of Q (from row `first` of the sequence, `at` of the row tile q), scaled, to where the MMAs read them,
+// with the extra columns; returns the factor of this lane's row.
 template <typename T, int D, int GS>
-__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvView c, const KvAttention a, int tiles) {
+__device__ __forceinline__ float load_q(const KvAttention &a, const Rows &rows, uint32_t sm, uint32_t tl, int first, int hk, int r, int q,
+                                        int at, int lane) {
+  using C = Prefill<D, GS>;
+  constexpr int G = C::G;
+  auto row_of = [&](int i) {
+    const int row = min(first + i, rows.rows - 1);  // rows past the last repeat it
+    return static_cast<const T *>(a.q) + (rows.t0 + row / r) * a.q_stride + (int64_t)(hk * r + row % r) * D;
+  };
+  if constexpr (C::kQTmem) {
+    // a row per lane, in two passes of 64 channels at a time
+    const T *src = row_of(lane);
+    float big = 0.f, sum[G] = {};
+#pragma unroll 1
+    for (int k = 0; k < D / 64; ++k) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(src) + 8 * k + i);
+      float all = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x[8];
+        widen8<T>(v[i], x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          big = fmaxf(big, fabsf(x[j]));
+          all += x[j];
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) sum[g] += g == 64 * k / GS ? all : 0.f;
+    }
+    const float2 f = q_factors(big, a.scale);
+#pragma unroll 1
+    for (int k = 0; k < D / 64; ++k) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(src) + 8 * k + i);
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x[8];
+        widen8<T>(v[i], x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[4 * i + j] = half2_bits(f.x * x[j], f.x * x[j + 4]);
+      }
+      tm_st32(tl + 128 + 32 * k, w);
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int g = 0; g < G; ++g) w[g] = high_low(f.x * sum[g]);
+    sts4(sm + C::kX + swz(at + lane, 4 + 2 * q), w[0], w[1], w[2], w[3]);
+    sts4(sm + C::kX + swz(at + lane, 5 + 2 * q), 0x00003C00u, 0u, 0u, 0u);  // 1, against what is -inf for a missing token
+    return f.y;
+  } else {
+    // whole rows by neighbouring lanes, 16 bytes each
+    constexpr int kPieces = D / 8, kRowsAtOnce = 32 / kPieces;
+    const int piece = lane % kPieces;
+    const uint32_t dst = sm + C::kQ + q * C::kQTile + (piece >> 3) * (128 * 128), fac = sm + 1024 + (128 * q + at) * 4;
+#pragma unroll 1
+    for (int n0 = 0; n0 < kPieces; n0 += 4) {
+    uint4 v[4];  // loads before the first store
+#pragma unroll
+    for (int n = 0; n < 4; ++n) v[n] = __ldg(reinterpret_cast<const uint4 *>(row_of((n0 + n) * kRowsAtOnce + lane / kPieces)) + piece);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int i = (n0 + n) * kRowsAtOnce + lane / kPieces;
+      float x[8];
+      widen8<T>(v[n], x);
+      float big = 0.f, sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        big = fmaxf(big, fabsf(x[j]));
+        sum += x[j];
+      }
+#pragma unroll
+      for (int o = 1; o < kPieces; o <<= 1) {
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        if (o < GS / 8) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      }
+      const float2 f = q_factors(big, a.scale);
+      sts4(dst + swz(at + i, piece & 7), half2_bits(f.x * x[0], f.x * x[4]), half2_bits(f.x * x[1], f.x * x[5]),
+           half2_bits(f.x * x[2], f.x * x[6]), half2_bits(f.x * x[3], f.x * x[7]));
+      auto sts1 = [](uint32_t to, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(v) : "memory"); };
+      const uint32_t extra = sm + C::kX + swz(at + i, 4 + 2 * q), one = sm + C::kX + swz(at + i, 5 + 2 * q);
+      if (piece % (GS / 8) == 0) sts1(extra + 4 * (piece / (GS / 8)), high_low(f.x * sum));
+      if (piece > 0 && piece < 4 && piece >= G) sts1(extra + 4 * piece, 0u);
+      if (piece >= 4 && piece < 8) sts1(one + 4 * (piece - 4), piece == 4 ? 0x00003C00u : 0u);  // 1, against what is -inf for a missing token
+      if (piece == 0) sts1(fac + 4 * i, __float_as_uint(f.y));
+    }
+    }
+    __syncwarp();
+    uint32_t f;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(f) : "r"(fac + 4 * lane) : "memory");
+    return __uint_as_float(f);
+  }
+}
+
+template <typename T, int D, int GS>
+__global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kernel(const KvView c, const KvAttention a, int tiles) {
   using C = Prefill<D, GS>;
   using X = Expander<D, GS>;
   constexpr int G = C::G, QT = C::QT, BN = C::BN;
@@ -409,16 +619,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvView c,
       if (again)
         for (uint64_t *bar = bars->k_full; bar <= &bars->drain; ++bar)
           asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < 4; ++s) {
         mbar_init(&bars->k_full[s], 4);
         mbar_init(&bars->v_full[s], 4);
         mbar_init(&bars->k_empty[s], 1);
         mbar_init(&bars->v_empty[s], 1);
         mbar_init(&bars->s_full[s], 1);
         mbar_init(&bars->p_ready[s], 4);
-        mbar_init(&bars->o_done[s], 1);
       }
-      mbar_init(&bars->q_full, C::kMajorWarps);
+      mbar_init(&bars->o_done[0], 1);
+      mbar_init(&bars->o_done[1], 1);
+      mbar_init(&bars->q_full, 4 * QT);
       mbar_init(&bars->drain, 1);
       bars->bad_v = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -426,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvView c,
   };
   if (tid == 0) bars->abort_flag = 0;
   init(false);
-  if (warp == 12) {
+  if (warp == C::kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -449,9 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvView c,
     return true;
   };
 
-  if (warp < C::kMajorWarps) {
+  if (warp < C::kFirstK) {
     // ---------------- softmax: a row per thread
-    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegS));
+    if constexpr (C::kRegS > C::kRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegS));
     const int q = warp >> 2, quarter = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16), to = tl + 256 + D * q;
     int tile = tile0;
@@ -461,120 +672,114 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvView c,
       const int head = hk * r + row % r, pos = rows.pos0 + row / r;
       const int hi = pos < 0 ? -1 : a.causal ? pos : rows.len - 1, lo = a.window ? max(pos, 0) - a.window : -1;  // lo < j <= hi is seen
       const int hi_all = __reduce_min_sync(0xffffffffu, hi), lo_all = __reduce_max_sync(0xffffffffu, lo);
-      float f;
-      {
-        const T *src = static_cast<const T *>(a.q) + tok * a.q_stride + (int64_t)head * D;
-        float big = 0.f, sum[G] = {};
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll 4
-          for (int i = g * GS / 8; i < (g + 1) * GS / 8; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x = meta_f32(w[k], std::is_same<T, __nv_bfloat16>::value), y = meta_f32(w[k] >> 16, std::is_same<T, __nv_bfloat16>::value);
-              big = fmaxf(big, fmaxf(fabsf(x), fabsf(y)));
-              sum[g] += x + y;
-            }
-          }
-        // the power of two that brings the largest into [2^7, 2^8)
-        const int be = (int)(__float_as_uint(big) >> 23);
-        const int e = be == 0 || be == 255 ? 0 : min(max(7 - (be - 127), -100), 100);
-        const float up = a.scale < 0.f ? -pow2f(e) : pow2f(e);
-        f = fmaxf(fabsf(a.scale) * kLog2e * pow2f(-e), 1e-30f);
-        const uint32_t dst = sm + C::kQ + q * C::kQTile;
-        const int rr = 32 * quarter + lane;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[2 * k] = up * meta_f32(w[k], std::is_same<T, __nv_bfloat16>::value);
-            x[2 * k + 1] = up * meta_f32(w[k] >> 16, std::is_same<T, __nv_bfloat16>::value);
-          }
-          sts4(dst + (i >> 3) * (128 * 128) + swz(rr, i & 7), half2_bits(x[0], x[4]), half2_bits(x[1], x[5]), half2_bits(x[2], x[6]),
-               half2_bits(x[3], x[7]));
-        }
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const float x = up * sum[g];
-          w[g] = half2_bits(x, x - __half2float(__float2half_rn(x)));
-        }
-        sts4(sm + C::kX + swz(rr, 4 + 2 * q), w[0], w[1], w[2], w[3]);
-        sts4(sm + C::kX + swz(rr, 5 + 2 * q), 0x00003C00u, 0u, 0u, 0u);  // 1, against what is -inf for a missing token
-        publish_smem(&bars->q_full, lane);
+      const float f = load_q<T, D, GS>(a, rows, sm, tl, tile * C::kRows + 128 * q + 32 * quarter, hk, r, q, 32 * quarter, lane);
+      if constexpr (C::kQTmem) {
+        wait_st();
+        fence_before();
       }
+      publish_smem(&bars->q_full, lane);
       float M = kNone, L = 0.f;
       bool ok = true;
       for (int i = 0; i < rows.tiles; ++i) {
-        const int buf = QT == 2 ? q : i & 1;
-        const uint32_t ph = QT == 2 ? i & 1 : (i >> 1) & 1, ts = tl + 128 * buf;
+        const int buf = (QT * i + q) % C::NB;
+        const uint32_t ph = (QT * i + q) / C::NB & 1, ts = tl + C::kS * buf;
         if (!(ok = wait_warp(&bars->s_full[buf], ph, bars))) break;
         fence_after();
-        float x[BN];
+        const int n0 = rows.first + i * BN, h = hi - n0, l = lo - n0;
+        const bool masked = n0 <= lo_all || n0 + BN - 1 > hi_all;
+        auto mask = [&](float(&x)[32], int k) {
 #pragma unroll
-        for (int k = 0; k < BN; k += 32) tm_ld32(ts + k, x + k);
-        wait_ld();
-        const int n0 = rows.first + i * BN;
-        if (n0 <= lo_all || n0 + BN - 1 > hi_all) {
-          const int h = hi - n0, l = lo - n0;
+          for (int j = 0; j < 32; ++j) x[j] = k + j > l && k + j <= h ? x[j] : -INFINITY;
+        };
+        float sum = 0.f;
+        // P of 32 columns, into the 16 that its part of S leaves free
+        auto piece = [&](float(&x)[32], int k) {
+          if (masked) mask(x, k);
+          uint32_t w[16];
+          float s4[4];
+          auto numerators = [&] {
+            const float neg = kShift - M;
+            s4[0] = s4[1] = s4[2] = s4[3] = 0.f;
 #pragma unroll
-          for (int k = 0; k < BN; ++k) x[k] = k > l && k <= h ? x[k] : -INFINITY;
-        }
-        float m4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int k = 4; k < BN; k += 8)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) m4[j] = k + 4 + j < BN ? max3(m4[j], x[k + j], x[k + 4 + j]) : fmaxf(m4[j], x[k + j]);
-        const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * f;
-        const bool grow = top > M + kSlack;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float down = grow ? ex2(M - top) : 1.f;
-          M = grow ? top : M;
-          L *= down;
-          if (i > 0) {
-            // O's product of the tile before (the one before that is complete, for S followed it); the next waits for P
-            if (!(ok = wait_warp(&bars->o_done[q], (i - 1) & 1, bars))) break;
-            fence_after();
-#pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-              float o[32];
-              tm_ld32(to + k, o);
-              wait_ld();
-              uint32_t w[32];
-#pragma unroll
-              for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] * down);
-              tm_st32(to + k, w);
+            for (int j = 0; j < 16; ++j) {
+              const float u = ex2(fmaf(x[2 * j], f, neg)), v = ex2(fmaf(x[2 * j + 1], f, neg));
+              s4[(2 * j) & 3] += u;
+              s4[(2 * j + 1) & 3] += v;
+              w[j] = half2_bits(u, v);
             }
-          }
-        }
-        const float neg = kShift - M;
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+            s4[0] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          };
+          numerators();
+          // What sums to no more than fp16's largest value has no part beyond it.  Else (on the first piece, and seldom
+          // again) the reference moves to the largest logit that is left in the tile, in whole octaves, so that what
+          // is there already, O, L and P, is scaled exactly.
+          if (__any_sync(0xffffffffu, !(s4[0] <= 65504.f))) {
+            float top = kNone;
+#pragma unroll 1
+            for (int n = k; n < BN; n += 32) {
+              float y[32];
+              tm_ld32(ts + n, y);
+              wait_ld32(y);
+              if (masked) mask(y, n);
 #pragma unroll
+              for (int j = 0; j < 32; j += 2) top = max3(top, y[j], y[j + 1]);
+            }
+            const float next = top > kNone ? fmaxf(M, ceilf(top * f)) : M, move = M - next;
+            const float down = move >= 0.f ? 1.f : move > -126.f ? pow2f((int)move) : 0.f;
+            M = next;
+            L *= down;
+            sum *= down;
+            const __half2 d2 = __float2half2_rn(down);
+#pragma unroll 1
+            for (int n = 0; n < k; n += 32) {
+              uint32_t y[16];
+              tm_ld16(ts + n / 2, y);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = bits(__hmul2(half2_of(y[j]), d2));
+              tm_st16(ts + n / 2, y);
+            }
+            if (i > 0) {
+              // O's product of the tile before (the one before that is complete, for S followed it or one later); the next
+              // waits for P
+              ok = wait_warp(&bars->o_done[q], (i - 1) & 1, bars) && ok;
+              fence_after();
+#pragma unroll 1
+              for (int n = 0; n < D; n += 32) {
+                float o[32];
+                tm_ld32(to + n, o);
+                wait_ld32(o);
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(o[j] * down);
+                tm_st32(to + n, v);
+              }
+            }
+            numerators();
+          }
+          sum += s4[0];
+          tm_st16(ts + k / 2, w);
+        };
+        float x[2][32];
+        tm_ld32(ts, x[0]);
+#pragma unroll 1
         for (int k = 0; k < BN; k += 64) {
-          uint32_t w[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float u = ex2(fmaf(x[k + 2 * j], f, neg)), v = ex2(fmaf(x[k + 2 * j + 1], f, neg));
-            s4[j & 1] += u;
-            s4[2 + (j & 1)] += v;
-            w[j] = half2_bits(u, v);
-          }
-          tm_st32(ts + k / 2, w);
+          wait_ld32(x[0]);
+          tm_ld32(ts + k + 32, x[1]);
+          piece(x[0], k);
+          wait_ld32(x[1]);
+          if (k + 64 < BN) tm_ld32(ts + k + 64, x[0]);
+          piece(x[1], k + 32);
         }
-        L += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        if (!ok) break;
+        L += sum;
         wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_ready[buf]);
       }
-      // O's last product.  With one row tile the last two may be open (S of a tile only says that the product two tiles
-      // before is complete), and o_done's parity cannot tell them apart: all MMAs, then.
-      if (ok && rows.tiles > 0) ok = QT == 2 ? wait_warp(&bars->o_done[q], (rows.tiles - 1) & 1, bars) : wait_warp(&bars->drain, 0, bars);
+      // O's last product.  With two buffers of S per row tile the last two may be open (S of a tile only says that the
+      // product two tiles before is complete), and o_done's parity cannot tell them apart: all MMAs, then.
+      if (ok && rows.tiles > 0) ok = C::NB == QT ? wait_warp(&bars->o_done[q], (rows.tiles - 1) & 1, bars) : wait_warp(&bars->drain, 0, bars);
       fence_after();
       float inv = L == 0.f ? 0.f : 1.f / L;
       if (ok && bars->bad_v) {
@@ -588,114 +793,123 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvView c,
         }
       }
       __syncwarp();
-      const bool write = ok && mine < rows.rows;
-      T *dst = static_cast<T *>(a.o) + tok * a.o_stride + (int64_t)head * D;
+      // rows of o through shared memory (Q's tile; K's stages for heads of 256: no MMA reads them any more), so that a
+      // warp stores whole rows
+      const uint32_t stage = sm + (C::kQTmem ? C::kK : C::kQ + q * C::kQTile) + quarter * (32 * D * 2);
+      constexpr int kPieces = D / 8;
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
         float o[32];
         if (rows.tiles > 0) {
           tm_ld32(to + k, o);
-          wait_ld();
+          wait_ld32(o);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = inv == 0.f ? 0.f : o[j] * inv;
-        if (write) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            // columns hold channels 0 4 1 5 2 6 3 7
-            uint32_t w[4];
-            if constexpr (std::is_same<T, __half>::value) {
-              w[0] = half2_bits(o[j], o[j + 2]), w[1] = half2_bits(o[j + 4], o[j + 6]);
-              w[2] = half2_bits(o[j + 1], o[j + 3]), w[3] = half2_bits(o[j + 5], o[j + 7]);
-            } else {
-              const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(o[j], o[j + 2]), __floats2bfloat162_rn(o[j + 4], o[j + 6]),
-                                           __floats2bfloat162_rn(o[j + 1], o[j + 3]), __floats2bfloat162_rn(o[j + 5], o[j + 7])};
+        for (int j = 0; j < 32; j += 8) {
+          // columns hold channels 0 4 1 5 2 6 3 7
+          uint32_t w[4];
+          if constexpr (std::is_same<T, __half>::value) {
+            w[0] = half2_bits(o[j], o[j + 2]), w[1] = half2_bits(o[j + 4], o[j + 6]);
+            w[2] = half2_bits(o[j + 1], o[j + 3]), w[3] = half2_bits(o[j + 5], o[j + 7]);
+          } else {
+            const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(o[j], o[j + 2]), __floats2bfloat162_rn(o[j + 4], o[j + 6]),
+                                         __floats2bfloat162_rn(o[j + 1], o[j + 3]), __floats2bfloat162_rn(o[j + 5], o[j + 7])};
 #pragma unroll
-              for (int n = 0; n < 4; ++n) w[n] = *reinterpret_cast<const uint32_t *>(&h[n]);
-            }
-            *reinterpret_cast<uint4 *>(dst + k + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int n = 0; n < 4; ++n) w[n] = *reinterpret_cast<const uint32_t *>(&h[n]);
           }
+          const int piece = (k + j) / 8;
+          sts4(stage + lane * (D * 2) + (((piece & ~7) | ((piece ^ lane) & 7)) << 4), w[0], w[1], w[2], w[3]);
         }
+      }
+      __syncwarp();
+      const bool write = ok && mine < rows.rows;
+#pragma unroll 4
+      for (int n = 0; n < kPieces; ++n) {
+        const int from = n * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;  // row of the warp, piece of the row
+        const int other = tile * C::kRows + 128 * q + 32 * quarter + from;
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(stage + from * (D * 2) + (((piece & ~7) | ((piece ^ from) & 7)) << 4))
+                     : "memory");
+        if (ok && other < rows.rows)
+          reinterpret_cast<uint4 *>(static_cast<T *>(a.o) + (rows.t0 + other / r) * a.o_stride + (int64_t)(hk * r + other % r) * D)[piece] = w;
       }
       if (write && a.lse) a.lse[tok * a.HQ + head] = L == 0.f ? -INFINITY : (M + log2f(L) - kShift) * kLn2;
     } while (next(tile));
-  } else if (warp < 12) {
-    // ---------------- expansion of K and V
-    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegD));
-    const X x{c, b, hk, warp & 3, lane};
+  } else if (warp < C::kMma) {
+    // ---------------- expansion of K, or of V
+    if constexpr (C::kRegX < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegX));
     int tile = tile0;
     do {
-      typename X::KRegs kr;
-      typename X::VRegs vr;
-      const bool has_k = QT == 2 || warp < 8, has_v = QT == 2 || warp >= 8;
-      int page[X::W], ahead[X::W];
-      const int n = c_kv_stall ? 0 : rows.tiles;
-#pragma unroll
-      for (int i = 0; i < X::W; ++i) page[i] = n > 0 ? x.page_of(rows.first, i) : -1;
-      if (n > 0) {
-        if (has_k) x.fetch_k(rows.first, page, kr);
-        if (has_v) x.fetch_v(rows.first, page, vr);
-      }
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int n0 = rows.first + i * BN, s = i & 1;
-        const uint32_t ph = ((i >> 1) & 1) ^ 1;
-#pragma unroll
-        for (int k = 0; k < X::W; ++k) ahead[k] = i + 1 < n ? x.page_of(n0 + BN, k) : -1;
-        if (has_k) {
-          if (!wait_warp(&bars->k_empty[s], ph, bars)) break;
-          x.put_k(kr, sm + C::kK + s * C::kStage, sm + C::kX, s);
-          publish_smem(&bars->k_full[s], lane);
-          x.fetch_k(n0 + BN, ahead, kr);
-        }
-        if (has_v) {
-          if (!wait_warp(&bars->v_empty[s], ph, bars)) break;
-          if (x.put_v(vr, sm + C::kV + s * C::kStage, rows.len - n0)) bars->bad_v = 1;
-          publish_smem(&bars->v_full[s], lane);
-          x.fetch_v(n0 + BN, ahead, vr);
-        }
-      }
+      const X x{c, b, hk, warp & 3, lane, rows.first, c_kv_stall ? 0 : rows.tiles * X::W};
+      if (warp < C::kFirstV) x.run_k(bars, sm);
+      else x.run_v(bars, sm, rows.len);
     } while (next(tile));
   } else {
-    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegM));
+    if constexpr (C::kRegM < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegM));
     int tile = tile0;
     do {
-      if (warp == 12) {
-        // ---------------- the MMAs, in units: row tile u mod QT of tile u / QT, S in buffer u mod 2
+      if (warp == C::kMma) {
+        // ---------------- the MMAs: S of row tile q over the tile i, O of it
         if (elect_one()) {
-          const int units = rows.tiles * QT;
-          const uint32_t kq = sm + C::kQ, kx = sm + C::kX;
+          const int n = rows.tiles;
           bool ok = wait_one(&bars->q_full, 0, bars);
+          const uint32_t q0 = desc_k(sm + C::kQ), k0 = desc_k(sm + C::kK), v0 = desc_mn(sm + C::kV, C::kBox), x0 = desc_k(sm + C::kX);
+          uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stages and their phases
           auto scores = [&](int u) {
-            const int i = u / QT, q = u % QT, s = i & 1;
-            if (q == 0 && !wait_one(&bars->k_full[s], (i >> 1) & 1, bars)) return false;
+            const int q = u % QT, buf = u % C::NB;
+            if (q == 0 && !wait_one(&bars->k_full[ks], kph, bars)) return false;
             fence_after();
-            const uint32_t d = tmem + 128 * (u & 1), ka = kq + q * C::kQTile, kb = sm + C::kK + s * C::kStage;
+            const uint32_t d = tmem + C::kS * buf;
+            uint32_t qa = C::kQTmem ? tmem + 128 : q0 + q * (C::kQTile / 16), kb = k0 + ks * (C::kStage / 16);
+#pragma unroll 1
+            for (int k = 0; k < D / 64; ++k, qa += C::kQTmem ? 32 : 128 * 128 / 16, kb += C::kBox / 16)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              umma_ss(d, desc_k(ka + (k >> 2) * (128 * 128) + (k & 3) * 32), desc_k(kb + (k >> 2) * C::kBox + (k & 3) * 32),
-                      idesc(128, BN, false), k > 0);
-            umma_ss(d, desc_k(kx + 64 + 32 * q), desc_k(kx + 32 * s), idesc(128, BN, false), true);
-            umma_commit(&bars->s_full[u & 1]);
-            if (q == QT - 1) umma_commit(&bars->k_empty[s]);
+              for (int j = 0; j < 4; ++j) {
+                if constexpr (C::kQTmem) umma_ts(d, qa + 8 * j, kb + 2 * j, idesc(128, BN, false), k > 0 || j > 0);
+                else umma_ss(d, qa + 2 * j, kb + 2 * j, idesc(128, BN, false), k > 0 || j > 0);
+              }
+            umma_ss(d, x0 + 4 + 2 * q, x0 + C::x_row(ks) * 8 + C::x_piece(ks), idesc(128, BN, false), true);
+            umma_commit(&bars->s_full[buf]);
+            if (q == QT - 1) {
+              umma_commit(&bars->k_empty[ks]);
+              if (++ks == C::NST) {
+                ks = 0;
+                kph ^= 1;
+              }
+            }
             return true;
           };
-          for (int u = 0; ok && u < 2 && u < units; ++u) ok = scores(u);
+          const int units = n * QT;
+          for (int u = 0; ok && u < C::NB && u < units; ++u) ok = scores(u);
+#pragma unroll 1
           for (int u = 0; ok && u < units; ++u) {
-            const int i = u / QT, q = u % QT, s = i & 1;
-            if (q == 0 && !(ok = wait_one(&bars->v_full[s], (i >> 1) & 1, bars))) break;
-            if (!(ok = wait_one(&bars->p_ready[u & 1], (u >> 1) & 1, bars))) break;
+            const int q = u % QT, buf = u % C::NB;
+            if (q == 0 && !(ok = wait_one(&bars->v_full[vs], vph, bars))) break;
+            if (!(ok = wait_one(&bars->p_ready[buf], u / C::NB & 1, bars))) break;
             fence_after();
-            const uint32_t vb = sm + C::kV + s * C::kStage, p = tmem + 128 * (u & 1);
+            uint32_t p = tmem + C::kS * buf, vb = v0 + vs * (C::kStage / 16);
+#pragma unroll 1
+            for (int k = 0; k < BN / 64; ++k, p += 32, vb += 4 * 2048 / 16)
 #pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-              umma_ts(tmem + 256 + D * q, p + 8 * k, desc_mn(vb + k * 2048, C::kBox), idesc(128, D, true), i > 0 || k > 0);
+              for (int j = 0; j < 4; ++j)
+                umma_ts(tmem + 256 + D * q, p + 8 * j, vb + j * (2048 / 16), idesc(128, D, true), u >= QT || k > 0 || j > 0);
             umma_commit(&bars->o_done[q]);
-            if (q == QT - 1) umma_commit(&bars->v_empty[s]);
-            if (u + 2 < units) ok = scores(u + 2);
+            if (q == QT - 1) {
+              umma_commit(&bars->v_empty[vs]);
+              if (++vs == C::NST) {
+                vs = 0;
+                vph ^= 1;
+              }
+            }
+            // P's place is free for other scores
+            if (u + C::NB < units) ok = scores(u + C::NB);
           }
           umma_commit(&bars->drain);  // every MMA issued, complete before their memory is used again
         }
@@ -706,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(const KvView c,
       }
     } while (next(tile));
   }
-  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (warp == C::kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
 template <typename T, int D, int GS>
@@ -720,14 +934,14 @@ cudaError_t run(const KvView &c, const KvAttention &a, cudaStream_t st) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kv_prefill_kernel<T, D, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     // the warps' shares come out of what the block was launched with
-    if (e == cudaSuccess && C::QT == 2 && at.numRegs * 4 < 2 * C::kRegS + C::kRegD + C::kRegM) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess && C::kRegS > C::kRegs && at.numRegs != C::kRegs) e = cudaErrorInvalidConfiguration;
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
   }
   const int r = a.HQ / c.HK;
   const int64_t tiles = (std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + C::kRows - 1) / C::kRows, ctas = tiles * c.B * c.HK;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  kv_prefill_kernel<T, D, GS><<<(unsigned)ctas, kThreads, C::kSmem, st>>>(c, a, (int)tiles);
+  kv_prefill_kernel<T, D, GS><<<(unsigned)ctas, C::kThreads, C::kSmem, st>>>(c, a, (int)tiles);
   return cudaGetLastError();
 }
 template <typename T>
