@@ -6,12 +6,17 @@
 // rounded to bf16 (include/q1.h has the formula; every step is one fp32 operation,
 // so the codes are the same everywhere).
 //
-// Both kernels are streams.  A thread owns a code word: 8 channels of a row, one or
-// two 16-byte pieces of the dense row.  A group is 8 or 16 neighbouring threads, which
-// find its least and largest value by shuffles.  A warp stays with one token, so
+// Both directions are streams, in two forms.  Few rows per sequence (decode): a thread
+// owns a code word, 8 channels of a row; a group is 8 or 16 neighbouring threads, which
+// find its least and largest value by shuffles; a warp stays with one token, so
 // that finding its sequence and page is the warp's work, not each thread's.
+// Many rows: a warp owns a block of 16 tokens of a head.  Four lanes share a token, lane t
+// of them has channels 32 j + 8 t .. + 7, so a group is found in two shuffles, K's codes leave
+// in the order in which they lie, 512 bytes per store, and V's go through shared memory,
+// where words of a token become words of a channel.
 #include <cuda_bf16.h>
 
+#include <climits>
 #include <type_traits>
 
 #include "q1_internal.h"
@@ -32,6 +37,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// The metadata word of a group with least and largest value lo, hi; its bias and the reciprocal of its scale.
+__device__ __forceinline__ uint32_t group_meta(float lo, float hi, float &b, float &inv) {
+  const bool bad = lo != lo;  // a NaN among them
+  lo = min_nan(max_nan(lo, -kLimit), kLimit);
+  hi = min_nan(max_nan(hi, -kLimit), kLimit);
+  const float s0 = __fmul_rn(__fsub_rn(hi, lo), (float)(1.0 / 15.0));
+  b = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, 8.f * s0)));
+  float s = __bfloat162float(__float2bfloat16_rn(
+      fmaxf(__fmul_rn(__fsub_rn(hi, b), (float)(1.0 / 7.0)), __fmul_rn(__fsub_rn(b, lo), 0.125f))));
+  if (s < kTiny) s = 0.f;
+  inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  return bad ? 0x7FC07FC0u : (__float_as_uint(b) & 0xFFFF0000u) | (__float_as_uint(s) >> 16);
+}
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8], float b, float inv) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float xc = fminf(fmaxf(x[i], -kLimit), kLimit);
+    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(xc, b), inv), -8.f), 7.f);
+    word |= (uint32_t)(__float2int_rn(q) + 8) << (4 * i);
+  }
+  return word;
 }
 
 template <typename T>
@@ -143,27 +172,8 @@ __global__ void __launch_bounds__(kThreads) kv_store_kernel(const KvView c, cons
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   if (!mine) return;
-  lo = min_nan(max_nan(lo, -kLimit), kLimit);
-  hi = min_nan(max_nan(hi, -kLimit), kLimit);
-  const float s0 = __fmul_rn(__fsub_rn(hi, lo), (float)(1.0 / 15.0));
-  const __nv_bfloat16 b16 = __float2bfloat16_rn(__fadd_rn(lo, 8.f * s0));
-  const float b = __bfloat162float(b16);
-  __nv_bfloat16 s16 = __float2bfloat16_rn(fmaxf(__fmul_rn(__fsub_rn(hi, b), (float)(1.0 / 7.0)), __fmul_rn(__fsub_rn(b, lo), 0.125f)));
-  float s = __bfloat162float(s16);
-  if (s < kTiny) s = 0.f;
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t word = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float xc = fminf(fmaxf(x[i], -kLimit), kLimit);
-    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(xc, b), inv), -8.f), 7.f);
-    word |= (uint32_t)(__float2int_rn(q) + 8) << (4 * i);
-  }
-  uint32_t meta = __float_as_uint(b) & 0xFFFF0000u | (__float_as_uint(s) >> 16);
-  if (lo != lo) {  // a NaN among them
-    meta = 0x7FC07FC0u;
-    word = 0x88888888u;
-  }
+  float b, inv;
+  const uint32_t meta = group_meta(lo, hi, b, inv), word = lo != lo ? 0x88888888u : codes8(x, b, inv);
   uint32_t *block = reinterpret_cast<uint32_t *>(c.block(at.page, h, at.pos));
   const int tok = at.pos & 15, G = c.D / c.gs, section = is_v ? 2 * c.D + 16 * G : 0;
   block[section + (is_v ? v_word(tok, w) : k_word(tok, w, c.D))] = word;
@@ -192,35 +202,265 @@ __global__ void __launch_bounds__(kThreads) kv_load_kernel(const KvView c, T *__
   store8(is_v ? v + t * v_stride + (int64_t)h * c.D + 8 * w : k + t * k_stride + (int64_t)h * c.D + 8 * w, x);
 }
 
+// ---- many rows: a warp per block of 16 tokens and head
+// The block of a work item: sequence b's blocks are items t0 / 16 + 2 b and on, t0 its first row, which leaves room for
+// each sequence's partial blocks without a sum over those before it.
+struct BlockOf {
+  int64_t t0;             // the sequence's first row, which stands for position pos0
+  int pos0, end, page, p; // positions of the sequence end there; page (or -1) and first position (may be negative) of the block
+};
+__device__ __forceinline__ bool block_of(const KvView &c, int64_t item, int lane, BlockOf &k) {
+  int64_t b;
+  if (c.cu) {
+    int64_t lo = 0, n = c.B;
+    b = -1;
+    while (n > 0) {
+      const int64_t step = (n + 31) / 32, at = min(lo + step * lane, c.B - 1);
+      const unsigned below =
+          __ballot_sync(0xffffffffu, step * lane < n && min(max((int64_t)c.cu[at], (int64_t)0), c.T) / 16 + 2 * at <= item);
+      const int votes = __popc(below);
+      if (votes == 0) break;
+      b = lo + step * (votes - 1);
+      n = step == 1 ? 0 : min(step, n - step * (votes - 1));
+      lo = b;
+    }
+    if (b < 0) return false;
+  } else {
+    const int64_t L = c.T / c.B;
+    b = min(item * 16 / (L + 32), c.B - 1);
+    while (b + 1 < c.B && (b + 1) * L / 16 + 2 * (b + 1) <= item) ++b;
+    while (b > 0 && b * L / 16 + 2 * b > item) --b;
+  }
+  int64_t t1;
+  c.range(b, k.t0, t1);
+  k.end = max(c.lengths[b], 0);
+  k.pos0 = k.end - (int)(t1 - k.t0);
+  const int64_t block = (k.pos0 >> 4) + (item - (k.t0 / 16 + 2 * b));
+  if (block < (k.pos0 >> 4) || block * 16 >= k.end) return false;
+  k.p = (int)(block * 16);
+  k.page = k.p < 0 ? -1 : c.page(b, k.p);
+  return true;
+}
+
+template <int D, int GS>
+struct Tile {
+  static constexpr int G = D / GS, J = D / 32;  // groups; words of a token per lane
+};
+
+// Eight codes and a group's scale and bias -> values
+__device__ __forceinline__ void values8(uint32_t word, uint32_t meta, float (&x)[8]) {
+  const float s = meta_f32(meta, true), b = __uint_as_float(meta & 0xFFFF0000u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)  // 2^23 + q + 8 as bits; the difference and the product are exact
+    x[i] = fmaf(__uint_as_float(0x4B000000u | ((word >> (4 * i)) & 15u)) - 8388616.f, s, b);
+}
+
+// The codes and metadata of one token's words (lane t of its four: channels 32 j + 8 t ..)
+template <int D, int GS>
+__device__ __forceinline__ void quantise(const float (&x)[D / 32][8], uint32_t (&word)[D / 32], uint32_t (&meta)[D / GS]) {
+  constexpr int G = D / GS, JG = GS / 32;  // words of a group per lane
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    float lo = x[g * JG][0], hi = lo;
+#pragma unroll
+    for (int j = g * JG; j < (g + 1) * JG; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo = min_nan(lo, x[j][i]);
+        hi = max_nan(hi, x[j][i]);
+      }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    float b, inv;
+    meta[g] = group_meta(lo, hi, b, inv);
+#pragma unroll
+    for (int j = g * JG; j < (g + 1) * JG; ++j) word[j] = lo != lo ? 0x88888888u : codes8(x[j], b, inv);
+  }
+}
+
+template <typename T, int D, int GS>
+__global__ void __launch_bounds__(kThreads) kv_store_blocks_kernel(const KvView c, const T *__restrict__ k, int64_t k_stride,
+                                                                   const T *__restrict__ v, int64_t v_stride, int64_t items) {
+  constexpr int G = Tile<D, GS>::G, J = Tile<D, GS>::J;
+  __shared__ uint32_t turn[kThreads / 32][2 * D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
+  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + warp, item = unit / c.HK;
+  const int h = (int)(unit - item * c.HK);
+  BlockOf at;
+  if (item >= items || !block_of(c, item, lane, at) || at.page < 0) return;
+  uint32_t *block = reinterpret_cast<uint32_t *>(c.block(at.page, h, at.p));
+  const bool all = at.p >= at.pos0 && at.p + 16 <= at.end;  // every token of the block is among the rows
+#pragma unroll
+  for (int is_v = 0; is_v < 2; ++is_v) {
+    const T *src = is_v ? v : k;
+    const int64_t stride = is_v ? v_stride : k_stride;
+    uint32_t *section = block + is_v * (2 * D + 16 * G);
+    float x[2][J][8];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int p = at.p + 8 * half + (lane >> 2);
+      const bool mine = p >= at.pos0 && p < at.end;
+      const T *row = src + (at.t0 + (mine ? p - at.pos0 : 0)) * stride + (int64_t)h * D + 8 * t;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (mine) {
+          load8(row + 32 * j, x[half][j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[half][j][i] = 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int tok = 8 * half + (lane >> 2), p = at.p + tok;
+      const bool mine = p >= at.pos0 && p < at.end;
+      uint32_t word[J], meta[G];
+      quantise<D, GS>(x[half], word, meta);
+      if (mine && t < G) {
+        uint32_t m = meta[0];
+#pragma unroll
+        for (int g = 1; g < G; ++g) m = t == g ? meta[g] : m;
+        section[2 * D + tok * G + t] = m;
+      }
+      if (!is_v) {
+        if (mine) {
+          if constexpr (J == 2) {
+            *reinterpret_cast<uint2 *>(section + tok * 8 + 2 * t) = make_uint2(word[0], word[1]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < J; j += 4)
+              *reinterpret_cast<uint4 *>(section + tok * (D / 8) + 4 * j + 4 * t) =
+                  make_uint4(word[j], word[j + 1], word[j + 2], word[j + 3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int w = v_word(tok, 4 * j + t);
+          if (all) turn[warp][w] = word[j];
+          else if (mine) section[w] = word[j];
+        }
+      }
+    }
+    if (is_v && all) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        reinterpret_cast<uint4 *>(section)[32 * i + lane] = reinterpret_cast<const uint4 *>(turn[warp])[32 * i + lane];
+    }
+  }
+}
+
+template <typename T, int D, int GS>
+__global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c, T *__restrict__ k, int64_t k_stride, T *__restrict__ v,
+                                                                  int64_t v_stride, int64_t items) {
+  constexpr int G = Tile<D, GS>::G, J = Tile<D, GS>::J;
+  const int lane = threadIdx.x & 31, t = lane & 3;
+  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), item = unit / c.HK;
+  const int h = (int)(unit - item * c.HK);
+  BlockOf at;
+  if (item >= items || !block_of(c, item, lane, at)) return;
+  const bool have = at.page >= 0;
+  const uint32_t *block = reinterpret_cast<const uint32_t *>(c.block(max(at.page, 0), h, max(at.p, 0)));
+  // K: a token for four lanes, as above
+  uint32_t word[2][J], meta[2][G];
+  uint4 vw[D / 64];
+  uint32_t vm[4][G];
+  const int w = lane >> 2;  // V: word w (and w + 8, ..) of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+  if (have) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int tok = 8 * half + w;
+      if constexpr (J == 2) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(block + tok * 8 + 2 * t));
+        word[half][0] = u.x, word[half][1] = u.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < J; j += 4) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4 *>(block + tok * (D / 8) + 4 * j + 4 * t));
+          word[half][j] = u.x, word[half][j + 1] = u.y, word[half][j + 2] = u.z, word[half][j + 3] = u.w;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) meta[half][g] = __ldg(block + 2 * D + tok * G + g);
+    }
+    const uint32_t *section = block + 2 * D + 16 * G;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) vw[i] = __ldg(reinterpret_cast<const uint4 *>(section) + (w + 8 * i) * 4 + t);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int g = 0; g < G; ++g) vm[j][g] = __ldg(section + 2 * D + (2 * t + (j & 1) + 8 * (j >> 1)) * G + g);
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int p = at.p + 8 * half + w;
+    if (p < at.pos0 || p >= at.end) continue;
+    T *row = k + (at.t0 + p - at.pos0) * k_stride + (int64_t)h * D + 8 * t;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float x[8] = {};
+      if (have) values8(word[half][j], meta[half][32 * j / GS], x);
+      store8(row + 32 * j, x);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int p = at.p + 2 * t + (j & 1) + 8 * (j >> 1);
+    if (p < at.pos0 || p >= at.end) continue;
+    T *row = v + (at.t0 + p - at.pos0) * v_stride + (int64_t)h * D + 8 * w;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      float x[8] = {};
+      if (have) values8(j == 0 ? vw[i].x : j == 1 ? vw[i].y : j == 2 ? vw[i].z : vw[i].w, vm[j][64 * i / GS], x);
+      store8(row + 64 * i, x);
+    }
+  }
+}
+
 // warps per token
 inline int parts_of(const KvView &c) { return (2 * c.HK * (c.D / 8) + 31) / 32; }
+// Blocks where sequences bring eight rows or more on average: below, most of a block's lanes would idle.
+inline bool by_blocks(const KvView &c) { return c.T >= 8 * c.B; }
 
-template <typename T>
-cudaError_t store_t(const KvView &c, const void *k, int64_t ks, const void *v, int64_t vs, cudaStream_t st) {
-  const int parts = parts_of(c);
-  const int64_t blocks = (c.T * parts + kThreads / 32 - 1) / (kThreads / 32);
-  kv_store_kernel<T><<<(unsigned)blocks, kThreads, 0, st>>>(c, static_cast<const T *>(k), ks, static_cast<const T *>(v), vs, parts);
+template <typename T, int D, int GS, bool LOAD, typename P>
+cudaError_t blocks_t(const KvView &c, P *k, int64_t ks, P *v, int64_t vs, cudaStream_t st) {
+  const int64_t items = c.T / 16 + 2 * c.B, ctas = (items * c.HK + kThreads / 32 - 1) / (kThreads / 32);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if constexpr (LOAD) kv_load_blocks_kernel<T, D, GS><<<(unsigned)ctas, kThreads, 0, st>>>(c, static_cast<T *>(k), ks, static_cast<T *>(v), vs, items);
+  else kv_store_blocks_kernel<T, D, GS><<<(unsigned)ctas, kThreads, 0, st>>>(c, static_cast<const T *>(k), ks, static_cast<const T *>(v), vs, items);
   return cudaGetLastError();
 }
-template <typename T>
-cudaError_t load_t(const KvView &c, void *k, int64_t ks, void *v, int64_t vs, cudaStream_t st) {
+template <typename T, bool LOAD, typename P>
+cudaError_t run_t(const KvView &c, P *k, int64_t ks, P *v, int64_t vs, cudaStream_t st) {
+  if (by_blocks(c)) {
+    if (c.D == 64) return blocks_t<T, 64, 64, LOAD>(c, k, ks, v, vs, st);
+    if (c.D == 128) return c.gs == 64 ? blocks_t<T, 128, 64, LOAD>(c, k, ks, v, vs, st) : blocks_t<T, 128, 128, LOAD>(c, k, ks, v, vs, st);
+    return c.gs == 64 ? blocks_t<T, 256, 64, LOAD>(c, k, ks, v, vs, st) : blocks_t<T, 256, 128, LOAD>(c, k, ks, v, vs, st);
+  }
   const int parts = parts_of(c);
-  const int64_t blocks = (c.T * parts + kThreads / 32 - 1) / (kThreads / 32);
-  kv_load_kernel<T><<<(unsigned)blocks, kThreads, 0, st>>>(c, static_cast<T *>(k), ks, static_cast<T *>(v), vs, parts);
+  const int64_t ctas = (c.T * parts + kThreads / 32 - 1) / (kThreads / 32);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if constexpr (LOAD) kv_load_kernel<T><<<(unsigned)ctas, kThreads, 0, st>>>(c, static_cast<T *>(k), ks, static_cast<T *>(v), vs, parts);
+  else kv_store_kernel<T><<<(unsigned)ctas, kThreads, 0, st>>>(c, static_cast<const T *>(k), ks, static_cast<const T *>(v), vs, parts);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_store(const KvView &c, const void *k, int64_t ks, const void *v, int64_t vs, q1_dtype t, cudaStream_t st) {
-  if (t == Q1_BF16) return store_t<__nv_bfloat16>(c, k, ks, v, vs, st);
-  if (t == Q1_F16) return store_t<__half>(c, k, ks, v, vs, st);
-  return store_t<float>(c, k, ks, v, vs, st);
+  if (t == Q1_BF16) return run_t<__nv_bfloat16, false>(c, k, ks, v, vs, st);
+  if (t == Q1_F16) return run_t<__half, false>(c, k, ks, v, vs, st);
+  return run_t<float, false>(c, k, ks, v, vs, st);
 }
 cudaError_t launch_kv_load(const KvView &c, void *k, int64_t ks, void *v, int64_t vs, q1_dtype t, cudaStream_t st) {
-  if (t == Q1_BF16) return load_t<__nv_bfloat16>(c, k, ks, v, vs, st);
-  if (t == Q1_F16) return load_t<__half>(c, k, ks, v, vs, st);
-  return load_t<float>(c, k, ks, v, vs, st);
+  if (t == Q1_BF16) return run_t<__nv_bfloat16, true>(c, k, ks, v, vs, st);
+  if (t == Q1_F16) return run_t<__half, true>(c, k, ks, v, vs, st);
+  return run_t<float, true>(c, k, ks, v, vs, st);
 }
 
 }  // namespace q1
