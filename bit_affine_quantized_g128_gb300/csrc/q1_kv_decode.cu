@@ -78,6 +78,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -89,13 +94,27 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 // Eight codes -> fp16 pairs (q_i, q_{i+4}), i = 0..3: an and-or puts the four bits
-// under the exponent of 1024 (bits 0..3 count 1 there) or of 64 (bits 4..7 do).
-__device__ __forceinline__ void expand(uint32_t w, uint32_t (&h)[4]) {
-  h[0] = hsub2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u);  // 1024 + u - 1032
-  h[1] = hsub2((w & 0x00F000F0u) | 0x54005400u, 0x54805480u);  // 64 + u - 72
+// under the exponent of 1024 (bits 0..3 count 1 there) or of 64 (bits 4..7 do).  The exponents come in registers: with
+// both constants in the instruction it takes two.
+struct Exponents {
+  uint32_t a, b;
+  __device__ __forceinline__ Exponents() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(a));
+    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(b));
+  }
+};
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t x) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(x));
+  return r;
+}
+__device__ __forceinline__ void expand(uint32_t w, const Exponents &x, uint32_t (&h)[4]) {
+  h[0] = hsub2(and_or<0x000F000Fu>(w, x.a), 0x64086408u);  // 1024 + u - 1032
+  h[1] = hsub2(and_or<0x00F000F0u>(w, x.b), 0x54805480u);  // 64 + u - 72
   w >>= 8;
-  h[2] = hsub2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-  h[3] = hsub2((w & 0x00F000F0u) | 0x54005400u, 0x54805480u);
+  h[2] = hsub2(and_or<0x000F000Fu>(w, x.a), 0x64086408u);
+  h[3] = hsub2(and_or<0x00F000F0u>(w, x.b), 0x54805480u);
 }
 __device__ __forceinline__ float meta_scale(uint32_t m) { return __uint_as_float(m << 16); }
 __device__ __forceinline__ float meta_bias(uint32_t m) { return __uint_as_float(m & 0xFFFF0000u); }
@@ -129,11 +148,27 @@ __device__ __forceinline__ void store4(T *p, float4 f) {
 
 // How a launch shares the work: row tiles and splits per sequence and head, and
 // blocks of 16 tokens per chunk.  Split s does chunks s, s + splits, ... of its
-// tile's context.
+// tile's context.  Up to kCluster splits are the CTAs of a cluster, which join through their shared
+// memory; more go through the workspace and a second kernel.
 struct Split {
   int tiles, splits, chunk;
+  bool cluster; // the splits of a tile are a cluster
   float *part;  // [B][HK][tiles][splits][8 NT][D + 4]: unnormalised rows, then maximum and sum
 };
+constexpr int kCluster = 8;
+
+__device__ __forceinline__ float4 load_shared_of(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n}\n"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // What a tile of rows sees: blocks [first, first + count) of the sequence.
 struct Span {
@@ -169,17 +204,19 @@ struct Decode {
   static constexpr int kQBytes = kQShared ? NT * QP * (D / 32) * 512 : 0;
   static constexpr int kStride = D + 8;                                              // floats of a joined row in shared memory
   static constexpr int kRing = kWarps * kStages * kBlock, kJoin = kWarps * kRows * kStride * 4;
-  static constexpr int kSmem = kQBytes + (kRing > kJoin ? kRing : kJoin) + kWarps * kRows * 8;
+  static constexpr int kOwn = kRows * (D + 4) * 4;                                    // this CTA's rows, for its cluster
+  static constexpr int kSmem = kQBytes + (kRing > kJoin ? kRing : kJoin) + kOwn + kWarps * kRows * 8;
   static constexpr int kCtas = kSmem * 2 <= 220 * 1024 && NT * D <= 128 && QP == 1 ? 2 : 1;
 };
 
-template <typename T, int D, int GS, int NT>
+template <typename T, int D, int GS, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv_decode_kernel(const KvView c, const KvAttention a,
                                                                                                const Split sp) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel, where there is one
   using C = Decode<T, D, GS, NT>;
   constexpr int G = C::G, QP = C::QP, PP = C::PP, J = D / 32, H = D / 64, kRows = C::kRows;
   extern __shared__ __align__(16) unsigned char smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
   const int split = (int)(blockIdx.x % sp.splits);
   int64_t id = blockIdx.x / sp.splits;
   const int64_t slot = id;
@@ -191,16 +228,17 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
   const uint32_t qs = smem_u32(smem), ring = qs + C::kQBytes + warp * (kStages * C::kBlock);
   float *join = reinterpret_cast<float *>(smem + C::kQBytes);
   float *sm_m = reinterpret_cast<float *>(smem + C::kSmem - kWarps * kRows * 8), *sm_l = sm_m + kWarps * kRows;
+  float *own = sm_m - C::kOwn / 4;
 
-  Span s;
+  const Exponents exps;
+  Span s{};
   // (tiles beyond those that the hint max_q foresaw are done whole by split 0)
   for (int tile = tile0; s.set<C::kRows>(c, a, b, tile); tile += sp.tiles) {
     const bool alone = sp.splits == 1 || tile != tile0;
     const int splits = alone ? 1 : sp.splits;
     if (alone && split > 0) return;
     const int chunks = (s.count + sp.chunk - 1) / sp.chunk;
-    if (split >= chunks && split > 0) return;  // the joining kernel knows
-    const int per = sp.chunk / kWarps, steps = split < chunks ? (chunks - split + splits - 1) / splits * per : 0;
+    if (!(CLUSTER && !alone) && split >= chunks && split > 0) return;  // the joining kernel knows
 
     // ---- q: fragments, and per group the sum of its channels
     uint32_t q[C::kQShared ? 1 : NT][QP][C::kQShared ? 1 : J][4];
@@ -227,7 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
       // the power of two that brings the largest into [2^14, 2^15)
       const int be = (int)(__float_as_uint(big) >> 23);
       const int e = be == 0 || be == 255 ? 0 : min(max(14 - (be - 127), -100), 100);
-      const float up = pow2f(e);
+      const float up = a.scale < 0.f ? -pow2f(e) : pow2f(e);
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
@@ -265,7 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
         const int from = 4 * (2 * t + k);
 #pragma unroll
         for (int i = 0; i < G; ++i) qsum[nt][i][k] = __shfl_sync(0xffffffffu, sum[i], from);
-        f[nt][k] = __shfl_sync(0xffffffffu, pow2f(-e), from) * (a.scale * kLog2e);
+        f[nt][k] = fmaxf(__shfl_sync(0xffffffffu, pow2f(-e), from) * (fabsf(a.scale) * kLog2e), 1e-30f);
         const int pos = s.pos0 + min(tile * kRows + 8 * nt + 2 * t + k, s.rows - 1) / r;
         hi[nt][k] = pos < 0 ? -1 : a.causal ? pos : s.len - 1;
         lo[nt][k] = a.window ? max(pos, 0) - a.window : -1;
@@ -289,52 +327,47 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
     for (int nt = 0; nt < NT; ++nt) M[nt][0] = M[nt][1] = kNone;
     float vfac = pow2f(100);           // V's scales times this stay below 2^6
 
-    // ---- the blocks, kStages - 1 ahead
+    // ---- the blocks of this warp: every kWarps-th of a chunk, kStages - 1 ahead
+    const int page_blocks = c.page_shift - 4, mask = (1 << page_blocks) - 1, pages = (int)min(c.n_pages, (int64_t)INT32_MAX),
+              width = (int)min(c.table_width, (int64_t)INT32_MAX);
+    const int32_t *table = c.table + b * c.table_stride;
+    const int64_t page_bytes = (int64_t)c.HK * C::kBlock << page_blocks;
+    const unsigned char *data = c.data + ((int64_t)hk * C::kBlock << page_blocks) + lane * 16;
+#pragma unroll 1
+    for (int chunk = split; chunk < chunks; chunk += splits) {
+    const int j0 = s.first + chunk * sp.chunk + warp;    // the first, in the sequence
+    const int n = max(0, (s.first + min((chunk + 1) * sp.chunk, s.count) - j0 + kWarps - 1) / kWarps);
     int there = 0;                     // a bit per stage: its page exists
-    int ib = split * sp.chunk + warp, ii = 0;  // the next block to fetch, and its number in its chunk
-    const int page_blocks = c.page_shift - 4, gap = (splits - 1) * sp.chunk;
-    auto page_of = [&](int i) { return i < s.count ? c.page(b, (s.first + i) << 4) : -1; };
-    int page = steps > 0 ? page_of(ib) : -1;
+    int ahead = j0, page = n > 0 && (ahead >> page_blocks) < width ? table[ahead >> page_blocks] : -1;
+    const int j1 = j0 + n * kWarps;
     auto fetch = [&](int stage) {
-      there &= ~(1 << stage);
-      if (page >= 0) {
-        there |= 1 << stage;
-        const unsigned char *src = c.data + (((int64_t)page * c.HK + hk) * (1 << page_blocks) + ((s.first + ib) & ((1 << page_blocks) - 1))) * C::kBlock;
-        const uint32_t dst = ring + stage * C::kBlock;
+      const bool have = (unsigned)page < (unsigned)pages;
+      there = (there & ~(1 << stage)) | (int)have << stage;
+      if (have) {
+        const unsigned char *src = data + page * page_bytes + (ahead & mask) * C::kBlock;
+        const uint32_t dst = ring + stage * C::kBlock + lane * 16;
 #pragma unroll
         for (int o = 0; o < C::kBlock; o += 512)
-          if (o + 512 <= C::kBlock || o + lane * 16 < C::kBlock) copy16(dst + o + lane * 16, src + o + lane * 16);
+          if (o + 512 <= C::kBlock || o + lane * 16 < C::kBlock) copy16(dst + o, src + o);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      ib += kWarps;
-      if (++ii == per) {
-        ii = 0;
-        ib += gap;
-      }
+      ahead += kWarps;
+      page = ahead < j1 && (ahead >> page_blocks) < width ? table[ahead >> page_blocks] : -1;
     };
-    int fetched = 0;
-    for (; fetched < kStages - 1; ++fetched) {
-      fetch(fetched);
-      page = fetched + 1 < steps ? page_of(ib) : -1;
-    }
-    int cb = split * sp.chunk + warp, ci = 0, stage = 0;  // the block at hand
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    int stage = 0;
 #pragma unroll 1
-    for (int n = 0; n < steps; ++n) {
+    for (int j = j0; j < j1; j += kWarps) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();  // every lane's part is there, and every lane is done with the stage that is filled next
-      fetch(stage == 0 ? kStages - 1 : stage - 1);
-      page = ++fetched < steps ? page_of(ib) : -1;
+      fetch((stage + kStages - 1) & (kStages - 1));
       const bool have = there >> stage & 1;
       const uint32_t at = ring + stage * C::kBlock;
-      const int p0 = ((s.first + cb) << 4) + g;  // this lane's tokens: p0 and p0 + 8
-      const bool whole = p0 - g > lo_all && p0 - g + 15 <= hi_all;
-      if (++stage == kStages) stage = 0;
-      cb += kWarps;
-      if (++ci == per) {
-        ci = 0;
-        cb += gap;
-      }
-      if (!have) continue;
+      const int p0 = (j << 4) + g;  // this lane's tokens: p0 and p0 + 8
+      const bool whole = (j << 4) > lo_all && (j << 4) + 15 <= hi_all;
+      stage = (stage + 1) & (kStages - 1);
+      if (!__any_sync(0xffffffffu, have)) continue;  // (a vote: a branch of the whole warp)
       // S^T
       float x[NT][4] = {};
       {
@@ -358,8 +391,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
 #pragma unroll
           for (int j = i * GS / 32; j < (i + 1) * GS / 32; ++j) {
             uint32_t u[4], v[4];
-            expand(k0[j], u);
-            expand(k1[j], v);
+            expand(k0[j], exps, u);
+            expand(k1[j], exps, v);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -384,43 +417,40 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
           }
         }
       }
-      // the softmax's numerators
-      bool move = false;
-      bool seen0 = true, seen1 = true;  // this lane's tokens are seen by some row (what is not may hold anything)
-      if (!whole) seen0 = seen1 = false;
+      // the softmax's numerators; what some row does not see may hold anything
+      uint32_t m0[G], m1[G];  // V's
+      lds_words(at + 16 * D + 64 * G + g * G * 4, m0);
+      lds_words(at + 16 * D + 64 * G + (g + 8) * G * 4, m1);
+      if (!whole) {
+        bool seen0 = false, seen1 = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          x[nt][k] *= f[nt][k];
-          x[nt][k + 2] *= f[nt][k];
-          if (!whole) {
+          for (int k = 0; k < 2; ++k) {
             const bool v0 = p0 > lo[nt][k] && p0 <= hi[nt][k], v1 = p0 + 8 > lo[nt][k] && p0 + 8 <= hi[nt][k];
             x[nt][k] = v0 ? x[nt][k] : -INFINITY;
             x[nt][k + 2] = v1 ? x[nt][k + 2] : -INFINITY;
             seen0 |= v0;
             seen1 |= v1;
           }
-          move |= fmaxf(x[nt][k], x[nt][k + 2]) > M[nt][k] + kSlack;
-        }
-      uint32_t m0[G], m1[G];  // V's
-      lds_words(at + 16 * D + 64 * G + g * G * 4, m0);
-      lds_words(at + 16 * D + 64 * G + (g + 8) * G * 4, m1);
-      if (!whole) {  // the other lanes' rows see the same tokens
+        // (the other lanes' rows see the same tokens)
         const unsigned any0 = __ballot_sync(0xffffffffu, seen0), any1 = __ballot_sync(0xffffffffu, seen1);
-        seen0 = (any0 >> (lane & 28) & 15u) != 0;
-        seen1 = (any1 >> (lane & 28) & 15u) != 0;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          m0[i] = seen0 ? m0[i] : 0u;
-          m1[i] = seen1 ? m1[i] : 0u;
+          m0[i] = (any0 >> (lane & 28) & 15u) ? m0[i] : 0u;
+          m1[i] = (any1 >> (lane & 28) & 15u) ? m1[i] : 0u;
         }
       }
-      float top = 0.f;
+      float y[NT][4], over = kNone, top = 0.f;
 #pragma unroll
-      for (int i = 0; i < G; ++i) top = fmaxf(top, fmaxf(fabsf(meta_scale(m0[i])), fabsf(meta_scale(m1[i]))));
-      move |= top * vfac > 64.f;
-      if (__any_sync(0xffffffffu, move)) {
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[nt][k] = fmaf(x[nt][k], f[nt][k & 1], -M[nt][k & 1]);
+        over = max3(max3(over, y[nt][0], y[nt][1]), y[nt][2], y[nt][3]);
+      }
+#pragma unroll
+      for (int i = 0; i < G; ++i) top = max3(top, fabsf(meta_scale(m0[i])), fabsf(meta_scale(m1[i])));
+      if (__any_sync(0xffffffffu, over > kSlack || top * vfac > 64.f)) {
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         float keep = 1.f;
@@ -436,10 +466,12 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
             float mx = fmaxf(x[nt][k], x[nt][k + 2]);
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = fmaxf(mx, M[nt][k]);
+            mx = fmaxf(mx * f[nt][k], M[nt][k]);
             const float down = ex2(M[nt][k] - mx);
             M[nt][k] = mx;
             L[nt][k] *= down;
+            y[nt][k] = fmaf(x[nt][k], f[nt][k], -mx);
+            y[nt][k + 2] = fmaf(x[nt][k + 2], f[nt][k], -mx);
 #pragma unroll
             for (int i = 0; i < G; ++i) bias[nt][i][k] *= down;
 #pragma unroll
@@ -455,8 +487,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          x[nt][k] = ex2(x[nt][k] - M[nt][k]);
-          x[nt][k + 2] = ex2(x[nt][k + 2] - M[nt][k]);
+          x[nt][k] = ex2(y[nt][k]);
+          x[nt][k + 2] = ex2(y[nt][k + 2]);
           L[nt][k] += x[nt][k] + x[nt][k + 2];
         }
       // O^T
@@ -467,16 +499,16 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float y[4] = {x[nt][0] * s0, x[nt][1] * s0, x[nt][2] * s1, x[nt][3] * s1};
-          float z[4] = {x[nt][0] * b0, x[nt][1] * b0, x[nt][2] * b1, x[nt][3] * b1};
-          if (!whole) {  // a token that other rows see may have a NaN
+          if (whole) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              y[k] = x[nt][k] == 0.f ? 0.f : y[k];
-              z[k] = x[nt][k] == 0.f ? 0.f : z[k];
-            }
+            for (int k = 0; k < 2; ++k) bias[nt][i][k] = fmaf(b0, x[nt][k], fmaf(b1, x[nt][k + 2], bias[nt][i][k]));
+          } else {  // a token that other rows see may have a NaN
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = x[nt][k] == 0.f ? 0.f : y[k];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              bias[nt][i][k] += (x[nt][k] == 0.f ? 0.f : x[nt][k] * b0) + (x[nt][k + 2] == 0.f ? 0.f : x[nt][k + 2] * b1);
           }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) bias[nt][i][k] += z[k] + z[k + 2];
           const uint32_t h0 = half2_bits(y[0], y[1]), h1 = half2_bits(y[2], y[3]);
           pb[nt][i][0][0] = movmatrix(h0);
           pb[nt][i][0][1] = movmatrix(h1);
@@ -492,10 +524,10 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
         const uint4 w = lds4(at + 8 * D + 64 * G + (g + 8 * h) * 64 + 16 * t);
         // tokens 2t, 2t + 1 and 2t + 8, 2t + 9: channels 0..3 of the word, and 4..7
         uint32_t x01[4], x89[4], y01[4], y89[4];
-        expand(__byte_perm(w.x, w.y, 0x5410), x01);
-        expand(__byte_perm(w.x, w.y, 0x7632), y01);
-        expand(__byte_perm(w.z, w.w, 0x5410), x89);
-        expand(__byte_perm(w.z, w.w, 0x7632), y89);
+        expand(__byte_perm(w.x, w.y, 0x5410), exps, x01);
+        expand(__byte_perm(w.x, w.y, 0x7632), exps, y01);
+        expand(__byte_perm(w.z, w.w, 0x5410), exps, x89);
+        expand(__byte_perm(w.z, w.w, 0x7632), exps, y89);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -506,6 +538,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    }
 
     // ---- join the warps
 #pragma unroll
@@ -565,63 +599,108 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
         const int64_t tok = s.t0 + all / r;
         store4(static_cast<T *>(a.o) + tok * a.o_stride + (int64_t)head * D + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
         if (d == 0 && a.lse) a.lse[tok * a.HQ + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      } else if constexpr (CLUSTER) {
+        *reinterpret_cast<float4 *>(own + row * (D + 4) + d) = o;
+        if (d == 0) *reinterpret_cast<float2 *>(own + row * (D + 4) + D) = make_float2(m, l);
       } else {
         float *dst = sp.part + ((slot * splits + split) * kRows + row) * (D + 4);
         *reinterpret_cast<float4 *>(dst + d) = o;
         if (d == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(m, l);
       }
     }
+    if constexpr (CLUSTER) {
+      if (!alone) {
+        // the cluster's CTAs share the rows' values among them
+        cluster_sync();
+        const uint32_t base = smem_u32(own);
+        for (int i = split * kWarps * 32 + threadIdx.x; i < valid * (D / 4); i += splits * kWarps * 32) {
+          const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+          float m = kNone, l = 0.f, ms[kCluster], ls[kCluster];
+#pragma unroll
+          for (int k = 0; k < kCluster; ++k)
+            if (k < splits) {
+              const float4 v = load_shared_of(base + (row * (D + 4) + D) * 4, k);
+              ms[k] = v.x;
+              ls[k] = v.y;
+              m = fmaxf(m, v.x);
+            }
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kCluster; ++k)
+            if (k < splits) {
+              const float z = ex2(ms[k] - m);
+              const float4 v = load_shared_of(base + (row * (D + 4) + d) * 4, k);
+              l = fmaf(z, ls[k], l);
+              o.x = fmaf(z, v.x, o.x);
+              o.y = fmaf(z, v.y, o.y);
+              o.z = fmaf(z, v.z, o.z);
+              o.w = fmaf(z, v.w, o.w);
+            }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int all = tile * kRows + row, head = hk * r + all % r;
+          const int64_t tok = s.t0 + all / r;
+          store4(static_cast<T *>(a.o) + tok * a.o_stride + (int64_t)head * D + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+          if (d == 0 && a.lse) a.lse[tok * a.HQ + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        }
+        cluster_sync();  // no CTA leaves while another reads its rows
+      }
+    }
     __syncthreads();  // before the next tile's blocks come
   }
 }
 
-// Joins the splits of a tile of rows; a warp per row.
+// Joins the splits of a row; a CTA per row, its threads in groups that take every so many-th split.
+constexpr int kJoinThreads = 256;
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(ROWS * 32) kv_join_kernel(const KvView c, const KvAttention a, const Split sp) {
-  int64_t id = blockIdx.x;
-  const int64_t slot = id;
-  const int tile = (int)(id % sp.tiles);
-  id /= sp.tiles;
-  const int hk = (int)(id % c.HK);
-  const int64_t b = id / c.HK;
-  const int r = a.HQ / c.HK, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Span s;
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvView c, const KvAttention a, const Split sp) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  __shared__ float4 part[kGroups][kLanes];
+  __shared__ float2 ml[kGroups];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t slot = blockIdx.x / ROWS;
+  const int row = (int)(blockIdx.x - slot * ROWS), tile = (int)(slot % sp.tiles);
+  const int64_t id = slot / sp.tiles, b = id / c.HK;
+  const int hk = (int)(id - b * c.HK), r = a.HQ / c.HK, group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  Span s{};
   if (!s.set<ROWS>(c, a, b, tile) || tile * ROWS + row >= s.rows) return;
   const int n = max(1, min(sp.splits, (s.count + sp.chunk - 1) / sp.chunk));
   const float *src = sp.part + (slot * sp.splits * ROWS + row) * (D + 4);
   const int64_t step = (int64_t)ROWS * (D + 4);
-  float m = kNone;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, src[i * step + D]);
+  float m = kNone, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float m2, float l2, float4 v) {
+    const float mx = fmaxf(m, m2), z = ex2(m - mx), z2 = ex2(m2 - mx);
+    m = mx;
+    l = fmaf(z, l, z2 * l2);
+    o.x = fmaf(z, o.x, z2 * v.x);
+    o.y = fmaf(z, o.y, z2 * v.y);
+    o.z = fmaf(z, o.z, z2 * v.z);
+    o.w = fmaf(z, o.w, z2 * v.w);
+  };
+  for (int i = group; i < n; i += 4 * kGroups) {
+    float2 q[4];
+    float4 v[4];
 #pragma unroll
-  for (int o = 1; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f;
-  constexpr int V = D / 128 > 0 ? D / 128 : 1;
-  float4 o[V] = {};
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = *reinterpret_cast<const float2 *>(src + i * step + D);
-    const float z = ex2(ml.x - m);
-    l = fmaf(z, ml.y, l);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int d = 4 * (lane + 32 * k);
-      if (d < D) {
-        const float4 v = *reinterpret_cast<const float4 *>(src + i * step + d);
-        o[k].x = fmaf(z, v.x, o[k].x);
-        o[k].y = fmaf(z, v.y, o[k].y);
-        o[k].z = fmaf(z, v.z, o[k].z);
-        o[k].w = fmaf(z, v.w, o[k].w);
+    for (int k = 0; k < 4; ++k)
+      if (i + k * kGroups < n) {
+        q[k] = *reinterpret_cast<const float2 *>(src + (i + k * kGroups) * step + D);
+        v[k] = *reinterpret_cast<const float4 *>(src + (i + k * kGroups) * step + 4 * lane);
       }
-    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * kGroups < n) add(q[k].x, q[k].y, v[k]);
   }
+  part[group][lane] = o;
+  if (lane == 0) ml[group] = make_float2(m, l);
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k)
+    if (k < n) add(ml[k].x, ml[k].y, part[k][lane]);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int all = tile * ROWS + row, head = hk * r + all % r;
   const int64_t tok = s.t0 + all / r;
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int d = 4 * (lane + 32 * k);
-    if (d < D) store4(static_cast<T *>(a.o) + tok * a.o_stride + (int64_t)head * D + d,
-                      make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
-  }
+  store4(static_cast<T *>(a.o) + tok * a.o_stride + (int64_t)head * D + 4 * lane, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
   if (lane == 0 && a.lse) a.lse[tok * a.HQ + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -629,38 +708,68 @@ __global__ void __launch_bounds__(ROWS * 32) kv_join_kernel(const KvView c, cons
 // are expanded once for both halves).
 inline int rows_of(const KvView &c, const KvAttention &a) { return std::max<int64_t>(a.max_q, 1) * (a.HQ / c.HK) <= 8 ? 8 : 16; }
 
-Split plan(const KvView &c, const KvAttention &a) {
+Split plan(const KvView &c, const KvAttention &a, bool fp32) {
   const int rows = rows_of(c, a), r = a.HQ / c.HK;
   Split s;
   s.tiles = (int)std::min<int64_t>((std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + rows - 1) / rows, 1 << 20);
   int64_t seen = std::max<int64_t>(a.max_len, 1);
   if (a.window) seen = std::min<int64_t>(seen, (int64_t)a.window + rows + 15);
   const int64_t blocks = (seen + 15) / 16, work = c.B * c.HK * s.tiles;
-  // about two CTAs per SM in all, at least two blocks per warp each
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((304 + work - 1) / work, blocks / (2 * kWarps)));
-  s.chunk = (int)(((blocks + want - 1) / want + kWarps - 1) / kWarps * kWarps);
+  // CTAs for one, two or four rounds of the GPU: the more, the better ragged batches even out, as long as each has 16, 64
+  // or 128 blocks to do.
+  const int64_t slots = 152 * (c.D == 64 || (c.D == 128 && rows == 8 && !fp32) ? 2 : 1);
+  int64_t want = std::min(slots / work, blocks / 16);
+  if (blocks / std::max<int64_t>(2 * slots / work, 1) >= 64) want = 2 * slots / work;
+  if (blocks / std::max<int64_t>(4 * slots / work, 1) >= 128) want = 4 * slots / work;
+  s.chunk = (int)(((blocks + std::max<int64_t>(want, 1) - 1) / std::max<int64_t>(want, 1) + kWarps - 1) / kWarps * kWarps);
   s.splits = (int)((blocks + s.chunk - 1) / s.chunk);
+  // (only where all run at once: a CTA whose split has no tokens would hold its place until the others are done)
+  s.cluster = s.splits > 1 && s.splits <= kCluster && work * s.splits <= slots;
   s.part = nullptr;
   return s;
 }
 
-template <typename T, int D, int GS, int NT>
-cudaError_t run(const KvView &c, const KvAttention &a, const Split &s, cudaStream_t st) {
+template <typename T, int D, int GS, int NT, bool CLUSTER>
+cudaError_t run_c(const KvView &c, const KvAttention &a, const Split &s, cudaStream_t st) {
   using C = Decode<T, D, GS, NT>;
   static std::atomic<uint64_t> ready{0};
   const int dev = current_device();
   if (not_done(ready, dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv_decode_kernel<T, D, GS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(kv_decode_kernel<T, D, GS, NT, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
   }
   const int64_t tiles = c.B * c.HK * s.tiles, ctas = tiles * s.splits;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  kv_decode_kernel<T, D, GS, NT><<<(unsigned)ctas, kWarps * 32, C::kSmem, st>>>(c, a, s);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || s.splits == 1) return e;
-  kv_join_kernel<T, D, 8 * NT><<<(unsigned)tiles, 8 * NT * 32, 0, st>>>(c, a, s);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  if (CLUSTER) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)s.splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_decode_kernel<T, D, GS, NT, CLUSTER>, c, a, s);
+  if (e != cudaSuccess || CLUSTER || s.splits == 1) return e;
+  if (tiles * 8 * NT > INT32_MAX) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)(tiles * 8 * NT), 1, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, 8 * NT>, c, a, s);
+}
+
+template <typename T, int D, int GS, int NT>
+cudaError_t run(const KvView &c, const KvAttention &a, const Split &s, cudaStream_t st) {
+  return s.cluster ? run_c<T, D, GS, NT, true>(c, a, s, st) : run_c<T, D, GS, NT, false>(c, a, s, st);
 }
 template <typename T, int D, int GS>
 cudaError_t run_rows(const KvView &c, const KvAttention &a, const Split &s, cudaStream_t st) {
@@ -675,14 +784,14 @@ cudaError_t run_t(const KvView &c, const KvAttention &a, const Split &s, cudaStr
 
 }  // namespace
 
-size_t kv_decode_workspace_bytes(const KvView &c, const KvAttention &a, q1_dtype) {
-  const Split s = plan(c, a);
-  if (s.splits == 1) return 0;
+size_t kv_decode_workspace_bytes(const KvView &c, const KvAttention &a, q1_dtype t) {
+  const Split s = plan(c, a, t == Q1_F32);
+  if (s.splits == 1 || s.cluster) return 0;
   return (size_t)(c.B * c.HK) * s.tiles * s.splits * rows_of(c, a) * (c.D + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv_decode(const KvView &c, const KvAttention &a, q1_dtype t, void *workspace, cudaStream_t st) {
-  Split s = plan(c, a);
+  Split s = plan(c, a, t == Q1_F32);
   s.part = static_cast<float *>(workspace);
   if (t == Q1_BF16) return run_t<__nv_bfloat16>(c, a, s, st);
   if (t == Q1_F16) return run_t<__half>(c, a, s, st);

@@ -204,13 +204,27 @@ __device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_ca
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) { return bits(__floats2half2_rn(a, b)); }
 
 // Eight codes -> fp16 pairs (q_i, q_{i+4}), i = 0..3: an and-or puts the four bits
-// under the exponent of 1024 (bits 0..3 count 1 there) or of 64 (bits 4..7 do).
-__device__ __forceinline__ void expand(uint32_t w, __half2 (&h)[4]) {
-  h[0] = __hsub2(half2_of((w & 0x000F000Fu) | 0x64006400u), half2_of(0x64086408u));  // 1024 + u - 1032
-  h[1] = __hsub2(half2_of((w & 0x00F000F0u) | 0x54005400u), half2_of(0x54805480u));  // 64 + u - 72
+// under the exponent of 1024 (bits 0..3 count 1 there) or of 64 (bits 4..7 do).  The exponents come in registers: with
+// both constants in the instruction it takes two.
+struct Exponents {
+  uint32_t a, b;
+  __device__ __forceinline__ Exponents() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(a));
+    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(b));
+  }
+};
+template <uint32_t MASK>
+__device__ __forceinline__ __half2 and_or(uint32_t w, uint32_t x) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(x));
+  return half2_of(r);
+}
+__device__ __forceinline__ void expand(uint32_t w, const Exponents &x, __half2 (&h)[4]) {
+  h[0] = __hsub2(and_or<0x000F000Fu>(w, x.a), half2_of(0x64086408u));  // 1024 + u - 1032
+  h[1] = __hsub2(and_or<0x00F000F0u>(w, x.b), half2_of(0x54805480u));  // 64 + u - 72
   w >>= 8;
-  h[2] = __hsub2(half2_of((w & 0x000F000Fu) | 0x64006400u), half2_of(0x64086408u));
-  h[3] = __hsub2(half2_of((w & 0x00F000F0u) | 0x54005400u), half2_of(0x54805480u));
+  h[2] = __hsub2(and_or<0x000F000Fu>(w, x.a), half2_of(0x64086408u));
+  h[3] = __hsub2(and_or<0x00F000F0u>(w, x.b), half2_of(0x54805480u));
 }
 __device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -310,6 +324,7 @@ struct Expander {
   const KvView &c;
   int64_t b;
   int hk, warp, lane, first, blocks;
+  Exponents exps;
   __device__ __forceinline__ int pos(int m) const { return first + m / W * C::BN + 16 * (W * warp + m % W); }
   __device__ __forceinline__ int page_of(int m) const { return m < blocks ? c.page(b, pos(m)) : -1; }
   __device__ __forceinline__ const unsigned char *block(int page, int m) const {
@@ -354,7 +369,7 @@ struct Expander {
 #pragma unroll
     for (int j = 0; j < KW; ++j) {
       __half2 v[4];
-      expand(r.code[j], v);
+      expand(r.code[j], exps, v);
       const __half2 f = s[32 * j / GS];
       sts4((j & 1 ? dst ^ 64 : dst) + (j >> 1) * C::kBox + half * 1024, bits(__hmul2(v[0], f)), bits(__hmul2(v[1], f)),
            bits(__hmul2(v[2], f)), bits(__hmul2(v[3], f)));
@@ -437,7 +452,7 @@ struct Expander {
       for (int w = 0; w < 2; ++w) {
         const uint4 &u = r.code[w];
         __half2 h[4];
-        expand(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, h);
+        expand(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, exps, h);
         sts4(dst + swz(row, v_piece(w)), bits(__hfma2(h[0], s, o)), bits(__hfma2(h[1], s, o)), bits(__hfma2(h[2], s, o)),
              bits(__hfma2(h[3], s, o)));
       }
