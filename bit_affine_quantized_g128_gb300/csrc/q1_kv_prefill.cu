@@ -1,9 +1,11 @@
 // Attention over the 4-bit cache for many query rows (prompts and pieces of
 // prompts), on the tcgen05 tensor cores.
 //
-// A CTA owns 256 rows (two tiles of 128; one for heads of 256) of a key head: row i of
+// A pair of CTAs owns 512 rows (two tiles of 128 each; one for heads of 256) of a key head: row i of
 // a sequence is its new token i / r, query head i mod r of the r that share the key
-// head, so K and V are expanded once for all of them.  Tiles of 128 cached tokens (64)
+// head.  Each expands half of K's tokens and half of V's channels, and the MMAs (cta_group::2) read both halves: with a
+// CTA on its own, the MMAs' operands and the expansions' stores took all of shared memory's bandwidth (heads of 64 do go that
+// way).  Tiles of 128 cached tokens (64)
 // go by:
 //   S = Q K^T                      both operands in shared memory, S in tensor memory
 //   P = 2^(f S - M + 7) as fp16    a thread per row, back into S's columns
@@ -118,22 +120,61 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r;
 }
+template <int CG>
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(kDescHigh), "r"((uint32_t)acc)
+      " tcgen05.mma.cta_group::%6.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(kDescHigh), "r"((uint32_t)acc), "n"(CG)
       : "memory");
 }
+template <int CG>
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %4};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(id), "r"(kDescHigh), "r"((uint32_t)acc)
+      " tcgen05.mma.cta_group::%6.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(kDescHigh), "r"((uint32_t)acc), "n"(CG)
       : "memory");
 }
+// arrives on the barrier (of both CTAs of a pair) once every MMA issued so far by this thread has completed
+template <int CG>
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Arrives on the barrier of the CTA that issues the MMAs (rank 0).  The default semantics (release at CTA scope) do: what
+// the arrival publishes is complete before it, tensor-memory stores by tcgen05.wait::st, shared-memory stores by the proxy
+// fence.  A release at cluster scope would wait for the loads in flight as well.
+template <int CG>
+__device__ __forceinline__ void arrive_lead(uint64_t *bar, int rank) {
+  if (CG == 1 || rank == 0) mbar_arrive(bar);
+  else asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_rank(smem_u32(bar), 0)) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void sync_all() {
+  __syncwarp();
+  if constexpr (CG == 1) __syncthreads();
+  else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// an int of any CTA of the pair, set by one of its roles
+template <int CG>
+__device__ __forceinline__ int any_flag(const volatile int *flag) {
+  if constexpr (CG == 1) return *flag;
+  int x, y;
+  const uint32_t a = smem_u32(const_cast<const int *>(flag));
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(of_rank(a, 0)) : "memory");
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(y) : "r"(of_rank(a, 1)) : "memory");
+  return x | y;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -258,20 +299,24 @@ __device__ __forceinline__ void ldg_words(const unsigned char *p, uint32_t (&w)[
 template <int D, int GS>
 struct Prefill {
   static constexpr int G = D / GS, kBlock = 16 * (D + 8 * G);
+  static constexpr int CG = D == 64 ? 1 : 2;                     // CTAs that work together
   static constexpr int QT = D <= 128 ? 2 : 1, kRows = 128 * QT;  // row tiles of a CTA
   static constexpr int BN = D == 64 ? 128 : 64;                  // cached tokens of a tile
+  static constexpr int BK = BN / CG, DV = D / CG;                // of them this CTA's tokens of K and channels of V
   static constexpr int NB = D == 128 ? 4 : 2;                    // buffers of S
   static constexpr bool kQTmem = D == 256;                       // Q as the MMA's operand in tensor memory
-  static constexpr int kQTile = kQTmem ? 0 : (D / 64) * 128 * 128, kBox = BN * 128, kStage = (D / 64) * kBox;
-  static constexpr int NST = D == 64 ? 2 : D == 128 ? 4 : 3;     // stages of K, and of V
+  static constexpr int kQTile = kQTmem ? 0 : (D / 64) * 128 * 128;
+  static constexpr int kBoxK = BK * 128, kStageK = (D / 64) * kBoxK, kBoxV = BN * 128, kStageV = (DV / 64) * kBoxV;
+  static constexpr int NST = D == 64 ? 2 : 4;                    // stages of K, and of V
   static constexpr int kHeader = 2048;  // barriers, and from byte 1024 on the rows' factors
-  static constexpr int kQ = kHeader, kK = kQ + QT * kQTile, kV = kK + NST * kStage, kX = kV + NST * kStage;
+  static constexpr int kQ = kHeader, kK = kQ + QT * kQTile, kV = kK + NST * kStageK, kX = kV + NST * kStageV;
   // kX: the extra k16 step, 32 bytes of each of 128 rows: K's stages in the first two columns, Q's tiles in the others
   static constexpr int kSmem = kX + 128 * 128 + 1024;
-  static_assert(kSmem <= 227 * 1024 && NST * BN <= 256, "shared memory");
+  static_assert(kSmem <= 227 * 1024 && NST * BK <= 256, "shared memory");
+  static_assert(!kQTmem || NST * kStageK >= 128 * D * 2, "room for a tile of o");
   // 16-byte pieces and rows of a stage's extra columns
-  static constexpr int x_piece(int stage) { return BN == 128 ? 2 * stage : stage & 2; }
-  static constexpr int x_row(int stage) { return BN == 128 ? 0 : 64 * (stage & 1); }
+  static constexpr int x_piece(int stage) { return 2 * (stage / (128 / BK)); }
+  static constexpr int x_row(int stage) { return BK * (stage % (128 / BK)); }
   static constexpr int kFirstK = 4 * QT, kFirstV = kFirstK + 4, kMma = kFirstV + 4;  // the roles' first warps
   static constexpr int kThreads = 32 * (kMma + 4);
   // registers per thread: what a block of kThreads gets, and after the split the
@@ -309,40 +354,43 @@ struct Rows {
 };
 
 // shared-memory stores of this warp, to the MMAs
-__device__ __forceinline__ void publish_smem(uint64_t *bar, int lane) {
+template <int CG>
+__device__ __forceinline__ void publish_smem(uint64_t *bar, int lane, int rank) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
+  if (lane == 0) arrive_lead<CG>(bar, rank);
 }
 
-// One warp's share of the expansion of K or V: of every tile, W blocks of 16 tokens, numbered m = 0, 1, ... through all
-// tiles.
+// One warp's share of the expansion of K or V, in units numbered through all tiles.
 template <int D, int GS>
 struct Expander {
   using C = Prefill<D, GS>;
-  static constexpr int G = C::G, W = C::BN / 64, KW = D / 32, VM = D / 64;
+  static constexpr int G = C::G, KW = D / 32;
   const KvView &c;
   int64_t b;
-  int hk, warp, lane, first, blocks;
+  int hk, warp, lane, rank, first, tiles;
   Exponents exps;
-  __device__ __forceinline__ int pos(int m) const { return first + m / W * C::BN + 16 * (W * warp + m % W); }
-  __device__ __forceinline__ int page_of(int m) const { return m < blocks ? c.page(b, pos(m)) : -1; }
-  __device__ __forceinline__ const unsigned char *block(int page, int m) const {
+  __device__ __forceinline__ int page_of(int p, bool in) const { return in ? c.page(b, p) : -1; }
+  __device__ __forceinline__ const unsigned char *block(int page, int p) const {
     const int per = 1 << (c.page_shift - 4);
-    return c.data + (((int64_t)page * c.HK + hk) * per + ((pos(m) >> 4) & (per - 1))) * C::kBlock;
+    return c.data + (((int64_t)page * c.HK + hk) * per + ((p >> 4) & (per - 1))) * C::kBlock;
   }
 
-  // ---- K: half a block at a time, a token for four lanes: lane t mod 4 has channels 32 j + 8 t .. + 7 of token
-  // lane / 8 + (lane & 4), so that 8 lanes store to 8 different banks
+  // ---- K: half a block at a time, HK of them per tile and warp; a token for four lanes: lane t mod 4 has channels
+  // 32 j + 8 t .. + 7 of token lane / 8 + (lane & 4), so that 8 lanes store to 8 different banks
+  static constexpr int HK = C::BK / 32;
   struct KHalf {
     uint32_t code[KW], meta[G];
     bool have;
   };
   __device__ __forceinline__ int token() const { return (lane >> 3) + (lane & 4); }
-  __device__ __forceinline__ void fetch_k(const unsigned char *p, bool have, int half, KHalf &r) const {
-    r.have = have;
-    if (!have) return;
-    const int t = token() + 8 * half;
+  __device__ __forceinline__ int k_half(int v) const { return HK * warp + v % HK; }  // of this CTA's in the tile
+  __device__ __forceinline__ int k_pos(int v) const { return first + v / HK * C::BN + rank * C::BK + (k_half(v) & ~1) * 8; }
+  __device__ __forceinline__ void fetch_k(int v, int page, KHalf &r) const {
+    r.have = page >= 0;
+    if (!r.have) return;
+    const unsigned char *p = block(page, k_pos(v));
+    const int t = token() + 8 * (k_half(v) & 1);
     if constexpr (D == 64) {
       ldg_words(p + t * 32 + 8 * (lane & 3), r.code);
     } else {
@@ -356,9 +404,8 @@ struct Expander {
     }
     ldg_words(p + 8 * D + t * G * 4, r.meta);
   }
-  // scale q into the tile at `dst`, the biases (twice) into the extra columns; both addresses are this lane's, of the
-  // first half block's row
-  __device__ __forceinline__ void put_k(const KHalf &r, int half, uint32_t dst, uint32_t extra) const {
+  // scale q into the tile, the biases (twice) into the extra columns; both addresses are this lane's
+  __device__ __forceinline__ void put_k(const KHalf &r, uint32_t dst, uint32_t extra) const {
     __half2 s[G], o[G];
     uint32_t e[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -371,75 +418,76 @@ struct Expander {
       __half2 v[4];
       expand(r.code[j], exps, v);
       const __half2 f = s[32 * j / GS];
-      sts4((j & 1 ? dst ^ 64 : dst) + (j >> 1) * C::kBox + half * 1024, bits(__hmul2(v[0], f)), bits(__hmul2(v[1], f)),
-           bits(__hmul2(v[2], f)), bits(__hmul2(v[3], f)));
+      sts4((j & 1 ? dst ^ 64 : dst) + (j >> 1) * C::kBoxK, bits(__hmul2(v[0], f)), bits(__hmul2(v[1], f)), bits(__hmul2(v[2], f)),
+           bits(__hmul2(v[3], f)));
     }
     // lane 0 of a token the biases, lane 1 the 17th column: -inf for a token without a page
     if (lane & 1) {
       e[0] = r.have ? 0u : 0x0000FC00u;
       e[1] = e[2] = e[3] = 0u;
     }
-    if ((lane & 2) == 0) sts4(extra + half * 1024, e[0], e[1], e[2], e[3]);
+    if ((lane & 2) == 0) sts4(extra, e[0], e[1], e[2], e[3]);
   }
   __device__ __forceinline__ void run_k(Bars *bars, uint32_t sm) const {
     KHalf r0, r1;
-    int page = page_of(0), ahead = page_of(1);
-    const unsigned char *p = block(max(page, 0), 0);
-    fetch_k(p, page >= 0, 0, r0);
-    fetch_k(p, page >= 0, 1, r1);
-    const uint32_t to = sm + C::kK + swz(16 * W * warp + token(), lane & 3);
+    const int units = tiles * HK;
+    auto page = [&](int v) { return page_of(k_pos(v), v < units); };
+    fetch_k(0, page(0), r0);
+    fetch_k(1, page(1), r1);
+    int ahead = page(2);
     uint32_t s = 0, ph = 1;
-#pragma unroll 1
-    for (int m = 0; m < blocks; ++m) {
-      if (m % W == 0 && !wait_warp(&bars->k_empty[s], ph, bars)) break;
-      const uint32_t dst = to + s * C::kStage + (m % W) * 2048,
-                     extra = sm + C::kX + swz(C::x_row(s) + 16 * (W * warp + m % W) + token(), C::x_piece(s) + (lane & 1));
-      page = ahead;
-      ahead = page_of(m + 2);
-      p = block(max(page, 0), m + 1);
-      put_k(r0, 0, dst, extra);
-      fetch_k(p, page >= 0, 0, r0);
-      put_k(r1, 1, dst, extra);
-      fetch_k(p, page >= 0, 1, r1);
-      if (m % W == W - 1) {
-        publish_smem(&bars->k_full[s], lane);
+    auto step = [&](int v, KHalf &r) {
+      if (v % HK == 0 && !wait_warp(&bars->k_empty[s], ph, bars)) return false;
+      const int row = 8 * k_half(v) + token();
+      put_k(r, sm + C::kK + s * C::kStageK + swz(row, lane & 3), sm + C::kX + swz(C::x_row(s) + row, C::x_piece(s) + (lane & 1)));
+      const int next = ahead;
+      ahead = page(v + 3);
+      if (v % HK == HK - 1) {
+        publish_smem<C::CG>(&bars->k_full[s], lane, rank);
         if (++s == C::NST) {
           s = 0;
           ph ^= 1;
         }
       }
-    }
+      fetch_k(v + 2, next, r);
+      return true;
+    };
+#pragma unroll 1
+    for (int v = 0; v < units; v += 2)
+      if (!step(v, r0) || (v + 1 < units && !step(v + 1, r1))) break;
   }
 
-  // ---- V: 64 channels of a block for a half warp, parts numbered through all tiles (NP per tile).  Lane l mod 16 has
-  // words 2 (l mod 4) and the next, tokens 2t, 2t + 1, 2t + 8, 2t + 9 with t = l / 4; where t is odd the words change
-  // places, again for the banks.
-  static constexpr int NP = W * VM / 2;
+  // ---- V: 64 channels of a block, VI of them per tile and warp.  Where there are two, a half warp has one each, words
+  // 2 (l mod 4) and the next of tokens 2t, 2t + 1, 2t + 8, 2t + 9, t = l / 4 mod 4, and where t is odd the words change places,
+  // again for the banks; else lane l has word l mod 8, t = l / 8.
+  static constexpr int VI = C::BN / 16 * (C::DV / 64) / 4, VW = VI;
+  static_assert(VI == 1 || VI == 2, "parts of V");
   struct VPart {
-    uint4 code[2];
+    uint4 code[VW];
     uint32_t meta[4];
     bool have;
   };
-  __device__ __forceinline__ int v_time() const { return (lane >> 2) & 3; }
-  __device__ __forceinline__ int v_piece(int w) const { return 2 * (lane & 3) + (w ^ ((lane >> 2) & 1)); }
-  __device__ __forceinline__ int v_item(int v) const { return 2 * (v % NP) + (lane >> 4); }  // 64 channels v_item % VM of block v_item / VM
-  __device__ __forceinline__ int v_block(int v) const { return v / NP * W + v_item(v) / VM; }
-  __device__ __forceinline__ void fetch_v(int v, int page, VPart &r) const {
+  __device__ __forceinline__ int v_block() const { return C::DV == 64 ? VI * warp + (VI == 2 ? lane >> 4 : 0) : warp; }
+  __device__ __forceinline__ int v_group() const { return C::DV == 64 ? 0 : lane >> 4; }  // of this CTA's 64 channels
+  __device__ __forceinline__ int v_time() const { return VI == 2 ? (lane >> 2) & 3 : lane >> 3; }
+  __device__ __forceinline__ int v_piece(int w) const { return VI == 2 ? 2 * (lane & 3) + (w ^ ((lane >> 2) & 1)) : lane & 7; }
+  __device__ __forceinline__ int v_pos(int i) const { return first + i * C::BN + 16 * v_block(); }
+  __device__ __forceinline__ void fetch_v(int i, int page, VPart &r) const {
     r.have = page >= 0;
     if (!r.have) return;
-    const int g = v_item(v) % VM, t = v_time();
-    const unsigned char *p = block(page, v_block(v)) + 8 * D + 64 * G;
+    const int g = rank * (C::DV / 64) + v_group(), t = v_time();
+    const unsigned char *p = block(page, v_pos(i)) + 8 * D + 64 * G;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) r.code[w] = __ldg(reinterpret_cast<const uint4 *>(p + (8 * g + v_piece(w)) * 64 + 16 * t));
+    for (int w = 0; w < VW; ++w) r.code[w] = __ldg(reinterpret_cast<const uint4 *>(p + (8 * g + v_piece(w)) * 64 + 16 * t));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       r.meta[j] = __ldg(reinterpret_cast<const uint32_t *>(p + 8 * D) + (2 * t + (j & 1) + 8 * (j >> 1)) * G + 64 * g / GS);
   }
   // scale q + bias; tokens with values beyond fp16 become 0, which no P of 0 turns into NaN, and are reported if they are
   // among the first `left` of the tile, the sequence's own
-  __device__ __forceinline__ bool put_v(int v, const VPart &r, uint32_t dst, int left) const {
-    const int row0 = 16 * (W * warp + v_item(v) / VM) + 2 * v_time();
-    dst += v_item(v) % VM * C::kBox;
+  __device__ __forceinline__ bool put_v(const VPart &r, uint32_t dst, int left) const {
+    const int row0 = 16 * v_block() + 2 * v_time();
+    dst += v_group() * C::kBoxV;
     bool bad = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -449,7 +497,7 @@ struct Expander {
       __half2 s, o;
       split_meta(r.have && !out ? r.meta[j] : 0u, s, o);
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < VW; ++w) {
         const uint4 &u = r.code[w];
         __half2 h[4];
         expand(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, exps, h);
@@ -461,31 +509,27 @@ struct Expander {
   }
   __device__ __forceinline__ void run_v(Bars *bars, uint32_t sm, int len) const {
     VPart r0, r1;
-    const int parts = blocks / W * NP;
-    auto page_of_part = [&](int v) { return v < parts ? page_of(v_block(v)) : -1; };
-    fetch_v(0, page_of_part(0), r0);
-    fetch_v(1, page_of_part(1), r1);
-    int ahead = page_of_part(2);
+    auto page = [&](int i) { return page_of(v_pos(i), i < tiles); };
+    fetch_v(0, page(0), r0);
+    fetch_v(1, page(1), r1);
+    int ahead = page(2);
     uint32_t s = 0, ph = 1;
-    auto step = [&](int v, VPart &r) {
-      const int i = v / NP;
-      if (v % NP == 0 && !wait_warp(&bars->v_empty[s], ph, bars)) return false;
-      const int page = ahead;
-      ahead = page_of_part(v + 3);
-      if (put_v(v, r, sm + C::kV + s * C::kStage, len - first - i * C::BN)) bars->bad_v = 1;
-      fetch_v(v + 2, page, r);
-      if (v % NP == NP - 1) {
-        publish_smem(&bars->v_full[s], lane);
-        if (++s == C::NST) {
-          s = 0;
-          ph ^= 1;
-        }
+    auto step = [&](int i, VPart &r) {
+      if (!wait_warp(&bars->v_empty[s], ph, bars)) return false;
+      if (put_v(r, sm + C::kV + s * C::kStageV, len - first - i * C::BN)) bars->bad_v = 1;
+      const int next = ahead;
+      ahead = page(i + 3);
+      publish_smem<C::CG>(&bars->v_full[s], lane, rank);
+      if (++s == C::NST) {
+        s = 0;
+        ph ^= 1;
       }
+      fetch_v(i + 2, next, r);
       return true;
     };
 #pragma unroll 1
-    for (int v = 0; v < parts; v += 2)
-      if (!step(v, r0) || (v + 1 < parts && !step(v + 1, r1))) break;
+    for (int i = 0; i < tiles; i += 2)
+      if (!step(i, r0) || (i + 1 < tiles && !step(i + 1, r1))) break;
   }
 };
 
@@ -613,21 +657,22 @@ template <typename T, int D, int GS>
 __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kernel(const KvView c, const KvAttention a, int tiles) {
   using C = Prefill<D, GS>;
   using X = Expander<D, GS>;
-  constexpr int G = C::G, QT = C::QT, BN = C::BN;
+  constexpr int G = C::G, QT = C::QT, BN = C::BN, CG = C::CG;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Bars *bars = reinterpret_cast<Bars *>(base);
   const uint32_t sm = smem_u32(base);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // the last tiles first: they see the most
-  int64_t id = blockIdx.x;
+  const int rank = blockIdx.x % CG;  // in the pair
+  int64_t id = blockIdx.x / CG;
   const int64_t heads = c.B * c.HK;
   const int tile0 = tiles - 1 - (int)(id / heads);
   id %= heads;
   const int hk = (int)(id % c.HK), r = a.HQ / c.HK;
   const int64_t b = id / c.HK;
   Rows rows;
-  if (!rows.set<C::kRows, BN>(c, a, b, tile0)) return;
+  if (!rows.set<CG * C::kRows, BN>(c, a, b, tile0)) return;
 
   auto init = [&](bool again) {
     if (tid == 0) {
@@ -635,16 +680,16 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
         for (uint64_t *bar = bars->k_full; bar <= &bars->drain; ++bar)
           asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
       for (int s = 0; s < 4; ++s) {
-        mbar_init(&bars->k_full[s], 4);
-        mbar_init(&bars->v_full[s], 4);
+        mbar_init(&bars->k_full[s], 4 * CG);
+        mbar_init(&bars->v_full[s], 4 * CG);
         mbar_init(&bars->k_empty[s], 1);
         mbar_init(&bars->v_empty[s], 1);
         mbar_init(&bars->s_full[s], 1);
-        mbar_init(&bars->p_ready[s], 4);
+        mbar_init(&bars->p_ready[s], 4 * CG);
       }
       mbar_init(&bars->o_done[0], 1);
       mbar_init(&bars->o_done[1], 1);
-      mbar_init(&bars->q_full, 4 * QT);
+      mbar_init(&bars->q_full, 4 * QT * CG);
       mbar_init(&bars->drain, 1);
       bars->bad_v = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -653,12 +698,13 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
   if (tid == 0) bars->abort_flag = 0;
   init(false);
   if (warp == C::kMma) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(512)
+    asm volatile("tcgen05.alloc.cta_group::%2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(512),
+                 "n"(CG)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::%0.sync.aligned;" ::"n"(CG) : "memory");
   }
   fence_before();
-  __syncthreads();
+  sync_all<CG>();
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
@@ -666,12 +712,14 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
   // and meets the others at the end of each; false: no other tile.
   auto next = [&](int &tile) -> bool {
     fence_before();
-    __syncthreads();
+    sync_all<CG>();
     fence_after();
     tile += tiles;
-    if (bars->abort_flag || !rows.set<C::kRows, BN>(c, a, b, tile)) return false;
+    const bool more = !any_flag<CG>(&bars->abort_flag) && rows.set<CG * C::kRows, BN>(c, a, b, tile);
+    if (CG > 1) sync_all<CG>();  // (each has read the other's flag)
+    if (!more) return false;
     init(true);
-    __syncthreads();
+    sync_all<CG>();
     return true;
   };
 
@@ -682,17 +730,18 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16), to = tl + 256 + D * q;
     int tile = tile0;
     do {
-      const int mine = tile * C::kRows + 128 * q + 32 * quarter + lane, row = min(mine, rows.rows - 1);
+      const int row0 = CG * (tile * C::kRows + 128 * q) + 128 * rank + 32 * quarter;  // this warp's rows
+      const int mine = row0 + lane, row = min(mine, rows.rows - 1);
       const int64_t tok = rows.t0 + row / r;
       const int head = hk * r + row % r, pos = rows.pos0 + row / r;
       const int hi = pos < 0 ? -1 : a.causal ? pos : rows.len - 1, lo = a.window ? max(pos, 0) - a.window : -1;  // lo < j <= hi is seen
       const int hi_all = __reduce_min_sync(0xffffffffu, hi), lo_all = __reduce_max_sync(0xffffffffu, lo);
-      const float f = load_q<T, D, GS>(a, rows, sm, tl, tile * C::kRows + 128 * q + 32 * quarter, hk, r, q, 32 * quarter, lane);
+      const float f = load_q<T, D, GS>(a, rows, sm, tl, row0, hk, r, q, 32 * quarter, lane);
       if constexpr (C::kQTmem) {
         wait_st();
         fence_before();
       }
-      publish_smem(&bars->q_full, lane);
+      publish_smem<CG>(&bars->q_full, lane, rank);
       float M = kNone, L = 0.f;
       bool ok = true;
       for (int i = 0; i < rows.tiles; ++i) {
@@ -790,14 +839,14 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
         wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_ready[buf]);
+        if (lane == 0) arrive_lead<CG>(&bars->p_ready[buf], rank);
       }
       // O's last product.  With two buffers of S per row tile the last two may be open (S of a tile only says that the
       // product two tiles before is complete), and o_done's parity cannot tell them apart: all MMAs, then.
       if (ok && rows.tiles > 0) ok = C::NB == QT ? wait_warp(&bars->o_done[q], (rows.tiles - 1) & 1, bars) : wait_warp(&bars->drain, 0, bars);
       fence_after();
       float inv = L == 0.f ? 0.f : 1.f / L;
-      if (ok && bars->bad_v) {
+      if (ok && any_flag<CG>(&bars->bad_v)) {
         // rows that see such a token become NaN
         for (int p = max(lo + 1, 0); p <= min(hi, (int)min((int64_t)rows.len, c.table_width << c.page_shift) - 1); ++p) {
           const int page = c.page(b, p);
@@ -846,7 +895,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
 #pragma unroll 4
       for (int n = 0; n < kPieces; ++n) {
         const int from = n * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;  // row of the warp, piece of the row
-        const int other = tile * C::kRows + 128 * q + 32 * quarter + from;
+        const int other = row0 + from;
         uint4 w;
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
@@ -862,7 +911,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     if constexpr (C::kRegX < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegX));
     int tile = tile0;
     do {
-      const X x{c, b, hk, warp & 3, lane, rows.first, c_kv_stall ? 0 : rows.tiles * X::W};
+      const X x{c, b, hk, warp & 3, lane, rank, rows.first, c_kv_stall ? 0 : rows.tiles};
       if (warp < C::kFirstV) x.run_k(bars, sm);
       else x.run_v(bars, sm, rows.len);
     } while (next(tile));
@@ -872,28 +921,28 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     do {
       if (warp == C::kMma) {
         // ---------------- the MMAs: S of row tile q over the tile i, O of it
-        if (elect_one()) {
+        if (rank == 0 && elect_one()) {
           const int n = rows.tiles;
           bool ok = wait_one(&bars->q_full, 0, bars);
-          const uint32_t q0 = desc_k(sm + C::kQ), k0 = desc_k(sm + C::kK), v0 = desc_mn(sm + C::kV, C::kBox), x0 = desc_k(sm + C::kX);
+          const uint32_t q0 = desc_k(sm + C::kQ), k0 = desc_k(sm + C::kK), v0 = desc_mn(sm + C::kV, C::kBoxV), x0 = desc_k(sm + C::kX);
           uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stages and their phases
           auto scores = [&](int u) {
             const int q = u % QT, buf = u % C::NB;
             if (q == 0 && !wait_one(&bars->k_full[ks], kph, bars)) return false;
             fence_after();
             const uint32_t d = tmem + C::kS * buf;
-            uint32_t qa = C::kQTmem ? tmem + 128 : q0 + q * (C::kQTile / 16), kb = k0 + ks * (C::kStage / 16);
+            uint32_t qa = C::kQTmem ? tmem + 128 : q0 + q * (C::kQTile / 16), kb = k0 + ks * (C::kStageK / 16);
 #pragma unroll 1
-            for (int k = 0; k < D / 64; ++k, qa += C::kQTmem ? 32 : 128 * 128 / 16, kb += C::kBox / 16)
+            for (int k = 0; k < D / 64; ++k, qa += C::kQTmem ? 32 : 128 * 128 / 16, kb += C::kBoxK / 16)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                if constexpr (C::kQTmem) umma_ts(d, qa + 8 * j, kb + 2 * j, idesc(128, BN, false), k > 0 || j > 0);
-                else umma_ss(d, qa + 2 * j, kb + 2 * j, idesc(128, BN, false), k > 0 || j > 0);
+                if constexpr (C::kQTmem) umma_ts<CG>(d, qa + 8 * j, kb + 2 * j, idesc(128 * CG, BN, false), k > 0 || j > 0);
+                else umma_ss<CG>(d, qa + 2 * j, kb + 2 * j, idesc(128 * CG, BN, false), k > 0 || j > 0);
               }
-            umma_ss(d, x0 + 4 + 2 * q, x0 + C::x_row(ks) * 8 + C::x_piece(ks), idesc(128, BN, false), true);
-            umma_commit(&bars->s_full[buf]);
+            umma_ss<CG>(d, x0 + 4 + 2 * q, x0 + C::x_row(ks) * 8 + C::x_piece(ks), idesc(128 * CG, BN, false), true);
+            umma_commit<CG>(&bars->s_full[buf]);
             if (q == QT - 1) {
-              umma_commit(&bars->k_empty[ks]);
+              umma_commit<CG>(&bars->k_empty[ks]);
               if (++ks == C::NST) {
                 ks = 0;
                 kph ^= 1;
@@ -909,15 +958,15 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
             if (q == 0 && !(ok = wait_one(&bars->v_full[vs], vph, bars))) break;
             if (!(ok = wait_one(&bars->p_ready[buf], u / C::NB & 1, bars))) break;
             fence_after();
-            uint32_t p = tmem + C::kS * buf, vb = v0 + vs * (C::kStage / 16);
+            uint32_t p = tmem + C::kS * buf, vb = v0 + vs * (C::kStageV / 16);
 #pragma unroll 1
             for (int k = 0; k < BN / 64; ++k, p += 32, vb += 4 * 2048 / 16)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                umma_ts(tmem + 256 + D * q, p + 8 * j, vb + j * (2048 / 16), idesc(128, D, true), u >= QT || k > 0 || j > 0);
-            umma_commit(&bars->o_done[q]);
+                umma_ts<CG>(tmem + 256 + D * q, p + 8 * j, vb + j * (2048 / 16), idesc(128 * CG, D, true), u >= QT || k > 0 || j > 0);
+            umma_commit<CG>(&bars->o_done[q]);
             if (q == QT - 1) {
-              umma_commit(&bars->v_empty[vs]);
+              umma_commit<CG>(&bars->v_empty[vs]);
               if (++vs == C::NST) {
                 vs = 0;
                 vph ^= 1;
@@ -926,7 +975,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
             // P's place is free for other scores
             if (u + C::NB < units) ok = scores(u + C::NB);
           }
-          umma_commit(&bars->drain);  // every MMA issued, complete before their memory is used again
+          umma_commit<CG>(&bars->drain);  // every MMA issued, complete before their memory is used again
         }
         __syncwarp();
         const unsigned long long since = global_ns();
@@ -935,7 +984,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       }
     } while (next(tile));
   }
-  if (warp == C::kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (warp == C::kMma) asm volatile("tcgen05.dealloc.cta_group::%2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512), "n"(CG));
 }
 
 template <typename T, int D, int GS>
@@ -954,10 +1003,21 @@ cudaError_t run(const KvView &c, const KvAttention &a, cudaStream_t st) {
     mark_done(ready, dev);
   }
   const int r = a.HQ / c.HK;
-  const int64_t tiles = (std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + C::kRows - 1) / C::kRows, ctas = tiles * c.B * c.HK;
+  const int64_t tiles = (std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + C::CG * C::kRows - 1) / (C::CG * C::kRows),
+                ctas = tiles * c.B * c.HK * C::CG;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  kv_prefill_kernel<T, D, GS><<<(unsigned)ctas, C::kThreads, C::kSmem, st>>>(c, a, (int)tiles);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C::CG;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = C::CG > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<T, D, GS>, c, a, (int)tiles);
 }
 template <typename T>
 cudaError_t run_t(const KvView &c, const KvAttention &a, cudaStream_t st) {
