@@ -682,15 +682,15 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       for (int s = 0; s < 4; ++s) {
         mbar_init(&bars->k_full[s], 4 * CG);
         mbar_init(&bars->v_full[s], 4 * CG);
-        mbar_init(&bars->k_empty[s], 1);
-        mbar_init(&bars->v_empty[s], 1);
+        mbar_init(&bars->k_empty[s], QT);
+        mbar_init(&bars->v_empty[s], QT);
         mbar_init(&bars->s_full[s], 1);
         mbar_init(&bars->p_ready[s], 4 * CG);
       }
       mbar_init(&bars->o_done[0], 1);
       mbar_init(&bars->o_done[1], 1);
       mbar_init(&bars->q_full, 4 * QT * CG);
-      mbar_init(&bars->drain, 1);
+      mbar_init(&bars->drain, QT);
       bars->bad_v = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -919,19 +919,23 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     if constexpr (C::kRegM < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegM));
     int tile = tile0;
     do {
-      if (warp == C::kMma) {
-        // ---------------- the MMAs: S of row tile q over the tile i, O of it
+      const int q = warp - C::kMma;
+      if (q < QT) {
+        // ---------------- the MMAs of row tile q: S over the tile i, O of it.  A thread per row tile: an issue takes 20 to
+        // 40 clocks and a wait on a barrier 80 to 180, also where it holds already, so that one thread for both kept the
+        // tensor cores waiting.
         if (rank == 0 && elect_one()) {
           const int n = rows.tiles;
           bool ok = wait_one(&bars->q_full, 0, bars);
-          const uint32_t q0 = desc_k(sm + C::kQ), k0 = desc_k(sm + C::kK), v0 = desc_mn(sm + C::kV, C::kBoxV), x0 = desc_k(sm + C::kX);
-          uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // stages and their phases
-          auto scores = [&](int u) {
-            const int q = u % QT, buf = u % C::NB;
-            if (q == 0 && !wait_one(&bars->k_full[ks], kph, bars)) return false;
+          const uint32_t q0 = C::kQTmem ? tmem + 128 : desc_k(sm + C::kQ + q * C::kQTile), k0 = desc_k(sm + C::kK),
+                         v0 = desc_mn(sm + C::kV, C::kBoxV), x0 = desc_k(sm + C::kX), o = tmem + 256 + D * q;
+          constexpr int kAhead = C::NB / QT;  // buffers of S of a row tile
+          auto scores = [&](int i) {
+            const int s = i % C::NST, buf = QT * (i % kAhead) + q;
+            if (!wait_one(&bars->k_full[s], i / C::NST & 1, bars)) return false;
             fence_after();
             const uint32_t d = tmem + C::kS * buf;
-            uint32_t qa = C::kQTmem ? tmem + 128 : q0 + q * (C::kQTile / 16), kb = k0 + ks * (C::kStageK / 16);
+            uint32_t qa = q0, kb = k0 + s * (C::kStageK / 16);
 #pragma unroll 1
             for (int k = 0; k < D / 64; ++k, qa += C::kQTmem ? 32 : 128 * 128 / 16, kb += C::kBoxK / 16)
 #pragma unroll
@@ -939,41 +943,28 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
                 if constexpr (C::kQTmem) umma_ts<CG>(d, qa + 8 * j, kb + 2 * j, idesc(128 * CG, BN, false), k > 0 || j > 0);
                 else umma_ss<CG>(d, qa + 2 * j, kb + 2 * j, idesc(128 * CG, BN, false), k > 0 || j > 0);
               }
-            umma_ss<CG>(d, x0 + 4 + 2 * q, x0 + C::x_row(ks) * 8 + C::x_piece(ks), idesc(128 * CG, BN, false), true);
+            umma_ss<CG>(d, x0 + 4 + 2 * q, x0 + C::x_row(s) * 8 + C::x_piece(s), idesc(128 * CG, BN, false), true);
             umma_commit<CG>(&bars->s_full[buf]);
-            if (q == QT - 1) {
-              umma_commit<CG>(&bars->k_empty[ks]);
-              if (++ks == C::NST) {
-                ks = 0;
-                kph ^= 1;
-              }
-            }
+            umma_commit<CG>(&bars->k_empty[s]);
             return true;
           };
-          const int units = n * QT;
-          for (int u = 0; ok && u < C::NB && u < units; ++u) ok = scores(u);
+          for (int i = 0; ok && i < kAhead && i < n; ++i) ok = scores(i);
 #pragma unroll 1
-          for (int u = 0; ok && u < units; ++u) {
-            const int q = u % QT, buf = u % C::NB;
-            if (q == 0 && !(ok = wait_one(&bars->v_full[vs], vph, bars))) break;
-            if (!(ok = wait_one(&bars->p_ready[buf], u / C::NB & 1, bars))) break;
+          for (int i = 0; ok && i < n; ++i) {
+            const int s = i % C::NST, buf = QT * (i % kAhead) + q;
+            if (!(ok = wait_one(&bars->v_full[s], i / C::NST & 1, bars))) break;
+            if (!(ok = wait_one(&bars->p_ready[buf], i / kAhead & 1, bars))) break;
             fence_after();
-            uint32_t p = tmem + C::kS * buf, vb = v0 + vs * (C::kStageV / 16);
+            uint32_t p = tmem + C::kS * buf, vb = v0 + s * (C::kStageV / 16);
 #pragma unroll 1
             for (int k = 0; k < BN / 64; ++k, p += 32, vb += 4 * 2048 / 16)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                umma_ts<CG>(tmem + 256 + D * q, p + 8 * j, vb + j * (2048 / 16), idesc(128 * CG, D, true), u >= QT || k > 0 || j > 0);
+                umma_ts<CG>(o, p + 8 * j, vb + j * (2048 / 16), idesc(128 * CG, D, true), i > 0 || k > 0 || j > 0);
             umma_commit<CG>(&bars->o_done[q]);
-            if (q == QT - 1) {
-              umma_commit<CG>(&bars->v_empty[vs]);
-              if (++vs == C::NST) {
-                vs = 0;
-                vph ^= 1;
-              }
-            }
+            umma_commit<CG>(&bars->v_empty[s]);
             // P's place is free for other scores
-            if (u + C::NB < units) ok = scores(u + C::NB);
+            if (i + kAhead < n) ok = scores(i + kAhead);
           }
           umma_commit<CG>(&bars->drain);  // every MMA issued, complete before their memory is used again
         }
