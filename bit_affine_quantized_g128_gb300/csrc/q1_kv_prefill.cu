@@ -68,17 +68,48 @@ __device__ __forceinline__ unsigned long long global_ns() {
   return t;
 }
 
+// A CTA's rows: those of `tile` of sequence b, and the positions that any of them sees.
+struct Rows {
+  int64_t t0;
+  int rows, len, pos0, first, tiles;  // rows of the sequence, its tokens, position of its first row; first position, number of tiles
+  template <int ROWS, int BN>
+  __device__ __forceinline__ bool set(const KvView &c, const KvAttention &a, int64_t b, int tile) {
+    int64_t t1;
+    c.range(b, t0, t1);
+    const int r = a.HQ / c.HK, n = (int)(t1 - t0);
+    const int64_t all = (int64_t)n * r;
+    if ((int64_t)tile * ROWS >= all) return false;
+    rows = (int)all;
+    len = max(c.lengths[b], 0);
+    pos0 = len - n;
+    const int row0 = tile * ROWS, row1 = min(row0 + ROWS, rows) - 1;
+    int end = a.causal ? pos0 + row1 / r + 1 : (pos0 + row1 / r < 0 ? 0 : len);
+    end = (int)min((int64_t)end, c.table_width << c.page_shift);
+    const int begin = a.window ? (int)max((int64_t)pos0 + row0 / r - a.window + 1, (int64_t)0) : 0;
+    first = begin / BN * BN;
+    tiles = end > begin ? (end - first + BN - 1) / BN : 0;
+    return true;
+  }
+  __device__ __forceinline__ void put(const Rows &x) volatile {
+    t0 = x.t0, rows = x.rows, len = x.len, pos0 = x.pos0, first = x.first, tiles = x.tiles;
+  }
+  __device__ __forceinline__ Rows get() const volatile { return {t0, rows, len, pos0, first, tiles}; }
+};
+
 struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[4], p_ready[4], o_done[2], q_full, drain;
   uint32_t tmem_base;
+  volatile Rows rows;              // here, as no role has registers to keep all of it
+  volatile int tile;
   volatile int abort_flag, bad_v;  // a wait ran out; V has values beyond fp16
 };
 
-// Whether a wait gives up: its limit has run out, or another role has given up.
-__device__ __noinline__ bool give_up(Bars *bars, unsigned long long since) {
+// Whether a wait gives up: its limit has run out, or another role has given up.  The clock is read on every 64th try only (a
+// read takes hundreds of cycles), the first time to start it.
+__device__ __noinline__ bool give_up(Bars *bars, unsigned long long since, unsigned long long now) {
   if (bars->abort_flag) return true;
-  if (global_ns() - since <= c_kv_wait_ns) return false;
+  if (now - since <= c_kv_wait_ns) return false;
   bars->abort_flag = 1;
   atomicOr(&g_kv_err, 1u);
   return true;
@@ -86,24 +117,28 @@ __device__ __noinline__ bool give_up(Bars *bars, unsigned long long since) {
 // Bounded wait of a whole warp; one verdict for all its lanes.
 __device__ __forceinline__ bool wait_warp(uint64_t *b, uint32_t parity, Bars *bars) {
   bool ok = mbar_try(b, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  const unsigned long long since = global_ns();
-  for (uint32_t i = 1;; ++i) {
+  unsigned long long since = 0;
+  for (uint32_t i = 1; !__all_sync(0xffffffffu, ok); ++i) {
     ok = ok || mbar_try(b, parity);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    if ((i & 31u) == 0 && __any_sync(0xffffffffu, give_up(bars, since))) return false;
+    if ((i & 63u) == 0) {
+      const unsigned long long now = global_ns();
+      if (i == 64) since = now;
+      if (__any_sync(0xffffffffu, give_up(bars, since, now))) return false;
+    }
   }
+  return true;
 }
 // the same for one thread
 __device__ __forceinline__ bool wait_one(uint64_t *b, uint32_t parity, Bars *bars) {
-  if (mbar_try(b, parity)) return true;
-  const unsigned long long since = global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try(b, parity)) return true;
-    if ((i & 31u) == 0 && give_up(bars, since)) return false;
-  }
+  unsigned long long since = 0;
+  for (uint32_t i = 1; !mbar_try(b, parity); ++i)
+    if ((i & 63u) == 0) {
+      const unsigned long long now = global_ns();
+      if (i == 64) since = now;
+      if (give_up(bars, since, now)) return false;
+    }
+  return true;
 }
-
 // Operands of 128-byte rows, the 16-byte pieces of row r exchanged by XOR with r mod 8,
 // 8-row groups 1024 bytes apart: the low word of a descriptor, with rows along M or N and the contraction
 // along the row, or with rows along the contraction and 64-column boxes `box` bytes apart
@@ -328,30 +363,6 @@ struct Prefill {
   static constexpr int kS = BN;
 };
 static_assert(sizeof(Bars) <= 1024, "header");
-
-// A CTA's rows: those of `tile` of sequence b, and the positions that any of them sees.
-struct Rows {
-  int64_t t0;
-  int rows, len, pos0, first, tiles;  // rows of the sequence, its tokens, position of its first row; first position, number of tiles
-  template <int ROWS, int BN>
-  __device__ __forceinline__ bool set(const KvView &c, const KvAttention &a, int64_t b, int tile) {
-    int64_t t1;
-    c.range(b, t0, t1);
-    const int r = a.HQ / c.HK, n = (int)(t1 - t0);
-    const int64_t all = (int64_t)n * r;
-    if ((int64_t)tile * ROWS >= all) return false;
-    rows = (int)all;
-    len = max(c.lengths[b], 0);
-    pos0 = len - n;
-    const int row0 = tile * ROWS, row1 = min(row0 + ROWS, rows) - 1;
-    int end = a.causal ? pos0 + row1 / r + 1 : (pos0 + row1 / r < 0 ? 0 : len);
-    end = (int)min((int64_t)end, c.table_width << c.page_shift);
-    const int begin = a.window ? (int)max((int64_t)pos0 + row0 / r - a.window + 1, (int64_t)0) : 0;
-    first = begin / BN * BN;
-    tiles = end > begin ? (end - first + BN - 1) / BN : 0;
-    return true;
-  }
-};
 
 // shared-memory stores of this warp, to the MMAs
 template <int CG>
@@ -671,11 +682,13 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
   id %= heads;
   const int hk = (int)(id % c.HK), r = a.HQ / c.HK;
   const int64_t b = id / c.HK;
-  Rows rows;
-  if (!rows.set<CG * C::kRows, BN>(c, a, b, tile0)) return;
+  Rows rows0;
+  if (!rows0.set<CG * C::kRows, BN>(c, a, b, tile0)) return;
 
-  auto init = [&](bool again) {
+  auto init = [&](bool again, const Rows &rows, int tile) {
     if (tid == 0) {
+      bars->rows.put(rows);
+      bars->tile = tile;
       if (again)
         for (uint64_t *bar = bars->k_full; bar <= &bars->drain; ++bar)
           asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -696,7 +709,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     }
   };
   if (tid == 0) bars->abort_flag = 0;
-  init(false);
+  init(false, rows0, tile0);
   if (warp == C::kMma) {
     asm volatile("tcgen05.alloc.cta_group::%2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(512),
                  "n"(CG)
@@ -710,15 +723,16 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
 
   // Every role goes through the CTA's tiles (one, unless the hint max_q was too small)
   // and meets the others at the end of each; false: no other tile.
-  auto next = [&](int &tile) -> bool {
+  auto next = [&]() -> bool {
     fence_before();
     sync_all<CG>();
     fence_after();
-    tile += tiles;
+    Rows rows;
+    const int tile = bars->tile + tiles;
     const bool more = !any_flag<CG>(&bars->abort_flag) && rows.set<CG * C::kRows, BN>(c, a, b, tile);
-    if (CG > 1) sync_all<CG>();  // (each has read the other's flag)
+    sync_all<CG>();  // (each has read what the other's may change)
     if (!more) return false;
-    init(true);
+    init(true, rows, tile);
     sync_all<CG>();
     return true;
   };
@@ -728,12 +742,10 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     if constexpr (C::kRegS > C::kRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegS));
     const int q = warp >> 2, quarter = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16), to = tl + 256 + D * q;
-    int tile = tile0;
     do {
-      const int row0 = CG * (tile * C::kRows + 128 * q) + 128 * rank + 32 * quarter;  // this warp's rows
-      const int mine = row0 + lane, row = min(mine, rows.rows - 1);
-      const int64_t tok = rows.t0 + row / r;
-      const int head = hk * r + row % r, pos = rows.pos0 + row / r;
+      Rows rows = bars->rows.get();
+      const int row0 = CG * (bars->tile * C::kRows + 128 * q) + 128 * rank + 32 * quarter;  // this warp's rows
+      const int pos = rows.pos0 + min(row0 + lane, rows.rows - 1) / r;
       const int hi = pos < 0 ? -1 : a.causal ? pos : rows.len - 1, lo = a.window ? max(pos, 0) - a.window : -1;  // lo < j <= hi is seen
       const int hi_all = __reduce_min_sync(0xffffffffu, hi), lo_all = __reduce_max_sync(0xffffffffu, lo);
       const float f = load_q<T, D, GS>(a, rows, sm, tl, row0, hk, r, q, 32 * quarter, lane);
@@ -744,12 +756,13 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       publish_smem<CG>(&bars->q_full, lane, rank);
       float M = kNone, L = 0.f;
       bool ok = true;
-      for (int i = 0; i < rows.tiles; ++i) {
+      const int n = rows.tiles, first = rows.first;
+      for (int i = 0; i < n; ++i) {
         const int buf = (QT * i + q) % C::NB;
         const uint32_t ph = (QT * i + q) / C::NB & 1, ts = tl + C::kS * buf;
         if (!(ok = wait_warp(&bars->s_full[buf], ph, bars))) break;
         fence_after();
-        const int n0 = rows.first + i * BN, h = hi - n0, l = lo - n0;
+        const int n0 = first + i * BN, h = hi - n0, l = lo - n0;
         const bool masked = n0 <= lo_all || n0 + BN - 1 > hi_all;
         auto mask = [&](float(&x)[32], int k) {
 #pragma unroll
@@ -841,6 +854,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
         __syncwarp();
         if (lane == 0) arrive_lead<CG>(&bars->p_ready[buf], rank);
       }
+      rows = bars->rows.get();
       // O's last product.  With two buffers of S per row tile the last two may be open (S of a tile only says that the
       // product two tiles before is complete), and o_done's parity cannot tell them apart: all MMAs, then.
       if (ok && rows.tiles > 0) ok = C::NB == QT ? wait_warp(&bars->o_done[q], (rows.tiles - 1) & 1, bars) : wait_warp(&bars->drain, 0, bars);
@@ -891,7 +905,6 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
         }
       }
       __syncwarp();
-      const bool write = ok && mine < rows.rows;
 #pragma unroll 4
       for (int n = 0; n < kPieces; ++n) {
         const int from = n * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;  // row of the warp, piece of the row
@@ -904,20 +917,20 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
         if (ok && other < rows.rows)
           reinterpret_cast<uint4 *>(static_cast<T *>(a.o) + (rows.t0 + other / r) * a.o_stride + (int64_t)(hk * r + other % r) * D)[piece] = w;
       }
-      if (write && a.lse) a.lse[tok * a.HQ + head] = L == 0.f ? -INFINITY : (M + log2f(L) - kShift) * kLn2;
-    } while (next(tile));
+      const int mine = row0 + lane;
+      if (ok && a.lse && mine < rows.rows) a.lse[(rows.t0 + mine / r) * a.HQ + hk * r + mine % r] = L == 0.f ? -INFINITY : (M + log2f(L) - kShift) * kLn2;
+    } while (next());
   } else if (warp < C::kMma) {
     // ---------------- expansion of K, or of V
     if constexpr (C::kRegX < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegX));
-    int tile = tile0;
     do {
+      const Rows rows = bars->rows.get();
       const X x{c, b, hk, warp & 3, lane, rank, rows.first, c_kv_stall ? 0 : rows.tiles};
       if (warp < C::kFirstV) x.run_k(bars, sm);
       else x.run_v(bars, sm, rows.len);
-    } while (next(tile));
+    } while (next());
   } else {
     if constexpr (C::kRegM < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegM));
-    int tile = tile0;
     do {
       const int q = warp - C::kMma;
       if (q < QT) {
@@ -925,14 +938,15 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
         // 40 clocks and a wait on a barrier 80 to 180, also where it holds already, so that one thread for both kept the
         // tensor cores waiting.
         if (rank == 0 && elect_one()) {
-          const int n = rows.tiles;
+          const int n = bars->rows.tiles;
           bool ok = wait_one(&bars->q_full, 0, bars);
           const uint32_t q0 = C::kQTmem ? tmem + 128 : desc_k(sm + C::kQ + q * C::kQTile), k0 = desc_k(sm + C::kK),
                          v0 = desc_mn(sm + C::kV, C::kBoxV), x0 = desc_k(sm + C::kX), o = tmem + 256 + D * q;
           constexpr int kAhead = C::NB / QT;  // buffers of S of a row tile
-          auto scores = [&](int i) {
+          auto k_ready = [&](int i) { return mbar_try(&bars->k_full[i % C::NST], i / C::NST & 1); };
+          auto scores = [&](int i, bool ready) {
             const int s = i % C::NST, buf = QT * (i % kAhead) + q;
-            if (!wait_one(&bars->k_full[s], i / C::NST & 1, bars)) return false;
+            if (!ready && !wait_one(&bars->k_full[s], i / C::NST & 1, bars)) return false;
             fence_after();
             const uint32_t d = tmem + C::kS * buf;
             uint32_t qa = q0, kb = k0 + s * (C::kStageK / 16);
@@ -948,23 +962,26 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
             umma_commit<CG>(&bars->k_empty[s]);
             return true;
           };
-          for (int i = 0; ok && i < kAhead && i < n; ++i) ok = scores(i);
+          for (int i = 0; ok && i < kAhead && i < n; ++i) ok = scores(i, false);
 #pragma unroll 1
           for (int i = 0; ok && i < n; ++i) {
             const int s = i % C::NST, buf = QT * (i % kAhead) + q;
-            if (!(ok = wait_one(&bars->v_full[s], i / C::NST & 1, bars))) break;
-            if (!(ok = wait_one(&bars->p_ready[buf], i / kAhead & 1, bars))) break;
+            // the three that this tile waits for, asked at once: the answers take a while
+            const bool v = mbar_try(&bars->v_full[s], i / C::NST & 1), pr = mbar_try(&bars->p_ready[buf], i / kAhead & 1),
+                       k = k_ready(i + kAhead);
+            if (!(ok = v || wait_one(&bars->v_full[s], i / C::NST & 1, bars))) break;
+            if (!(ok = pr || wait_one(&bars->p_ready[buf], i / kAhead & 1, bars))) break;
             fence_after();
             uint32_t p = tmem + C::kS * buf, vb = v0 + s * (C::kStageV / 16);
 #pragma unroll 1
-            for (int k = 0; k < BN / 64; ++k, p += 32, vb += 4 * 2048 / 16)
+            for (int h = 0; h < BN / 64; ++h, p += 32, vb += 4 * 2048 / 16)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                umma_ts<CG>(o, p + 8 * j, vb + j * (2048 / 16), idesc(128 * CG, D, true), i > 0 || k > 0 || j > 0);
+                umma_ts<CG>(o, p + 8 * j, vb + j * (2048 / 16), idesc(128 * CG, D, true), i > 0 || h > 0 || j > 0);
             umma_commit<CG>(&bars->o_done[q]);
             umma_commit<CG>(&bars->v_empty[s]);
             // P's place is free for other scores
-            if (i + kAhead < n) ok = scores(i + kAhead);
+            if (i + kAhead < n) ok = scores(i + kAhead, k);
           }
           umma_commit<CG>(&bars->drain);  // every MMA issued, complete before their memory is used again
         }
@@ -973,7 +990,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
         while (!mbar_try(&bars->drain, 0) && global_ns() - since < c_kv_wait_ns) {
         }
       }
-    } while (next(tile));
+    } while (next());
   }
   if (warp == C::kMma) asm volatile("tcgen05.dealloc.cta_group::%2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512), "n"(CG));
 }
