@@ -62,6 +62,14 @@ __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
       : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
   return ok != 0;
 }
+// the same without letting the thread sleep for a while where the phase is not complete
+__device__ __forceinline__ bool mbar_test(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ unsigned long long global_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
@@ -269,6 +277,23 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// two fp32 at once
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -359,6 +384,10 @@ struct Prefill {
   static constexpr int kRegs = QT == 2 ? 96 : 128;
   static constexpr int kRegS = QT == 2 ? 128 : 128, kRegX = QT == 2 ? 80 : 128, kRegM = QT == 2 ? 64 : 128;
   static_assert(QT * kRegS + 2 * kRegX + kRegM <= (QT + 3) * kRegs, "registers");
+  // Pieces of S that the softmax's loop has at a time, the next loading meanwhile: heads of 128 gain from two (480 us for a
+  // prompt of 8192 tokens, 501 with one), the others lose by the longer code (64: 46 us for six prompts of 650, 43 with one;
+  // 256: 392 us for 1000 rows over 15000 tokens, 390 with one).
+  static constexpr int kPieces = D == 128 ? 2 : 1;
   // tensor memory: S (and P) in NB times kS columns, O in 256 + D q; Q of heads of 256 in 128
   static constexpr int kS = BN;
 };
@@ -625,37 +654,39 @@ __device__ __forceinline__ float load_q(const KvAttention &a, const Rows &rows, 
     constexpr int kPieces = D / 8, kRowsAtOnce = 32 / kPieces;
     const int piece = lane % kPieces;
     const uint32_t dst = sm + C::kQ + q * C::kQTile + (piece >> 3) * (128 * 128), fac = sm + 1024 + (128 * q + at) * 4;
+    const long long own = reinterpret_cast<long long>(row_of(lane));  // (a division, once per lane)
 #pragma unroll 1
     for (int n0 = 0; n0 < kPieces; n0 += 4) {
-    uint4 v[4];  // loads before the first store
+      uint4 v[4];  // loads before the first store
 #pragma unroll
-    for (int n = 0; n < 4; ++n) v[n] = __ldg(reinterpret_cast<const uint4 *>(row_of((n0 + n) * kRowsAtOnce + lane / kPieces)) + piece);
+      for (int n = 0; n < 4; ++n)
+        v[n] = __ldg(reinterpret_cast<const uint4 *>(__shfl_sync(0xffffffffu, own, (n0 + n) * kRowsAtOnce + lane / kPieces)) + piece);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int i = (n0 + n) * kRowsAtOnce + lane / kPieces;
-      float x[8];
-      widen8<T>(v[n], x);
-      float big = 0.f, sum = 0.f;
+      for (int n = 0; n < 4; ++n) {
+        const int i = (n0 + n) * kRowsAtOnce + lane / kPieces;
+        float x[8];
+        widen8<T>(v[n], x);
+        float big = 0.f, sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        big = fmaxf(big, fabsf(x[j]));
-        sum += x[j];
+        for (int j = 0; j < 8; ++j) {
+          big = fmaxf(big, fabsf(x[j]));
+          sum += x[j];
+        }
+#pragma unroll
+        for (int o = 1; o < kPieces; o <<= 1) {
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          if (o < GS / 8) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        const float2 f = q_factors(big, a.scale);
+        sts4(dst + swz(at + i, piece & 7), half2_bits(f.x * x[0], f.x * x[4]), half2_bits(f.x * x[1], f.x * x[5]),
+             half2_bits(f.x * x[2], f.x * x[6]), half2_bits(f.x * x[3], f.x * x[7]));
+        auto sts1 = [](uint32_t to, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(v) : "memory"); };
+        const uint32_t extra = sm + C::kX + swz(at + i, 4 + 2 * q), one = sm + C::kX + swz(at + i, 5 + 2 * q);
+        if (piece % (GS / 8) == 0) sts1(extra + 4 * (piece / (GS / 8)), high_low(f.x * sum));
+        if (piece > 0 && piece < 4 && piece >= G) sts1(extra + 4 * piece, 0u);
+        if (piece >= 4 && piece < 8) sts1(one + 4 * (piece - 4), piece == 4 ? 0x00003C00u : 0u);  // 1, against what is -inf for a missing token
+        if (piece == 0) sts1(fac + 4 * i, __float_as_uint(f.y));
       }
-#pragma unroll
-      for (int o = 1; o < kPieces; o <<= 1) {
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        if (o < GS / 8) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      }
-      const float2 f = q_factors(big, a.scale);
-      sts4(dst + swz(at + i, piece & 7), half2_bits(f.x * x[0], f.x * x[4]), half2_bits(f.x * x[1], f.x * x[5]),
-           half2_bits(f.x * x[2], f.x * x[6]), half2_bits(f.x * x[3], f.x * x[7]));
-      auto sts1 = [](uint32_t to, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(v) : "memory"); };
-      const uint32_t extra = sm + C::kX + swz(at + i, 4 + 2 * q), one = sm + C::kX + swz(at + i, 5 + 2 * q);
-      if (piece % (GS / 8) == 0) sts1(extra + 4 * (piece / (GS / 8)), high_low(f.x * sum));
-      if (piece > 0 && piece < 4 && piece >= G) sts1(extra + 4 * piece, 0u);
-      if (piece >= 4 && piece < 8) sts1(one + 4 * (piece - 4), piece == 4 ? 0x00003C00u : 0u);  // 1, against what is -inf for a missing token
-      if (piece == 0) sts1(fac + 4 * i, __float_as_uint(f.y));
-    }
     }
     __syncwarp();
     uint32_t f;
@@ -774,23 +805,25 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
           if (masked) mask(x, k);
           uint32_t w[16];
           float s4[4];
-          auto numerators = [&] {
-            const float neg = kShift - M;
-            s4[0] = s4[1] = s4[2] = s4[3] = 0.f;
+#pragma unroll 1
+          for (bool again = false;; again = true) {
+            const uint64_t f2 = pair(f, f), neg2 = pair(kShift - M, kShift - M);
+            uint64_t s2[2] = {0, 0};
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float u = ex2(fmaf(x[2 * j], f, neg)), v = ex2(fmaf(x[2 * j + 1], f, neg));
-              s4[(2 * j) & 3] += u;
-              s4[(2 * j + 1) & 3] += v;
+              float u, v;
+              unpair(fma2(pair(x[2 * j], x[2 * j + 1]), f2, neg2), u, v);
+              u = ex2(u), v = ex2(v);
+              s2[j & 1] = add2(s2[j & 1], pair(u, v));
               w[j] = half2_bits(u, v);
             }
+            unpair(s2[0], s4[0], s4[1]);
+            unpair(s2[1], s4[2], s4[3]);
             s4[0] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          };
-          numerators();
           // What sums to no more than fp16's largest value has no part beyond it.  Else (on the first piece, and seldom
           // again) the reference moves to the largest logit that is left in the tile, in whole octaves, so that what
           // is there already, O, L and P, is scaled exactly.
-          if (__any_sync(0xffffffffu, !(s4[0] <= 65504.f))) {
+          if (again || !__any_sync(0xffffffffu, !(s4[0] <= 65504.f))) break;
             float top = kNone;
 #pragma unroll 1
             for (int n = k; n < BN; n += 32) {
@@ -831,21 +864,20 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
                 tm_st32(to + n, v);
               }
             }
-            numerators();
           }
           sum += s4[0];
           tm_st16(ts + k / 2, w);
         };
-        float x[2][32];
-        tm_ld32(ts, x[0]);
 #pragma unroll 1
-        for (int k = 0; k < BN; k += 64) {
-          wait_ld32(x[0]);
-          tm_ld32(ts + k + 32, x[1]);
-          piece(x[0], k);
-          wait_ld32(x[1]);
-          if (k + 64 < BN) tm_ld32(ts + k + 64, x[0]);
-          piece(x[1], k + 32);
+        for (int k = 0; k < BN; k += 32 * C::kPieces) {
+          float x[C::kPieces][32];
+          tm_ld32(ts + k, x[0]);
+#pragma unroll
+          for (int h = 0; h < C::kPieces; ++h) {
+            wait_ld32(x[h]);
+            if (h + 1 < C::kPieces) tm_ld32(ts + k + 32 * (h + 1), x[h + 1]);
+            piece(x[h], k + 32 * h);
+          }
         }
         if (!ok) break;
         L += sum;
@@ -943,7 +975,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
           const uint32_t q0 = C::kQTmem ? tmem + 128 : desc_k(sm + C::kQ + q * C::kQTile), k0 = desc_k(sm + C::kK),
                          v0 = desc_mn(sm + C::kV, C::kBoxV), x0 = desc_k(sm + C::kX), o = tmem + 256 + D * q;
           constexpr int kAhead = C::NB / QT;  // buffers of S of a row tile
-          auto k_ready = [&](int i) { return mbar_try(&bars->k_full[i % C::NST], i / C::NST & 1); };
+          auto k_ready = [&](int i) { return mbar_test(&bars->k_full[i % C::NST], i / C::NST & 1); };
           auto scores = [&](int i, bool ready) {
             const int s = i % C::NST, buf = QT * (i % kAhead) + q;
             if (!ready && !wait_one(&bars->k_full[s], i / C::NST & 1, bars)) return false;
@@ -967,7 +999,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
           for (int i = 0; ok && i < n; ++i) {
             const int s = i % C::NST, buf = QT * (i % kAhead) + q;
             // the three that this tile waits for, asked at once: the answers take a while
-            const bool v = mbar_try(&bars->v_full[s], i / C::NST & 1), pr = mbar_try(&bars->p_ready[buf], i / kAhead & 1),
+            const bool v = mbar_test(&bars->v_full[s], i / C::NST & 1), pr = mbar_test(&bars->p_ready[buf], i / kAhead & 1),
                        k = k_ready(i + kAhead);
             if (!(ok = v || wait_one(&bars->v_full[s], i / C::NST & 1, bars))) break;
             if (!(ok = pr || wait_one(&bars->p_ready[buf], i / kAhead & 1, bars))) break;
