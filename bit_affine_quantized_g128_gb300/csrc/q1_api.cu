@@ -462,17 +462,12 @@ q1_status q1_kv_load(const q1_kv_cache *c, void *k, int64_t k_stride, void *v, i
   return cuda_status(q1::launch_kv_load(kv_view(c), k, k_stride, v, v_stride, t, (cudaStream_t)stream));
 }
 
-namespace {
-// Many rows per key head go to the tensor-memory kernel (fp32 ones do not: its
-// operands hold 16-bit inputs exactly, not fp32 ones).
-bool kv_by_tiles(const q1_kv_cache *c, const q1_kv_attention_args *a) {
-  return a->dtype != Q1_F32 && std::min(a->max_q, c->T) * (a->HQ / c->HK) > 64;
-}
-}  // namespace
-
 size_t q1_kv_attention_workspace_size(const q1_kv_cache *c, const q1_kv_attention_args *a) {
-  if (check_kv_attention_sizes(c, a) != Q1_OK || c->T == 0 || kv_by_tiles(c, a)) return 0;
-  return q1::kv_decode_workspace_bytes(kv_view(c), kv_attention_view(a), (q1_dtype)a->dtype);
+  if (check_kv_attention_sizes(c, a) != Q1_OK || c->T == 0) return 0;
+  const q1::KvView v = kv_view(c);
+  const q1::KvAttention at = kv_attention_view(a);
+  const int splits = q1::kv_tiles_splits(v, at, (q1_dtype)a->dtype);
+  return splits ? q1::kv_tiles_workspace_bytes(v, at, splits) : q1::kv_decode_workspace_bytes(v, at, (q1_dtype)a->dtype);
 }
 
 q1_status q1_kv_attention(const q1_kv_cache *c, const q1_kv_attention_args *a, void *workspace, size_t workspace_bytes,
@@ -488,9 +483,10 @@ q1_status q1_kv_attention(const q1_kv_cache *c, const q1_kv_attention_args *a, v
   if (!aligned(a->lse, 4)) return Q1_ERR_ALIGN;
   const q1::KvView v = kv_view(c);
   const q1::KvAttention at = kv_attention_view(a);
-  if (kv_by_tiles(c, a)) return cuda_status(q1::launch_kv_prefill(v, at, t, (cudaStream_t)stream));
-  const size_t need = q1::kv_decode_workspace_bytes(v, at, t);
+  const int splits = q1::kv_tiles_splits(v, at, t);
+  const size_t need = splits ? q1::kv_tiles_workspace_bytes(v, at, splits) : q1::kv_decode_workspace_bytes(v, at, t);
   if (need && (s = check_ws(workspace, workspace_bytes, need)) != Q1_OK) return s;
+  if (splits) return cuda_status(q1::launch_kv_prefill(v, at, t, splits, workspace, (cudaStream_t)stream));
   return cuda_status(q1::launch_kv_decode(v, at, t, workspace, (cudaStream_t)stream));
 }
 

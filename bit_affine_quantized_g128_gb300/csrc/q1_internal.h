@@ -179,7 +179,10 @@ cudaError_t launch_kv_store(const KvView &c, const void *k, int64_t k_stride, co
 cudaError_t launch_kv_load(const KvView &c, void *k, int64_t k_stride, void *v, int64_t v_stride, q1_dtype t, cudaStream_t st);
 size_t kv_decode_workspace_bytes(const KvView &c, const KvAttention &a, q1_dtype t);
 cudaError_t launch_kv_decode(const KvView &c, const KvAttention &a, q1_dtype t, void *workspace, cudaStream_t st);
-cudaError_t launch_kv_prefill(const KvView &c, const KvAttention &a, q1_dtype t, cudaStream_t st);
+// parts of the context of many rows' tiles; 0: the form for few rows
+int kv_tiles_splits(const KvView &c, const KvAttention &a, q1_dtype t);
+size_t kv_tiles_workspace_bytes(const KvView &c, const KvAttention &a, int splits);
+cudaError_t launch_kv_prefill(const KvView &c, const KvAttention &a, q1_dtype t, int splits, void *workspace, cudaStream_t st);
 
 // ---- device error words (each translation unit with bounded waits owns one)
 // and the diagnostics of the bounded waits: their limit, and producers that

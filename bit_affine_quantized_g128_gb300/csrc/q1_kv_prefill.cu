@@ -76,12 +76,12 @@ __device__ __forceinline__ unsigned long long global_ns() {
   return t;
 }
 
-// A CTA's rows: those of `tile` of sequence b, and the positions that any of them sees.
+// A CTA's rows: those of `tile` of sequence b, and the positions that any of them sees, or a part of these.
 struct Rows {
   int64_t t0;
   int rows, len, pos0, first, tiles;  // rows of the sequence, its tokens, position of its first row; first position, number of tiles
   template <int ROWS, int BN>
-  __device__ __forceinline__ bool set(const KvView &c, const KvAttention &a, int64_t b, int tile) {
+  __device__ __forceinline__ bool set(const KvView &c, const KvAttention &a, int64_t b, int tile, int split, int splits) {
     int64_t t1;
     c.range(b, t0, t1);
     const int r = a.HQ / c.HK, n = (int)(t1 - t0);
@@ -96,6 +96,10 @@ struct Rows {
     const int begin = a.window ? (int)max((int64_t)pos0 + row0 / r - a.window + 1, (int64_t)0) : 0;
     first = begin / BN * BN;
     tiles = end > begin ? (end - first + BN - 1) / BN : 0;
+    const int64_t all_tiles = tiles;
+    const int from = (int)(all_tiles * split / splits);
+    first += from * BN;
+    tiles = (int)(all_tiles * (split + 1) / splits) - from;
     return true;
   }
   __device__ __forceinline__ void put(const Rows &x) volatile {
@@ -696,7 +700,8 @@ __device__ __forceinline__ float load_q(const KvAttention &a, const Rows &rows, 
 }
 
 template <typename T, int D, int GS>
-__global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kernel(const KvView c, const KvAttention a, int tiles) {
+__global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kernel(const KvView c, const KvAttention a, int tiles, int splits,
+                                                                                      float *part) {
   using C = Prefill<D, GS>;
   using X = Expander<D, GS>;
   constexpr int G = C::G, QT = C::QT, BN = C::BN, CG = C::CG;
@@ -708,13 +713,15 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
   // the last tiles first: they see the most
   const int rank = blockIdx.x % CG;  // in the pair
   int64_t id = blockIdx.x / CG;
+  const int split = (int)(id % splits);
+  id /= splits;
   const int64_t heads = c.B * c.HK;
   const int tile0 = tiles - 1 - (int)(id / heads);
   id %= heads;
   const int hk = (int)(id % c.HK), r = a.HQ / c.HK;
   const int64_t b = id / c.HK;
   Rows rows0;
-  if (!rows0.set<CG * C::kRows, BN>(c, a, b, tile0)) return;
+  if (!rows0.set<CG * C::kRows, BN>(c, a, b, tile0, split, splits)) return;
 
   auto init = [&](bool again, const Rows &rows, int tile) {
     if (tid == 0) {
@@ -760,7 +767,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     fence_after();
     Rows rows;
     const int tile = bars->tile + tiles;
-    const bool more = !any_flag<CG>(&bars->abort_flag) && rows.set<CG * C::kRows, BN>(c, a, b, tile);
+    const bool more = !any_flag<CG>(&bars->abort_flag) && rows.set<CG * C::kRows, BN>(c, a, b, tile, split, splits);
     sync_all<CG>();  // (each has read what the other's may change)
     if (!more) return false;
     init(true, rows, tile);
@@ -891,7 +898,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       // product two tiles before is complete), and o_done's parity cannot tell them apart: all MMAs, then.
       if (ok && rows.tiles > 0) ok = C::NB == QT ? wait_warp(&bars->o_done[q], (rows.tiles - 1) & 1, bars) : wait_warp(&bars->drain, 0, bars);
       fence_after();
-      float inv = L == 0.f ? 0.f : 1.f / L;
+      float inv = splits > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L;
       if (ok && any_flag<CG>(&bars->bad_v)) {
         // rows that see such a token become NaN
         for (int p = max(lo + 1, 0); p <= min(hi, (int)min((int64_t)rows.len, c.table_width << c.page_shift) - 1); ++p) {
@@ -906,7 +913,46 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       // rows of o through shared memory (Q's tile; K's stages for heads of 256: no MMA reads them any more), so that a
       // warp stores whole rows
       const uint32_t stage = sm + (C::kQTmem ? C::kK : C::kQ + q * C::kQTile) + quarter * (32 * D * 2);
+      auto lds4 = [](uint32_t from) {
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(from) : "memory");
+        return w;
+      };
+      const int mine = row0 + lane;
       constexpr int kPieces = D / 8;
+      if (splits > 1) {
+        // a part: o as it is, fp32, 32 channels at a time, its reference and its sum
+        const int64_t step = (int64_t)splits * (D + 4);
+        auto part_of = [&](int row) { return part + ((rows.t0 + row / r) * a.HQ + hk * r + row % r) * step + (int64_t)split * (D + 4); };
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          float o[32];
+          if (rows.tiles > 0) {
+            tm_ld32(to + k, o);
+            wait_ld32(o);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0.f;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            // columns hold channels 0 4 1 5 2 6 3 7
+            const int at = j & ~7, odd = (j >> 2) & 1;
+            sts4(stage + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4), __float_as_uint(o[at + odd] * inv), __float_as_uint(o[at + odd + 2] * inv),
+                 __float_as_uint(o[at + odd + 4] * inv), __float_as_uint(o[at + odd + 6] * inv));
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int n = 0; n < 8; ++n) {
+            const int from = 4 * n + (lane >> 3), piece = lane & 7;
+            const uint4 w = lds4(stage + from * 128 + ((piece ^ (from & 7)) << 4));
+            if (ok && row0 + from < rows.rows) reinterpret_cast<uint4 *>(part_of(row0 + from) + k)[piece] = w;
+          }
+        }
+        if (ok && mine < rows.rows) *reinterpret_cast<float2 *>(part_of(mine) + D) = make_float2(M - kShift, inv == 1.f ? L : inv);
+        continue;
+      }
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
         float o[32];
@@ -941,15 +987,10 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       for (int n = 0; n < kPieces; ++n) {
         const int from = n * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;  // row of the warp, piece of the row
         const int other = row0 + from;
-        uint4 w;
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                     : "r"(stage + from * (D * 2) + (((piece & ~7) | ((piece ^ from) & 7)) << 4))
-                     : "memory");
+        const uint4 w = lds4(stage + from * (D * 2) + (((piece & ~7) | ((piece ^ from) & 7)) << 4));
         if (ok && other < rows.rows)
           reinterpret_cast<uint4 *>(static_cast<T *>(a.o) + (rows.t0 + other / r) * a.o_stride + (int64_t)(hk * r + other % r) * D)[piece] = w;
       }
-      const int mine = row0 + lane;
       if (ok && a.lse && mine < rows.rows) a.lse[(rows.t0 + mine / r) * a.HQ + hk * r + mine % r] = L == 0.f ? -INFINITY : (M + log2f(L) - kShift) * kLn2;
     } while (next());
   } else if (warp < C::kMma) {
@@ -1027,25 +1068,81 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
   if (warp == C::kMma) asm volatile("tcgen05.dealloc.cta_group::%2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512), "n"(CG));
 }
 
+// Joins the parts of a row: D / 4 threads per row, four channels each.
+constexpr int kJoinThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_parts_kernel(const KvView c, const KvAttention a, int splits, const float *part) {
+  constexpr int kLanes = D / 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t id = (int64_t)blockIdx.x * (kJoinThreads / kLanes) + threadIdx.x / kLanes, tok = id / a.HQ;
+  const int lane = threadIdx.x % kLanes;
+  int64_t first, last, skip;
+  c.range(0, first, skip);
+  c.range(c.B - 1, skip, last);
+  if (tok < first || tok >= last) return;  // (a row of no sequence)
+  const float *src = part + id * splits * (D + 4);
+  float m = kNone, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < splits; i += 4) {
+    float2 q[4];
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < splits) {
+        q[k] = __ldcs(reinterpret_cast<const float2 *>(src + (i + k) * (D + 4) + D));
+        v[k] = __ldcs(reinterpret_cast<const float4 *>(src + (i + k) * (D + 4)) + lane);
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < splits) {
+        const float top = fmaxf(m, q[k].x), z = ex2(m - top), z2 = ex2(q[k].x - top);
+        m = top;
+        l = fmaf(z, l, z2 * q[k].y);
+        o.x = fmaf(z, o.x, z2 * v[k].x);
+        o.y = fmaf(z, o.y, z2 * v[k].y);
+        o.z = fmaf(z, o.z, z2 * v[k].z);
+        o.w = fmaf(z, o.w, z2 * v[k].w);
+      }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T *dst = static_cast<T *>(a.o) + tok * a.o_stride + (id - tok * a.HQ) * D + 4 * lane;
+  uint2 w;
+  if constexpr (std::is_same<T, __half>::value) {
+    w = make_uint2(half2_bits(o.x * inv, o.y * inv), half2_bits(o.z * inv, o.w * inv));
+  } else {
+    const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+    w = make_uint2(*reinterpret_cast<const uint32_t *>(&h[0]), *reinterpret_cast<const uint32_t *>(&h[1]));
+  }
+  *reinterpret_cast<uint2 *>(dst) = w;
+  if (lane == 0 && a.lse) a.lse[id] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+struct Shape {
+  int64_t rows, tiles, units, slots;  // rows of a tile of a CTA or pair; tiles that the longest sequence has; of all; how many run at once
+};
+Shape shape(const KvView &c, const KvAttention &a) {
+  const int r = a.HQ / c.HK, cg = c.D == 64 ? 1 : 2;
+  Shape s;
+  s.rows = c.D == 128 ? 512 : 256;
+  s.tiles = (std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + s.rows - 1) / s.rows;
+  s.units = std::min(s.tiles * c.B, c.T * r / s.rows + c.B) * c.HK;
+  s.slots = 152 / cg;
+  return s;
+}
+
 template <typename T, int D, int GS>
-cudaError_t run(const KvView &c, const KvAttention &a, cudaStream_t st) {
+cudaError_t run(const KvView &c, const KvAttention &a, int splits, float *part, cudaStream_t st) {
   using C = Prefill<D, GS>;
   static std::atomic<uint64_t> ready{0};
   const int dev = current_device();
   if (not_done(ready, dev)) {
-    cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, kv_prefill_kernel<T, D, GS>);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kv_prefill_kernel<T, D, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    // the warps' shares come out of what the block was launched with
-    if (e == cudaSuccess && C::kRegS > C::kRegs && at.numRegs != C::kRegs) e = cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel<T, D, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
   }
-  const int r = a.HQ / c.HK;
-  const int64_t tiles = (std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + C::CG * C::kRows - 1) / (C::CG * C::kRows),
-                ctas = tiles * c.B * c.HK * C::CG;
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t tiles = shape(c, a).tiles, ctas = tiles * c.B * c.HK * C::CG * splits;
+  const int64_t joins = (c.T * a.HQ * (D / 4) + kJoinThreads - 1) / kJoinThreads;
+  if (ctas > INT32_MAX || joins > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas, 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);
@@ -1057,19 +1154,58 @@ cudaError_t run(const KvView &c, const KvAttention &a, cudaStream_t st) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = C::CG > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<T, D, GS>, c, a, (int)tiles);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<T, D, GS>, c, a, (int)tiles, splits, part);
+  if (e != cudaSuccess || splits == 1) return e;
+  cfg.gridDim = dim3((unsigned)joins, 1, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_join_parts_kernel<T, D>, c, a, splits, const_cast<const float *>(part));
 }
 template <typename T>
-cudaError_t run_t(const KvView &c, const KvAttention &a, cudaStream_t st) {
-  if (c.D == 64) return run<T, 64, 64>(c, a, st);
-  if (c.D == 128) return c.gs == 64 ? run<T, 128, 64>(c, a, st) : run<T, 128, 128>(c, a, st);
-  return c.gs == 64 ? run<T, 256, 64>(c, a, st) : run<T, 256, 128>(c, a, st);
+cudaError_t run_t(const KvView &c, const KvAttention &a, int splits, float *part, cudaStream_t st) {
+  if (c.D == 64) return run<T, 64, 64>(c, a, splits, part, st);
+  if (c.D == 128) return c.gs == 64 ? run<T, 128, 64>(c, a, splits, part, st) : run<T, 128, 128>(c, a, splits, part, st);
+  return c.gs == 64 ? run<T, 256, 64>(c, a, splits, part, st) : run<T, 256, 128>(c, a, splits, part, st);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_prefill(const KvView &c, const KvAttention &a, q1_dtype t, cudaStream_t st) {
-  return t == Q1_BF16 ? run_t<__nv_bfloat16>(c, a, st) : run_t<__half>(c, a, st);
+// Costs in units of what a tile of rows takes per cached token, 12 to 14 ns for each size of heads.  A tile's CTAs cost 900
+// of them besides (12 us: start, Q, O); its tokens may be split over several, which costs the join's launch (230) and
+// the parts' traffic.  Few rows at a time take 2^-19 per row, channel and token (3.2 ps per row of 128 channels), 0.001 per row and
+// channel (128 at most) for their CTAs' starts, 400 for the call.  Both sides measured, in us, few rows / tiles in one part / as
+// chosen here, 32 query heads over 8 of 128 channels:
+//   16 new tokens over 60000           104 / 806 / 112
+//   64                                 401 / 807 / 112
+//   128 over 4000                       81 /  69 /  30
+//   12 of 16 sequences over 4000        92 / 134 /  92
+//   24                                 181 / 134 / 136
+//   128 alone                           12 /  15 /  12
+int kv_tiles_splits(const KvView &c, const KvAttention &a, q1_dtype t) {
+  if (t == Q1_F32) return 0;
+  const Shape s = shape(c, a);
+  int64_t seen = std::max<int64_t>(a.max_len, 1);
+  if (a.window) seen = std::min<int64_t>(seen, (int64_t)a.window + s.rows / (a.HQ / c.HK));
+  const double values = (double)c.T * a.HQ * c.D;
+  double best = values / (1 << 19) * (double)seen + 0.001 * values / c.D * std::min(c.D, 128) + 400;
+  int splits = 0;
+  for (int n = 1; n <= 32 && (n == 1 || seen / n >= 128); ++n) {
+    const double rounds = (double)((s.units * n + s.slots - 1) / s.slots);
+    const double cost = rounds * (900 + (double)seen / n) + (n > 1 ? 230 + 9e-5 * n * values : 0);
+    if (cost < best) best = cost, splits = n;
+  }
+  return splits;
+}
+size_t kv_tiles_workspace_bytes(const KvView &c, const KvAttention &a, int splits) {
+  return splits > 1 ? (size_t)c.T * a.HQ * splits * (c.D + 4) * sizeof(float) : 0;
+}
+
+cudaError_t launch_kv_prefill(const KvView &c, const KvAttention &a, q1_dtype t, int splits, void *workspace, cudaStream_t st) {
+  float *part = static_cast<float *>(workspace);
+  return t == Q1_BF16 ? run_t<__nv_bfloat16>(c, a, splits, part, st) : run_t<__half>(c, a, splits, part, st);
 }
 
 cudaError_t set_kv_diagnostics(unsigned long long wait_ns, int stall) {

@@ -268,7 +268,8 @@ def check(q1, c, cache, new, HQ, dtype="bf16", causal=True, window=0, seed=11, s
     q, qv = _rounded(rng.standard_normal((T, HQ, D)) * qsize, dtype)
     cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     tab = c.table if table is None else table
-    kw = {"max_q": max(new), "max_len": max(c.lengths), **kw}
+    # (the hint of a long context has few rows take the tiles' form, in parts)
+    kw = {"max_q": max(new), "max_len": 1 << 20 if tiles else max(c.lengths), **kw}
     o, lse = q1.kv_attention(q.cuda(), cache, torch.from_numpy(tab).cuda(), c.d_lengths(), cu_seqlens=torch.from_numpy(cu).cuda(),
                              scale=scale, causal=causal, window=window, return_lse=True, **kw)
     assert o.dtype == DTYPES[dtype] and o.shape == (T, HQ, D) and lse.shape == (T, HQ)
@@ -341,6 +342,27 @@ MANY = [  # D, gs, HK, HQ / HK, page, dtype, lengths, new, window
 def test_attention_of_many_rows(q1, D, gs, HK, r, page, dtype, lengths, new, window):
     c = Cache(q1, lengths, HK, D, gs, page, seed=sum(lengths))
     check(q1, c, c.store(q1), new, HK * r, dtype, window=window, tiles=True)
+    assert q1.device_errors() == 0
+
+
+WHOLE = [  # the same, with enough heads that tiles are taken with their context in one part
+    (128, 64, 32, 4, 64, "bf16", [260], [260], 0),
+    (128, 64, 40, 2, 32, "fp16", [300, 140], [300, 33], 0),
+    (128, 128, 16, 5, 16, "bf16", [257, 600, 70], [100, 1, 70], 0),
+    (64, 64, 100, 1, 16, "bf16", [520, 129], [300, 129], 0),
+    (64, 64, 24, 8, 128, "fp16", [800, 33, 900], [300, 33, 90], 300),
+    (256, 64, 20, 2, 64, "bf16", [333, 65], [200, 65], 0),
+    (256, 64, 30, 2, 64, "bf16", [400], [400], 0),
+    (256, 128, 12, 6, 32, "fp16", [700, 64], [50, 64], 0),
+    (128, 64, 24, 1, 64, "fp16", [900], [613], 33),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,gs,HK,r,page,dtype,lengths,new,window", WHOLE)
+def test_attention_of_many_rows_and_heads(q1, D, gs, HK, r, page, dtype, lengths, new, window):
+    c = Cache(q1, lengths, HK, D, gs, page, seed=sum(lengths))
+    check(q1, c, c.store(q1), new, HK * r, dtype, window=window, tiles=True, max_len=max(lengths))
     assert q1.device_errors() == 0
 
 
@@ -475,7 +497,7 @@ def test_many_rows_beside_what_they_do_not_see(q1):
                     cu_seqlens=torch.tensor([0, 1, 1], dtype=torch.int32).cuda())
         q, qv = _rounded(_rng(9).standard_normal((280, 2, 128)), "bf16")
         o, lse = q1.kv_attention(q.cuda(), cache, c.d_table(), c.d_lengths(), cu_seqlens=torch.tensor([0, 140, 280], dtype=torch.int32).cuda(),
-                                 max_q=140, max_len=300, window=window, return_lse=True)
+                                 max_q=140, max_len=1 << 20, window=window, return_lse=True)
         for s in range(2):
             pos = np.arange(140) + c.lengths[s] - 140
             hit = (pos >= at) & ((pos < at + window) if window else True) if s == 0 else np.zeros(140, bool)
@@ -517,7 +539,8 @@ def test_stalled_expansion_times_out_and_recovers(q1, D):
     try:
         q1.set_wait_limit_ns(1_000_000)
         q1.set_stalled_producers(True)
-        q1.kv_attention(torch.zeros(1, 300, 4, D, dtype=torch.bfloat16, device="cuda"), cache, c.d_table(), c.d_lengths())
+        q1.kv_attention(torch.zeros(1, 300, 4, D, dtype=torch.bfloat16, device="cuda"), cache, c.d_table(), c.d_lengths(),
+                        max_len=1 << 20)
         torch.cuda.synchronize()
         assert q1.device_errors() == 8
     finally:
