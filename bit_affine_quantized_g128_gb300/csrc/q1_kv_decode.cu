@@ -531,10 +531,17 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            // fp32: a block at a time, as the tensor cores cut their sums (not round them), which adds up over a long context
+            float sum[4] = {};
+            float(&to)[4] = sizeof(T) == 4 ? sum : O[nt][h][i];
 #pragma unroll
             for (int p = 0; p < PP; ++p)
-              mma16(O[nt][h][i], x01[i], y01[i], x89[i], y89[i], pb[nt][64 * h / GS][p][0], pb[nt][64 * h / GS][p][1]);
+              mma16(to, x01[i], y01[i], x89[i], y89[i], pb[nt][64 * h / GS][p][0], pb[nt][64 * h / GS][p][1]);
+            if constexpr (sizeof(T) == 4)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) O[nt][h][i][k] += sum[k];
+          }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");

@@ -386,6 +386,19 @@ def test_long_contexts_are_split(q1, D, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_sums_of_one_sign(q1, D):
+    # V's codes of one sign (one channel of a group has the other) over a long context that the hint leaves to one CTA: hundreds
+    # of blocks into one sum
+    n = 30000
+    rng = _rng(17)
+    v = np.where(np.arange(D) % 64 == 5, -1.0, 1.0) * (1.0 + 0.05 * rng.random((n, 1, D)))
+    c = Cache(q1, [n], 1, D, seed=18, k=[0.2 * rng.standard_normal((n, 1, D))], v=[v])
+    check(q1, c, c.store(q1), [1], 2, "fp32", max_len=1)
+    check(q1, c, c.store(q1), [5], 3, "fp32", max_len=1)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_rows_that_see_nothing(q1, dtype):
     # a sequence without tokens, more rows than tokens, a page that is not there (alone, and among others), a short table
