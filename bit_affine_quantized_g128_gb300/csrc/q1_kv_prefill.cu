@@ -4,17 +4,23 @@
 // A pair of CTAs owns 512 rows (two tiles of 128 each; one for heads of 256) of a key head: row i of
 // a sequence is its new token i / r, query head i mod r of the r that share the key
 // head.  Each expands half of K's tokens and half of V's channels, and the MMAs (cta_group::2) read both halves: with a
-// CTA on its own, the MMAs' operands and the expansions' stores took all of shared memory's bandwidth (heads of 64 do go that
-// way).  Tiles of 128 cached tokens (64)
-// go by:
+// CTA on its own, the MMAs' operands and the expansions' stores took all of shared memory's bandwidth (a prompt of 8192 tokens
+// 561 us, 550 by pairs; heads of 64, whose operands are half as large, stay with one CTA).  Where tiles are few, their context is
+// split over CTAs, whose fp32 parts a second kernel joins.  Tiles of 64 cached tokens (128 for heads of 64) go by:
 //   S = Q K^T                      both operands in shared memory, S in tensor memory
 //   P = 2^(f S - M + 7) as fp16    a thread per row, back into S's columns
 //   O += P V                       P from tensor memory, O stays in tensor memory
 //
 // Roles, in groups of four warps: the softmax of a row tile each; K's expansion; V's; the
-// MMAs (one thread).  Five roles share each scheduler and its instruction cache, so their loops
+// MMAs (a thread per row tile).  Five roles share each scheduler and its instruction cache, so their loops
 // are kept short (a few KB each): with the same loops unrolled twice as far the kernel took
 // 1.5 times as long, though it issued fewer instructions.
+//
+// What bounds it.  8192 tokens, 32 heads over 8 of 128 channels: 480 us, 1150 TFLOP/s, 60 % of the measured bf16 peak; 1000 rows
+// over 15000 tokens, 24 heads over 4 of 256: 345 us, 58 %.  A tile of 64 tokens takes a CTA 1800 clocks for 1266 of MMAs (an MMA
+// of 256 x 64 x 16 takes 43 clocks with both operands in shared memory, 32 with Q in tensor memory; of 256 x 128 x 16 64): the two row
+// tiles' softmax warps on a scheduler go through a tile in step, 600 clocks per 32 columns, and wait 450 for barriers and tensor
+// memory.  Neither the other roles' traffic nor the fences slow the MMAs (633 clocks per row tile and 64 tokens beside all of it).
 //
 // Exactness.  K enters as scale q, which fp16 holds exactly (8 bits of scale, 4 of
 // code), and the biases through one more k16 step: columns bias_g (twice per
@@ -1173,8 +1179,8 @@ cudaError_t run_t(const KvView &c, const KvAttention &a, int splits, float *part
 
 }  // namespace
 
-// Costs in units of what a tile of rows takes per cached token, 12 to 14 ns for each size of heads.  A tile's CTAs cost 900
-// of them besides (12 us: start, Q, O); its tokens may be split over several, which costs the join's launch (230) and
+// Costs in units of what a tile of rows takes per cached token, 12 to 14 ns for each size of heads.  A tile's CTAs cost 1050
+// of them besides (14 us: start, Q, O); its tokens may be split over several, which costs the join's launch (230) and
 // the parts' traffic.  Few rows at a time take 2^-19 per row, channel and token (3.2 ps per row of 128 channels), 0.001 per row and
 // channel (128 at most) for their CTAs' starts, 400 for the call.  Both sides measured, in us, few rows / tiles in one part / as
 // chosen here, 32 query heads over 8 of 128 channels:
@@ -1194,7 +1200,7 @@ int kv_tiles_splits(const KvView &c, const KvAttention &a, q1_dtype t) {
   int splits = 0;
   for (int n = 1; n <= 32 && (n == 1 || seen / n >= 128); ++n) {
     const double rounds = (double)((s.units * n + s.slots - 1) / s.slots);
-    const double cost = rounds * (900 + (double)seen / n) + (n > 1 ? 230 + 9e-5 * n * values : 0);
+    const double cost = rounds * (1050 + (double)seen / n) + (n > 1 ? 230 + 9e-5 * n * values : 0);
     if (cost < best) best = cost, splits = n;
   }
   return splits;
