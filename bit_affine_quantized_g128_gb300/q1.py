@@ -710,10 +710,29 @@ def _kv(cache, block_table, lengths, cu_seqlens, T: int, dev):
 
 
 def _kv_rows(x: torch.Tensor, name: str, B: int, packed: bool):
-    """x [T, H, D] (packed) or [B, L, H, D], as [T, H, D]."""
-    if x.dim() != (3 if packed else 4) or not packed and x.shape[0] != B:
-        raise ValueError(f"{name} must be {'[T, H, D] with' if packed else f'[{B}, L, H, D] without'} cu_seqlens (got {tuple(x.shape)})")
-    return x if packed else x.flatten(0, 1)
+    """x [T, H, D] (packed) or [B, L, H, D] as rows: a tensor that holds them (x itself where it can be), T, H, D, the pointer
+    and the row stride."""
+    shape = x.shape
+    if len(shape) != (3 if packed else 4) or not packed and shape[0] != B:
+        raise ValueError(f"{name} must be {'[T, H, D] with' if packed else f'[{B}, L, H, D] without'} cu_seqlens (got {tuple(shape)})")
+    if packed:
+        T, H, D = shape
+        s0, s1, s2 = x.stride()
+    else:
+        _, L, H, D = shape
+        T = B * L
+        batch, s0, s1, s2 = x.stride()
+        if L == 1:
+            s0 = batch
+        elif B > 1 and batch != L * s0:
+            s2 = 0     # (copied below)
+    p = x.data_ptr()
+    if s2 != 1 or s1 != D and H != 1 or s0 % (16 // x.element_size()) or p % 16 or s0 < H * D:
+        x = x.contiguous()
+        if x.data_ptr() % 16:
+            x = x.clone()
+        p, s0 = x.data_ptr(), H * D
+    return x, T, H, D, p, s0
 
 
 def _kv_on_device(first, **tensors):
@@ -738,13 +757,11 @@ def kv_store(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_table:
     if v.dtype != k.dtype or v.shape != k.shape:
         raise ValueError(f"k and v must agree (got {k.dtype} {tuple(k.shape)}, {v.dtype} {tuple(v.shape)})")
     B = block_table.shape[0] if block_table.dim() == 2 else 0
-    k, v = _kv_rows(k, "k", B, packed), _kv_rows(v, "v", B, packed)
-    c, keep, heads, dim, _ = _kv(cache, block_table, lengths, cu_seqlens, k.shape[0], dev)
-    if k.shape[1:] != (heads, dim):
-        raise ValueError(f"the cache holds {heads} heads of {dim} (k and v have {tuple(k.shape[1:])})")
-    per16 = 4 if k.dtype == _F32 else 8
-    k, kp, ks = _rows(k, heads, dim, per16)
-    v, vp, vs = _rows(v, heads, dim, per16)
+    k, T, H, D, kp, ks = _kv_rows(k, "k", B, packed)
+    v, _, _, _, vp, vs = _kv_rows(v, "v", B, packed)
+    c, keep, heads, dim, _ = _kv(cache, block_table, lengths, cu_seqlens, T, dev)
+    if H != heads or D != dim:
+        raise ValueError(f"the cache holds {heads} heads of {dim} (k and v have {(H, D)})")
     st = (_lib or lib()).q1_kv_store(c, kp, ks, vp, vs, dt, _raw_stream(dev.index))
     if st:
         _check("q1_kv_store", st)
@@ -791,16 +808,14 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor
     dt = _x_dtype(q, "q")
     B = block_table.shape[0] if block_table.dim() == 2 else 0
     lead = q.shape[:-2]
-    q = _kv_rows(q, "q", B, packed)
-    T, HQ, D = q.shape
+    q, T, HQ, D, qp, qs = _kv_rows(q, "q", B, packed)
     c, keep, heads, dim, B = _kv(cache, block_table, lengths, cu_seqlens, T, dev)
     if D != dim or HQ < 1 or HQ % heads:
-        raise ValueError(f"the cache holds {heads} heads of {dim}; q must have a multiple of them (got {tuple(q.shape[1:])})")
+        raise ValueError(f"the cache holds {heads} heads of {dim}; q must have a multiple of them (got {(HQ, D)})")
     if window < 0 or window and not causal:
         raise ValueError("window must not be negative, and needs causal")
-    q, qp, qs = _rows(q, HQ, dim, 4 if dtype == _F32 else 8)
-    o = torch.empty((T, HQ, dim), dtype=dtype, device=dev) if out is None else _out(out, (T, HQ, dim), dtype, dev)
-    lse = torch.empty((T, HQ), dtype=_F32, device=dev) if return_lse else None
+    o = torch.empty((*lead, HQ, dim), dtype=dtype, device=dev) if out is None else _out(out, (T, HQ, dim), dtype, dev)
+    lse = torch.empty((*lead, HQ), dtype=_F32, device=dev) if return_lse else None
     if max_q is None or not packed:
         max_q = T if packed else lead[1]
     if max_len is None:
@@ -820,9 +835,8 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor
             st = L.q1_kv_attention(c, a, workspace.data_ptr(), n, stream)
     if st:
         _check("q1_kv_attention", st)
-    if not packed:
+    if out is not None and not packed:
         o = o.reshape(*lead, HQ, dim)
-        lse = None if lse is None else lse.reshape(*lead, HQ)
     return (o, lse) if return_lse else o
 
 
