@@ -623,6 +623,56 @@ def test_step_by_step_in_a_graph(q1):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("max_len", [1 << 20, 900])
+def test_many_rows_in_a_graph_beside_rows_of_no_sequence(q1, max_len):
+    # the tiles' form in parts (by the hint) and the few rows': what no sequence owns stays, a replay follows the lengths
+    c = Cache(q1, [300, 900], 2, 128, seed=31)
+    cache, table, lengths = c.store(q1), c.d_table(), c.d_lengths()
+    cu = torch.tensor([5, 105, 170], dtype=torch.int32).cuda()
+    q, qv = _rounded(_rng(32).standard_normal((200, 8, 128)), "bf16")
+    q, out = q.cuda(), torch.full((200, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        return q1.kv_attention(q, cache, table, lengths, cu_seqlens=cu, max_q=100, max_len=max_len, out=out)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for now in ([300, 900], [150, 470], [40, 900]):
+        lengths.copy_(torch.tensor(now, dtype=torch.int32))
+        out.fill_(7.0)
+        graph.replay()
+        got = out.double().cpu().numpy()
+        assert (got[:5] == 7).all() and (got[170:] == 7).all()
+        for b, (t0, t1) in enumerate(((5, 105), (105, 170))):
+            n = now[b]
+            want, _, size, _ = O.kv_attention(qv[t0:t1], c.kval[b][:n], c.vval[b][:n], np.arange(t1 - t0) + n - (t1 - t0), 128 ** -0.5)
+            # check()'s bound with its logits' part below 2^-14 of what |bias|, at most 2 here, adds to the sizes
+            assert (np.abs(got[t0:t1] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * size + 2.0 ** -10).all(), (now, b)
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_calls_at_once(q1):
+    # on two streams, each with its own workspace: the bits of one after the other
+    c = Cache(q1, [2000], 2, 128, seed=33)
+    cache, table, lengths = c.store(q1), c.d_table(), c.d_lengths()
+    qs = [torch.randn(1, n, 8, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(n)).bfloat16() for n in (100, 1, 33, 100)]
+    hints = (1 << 20, 2000, 1 << 20, 2000)
+    want = [q1.kv_attention(q, cache, table, lengths, max_len=m) for q, m in zip(qs, hints)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(3):
+        got = []
+        for stream, q, m in zip(streams, qs, hints):
+            with torch.cuda.stream(stream):
+                got.append(q1.kv_attention(q, cache, table, lengths, max_len=m))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.gpu
 def test_calls_that_share_a_workspace(q1):
     c = Cache(q1, [5000, 6000], 1, 128, seed=17)
     cache, ws = c.store(q1), torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
