@@ -734,6 +734,9 @@ Split plan(const KvView &c, const KvAttention &a, bool fp32) {
   int64_t want = std::min(slots / work, blocks / 16);
   if (blocks / std::max<int64_t>(2 * slots / work, 1) >= 64) want = 2 * slots / work;
   if (blocks / std::max<int64_t>(4 * slots / work, 1) >= 128) want = 4 * slots / work;
+  // Heads of 64: 9 to 16 splits are rather 8, in a cluster, whose join saves more than twice the blocks cost (12 heads over 4096
+  // tokens 7.1 us, 8.4 with 16; heads of 128 and 256: 9.1 and 11.0, 8.4 and 9.4 with 16; clusters of 16 were slower yet).
+  if (c.D == 64 && want > kCluster && want <= 2 * kCluster && work * kCluster <= slots) want = kCluster;
   s.chunk = (int)(((blocks + std::max<int64_t>(want, 1) - 1) / std::max<int64_t>(want, 1) + kWarps - 1) / kWarps * kWarps);
   s.splits = (int)((blocks + s.chunk - 1) / s.chunk);
   // (only where all run at once: a CTA whose split has no tokens would hold its place until the others are done)
