@@ -14,8 +14,8 @@
 // of them has channels 32 j + 8 t .. + 7, so a group is found in two shuffles, K's codes leave
 // in the order in which they lie, 512 bytes per store, and V's go through shared memory,
 // where words of a token become words of a channel.  Measured: 65536 tokens of 8 heads of 128 loaded in 55 us, 92 % of the copy
-// rate (191 us by words); a prompt of 8192 stored and loaded again in 24.5 us, two launches (58 us by words); one token of a
-// sequence 5.9 us, two launches.
+// rate (191 us by words); a prompt of 8192 stored and loaded again in 23.4 us, two launches (58 us by words); one token of a
+// sequence 5.8 us, two launches.
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -283,20 +283,20 @@ __device__ __forceinline__ void quantise(const float (&x)[D / 32][8], uint32_t (
   }
 }
 
-template <typename T, int D, int GS>
+// APART: a warp for a block's K, one for its V.
+template <typename T, int D, int GS, bool APART>
 __global__ void __launch_bounds__(kThreads) kv_store_blocks_kernel(const KvView c, const T *__restrict__ k, int64_t k_stride,
                                                                    const T *__restrict__ v, int64_t v_stride, int64_t items) {
   constexpr int G = Tile<D, GS>::G, J = Tile<D, GS>::J;
   __shared__ uint32_t turn[kThreads / 32][2 * D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + warp, item = unit / c.HK;
+  const int64_t unit = ((int64_t)blockIdx.x * (kThreads / 32) + warp) >> APART, item = unit / c.HK;
   const int h = (int)(unit - item * c.HK);
   BlockOf at;
   if (item >= items || !block_of(c, item, lane, at) || at.page < 0) return;
   uint32_t *block = reinterpret_cast<uint32_t *>(c.block(at.page, h, at.p));
   const bool all = at.p >= at.pos0 && at.p + 16 <= at.end;  // every token of the block is among the rows
-#pragma unroll
-  for (int is_v = 0; is_v < 2; ++is_v) {
+  auto section_of = [&](const int is_v) {
     const T *src = is_v ? v : k;
     const int64_t stride = is_v ? v_stride : k_stride;
     uint32_t *section = block + is_v * (2 * D + 16 * G);
@@ -354,26 +354,32 @@ __global__ void __launch_bounds__(kThreads) kv_store_blocks_kernel(const KvView 
       for (int i = 0; i < D / 64; ++i)
         reinterpret_cast<uint4 *>(section)[32 * i + lane] = reinterpret_cast<const uint4 *>(turn[warp])[32 * i + lane];
     }
+  };
+  if constexpr (APART) {
+    section_of(warp & 1);
+  } else {
+    section_of(0);
+    section_of(1);
   }
 }
 
-template <typename T, int D, int GS>
+template <typename T, int D, int GS, bool APART>
 __global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c, T *__restrict__ k, int64_t k_stride, T *__restrict__ v,
                                                                   int64_t v_stride, int64_t items) {
   constexpr int G = Tile<D, GS>::G, J = Tile<D, GS>::J;
   const int lane = threadIdx.x & 31, t = lane & 3;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), item = unit / c.HK;
+  const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), unit = warp >> APART, item = unit / c.HK;
   const int h = (int)(unit - item * c.HK);
   BlockOf at;
   if (item >= items || !block_of(c, item, lane, at)) return;
-  const bool have = at.page >= 0;
+  const bool have = at.page >= 0, of_k = !APART || (warp & 1) == 0, of_v = !APART || (warp & 1) == 1;
   const uint32_t *block = reinterpret_cast<const uint32_t *>(c.block(max(at.page, 0), h, max(at.p, 0)));
   // K: a token for four lanes, as above
   uint32_t word[2][J], meta[2][G];
   uint4 vw[D / 64];
   uint32_t vm[4][G];
   const int w = lane >> 2;  // V: word w (and w + 8, ..) of tokens 2t, 2t + 1, 2t + 8, 2t + 9
-  if (have) {
+  if (have && of_k) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int tok = 8 * half + w;
@@ -390,6 +396,8 @@ __global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c
 #pragma unroll
       for (int g = 0; g < G; ++g) meta[half][g] = __ldg(block + 2 * D + tok * G + g);
     }
+  }
+  if (have && of_v) {
     const uint32_t *section = block + 2 * D + 16 * G;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) vw[i] = __ldg(reinterpret_cast<const uint4 *>(section) + (w + 8 * i) * 4 + t);
@@ -401,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int p = at.p + 8 * half + w;
-    if (p < at.pos0 || p >= at.end) continue;
+    if (!of_k || p < at.pos0 || p >= at.end) continue;
     T *row = k + (at.t0 + p - at.pos0) * k_stride + (int64_t)h * D + 8 * t;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -413,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int p = at.p + 2 * t + (j & 1) + 8 * (j >> 1);
-    if (p < at.pos0 || p >= at.end) continue;
+    if (!of_v || p < at.pos0 || p >= at.end) continue;
     T *row = v + (at.t0 + p - at.pos0) * v_stride + (int64_t)h * D + 8 * w;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
@@ -429,13 +437,25 @@ inline int parts_of(const KvView &c) { return (2 * c.HK * (c.D / 8) + 31) / 32; 
 // Blocks where sequences bring eight rows or more on average: below, most of a block's lanes would idle.
 inline bool by_blocks(const KvView &c) { return c.T >= 8 * c.B; }
 
+template <typename T, int D, int GS, bool LOAD, bool APART, typename P>
+cudaError_t blocks_run(const KvView &c, int64_t items, P *k, int64_t ks, P *v, int64_t vs, cudaStream_t st) {
+  const int64_t ctas = ((items * c.HK << APART) + kThreads / 32 - 1) / (kThreads / 32);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if constexpr (LOAD)
+    kv_load_blocks_kernel<T, D, GS, APART><<<(unsigned)ctas, kThreads, 0, st>>>(c, static_cast<T *>(k), ks, static_cast<T *>(v), vs, items);
+  else
+    kv_store_blocks_kernel<T, D, GS, APART>
+        <<<(unsigned)ctas, kThreads, 0, st>>>(c, static_cast<const T *>(k), ks, static_cast<const T *>(v), vs, items);
+  return cudaGetLastError();
+}
+// K and V by a warp each where warps are few, up to 10 of blocks per SM: what one does is then most of the call's time.  Store and
+// load, us, by one warp and by two: 100 tokens of 8 heads of 128 in fp32 12.9 and 8.8, 1000 of 4 of 256 15.0 and 10.1, of 12 of 64
+// 8.2 and 7.7; 8192 tokens of 4 of 256 (14 per SM) 26.3 and 28.5, of 12 of 64 (41) 19.0 and 21.2.
 template <typename T, int D, int GS, bool LOAD, typename P>
 cudaError_t blocks_t(const KvView &c, P *k, int64_t ks, P *v, int64_t vs, cudaStream_t st) {
-  const int64_t items = c.T / 16 + 2 * c.B, ctas = (items * c.HK + kThreads / 32 - 1) / (kThreads / 32);
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  if constexpr (LOAD) kv_load_blocks_kernel<T, D, GS><<<(unsigned)ctas, kThreads, 0, st>>>(c, static_cast<T *>(k), ks, static_cast<T *>(v), vs, items);
-  else kv_store_blocks_kernel<T, D, GS><<<(unsigned)ctas, kThreads, 0, st>>>(c, static_cast<const T *>(k), ks, static_cast<const T *>(v), vs, items);
-  return cudaGetLastError();
+  const int64_t items = c.T / 16 + 2 * c.B;
+  return items * c.HK <= 10 * 152 ? blocks_run<T, D, GS, LOAD, true>(c, items, k, ks, v, vs, st)
+                                  : blocks_run<T, D, GS, LOAD, false>(c, items, k, ks, v, vs, st);
 }
 template <typename T, bool LOAD, typename P>
 cudaError_t run_t(const KvView &c, P *k, int64_t ks, P *v, int64_t vs, cudaStream_t st) {

@@ -214,6 +214,23 @@ def test_load(q1, D, gs, heads, page, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,gs,dtype", [(64, 64, "bf16"), (128, 64, "fp32"), (128, 128, "fp16"), (256, 64, "fp32"), (256, 128, "bf16")])
+def test_many_blocks(q1, D, gs, dtype):
+    # enough blocks that a warp does a block's K and V: codes and values as the oracle's, whole blocks and cut ones
+    c = Cache(q1, [1500, 205], 16, D, gs, 32, seed=D + gs)
+    cache = c.store(q1)
+    before = cache.clone()
+    cu = torch.tensor([0, 1490, 1695], dtype=torch.int32).cuda()
+    k, v = q1.kv_load(cache, c.d_table(), c.d_lengths(), 1695, cu_seqlens=cu, dtype=DTYPES[dtype])
+    for got, vals in ((k, c.kval), (v, c.vval)):
+        want, _ = _rounded(np.concatenate([vals[0][10:], vals[1]]), dtype)
+        assert torch.equal(got.cpu(), want)
+    q1.kv_store(cache, torch.from_numpy(np.concatenate([c.k[0][10:], c.k[1]]).astype(np.float32)).cuda(),
+                torch.from_numpy(np.concatenate([c.v[0][10:], c.v[1]]).astype(np.float32)).cuda(), c.d_table(), c.d_lengths(), cu_seqlens=cu)
+    assert torch.equal(cache, before)
+
+
+@pytest.mark.gpu
 def test_equal_lengths_without_offsets(q1):
     c = Cache(q1, [70, 70, 70], 2, 128, seed=4)
     cache = c.store(q1)
