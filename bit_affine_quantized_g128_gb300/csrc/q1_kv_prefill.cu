@@ -1142,7 +1142,11 @@ cudaError_t run(const KvView &c, const KvAttention &a, int splits, float *part, 
   static std::atomic<uint64_t> ready{0};
   const int dev = current_device();
   if (not_done(ready, dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel<T, D, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, kv_prefill_kernel<T, D, GS>);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kv_prefill_kernel<T, D, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    // the warps' shares come out of what the block was launched with
+    if (e == cudaSuccess && C::kRegS > C::kRegs && at.numRegs != C::kRegs) e = cudaErrorInvalidConfiguration;
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
   }
