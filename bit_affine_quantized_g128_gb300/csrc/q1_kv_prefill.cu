@@ -847,6 +847,8 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
 #pragma unroll
               for (int j = 0; j < 32; j += 2) top = max3(top, y[j], y[j + 1]);
             }
+            // (a load of tensor memory is not ordered behind this thread's stores: P of earlier pieces, O of an earlier move)
+            wait_st();
             const float next = top > kNone ? fmaxf(M, ceilf(top * f)) : M, move = M - next;
             const float down = move >= 0.f ? 1.f : move > -126.f ? pow2f((int)move) : 0.f;
             M = next;

@@ -1,0 +1,61 @@
+"""q1_kv_attention's form for many rows (tcgen05): cases that test_kv_cache.py does not bring there."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as O
+from tests.test_kv_cache import DTYPES, Cache, _rng, _rounded
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q1():
+    from bit_affine_quantized_g128_gb300 import q1 as mod
+    mod.load_library()
+    return mod
+
+
+def _starts(new):
+    return np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+
+
+def attend(q1, c, cache, q, new, **kw):
+    """o and lse (float64) of the rows q, the tiles' form by the hint max_len (a long context has few rows take it, in parts)."""
+    kw = {"max_q": max(new), "max_len": 1 << 20, **kw}
+    o, lse = q1.kv_attention(q.cuda(), cache, c.d_table(), c.d_lengths(), cu_seqlens=torch.from_numpy(_starts(new)).cuda(),
+                             return_lse=True, **kw)
+    return o.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def bounds(c, b, qv, want, size, big, scale, dtype):
+    """Errors of o and lse of sequence b: those that test_kv_cache.check derives for tiles."""
+    D, r = c.D, qv.shape[1] // c.heads
+    kb = np.abs(c.kq[b][2]).max(0).repeat(c.gs, -1).repeat(r, 0)
+    logit = (D / 8 + 16) * 2.0 ** -24 * big + ((D / 8 + 16) * 2.0 ** -23 + 2.0 ** -22) * abs(scale) * (kb * np.abs(qv)).sum(-1)
+    info = torch.finfo(DTYPES[dtype])
+    floor = 2.0 ** -25 + c.lengths[b] * 2.0 ** -32 * np.abs(c.vval[b]).max()
+    return (info.eps / 2 * np.maximum(np.abs(want), info.tiny) + floor + 2.0 ** -10 * size + 2 * (2.0 ** -21 + logit)[..., None] * size,
+            2.0 ** -21 + logit)
+
+
+@pytest.mark.parametrize("D,HK,dtype,hint", [(64, 36, "bf16", 640), (64, 24, "fp16", 2000), (128, 24, "fp16", 640), (128, 16, "bf16", 2000),
+                                             (256, 24, "bf16", 640), (256, 12, "fp16", 2000)])
+def test_logits_that_jump_inside_a_tile(q1, D, HK, dtype, hint):
+    # logits rise by 7 octaves at one column of every tile, 32, 64 or 96 of it: a piece of P that the softmax's reference does not
+    # fit comes after pieces that are stored already (by their hints, the tiles' context is in one part, in two, in one, ..)
+    n, new = 640, 300
+    rng = _rng(D)
+    tile = 128 if D == 64 else 64
+    at = np.arange(n)
+    for jump in range(32, tile, 32):
+        level = at // tile + (at % tile >= jump)
+        k = 0.02 * rng.standard_normal((n, HK, D)) + (7 * np.log(2) * D ** -0.5 * level)[:, None, None]
+        c = Cache(q1, [n], HK, D, seed=D + jump, k=[k])
+        q, qv = _rounded(1 + 0.02 * rng.standard_normal((new, 2 * HK, D)), dtype)
+        o, lse = attend(q1, c, c.store(q1), q, [new], max_len=hint)
+        some = [0, 1, 31, 32, 77, new - 1]
+        want, want_lse, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], np.array(some) + n - new, D ** -0.5)
+        err, lerr = bounds(c, 0, qv[some], want, size, big, D ** -0.5, dtype)
+        assert (np.abs(o[some] - want) <= err).all() and (np.abs(lse[some] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse)).all(), jump
+    assert q1.device_errors() == 0
