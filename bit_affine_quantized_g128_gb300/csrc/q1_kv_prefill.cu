@@ -219,7 +219,7 @@ __device__ __forceinline__ void sync_all() {
   if constexpr (CG == 1) __syncthreads();
   else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// an int of any CTA of the pair, set by one of its roles
+// an int of any CTA of the pair, set by one of its roles before the last sync_all
 template <int CG>
 __device__ __forceinline__ int any_flag(const volatile int *flag) {
   if constexpr (CG == 1) return *flag;
@@ -905,6 +905,9 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       // O's last product.  With two buffers of S per row tile the last two may be open (S of a tile only says that the
       // product two tiles before is complete), and o_done's parity cannot tell them apart: all MMAs, then.
       if (ok && rows.tiles > 0) ok = C::NB == QT ? wait_warp(&bars->o_done[q], (rows.tiles - 1) & 1, bars) : wait_warp(&bars->drain, 0, bars);
+      // every role meets here: bad_v of both CTAs is final, and seen
+      fence_before();
+      sync_all<CG>();
       fence_after();
       float inv = splits > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L;
       if (ok && any_flag<CG>(&bars->bad_v)) {
@@ -1009,6 +1012,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       const X x{c, b, hk, warp & 3, lane, rank, rows.first, c_kv_stall ? 0 : rows.tiles};
       if (warp < C::kFirstV) x.run_k(bars, sm);
       else x.run_v(bars, sm, rows.len);
+      sync_all<CG>();  // (the softmax's, before it looks at bad_v)
     } while (next());
   } else {
     if constexpr (C::kRegM < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegM));
@@ -1071,6 +1075,9 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
         while (!mbar_try(&bars->drain, 0) && global_ns() - since < c_kv_wait_ns) {
         }
       }
+      fence_before();
+      sync_all<CG>();
+      fence_after();
     } while (next());
   }
   if (warp == C::kMma) asm volatile("tcgen05.dealloc.cta_group::%2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512), "n"(CG));

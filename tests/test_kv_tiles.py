@@ -59,3 +59,29 @@ def test_logits_that_jump_inside_a_tile(q1, D, HK, dtype, hint):
         err, lerr = bounds(c, 0, qv[some], want, size, big, D ** -0.5, dtype)
         assert (np.abs(o[some] - want) <= err).all() and (np.abs(lse[some] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse)).all(), jump
     assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("D,gs,dtype", [(64, 64, "bf16"), (128, 64, "bf16"), (128, 128, "fp16"), (256, 64, "fp16"), (256, 128, "bf16")])
+def test_nan_in_one_group_of_v(q1, D, gs, dtype):
+    # of a token in the middle, each group in turn (a CTA of a pair has half of the channels): the rows that see it have NaN in
+    # that group's channels, the rows before it what they have without it
+    n, HK, new, at = 500, 24, 300, 333
+    c = Cache(q1, [n], HK, D, gs, seed=D + gs)
+    cache = c.store(q1)
+    q, qv = _rounded(_rng(D).standard_normal((new, 2 * HK, D)), dtype)
+    pos = np.arange(new) + n - new
+    some = [0, 100, int(np.argmax(pos == at)) - 1, int(np.argmax(pos == at)), 200, new - 1]
+    want, _, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], pos[some], D ** -0.5)
+    err, _ = bounds(c, 0, qv[some], want, size, big, D ** -0.5, dtype)
+    hit = pos[some] >= at
+    for g in range(D // gs):
+        k, v = (torch.from_numpy(x[0][at:at + 1].astype(np.float32)).cuda() for x in (c.k, c.v))
+        v[:, :, g * gs] = float("nan")
+        one = cache.clone()
+        q1.kv_store(one, k, v, c.d_table(), torch.tensor([at + 1], dtype=torch.int32).cuda(),
+                    cu_seqlens=torch.tensor([0, 1], dtype=torch.int32).cuda())
+        for hint in (n, 2000, 1 << 20):
+            o, _ = attend(q1, c, one, q, [new], max_len=hint)
+            assert np.isnan(o[pos >= at][:, :, g * gs:(g + 1) * gs]).all(), (g, hint)
+            assert (np.abs(o[some] - want) <= err)[~hit].all() and not np.isnan(o[pos < at]).any(), (g, hint)
+    assert q1.device_errors() == 0
