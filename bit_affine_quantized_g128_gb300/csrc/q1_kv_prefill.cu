@@ -909,17 +909,18 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       fence_before();
       sync_all<CG>();
       fence_after();
-      float inv = splits > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L;
+      const float inv = splits > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L;
+      uint32_t nan = 0;  // a bit per group of channels
       if (ok && any_flag<CG>(&bars->bad_v)) {
-        // rows that see such a token become NaN
+        // rows that see such a token become NaN in its group's channels
         for (int p = max(lo + 1, 0); p <= min(hi, (int)min((int64_t)rows.len, c.table_width << c.page_shift) - 1); ++p) {
           const int page = c.page(b, p);
           if (page < 0) continue;
           const unsigned char *blk = c.block(page, hk, p) + 16 * D + 64 * G + (p & 15) * G * 4;
-          for (int g = 0; g < G; ++g)
-            if (beyond_fp16(__ldg(reinterpret_cast<const uint32_t *>(blk) + g))) inv = __int_as_float(0x7fc00000);
+          for (int g = 0; g < G; ++g) nan |= (uint32_t)beyond_fp16(__ldg(reinterpret_cast<const uint32_t *>(blk) + g)) << g;
         }
       }
+      auto factor = [&](int k) { return nan >> (k / GS) & 1u ? __int_as_float(0x7fc00000) : inv; };  // of channel k and the others of its group
       __syncwarp();
       // rows of o through shared memory (Q's tile; K's stages for heads of 256: no MMA reads them any more), so that a
       // warp stores whole rows
@@ -945,13 +946,14 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0.f;
           }
+          const float by = factor(k);
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             // columns hold channels 0 4 1 5 2 6 3 7
             const int at = j & ~7, odd = (j >> 2) & 1;
-            sts4(stage + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4), __float_as_uint(o[at + odd] * inv), __float_as_uint(o[at + odd + 2] * inv),
-                 __float_as_uint(o[at + odd + 4] * inv), __float_as_uint(o[at + odd + 6] * inv));
+            sts4(stage + lane * 128 + (((j >> 2) ^ (lane & 7)) << 4), __float_as_uint(o[at + odd] * by), __float_as_uint(o[at + odd + 2] * by),
+                 __float_as_uint(o[at + odd + 4] * by), __float_as_uint(o[at + odd + 6] * by));
           }
           __syncwarp();
 #pragma unroll 1
@@ -961,7 +963,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
             if (ok && row0 + from < rows.rows) reinterpret_cast<uint4 *>(part_of(row0 + from) + k)[piece] = w;
           }
         }
-        if (ok && mine < rows.rows) *reinterpret_cast<float2 *>(part_of(mine) + D) = make_float2(M - kShift, inv == 1.f ? L : inv);
+        if (ok && mine < rows.rows) *reinterpret_cast<float2 *>(part_of(mine) + D) = make_float2(M - kShift, L);
         continue;
       }
 #pragma unroll 1
@@ -974,8 +976,9 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0.f;
         }
+        const float by = factor(k);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = inv == 0.f ? 0.f : o[j] * inv;
+        for (int j = 0; j < 32; ++j) o[j] = by == 0.f ? 0.f : o[j] * by;
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           // columns hold channels 0 4 1 5 2 6 3 7

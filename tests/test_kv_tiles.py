@@ -85,3 +85,34 @@ def test_nan_in_one_group_of_v(q1, D, gs, dtype):
             assert np.isnan(o[pos >= at][:, :, g * gs:(g + 1) * gs]).all(), (g, hint)
             assert (np.abs(o[some] - want) <= err)[~hit].all() and not np.isnan(o[pos < at]).any(), (g, hint)
     assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("D,gs,dtype", [(64, 64, "fp16"), (128, 64, "fp16"), (128, 128, "bf16"), (256, 64, "bf16"), (256, 128, "fp16")])
+def test_nan_in_v_keeps_to_its_group(q1, D, gs, dtype):
+    # the other groups' channels, and lse, are what they are without it; by tiles in one part and in several, and by few rows
+    n, HK, new, at = 500, 24, 300, 333
+    c = Cache(q1, [n], HK, D, gs, seed=D + gs + 1)
+    cache = c.store(q1)
+    q, qv = _rounded(_rng(D).standard_normal((new, 2 * HK, D)), dtype)
+    pos = np.arange(new) + n - new
+    some = [0, 100, 200, new - 1]
+    want, want_lse, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], pos[some], D ** -0.5)
+    err, lerr = bounds(c, 0, qv[some], want, size, big, D ** -0.5, dtype)
+    hit = pos[some] >= at
+    for g in range(D // gs):
+        k, v = (torch.from_numpy(x[0][at:at + 1].astype(np.float32)).cuda() for x in (c.k, c.v))
+        v[:, :, g * gs + 5] = float("nan")
+        one = cache.clone()
+        q1.kv_store(one, k, v, c.d_table(), torch.tensor([at + 1], dtype=torch.int32).cuda(),
+                    cu_seqlens=torch.tensor([0, 1], dtype=torch.int32).cuda())
+        ch = np.zeros(D, bool)
+        ch[g * gs:(g + 1) * gs] = True
+        nan = hit[:, None, None] & ch
+        for hint in (n, 2000, 1 << 20):
+            o, lse = attend(q1, c, one, q, [new], max_len=hint)
+            assert np.array_equal(np.isnan(o[some]), np.broadcast_to(nan, want.shape)), (g, hint)
+            assert (np.abs(o[some] - want) <= err)[~np.broadcast_to(nan, want.shape)].all(), (g, hint)
+            assert (np.abs(lse[some] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse)).all(), (g, hint)
+        o, lse = attend(q1, c, one, q[-1:], [1], max_len=n)
+        assert np.isnan(o[..., ch]).all() and (np.abs(o[0] - want[-1]) <= err[-1])[:, ~ch].all() and np.isfinite(lse).all()
+    assert q1.device_errors() == 0
