@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
       uint32_t m0[G], m1[G];  // V's
       lds_words(at + 16 * D + 64 * G + g * G * 4, m0);
       lds_words(at + 16 * D + 64 * G + (g + 8) * G * 4, m1);
+      uint32_t see = 0;  // a bit per value of x, where the block is not whole
       if (!whole) {
         bool seen0 = false, seen1 = false;
 #pragma unroll
@@ -436,6 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
             const bool v0 = p0 > lo[nt][k] && p0 <= hi[nt][k], v1 = p0 + 8 > lo[nt][k] && p0 + 8 <= hi[nt][k];
             x[nt][k] = v0 ? x[nt][k] : -INFINITY;
             x[nt][k + 2] = v1 ? x[nt][k + 2] : -INFINITY;
+            see |= (uint32_t)v0 << (4 * nt + k) | (uint32_t)v1 << (4 * nt + k + 2);
             seen0 |= v0;
             seen1 |= v1;
           }
@@ -508,12 +510,12 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
           if (whole) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) bias[nt][i][k] = fmaf(b0, x[nt][k], fmaf(b1, x[nt][k + 2], bias[nt][i][k]));
-          } else {  // a token that other rows see may have a NaN
+          } else {  // a token that other rows see may have a NaN; one that this row sees shows it whatever its weight
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = x[nt][k] == 0.f ? 0.f : y[k];
+            for (int k = 0; k < 4; ++k) y[k] = see >> (4 * nt + k) & 1u ? y[k] : 0.f;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              bias[nt][i][k] += (x[nt][k] == 0.f ? 0.f : x[nt][k] * b0) + (x[nt][k + 2] == 0.f ? 0.f : x[nt][k + 2] * b1);
+              bias[nt][i][k] += (see >> (4 * nt + k) & 1u ? x[nt][k] * b0 : 0.f) + (see >> (4 * nt + k + 2) & 1u ? x[nt][k + 2] * b1 : 0.f);
           }
           const uint32_t h0 = half2_bits(y[0], y[1]), h1 = half2_bits(y[2], y[3]);
           pb[nt][i][0][0] = movmatrix(h0);

@@ -116,3 +116,21 @@ def test_nan_in_v_keeps_to_its_group(q1, D, gs, dtype):
         o, lse = attend(q1, c, one, q[-1:], [1], max_len=n)
         assert np.isnan(o[..., ch]).all() and (np.abs(o[0] - want[-1]) <= err[-1])[:, ~ch].all() and np.isfinite(lse).all()
     assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_nan_of_vanishing_weight(q1, dtype):
+    # a token whose weight is below fp32's least value is seen all the same: its NaN shows, in a block that the row sees all of
+    # and in one that it sees in part, however the call's hints split the work
+    n, D = 40, 128
+    rng = _rng(10)
+    for at in (5, 35):
+        k, v = rng.standard_normal((n, 1, D)), rng.standard_normal((n, 1, D))
+        k[:, 0, 0], k[at, 0, 0] = 10.0, -10.0
+        v[at] = np.nan
+        c = Cache(q1, [n], 1, D, seed=11, k=[k], v=[v])
+        q = np.zeros((1, 2, D))
+        q[..., 0] = 20.0
+        for hint in (n, 1 << 20):
+            o, lse = attend(q1, c, c.store(q1), _rounded(q, dtype)[0], [1], max_len=hint, scale=1.0)
+            assert np.isnan(o).all() and np.isfinite(lse).all(), (at, hint)
