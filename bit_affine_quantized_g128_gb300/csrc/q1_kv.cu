@@ -363,6 +363,25 @@ __global__ void __launch_bounds__(kThreads) kv_store_blocks_kernel(const KvView 
   }
 }
 
+// Rows before the first sequence and behind the last, which no block has: zeros, by the call's warps in turn.
+template <typename T>
+__device__ __forceinline__ void zero_rest(const KvView &c, T *k, int64_t k_stride, T *v, int64_t v_stride, int64_t warp, int lane) {
+  if (!c.cu) return;
+  int64_t first, last, skip;
+  c.range(0, first, skip);
+  c.range(c.B - 1, skip, last);
+  last = max(last, first);
+  const int64_t n = first + (c.T - last), warps = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t i = warp; i < n; i += warps) {
+    const int64_t t = i < first ? i : last + (i - first);
+    for (int w = lane; w < c.HK * c.D / 8; w += 32) {
+      const float none[8] = {};
+      store8(k + t * k_stride + 8 * w, none);
+      store8(v + t * v_stride + 8 * w, none);
+    }
+  }
+}
+
 template <typename T, int D, int GS, bool APART>
 __global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c, T *__restrict__ k, int64_t k_stride, T *__restrict__ v,
                                                                   int64_t v_stride, int64_t items) {
@@ -370,6 +389,7 @@ __global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c
   const int lane = threadIdx.x & 31, t = lane & 3;
   const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), unit = warp >> APART, item = unit / c.HK;
   const int h = (int)(unit - item * c.HK);
+  zero_rest(c, k, k_stride, v, v_stride, warp, lane);
   BlockOf at;
   if (item >= items || !block_of(c, item, lane, at)) return;
   const bool have = at.page >= 0, of_k = !APART || (warp & 1) == 0, of_v = !APART || (warp & 1) == 1;

@@ -772,7 +772,8 @@ def kv_load(cache: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tenso
     """The cached K and V of the last tokens of each sequence, as `dtype`.
 
     With cu_seqlens, `rows` tokens in all, cu_seqlens[b+1] - cu_seqlens[b] of sequence b: two [rows, heads, dim].
-    Without it, `rows` tokens of each sequence: two [B, rows, heads, dim].  Tokens without a page are zeros."""
+    Without it, `rows` tokens of each sequence: two [B, rows, heads, dim].  Tokens without a page, and rows of no sequence,
+    are zeros."""
     _kv_on_device(("cache", cache), block_table=block_table)
     dev, packed = cache.device, cu_seqlens is not None
     if dtype not in _DT:
@@ -802,7 +803,8 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor
     window > 0 only j > i - window.  scale defaults to dim ** -0.5.  `max_q` (the longest sequence's rows) and
     `max_len` (the largest of lengths) are best given: they pick the kernels and how the work is split; without them T
     (or L) and the block table's width count.  Returns o like q, and with return_lse the fp32 logarithms of the sums
-    of exponentials, o without its last dimension; a row that sees nothing gets 0 and -inf."""
+    of exponentials, o without its last dimension; a row that sees nothing gets 0 and -inf.  Rows of no sequence (before
+    cu_seqlens[0], from cu_seqlens[B] on) are left as they are in `out`, undefined without it."""
     _kv_on_device(("q", q), cache=cache, block_table=block_table)
     dev, dtype, packed = q.device, q.dtype, cu_seqlens is not None
     dt = _x_dtype(q, "q")

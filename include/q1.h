@@ -396,9 +396,12 @@ q1_status q1_sample(const q1_sample_args *args, q1_stream stream);
  *   cu_seqlens  device int32 [B+1], ascending from 0 to T: rows [cu[b], cu[b+1]) of the
  *               call's T rows belong to sequence b and stand for its last positions,
  *               the last of them for position lengths[b] - 1.  NULL: T / B rows each.
- *               Offsets that leave [0, T] or decrease are cut to it.  Rows with a
- *               negative position (more rows than tokens) are not stored, load as
- *               zeros and attend to nothing.
+ *               Rows with a negative position (more rows than tokens) are not
+ *               stored, load as zeros and attend to nothing.  Rows before cu[0] or
+ *               from cu[B] on belong to no sequence: they are not stored, load as
+ *               zeros, and attention leaves o and lse there as they were.  Offsets
+ *               that leave [0, T] or decrease are cut to it: the results of such a
+ *               call are undefined, its accesses stay inside the arrays.
  * The three calls take the same description, so a step is: store the new K and V,
  * then attend.  lengths, block_table and cu_seqlens are read on the device: a
  * captured graph follows their contents.  D 64, 128 or 256; group_size 64 or 128, at most

@@ -118,6 +118,24 @@ def test_nan_in_v_keeps_to_its_group(q1, D, gs, dtype):
     assert q1.device_errors() == 0
 
 
+@pytest.mark.parametrize("T,new", [(40, [1, 0, 2, 1, 1]), (47, [20, 0, 13]), (200, [90, 33, 40]), (9, [0, 0]), (64, [0])])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_load_of_rows_of_no_sequence(q1, T, new, dtype):
+    # before the first sequence and behind the last: zeros, by either form
+    c = Cache(q1, [95] * len(new), 3, 64, seed=9)
+    cache = c.store(q1)
+    for first in {0, 3, T - sum(new)} if sum(new) else {0, 5, T}:
+        cu = _starts(new) + first
+        big = torch.full((1 << 22,), float("nan"), device="cuda")    # what the allocator hands out next
+        del big
+        for got, vals in zip(q1.kv_load(cache, c.d_table(), c.d_lengths(), T, cu_seqlens=torch.from_numpy(cu).cuda(), dtype=DTYPES[dtype]),
+                             (c.kval, c.vval)):
+            want = np.zeros((T, 3, 64), np.float32)
+            for b, n in enumerate(new):
+                want[cu[b]:cu[b + 1]] = vals[b][95 - n:]
+            assert torch.equal(got.cpu(), torch.from_numpy(want).to(DTYPES[dtype])), first
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_nan_of_vanishing_weight(q1, dtype):
     # a token whose weight is below fp32's least value is seen all the same: its NaN shows, in a block that the row sees all of
