@@ -382,17 +382,13 @@ __device__ __forceinline__ void zero_rest(const KvView &c, T *k, int64_t k_strid
   }
 }
 
-template <typename T, int D, int GS, bool APART>
-__global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c, T *__restrict__ k, int64_t k_stride, T *__restrict__ v,
-                                                                  int64_t v_stride, int64_t items) {
+// A block's rows, its K, its V or both
+template <typename T, int D, int GS>
+__device__ __forceinline__ void load_block(const KvView &c, const BlockOf &at, int h, int lane, bool of_k, bool of_v, T *k, int64_t k_stride,
+                                           T *v, int64_t v_stride) {
   constexpr int G = Tile<D, GS>::G, J = Tile<D, GS>::J;
-  const int lane = threadIdx.x & 31, t = lane & 3;
-  const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), unit = warp >> APART, item = unit / c.HK;
-  const int h = (int)(unit - item * c.HK);
-  zero_rest(c, k, k_stride, v, v_stride, warp, lane);
-  BlockOf at;
-  if (item >= items || !block_of(c, item, lane, at)) return;
-  const bool have = at.page >= 0, of_k = !APART || (warp & 1) == 0, of_v = !APART || (warp & 1) == 1;
+  const int t = lane & 3;
+  const bool have = at.page >= 0;
   const uint32_t *block = reinterpret_cast<const uint32_t *>(c.block(max(at.page, 0), h, max(at.p, 0)));
   // K: a token for four lanes, as above
   uint32_t word[2][J], meta[2][G];
@@ -450,6 +446,17 @@ __global__ void __launch_bounds__(kThreads) kv_load_blocks_kernel(const KvView c
       store8(row + 64 * i, x);
     }
   }
+}
+
+template <typename T, int D, int GS, bool APART>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 3 : 4) kv_load_blocks_kernel(const KvView c, T *__restrict__ k, int64_t k_stride, T *__restrict__ v,
+                                                                  int64_t v_stride, int64_t items) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), unit = warp >> APART, item = unit / c.HK;
+  BlockOf at;
+  if (item < items && block_of(c, item, lane, at))
+    load_block<T, D, GS>(c, at, (int)(unit - item * c.HK), lane, !APART || (warp & 1) == 0, !APART || (warp & 1) == 1, k, k_stride, v, v_stride);
+  zero_rest(c, k, k_stride, v, v_stride, warp, lane);
 }
 
 // warps per token
