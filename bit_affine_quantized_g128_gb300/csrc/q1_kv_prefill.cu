@@ -25,10 +25,14 @@
 // Exactness.  K enters as scale q, which fp16 holds exactly (8 bits of scale, 4 of
 // code), and the biases through one more k16 step: columns bias_g (twice per
 // group) of K against the high and low fp16 half of the sum of Q's channels in group g.
-// So S is exact up to fp32 sums.  Q is fp16, scaled by a power of two per row so that its
+// So S is exact up to fp32 sums, as far as fp16 reaches: K and V are multiplied with a power of
+// two that brings the largest scale or bias that a tile's rows see to 2^-2 or more (V: 2^-5), so that
+// scales and biases of K are exact down to 2^-15 of the largest and off by at most 2^-23 of it below.  It is a fixed one, and a tile
+// that it turns out not to suit is done once more with one that does (a prompt of 8192 tokens 486 us, 481 without the
+// search for the largest, 925 done twice).  Q is fp16, scaled by a power of two per row so that its
 // largest value lies in [2^7, 2^8): bf16 and fp16 inputs are exact down to 2^-22 of
 // that.  A 17th column of K is -inf where a token's page is missing, against 1 in Q.
-// V is scale q + bias rounded to fp16 (2^-12), P is rounded to fp16 (2^-12); the sum
+// V is scale q + bias rounded to fp16 (2^-11 of it, or 2^-20 of the largest scale or bias), P is rounded to fp16 (2^-11); the sum
 // of P is fp32 of the unrounded values.  M is a reference that moves when a tile's P would
 // overflow fp16; 2^7 keeps all of P that matters among fp16's normal values.
 //
@@ -86,6 +90,7 @@ __device__ __forceinline__ unsigned long long global_ns() {
 struct Rows {
   int64_t t0;
   int rows, len, pos0, first, tiles;  // rows of the sequence, its tokens, position of its first row; first position, number of tiles
+  int begin, end;                     // what any of the CTA's rows sees
   template <int ROWS, int BN>
   __device__ __forceinline__ bool set(const KvView &c, const KvAttention &a, int64_t b, int tile, int split, int splits) {
     int64_t t1;
@@ -97,9 +102,9 @@ struct Rows {
     len = max(c.lengths[b], 0);
     pos0 = len - n;
     const int row0 = tile * ROWS, row1 = min(row0 + ROWS, rows) - 1;
-    int end = a.causal ? pos0 + row1 / r + 1 : (pos0 + row1 / r < 0 ? 0 : len);
+    end = a.causal ? pos0 + row1 / r + 1 : (pos0 + row1 / r < 0 ? 0 : len);
     end = (int)min((int64_t)end, c.table_width << c.page_shift);
-    const int begin = a.window ? (int)max((int64_t)pos0 + row0 / r - a.window + 1, (int64_t)0) : 0;
+    begin = a.window ? (int)max((int64_t)pos0 + row0 / r - a.window + 1, (int64_t)0) : 0;
     first = begin / BN * BN;
     tiles = end > begin ? (end - first + BN - 1) / BN : 0;
     const int64_t all_tiles = tiles;
@@ -109,9 +114,9 @@ struct Rows {
     return true;
   }
   __device__ __forceinline__ void put(const Rows &x) volatile {
-    t0 = x.t0, rows = x.rows, len = x.len, pos0 = x.pos0, first = x.first, tiles = x.tiles;
+    t0 = x.t0, rows = x.rows, len = x.len, pos0 = x.pos0, first = x.first, tiles = x.tiles, begin = x.begin, end = x.end;
   }
-  __device__ __forceinline__ Rows get() const volatile { return {t0, rows, len, pos0, first, tiles}; }
+  __device__ __forceinline__ Rows get() const volatile { return {t0, rows, len, pos0, first, tiles, begin, end}; }
 };
 
 struct Bars {
@@ -120,8 +125,24 @@ struct Bars {
   uint32_t tmem_base;
   volatile Rows rows;              // here, as no role has registers to keep all of it
   volatile int tile;
-  volatile int abort_flag, bad_v;  // a wait ran out; V has values beyond fp16
+  volatile int abort_flag, bad_v;  // a wait ran out; V has a NaN or an infinity
+  // K and V are multiplied with 2^up_k and 2^up_v; the largest scale or bias of those that rows of the pair see (bits of an fp32);
+  // whether this is the second time that the CTA does its tile
+  volatile int up_k, up_v, second;
+  uint32_t top_k, top_v;
 };
+// Before scales, biases and values are rounded to fp16 their sizes are brought into its range, by a power of two that O and the
+// logits' factor give back.  It starts at 2^kUpK and 2^kUpV, which suits a largest scale or bias in [2^-6, 2^8) for K and [2^-12,
+// 2^5) for V; where a CTA finds another one it does its tile a second time, with that one brought into [2^11, 2^12) (9 times that,
+// the largest value, is below fp16's).
+constexpr int kUpK = 4, kUpV = 7, kLowK = -2, kLowV = -5, kHigh = 12;
+__device__ __forceinline__ int octave(uint32_t bits) { return (int)(bits >> 23) - 127; }
+__device__ __forceinline__ bool unsuited(uint32_t top, int up, int low) {
+  return top != 0 && (octave(top) + up < low || octave(top) + up >= kHigh);
+}
+__device__ __forceinline__ bool once_more(const Bars *bars) {
+  return !bars->second && (unsuited(bars->top_k, bars->up_k, kLowK) || unsuited(bars->top_v, bars->up_v, kLowV));
+}
 
 // Whether a wait gives up: its limit has run out, or another role has given up.  The clock is read on every 64th try only (a
 // read takes hundreds of cycles), the first time to start it.
@@ -228,6 +249,19 @@ __device__ __forceinline__ int any_flag(const volatile int *flag) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(of_rank(a, 0)) : "memory");
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(y) : "r"(of_rank(a, 1)) : "memory");
   return x | y;
+}
+// raises a word of every CTA of the pair to the largest of the warp's values (none negative)
+template <int CG>
+__device__ __forceinline__ void raise(uint32_t *word, float x, int lane) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(x));
+  if (lane != 0 || top == 0) return;
+  if constexpr (CG == 1) {
+    atomicMax(word, top);
+  } else {
+#pragma unroll
+    for (uint32_t k = 0; k < CG; ++k)
+      asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(of_rank(smem_u32(word), k)), "r"(top) : "memory");
+  }
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -340,13 +374,15 @@ __device__ __forceinline__ void expand(uint32_t w, const Exponents &x, __half2 (
 __device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// whether a group of V has a value that fp16 does not hold (none that was stored does, but for a NaN)
-__device__ __forceinline__ bool beyond_fp16(uint32_t meta) {
-  return !(fmaf(8.f, fabsf(__uint_as_float(meta << 16)), fabsf(__uint_as_float(meta & 0xFFFF0000u))) <= 65504.f);
+// the larger of a group's scale and bias, by size; NaN or infinite where one of them is (of those that were stored, NaN)
+__device__ __forceinline__ float meta_size(uint32_t meta) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(__uint_as_float(meta << 16))), "f"(fabsf(__uint_as_float(meta & 0xFFFF0000u))));
+  return r;
 }
-// scale and bias of a metadata word as fp16, twice each
-__device__ __forceinline__ void split_meta(uint32_t meta, __half2 &s, __half2 &o) {
-  const uint32_t h = half2_bits(__uint_as_float(meta << 16), __uint_as_float(meta & 0xFFFF0000u));
+// scale and bias of a metadata word, times up, as fp16, twice each
+__device__ __forceinline__ void split_meta(uint32_t meta, float up, __half2 &s, __half2 &o) {
+  const uint32_t h = half2_bits(up * __uint_as_float(meta << 16), up * __uint_as_float(meta & 0xFFFF0000u));
   s = half2_of(__byte_perm(h, h, 0x1010));
   o = half2_of(__byte_perm(h, h, 0x3232));
 }
@@ -418,8 +454,10 @@ struct Expander {
   static constexpr int G = C::G, KW = D / 32;
   const KvView &c;
   int64_t b;
-  int hk, warp, lane, rank, first, tiles;
+  int hk, warp, lane, rank, first, tiles, begin, end;
+  float up;  // what K or V is multiplied with
   Exponents exps;
+  __device__ __forceinline__ bool seen(int p) const { return (unsigned)(p - begin) < (unsigned)(end - begin); }
   __device__ __forceinline__ int page_of(int p, bool in) const { return in ? c.page(b, p) : -1; }
   __device__ __forceinline__ const unsigned char *block(int page, int p) const {
     const int per = 1 << (c.page_shift - 4);
@@ -455,12 +493,15 @@ struct Expander {
     ldg_words(p + 8 * D + t * G * 4, r.meta);
   }
   // scale q into the tile, the biases (twice) into the extra columns; both addresses are this lane's
-  __device__ __forceinline__ void put_k(const KHalf &r, uint32_t dst, uint32_t extra) const {
+  __device__ __forceinline__ void put_k(const KHalf &r, uint32_t dst, uint32_t extra, bool in_sight, float &top) const {
     __half2 s[G], o[G];
     uint32_t e[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < G; ++k) {
-      split_meta(r.have ? r.meta[k] : 0u, s[k], o[k]);
+      const uint32_t meta = r.have ? r.meta[k] : 0u;
+      const float size = meta_size(meta);
+      if (in_sight && size < INFINITY) top = fmaxf(top, size);
+      split_meta(meta, up, s[k], o[k]);
       e[k] = bits(o[k]);
     }
 #pragma unroll
@@ -480,6 +521,7 @@ struct Expander {
   }
   __device__ __forceinline__ void run_k(Bars *bars, uint32_t sm) const {
     KHalf r0, r1;
+    float top = 0.f;
     const int units = tiles * HK;
     auto page = [&](int v) { return page_of(k_pos(v), v < units); };
     fetch_k(0, page(0), r0);
@@ -489,7 +531,8 @@ struct Expander {
     auto step = [&](int v, KHalf &r) {
       if (v % HK == 0 && !wait_warp(&bars->k_empty[s], ph, bars)) return false;
       const int row = 8 * k_half(v) + token();
-      put_k(r, sm + C::kK + s * C::kStageK + swz(row, lane & 3), sm + C::kX + swz(C::x_row(s) + row, C::x_piece(s) + (lane & 1)));
+      put_k(r, sm + C::kK + s * C::kStageK + swz(row, lane & 3), sm + C::kX + swz(C::x_row(s) + row, C::x_piece(s) + (lane & 1)),
+            seen(k_pos(v) + 8 * (k_half(v) & 1) + token()), top);
       const int next = ahead;
       ahead = page(v + 3);
       if (v % HK == HK - 1) {
@@ -505,6 +548,7 @@ struct Expander {
 #pragma unroll 1
     for (int v = 0; v < units; v += 2)
       if (!step(v, r0) || (v + 1 < units && !step(v + 1, r1))) break;
+    raise<C::CG>(&bars->top_k, top, lane);
   }
 
   // ---- V: 64 channels of a block, VI of them per tile and warp.  Where there are two, a half warp has one each, words
@@ -533,19 +577,21 @@ struct Expander {
     for (int j = 0; j < 4; ++j)
       r.meta[j] = __ldg(reinterpret_cast<const uint32_t *>(p + 8 * D) + (2 * t + (j & 1) + 8 * (j >> 1)) * G + 64 * g / GS);
   }
-  // scale q + bias; tokens with values beyond fp16 become 0, which no P of 0 turns into NaN, and are reported if they are
-  // among the first `left` of the tile, the sequence's own
-  __device__ __forceinline__ bool put_v(const VPart &r, uint32_t dst, int left) const {
+  // scale q + bias; tokens with values beyond fp16 become 0, which no P of 0 turns into NaN: those that no row sees, and
+  // else NaN and infinities, which are reported (or what the second time brings into range)
+  __device__ __forceinline__ bool put_v(const VPart &r, uint32_t dst, int pos, float &top) const {
     const int row0 = 16 * v_block() + 2 * v_time();
     dst += v_group() * C::kBoxV;
     bool bad = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = row0 + (j & 1) + 8 * (j >> 1);
-      const bool out = beyond_fp16(r.meta[j]);
-      bad |= r.have && out && row < left;
+      const float size = meta_size(r.meta[j]);
+      const bool finite = size < INFINITY, in_sight = r.have && seen(pos + row);
+      bad |= in_sight && !finite;
+      if (in_sight && finite) top = fmaxf(top, size);
       __half2 s, o;
-      split_meta(r.have && !out ? r.meta[j] : 0u, s, o);
+      split_meta(r.have && size * up < (float)(1 << kHigh) ? r.meta[j] : 0u, up, s, o);
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
         const uint4 &u = r.code[w];
@@ -557,8 +603,9 @@ struct Expander {
     }
     return bad;
   }
-  __device__ __forceinline__ void run_v(Bars *bars, uint32_t sm, int len) const {
+  __device__ __forceinline__ void run_v(Bars *bars, uint32_t sm) const {
     VPart r0, r1;
+    float top = 0.f;
     auto page = [&](int i) { return page_of(v_pos(i), i < tiles); };
     fetch_v(0, page(0), r0);
     fetch_v(1, page(1), r1);
@@ -566,7 +613,7 @@ struct Expander {
     uint32_t s = 0, ph = 1;
     auto step = [&](int i, VPart &r) {
       if (!wait_warp(&bars->v_empty[s], ph, bars)) return false;
-      if (put_v(r, sm + C::kV + s * C::kStageV, len - first - i * C::BN)) bars->bad_v = 1;
+      if (put_v(r, sm + C::kV + s * C::kStageV, first + i * C::BN, top)) bars->bad_v = 1;
       const int next = ahead;
       ahead = page(i + 3);
       publish_smem<C::CG>(&bars->v_full[s], lane, rank);
@@ -580,6 +627,7 @@ struct Expander {
 #pragma unroll 1
     for (int i = 0; i < tiles; i += 2)
       if (!step(i, r0) || (i + 1 < tiles && !step(i + 1, r1))) break;
+    raise<C::CG>(&bars->top_v, top, lane);
   }
 };
 
@@ -729,10 +777,12 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
   Rows rows0;
   if (!rows0.set<CG * C::kRows, BN>(c, a, b, tile0, split, splits)) return;
 
-  auto init = [&](bool again, const Rows &rows, int tile) {
+  auto init = [&](bool again, const Rows &rows, int tile, int up_k, int up_v, bool second) {
     if (tid == 0) {
       bars->rows.put(rows);
       bars->tile = tile;
+      bars->up_k = up_k, bars->up_v = up_v, bars->second = second;
+      bars->top_k = bars->top_v = 0;
       if (again)
         for (uint64_t *bar = bars->k_full; bar <= &bars->drain; ++bar)
           asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -753,7 +803,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     }
   };
   if (tid == 0) bars->abort_flag = 0;
-  init(false, rows0, tile0);
+  init(false, rows0, tile0, kUpK, kUpV, false);
   if (warp == C::kMma) {
     asm volatile("tcgen05.alloc.cta_group::%2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)), "r"(512),
                  "n"(CG)
@@ -765,18 +815,23 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
-  // Every role goes through the CTA's tiles (one, unless the hint max_q was too small)
-  // and meets the others at the end of each; false: no other tile.
+  // Every role goes through the CTA's tiles (one, unless the hint max_q was too small; twice, where the sizes of K or V turn out
+  // not to suit) and meets the others at the end of each; false: no other tile.
   auto next = [&]() -> bool {
     fence_before();
     sync_all<CG>();
     fence_after();
     Rows rows;
-    const int tile = bars->tile + tiles;
+    const bool second = once_more(bars);
+    const uint32_t top_k = bars->top_k, top_v = bars->top_v;
+    int up_k = bars->up_k, up_v = bars->up_v;
+    if (second && unsuited(top_k, up_k, kLowK)) up_k = min(kHigh - 1 - octave(top_k), 100);
+    if (second && unsuited(top_v, up_v, kLowV)) up_v = min(kHigh - 1 - octave(top_v), 100);
+    const int tile = bars->tile + (second ? 0 : tiles);
     const bool more = !any_flag<CG>(&bars->abort_flag) && rows.set<CG * C::kRows, BN>(c, a, b, tile, split, splits);
     sync_all<CG>();  // (each has read what the other's may change)
     if (!more) return false;
-    init(true, rows, tile);
+    init(true, rows, tile, up_k, up_v, second);
     sync_all<CG>();
     return true;
   };
@@ -792,7 +847,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       const int pos = rows.pos0 + min(row0 + lane, rows.rows - 1) / r;
       const int hi = pos < 0 ? -1 : a.causal ? pos : rows.len - 1, lo = a.window ? max(pos, 0) - a.window : -1;  // lo < j <= hi is seen
       const int hi_all = __reduce_min_sync(0xffffffffu, hi), lo_all = __reduce_max_sync(0xffffffffu, lo);
-      const float f = load_q<T, D, GS>(a, rows, sm, tl, row0, hk, r, q, 32 * quarter, lane);
+      const float f = fmaxf(load_q<T, D, GS>(a, rows, sm, tl, row0, hk, r, q, 32 * quarter, lane) * pow2f(-bars->up_k), 1e-30f);
       if constexpr (C::kQTmem) {
         wait_st();
         fence_before();
@@ -905,11 +960,12 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
       // O's last product.  With two buffers of S per row tile the last two may be open (S of a tile only says that the
       // product two tiles before is complete), and o_done's parity cannot tell them apart: all MMAs, then.
       if (ok && rows.tiles > 0) ok = C::NB == QT ? wait_warp(&bars->o_done[q], (rows.tiles - 1) & 1, bars) : wait_warp(&bars->drain, 0, bars);
-      // every role meets here: bad_v of both CTAs is final, and seen
+      // every role meets here: what the expansions found, in both CTAs, is final, and seen
       fence_before();
       sync_all<CG>();
       fence_after();
-      const float inv = splits > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L;
+      if (once_more(bars)) continue;
+      const float back = pow2f(-bars->up_v), inv = splits > 1 ? back : L == 0.f ? 0.f : back / L;
       uint32_t nan = 0;  // a bit per group of channels
       if (ok && any_flag<CG>(&bars->bad_v)) {
         // rows that see such a token become NaN in its group's channels
@@ -917,7 +973,7 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
           const int page = c.page(b, p);
           if (page < 0) continue;
           const unsigned char *blk = c.block(page, hk, p) + 16 * D + 64 * G + (p & 15) * G * 4;
-          for (int g = 0; g < G; ++g) nan |= (uint32_t)beyond_fp16(__ldg(reinterpret_cast<const uint32_t *>(blk) + g)) << g;
+          for (int g = 0; g < G; ++g) nan |= (uint32_t)!(meta_size(__ldg(reinterpret_cast<const uint32_t *>(blk) + g)) < INFINITY) << g;
         }
       }
       auto factor = [&](int k) { return nan >> (k / GS) & 1u ? __int_as_float(0x7fc00000) : inv; };  // of channel k and the others of its group
@@ -1012,10 +1068,11 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
     if constexpr (C::kRegX < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegX));
     do {
       const Rows rows = bars->rows.get();
-      const X x{c, b, hk, warp & 3, lane, rank, rows.first, c_kv_stall ? 0 : rows.tiles};
-      if (warp < C::kFirstV) x.run_k(bars, sm);
-      else x.run_v(bars, sm, rows.len);
-      sync_all<CG>();  // (the softmax's, before it looks at bad_v)
+      const bool of_k = warp < C::kFirstV;
+      const X x{c, b, hk, warp & 3, lane, rank, rows.first, c_kv_stall ? 0 : rows.tiles, rows.begin, rows.end, pow2f(of_k ? bars->up_k : bars->up_v)};
+      if (of_k) x.run_k(bars, sm);
+      else x.run_v(bars, sm);
+      sync_all<CG>();  // (the softmax's, before it looks at what was found)
     } while (next());
   } else {
     if constexpr (C::kRegM < C::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegM));

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import serving_oracle as O
-from tests.test_kv_cache import DTYPES, Cache, _rng, _rounded
+from tests.test_kv_cache import DTYPES, Cache, _rng, _rounded, check
 
 pytestmark = pytest.mark.gpu
 
@@ -28,13 +28,13 @@ def attend(q1, c, cache, q, new, **kw):
     return o.double().cpu().numpy(), lse.double().cpu().numpy()
 
 
-def bounds(c, b, qv, want, size, big, scale, dtype):
-    """Errors of o and lse of sequence b: those that test_kv_cache.check derives for tiles."""
+def bounds(c, b, qv, want, size, big, scale, dtype, least=2.0 ** -25):
+    """Errors of o and lse of sequence b: those that test_kv_cache.check derives for tiles (least: half a step of V's smallest values)."""
     D, r = c.D, qv.shape[1] // c.heads
     kb = np.abs(c.kq[b][2]).max(0).repeat(c.gs, -1).repeat(r, 0)
     logit = (D / 8 + 16) * 2.0 ** -24 * big + ((D / 8 + 16) * 2.0 ** -23 + 2.0 ** -22) * abs(scale) * (kb * np.abs(qv)).sum(-1)
     info = torch.finfo(DTYPES[dtype])
-    floor = 2.0 ** -25 + c.lengths[b] * 2.0 ** -32 * np.abs(c.vval[b]).max()
+    floor = least + c.lengths[b] * 2.0 ** -32 * np.abs(c.vval[b]).max()
     return (info.eps / 2 * np.maximum(np.abs(want), info.tiny) + floor + 2.0 ** -10 * size + 2 * (2.0 ** -21 + logit)[..., None] * size,
             2.0 ** -21 + logit)
 
@@ -116,6 +116,133 @@ def test_nan_in_v_keeps_to_its_group(q1, D, gs, dtype):
         o, lse = attend(q1, c, one, q[-1:], [1], max_len=n)
         assert np.isnan(o[..., ch]).all() and (np.abs(o[0] - want[-1]) <= err[-1])[:, ~ch].all() and np.isfinite(lse).all()
     assert q1.device_errors() == 0
+
+
+def scaled(c, cache, part, octaves):
+    """The cache with all scales and biases of K (part 0) or V (part 1) times 2^octaves, and the oracle's values with them."""
+    G = c.D // c.gs
+    at = part * (2 * c.D + 16 * G) + 2 * c.D
+    words = cache.view(torch.int32).clone()
+    meta = words[..., at:at + 16 * G].contiguous().view(torch.bfloat16)
+    words[..., at:at + 16 * G] = (meta.double() * 2.0 ** octaves).bfloat16().view(torch.int32)
+    name, vals = (("kq", "kval"), ("vq", "vval"))[part]
+    setattr(c, name, [(x, s * np.float32(2.0 ** octaves), b * np.float32(2.0 ** octaves)) for x, s, b in getattr(c, name)])
+    setattr(c, vals, [x * np.float32(2.0 ** octaves) for x in getattr(c, vals)])
+    return words.view(torch.uint8)
+
+
+def small_bounds(c, b, qv, want, size, big, scale, dtype):
+    """bounds() for sizes of any kind.  A power of two brings the largest scale or bias `top` of a head (of those that the rows of
+    a tile see) to at least 2^-2 (K) or 2^-5 (V) before scales, biases and values are rounded to fp16, whose steps end at 2^-24:
+    halves of these are 2^-23 top and 2^-20 top.  An element of K has three such roundings, that of the scale up to 8 times: below
+    2^-19 top."""
+    r = qv.shape[1] // c.heads
+    top = [np.maximum(np.abs(x[b][1]), np.abs(x[b][2])).max((0, 2)).repeat(r) for x in (c.kq, c.vq)]
+    # (half a step among the sum's terms, not taken off a sum that holds 2^-25: in float64 that leaves nothing of terms below 2^-78)
+    err, lerr = bounds(c, b, qv, want, size, big, scale, dtype, 2.0 ** -20 * top[1][:, None])
+    more = abs(scale) * np.abs(qv).sum(-1) * top[0] * 2.0 ** -19
+    return err + 2 * more[..., None] * size, lerr + more
+
+
+SIZES = [(0, -16), (0, -22), (0, -40), (0, -70), (-16, 0), (-20, 0), (-40, 0), (-18, -18), (12, 12), (40, 40)]    # octaves of K and V
+
+
+@pytest.mark.parametrize("D,gs,HK,hint", [(64, 64, 36, 400), (64, 64, 24, 2000), (128, 64, 24, 400), (128, 128, 16, 2000), (256, 64, 24, 400),
+                                          (256, 128, 12, 2000)])
+def test_sizes_of_keys_and_values(q1, D, gs, HK, hint):
+    # K and V of any size (of K with a softmax scale to match), by tiles in one part and in two: as right as those of size one
+    n, new = 400, 300
+    some = [0, 131, new - 1]
+    for ke, ve in SIZES:
+        c = Cache(q1, [n], HK, D, gs, seed=D + gs)
+        cache = scaled(c, scaled(c, c.store(q1), 0, ke), 1, ve)
+        dtype, scale = "bf16", D ** -0.5 * 2.0 ** -ke
+        q, qv = _rounded(_rng(7).standard_normal((new, 2 * HK, D)), dtype)
+        o, lse = attend(q1, c, cache, q, [new], max_len=hint, scale=scale)
+        want, want_lse, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], np.array(some) + n - new, scale)
+        err, lerr = small_bounds(c, 0, qv[some], want, size, big, scale, dtype)
+        assert (np.abs(o[some] - want) <= err).all(), (ke, ve, float((np.abs(o[some] - want) / err).max()))
+        assert (np.abs(lse[some] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse)).all(), (ke, ve)
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_sizes_differ_between_heads_and_sequences(q1, D):
+    # each head of each sequence with sizes of its own, a sequence of zeros, another of which rows see nothing; more row tiles than the
+    # hint foresees; missing pages and a short table
+    lengths, new, HK = [300, 260, 200, 20], [280, 90, 200, 60], 24
+    rng = _rng(D + 1)
+    ks, vs = (2.0 ** rng.integers(-24, 9, (4, 1, HK, 1)) for _ in range(2))
+    for x in (ks, vs):
+        x[2] = 0.0
+    data = [[rng.standard_normal((n, HK, D)) * s[b] for b, n in enumerate(lengths)] for s in (ks, vs)]
+    c = Cache(q1, lengths, HK, D, seed=5, k=data[0], v=data[1])
+    c.table[1, 1] = -1
+    cache = c.store(q1)
+    # rows that bring each head's logits to some size: q against K's size
+    q = rng.standard_normal((sum(new), HK, 2, D))
+    cu = _starts(new)
+    for b in range(4):
+        q[cu[b]:cu[b + 1]] /= np.maximum(ks[b], 1e-9)[..., None] if b != 2 else 1.0
+    q, qv = _rounded(q.reshape(sum(new), 2 * HK, D), "bf16")
+    for kw in (dict(max_len=300), dict(max_len=2000), dict(max_len=2000, max_q=40)):
+        o, lse = attend(q1, c, cache, q, new, **kw)
+        for b, n in enumerate(new):
+            some = np.array([0, n // 2, n - 1])
+            rows, pos = cu[b] + some, some + lengths[b] - n
+            there = np.array([0 <= c.table[b, p // c.page] < c.n_pages for p in range(lengths[b])])
+            want, want_lse, size, big = O.kv_attention(qv[rows], c.kval[b], c.vval[b], pos, D ** -0.5, there=there)
+            err, lerr = small_bounds(c, b, qv[rows], want, size, big, D ** -0.5, "bf16")
+            assert (np.abs(o[rows] - want) <= err).all(), (kw, b, float((np.abs(o[rows] - want) / err).max()))
+            empty = np.isneginf(want_lse)
+            assert np.array_equal(np.isneginf(lse[rows]), empty)
+            assert (np.abs(lse[rows][~empty] - want_lse[~empty]) <= (lerr + 2.0 ** -23 * np.abs(want_lse))[~empty]).all(), (kw, b)
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_sizes_beside_what_is_not_seen(q1, D):
+    # small values in the window, the largest that are stored, infinities and NaN before it, behind the sequence and in the pages' rest
+    n, HK, new, window = 700, 24, 300, 100
+    rng = _rng(D + 2)
+    first = n - new - window + 1                       # the first token that a row sees
+    k, v = (rng.standard_normal((n, HK, D)) * 1e-6 for _ in range(2))
+    for x, y in ((k, 3e4), (v, -3e4)):
+        x[:first] = y * rng.random((first, HK, D))
+    c = Cache(q1, [n], HK, D, page=32, seed=6, k=[k], v=[v])
+    q, qv = _rounded(rng.standard_normal((new, 2 * HK, D)) * 1e6, "bf16")
+    some = [0, 130, new - 1]
+    pos = np.array(some) + n - new
+    want, want_lse, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], pos, D ** -0.5, window=window)
+    for x in ("kq", "vq"):                             # (the bounds go by what is seen)
+        setattr(c, x, [tuple(a[first:] for a in getattr(c, x)[0])])
+    c.vval = [c.vval[0][first:]]
+    err, lerr = small_bounds(c, 0, qv[some], want, size, big, D ** -0.5, "bf16")
+    cache = torch.full((c.n_pages, HK, 2, 16 * (D + 8 * (D // 64))), 255, dtype=torch.uint8, device="cuda")
+    words = cache.view(torch.int32)
+    words[::2] = 0x7F807F80                            # infinities in half of the pages, NaN in the others
+    q1.kv_store(cache, torch.from_numpy(k.astype(np.float32)).cuda(), torch.from_numpy(v.astype(np.float32)).cuda(), c.d_table(), c.d_lengths(),
+                cu_seqlens=torch.tensor([0, n], dtype=torch.int32).cuda())
+    bad = cache.clone()
+    nan = torch.full((new, HK, D), float("nan"), device="cuda")
+    q1.kv_store(bad, nan, nan, c.d_table(), torch.tensor([first], dtype=torch.int32).cuda(), cu_seqlens=torch.tensor([0, new], dtype=torch.int32).cuda())
+    for x in (cache, bad):
+        o, lse = attend(q1, c, x, q, [new], max_len=n, window=window)
+        assert (np.abs(o[some] - want) <= err).all(), float((np.abs(o[some] - want) / err).max())
+        assert (np.abs(lse[some] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse)).all()
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("octaves", [-16, -20, -27, -60, 9])
+def test_sizes_of_keys_by_few_rows(q1, dtype, octaves):
+    c = Cache(q1, [300, 41], 2, 128, seed=8)
+    cache = scaled(c, c.store(q1), 0, octaves)
+
+    class Stored:                                      # check() attends to the cache that it is given
+        def __getattr__(self, name):
+            return getattr(c, name)
+    check(q1, Stored(), cache, [1, 2], 4, dtype, scale=128 ** -0.5 * 2.0 ** -octaves)
 
 
 @pytest.mark.parametrize("T,new", [(40, [1, 0, 2, 1, 1]), (47, [20, 0, 13]), (200, [90, 33, 40]), (9, [0, 0]), (64, [0])])
