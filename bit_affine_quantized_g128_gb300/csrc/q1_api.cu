@@ -434,7 +434,9 @@ q1::KvView kv_view(const q1_kv_cache *c) {
 }
 
 q1::KvAttention kv_attention_view(const q1_kv_attention_args *a) {
-  return q1::KvAttention{a->q, a->o, a->lse, a->q_stride, a->o_stride, a->max_q, a->max_len, a->HQ, a->causal != 0, a->window,
+  // no sequence is longer than lengths can say: the plans count in 32 bits
+  const int64_t max_len = std::min<int64_t>(a->max_len, INT32_MAX);
+  return q1::KvAttention{a->q, a->o, a->lse, a->q_stride, a->o_stride, a->max_q, max_len, a->HQ, a->causal != 0, a->window,
                          a->scale};
 }
 }  // namespace
