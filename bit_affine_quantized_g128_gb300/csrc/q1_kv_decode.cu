@@ -726,7 +726,7 @@ inline int rows_of(const KvView &c, const KvAttention &a) { return std::max<int6
 Split plan(const KvView &c, const KvAttention &a, bool fp32) {
   const int rows = rows_of(c, a), r = a.HQ / c.HK;
   Split s;
-  s.tiles = (int)std::min<int64_t>((std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + rows - 1) / rows, 1 << 20);
+  s.tiles = (int)kv_tiles_of_grid(c, (std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + rows - 1) / rows, c.T * r, rows);
   int64_t seen = std::max<int64_t>(a.max_len, 1);
   if (a.window) seen = std::min<int64_t>(seen, (int64_t)a.window + rows + 15);
   const int64_t blocks = (seen + 15) / 16, work = c.B * c.HK * s.tiles;

@@ -1219,7 +1219,8 @@ cudaError_t run(const KvView &c, const KvAttention &a, int splits, float *part, 
     if (e != cudaSuccess) return e;
     mark_done(ready, dev);
   }
-  const int64_t tiles = shape(c, a).tiles, ctas = tiles * c.B * c.HK * C::CG * splits;
+  const Shape s = shape(c, a);
+  const int64_t tiles = kv_tiles_of_grid(c, s.tiles, c.T * (a.HQ / c.HK), s.rows), ctas = tiles * c.B * c.HK * C::CG * splits;
   const int64_t joins = (c.T * a.HQ * (D / 4) + kJoinThreads - 1) / kJoinThreads;
   if (ctas > INT32_MAX || joins > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};

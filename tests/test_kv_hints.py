@@ -17,3 +17,56 @@ def test_any_max_len_has_a_plan(dtype, B, D):
     assert want < 1 << 30
     for max_len in (1 << 31, 152 << 32, 304 << 32, 0x98000000000, 0x130000000000, 1 << 62, (1 << 63) - 1):
         assert plan(max_len) == want, hex(max_len)
+
+
+@pytest.mark.gpu
+def test_many_sequences_without_max_q():
+    # 60000 sequences of a row each, their longest unknown: as with the hint, and not refused
+    import torch
+    B, HK, r, D = 60000, 1, 16, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache, table = mod.kv_cache(B, HK, D, page_size=16), torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+    lengths = torch.randint(1, 17, (B,), generator=g, device="cuda", dtype=torch.int32)
+    kv = torch.randn(2, B, 16, HK, D, generator=g, device="cuda").bfloat16()
+    mod.kv_store(cache, kv[0], kv[1], table, torch.full_like(lengths, 16))
+    q = torch.randn(B, HK * r, D, generator=g, device="cuda").bfloat16()
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    want = mod.kv_attention(q, cache, table, lengths, cu_seqlens=cu, max_q=1, max_len=16)
+    assert torch.equal(mod.kv_attention(q, cache, table, lengths, cu_seqlens=cu, max_len=16), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r,dtype", [(16, "float32"), (64, "float16")])
+def test_a_prompt_among_many_tokens(r, dtype):
+    # few rows, and tiles (fp16): more row tiles of one sequence than the grid has for each, with the hint and without; rows behind
+    # the last sequence
+    import numpy as np
+    import torch
+
+    from oracle import serving_oracle as O
+    B, n, D = 3000, 4001, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = torch.ones(B, dtype=torch.int32, device="cuda")
+    rows[1234] = n
+    cu = torch.cat([rows[:1] * 0, rows.cumsum(0).int()])
+    T = int(cu[-1])
+    width = -(-n // 64)
+    table = torch.zeros(B, width, dtype=torch.int32, device="cuda")
+    table[:, 0] = torch.arange(B)
+    table[1234, 1:] = B + torch.arange(width - 1)
+    cache = mod.kv_cache(B + width - 1, 1, D)
+    kv = torch.randn(2, T, 1, D, generator=g, device="cuda")
+    mod.kv_store(cache, kv[0], kv[1], table, rows, cu_seqlens=cu)
+    q = torch.randn(T + 5, r, D, generator=g, device="cuda").to(getattr(torch, dtype))
+    out = [torch.full_like(q, 7.0) for _ in range(3)]
+    for o, max_q in zip(out, (n, None, 1)):
+        mod.kv_attention(q, cache, table, rows, cu_seqlens=cu, max_q=max_q, max_len=n, out=o)
+    assert torch.equal(out[0], out[1]) and all(bool((o[T:] == 7).all()) for o in out)
+    k, v = (x[1234:1234 + n].double().cpu().numpy() for x in mod.kv_load(cache, table, rows, T, cu_seqlens=cu, dtype=torch.float32))
+    some = np.array([0, 5, 1000, n - 1])
+    want, _, size, _ = O.kv_attention(q[1234 + some].double().cpu().numpy(), k, v, some, D ** -0.5)
+    # fp16 outputs and, by tiles, weights and values: three roundings; logits below 2^-14
+    bound = 2.0 ** -11 * np.abs(want) + 2.0 ** -10 * size + 2.0 ** -13 * size
+    for o in out:
+        assert (np.abs(o[1234 + some].double().cpu().numpy() - want) <= bound).all()
+    assert mod.device_errors() == 0
