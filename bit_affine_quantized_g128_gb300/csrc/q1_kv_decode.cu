@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Decode<T, D, GS, NT>::kCtas)) kv
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
       // the power of two that brings the largest into [2^14, 2^15)
       const int be = (int)(__float_as_uint(big) >> 23);
-      const int e = be == 0 || be == 255 ? 0 : min(max(14 - (be - 127), -100), 100);
+      const int e = be == 0 || be == 255 ? 0 : min(14 - (be - 127), 126);
       const float up = a.scale < 0.f ? -pow2f(e) : pow2f(e);
 #pragma unroll
       for (int i = 0; i < G; ++i) {

@@ -635,7 +635,7 @@ struct Expander {
 // it), and what S is multiplied with to give logits in octaves.
 __device__ __forceinline__ float2 q_factors(float big, float scale) {
   const int be = (int)(__float_as_uint(big) >> 23);
-  const int e = be == 0 || be == 255 ? 0 : min(max(7 - (be - 127), -100), 100);
+  const int e = be == 0 || be == 255 ? 0 : min(7 - (be - 127), 126);
   return make_float2(scale < 0.f ? -pow2f(e) : pow2f(e), fmaxf(fabsf(scale) * kLog2e * pow2f(-e), 1e-30f));
 }
 template <typename T>

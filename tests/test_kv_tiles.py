@@ -279,3 +279,22 @@ def test_nan_of_vanishing_weight(q1, dtype):
         for hint in (n, 1 << 20):
             o, lse = attend(q1, c, c.store(q1), _rounded(q, dtype)[0], [1], max_len=hint, scale=1.0)
             assert np.isnan(o).all() and np.isfinite(lse).all(), (at, hint)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("size", [1e36, 1e-36])
+def test_sizes_of_queries(q1, D, size):
+    # rows as large and as small as bf16 and fp32 hold them, with a softmax scale to match, by both forms
+    n, new, HK = 400, 300, 24
+    c = Cache(q1, [n], HK, D, seed=D + 3)
+    cache, scale = c.store(q1), D ** -0.5 / size
+    some = [0, 131, new - 1]
+    for dtype, first in (("bf16", 0), ("bf16", new - 2), ("fp32", new - 2)):
+        q, qv = _rounded(_rng(12).standard_normal((new, 2 * HK, D)) * size, dtype)
+        rows = [i for i in some if i >= first]
+        o, lse = attend(q1, c, cache, q[first:], [new - first], max_len=n, scale=scale)
+        want, want_lse, wsize, big = O.kv_attention(qv[rows], c.kval[0], c.vval[0], np.array(rows) + n - new, scale)
+        err, lerr = small_bounds(c, 0, qv[rows], want, wsize, big, scale, "bf16")
+        rows = np.array(rows) - first
+        assert (np.abs(o[rows] - want) <= err).all() and (np.abs(lse[rows] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse)).all(), dtype
+    assert q1.device_errors() == 0
