@@ -472,6 +472,11 @@ size_t q1_kv_attention_workspace_size(const q1_kv_cache *c, const q1_kv_attentio
   return splits ? q1::kv_tiles_workspace_bytes(v, at, splits) : q1::kv_decode_workspace_bytes(v, at, (q1_dtype)a->dtype);
 }
 
+int32_t q1_kv_attention_parts(const q1_kv_cache *c, const q1_kv_attention_args *a) {
+  if (check_kv_attention_sizes(c, a) != Q1_OK) return -1;
+  return c->T == 0 ? 0 : q1::kv_tiles_splits(kv_view(c), kv_attention_view(a), (q1_dtype)a->dtype);
+}
+
 q1_status q1_kv_attention(const q1_kv_cache *c, const q1_kv_attention_args *a, void *workspace, size_t workspace_bytes,
                           q1_stream stream) {
   q1_status s = check_device();

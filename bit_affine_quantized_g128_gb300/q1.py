@@ -29,7 +29,7 @@ EXPORTED = [
     "q1_set_wait_limit_ns", "q1_set_stalled_producers",
     "q1_decode_chain_workspace_size", "q1_decode_chain", "q1_pack_from_dense",
     "q1_gated_delta_workspace_size", "q1_gated_delta", "q1_sample",
-    "q1_kv_store", "q1_kv_load", "q1_kv_attention_workspace_size", "q1_kv_attention",
+    "q1_kv_store", "q1_kv_load", "q1_kv_attention_workspace_size", "q1_kv_attention_parts", "q1_kv_attention",
 ]
 
 
@@ -136,6 +136,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "q1_kv_store": ([ctypes.POINTER(_CKvCache), P, I64, P, I64, I32, P], I32),
         "q1_kv_load": ([ctypes.POINTER(_CKvCache), P, I64, P, I64, I32, P], I32),
         "q1_kv_attention_workspace_size": ([ctypes.POINTER(_CKvCache), ctypes.POINTER(_CKvAttention)], SZ),
+        "q1_kv_attention_parts": ([ctypes.POINTER(_CKvCache), ctypes.POINTER(_CKvAttention)], I32),
         "q1_kv_attention": ([ctypes.POINTER(_CKvCache), ctypes.POINTER(_CKvAttention), P, SZ, P], I32),
         "q1_device_errors": ([ctypes.POINTER(ctypes.c_uint), P], I32),
         "q1_status_string": ([I32], ctypes.c_char_p),

@@ -458,6 +458,9 @@ typedef struct {
 size_t q1_kv_attention_workspace_size(const q1_kv_cache *cache, const q1_kv_attention_args *args);
 q1_status q1_kv_attention(const q1_kv_cache *cache, const q1_kv_attention_args *args, void *workspace,
                           size_t workspace_bytes, q1_stream stream);
+/* Which form a call takes, by sizes and hints like the workspace: 0 that of few rows, else that
+ * of many with the context in so many parts; -1 where the sizes are refused.  (For tests and measurements.) */
+int32_t q1_kv_attention_parts(const q1_kv_cache *cache, const q1_kv_attention_args *args);
 
 /* ---- symmetric check (higgs PR #212, walkthrough: symmetric bias
  * compaction and validation) -------------------------------------------------

@@ -19,6 +19,21 @@ def test_any_max_len_has_a_plan(dtype, B, D):
         assert plan(max_len) == want, hex(max_len)
 
 
+def test_cases_for_tiles_go_by_tiles():
+    # (no GPU needed) the lists of test_kv_cache.py that are meant for the form for many rows: all without a window in parts, or in one
+    # part; with a window those of WHOLE
+    from tests.test_kv_cache import DTYPES, MANY, WHOLE
+    for cases, whole in ((MANY, False), (WHOLE, True)):
+        for D, gs, HK, r, page, dtype, lengths, new, window in cases:
+            c = mod._CKvCache(T=sum(new), B=len(new), HK=HK, D=D, group_size=gs, page_size=page, n_pages=99, table_width=99, table_stride=99)
+            a = mod._CKvAttention(HQ=HK * r, dtype=list(DTYPES).index(dtype), causal=1, max_q=max(new), window=window, scale=1.0,
+                                  max_len=max(lengths) if whole else 1 << 20)
+            parts = mod.lib().q1_kv_attention_parts(c, a)
+            assert parts == 1 if whole else window > 0 or parts > 1, (D, HK, r, new)
+    a = mod._CKvAttention(HQ=3, dtype=0, causal=1, max_q=1, max_len=1, scale=1.0)
+    assert mod.lib().q1_kv_attention_parts(c, a) == -1 and mod.lib().q1_kv_attention_parts(None, a) == -1
+
+
 @pytest.mark.gpu
 def test_many_sequences_without_max_q():
     # 60000 sequences of a row each, their longest unknown: as with the hint, and not refused

@@ -20,9 +20,20 @@ def _starts(new):
     return np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
 
 
-def attend(q1, c, cache, q, new, **kw):
-    """o and lse (float64) of the rows q, the tiles' form by the hint max_len (a long context has few rows take it, in parts)."""
+def parts_of(q1, c, T, HQ, dtype, max_q, max_len, window=0, causal=True):
+    """The form that such a call takes: 0, or the tiles' with the context in so many parts."""
+    B, width = c.table.shape
+    cache = q1._CKvCache(T=T, B=B, HK=c.heads, D=c.D, group_size=c.gs, page_size=c.page, n_pages=c.n_pages, table_width=width, table_stride=width)
+    return q1.lib().q1_kv_attention_parts(cache, q1._CKvAttention(HQ=HQ, dtype=list(DTYPES).index(dtype), max_q=max_q, max_len=max_len,
+                                                                   causal=causal, window=window, scale=1.0))
+
+
+def attend(q1, c, cache, q, new, few=False, whole=None, **kw):
+    """o and lse (float64) of the rows q: by tiles (the context in one part or in several, as `whole` says, if given), or few."""
     kw = {"max_q": max(new), "max_len": 1 << 20, **kw}
+    dtype = [n for n, t in DTYPES.items() if t == q.dtype][0]
+    form = parts_of(q1, c, q.shape[0], q.shape[1], dtype, kw["max_q"], kw["max_len"], kw.get("window", 0), kw.get("causal", True))
+    assert (form > 0) != few and whole in (None, form == 1)
     o, lse = q1.kv_attention(q.cuda(), cache, c.d_table(), c.d_lengths(), cu_seqlens=torch.from_numpy(_starts(new)).cuda(),
                              return_lse=True, **kw)
     return o.double().cpu().numpy(), lse.double().cpu().numpy()
@@ -30,7 +41,7 @@ def attend(q1, c, cache, q, new, **kw):
 
 def bounds(c, b, qv, want, size, big, scale, dtype, least=2.0 ** -25):
     """Errors of o and lse of sequence b: those that test_kv_cache.check derives for tiles (least: half a step of V's smallest values)."""
-    D, r = c.D, qv.shape[1] // c.heads
+    D, r, qv = c.D, qv.shape[1] // c.heads, qv.astype(np.float64)
     kb = np.abs(c.kq[b][2]).max(0).repeat(c.gs, -1).repeat(r, 0)
     logit = (D / 8 + 16) * 2.0 ** -24 * big + ((D / 8 + 16) * 2.0 ** -23 + 2.0 ** -22) * abs(scale) * (kb * np.abs(qv)).sum(-1)
     info = torch.finfo(DTYPES[dtype])
@@ -53,7 +64,7 @@ def test_logits_that_jump_inside_a_tile(q1, D, HK, dtype, hint):
         k = 0.02 * rng.standard_normal((n, HK, D)) + (7 * np.log(2) * D ** -0.5 * level)[:, None, None]
         c = Cache(q1, [n], HK, D, seed=D + jump, k=[k])
         q, qv = _rounded(1 + 0.02 * rng.standard_normal((new, 2 * HK, D)), dtype)
-        o, lse = attend(q1, c, c.store(q1), q, [new], max_len=hint)
+        o, lse = attend(q1, c, c.store(q1), q, [new], max_len=hint, whole=hint == n)
         some = [0, 1, 31, 32, 77, new - 1]
         want, want_lse, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], np.array(some) + n - new, D ** -0.5)
         err, lerr = bounds(c, 0, qv[some], want, size, big, D ** -0.5, dtype)
@@ -113,7 +124,7 @@ def test_nan_in_v_keeps_to_its_group(q1, D, gs, dtype):
             assert np.array_equal(np.isnan(o[some]), np.broadcast_to(nan, want.shape)), (g, hint)
             assert (np.abs(o[some] - want) <= err)[~np.broadcast_to(nan, want.shape)].all(), (g, hint)
             assert (np.abs(lse[some] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse)).all(), (g, hint)
-        o, lse = attend(q1, c, one, q[-1:], [1], max_len=n)
+        o, lse = attend(q1, c, one, q[-1:], [1], max_len=n, few=True)
         assert np.isnan(o[..., ch]).all() and (np.abs(o[0] - want[-1]) <= err[-1])[:, ~ch].all() and np.isfinite(lse).all()
     assert q1.device_errors() == 0
 
@@ -140,7 +151,7 @@ def small_bounds(c, b, qv, want, size, big, scale, dtype):
     top = [np.maximum(np.abs(x[b][1]), np.abs(x[b][2])).max((0, 2)).repeat(r) for x in (c.kq, c.vq)]
     # (half a step among the sum's terms, not taken off a sum that holds 2^-25: in float64 that leaves nothing of terms below 2^-78)
     err, lerr = bounds(c, b, qv, want, size, big, scale, dtype, 2.0 ** -20 * top[1][:, None])
-    more = abs(scale) * np.abs(qv).sum(-1) * top[0] * 2.0 ** -19
+    more = abs(scale) * np.abs(qv.astype(np.float64)).sum(-1) * top[0] * 2.0 ** -19
     return err + 2 * more[..., None] * size, lerr + more
 
 
@@ -158,7 +169,7 @@ def test_sizes_of_keys_and_values(q1, D, gs, HK, hint):
         cache = scaled(c, scaled(c, c.store(q1), 0, ke), 1, ve)
         dtype, scale = "bf16", D ** -0.5 * 2.0 ** -ke
         q, qv = _rounded(_rng(7).standard_normal((new, 2 * HK, D)), dtype)
-        o, lse = attend(q1, c, cache, q, [new], max_len=hint, scale=scale)
+        o, lse = attend(q1, c, cache, q, [new], max_len=hint, scale=scale, whole=hint == n)
         want, want_lse, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], np.array(some) + n - new, scale)
         err, lerr = small_bounds(c, 0, qv[some], want, size, big, scale, dtype)
         assert (np.abs(o[some] - want) <= err).all(), (ke, ve, float((np.abs(o[some] - want) / err).max()))
@@ -277,7 +288,7 @@ def test_nan_of_vanishing_weight(q1, dtype):
         q = np.zeros((1, 2, D))
         q[..., 0] = 20.0
         for hint in (n, 1 << 20):
-            o, lse = attend(q1, c, c.store(q1), _rounded(q, dtype)[0], [1], max_len=hint, scale=1.0)
+            o, lse = attend(q1, c, c.store(q1), _rounded(q, dtype)[0], [1], max_len=hint, scale=1.0, few=True)
             assert np.isnan(o).all() and np.isfinite(lse).all(), (at, hint)
 
 
@@ -292,9 +303,84 @@ def test_sizes_of_queries(q1, D, size):
     for dtype, first in (("bf16", 0), ("bf16", new - 2), ("fp32", new - 2)):
         q, qv = _rounded(_rng(12).standard_normal((new, 2 * HK, D)) * size, dtype)
         rows = [i for i in some if i >= first]
-        o, lse = attend(q1, c, cache, q[first:], [new - first], max_len=n, scale=scale)
+        o, lse = attend(q1, c, cache, q[first:], [new - first], max_len=n, scale=scale, few=first > 0)
         want, want_lse, wsize, big = O.kv_attention(qv[rows], c.kval[0], c.vval[0], np.array(rows) + n - new, scale)
         err, lerr = small_bounds(c, 0, qv[rows], want, wsize, big, scale, "bf16")
         rows = np.array(rows) - first
         assert (np.abs(o[rows] - want) <= err).all() and (np.abs(lse[rows] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse)).all(), dtype
+    assert q1.device_errors() == 0
+
+
+WINDOWS = [  # D, gs, HK, HQ / HK, page, dtype, window, whether the context is in one part
+    (64, 64, 24, 2, 32, "fp16", 100, True), (64, 64, 12, 2, 64, "bf16", 1000, False), (64, 64, 24, 2, 16, "bf16", 1, True),
+    (128, 64, 16, 2, 64, "bf16", 20, True), (128, 128, 8, 2, 16, "fp16", 600, False), (128, 64, 10, 3, 32, "bf16", 77, True),
+    (256, 64, 12, 2, 32, "bf16", 100, True), (256, 128, 6, 2, 128, "fp16", 800, False), (256, 64, 8, 2, 64, "fp16", 1, True)]
+
+
+@pytest.mark.parametrize("D,gs,HK,r,page,dtype,window,whole", WINDOWS)
+def test_windows_by_tiles(q1, D, gs, HK, r, page, dtype, window, whole):
+    lengths, new = [1200, 400, 33], [300, 40, 33]
+    c = Cache(q1, lengths, HK, D, gs, page, seed=D + window)
+    kw = dict(max_q=300, max_len=1200, window=window)
+    parts = parts_of(q1, c, sum(new), HK * r, dtype, **kw)
+    assert parts == 1 if whole else parts > 1
+    check(q1, c, c.store(q1), new, HK * r, dtype, tiles=True, **kw)
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("D,gs,HK,r,page,dtype,window,whole", [w for w in WINDOWS if w[6] > 1])
+def test_windows_by_tiles_beside_nan(q1, D, gs, HK, r, page, dtype, window, whole):
+    # NaN in K or V of one token, behind the sequences and in pages of no sequence: rows whose window has left it, or not reached it
+    n, new = 1200, 300
+    at = n - new - window + 150                        # the first 150 rows see it, or as many as the window has
+    c = Cache(q1, [n, 40], HK, D, gs, page, seed=D + window + 1)
+    kept = torch.full((c.n_pages, HK, page // 16, 16 * (D + 8 * (D // gs))), 255, dtype=torch.uint8, device="cuda")
+    rows = [torch.from_numpy(np.concatenate(x).astype(np.float32)).cuda() for x in (c.k, c.v)]
+    q1.kv_store(kept, *rows, c.d_table(), c.d_lengths(), cu_seqlens=torch.tensor([0, n, n + 40], dtype=torch.int32).cuda())
+    q, qv = _rounded(_rng(9).standard_normal((new, HK * r, D)), dtype)
+    pos = np.arange(new) + n - new
+    some = np.unique(np.clip([0, 149 - window, 150 - window, 149, 150, new - 1], 0, None))
+    want, want_lse, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], pos[some], D ** -0.5, window=window)
+    err, lerr = bounds(c, 0, qv[some], want, size, big, D ** -0.5, dtype)
+    hit = (pos >= at) & (pos < at + window)
+    for of_v in (False, True):
+        one = [x[at:at + 1].clone() for x in rows]
+        one[of_v][:] = float("nan")
+        cache = kept.clone()
+        q1.kv_store(cache, *one, c.d_table(), torch.tensor([at + 1, 0], dtype=torch.int32).cuda(),
+                    cu_seqlens=torch.tensor([0, 1, 1], dtype=torch.int32).cuda())
+        o, lse = attend(q1, c, cache, q, [new, 0], max_len=n, window=window, whole=whole)
+        assert np.isnan(o[hit]).all() and not np.isnan(o[~hit]).any()
+        assert (np.abs(o[some] - want) <= err)[~hit[some]].all()
+        good = ~hit[some] | of_v
+        assert (np.abs(lse[some] - want_lse) <= lerr + 2.0 ** -23 * np.abs(want_lse))[good].all() and (of_v or np.isnan(lse[hit]).all())
+    assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("D,HK,whole", [(64, 36, True), (64, 16, False), (128, 24, True), (128, 12, False), (256, 24, True), (256, 8, False)])
+def test_offsets_out_of_range_stay_inside_by_tiles(q1, D, HK, whole):
+    # (results are undefined; nothing outside the arrays is touched, and the next call is right)
+    n, T, hint = 400, 300, 400 if whole else 2000
+    c = Cache(q1, [n, 90], HK, D, seed=15)
+    cache, table = c.store(q1), c.d_table()
+    q, qv = _rounded(_rng(16).standard_normal((T, 2 * HK, D)), "bf16")
+    qd, out = q.cuda(), torch.zeros(T + 2, 2 * HK, D, dtype=torch.bfloat16, device="cuda")
+    parts = parts_of(q1, c, T, 2 * HK, "bf16", T, hint)
+    assert parts == 1 if whole else parts > 1
+    out[0], out[-1] = 7.0, 7.0
+
+    def call(cu, lengths):
+        q1.kv_attention(qd, cache, table, torch.tensor(lengths, dtype=torch.int32).cuda(), cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(),
+                        max_q=T, max_len=hint, out=out[1:-1])
+    for cu in ([0, 900, 40], [-5, 200, 300], [300, 1, 1 << 30], [0, 0, 0], [300, 300, 300], [200, 100, 300], [1 << 30, -(1 << 31), 5]):
+        call(cu, [n, 90])
+    for lengths in ([-3, 90], [1 << 30, 90], [-(1 << 31), (1 << 31) - 1]):
+        call([0, 290, 300], lengths)
+    torch.cuda.synchronize()
+    assert bool((out[0] == 7).all()) and bool((out[-1] == 7).all())
+    call([0, 290, 300], [n, 90])
+    some = np.array([0, 130, 289])
+    want, _, size, big = O.kv_attention(qv[some], c.kval[0], c.vval[0], some + n - 290, D ** -0.5)
+    err, _ = bounds(c, 0, qv[some], want, size, big, D ** -0.5, "bf16")
+    assert (np.abs(out[1:-1][some].double().cpu().numpy() - want) <= err).all()
     assert q1.device_errors() == 0
