@@ -732,7 +732,8 @@ Split plan(const KvView &c, const KvAttention &a, bool fp32) {
   const int64_t blocks = (seen + 15) / 16, work = c.B * c.HK * s.tiles;
   // CTAs for one, two or four rounds of the GPU: the more, the better ragged batches even out, as long as each has 16, 64
   // or 128 blocks to do.
-  const int64_t slots = 152 * (c.D == 64 || (c.D == 128 && rows == 8 && !fp32) ? 2 : 1);
+  // (as Decode::kCtas has it: fp32 rows and large tiles take an SM for a CTA)
+  const int64_t slots = 152 * (!fp32 && c.D * rows <= 128 * 8 ? 2 : 1);
   int64_t want = std::min(slots / work, blocks / 16);
   if (blocks / std::max<int64_t>(2 * slots / work, 1) >= 64) want = 2 * slots / work;
   if (blocks / std::max<int64_t>(4 * slots / work, 1) >= 128) want = 4 * slots / work;
