@@ -805,7 +805,7 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor
     `max_len` (the largest of lengths) are best given: they pick the kernels and how the work is split; without them T
     (or L) and the block table's width count.  Returns o like q, and with return_lse the fp32 logarithms of the sums
     of exponentials, o without its last dimension; a row that sees nothing gets 0 and -inf.  Rows of no sequence (before
-    cu_seqlens[0], from cu_seqlens[B] on) are left as they are in `out`, undefined without it."""
+    cu_seqlens[0], from cu_seqlens[B] on) are left as they are in `out`, undefined without it.  `out` must not overlap q."""
     _kv_on_device(("q", q), cache=cache, block_table=block_table)
     dev, dtype, packed = q.device, q.dtype, cu_seqlens is not None
     dt = _x_dtype(q, "q")
@@ -817,7 +817,14 @@ def kv_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor
         raise ValueError(f"the cache holds {heads} heads of {dim}; q must have a multiple of them (got {(HQ, D)})")
     if window < 0 or window and not causal:
         raise ValueError("window must not be negative, and needs causal")
-    o = torch.empty((*lead, HQ, dim), dtype=dtype, device=dev) if out is None else _out(out, (T, HQ, dim), dtype, dev)
+    if out is None:
+        o = torch.empty((*lead, HQ, dim), dtype=dtype, device=dev)
+    else:
+        o, n = _out(out, (T, HQ, dim), dtype, dev), HQ * dim
+        d = (o.data_ptr() - qp) // q.element_size()
+        row = max((d - n) // qs + 1, 0) if qs else 0    # the first of q that ends behind out's start
+        if row < T and row * qs < d + T * n:
+            raise ValueError("out must not overlap q")
     lse = torch.empty((*lead, HQ), dtype=_F32, device=dev) if return_lse else None
     if max_q is None or not packed:
         max_q = T if packed else lead[1]

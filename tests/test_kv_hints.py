@@ -85,3 +85,32 @@ def test_a_prompt_among_many_tokens(r, dtype):
     for o in out:
         assert (np.abs(o[1234 + some].double().cpu().numpy() - want) <= bound).all()
     assert mod.device_errors() == 0
+
+
+def test_out_must_not_overlap_q(monkeypatch):
+    # (no GPU needed) a row is read by several CTAs; columns beside q's are none of it
+    import torch
+    reached = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: reached.append(name) or 0
+    monkeypatch.setattr(mod, "_lib", Library())
+    monkeypatch.setattr(mod, "_is_cuda", lambda t: True)
+    monkeypatch.setattr(mod, "_current_device", lambda: torch.device("cpu"))
+    monkeypatch.setattr(mod, "_raw_stream", lambda i: 0)
+    cache, table = torch.zeros(4, 2, 4, 2304, dtype=torch.uint8), torch.zeros(2, 3, dtype=torch.int32)
+    lengths, cu = torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    n = 4 * 128
+    flat = torch.zeros(64 * n, dtype=torch.bfloat16)
+
+    def call(T, stride, at, out):
+        q = flat[at * n:].as_strided((T, 4, 128), (stride * n, 128, 1))
+        mod.kv_attention(q, cache, table, lengths, cu_seqlens=cu, out=flat[out * n:(out + T) * n].view(T, 4, 128))
+    for T, stride, at, out in ((6, 1, 8, 2), (6, 1, 8, 14), (1, 1, 8, 7), (1, 1, 8, 9), (3, 8, 8, 9), (3, 8, 8, 13), (3, 8, 8, 5), (3, 8, 8, 25)):
+        call(T, stride, at, out)
+    assert len(reached) == 8
+    for T, stride, at, out in ((6, 1, 8, 8), (6, 1, 8, 3), (6, 1, 8, 13), (1, 1, 8, 8), (3, 8, 8, 14), (3, 8, 8, 6), (3, 8, 8, 24), (3, 2, 8, 9)):
+        with pytest.raises(ValueError, match="overlap"):
+            call(T, stride, at, out)
+    assert len(reached) == 8
