@@ -723,7 +723,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvView c, c
 // are expanded once for both halves).
 inline int rows_of(const KvView &c, const KvAttention &a) { return std::max<int64_t>(a.max_q, 1) * (a.HQ / c.HK) <= 8 ? 8 : 16; }
 
-Split plan(const KvView &c, const KvAttention &a, bool fp32) {
+Split plan(const KvView &c, const KvAttention &a, q1_dtype t) {
+  const bool fp32 = t == Q1_F32;
   const int rows = rows_of(c, a), r = a.HQ / c.HK;
   Split s;
   s.tiles = (int)kv_tiles_of_grid(c, (std::min(std::max<int64_t>(a.max_q, 1), c.T) * r + rows - 1) / rows, c.T * r, rows);
@@ -737,6 +738,10 @@ Split plan(const KvView &c, const KvAttention &a, bool fp32) {
   int64_t want = std::min(slots / work, blocks / 16);
   if (blocks / std::max<int64_t>(2 * slots / work, 1) >= 64) want = 2 * slots / work;
   if (blocks / std::max<int64_t>(4 * slots / work, 1) >= 128) want = 4 * slots / work;
+  // The tensor cores cut what they add to O instead of rounding it, fp16 rows' two parts of P at 2^-27 of O per token of a warp, where
+  // all are of one sign: so a CTA's warps have at most 2^18 tokens (a quarter of a step).  Half a step of bf16 is more than 2^21
+  // tokens lose with one part, and fp32 rows have their sums added up apart.
+  want = std::max(want, std::min<int64_t>((blocks - 1) >> (t == Q1_F16 ? 14 : 17), 1 << 10) + 1);
   // Heads of 64: 9 to 16 splits are rather 8, in a cluster, whose join saves more than twice the blocks cost (12 heads over 4096
   // tokens 7.1 us, 8.4 with 16; heads of 128 and 256: 9.1 and 11.0, 8.4 and 9.4 with 16; clusters of 16 were slower yet).
   if (c.D == 64 && want > kCluster && want <= 2 * kCluster && work * kCluster <= slots) want = kCluster;
@@ -804,13 +809,13 @@ cudaError_t run_t(const KvView &c, const KvAttention &a, const Split &s, cudaStr
 }  // namespace
 
 size_t kv_decode_workspace_bytes(const KvView &c, const KvAttention &a, q1_dtype t) {
-  const Split s = plan(c, a, t == Q1_F32);
+  const Split s = plan(c, a, t);
   if (s.splits == 1 || s.cluster) return 0;
   return (size_t)(c.B * c.HK) * s.tiles * s.splits * rows_of(c, a) * (c.D + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv_decode(const KvView &c, const KvAttention &a, q1_dtype t, void *workspace, cudaStream_t st) {
-  Split s = plan(c, a, t == Q1_F32);
+  Split s = plan(c, a, t);
   s.part = static_cast<float *>(workspace);
   if (t == Q1_BF16) return run_t<__nv_bfloat16>(c, a, s, st);
   if (t == Q1_F16) return run_t<__half>(c, a, s, st);

@@ -1270,9 +1270,12 @@ int kv_tiles_splits(const KvView &c, const KvAttention &a, q1_dtype t) {
   int64_t seen = std::max<int64_t>(a.max_len, 1);
   if (a.window) seen = std::min<int64_t>(seen, (int64_t)a.window + s.rows / (a.HQ / c.HK));
   const double values = (double)c.T * a.HQ * c.D;
+  // The tensor cores cut what they add to O instead of rounding it: 2^-27.5 of O per token, where all are of one sign (200000
+  // tokens 1.0e-3).  So a part has at most 2^16 tokens of fp16 outputs, 2^18 of bf16, which stays below half a step of these.
+  const int least = (int)std::min<int64_t>((seen - 1) >> (t == Q1_F16 ? 16 : 18), 31) + 1;
   double best = values / (1 << 19) * (double)seen + 0.001 * values / c.D * std::min(c.D, 128) + 400;
   int splits = 0;
-  for (int n = 1; n <= 32 && (n == 1 || seen / n >= 128); ++n) {
+  for (int n = least; n <= 32 && (n == least || seen / n >= 128); ++n) {
     const double rounds = (double)((s.units * n + s.slots - 1) / s.slots);
     const double cost = rounds * (1050 + (double)seen / n) + (n > 1 ? 230 + 9e-5 * n * values : 0);
     if (cost < best) best = cost, splits = n;

@@ -435,7 +435,9 @@ q1_status q1_kv_load(const q1_kv_cache *cache, void *k, int64_t k_stride, void *
  *   q, o        [T][HQ][D] in dtype, rows *_stride elements apart, as above; o must not overlap q
  *   lse         fp32 [T][HQ] or NULL
  *   max_q       the longest sequence's rows, max_len the largest of lengths: hints that pick
- *               the kernels and their split (results do not depend on them beyond rounding).
+ *               the kernels and their split (results do not depend on them beyond rounding;
+ *               but the tensor cores cut their fp32 sums, which fp16 rows over more than 2^16
+ *               tokens see, so max_len picks a split there that a smaller one would lack).
  * Sums, maxima and the states of the softmax are fp32.  Few rows per key head, and all fp32
  * ones, go through mma.sync with the codes as they are: keys and values enter exactly, and
  * the weights as fp16 (bf16 outputs) or with 22 bits.  Many bf16 or fp16 rows (by rows, heads

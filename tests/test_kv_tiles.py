@@ -384,3 +384,36 @@ def test_offsets_out_of_range_stay_inside_by_tiles(q1, D, HK, whole):
     err, _ = bounds(c, 0, qv[some], want, size, big, D ** -0.5, "bf16")
     assert (np.abs(out[1:-1][some].double().cpu().numpy() - want) <= err).all()
     assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("D,HK,r,new,dtype,n", [(128, 19, 4, 512, "fp16", 200000), (128, 19, 4, 512, "fp16", 400000), (64, 38, 2, 500, "fp16", 150000), (256, 38, 2, 512, "bf16", 600000),
+                                                (128, 1, 2, 1, "fp16", 1200000), (64, 200, 1, 1, "fp16", 700000)])
+def test_long_sums_of_one_sign_in_16_bits(q1, D, HK, r, new, dtype, n):
+    # contexts so long that what the tensor cores cut off their sums would show, with enough heads to fill the GPU without a split.
+    # Relative to o of nearly equal weights: its rounding eps / 2, and in a part of 2^16 (fp16) or 2^18 (bf16) tokens, by few
+    # rows 2^15 per warp in two parts, 2^12 (2^14) additions that each cut at most 2^-23 of what has grown to half on average: 2^-12
+    # (2^-10).  By tiles V's rounding, 2^-11: it does not average over the tokens, as nearly all of a channel's values have the same
+    # code (the range of a group is -1 .. 1.05, its step 0.14), and so differ by the few values of their scale and bias in bf16.
+    # P's roundings do, below 2^-14.
+    g = torch.Generator(device="cuda").manual_seed(D)
+    width = -(-n // 64)
+    cache, table = q1.kv_cache(width, HK, D), torch.arange(width, dtype=torch.int32, device="cuda").view(1, -1)
+    kept = torch.zeros(2, n, D, device="cuda")
+    step = 1 << 14
+    for t in range(0, n, step):
+        m = min(step, n - t)
+        k, v = 0.2 * torch.randn(1, m, HK, D, generator=g, device="cuda"), 1 + 0.05 * torch.rand(1, m, HK, D, generator=g, device="cuda")
+        v[..., 5::64] = -1.0
+        length = torch.tensor([t + m], dtype=torch.int32, device="cuda")
+        q1.kv_store(cache, k, v, table, length)
+        kept[:, t:t + m] = torch.stack([x[0, :, HK - 1] for x in q1.kv_load(cache, table, length, m, dtype=torch.float32)])
+    q = torch.randn(1, new, HK * r, D, generator=g, device="cuda").to(DTYPES[dtype])
+    o, lse = q1.kv_attention(q, cache, table, length, max_len=n, return_lse=True)
+    k, v = kept.double()
+    x = (k @ q[0, -1, -1].double()) * D ** -0.5
+    want = torch.softmax(x, 0) @ v
+    cut = 2.0 ** -12 if dtype == "fp16" else 2.0 ** -10
+    of_v = 2.0 ** -11 if new > 1 else 0.0
+    assert ((o[0, -1, -1].double() - want).abs() <= (torch.finfo(DTYPES[dtype]).eps / 2 + of_v + cut + 2.0 ** -14) * want.abs()).all()
+    assert abs(float(lse[0, -1, -1]) - float(torch.logsumexp(x, 0))) <= 2.0 ** -18
+    assert q1.device_errors() == 0
