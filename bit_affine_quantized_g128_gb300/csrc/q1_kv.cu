@@ -14,7 +14,7 @@
 // of them has channels 32 j + 8 t .. + 7, so a group is found in two shuffles, K's codes leave
 // in the order in which they lie, 512 bytes per store, and V's go through shared memory,
 // where words of a token become words of a channel.  Measured: 65536 tokens of 8 heads of 128 loaded in 55 us, 92 % of the copy
-// rate (191 us by words); a prompt of 8192 stored and loaded again in 23.4 us, two launches (58 us by words); one token of a
+// rate (191 us by words); a prompt of 8192 stored and loaded again in 24 us, two launches (58 us by words); one token of a
 // sequence 5.8 us, two launches.
 #include <cuda_bf16.h>
 

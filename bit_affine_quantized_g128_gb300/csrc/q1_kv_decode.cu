@@ -17,16 +17,17 @@
 // CTAs, and joined in a fixed order.  The maximum is a reference that moves only when
 // a logit exceeds it by more than 8 octaves, so most blocks need no reduction.
 //
-// What bounds it: instructions.  A block of 16 tokens of 128 channels takes a warp 380 of them (144 to expand the codes, 16 to 18
+// What bounds it: issue.  A block of 16 tokens of 128 channels takes a warp 380 instructions (144 to expand the codes, 16 to 18
 // MMAs, the rest softmax, scales and copies); 64 sequences of 8000 tokens, 40 heads over 8 of 128: 158 us, 3.7 TB/s, 55 % of the
-// measured copy rate, 0.67 to 0.77 issued per scheduler and clock, the pipe of the logic instructions the fullest.  One sequence of
-// 200000, 24 heads over 4 of 256: 59 us, 55 %.  One of 4096: 8.7 us, of which the launch and one CTA's chain of loads, blocks
+// measured copy rate, 0.67 issued per scheduler and clock (0.83 on the busiest SM, as lengths differ), the pipe of the logic
+// instructions the fullest.  One sequence of 200000, 24 heads over 4 of 256: 60 us, 55 %, 0.49 issued, as registers leave 8 warps
+// on an SM.  One of 4096: 8.7 us, of which the launch and one CTA's chain of loads, blocks
 // and join are most.
 //
 // Precision: q in bf16 or fp16 is one fp16 value scaled by a power of two per row
 // (exact down to 2^-28 of the row's largest), fp32 a sum of two.  P scale is one fp16
-// value for bf16 outputs (2^-12), a sum of two for fp16 and fp32 ones, with a power
-// of two that follows the largest scale seen.  Sums are fp32.
+// value for bf16 outputs (2^-11), a sum of two for fp16 and fp32 ones, with a power
+// of two that follows the largest scale seen (of which it keeps 2^-30).  Sums are fp32.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -16,8 +16,8 @@
 // are kept short (a few KB each): with the same loops unrolled twice as far the kernel took
 // 1.5 times as long, though it issued fewer instructions.
 //
-// What bounds it.  8192 tokens, 32 heads over 8 of 128 channels: 480 us, 1150 TFLOP/s, 60 % of the measured bf16 peak; 1000 rows
-// over 15000 tokens, 24 heads over 4 of 256: 345 us, 58 %.  A tile of 64 tokens takes a CTA 1800 clocks for 1266 of MMAs (an MMA
+// What bounds it.  8192 tokens, 32 heads over 8 of 128 channels: 486 us, 1130 TFLOP/s, 60 % of the measured bf16 peak; 1000 rows
+// over 15000 tokens, 24 heads over 4 of 256: 353 us, 57 %.  A tile of 64 tokens takes a CTA 1800 clocks for 1266 of MMAs (an MMA
 // of 256 x 64 x 16 takes 43 clocks with both operands in shared memory, 32 with Q in tensor memory; of 256 x 128 x 16 64): the two row
 // tiles' softmax warps on a scheduler go through a tile in step, 600 clocks per 32 columns, and wait 450 for barriers and tensor
 // memory.  Neither the other roles' traffic nor the fences slow the MMAs (633 clocks per row tile and 64 tokens beside all of it).

@@ -440,7 +440,8 @@ q1_status q1_kv_load(const q1_kv_cache *cache, void *k, int64_t k_stride, void *
  *               tokens see, so max_len picks a split there that a smaller one would lack).
  * Sums, maxima and the states of the softmax are fp32.  Few rows per key head, and all fp32
  * ones, go through mma.sync with the codes as they are: keys and values enter exactly, and
- * the weights as fp16 (bf16 outputs) or with 22 bits.  Many bf16 or fp16 rows (by rows, heads
+ * the products of weights and scales as fp16 (bf16 outputs) or with 22 bits, and 2^-30 of the
+ * largest scale.  Many bf16 or fp16 rows (by rows, heads
  * and hints, where it costs less) go through the tcgen05 kernel.  There values and weights
  * are rounded to fp16 (2^-11 of each), with a power of two for the sizes of a key head: of the
  * largest scale or bias that 128 to 512 neighbouring rows see, values keep 2^-20, scales and biases of
