@@ -742,7 +742,7 @@ Split plan(const KvView &c, const KvAttention &a, q1_dtype t) {
   // The tensor cores cut what they add to O instead of rounding it, fp16 rows' two parts of P at 2^-27 of O per token of a warp, where
   // all are of one sign: so a CTA's warps have at most 2^18 tokens (a quarter of a step).  Half a step of bf16 is more than 2^21
   // tokens lose with one part, and fp32 rows have their sums added up apart.
-  want = std::max(want, std::min<int64_t>((blocks - 1) >> (t == Q1_F16 ? 14 : 17), 1 << 10) + 1);
+  want = std::max(want, std::min<int64_t>((blocks - 1) >> (t == Q1_F16 ? 14 : 17), 63) + 1);
   // Heads of 64: 9 to 16 splits are rather 8, in a cluster, whose join saves more than twice the blocks cost (12 heads over 4096
   // tokens 7.1 us, 8.4 with 16; heads of 128 and 256: 9.1 and 11.0, 8.4 and 9.4 with 16; clusters of 16 were slower yet).
   if (c.D == 64 && want > kCluster && want <= 2 * kCluster && work * kCluster <= slots) want = kCluster;
