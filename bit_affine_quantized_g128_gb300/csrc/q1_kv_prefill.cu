@@ -17,7 +17,7 @@
 // 1.5 times as long, though it issued fewer instructions.
 //
 // What bounds it.  8192 tokens, 32 heads over 8 of 128 channels: 486 us, 1130 TFLOP/s, 60 % of the measured bf16 peak; 1000 rows
-// over 15000 tokens, 24 heads over 4 of 256: 353 us, 57 %.  A tile of 64 tokens takes a CTA 1800 clocks for 1266 of MMAs (an MMA
+// over 15000 tokens, 24 heads over 4 of 256, fp16: 376 us, 53 %.  A tile of 64 tokens takes a CTA 1800 clocks for 1266 of MMAs (an MMA
 // of 256 x 64 x 16 takes 43 clocks with both operands in shared memory, 32 with Q in tensor memory; of 256 x 128 x 16 64): the two row
 // tiles' softmax warps on a scheduler go through a tile in step, 600 clocks per 32 columns, and wait 450 for barriers and tensor
 // memory.  Neither the other roles' traffic nor the fences slow the MMAs (633 clocks per row tile and 64 tokens beside all of it).
@@ -26,14 +26,16 @@
 // code), and the biases through one more k16 step: columns bias_g (twice per
 // group) of K against the high and low fp16 half of the sum of Q's channels in group g.
 // So S is exact up to fp32 sums, as far as fp16 reaches: K and V are multiplied with a power of
-// two that brings the largest scale or bias that a tile's rows see to 2^-2 or more (V: 2^-5), so that
-// scales and biases of K are exact down to 2^-15 of the largest and off by at most 2^-23 of it below.  It is a fixed one, and a tile
+// two that brings the largest scale or bias that a tile's rows see to 2^-2 or more, so that
+// scales and biases are exact down to 2^-15 of the largest and off by at most 2^-23 of it below.  It is a fixed one, and a tile
 // that it turns out not to suit is done once more with one that does (a prompt of 8192 tokens 486 us, 481 without the
 // search for the largest, 925 done twice).  Q is fp16, scaled by a power of two per row so that its
 // largest value lies in [2^7, 2^8): bf16 and fp16 inputs are exact down to 2^-22 of
 // that.  A 17th column of K is -inf where a token's page is missing, against 1 in Q.
-// V is scale q + bias rounded to fp16 (2^-11 of it, or 2^-20 of the largest scale or bias), P is rounded to fp16 (2^-11); the sum
-// of P is fp32 of the unrounded values.  M is a reference that moves when a tile's P would
+// V is scale q + bias rounded to fp16 (2^-11) for bf16 outputs; for fp16 ones, whose own rounding is as small, scale q and bias are
+// two operands, exact like K's, and O has two products (1000 rows over 15000 tokens 376 us and 2.9e-4 off, 354 and
+// 3.2e-4 with one; their output's rounding is 2.1e-4).  P is rounded to fp16 (2^-11): its low part in a third product took 461 us, for
+// 2.2e-4.  The sum of P is fp32 of the unrounded values.  M is a reference that moves when a tile's P would
 // overflow fp16; 2^7 keeps all of P that matters among fp16's normal values.
 //
 // The channels of a group of 8 are stored in the order 0 4 1 5 2 6 3 7, as a code word
@@ -132,10 +134,10 @@ struct Bars {
   uint32_t top_k, top_v;
 };
 // Before scales, biases and values are rounded to fp16 their sizes are brought into its range, by a power of two that O and the
-// logits' factor give back.  It starts at 2^kUpK and 2^kUpV, which suits a largest scale or bias in [2^-6, 2^8) for K and [2^-12,
+// logits' factor give back.  It starts at 2^kUpK and 2^kUpV, which suits a largest scale or bias in [2^-6, 2^8) for K and [2^-9,
 // 2^5) for V; where a CTA finds another one it does its tile a second time, with that one brought into [2^11, 2^12) (9 times that,
 // the largest value, is below fp16's).
-constexpr int kUpK = 4, kUpV = 7, kLowK = -2, kLowV = -5, kHigh = 12;
+constexpr int kUpK = 4, kUpV = 7, kLowK = -2, kLowV = -2, kHigh = 12;
 __device__ __forceinline__ int octave(uint32_t bits) { return (int)(bits >> 23) - 127; }
 __device__ __forceinline__ bool unsuited(uint32_t top, int up, int low) {
   return top != 0 && (octave(top) + up < low || octave(top) + up >= kHigh);
@@ -402,7 +404,7 @@ __device__ __forceinline__ void ldg_words(const unsigned char *p, uint32_t (&w)[
   }
 }
 
-template <int D, int GS>
+template <typename T, int D, int GS>
 struct Prefill {
   static constexpr int G = D / GS, kBlock = 16 * (D + 8 * G);
   static constexpr int CG = D == 64 ? 1 : 2;                     // CTAs that work together
@@ -412,7 +414,8 @@ struct Prefill {
   static constexpr int NB = D == 128 ? 4 : 2;                    // buffers of S
   static constexpr bool kQTmem = D == 256;                       // Q as the MMA's operand in tensor memory
   static constexpr int kQTile = kQTmem ? 0 : (D / 64) * 128 * 128;
-  static constexpr int kBoxK = BK * 128, kStageK = (D / 64) * kBoxK, kBoxV = BN * 128, kStageV = (DV / 64) * kBoxV;
+  static constexpr int kBoxK = BK * 128, kStageK = (D / 64) * kBoxK, kBoxV = BN * 128, kPartV = (DV / 64) * kBoxV;
+  static constexpr int VP = std::is_same<T, __half>::value ? 2 : 1, kStageV = VP * kPartV;  // operands that add up to V
   static constexpr int NST = D == 64 ? 2 : 4;                    // stages of K, and of V
   static constexpr int kHeader = 2048;  // barriers, and from byte 1024 on the rows' factors
   static constexpr int kQ = kHeader, kK = kQ + QT * kQTile, kV = kK + NST * kStageK, kX = kV + NST * kStageV;
@@ -448,9 +451,9 @@ __device__ __forceinline__ void publish_smem(uint64_t *bar, int lane, int rank) 
 }
 
 // One warp's share of the expansion of K or V, in units numbered through all tiles.
-template <int D, int GS>
+template <typename T, int D, int GS>
 struct Expander {
-  using C = Prefill<D, GS>;
+  using C = Prefill<T, D, GS>;
   static constexpr int G = C::G, KW = D / 32;
   const KvView &c;
   int64_t b;
@@ -597,8 +600,13 @@ struct Expander {
         const uint4 &u = r.code[w];
         __half2 h[4];
         expand(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, exps, h);
-        sts4(dst + swz(row, v_piece(w)), bits(__hfma2(h[0], s, o)), bits(__hfma2(h[1], s, o)), bits(__hfma2(h[2], s, o)),
-             bits(__hfma2(h[3], s, o)));
+        if constexpr (C::VP == 1) {
+          sts4(dst + swz(row, v_piece(w)), bits(__hfma2(h[0], s, o)), bits(__hfma2(h[1], s, o)), bits(__hfma2(h[2], s, o)),
+               bits(__hfma2(h[3], s, o)));
+        } else {
+          sts4(dst + swz(row, v_piece(w)), bits(__hmul2(h[0], s)), bits(__hmul2(h[1], s)), bits(__hmul2(h[2], s)), bits(__hmul2(h[3], s)));
+          sts4(dst + C::kPartV + swz(row, v_piece(w)), bits(o), bits(o), bits(o), bits(o));
+        }
       }
     }
     return bad;
@@ -656,7 +664,7 @@ __device__ __forceinline__ uint32_t high_low(float x) { return half2_bits(x, x -
 template <typename T, int D, int GS>
 __device__ __forceinline__ float load_q(const KvAttention &a, const Rows &rows, uint32_t sm, uint32_t tl, int first, int hk, int r, int q,
                                         int at, int lane) {
-  using C = Prefill<D, GS>;
+  using C = Prefill<T, D, GS>;
   constexpr int G = C::G;
   auto row_of = [&](int i) {
     const int row = min(first + i, rows.rows - 1);  // rows past the last repeat it
@@ -754,10 +762,10 @@ __device__ __forceinline__ float load_q(const KvAttention &a, const Rows &rows, 
 }
 
 template <typename T, int D, int GS>
-__global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kernel(const KvView c, const KvAttention a, int tiles, int splits,
+__global__ void __launch_bounds__((Prefill<T, D, GS>::kThreads), 1) kv_prefill_kernel(const KvView c, const KvAttention a, int tiles, int splits,
                                                                                       float *part) {
-  using C = Prefill<D, GS>;
-  using X = Expander<D, GS>;
+  using C = Prefill<T, D, GS>;
+  using X = Expander<T, D, GS>;
   constexpr int G = C::G, QT = C::QT, BN = C::BN, CG = C::CG;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -1121,8 +1129,9 @@ __global__ void __launch_bounds__((Prefill<D, GS>::kThreads), 1) kv_prefill_kern
 #pragma unroll 1
             for (int h = 0; h < BN / 64; ++h, p += 32, vb += 4 * 2048 / 16)
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                umma_ts<CG>(o, p + 8 * j, vb + j * (2048 / 16), idesc(128 * CG, D, true), i > 0 || h > 0 || j > 0);
+              for (int j = 0; j < 4 * C::VP; ++j)
+                umma_ts<CG>(o, p + 8 * (j & 3), vb + (j & 3) * (2048 / 16) + (j >> 2) * (C::kPartV / 16), idesc(128 * CG, D, true),
+                            i > 0 || h > 0 || j > 0);
             umma_commit<CG>(&bars->o_done[q]);
             umma_commit<CG>(&bars->v_empty[s]);
             // P's place is free for other scores
@@ -1207,7 +1216,7 @@ Shape shape(const KvView &c, const KvAttention &a) {
 
 template <typename T, int D, int GS>
 cudaError_t run(const KvView &c, const KvAttention &a, int splits, float *part, cudaStream_t st) {
-  using C = Prefill<D, GS>;
+  using C = Prefill<T, D, GS>;
   static std::atomic<uint64_t> ready{0};
   const int dev = current_device();
   if (not_done(ready, dev)) {
@@ -1270,9 +1279,10 @@ int kv_tiles_splits(const KvView &c, const KvAttention &a, q1_dtype t) {
   int64_t seen = std::max<int64_t>(a.max_len, 1);
   if (a.window) seen = std::min<int64_t>(seen, (int64_t)a.window + s.rows / (a.HQ / c.HK));
   const double values = (double)c.T * a.HQ * c.D;
-  // The tensor cores cut what they add to O instead of rounding it: 2^-27.5 of O per token, where all are of one sign (200000
-  // tokens 1.0e-3).  So a part has at most 2^16 tokens of fp16 outputs, 2^18 of bf16, which stays below half a step of these.
-  const int least = (int)std::min<int64_t>((seen - 1) >> (t == Q1_F16 ? 16 : 18), 31) + 1;
+  // The tensor cores cut what they add to O instead of rounding it: 2^-27.5 of O per token and product, where all are of one sign
+  // (200000 tokens 1.0e-3).  So a part has at most 2^15 tokens of fp16 outputs (two products), 2^18 of bf16, which stays below half
+  // a step of these.
+  const int least = (int)std::min<int64_t>((seen - 1) >> (t == Q1_F16 ? 15 : 18), 31) + 1;
   double best = values / (1 << 19) * (double)seen + 0.001 * values / c.D * std::min(c.D, 128) + 400;
   int splits = 0;
   for (int n = least; n <= 32 && (n == least || seen / n >= 128); ++n) {

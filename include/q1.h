@@ -436,18 +436,18 @@ q1_status q1_kv_load(const q1_kv_cache *cache, void *k, int64_t k_stride, void *
  *   lse         fp32 [T][HQ] or NULL
  *   max_q       the longest sequence's rows, max_len the largest of lengths: hints that pick
  *               the kernels and their split (results do not depend on them beyond rounding;
- *               but the tensor cores cut their fp32 sums, which fp16 rows over more than 2^16
+ *               but the tensor cores cut their fp32 sums, which fp16 rows over more than 2^15
  *               tokens see, so max_len picks a split there that a smaller one would lack).
  * Sums, maxima and the states of the softmax are fp32.  Few rows per key head, and all fp32
  * ones, go through mma.sync with the codes as they are: keys and values enter exactly, and
  * the products of weights and scales as fp16 (bf16 outputs) or with 22 bits, and 2^-30 of the
- * largest scale.  Many bf16 or fp16 rows (by rows, heads
- * and hints, where it costs less) go through the tcgen05 kernel.  There values and weights
- * are rounded to fp16 (2^-11 of each), with a power of two for the sizes of a key head: of the
- * largest scale or bias that 128 to 512 neighbouring rows see, values keep 2^-20, scales and biases of
- * keys 2^-23 (they are exact from 2^-15 of it on).  Where that largest one lies outside
- * [2^-6, 2^8) (keys) or [2^-12, 2^5) (values) the call takes up to twice the time.  A NaN in a
- * group of V that a row sees makes that group's channels of the row NaN.  Where a wait of that kernel runs out (q1_device_errors, bit 3) the outputs are
+ * largest scale.  Many bf16 or fp16 rows (by rows, heads and hints, where it costs less) go
+ * through the tcgen05 kernel.  There weights are rounded to fp16 (2^-11 of each), and values for
+ * bf16 outputs.  Scales and biases are exact down to 2^-15 of the largest that 128 to 512
+ * neighbouring rows see of a key head's keys (or values), and keep 2^-23 of it below; where
+ * that largest one lies outside [2^-6, 2^8) (keys) or [2^-9, 2^5) (values) the call takes up to
+ * twice the time.  A NaN in a group of V that a row sees makes that group's channels of the row
+ * NaN.  Where a wait of that kernel runs out (q1_device_errors, bit 3) the outputs are
  * undefined.  Workspace: q1_kv_attention_workspace_size bytes, 256-byte aligned (may be 0); it
  * goes by sizes and hints, not by pointers.  Calls that may run at the same time need one each. */
 typedef struct {

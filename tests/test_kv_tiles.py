@@ -144,13 +144,12 @@ def scaled(c, cache, part, octaves):
 
 def small_bounds(c, b, qv, want, size, big, scale, dtype):
     """bounds() for sizes of any kind.  A power of two brings the largest scale or bias `top` of a head (of those that the rows of
-    a tile see) to at least 2^-2 (K) or 2^-5 (V) before scales, biases and values are rounded to fp16, whose steps end at 2^-24:
-    halves of these are 2^-23 top and 2^-20 top.  An element of K has three such roundings, that of the scale up to 8 times: below
-    2^-19 top."""
+    a tile see) to at least 2^-2 before scales, biases and values are rounded to fp16, whose steps end at 2^-24: half a step is
+    2^-23 top.  A value of K or V has three such roundings, that of the scale up to 8 times: (8 + 1 + 1) 2^-23 < 2^-19 top."""
     r = qv.shape[1] // c.heads
     top = [np.maximum(np.abs(x[b][1]), np.abs(x[b][2])).max((0, 2)).repeat(r) for x in (c.kq, c.vq)]
     # (half a step among the sum's terms, not taken off a sum that holds 2^-25: in float64 that leaves nothing of terms below 2^-78)
-    err, lerr = bounds(c, b, qv, want, size, big, scale, dtype, 2.0 ** -20 * top[1][:, None])
+    err, lerr = bounds(c, b, qv, want, size, big, scale, dtype, 2.0 ** -19 * top[1][:, None])
     more = abs(scale) * np.abs(qv.astype(np.float64)).sum(-1) * top[0] * 2.0 ** -19
     return err + 2 * more[..., None] * size, lerr + more
 
@@ -390,8 +389,8 @@ def test_offsets_out_of_range_stay_inside_by_tiles(q1, D, HK, whole):
                                                 (128, 1, 2, 1, "fp16", 1200000), (64, 200, 1, 1, "fp16", 700000)])
 def test_long_sums_of_one_sign_in_16_bits(q1, D, HK, r, new, dtype, n):
     # contexts so long that what the tensor cores cut off their sums would show, with enough heads to fill the GPU without a split.
-    # Relative to o of nearly equal weights: its rounding eps / 2, and in a part of 2^16 (fp16) or 2^18 (bf16) tokens, by few
-    # rows 2^15 per warp in two parts, 2^12 (2^14) additions that each cut at most 2^-23 of what has grown to half on average: 2^-12
+    # Relative to o of nearly equal weights: its rounding eps / 2, and in a part of 2^15 tokens with two products (fp16) or of 2^18 (bf16),
+    # by few rows 2^15 per warp with two, 2^12 (2^14) additions that each cut at most 2^-23 of what has grown to half on average: 2^-12
     # (2^-10).  By tiles V's rounding, 2^-11: it does not average over the tokens, as nearly all of a channel's values have the same
     # code (the range of a group is -1 .. 1.05, its step 0.14), and so differ by the few values of their scale and bias in bf16.
     # P's roundings do, below 2^-14.
@@ -417,3 +416,18 @@ def test_long_sums_of_one_sign_in_16_bits(q1, D, HK, r, new, dtype, n):
     assert ((o[0, -1, -1].double() - want).abs() <= (torch.finfo(DTYPES[dtype]).eps / 2 + of_v + cut + 2.0 ** -14) * want.abs()).all()
     assert abs(float(lse[0, -1, -1]) - float(torch.logsumexp(x, 0))) <= 2.0 ** -18
     assert q1.device_errors() == 0
+
+
+@pytest.mark.parametrize("D,HK,hint", [(64, 36, 600), (64, 24, 2000), (128, 24, 600), (128, 16, 2000), (256, 24, 600), (256, 12, 2000)])
+def test_values_enter_fp16_rows_exactly(q1, D, HK, hint):
+    # equal weights, which are powers of two, over values of two sizes per channel: what o is off beyond its own rounding (2^-11) is
+    # what the values were, and sums of 600 tokens in two products, below 2^-16 of what they add up in size
+    n, new = 600, 300
+    base = _rng(D).standard_normal((1, HK, D))
+    c = Cache(q1, [n], HK, D, seed=D, k=[_rng(D + 1).standard_normal((n, HK, D))], v=[base * np.where(np.arange(n) % 2, 1.37, 1.0)[:, None, None]])
+    o, lse = attend(q1, c, c.store(q1), torch.zeros(new, 2 * HK, D, dtype=torch.float16), [new], max_len=hint, causal=False, whole=hint == n)
+    v = c.vval[0].astype(np.float64)
+    want = v.mean(0).repeat(2, 0)
+    size = (np.abs(v - np.repeat(c.vq[0][2], 64, -1)) + np.abs(np.repeat(c.vq[0][2], 64, -1))).mean(0).repeat(2, 0)
+    assert (np.abs(o - want) <= 2.0 ** -11 * np.maximum(np.abs(want), 2.0 ** -14) + 2.0 ** -16 * size).all()
+    assert (np.abs(lse - np.log(n)) <= 2.0 ** -20).all()
